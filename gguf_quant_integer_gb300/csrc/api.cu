@@ -2,6 +2,7 @@
 // Every check runs before anything is enqueued; nothing here allocates.
 #include <cstdint>
 
+#include "kv_common.cuh"
 #include "xq.h"
 #include "xq_common.cuh"
 
@@ -778,14 +779,24 @@ xq_status xq_device_error(xq_stream stream, unsigned int* code_out) {
       *code_out = (static_cast<unsigned int>(k + 1) << 8) | (c[k] & 0xFFu);
       break;
     }
+  unsigned int kv[2] = {0u, 0u};
+  const cudaError_t k0 = xq::take_kv_cache_error(&kv[0]);
+  const cudaError_t k1 = xq::take_kv_attn_error(&kv[1]);
+  if (k0 != cudaSuccess || k1 != cudaSuccess) return XQ_ERR_CUDA;
+  for (int k = 0; k < 2 && *code_out == 0; ++k)
+    if (kv[k]) *code_out = (3u << 8) | (kv[k] & 0xFFu);
   // checked builds: the first failed bounds check of each kernel file
-  unsigned int chk[4] = {0u, 0u, 0u, 0u};
+  unsigned int chk[6] = {0u, 0u, 0u, 0u, 0u, 0u};
   const cudaError_t c0 = xq::take_gemv_check(&chk[0]);
   const cudaError_t c1 = xq::take_tile_check(&chk[1]);
   const cudaError_t c2 = xq::take_quant_check(&chk[2]);
   const cudaError_t c3 = xq::take_q6k_check(&chk[3]);
-  if (c0 != cudaSuccess || c1 != cudaSuccess || c2 != cudaSuccess || c3 != cudaSuccess) return XQ_ERR_CUDA;
-  for (int k = 0; k < 4 && *code_out == 0; ++k)
+  const cudaError_t c4 = xq::take_kv_cache_check(&chk[4]);
+  const cudaError_t c5 = xq::take_kv_attn_check(&chk[5]);
+  if (c0 != cudaSuccess || c1 != cudaSuccess || c2 != cudaSuccess || c3 != cudaSuccess || c4 != cudaSuccess ||
+      c5 != cudaSuccess)
+    return XQ_ERR_CUDA;
+  for (int k = 0; k < 6 && *code_out == 0; ++k)
     if (chk[k]) *code_out = (9u << 8) | (chk[k] & 0xFFu);
   return XQ_OK;
 }

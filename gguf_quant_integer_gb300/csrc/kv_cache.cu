@@ -1,0 +1,350 @@
+// Writing the quantized KV cache and reading it back (block formulas and the
+// page layout in the public header).
+//
+// Both kernels move each byte once and compute about 20 operations a value,
+// so HBM bounds them from a few hundred tokens on, and launch latency below.
+// A 32-value block belongs to a group of neighbouring lanes of one warp, each
+// with 16 bytes of float values (8 lanes for fp32, 4 for 16-bit types): the
+// loads and stores of a warp are then whole 128-byte lines, and the block's
+// maximum takes two or three shuffles and no shared memory. A thread handles
+// the same block of K and of V, which doubles the loads in flight.
+#include <climits>
+
+#include "kv_common.cuh"
+#include "xq_ptx.cuh"
+
+namespace xq {
+namespace {
+
+__device__ unsigned int g_kv_cache_error;
+
+constexpr int kThreads = 256;
+
+struct WriteArgs {
+  KvView c;
+  const void* x[2];       // K and V rows
+  long long stride[2];    // elements between tokens
+  const int64_t* slots;
+  unsigned units;         // blocks of K (and of V) in this launch
+  unsigned row_blocks;    // heads * dim / 32
+  bool wide;              // every 16-byte piece of x is 16-byte aligned
+};
+
+struct ReadArgs {
+  KvView c;
+  void* y[2];
+  const int64_t* slots;
+  unsigned units;
+  unsigned row_blocks;
+};
+
+template <typename X>
+__device__ __forceinline__ float to_float(X v);
+template <>
+__device__ __forceinline__ float to_float(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ float to_float(__half v) {
+  return __half2float(v);
+}
+template <>
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) {
+  return __bfloat162float(v);
+}
+
+// 16 bytes of row elements as floats.
+template <typename X, int N>
+__device__ __forceinline__ void load_piece(const X* p, bool wide, float (&f)[N]) {
+  static_assert(N * sizeof(X) == 16, "a piece is 16 bytes");
+  union {
+    uint4 u;
+    X e[N];
+  } r;
+  if (wide) {
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.u.x), "=r"(r.u.y), "=r"(r.u.z), "=r"(r.u.w)
+                 : "l"(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.e[i] = p[i];
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) f[i] = to_float<X>(r.e[i]);
+}
+
+// The page row of a slot, or false (recorded) if the cache has no such slot.
+__device__ __forceinline__ bool slot_row(const KvView& c, long long slot, long long* page, int* row) {
+  *page = slot >> c.page_shift;
+  *row = static_cast<int>(slot & ((1 << c.page_shift) - 1));
+  if (slot < 0) return false;
+  if (*page >= c.n_pages) {
+    atomicCAS(&g_kv_cache_error, 0u, kKvBadSlot);
+    return false;
+  }
+  return true;
+}
+
+// round(x / d), halves away from zero, clamped; a quotient that is not a
+// number (0 / 0 never reaches here; inf / inf) gives 0.
+__device__ __forceinline__ int quant(float x, float d, float low, float top) {
+  float y = roundf(__fdiv_rn(x, d));
+  y = (y != y) ? 0.0f : y;
+  return static_cast<int>(fminf(fmaxf(y, low), top));
+}
+
+// The block of N values in each of 32 / N neighbouring lanes: scale, and this
+// lane's codes as stored. Q4_0: lanes of the block's first half return the
+// bytes of elements (own, own + 16), the others nothing of use.
+template <int BITS, int N>
+__device__ __forceinline__ float quantize_piece(const float (&f)[N], int lane, uint32_t (&code)[N / 4]) {
+  constexpr int G = 32 / N;
+  __half dh;
+  if (BITS == 8) {
+    unsigned top = 0;  // |x| >= 0, so its bit pattern orders like the value (a NaN above all)
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(fabsf(f[i])));
+#pragma unroll
+    for (int o = 1; o < G; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    dh = __float2half_rn(__fdiv_rn(__uint_as_float(top), 127.0f));
+  } else {
+    float m = f[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i)
+      if (__float_as_uint(fabsf(f[i])) > __float_as_uint(fabsf(m))) m = f[i];
+#pragma unroll
+    for (int o = 1; o < G; o *= 2) {
+      const float other = __shfl_xor_sync(0xffffffffu, m, o);
+      const unsigned a = __float_as_uint(fabsf(m)), b = __float_as_uint(fabsf(other));
+      // elements are in lane order, so of two equal magnitudes the lower lane's is the first
+      if (b > a || (b == a && (lane & o))) m = other;
+    }
+    dh = __float2half_rn(m * -0.125f);
+  }
+  const float d = __half2float(dh);
+  if (BITS == 8) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const unsigned q = d != 0.0f ? quant(f[i], d, -127.0f, 127.0f) + 128 : 128;
+      code[i / 4] = (i & 3) ? (code[i / 4] | (q << (8 * (i & 3)))) : q;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const unsigned q = d != 0.0f ? quant(f[i], d, -8.0f, 7.0f) + 8 : 8;
+      code[i / 4] = (i & 3) ? (code[i / 4] | (q << (8 * (i & 3)))) : q;
+    }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) code[i] |= __shfl_xor_sync(0xffffffffu, code[i], G / 2) << 4;
+  }
+  return d;
+}
+
+template <int BITS, typename X>
+__global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constant__ WriteArgs A) {
+  constexpr int N = 16 / sizeof(X), G = 32 / N;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const unsigned at = blockIdx.x * kThreads + threadIdx.x;
+  const unsigned u = at / G;  // block of 32; the lanes of a warp stay together for the shuffles
+  const int piece = static_cast<int>(at % G), lane = static_cast<int>(threadIdx.x & 31);
+  const bool live = u < A.units;
+  const unsigned t = live ? u / A.row_blocks : 0, hb = live ? u - t * A.row_blocks : 0;
+  const long long slot = A.slots[t];
+  long long page;
+  int row;
+  const bool ok = live && slot_row(A.c, slot, &page, &row);
+  float f[2][N];
+#pragma unroll
+  for (int z = 0; z < 2; ++z) {
+    if (ok) {
+      load_piece<X, N>(static_cast<const X*>(A.x[z]) + static_cast<long long>(t) * A.stride[z] + hb * 32 + piece * N, A.wide,
+                       f[z]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) f[z][i] = 0.0f;
+    }
+  }
+  const int nb = A.c.dim / 32;
+  const unsigned h = hb / nb, b = hb - h * nb;
+#pragma unroll
+  for (int z = 0; z < 2; ++z) {
+    uint32_t code[N / 4];
+    const float d = quantize_piece<BITS, N>(f[z], lane, code);
+    if (!ok) continue;
+    uint8_t* base = (z ? A.c.v : A.c.k) + page * A.c.page_bytes;
+    const long long line = (static_cast<long long>(h) << A.c.page_shift) + row;
+    if (!XQ_IN(line, static_cast<long long>(A.c.heads) << A.c.page_shift, kChkKvRow)) continue;
+    // Q8_0: every lane N bytes; Q4_0: the lanes of the first half N bytes (two elements each)
+    if (BITS == 8 || piece < G / 2) {
+      uint8_t* to = base + line * A.c.row_bytes + b * (4 * BITS) + piece * N;
+      if (N == 8)
+        *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[N / 4 - 1]);
+      else
+        *reinterpret_cast<uint32_t*>(to) = code[0];
+    }
+    if (piece == 0) *reinterpret_cast<__half*>(base + A.c.scale_off + (line * nb + b) * 2) = __float2half_rn(d);
+  }
+}
+
+// 16 bytes of float values from N codes.
+template <typename Y, int N>
+__device__ __forceinline__ void store_piece(Y* p, const float (&f)[N]) {
+  union {
+    uint4 u;
+    Y e[N];
+  } r;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (sizeof(Y) == 4)
+      r.e[i] = f[i];
+    else if constexpr (sizeof(Y) == 2 && std::is_same<Y, __half>::value)
+      r.e[i] = __float2half_rn(f[i]);
+    else
+      r.e[i] = __float2bfloat16_rn(f[i]);
+  }
+  *reinterpret_cast<uint4*>(p) = r.u;
+}
+
+// A thread takes N code bytes of K and of V: N values of a Q8_0 block, or the
+// N low and N high halves (elements j and j + 16) of a Q4_0 block.
+template <int BITS, typename Y>
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ ReadArgs A) {
+  constexpr int N = 16 / sizeof(Y), G = 4 * BITS / N;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const unsigned at = blockIdx.x * kThreads + threadIdx.x;
+  const unsigned u = at / G;
+  const int piece = static_cast<int>(at % G);
+  if (u >= A.units) return;
+  const unsigned t = u / A.row_blocks, hb = u - t * A.row_blocks;
+  const int nb = A.c.dim / 32;
+  const unsigned h = hb / nb, b = hb - h * nb;
+  long long page;
+  int row;
+  const bool ok = slot_row(A.c, A.slots[t], &page, &row);
+  uint32_t code[2][N / 4];
+  float d[2];
+#pragma unroll
+  for (int z = 0; z < 2; ++z) {
+    d[z] = 0.0f;
+    code[z][0] = code[z][N / 4 - 1] = 0u;
+    if (!ok) continue;
+    const uint8_t* base = (z ? A.c.v : A.c.k) + page * A.c.page_bytes;
+    const long long line = (static_cast<long long>(h) << A.c.page_shift) + row;
+    if (!XQ_IN(line, static_cast<long long>(A.c.heads) << A.c.page_shift, kChkKvRow)) continue;
+    const uint8_t* from = base + line * A.c.row_bytes + b * (4 * BITS) + piece * N;
+    if (N == 8) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(from));
+      code[z][0] = w.x;
+      code[z][N / 4 - 1] = w.y;
+    } else {
+      code[z][0] = __ldg(reinterpret_cast<const uint32_t*>(from));
+    }
+    d[z] = __half2float(__ushort_as_half(__ldg(reinterpret_cast<const unsigned short*>(base + A.c.scale_off + (line * nb + b) * 2))));
+  }
+#pragma unroll
+  for (int z = 0; z < 2; ++z) {
+    Y* to = static_cast<Y*>(A.y[z]) + static_cast<size_t>(u) * 32 + piece * N;
+    float f[N];
+    if (BITS == 8) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        f[i] = ok ? __fmul_rn(d[z], static_cast<float>(static_cast<int>((code[z][i / 4] >> (8 * (i & 3))) & 255u) - 128)) : 0.0f;
+      store_piece<Y, N>(to, f);
+    } else {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          f[i] = ok ? __fmul_rn(d[z], static_cast<float>(static_cast<int>((code[z][i / 4] >> (8 * (i & 3) + 4 * half)) & 15u) - 8))
+                    : 0.0f;
+        store_piece<Y, N>(to + 16 * half, f);
+      }
+    }
+  }
+}
+
+template <typename K, typename Args>
+cudaError_t launch(K kernel, const Args& A, int lanes, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((A.units + kThreads / lanes - 1) / (kThreads / lanes));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, A);
+}
+
+// Tokens per launch: thread indices stay within 31 bits.
+int tokens_per_launch(const KvView& c) {
+  const long long most = (1LL << 27) / (static_cast<long long>(c.heads) * (c.dim / 32));
+  return most < 1 ? 1 : most > INT_MAX ? INT_MAX : static_cast<int>(most);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_write(const KvView& c, int bits, int x_type, const void* k, long long k_stride, const void* v,
+                            long long v_stride, const int64_t* slots, int n_tokens, cudaStream_t s) {
+  const int eb = kv_elt_bytes(x_type), step = tokens_per_launch(c);
+  WriteArgs A;
+  A.c = c;
+  A.stride[0] = k_stride;
+  A.stride[1] = v_stride;
+  A.row_blocks = static_cast<unsigned>(c.heads) * (c.dim / 32);
+  A.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | static_cast<uintptr_t>(k_stride * eb) |
+             static_cast<uintptr_t>(v_stride * eb)) & 15u) == 0;
+  for (long long t0 = 0; t0 < n_tokens; t0 += step) {
+    const long long n = n_tokens - t0 < step ? n_tokens - t0 : step;
+    A.x[0] = static_cast<const char*>(k) + t0 * k_stride * eb;
+    A.x[1] = static_cast<const char*>(v) + t0 * v_stride * eb;
+    A.slots = slots + t0;
+    A.units = static_cast<unsigned>(n) * A.row_blocks;
+    cudaError_t e;
+    if (x_type == kF32)
+      e = bits == 8 ? launch(kv_write_kernel<8, float>, A, 8, s) : launch(kv_write_kernel<4, float>, A, 8, s);
+    else if (x_type == kF16)
+      e = bits == 8 ? launch(kv_write_kernel<8, __half>, A, 4, s) : launch(kv_write_kernel<4, __half>, A, 4, s);
+    else
+      e = bits == 8 ? launch(kv_write_kernel<8, __nv_bfloat16>, A, 4, s) : launch(kv_write_kernel<4, __nv_bfloat16>, A, 4, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_kv_read(const KvView& c, int bits, const int64_t* slots, int n_tokens, int y_type, void* k, void* v,
+                           cudaStream_t s) {
+  const int eb = kv_elt_bytes(y_type), step = tokens_per_launch(c);
+  const long long row = static_cast<long long>(c.heads) * c.dim * eb;
+  ReadArgs A;
+  A.c = c;
+  A.row_blocks = static_cast<unsigned>(c.heads) * (c.dim / 32);
+  for (long long t0 = 0; t0 < n_tokens; t0 += step) {
+    const long long n = n_tokens - t0 < step ? n_tokens - t0 : step;
+    A.y[0] = static_cast<char*>(k) + t0 * row;
+    A.y[1] = static_cast<char*>(v) + t0 * row;
+    A.slots = slots + t0;
+    A.units = static_cast<unsigned>(n) * A.row_blocks;
+    cudaError_t e;  // code bytes a thread: 4 for fp32, 8 for 16-bit values
+    if (y_type == kF32)
+      e = bits == 8 ? launch(kv_read_kernel<8, float>, A, 8, s) : launch(kv_read_kernel<4, float>, A, 4, s);
+    else if (y_type == kF16)
+      e = bits == 8 ? launch(kv_read_kernel<8, __half>, A, 4, s) : launch(kv_read_kernel<4, __half>, A, 2, s);
+    else
+      e = bits == 8 ? launch(kv_read_kernel<8, __nv_bfloat16>, A, 4, s) : launch(kv_read_kernel<4, __nv_bfloat16>, A, 2, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t take_kv_cache_error(unsigned int* code) {
+  unsigned int v = 0, z = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_kv_cache_error, sizeof(v));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_kv_cache_error, &z, sizeof(z));
+  *code = v;
+  return e;
+}
+cudaError_t take_kv_cache_check(unsigned int* code) { return take_check_word(code); }
+
+}  // namespace xq

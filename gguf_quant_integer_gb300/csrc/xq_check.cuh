@@ -74,6 +74,8 @@ enum CheckSite : unsigned {
   kChkQ6Act = 41,  // quant / d8 read inside the Q8 buffer
   kChkQ6Y = 42,
   kChkQ6Isum = 43,
+  // kv_cache.cu, kv_attn.cu
+  kChkKvRow = 50,   // row inside its page
 };
 
 }  // namespace xq

@@ -15,10 +15,14 @@ from . import synth
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libxq.so")
 
+XQ_TYPE_F32 = 0
+XQ_TYPE_F16 = 1
+XQ_TYPE_Q4_0 = 2
 XQ_TYPE_Q8_0 = 8
 XQ_TYPE_Q4_K = 12
 XQ_TYPE_Q6_K = 14
 XQ_TYPE_IQ4_XS = 23
+XQ_TYPE_BF16 = 30
 
 STATUS = {0: "XQ_OK", 1: "XQ_ERR_ARG", 2: "XQ_ERR_SHAPE", 3: "XQ_ERR_ALIGN",
           4: "XQ_ERR_WORKSPACE", 5: "XQ_ERR_CUDA", 6: "XQ_ERR_UNSUPPORTED"}
@@ -31,7 +35,9 @@ SYMBOLS = ("xq_status_str", "xq_q8_bytes", "xq_weight_bytes", "xq_quantize_q8",
            "xq_matmul_q8_0_q8", "xq_debug_isums_q8_0", "xq_silu_mul_quantize_q8",
            "xq_layer_ffn_workspace_bytes", "xq_layer_mixed_ffn", "xq_matmul_iq4xs_q8",
            "xq_debug_isums_iq4xs", "xq_device_error", "xq_debug_stalled_matmul_q4k", "xq_debug_tile_sums",
-           "xq_debug_layer_matmuls", "xq_debug_check_probe", "xq_debug_stalled_ffn_layer")
+           "xq_debug_layer_matmuls", "xq_debug_check_probe", "xq_debug_stalled_ffn_layer",
+           "xq_kv_bytes", "xq_kv_write", "xq_kv_read", "xq_kv_attn_workspace_bytes", "xq_kv_attn",
+           "xq_kv_attn_shared")
 
 
 class XQError(RuntimeError):
@@ -44,6 +50,19 @@ class xq_proj(ctypes.Structure):
     _fields_ = [("type", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int),
                 ("W", ctypes.c_void_p), ("y", ctypes.c_void_p), ("input", ctypes.c_int),
                 ("codebook", ctypes.c_void_p)]
+
+
+class xq_kv_cache(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("heads", ctypes.c_int), ("dim", ctypes.c_int), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p)]
+
+
+class xq_kv_query(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("batch", ctypes.c_int), ("n_q", ctypes.c_int), ("heads", ctypes.c_int),
+                ("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int), ("max_pages", ctypes.c_int), ("lens", ctypes.c_void_p),
+                ("scale", ctypes.c_float), ("window", ctypes.c_int), ("prefix_pages", ctypes.c_void_p),
+                ("prefix_len", ctypes.c_int)]
 
 
 _lib = None
@@ -102,6 +121,17 @@ def lib(path: str | None = None):
     L.xq_layer_mixed_static.argtypes = [ctypes.POINTER(xq_proj), I, ctypes.POINTER(ctypes.c_void_p), I, I, P]
     L.xq_debug_layer_matmuls.argtypes = [ctypes.POINTER(xq_proj), I, I, I, P, S, P]
     L.xq_debug_check_probe.argtypes = [P, P, I, I, I, P, P]
+    C, Q, LL = ctypes.POINTER(xq_kv_cache), ctypes.POINTER(xq_kv_query), ctypes.c_longlong
+    L.xq_kv_bytes.argtypes = [I, I, I, I, I]
+    L.xq_kv_bytes.restype = S
+    L.xq_kv_write.argtypes = [C, I, P, LL, P, LL, P, I, P]
+    L.xq_kv_read.argtypes = [C, P, I, I, P, P, P]
+    L.xq_kv_attn_workspace_bytes.argtypes = [C, Q]
+    L.xq_kv_attn_workspace_bytes.restype = S
+    for fn in ("xq_kv_attn", "xq_kv_attn_shared"):
+        getattr(L, fn).argtypes = [C, Q, P, S, P]
+    for fn in ("xq_kv_write", "xq_kv_read", "xq_kv_attn", "xq_kv_attn_shared"):
+        getattr(L, fn).restype = I
     for fn in ("xq_quantize_q8", "xq_matmul_q4k_q8", "xq_matmul_q6k_q8", "xq_debug_isums_q4k",
                "xq_debug_isums_q6k", "xq_layer_mixed", "xq_layer_mixed_static", "xq_matmul_q8_0_q8",
                "xq_debug_isums_q8_0", "xq_debug_layer_matmuls", "xq_debug_check_probe"):
@@ -384,3 +414,161 @@ class Layer:
 
     def weight_bytes(self) -> int:
         return sum(synth.weight_bytes(p.qtype, p.N, p.K) for p in self.projs)
+
+
+def kv_bytes(qtype: int, n_pages: int, page_size: int, heads: int, dim: int) -> int:
+    return lib().xq_kv_bytes(qtype, n_pages, page_size, heads, dim)
+
+
+_FLOAT_TYPES = {}
+
+
+def _float_type(dtype):
+    if not _FLOAT_TYPES:
+        import torch
+        _FLOAT_TYPES.update({torch.float32: XQ_TYPE_F32, torch.float16: XQ_TYPE_F16, torch.bfloat16: XQ_TYPE_BF16})
+    try:
+        return _FLOAT_TYPES[dtype]
+    except KeyError:
+        raise ValueError(f"float32, float16 or bfloat16 expected, got {dtype}") from None
+
+
+class KVCache:
+    """Paged K and V of one layer, quantized as they are written.
+
+    qtype is XQ_TYPE_Q8_0 or XQ_TYPE_Q4_0. The pools are uint8 tensors of
+    kv_bytes(...) bytes each (k, v: existing ones; otherwise zeroed ones are
+    made). Token slot s is row s % page_size of page s // page_size; which
+    pages belong to which sequence is the caller's: attn takes a page table.
+
+    A call that needs a workspace uses one that the object keeps for each
+    stream. Pass `workspace` (uint8, at least attn_workspace_bytes) to use
+    another, as a CUDA graph that is replayed beside eager calls has to.
+    """
+
+    def __init__(self, qtype: int, n_pages: int, page_size: int, heads: int, dim: int, device="cuda", k=None, v=None):
+        import torch
+        self._torch = torch
+        nb = kv_bytes(qtype, n_pages, page_size, heads, dim)
+        if nb == 0 and n_pages != 0:
+            raise XQError("xq_kv_bytes", 2)
+        self.k = torch.zeros(nb, dtype=torch.uint8, device=device) if k is None else k
+        self.v = torch.zeros(nb, dtype=torch.uint8, device=device) if v is None else v
+        for pool in (self.k, self.v):
+            if pool.dtype != torch.uint8 or pool.numel() < nb or not pool.is_contiguous():
+                raise ValueError(f"a pool is a contiguous uint8 tensor of {nb} bytes")
+        self.device = self.k.device
+        if self.v.device != self.device:
+            raise ValueError("both pools have to be on one device")
+        self.qtype, self.n_pages, self.page_size, self.heads, self.dim = qtype, n_pages, page_size, heads, dim
+        self._desc = xq_kv_cache(qtype, n_pages, page_size, heads, dim, self.k.data_ptr(), self.v.data_ptr())
+        self._ref = ctypes.byref(self._desc)
+        self._lib = lib()
+        self._ws = {}   # stream -> workspace
+        self._need = {}  # sizes of a call -> workspace bytes
+
+    def _on_device(self, *tensors):
+        for t in tensors:
+            if t.device != self.device:
+                raise ValueError(f"a tensor on {t.device} for a cache on {self.device}")
+
+    def write(self, k, v, slots, stream=None):
+        """Quantize rows k, v [tokens, heads, dim] into slots int64 [tokens]
+        (negative ones are skipped). A token's row is contiguous; rows may be
+        a part of longer ones (k.stride(0))."""
+        n = slots.shape[0]
+        shape, inner = (n, self.heads, self.dim), (self.dim, 1)
+        if k.shape != shape or v.shape != shape or k.dtype != v.dtype or k.stride()[1:] != inner or v.stride()[1:] != inner:
+            raise ValueError(f"k and v: {shape} of one dtype, each token's row contiguous")
+        if slots.dtype != self._torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
+            raise ValueError("slots: contiguous int64 [tokens]")
+        self._on_device(k, v, slots)
+        rc = self._lib.xq_kv_write(self._ref, _float_type(k.dtype), k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0),
+                                   slots.data_ptr(), n, _stream(stream))
+        if rc:
+            raise XQError("xq_kv_write", rc)
+
+    def read(self, slots, dtype=None, k=None, v=None, stream=None):
+        """The rows of slots int64 [tokens] as floats: (k, v), each
+        [tokens, heads, dim] of dtype (float32)."""
+        torch = self._torch
+        if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
+            raise ValueError("slots: contiguous int64 [tokens]")
+        shape = (slots.shape[0], self.heads, self.dim)
+        dtype = (k.dtype if k is not None else torch.float32) if dtype is None else dtype
+        k = torch.empty(shape, dtype=dtype, device=self.device) if k is None else k
+        v = torch.empty(shape, dtype=dtype, device=self.device) if v is None else v
+        for t in (k, v):
+            if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+                raise ValueError(f"k and v: contiguous {shape} of {dtype}")
+        self._on_device(slots, k, v)
+        rc = self._lib.xq_kv_read(self._ref, slots.data_ptr(), shape[0], _float_type(dtype), k.data_ptr(), v.data_ptr(),
+                                  _stream(stream))
+        if rc:
+            raise XQError("xq_kv_read", rc)
+        return k, v
+
+    def attn_workspace_bytes(self, dtype, batch: int, n_q: int, heads: int, max_pages: int, prefix_len: int = 0) -> int:
+        q = xq_kv_query(type=_float_type(dtype), batch=batch, n_q=n_q, heads=heads, max_pages=max_pages,
+                        page_stride=max_pages, prefix_len=prefix_len)
+        nb = self._lib.xq_kv_attn_workspace_bytes(self._ref, ctypes.byref(q))
+        if nb == 0:
+            raise XQError("xq_kv_attn_workspace_bytes", 2)
+        return nb
+
+    def _workspace(self, key, stream):
+        need = self._need.get(key)
+        if need is None:
+            need = self._need[key] = self.attn_workspace_bytes(*key)
+        ws = self._ws.get(stream)
+        if ws is None or ws.numel() < need:
+            torch = self._torch
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device)):
+                ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            self._ws[stream] = ws
+        return ws
+
+    def _attn(self, fn, q, pages, lens, scale, window, prefix_pages, prefix_len, out, workspace, stream):
+        torch = self._torch
+        if q.dim() != 4 or q.shape[3] != self.dim or not q.is_contiguous():
+            raise ValueError(f"q: contiguous [batch, n_q, heads, {self.dim}]")
+        batch, n_q, heads, dim = q.shape
+        if pages.dtype != torch.int32 or pages.dim() != 2 or pages.shape[0] != batch or (pages.shape[1] > 1 and pages.stride(1) != 1):
+            raise ValueError("pages: int32 [batch, pages], each row contiguous")
+        if lens.dtype != torch.int32 or lens.shape != (batch,) or not lens.is_contiguous():
+            raise ValueError("lens: contiguous int32 [batch]")
+        if out is None:
+            out = torch.empty_like(q)
+        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+            raise ValueError("out: a contiguous tensor like q")
+        if prefix_pages is not None and (prefix_pages.dtype != torch.int32 or prefix_pages.dim() != 1 or
+                                         not prefix_pages.is_contiguous() or
+                                         prefix_pages.shape[0] * self.page_size < prefix_len):
+            raise ValueError("prefix_pages: contiguous int32 ids of the prefix's pages")
+        self._on_device(q, pages, lens, out)
+        s = _stream(stream)
+        width = pages.shape[1]
+        if workspace is None:
+            workspace = self._workspace((q.dtype, batch, n_q, heads, width, prefix_len), s.value or 0)
+        query = xq_kv_query(_float_type(q.dtype), batch, n_q, heads, q.data_ptr(), out.data_ptr(), pages.data_ptr(),
+                            pages.stride(0) if batch > 1 else width, width, lens.data_ptr(),
+                            dim ** -0.5 if scale is None else scale, window,
+                            prefix_pages.data_ptr() if prefix_pages is not None else None, prefix_len)
+        rc = fn(self._ref, ctypes.byref(query), workspace.data_ptr(), workspace.numel(), s)
+        if rc:
+            raise XQError(fn.__name__, rc)
+        return out
+
+    def attn(self, q, pages, lens, scale=None, window: int = 0, out=None, workspace=None, stream=None):
+        """Attention of q [batch, n_q, heads, dim], the last n_q tokens of
+        each sequence, over lens int32 [batch] tokens (those n_q among them)
+        in the pages int32 [batch, max_pages]. scale: 1 / sqrt(dim). window:
+        how many keys a query sees at most, 0 for all."""
+        return self._attn(self._lib.xq_kv_attn, q, pages, lens, scale, window, None, 0, out, workspace, stream)
+
+    def attn_shared(self, q, prefix_pages, prefix_len: int, pages, lens, scale=None, out=None, workspace=None, stream=None):
+        """attn for sequences that all begin with the prefix_len tokens in
+        prefix_pages int32 [pages]; pages and lens are of the tokens after it."""
+        self._on_device(prefix_pages)
+        return self._attn(self._lib.xq_kv_attn_shared, q, pages, lens, scale, 0, prefix_pages, prefix_len, out, workspace,
+                          stream)

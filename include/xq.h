@@ -86,10 +86,14 @@ typedef enum {
 } xq_status;
 
 /* GGUF tensor type ids. */
+#define XQ_TYPE_F32 0
+#define XQ_TYPE_F16 1
+#define XQ_TYPE_Q4_0 2
 #define XQ_TYPE_Q8_0 8
 #define XQ_TYPE_Q4_K 12
 #define XQ_TYPE_Q6_K 14
 #define XQ_TYPE_IQ4_XS 23
+#define XQ_TYPE_BF16 30
 
 /* Human-readable name of a status code (static string, never NULL). */
 XQ_API const char *xq_status_str(xq_status s);
@@ -328,11 +332,15 @@ XQ_API xq_status xq_layer_mixed_static(const xq_proj *proj, int n_proj,
  * the tile kernel (M > 64); wait = the kernel's number of the wait that gave
  * up (GEMV: 1 the producer waiting for a free stage, 2 a consumer waiting for
  * a full one, 3 a down projection's producer waiting for h in the fused
- * feed of xq_layer_mixed_ffn). Checked builds (the library compiled with
+ * feed of xq_layer_mixed_ffn). Kernel 3 = the KV cache kernels, whose record
+ * is of an invalid index, not of a wait: 1 a slot past the cache, 2 a page id
+ * outside it, 3 a sequence longer than its page table (see xq_kv_write and
+ * xq_kv_attn). Checked builds (the library compiled with
  * -DXQ_CHECK) also test the index, range or 16-byte alignment of each global
  * access whose address comes from nontrivial arithmetic, skip an access that
  * fails and record the site: kernel 9, wait = site (10-16 the GEMV, 20-26
- * the tile kernel, 30-32 the quantizer, 40-43 the dp4a Q6_K GEMV), reported
+ * the tile kernel, 30-32 the quantizer, 40-43 the dp4a Q6_K GEMV,
+ * 50-59 the KV cache kernels), reported
  * after any wait code. If several kernels recorded one,
  * the lowest kernel number is reported and all are cleared. The reads and
  * writes are synchronous. XQ_ERR_ARG for a null code_out, XQ_ERR_CUDA if the
@@ -408,6 +416,120 @@ XQ_API xq_status xq_debug_tile_sums(int type, const void *W, const int8_t *codeb
  * not hold the state of such a call. */
 XQ_API xq_status xq_debug_layer_matmuls(const xq_proj *proj, int n_proj, int n_inputs, int M, void *workspace,
                                         size_t ws_bytes, xq_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Quantized KV cache: the step between a layer's k/v projections and its
+ * attn_o projection. K and V rows are quantized as they are written and stay
+ * packed; attention reads the packed blocks.
+ *
+ * Blocks are 32 consecutive values of one head's row:
+ *   XQ_TYPE_Q8_0: d = fp16(max|x| / 127), q = clamp(round(x / d), -127, 127),
+ *                 stored as the byte q + 128; 34 bytes a block.
+ *   XQ_TYPE_Q4_0: d = fp16(m / -8), m the element of largest magnitude (the
+ *                 first such), q = clamp(round(x / d), -8, 7), stored as the
+ *                 nibble q + 8, byte j holding elements j (low) and j + 16
+ *                 (high); 18 bytes a block.
+ * max, the division and the rounding (halves away from zero) are fp32; d is
+ * rounded to nearest fp16 before it divides, so x is within d/2 of the value
+ * d * q up to the clamp. d = 0 gives q = 0. A block whose scale is not a
+ * finite fp16 (an infinity or NaN in it, or |x| above about 8.3e6 for Q8_0
+ * and 5.2e5 for Q4_0) stores that scale and reads back as NaN or infinity.
+ *
+ * A pool (one for K, one for V, xq_kv_bytes each) is n_pages pages. A page
+ * holds the codes of its tokens, [heads][page_size][dim * bits / 8] bytes,
+ * then their scales, fp16 [heads][page_size][dim / 32]. Token slot s is row
+ * s % page_size of page s / page_size.
+ *
+ * dim is 64, 96, 128 or 256; page_size is a power of two from 16 to 4096.
+ * Every pointer is 16-byte aligned except the rows that xq_kv_write takes
+ * (aligned to their element; rows at multiples of 16 bytes are read in
+ * 16-byte pieces), slots (8 bytes) and pages, lens (4 bytes).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    int type;       /* XQ_TYPE_Q8_0 or XQ_TYPE_Q4_0, of K and V */
+    int n_pages;
+    int page_size;  /* tokens a page */
+    int heads;      /* KV heads */
+    int dim;        /* head size */
+    void *k, *v;    /* device pools of xq_kv_bytes() bytes */
+} xq_kv_cache;
+
+/* Bytes of one pool: n_pages * heads * page_size * (dim / 32) * 34 (Q8_0) or
+ * * 18 (Q4_0). 0 on bad arguments. */
+XQ_API size_t xq_kv_bytes(int type, int n_pages, int page_size, int heads, int dim);
+
+/* Quantize n_tokens rows of K and of V and write them into their slots.
+ *   x_type  : XQ_TYPE_F32, XQ_TYPE_F16 or XQ_TYPE_BF16, of k and v.
+ *   k, v    : element (t, h, i) at k[t * k_stride + h * dim + i]; strides in
+ *             elements, at least heads * dim (rows may be a part of a longer
+ *             q/k/v row).
+ *   slots   : int64 [n_tokens], device. A negative slot is skipped (padding
+ *             of a static batch). One at or past n_pages * page_size is
+ *             skipped and recorded (xq_device_error: kernel 3, wait 1). The
+ *             slots of one call must differ; which row stays is otherwise
+ *             undefined.
+ * n_tokens == 0 enqueues nothing. */
+XQ_API xq_status xq_kv_write(const xq_kv_cache *cache, int x_type, const void *k, long long k_stride,
+                             const void *v, long long v_stride, const int64_t *slots, int n_tokens,
+                             xq_stream stream);
+
+/* Read the rows of n_tokens slots back as floats: d * q rounded once to
+ * y_type (fp32 holds it exactly), k and v contiguous [n_tokens][heads][dim].
+ * The row of a negative slot is zero; so is that of one past the cache,
+ * which is recorded as above (slots may repeat). */
+XQ_API xq_status xq_kv_read(const xq_kv_cache *cache, const int64_t *slots, int n_tokens, int y_type,
+                            void *k, void *v, xq_stream stream);
+
+/* Queries of an attention call over the cache. */
+typedef struct {
+    int type;            /* XQ_TYPE_F32, XQ_TYPE_F16 or XQ_TYPE_BF16, of q and out */
+    int batch;           /* sequences */
+    int n_q;             /* query tokens of each sequence, its last ones */
+    int heads;           /* query heads, a multiple of the KV heads: heads h*g .. h*g+g-1
+                            read KV head h */
+    const void *q;       /* [batch][n_q][heads][dim], contiguous */
+    void *out;           /* same shape and type; must not overlap q */
+    const int32_t *pages;   /* [batch] rows of page ids, page_stride entries apart */
+    int page_stride;
+    int max_pages;       /* entries of a row that may be read, at most page_stride */
+    const int32_t *lens; /* [batch] tokens in each sequence's own pages, the n_q query
+                            tokens among them (their K and V already written) */
+    float scale;         /* of the scores, usually 1 / sqrt(dim) */
+    int window;          /* 0, or how many keys a query sees at most, its own among them */
+    const int32_t *prefix_pages; /* xq_kv_attn_shared: page ids of the common prefix */
+    int prefix_len;              /* xq_kv_attn_shared: its tokens */
+} xq_kv_query;
+
+/* Workspace bytes of xq_kv_attn and xq_kv_attn_shared for this cache and
+ * these queries (only type, batch, n_q, heads, max_pages and prefix_len are
+ * looked at): partial results of sequences that several CTAs share. 0 on bad
+ * arguments. */
+XQ_API size_t xq_kv_attn_workspace_bytes(const xq_kv_cache *cache, const xq_kv_query *query);
+
+/* Attention of the last n_q tokens of each sequence over its own pages:
+ *   s_j = scale * sum_d q_d * k_jd,   o = sum_j softmax(s)_j * v_j
+ * over the keys j <= pos and, with a window, j > pos - window, where query
+ * token i of a sequence of n tokens is at pos = n - n_q + i. A query that
+ * sees no key (pos < 0; an idle entry with lens 0) gives 0. Scores, softmax
+ * statistics and sums are fp32. fp32 queries and weights enter the tensor
+ * cores as two fp16 numbers each (22 bits), 16-bit ones and their softmax
+ * weights as one; the stored codes are exact there, and block scales are
+ * applied in fp32. Results do not depend on what the slots past a sequence's
+ * length hold. They depend on the other sequences of the call only through
+ * where a long sequence is cut into parts (in rounding).
+ * lens beyond max_pages * page_size are cut to that, and a page id outside
+ * 0 .. n_pages-1 within a sequence's length is taken as masked keys; both
+ * are recorded (xq_device_error: kernel 3, waits 3 and 2). prefix_pages and
+ * prefix_len are ignored. */
+XQ_API xq_status xq_kv_attn(const xq_kv_cache *cache, const xq_kv_query *query, void *workspace,
+                            size_t ws_bytes, xq_stream stream);
+
+/* The same for sequences that all begin with one prefix, whose pages are
+ * stored once: the keys of a sequence are the prefix's prefix_len tokens
+ * (which may end inside a page), then its own; pos = prefix_len + n - n_q + i.
+ * The prefix is read once for the whole batch. window must be 0. */
+XQ_API xq_status xq_kv_attn_shared(const xq_kv_cache *cache, const xq_kv_query *query, void *workspace,
+                                   size_t ws_bytes, xq_stream stream);
 
 #ifdef __cplusplus
 }
