@@ -1,128 +1,114 @@
-// Attention over the quantized KV cache: one CTA per query row.
-//
-// The plainest form: each warp takes every fourth key, a lane holds dim / 32
-// of the row's elements, and each warp keeps the running maximum m and sum l
-// of its own keys' softmax, so that one pass over the keys suffices:
-//   m' = max(m, s),  l = l e^(m-m') + e^(s-m'),  o = o e^(m-m') + e^(s-m') v.
-#include "kv_common.cuh"
+// Attention over the quantized KV cache: which kernels a call runs, and their
+// workspace.
+#include "kv_attn.cuh"
 
 namespace xq {
 namespace {
 
-__device__ unsigned int g_kv_attn_error;
+// Query rows of a CTA: n-tiles of 8 columns, two columns a row for fp32.
+// More rows than one tile holds take two; more than two, several row chunks,
+// which read the same keys (through L2). dim 256 has registers for one.
+int pieces(const KvAttnArgs& a) { return a.type == kF32 ? 2 : 1; }
+int tiles_for(const KvAttnArgs& a, int rows) { return rows <= 8 / pieces(a) || a.c.dim == 256 ? 1 : 2; }
 
-constexpr int kWarps = 4;
+constexpr int kMaxCtas = 4 * kNumSMs;
+constexpr int kMaxRows = 16;
 
-__device__ __forceinline__ float load_elt(const void* p, int type, size_t i) {
-  return type == kF32   ? static_cast<const float*>(p)[i]
-         : type == kF16 ? __half2float(static_cast<const __half*>(p)[i])
-                        : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
+
+struct Layout {
+  size_t record, part_el, part_o, pre_el, pre_o, total;
+};
+Layout layout(const KvAttnArgs& a) {
+  Layout L;
+  const size_t rows = static_cast<size_t>(2) * kMaxCtas * kMaxRows;
+  const size_t outs = a.prefix_len > 0 ? static_cast<size_t>(a.batch) * a.n_q * a.q_heads : 0;
+  L.record = 0;
+  L.part_el = L.record + kMaxCtas * sizeof(int4);
+  L.part_o = L.part_el + rows * 8;
+  L.pre_el = L.part_o + rows * a.c.dim * 4;
+  L.pre_o = L.pre_el + round16(outs * 8);
+  L.total = L.pre_o + outs * a.c.dim * 4;
+  return L;
 }
 
-template <int BITS>
-__global__ void __launch_bounds__(32 * kWarps) kv_attn_row_kernel(const __grid_constant__ KvAttnArgs A) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.x % A.q_heads, i = blockIdx.x / A.q_heads % A.n_q, b = blockIdx.x / A.q_heads / A.n_q;
-  const int kvh = h / A.group, nb = A.c.dim / 32, mask = (1 << A.c.page_shift) - 1;
-  int n = A.lens[b];
-  const int most = A.max_pages << A.c.page_shift;
-  if (n > most) {
-    n = most;
-    atomicCAS(&g_kv_attn_error, 0u, kKvBadLen);
-  }
-  n = n < 0 ? 0 : n;
-  const int pos = kv_pos(A.prefix_len, n, A.n_q, i);
-  const int first = A.window && pos - A.window + 1 > 0 ? pos - A.window + 1 : 0;
-  const size_t at = static_cast<size_t>(blockIdx.x) * A.c.dim;
-  float q[8], o[8];
-  for (int e = 0; e < nb; ++e) {
-    q[e] = load_elt(A.q, A.type, at + 32 * e + lane) * A.scale;
-    o[e] = 0.0f;
-  }
-  float m = -1e30f, l = 0.0f;
-  for (int j = first + warp; j <= pos; j += kWarps) {
-    const bool pre = j < A.prefix_len;
-    const int t = pre ? j : j - A.prefix_len;
-    const int page = pre ? A.prefix_pages[t >> A.c.page_shift]
-                         : A.pages[static_cast<size_t>(b) * A.page_stride + (t >> A.c.page_shift)];
-    if (page < 0 || page >= A.c.n_pages) {
-      atomicCAS(&g_kv_attn_error, 0u, kKvBadPage);
-      continue;
-    }
-    const long long line = (static_cast<long long>(kvh) << A.c.page_shift) + (t & mask);
-    const uint8_t* kp = A.c.k + page * A.c.page_bytes;
-    const uint8_t* vp = A.c.v + page * A.c.page_bytes;
-    float s = 0.0f, v[8];
-    for (int e = 0; e < nb; ++e) {
-      int kc, vc;
-      if (BITS == 8) {
-        kc = kp[line * A.c.row_bytes + 32 * e + lane] - 128;
-        vc = vp[line * A.c.row_bytes + 32 * e + lane] - 128;
-      } else {
-        kc = ((kp[line * A.c.row_bytes + 16 * e + (lane & 15)] >> (lane & 16 ? 4 : 0)) & 15) - 8;
-        vc = ((vp[line * A.c.row_bytes + 16 * e + (lane & 15)] >> (lane & 16 ? 4 : 0)) & 15) - 8;
-      }
-      const long long so = A.c.scale_off + (line * nb + e) * 2;
-      s += q[e] * (kc * __half2float(*reinterpret_cast<const __half*>(kp + so)));
-      v[e] = vc * __half2float(*reinterpret_cast<const __half*>(vp + so));
-    }
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float top = fmaxf(m, s), keep = expf(m - top), p = expf(s - top);
-    l = l * keep + p;
-    for (int e = 0; e < nb; ++e) o[e] = o[e] * keep + p * v[e];
-    m = top;
-  }
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][256];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-  for (int e = 0; e < nb; ++e) so[warp][32 * e + lane] = o[e];
-  __syncthreads();
-  float top = sm[0];
-  for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-  for (int e = threadIdx.x; e < A.c.dim; e += 32 * kWarps) {
-    float sum = 0.0f, acc = 0.0f;
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = expf(sm[w] - top);
-      sum += sl[w] * f;
-      acc += so[w][e] * f;
-    }
-    const float y = sum > 0.0f || sum != sum ? acc / sum : 0.0f;
-    if (A.type == kF32)
-      static_cast<float*>(A.out)[at + e] = y;
-    else if (A.type == kF16)
-      static_cast<__half*>(A.out)[at + e] = __float2half_rn(y);
-    else
-      static_cast<__nv_bfloat16*>(A.out)[at + e] = __float2bfloat16_rn(y);
+cudaError_t run(SplitArgs& p, const KvAttnArgs& a, int bits, cudaStream_t s) {
+  const int np = pieces(a), nt = tiles_for(a, p.rows), r = nt * 8 / np;
+  p.chunks = (p.rows + r - 1) / r;
+  switch (a.c.dim) {
+    case 64: return KvAttnDim<64>::launch(p, bits, np, nt, s);
+    case 96: return KvAttnDim<96>::launch(p, bits, np, nt, s);
+    case 128: return KvAttnDim<128>::launch(p, bits, np, nt, s);
+    default: return KvAttnDim<256>::launch(p, bits, np, nt, s);
   }
 }
 
 }  // namespace
 
-size_t kv_attn_workspace(const KvAttnArgs&, int) { return 0; }
+size_t kv_attn_workspace(const KvAttnArgs& a, int) { return layout(a).total; }
 
-cudaError_t launch_kv_attn(const KvAttnArgs& a, int bits, void*, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * a.n_q * a.q_heads);
-  cfg.blockDim = dim3(32 * kWarps);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return bits == 8 ? cudaLaunchKernelEx(&cfg, kv_attn_row_kernel<8>, a) : cudaLaunchKernelEx(&cfg, kv_attn_row_kernel<4>, a);
+cudaError_t launch_kv_attn(const KvAttnArgs& a, int bits, void* workspace, cudaStream_t s) {
+  const Layout L = layout(a);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  SplitArgs p = {};
+  p.c = a.c;
+  p.type = a.type;
+  p.group = a.group;
+  p.q_heads = a.q_heads;
+  p.n_q = a.n_q;
+  p.q = a.q;
+  p.max_pages = a.max_pages;
+  p.lens = a.lens;
+  p.prefix_len = a.prefix_len;
+  p.scale = a.scale;
+  p.window = a.window;
+  p.record = reinterpret_cast<int4*>(ws + L.record);
+  p.part_el = reinterpret_cast<float*>(ws + L.part_el);
+  p.part_o = reinterpret_cast<float*>(ws + L.part_o);
+  p.pre_el = reinterpret_cast<float*>(ws + L.pre_el);
+  p.pre_o = reinterpret_cast<float*>(ws + L.pre_o);
+  p.out = a.out;
+  if (a.prefix_len > 0) {  // every row of the call against the prefix, read once
+    p.flat = true;
+    p.seqs = 1;
+    p.rows = a.batch * a.rows;
+    p.pages = a.prefix_pages;
+    const cudaError_t e = run(p, a, bits, s);
+    if (e != cudaSuccess) return e;
+    p.flat = false;
+    p.merge = true;
+  }
+  p.seqs = a.batch;
+  p.rows = a.rows;
+  p.pages = a.pages;
+  p.page_stride = a.page_stride;
+  return run(p, a, bits, s);
 }
+
+namespace {
+typedef cudaError_t (*TakeFn)(unsigned int*);
+// The first word recorded in any of the kernels' translation units; all are cleared.
+cudaError_t take_all(const TakeFn (&fns)[4], unsigned int* code) {
+  *code = 0;
+  for (TakeFn f : fns) {
+    unsigned int c = 0;
+    const cudaError_t e = f(&c);
+    if (e != cudaSuccess) return e;
+    if (*code == 0) *code = c;
+  }
+  return cudaSuccess;
+}
+}  // namespace
 
 cudaError_t take_kv_attn_error(unsigned int* code) {
-  unsigned int v = 0, z = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_kv_attn_error, sizeof(v));
-  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_kv_attn_error, &z, sizeof(z));
-  *code = v;
-  return e;
+  const TakeFn fns[4] = {KvAttnDim<64>::take_error, KvAttnDim<96>::take_error, KvAttnDim<128>::take_error,
+                         KvAttnDim<256>::take_error};
+  return take_all(fns, code);
 }
-cudaError_t take_kv_attn_check(unsigned int* code) { return take_check_word(code); }
+cudaError_t take_kv_attn_check(unsigned int* code) {
+  const TakeFn fns[4] = {KvAttnDim<64>::take_check, KvAttnDim<96>::take_check, KvAttnDim<128>::take_check,
+                         KvAttnDim<256>::take_check};
+  return take_all(fns, code);
+}
 
 }  // namespace xq

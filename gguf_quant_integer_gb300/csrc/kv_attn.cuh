@@ -1,0 +1,912 @@
+// Attention over the quantized KV cache for few query rows a KV head: a
+// split-KV kernel on the warp-level tensor cores, and the join of its parts.
+//
+// Mathematics. A CTA holds up to R query rows that read one KV head (grouped
+// heads and neighbouring query tokens) and streams that head's keys through
+// four independent warps, 16 keys at a time:
+//   scores    s = c * sum_b dk_b * (codes_b . q_b)   over the 32-value blocks b
+//   weights   p = 2^(s - e),   w_b = p * dv_b
+//   outputs   o = sum_keys w_b * codes_b,   l = sum_keys p
+// The codes are small integers, exact in fp16, so both products run on
+// m16n8k16 with the codes as the A operand (16 keys x 16 elements, then 16
+// elements x 16 keys) and block scales applied in fp32: dk to a block's sum,
+// dv to the weight. q and w enter as fp16: 16-bit queries as one number,
+// fp32 ones as two (hi + lo, 22 bits, one column each), so that a column pair
+// adds up to the fp32 product.
+// e is a running reference per query instead of the exact running maximum: it
+// moves only when some weight w would pass 2^15 (it then restarts at 2^11), which also keeps w inside
+// fp16 whatever the sizes of V. One vote per 16 keys; the rescale is rare.
+// Score columns become weight columns by movmatrix, whose 8x8 transpose takes
+// an accumulator's (key, query pair) registers to the B operand.
+//
+// What bounds it: HBM, at a few query rows. One key of dim 128 is 272 bytes of
+// Q8_0 and 544 multiply-adds a query; an SM has about 24 bytes a clock to
+// itself, against 4 instructions. Unpacking costs about one instruction per
+// value, hence no per-row work on codes, and codes loaded by ldmatrix (plain
+// for K, transposed for V) straight into operand order.
+//
+// Work split. Sequences differ in length, so the keys of all (sequence, KV
+// head, row chunk) pairs are one line of 64-key units that is cut evenly over
+// the resident CTAs. A CTA that does not cover a pair alone writes a partial
+// (o, e, l); the CTA where the pair begins leaves a record and the join kernel
+// adds the parts in order, so results do not depend on timing.
+#pragma once
+
+#include <climits>
+
+#include "kv_common.cuh"
+#include "xq_common.cuh"
+#include "xq_ptx.cuh"
+
+namespace xq {
+
+constexpr int kAttnWarps = 4;
+// A weight's second fp16 number, w - hi, is stored 2^11 larger (its column has
+// accumulators of its own, scaled back at the end): small weights, whose hi
+// is a subnormal fp16, keep their bits.
+constexpr float kLoUp = 2048.0f;
+constexpr int kAttnUnit = 16 * kAttnWarps;  // keys a unit
+
+// Kernel arguments. A pair's rows are `tokens` query tokens x group heads;
+// token and head select q's and out's row. Own pages: sequence b has the
+// tokens b * n_q .. + n_q - 1. Prefix (flat): one sequence of prefix_len keys
+// whose tokens are all batch * n_q of the call.
+struct SplitArgs {
+  KvView c;
+  int type, group, q_heads, n_q;
+  int seqs;     // sequences (1 when flat)
+  int rows;     // query rows of a pair
+  int chunks;   // row chunks of a pair
+  bool flat;
+  const void* q;
+  const int32_t* pages;
+  int page_stride, max_pages;
+  const int32_t* lens;
+  int prefix_len;
+  float scale;
+  int window;
+  int ctas;         // of the launch
+  float* part_o;    // [2 * ctas][R][dim]
+  float* part_el;   // [2 * ctas][R][2]
+  int4* record;     // [ctas]: sequence, head * chunks + chunk, last CTA (or -1)
+  // Results: out rows (o / l in the call's type), or, when flat, o and (e, l)
+  // per (token, query head) for the own pages' pass to merge.
+  void* out;
+  float* pre_o;
+  float* pre_el;
+  bool merge;       // own pages: merge pre_o, pre_el
+};
+
+template <int BITS, int D, int NP, int NT>
+struct SplitShape {
+  static constexpr int NB = D / 32;
+  static constexpr int kRow = D * BITS / 8;
+  static constexpr int kChunks = kRow / 16;          // 16-byte chunks a row
+  static constexpr int kSteps = (kChunks + 1) / 2;   // copies of 32 chunks a tile
+  static constexpr bool kPow2 = (kChunks & (kChunks - 1)) == 0;
+  // The swizzle of step x's rows (x * 32 / kChunks further down) against the
+  // first step's, on the chunk's byte offset.
+  static constexpr uint32_t turn(int x) {
+    return kChunks == 8 ? (x & 1) * 64u : kChunks == 16 ? (x & 3) * 32u : 0u;
+  }
+  static constexpr int R = NT * 8 / NP;              // query rows of a CTA
+  static constexpr int kCodes = 16 * kRow;
+  static constexpr int kScales = 16 * NB * 2;
+  static constexpr int kStage = 2 * (kCodes + kScales);
+  // Stages of 16 keys a warp: about 13 KB (three 4.25 KB stages of Q8_0 at dim
+  // 128), so that 16 warps an SM keep over 100 KB in flight.
+  static constexpr int kStages = kStage * 3 > 13312 ? 3 : 13312 / kStage > 6 ? 6 : 13312 / kStage;
+  static constexpr int kWarpBytes = kStages * kStage > R * D * 4 ? kStages * kStage : R * D * 4;
+  static constexpr int kSmem = kAttnWarps * kWarpBytes;
+  // Resident CTAs an SM: the accumulators take NT * D / 4 registers a thread.
+  static constexpr int kCtas = D == 256 ? 2 : NT == 1 ? 4 : 3;
+};
+
+// One dim's kernels, in a translation unit of their own.
+template <int D>
+struct KvAttnDim {
+  static cudaError_t launch(SplitArgs& a, int bits, int np, int nt, cudaStream_t s);
+  static cudaError_t take_error(unsigned int* code);
+  static cudaError_t take_check(unsigned int* code);
+};
+
+#ifdef XQ_KV_ATTN_IMPL
+
+namespace {
+
+__device__ unsigned int g_kv_attn_error;
+
+__device__ __forceinline__ void kv_record(unsigned what) { atomicCAS(&g_kv_attn_error, 0u, what); }
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
+// lo in the low half
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(v), "r"(mask), "r"(bits));
+  return d;
+}
+__device__ __forceinline__ uint32_t hfma2_of(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
+// fp16 pairs of codes. A stored byte u put under 0x64 is the fp16 number
+// 1024 + u, so one subtraction gives u - 128 (and u - 8 for a low nibble); a
+// high nibble in place is 1024 + 16 u, brought to u - 8 by one fma. All exact.
+__device__ __forceinline__ uint32_t bytes02(uint32_t v) { return ptx::hsub2(prmt(v, 0x64646464u, 0x4240u), 0x64806480u); }
+__device__ __forceinline__ uint32_t bytes13(uint32_t v) { return ptx::hsub2(prmt(v, 0x64646464u, 0x4341u), 0x64806480u); }
+__device__ __forceinline__ uint32_t nib_low(uint32_t v) { return ptx::hsub2(and_or(v, 0x000F000Fu, 0x64006400u), 0x64086408u); }
+__device__ __forceinline__ uint32_t nib_high(uint32_t v) {
+  return hfma2_of(and_or(v, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u);  // x / 16 - 72
+}
+
+// Byte offset of 16-byte chunk c of row r in a staged tile. The xor spreads a
+// chunk's 8 rows over all banks, for ldmatrix.
+template <int NCH>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+  const int x = NCH % 8 == 0 ? c ^ (r & 7) : NCH == 4 ? c ^ ((r >> 1) & 3) : NCH % 2 == 0 ? c ^ ((r >> 2) & 1) : c;
+  return static_cast<uint32_t>(r * NCH + x) * 16;
+}
+
+// N halves at p (4-byte aligned when N is even) as floats.
+template <int N>
+__device__ __forceinline__ void load_scales(const __half* p, float (&f)[N]) {
+  if (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint2 w = *reinterpret_cast<const uint2*>(p + i);
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+      f[i] = a.x;
+      f[(i + 1) % N] = a.y;
+      f[(i + 2) % N] = b.x;
+      f[(i + 3) % N] = b.y;
+    }
+  } else if (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(p + i));
+      f[i] = a.x;
+      f[(i + 1) % N] = a.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = __half2float(p[i]);
+  }
+}
+
+__device__ __forceinline__ float4 load4(const void* p, int type, size_t i) {
+  if (type == kF32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+  const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+  if (type == kF16) {
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ void store4(void* p, int type, size_t i, float4 v) {
+  if (type == kF32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = v;
+  } else {
+    uint2 w;
+    if (type == kF16) {
+      w.x = half2_of(v.x, v.y);
+      w.y = half2_of(v.z, v.w);
+    } else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+      w.x = *reinterpret_cast<const uint32_t*>(&a);
+      w.y = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = w;
+  }
+}
+
+// Tokens of sequence b that its table can hold.
+__device__ __forceinline__ int seq_len(const SplitArgs& A, int b) {
+  if (A.flat) return A.prefix_len;
+  const int n = A.lens[b];
+  const long long most = static_cast<long long>(A.max_pages) << A.c.page_shift;
+  return n < 0 ? 0 : n > most ? static_cast<int>(most) : n;
+}
+// First unit with a key that some query of the sequence sees (a window hides
+// earlier ones), and how many units follow. At least one, so that every row
+// has a CTA that writes it.
+__device__ __forceinline__ int first_unit(const SplitArgs& A, int n) {
+  if (!A.window) return 0;
+  const long long k = static_cast<long long>(n) - A.n_q - A.window + 1;
+  return k > 0 ? static_cast<int>(k / kAttnUnit) : 0;
+}
+__device__ __forceinline__ int unit_count(const SplitArgs& A, int n) {
+  const int u = (n + kAttnUnit - 1) / kAttnUnit - first_unit(A, n);
+  return u > 1 ? u : 1;
+}
+
+// A pair's row r of chunk base: its query token and head.
+__device__ __forceinline__ size_t row_at(const SplitArgs& A, int seq, int head, int r) {
+  const int token = r / A.group;
+  return (static_cast<size_t>(seq) * A.n_q + token) * A.q_heads + head * A.group + (r - token * A.group);
+}
+
+// Last key + 1 and first key that row r of a pair sees.
+__device__ __forceinline__ void row_range(const SplitArgs& A, int seq, int n, int r, int* start, int* end) {
+  const int token = r / A.group;
+  if (A.flat) {
+    const int b = token / A.n_q;
+    int own = A.lens[b];
+    const long long most = static_cast<long long>(A.max_pages) << A.c.page_shift;
+    own = own < 0 ? 0 : own > most ? static_cast<int>(most) : own;
+    const int pos = kv_pos(A.prefix_len, own, A.n_q, token - b * A.n_q);
+    *start = 0;
+    *end = pos + 1 < A.prefix_len ? pos + 1 : A.prefix_len;
+  } else {
+    const int pos = kv_pos(0, n, A.n_q, token);
+    *start = A.window && pos >= A.window ? pos - A.window + 1 : 0;
+    *end = pos + 1;
+  }
+}
+
+// Row (token, head) `at` of the result: sums o and l relative to 2^e.
+__device__ __forceinline__ void finish4(const SplitArgs& A, int D, size_t at, int d, float4 o, float e, float l) {
+  if (A.flat) {
+    *reinterpret_cast<float4*>(A.pre_o + at * D + d) = o;
+    if (d == 0) *reinterpret_cast<float2*>(A.pre_el + at * 2) = make_float2(e, l);
+    return;
+  }
+  if (A.merge) {
+    const float4 po = *reinterpret_cast<const float4*>(A.pre_o + at * D + d);
+    const float2 pel = *reinterpret_cast<const float2*>(A.pre_el + at * 2);
+    const float top = fmaxf(e, pel.x), f = ex2(e - top), g = ex2(pel.x - top);
+    o = make_float4(o.x * f + po.x * g, o.y * f + po.y * g, o.z * f + po.z * g, o.w * f + po.w * g);
+    l = l * f + pel.y * g;
+  }
+  // no visible key: l = 0 and the row is 0 (a NaN stays one)
+  const float4 y = l != 0.0f ? make_float4(__fdiv_rn(o.x, l), __fdiv_rn(o.y, l), __fdiv_rn(o.z, l), __fdiv_rn(o.w, l))
+                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  store4(A.out, A.type, at * D + d, y);
+}
+
+template <int NT, int M>
+__device__ __forceinline__ void scale_all(float (&o)[NT][M][4], float f) {
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      o[j][m][0] *= f;
+      o[j][m][1] *= f;
+      o[j][m][2] *= f;
+      o[j][m][3] *= f;
+    }
+}
+
+template <int BITS, int D, int NP, int NT>
+__global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::kCtas)
+    kv_split_kernel(const __grid_constant__ SplitArgs A) {
+  using S = SplitShape<BITS, D, NP, NT>;
+  constexpr int NB = S::NB, R = S::R, kStages = S::kStages, NS = NP == 2 ? 2 : 4;
+  extern __shared__ __align__(256) uint8_t smem[];  // stage and matrix addresses are put together by xor
+  __shared__ long long sh_sum[kAttnWarps];
+  __shared__ int sh_seq, sh_scan[kAttnWarps];
+  __shared__ long long sh_before;
+  __shared__ float sh_el[kAttnWarps][R][2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its place; it waits
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // ---- this CTA's units u0 .. u1-1 of the whole line, and the sequence of u0
+  const long long per = static_cast<long long>(A.c.heads) * A.chunks;
+  long long sum = 0;
+  for (int b = tid; b < A.seqs; b += 32 * kAttnWarps) sum += unit_count(A, seq_len(A, b));
+#pragma unroll
+  for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  if (lane == 0) sh_sum[warp] = sum;
+  __syncthreads();
+  sum = sh_sum[0] + sh_sum[1] + sh_sum[2] + sh_sum[3];
+  const long long total = sum * per;
+  const int ctas = total < A.ctas ? static_cast<int>(total) : A.ctas, cta = blockIdx.x;
+  if (cta >= ctas) {
+    if (tid == 0) A.record[cta] = make_int4(0, 0, -1, 0);
+    return;
+  }
+  const long long u0 = total * cta / ctas, u1 = total * (cta + 1) / ctas;
+  {
+    const long long v0 = u0 / per;
+    long long before = 0;
+    for (int base = 0; base < A.seqs; base += 32 * kAttnWarps) {
+      const int b = base + tid;
+      const int mine = b < A.seqs ? unit_count(A, seq_len(A, b)) : 0;
+      int scan = mine;
+#pragma unroll
+      for (int x = 1; x < 32; x <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, scan, x);
+        if (lane >= x) scan += o;
+      }
+      if (lane == 31) sh_scan[warp] = scan;
+      __syncthreads();
+      int add = 0, all = 0;
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) {
+        add += w < warp ? sh_scan[w] : 0;
+        all += sh_scan[w];
+      }
+      const long long end = before + add + scan;
+      if (mine && end - mine <= v0 && v0 < end) {
+        sh_seq = b;
+        sh_before = end - mine;
+      }
+      before += all;
+      __syncthreads();
+      if (before > v0) break;
+    }
+  }
+  int seq = sh_seq;
+  long long off = u0 - sh_before * per;  // units into the sequence
+
+  uint8_t* const stages = smem + warp * S::kWarpBytes;
+  const uint32_t stage0 = ptx::smem_addr(stages);
+  // Where this lane's copies of a tile go and come from. Scales: the first
+  // lanes take K's, the next ones V's.
+  const uint32_t code_to = chunk_at<S::kChunks>(lane / S::kChunks, lane % S::kChunks);
+  const long long v_off = reinterpret_cast<long long>(A.c.v) - reinterpret_cast<long long>(A.c.k);
+  const bool v_scale = lane >= S::kScales / 16;
+  const int scale_lane = (v_scale ? lane - S::kScales / 16 : lane) * 16;
+  const uint32_t scale_to = S::kCodes + scale_lane + (v_scale ? S::kCodes + S::kScales : 0);
+  const long long scale_from = A.c.scale_off + scale_lane + (v_scale ? v_off : 0);
+  bool left_record = false;
+  for (long long u = u0; u < u1;) {
+    const int n = seq_len(A, seq), nu = unit_count(A, n), f0 = first_unit(A, n);
+    if (!A.flat && tid == 0 && A.lens[seq] > n) kv_record(kKvBadLen);
+    const int pair = static_cast<int>(off / nu), k0 = static_cast<int>(off - static_cast<long long>(pair) * nu);
+    const int k1 = nu - k0 < u1 - u ? nu : k0 + static_cast<int>(u1 - u);  // units k0 .. k1-1 of the pair
+    const int head = pair / A.chunks, chunk = pair - head * A.chunks;
+    const int row0 = chunk * R, rows = A.rows - row0 < R ? A.rows - row0 : R;
+
+    // ---- queries as B operands. Column g of n-tile j: NP = 2: row 4 j + g/2, piece g & 1; NP = 1: row 8 j + g.
+    uint32_t qf[NT][D / 16][2];
+    float cs[NT][NP == 2 ? 1 : 2];
+    int lim0[NT][NP == 2 ? 1 : 2], lim1[NT][NP == 2 ? 1 : 2];
+    int all0 = 0, all1 = INT_MAX;  // keys that every row of the chunk sees
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int r = NP == 2 ? 4 * j + (g >> 1) : 8 * j + g;
+      float4 v[D / 16];
+      float top = 0.0f;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        v[k] = r < rows ? load4(A.q, A.type, row_at(A, seq, head, row0 + r) * D + 16 * k + 4 * t)
+                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        top = fmaxf(fmaxf(top, fmaxf(fabsf(v[k].x), fabsf(v[k].y))), fmaxf(fabsf(v[k].z), fabsf(v[k].w)));
+      }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // a power of two that takes the row's largest element to 2^12 .. 2^13
+      int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+      ex = ex < -100 ? -100 : ex;
+      const float up = __uint_as_float(static_cast<unsigned>(127 + 12 - ex) << 23);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const float x = v[k].x * up, y = v[k].y * up, z = v[k].z * up, w = v[k].w * up;
+        uint32_t b0 = half2_of(x, z), b1 = half2_of(y, w);
+        if (NP == 2 && (g & 1)) {  // lo = q - hi, exact in fp32
+          const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&b0));
+          const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&b1));
+          b0 = half2_of(x - h0.x, z - h0.y);
+          b1 = half2_of(y - h1.x, w - h1.y);
+        }
+        qf[j][k][0] = b0;
+        qf[j][k][1] = b1;
+      }
+      const float down = A.scale * 1.4426950408889634f * __uint_as_float(static_cast<unsigned>(127 - 12 + ex) << 23);
+#pragma unroll
+      for (int i = 0; i < (NP == 2 ? 1 : 2); ++i) {
+        // the lane that holds this accumulator column's row as column g
+        cs[j][i] = __shfl_sync(0xffffffffu, down, 8 * t + 4 * i);
+        const int rr = NP == 2 ? 4 * j + t : 8 * j + 2 * t + i;
+        lim0[j][i] = 0;
+        lim1[j][i] = 0;
+        if (rr < rows) {
+          row_range(A, seq, n, row0 + rr, &lim0[j][i], &lim1[j][i]);
+          all0 = max(all0, lim0[j][i]);
+          all1 = min(all1, lim1[j][i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int x = 1; x < 4; x <<= 1) {
+      all0 = max(all0, __shfl_xor_sync(0xffffffffu, all0, x));
+      all1 = min(all1, __shfl_xor_sync(0xffffffffu, all1, x));
+    }
+
+    // ---- the warp's tiles of 16 keys: warp, warp + 4, ... of the units
+    const int tile0 = (f0 + k0) * kAttnWarps + warp;
+    int tiles = k1 - k0;
+    {  // only tiles with keys
+      const int all = (n + 15) / 16;
+      const int have = all > tile0 ? (all - tile0 + kAttnWarps - 1) / kAttnWarps : 0;
+      tiles = tiles < have ? tiles : have;
+    }
+    const int32_t* const table = A.flat ? A.pages : A.pages + static_cast<size_t>(seq) * A.page_stride;
+    const int shift = A.c.page_shift - 4;  // tiles a page
+    // page ids of the next 32 tiles, one a lane
+    int ids = lane < tiles ? table[(tile0 + lane * kAttnWarps) >> shift] : 0, ids_next = 0;
+    unsigned bad = 0;  // stages whose page id was invalid
+    auto issue = [&](int i, int stage) {
+      if (i < tiles) {
+        if ((i & 31) == 0) {
+          if (i) ids = ids_next;
+          const int ahead = i + 32 + lane;
+          ids_next = ahead < tiles ? table[(tile0 + ahead * kAttnWarps) >> shift] : 0;
+        }
+        const int tile = tile0 + i * kAttnWarps;
+        const int page = __shfl_sync(0xffffffffu, ids, i & 31);
+        const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(A.c.n_pages);
+        bad = ok ? bad & ~(1u << stage) : bad | (1u << stage);
+        if (ok) {
+          const uint8_t* const base = A.c.k + page * A.c.page_bytes;
+          const int line = (head << A.c.page_shift) + ((tile & ((1 << shift) - 1)) << 4);
+          const uint8_t* const kc = base + (line * S::kRow + lane * 16);
+          const uint8_t* const vc = kc + v_off;
+          const uint32_t dst = stage0 + stage * S::kStage + code_to;
+#pragma unroll
+          for (int x = 0; x < S::kSteps; ++x) {
+            // 32 chunks a step; a step's rows differ from the first one's in the swizzle by a constant
+            const uint32_t to = S::kPow2 ? (dst ^ S::turn(x)) + x * 512
+                                         : dst - code_to + chunk_at<S::kChunks>((x * 32 + lane) / S::kChunks, (x * 32 + lane) % S::kChunks);
+            if (S::kChunks % 2 == 0 || x * 32 + lane < 16 * S::kChunks) {
+              cp16(to, kc + x * 512);
+              cp16(to + S::kCodes + S::kScales, vc + x * 512);
+            }
+          }
+          if (lane < 2 * S::kScales / 16) cp16(stage0 + stage * S::kStage + scale_to, base + (line * (NB * 2)) + scale_from);
+        } else if (lane == 0) {
+          kv_record(kKvBadPage);
+        }
+      }
+      cp_commit();
+    };
+
+    float o[NT][D / 16][4], er[NT][NP == 2 ? 1 : 2], l[NT][NP == 2 ? 1 : 2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int m = 0; m < D / 16; ++m) o[j][m][0] = o[j][m][1] = o[j][m][2] = o[j][m][3] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < (NP == 2 ? 1 : 2); ++i) {
+        er[j][i] = -1e30f;
+        l[j][i] = 0.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i, i);
+    int stage = 0;
+    // ldmatrix row addresses: matrix m of 4 covers rows 8 (m & 1) .. + 7, chunk m >> 1
+    const int lrow = (lane & 7) + (lane & 8), lch = lane >> 4;
+    const uint32_t code_from = chunk_at<S::kChunks>(lrow, lch);
+    // chunk c + lch (c even) of the lane's row
+    auto from = [&](uint32_t base, int c) {
+      return S::kPow2 ? (base + code_from) ^ (c * 16) : base + chunk_at<S::kChunks>(lrow, (c + lch) % S::kChunks);
+    };
+    for (int i = 0; i < tiles; ++i) {
+      cp_wait<kStages - 2>();
+      __syncwarp();  // this tile has landed for every lane, and the one before has been read by every lane
+      issue(i + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+      const uint32_t kb = stage0 + stage * S::kStage, vb = kb + S::kCodes + S::kScales;
+      const __half* ks = reinterpret_cast<const __half*>(stages + stage * S::kStage + S::kCodes);
+      const __half* vs = ks + (S::kCodes + S::kScales) / 2;
+      // ---- scores of keys g and g + 8
+      float s[NT][NS];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int x = 0; x < NS; ++x) s[j][x] = 0.0f;
+      {
+        float d0[NB], d1[NB];
+        load_scales<NB>(ks + g * NB, d0);
+        load_scales<NB>(ks + (g + 8) * NB, d1);
+        uint32_t w[4];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint32_t a0[4], a1[4];  // operands of the block's two 16-element halves
+          if (BITS == 8) {
+            ldm4(from(kb, 2 * b), w);
+            a0[0] = bytes02(w[0]);
+            a0[1] = bytes02(w[1]);
+            a0[2] = bytes13(w[0]);
+            a0[3] = bytes13(w[1]);
+            a1[0] = bytes02(w[2]);
+            a1[1] = bytes02(w[3]);
+            a1[2] = bytes13(w[2]);
+            a1[3] = bytes13(w[3]);
+          } else {
+            // one load holds two blocks (16 bytes each); an odd last one is paired with the first
+            if (b % 2 == 0) ldm4(from(kb, b), w);
+            const uint32_t x = w[2 * (b & 1)], y = w[2 * (b & 1) + 1];
+            a0[0] = nib_low(x);
+            a0[1] = nib_low(y);
+            a0[2] = nib_low(x >> 8);
+            a0[3] = nib_low(y >> 8);
+            a1[0] = nib_high(x);
+            a1[1] = nib_high(y);
+            a1[2] = nib_high(x >> 8);
+            a1[3] = nib_high(y >> 8);
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma16(c, a0, qf[j][2 * b][0], qf[j][2 * b][1]);
+            mma16(c, a1, qf[j][2 * b + 1][0], qf[j][2 * b + 1][1]);
+            if (NP == 2) {
+              s[j][0] = fmaf(d0[b], c[0] + c[1], s[j][0]);
+              s[j][1] = fmaf(d1[b], c[2] + c[3], s[j][1]);
+            } else {
+              s[j][0] = fmaf(d0[b], c[0], s[j][0]);
+              s[j][1] = fmaf(d0[b], c[1], s[j][1]);
+              s[j][NS - 2] = fmaf(d1[b], c[2], s[j][NS - 2]);
+              s[j][NS - 1] = fmaf(d1[b], c[3], s[j][NS - 1]);
+            }
+          }
+        }
+      }
+      float v0[NB], v1[NB];
+      load_scales<NB>(vs + g * NB, v0);
+      load_scales<NB>(vs + (g + 8) * NB, v1);
+      // ---- scale, and mask where the tile holds keys that some row does not see
+      const int key = (tile0 + i * kAttnWarps) * 16;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int x = 0; x < NS; ++x) s[j][x] *= cs[j][NP == 2 ? 0 : (x & 1)];
+      if (key < all0 || key + 16 > all1 || ((bad >> stage) & 1)) {
+        const bool gone = (bad >> stage) & 1;
+        const int ka = key + g, kb8 = key + g + 8;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int x = 0; x < NS; ++x) {
+            const int col = NP == 2 ? 0 : (x & 1), kk = x < NS / 2 ? ka : kb8;
+            if (gone || kk < lim0[j][col] || kk >= lim1[j][col]) s[j][x] = -INFINITY;
+          }
+        // what lies past the sequence may be anything: its scales must not reach a product
+        if (gone || ka >= n) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) v0[b] = 0.0f;
+        }
+        if (gone || kb8 >= n) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) v1[b] = 0.0f;
+        }
+      }
+      // ---- weights 2^(s - e); e moves if some weight times its largest V scale passes 2^15
+      float m0 = 5.9604645e-8f, m1 = 5.9604645e-8f;  // the least fp16 step
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        m0 = fmaxf(m0, fabsf(v0[b]));  // a Q4_0 scale may be negative
+        m1 = fmaxf(m1, fabsf(v1[b]));
+      }
+      m0 = fminf(m0, 65504.0f);
+      m1 = fminf(m1, 65504.0f);
+      float p[NT][NS];
+      bool move = false;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int x = 0; x < NS; ++x) {
+          p[j][x] = ex2(s[j][x] - er[j][NP == 2 ? 0 : (x & 1)]);
+          move |= !(p[j][x] * (x < NS / 2 ? m0 : m1) <= 32768.0f);
+        }
+      if (__any_sync(0xffffffffu, move)) {
+        const float lg0 = __log2f(m0), lg1 = __log2f(m1);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int c = 0; c < (NP == 2 ? 1 : 2); ++c) {
+            float top = fmaxf(s[j][c] + lg0, s[j][NS / 2 + c] + lg1) - 11.0f;
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            top = fmaxf(top, er[j][c]);
+            const float f = ex2(er[j][c] - top);
+            er[j][c] = top;
+            l[j][c] *= f;
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m) {
+              if (NP == 2) {
+                o[j][m][0] *= f;
+                o[j][m][1] *= f;
+                o[j][m][2] *= f;
+                o[j][m][3] *= f;
+              } else {
+                o[j][m][c] *= f;
+                o[j][m][2 + c] *= f;
+              }
+            }
+            p[j][c] = ex2(s[j][c] - top);
+            p[j][NS / 2 + c] = ex2(s[j][NS / 2 + c] - top);
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int c = 0; c < (NP == 2 ? 1 : 2); ++c) l[j][c] += p[j][c] + p[j][NS / 2 + c];
+      // ---- outputs, block by block. fp32: weights below 2^-13 would lose bits in fp16 (they count only where the larger
+      // ones meet zero codes); they follow 2^24 larger, on accumulators scaled alike, at most three times: 2^-85.
+      for (int level = 0;; ++level) {
+        float pn[NT][NS];
+        bool more = false;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int x = 0; x < NS; ++x) {
+            const bool later = NP == 2 && level < 3 && p[j][x] * (x < NS / 2 ? m0 : m1) < 1.220703125e-4f;
+            pn[j][x] = later ? 0.0f : p[j][x];
+            p[j][x] = later ? p[j][x] * 16777216.0f : 0.0f;
+            more |= p[j][x] > 0.0f;
+          }
+        uint32_t w[4];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint32_t a0[4], a1[4];
+          if (BITS == 8) {
+            ldm4t(from(vb, 2 * b), w);
+            a0[0] = bytes02(w[0]);
+            a0[1] = bytes13(w[0]);
+            a0[2] = bytes02(w[1]);
+            a0[3] = bytes13(w[1]);
+            a1[0] = bytes02(w[2]);
+            a1[1] = bytes13(w[2]);
+            a1[2] = bytes02(w[3]);
+            a1[3] = bytes13(w[3]);
+          } else {
+            if (b % 2 == 0) ldm4t(from(vb, b), w);
+            const uint32_t x = w[2 * (b & 1)], y = w[2 * (b & 1) + 1];
+            a0[0] = nib_low(x);
+            a0[1] = nib_low(x >> 8);
+            a0[2] = nib_low(y);
+            a0[3] = nib_low(y >> 8);
+            a1[0] = nib_high(x);
+            a1[1] = nib_high(x >> 8);
+            a1[2] = nib_high(y);
+            a1[3] = nib_high(y >> 8);
+          }
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            uint32_t b0, b1;
+            if (NP == 2) {
+              const float x0 = pn[j][0] * v0[b], x1 = pn[j][1] * v1[b];
+              const float h0 = __half2float(__float2half_rn(x0)), h1 = __half2float(__float2half_rn(x1));
+              b0 = transpose8(half2_of(h0, (x0 - h0) * kLoUp));
+              b1 = transpose8(half2_of(h1, (x1 - h1) * kLoUp));
+            } else {
+              b0 = transpose8(half2_of(pn[j][0] * v0[b], pn[j][1] * v0[b]));
+              b1 = transpose8(half2_of(pn[j][NS - 2] * v1[b], pn[j][NS - 1] * v1[b]));
+            }
+            mma16(o[j][2 * b], a0, b0, b1);
+            mma16(o[j][2 * b + 1], a1, b0, b1);
+          }
+        }
+        if (NP == 1 || !__any_sync(0xffffffffu, more)) {
+          if (level > 0) scale_all(o, level == 1 ? 5.9604645e-8f : level == 2 ? 3.5527137e-15f : 2.1175824e-22f);
+          break;
+        }
+        scale_all(o, 16777216.0f);
+      }
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    cp_wait<0>();
+    __syncwarp();
+
+    // ---- merge the four warps in shared memory (each in its own stage area)
+    float* const mine = reinterpret_cast<float*>(stages);
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int c = 0; c < (NP == 2 ? 1 : 2); ++c) {
+        float sum_l = l[j][c];
+        sum_l += __shfl_xor_sync(0xffffffffu, sum_l, 4);
+        sum_l += __shfl_xor_sync(0xffffffffu, sum_l, 8);
+        sum_l += __shfl_xor_sync(0xffffffffu, sum_l, 16);
+        const int r = NP == 2 ? 4 * j + t : 8 * j + 2 * t + c;
+        if (g == 0) {
+          sh_el[warp][r][0] = er[j][c];
+          sh_el[warp][r][1] = sum_l;
+        }
+#pragma unroll
+        for (int m = 0; m < D / 16; ++m) {
+          const float2 y = NP == 2 ? make_float2(fmaf(o[j][m][1], 1.0f / kLoUp, o[j][m][0]),
+                                                 fmaf(o[j][m][3], 1.0f / kLoUp, o[j][m][2]))
+                                   : make_float2(o[j][m][c], o[j][m][2 + c]);
+          *reinterpret_cast<float2*>(mine + r * D + 16 * m + 2 * g) = y;
+        }
+      }
+    __syncthreads();
+    const bool whole = k0 == 0 && k1 == nu;
+    for (int x = tid * 4; x < rows * D; x += 32 * kAttnWarps * 4) {
+      const int r = x / D, d = x - r * D;
+      float e = sh_el[0][r][0];
+#pragma unroll
+      for (int w = 1; w < kAttnWarps; ++w) e = fmaxf(e, sh_el[w][r][0]);
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float ll = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kAttnWarps; ++w) {
+        const float f = ex2(sh_el[w][r][0] - e);
+        const float4 z = *reinterpret_cast<const float4*>(smem + w * S::kWarpBytes + x * 4);
+        y = make_float4(fmaf(z.x, f, y.x), fmaf(z.y, f, y.y), fmaf(z.z, f, y.z), fmaf(z.w, f, y.w));
+        ll = fmaf(sh_el[w][r][1], f, ll);
+      }
+      if (whole) {
+        finish4(A, D, row_at(A, seq, head, row0 + r), d, y, e, ll);
+      } else {
+        // a pair that began in an earlier CTA goes to the first slot, one that goes on in the next to the second
+        const size_t ps = (static_cast<size_t>(cta) * 2 + (k0 == 0 ? 1 : 0)) * R + r;
+        *reinterpret_cast<float4*>(A.part_o + ps * D + d) = y;
+        if (d == 0) *reinterpret_cast<float2*>(A.part_el + ps * 2) = make_float2(e, ll);
+      }
+    }
+    if (!whole && k0 == 0) {
+      left_record = true;
+      if (tid == 0) {
+        // the CTA of the pair's last unit: the largest c with total * c / ctas <= last
+        const long long last = u + nu - 1;
+        const int c1 = static_cast<int>(((last + 1) * ctas - 1) / total);
+        A.record[cta] = make_int4(seq, pair, c1, 0);
+      }
+    }
+    __syncthreads();
+    const int did = k1 - k0;
+    u += did;
+    off += did;
+    if (off == static_cast<long long>(nu) * per) {
+      off = 0;
+      ++seq;
+    }
+  }
+  if (!left_record && tid == 0) A.record[cta] = make_int4(0, 0, -1, 0);
+}
+
+// The parts of the pair that begins in CTA blockIdx.x, row blockIdx.y: each
+// warp takes every fourth part, then the warps are merged.
+template <int D, int R>
+__global__ void __launch_bounds__(128) kv_join_kernel(const __grid_constant__ SplitArgs A) {
+  constexpr int kLanes = D / 4;  // threads that hold a float4 of the row
+  constexpr int kTeams = 128 / kLanes;
+  __shared__ float so[kTeams][D];
+  __shared__ float sel[kTeams][2];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 rec = A.record[blockIdx.x];
+  if (rec.z < 0) return;
+  const int head = rec.y / A.chunks, chunk = rec.y - head * A.chunks, r = blockIdx.y;
+  if (chunk * R + r >= A.rows) return;
+  const int team = threadIdx.x / kLanes, d = (threadIdx.x % kLanes) * 4, c0 = blockIdx.x;
+  float e = -1e30f, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (team < kTeams) {
+#pragma unroll 4
+    for (int c = c0 + team; c <= rec.z; c += kTeams) {
+      const size_t ps = (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * R + r;
+      const float4 z = *reinterpret_cast<const float4*>(A.part_o + ps * D + d);
+      const float2 el = *reinterpret_cast<const float2*>(A.part_el + ps * 2);
+      const float top = fmaxf(e, el.x), f = ex2(e - top), h = ex2(el.x - top);
+      o = make_float4(o.x * f + z.x * h, o.y * f + z.y * h, o.z * f + z.z * h, o.w * f + z.w * h);
+      l = l * f + el.y * h;
+      e = top;
+    }
+    *reinterpret_cast<float4*>(&so[team][d]) = o;
+    if (d == 0) {
+      sel[team][0] = e;
+      sel[team][1] = l;
+    }
+  }
+  __syncthreads();
+  if (team != 0) return;
+  e = sel[0][0];
+#pragma unroll
+  for (int w = 1; w < kTeams; ++w) e = fmaxf(e, sel[w][0]);
+  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  l = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kTeams; ++w) {
+    const float f = ex2(sel[w][0] - e);
+    const float4 z = *reinterpret_cast<const float4*>(&so[w][d]);
+    o = make_float4(fmaf(z.x, f, o.x), fmaf(z.y, f, o.y), fmaf(z.z, f, o.z), fmaf(z.w, f, o.w));
+    l = fmaf(sel[w][1], f, l);
+  }
+  finish4(A, D, row_at(A, rec.x, head, chunk * R + r), d, o, e, l);
+}
+
+template <int BITS, int D, int NP, int NT>
+cudaError_t launch_split(SplitArgs& a, cudaStream_t s) {
+  using S = SplitShape<BITS, D, NP, NT>;
+  a.ctas = S::kCtas * kNumSMs;
+  cudaError_t e = cudaFuncSetAttribute(kv_split_kernel<BITS, D, NP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
+  cfg.blockDim = dim3(32 * kAttnWarps);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kv_split_kernel<BITS, D, NP, NT>, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.ctas), S::R);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, S::R>, a);
+}
+
+}  // namespace
+
+template <int D>
+cudaError_t KvAttnDim<D>::launch(SplitArgs& a, int bits, int np, int nt, cudaStream_t s) {
+  constexpr int N2 = D == 256 ? 1 : 2;  // two n-tiles of dim 256 would not fit the registers
+  if (bits == 8)
+    return np == 2 ? (nt == 1 ? launch_split<8, D, 2, 1>(a, s) : launch_split<8, D, 2, N2>(a, s))
+                   : (nt == 1 ? launch_split<8, D, 1, 1>(a, s) : launch_split<8, D, 1, N2>(a, s));
+  return np == 2 ? (nt == 1 ? launch_split<4, D, 2, 1>(a, s) : launch_split<4, D, 2, N2>(a, s))
+                 : (nt == 1 ? launch_split<4, D, 1, 1>(a, s) : launch_split<4, D, 1, N2>(a, s));
+}
+
+template <int D>
+cudaError_t KvAttnDim<D>::take_error(unsigned int* code) {
+  unsigned int v = 0, z = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_kv_attn_error, sizeof(v));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_kv_attn_error, &z, sizeof(z));
+  *code = v;
+  return e;
+}
+
+template <int D>
+cudaError_t KvAttnDim<D>::take_check(unsigned int* code) {
+  return take_check_word(code);
+}
+
+#endif  // XQ_KV_ATTN_IMPL
+
+}  // namespace xq
