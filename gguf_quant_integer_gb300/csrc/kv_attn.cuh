@@ -45,7 +45,12 @@ constexpr int kAttnWarps = 4;
 // accumulators of its own, scaled back at the end): small weights, whose hi
 // is a subnormal fp16, keep their bits.
 constexpr float kLoUp = 2048.0f;
+constexpr float kWeightTop = 32768.0f, kWeightLow = 1.220703125e-4f;  // 2^15, 2^-13
 constexpr int kAttnUnit = 16 * kAttnWarps;  // keys a unit
+// Units of time that a CTA spends on a pair besides its keys (queries, page
+// ids, filling the pipeline, merging): the cut counts them, or CTAs with many
+// short sequences would finish last.
+constexpr int kAttnHead = 2;
 
 // Kernel arguments. A pair's rows are `tokens` query tokens x group heads;
 // token and head select q's and out's row. Own pages: sequence b has the
@@ -144,6 +149,12 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
@@ -189,30 +200,40 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return static_cast<uint32_t>(r * NCH + x) * 16;
 }
 
-// N halves at p (4-byte aligned when N is even) as floats.
+// N halves at p (4-byte aligned when N is even) as floats, and their largest magnitude.
 template <int N>
-__device__ __forceinline__ void load_scales(const __half* p, float (&f)[N]) {
-  if (N % 4 == 0) {
+__device__ __forceinline__ float load_scales(const __half* p, float (&f)[N]) {
+  if constexpr (N % 2 == 0) {
+    uint32_t w[N / 2];
+    if constexpr (N % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const uint2 w = *reinterpret_cast<const uint2*>(p + i);
-      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
-      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-      f[i] = a.x;
-      f[(i + 1) % N] = a.y;
-      f[(i + 2) % N] = b.x;
-      f[(i + 3) % N] = b.y;
-    }
-  } else if (N % 2 == 0) {
+      for (int i = 0; i < N / 4; ++i) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p + 4 * i);
+        w[2 * i] = v.x;
+        w[2 * i + 1] = v.y;
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(p + i));
-      f[i] = a.x;
-      f[(i + 1) % N] = a.y;
+      for (int i = 0; i < N / 2; ++i) w[i] = *reinterpret_cast<const uint32_t*>(p + 2 * i);
     }
+    __half2 top = __habs2(*reinterpret_cast<const __half2*>(&w[0]));
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const __half2 h = *reinterpret_cast<const __half2*>(&w[i]);
+      const float2 v = __half22float2(h);
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
+      if (i) top = __hmax2(top, __habs2(h));
+    }
+    return __half2float(__hmax(__low2half(top), __high2half(top)));
   } else {
+    float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = __half2float(p[i]);
+    for (int i = 0; i < N; ++i) {
+      f[i] = __half2float(p[i]);
+      top = fmaxf(top, fabsf(f[i]));
+    }
+    return top;
   }
 }
 
@@ -254,7 +275,7 @@ __device__ __forceinline__ int seq_len(const SplitArgs& A, int b) {
 }
 // First unit with a key that some query of the sequence sees (a window hides
 // earlier ones), and how many units follow. At least one, so that every row
-// has a CTA that writes it.
+// has a CTA that writes it. A pair counts kAttnHead more.
 __device__ __forceinline__ int first_unit(const SplitArgs& A, int n) {
   if (!A.window) return 0;
   const long long k = static_cast<long long>(n) - A.n_q - A.window + 1;
@@ -339,7 +360,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
   // ---- this CTA's units u0 .. u1-1 of the whole line, and the sequence of u0
   const long long per = static_cast<long long>(A.c.heads) * A.chunks;
   long long sum = 0;
-  for (int b = tid; b < A.seqs; b += 32 * kAttnWarps) sum += unit_count(A, seq_len(A, b));
+  for (int b = tid; b < A.seqs; b += 32 * kAttnWarps) sum += unit_count(A, seq_len(A, b)) + kAttnHead;
 #pragma unroll
   for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
   if (lane == 0) sh_sum[warp] = sum;
@@ -357,7 +378,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
     long long before = 0;
     for (int base = 0; base < A.seqs; base += 32 * kAttnWarps) {
       const int b = base + tid;
-      const int mine = b < A.seqs ? unit_count(A, seq_len(A, b)) : 0;
+      const int mine = b < A.seqs ? unit_count(A, seq_len(A, b)) + kAttnHead : 0;
       int scan = mine;
 #pragma unroll
       for (int x = 1; x < 32; x <<= 1) {
@@ -397,10 +418,21 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
   const long long scale_from = A.c.scale_off + scale_lane + (v_scale ? v_off : 0);
   bool left_record = false;
   for (long long u = u0; u < u1;) {
-    const int n = seq_len(A, seq), nu = unit_count(A, n), f0 = first_unit(A, n);
+    const int n = seq_len(A, seq), nu = unit_count(A, n), nv = nu + kAttnHead, f0 = first_unit(A, n);
     if (!A.flat && tid == 0 && A.lens[seq] > n) kv_record(kKvBadLen);
-    const int pair = static_cast<int>(off / nu), k0 = static_cast<int>(off - static_cast<long long>(pair) * nu);
-    const int k1 = nu - k0 < u1 - u ? nu : k0 + static_cast<int>(u1 - u);  // units k0 .. k1-1 of the pair
+    const int pair = static_cast<int>(off / nv), at = static_cast<int>(off - static_cast<long long>(pair) * nv);
+    const int did = nv - at < u1 - u ? nv - at : static_cast<int>(u1 - u);
+    // units k0 .. k1-1 of the pair's keys; a CTA that gets only from its head leaves the pair to the next
+    const int k0 = at > kAttnHead ? at - kAttnHead : 0, k1 = at + did - kAttnHead;
+    const long long first = u - at;  // where the pair begins
+    u += did;
+    off += did;
+    const int sq = seq;
+    if (off == nv * per) {
+      off = 0;
+      ++seq;
+    }
+    if (k1 <= 0) continue;
     const int head = pair / A.chunks, chunk = pair - head * A.chunks;
     const int row0 = chunk * R, rows = A.rows - row0 < R ? A.rows - row0 : R;
 
@@ -416,7 +448,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
       float top = 0.0f;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        v[k] = r < rows ? load4(A.q, A.type, row_at(A, seq, head, row0 + r) * D + 16 * k + 4 * t)
+        v[k] = r < rows ? load4(A.q, A.type, row_at(A, sq, head, row0 + r) * D + 16 * k + 4 * t)
                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         top = fmaxf(fmaxf(top, fmaxf(fabsf(v[k].x), fabsf(v[k].y))), fmaxf(fabsf(v[k].z), fabsf(v[k].w)));
       }
@@ -448,7 +480,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
         lim0[j][i] = 0;
         lim1[j][i] = 0;
         if (rr < rows) {
-          row_range(A, seq, n, row0 + rr, &lim0[j][i], &lim1[j][i]);
+          row_range(A, sq, n, row0 + rr, &lim0[j][i], &lim1[j][i]);
           all0 = max(all0, lim0[j][i]);
           all1 = min(all1, lim1[j][i]);
         }
@@ -468,7 +500,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
       const int have = all > tile0 ? (all - tile0 + kAttnWarps - 1) / kAttnWarps : 0;
       tiles = tiles < have ? tiles : have;
     }
-    const int32_t* const table = A.flat ? A.pages : A.pages + static_cast<size_t>(seq) * A.page_stride;
+    const int32_t* const table = A.flat ? A.pages : A.pages + static_cast<size_t>(sq) * A.page_stride;
     const int shift = A.c.page_shift - 4;  // tiles a page
     // page ids of the next 32 tiles, one a lane
     int ids = lane < tiles ? table[(tile0 + lane * kAttnWarps) >> shift] : 0, ids_next = 0;
@@ -575,8 +607,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
           }
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma16(c, a0, qf[j][2 * b][0], qf[j][2 * b][1]);
+            float c[4];
+            mma16_first(c, a0, qf[j][2 * b][0], qf[j][2 * b][1]);
             mma16(c, a1, qf[j][2 * b + 1][0], qf[j][2 * b + 1][1]);
             if (NP == 2) {
               s[j][0] = fmaf(d0[b], c[0] + c[1], s[j][0]);
@@ -591,8 +623,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
         }
       }
       float v0[NB], v1[NB];
-      load_scales<NB>(vs + g * NB, v0);
-      load_scales<NB>(vs + (g + 8) * NB, v1);
+      float m0 = load_scales<NB>(vs + g * NB, v0), m1 = load_scales<NB>(vs + (g + 8) * NB, v1);
       // ---- scale, and mask where the tile holds keys that some row does not see
       const int key = (tile0 + i * kAttnWarps) * 16;
 #pragma unroll
@@ -613,31 +644,38 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
         if (gone || ka >= n) {
 #pragma unroll
           for (int b = 0; b < NB; ++b) v0[b] = 0.0f;
+          m0 = 0.0f;
         }
         if (gone || kb8 >= n) {
 #pragma unroll
           for (int b = 0; b < NB; ++b) v1[b] = 0.0f;
+          m1 = 0.0f;
         }
       }
-      // ---- weights 2^(s - e); e moves if some weight times its largest V scale passes 2^15
-      float m0 = 5.9604645e-8f, m1 = 5.9604645e-8f;  // the least fp16 step
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        m0 = fmaxf(m0, fabsf(v0[b]));  // a Q4_0 scale may be negative
-        m1 = fmaxf(m1, fabsf(v1[b]));
-      }
-      m0 = fminf(m0, 65504.0f);
-      m1 = fminf(m1, 65504.0f);
+      // ---- weights p = 2^(s - e). w: p times the key's largest V scale (no less than the least fp16 step). e moves if some
+      // w passes 2^15; the fp32 form also looks for weights below 2^-13.
+      m0 = fminf(fmaxf(m0, 5.9604645e-8f), 65504.0f);
+      m1 = fminf(fmaxf(m1, 5.9604645e-8f), 65504.0f);
       float p[NT][NS];
-      bool move = false;
+      bool odd = false;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int x = 0; x < NS; ++x) {
           p[j][x] = ex2(s[j][x] - er[j][NP == 2 ? 0 : (x & 1)]);
-          move |= !(p[j][x] * (x < NS / 2 ? m0 : m1) <= 32768.0f);
+          const float w = p[j][x] * (x < NS / 2 ? m0 : m1);
+          odd |= !(w <= kWeightTop && (NP == 1 || w >= kWeightLow));
         }
-      if (__any_sync(0xffffffffu, move)) {
+      const bool any_odd = __any_sync(0xffffffffu, odd);
+      if (any_odd) {
+        bool move = false;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int x = 0; x < NS; ++x) move |= !(p[j][x] * (x < NS / 2 ? m0 : m1) <= kWeightTop);
+        odd = __any_sync(0xffffffffu, move);
+      }
+      if (any_odd && odd) {
         const float lg0 = __log2f(m0), lg1 = __log2f(m1);
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -674,17 +712,19 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
       // ---- outputs, block by block. fp32: weights below 2^-13 would lose bits in fp16 (they count only where the larger
       // ones meet zero codes); they follow 2^24 larger, on accumulators scaled alike, at most three times: 2^-85.
       for (int level = 0;; ++level) {
-        float pn[NT][NS];
+        float rest[NT][NS];
         bool more = false;
+        if (NP == 2 && any_odd) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+          for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int x = 0; x < NS; ++x) {
-            const bool later = NP == 2 && level < 3 && p[j][x] * (x < NS / 2 ? m0 : m1) < 1.220703125e-4f;
-            pn[j][x] = later ? 0.0f : p[j][x];
-            p[j][x] = later ? p[j][x] * 16777216.0f : 0.0f;
-            more |= p[j][x] > 0.0f;
-          }
+            for (int x = 0; x < NS; ++x) {
+              const bool later = level < 3 && p[j][x] * (x < NS / 2 ? m0 : m1) < kWeightLow;
+              rest[j][x] = later ? p[j][x] * 16777216.0f : 0.0f;
+              p[j][x] = later ? 0.0f : p[j][x];
+              more |= rest[j][x] > 0.0f;
+            }
+        }
         uint32_t w[4];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -715,23 +755,32 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
           for (int j = 0; j < NT; ++j) {
             uint32_t b0, b1;
             if (NP == 2) {
-              const float x0 = pn[j][0] * v0[b], x1 = pn[j][1] * v1[b];
-              const float h0 = __half2float(__float2half_rn(x0)), h1 = __half2float(__float2half_rn(x1));
-              b0 = transpose8(half2_of(h0, (x0 - h0) * kLoUp));
-              b1 = transpose8(half2_of(h1, (x1 - h1) * kLoUp));
+              const ptx::f2 up = ptx::pk(kLoUp, kLoUp), down = ptx::pk(-kLoUp, -kLoUp);
+              const ptx::f2 x = ptx::mul2(ptx::pk(p[j][0], p[j][1]), ptx::pk(v0[b], v1[b]));
+              const uint32_t hi = half2_of(ptx::lo32(x), ptx::hi32(x));
+              const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+              const ptx::f2 r = ptx::fma2(ptx::pk(h.x, h.y), down, ptx::mul2(x, up));  // (w - hi) * 2^11, exact
+              const uint32_t lo = half2_of(ptx::lo32(r), ptx::hi32(r));
+              b0 = transpose8(prmt(hi, lo, 0x5410u));
+              b1 = transpose8(prmt(hi, lo, 0x7632u));
             } else {
-              b0 = transpose8(half2_of(pn[j][0] * v0[b], pn[j][1] * v0[b]));
-              b1 = transpose8(half2_of(pn[j][NS - 2] * v1[b], pn[j][NS - 1] * v1[b]));
+              b0 = transpose8(half2_of(p[j][0] * v0[b], p[j][1] * v0[b]));
+              b1 = transpose8(half2_of(p[j][NS - 2] * v1[b], p[j][NS - 1] * v1[b]));
             }
             mma16(o[j][2 * b], a0, b0, b1);
             mma16(o[j][2 * b + 1], a1, b0, b1);
           }
         }
-        if (NP == 1 || !__any_sync(0xffffffffu, more)) {
+        if (NP == 1 || !any_odd) break;
+        if (!__any_sync(0xffffffffu, more)) {
           if (level > 0) scale_all(o, level == 1 ? 5.9604645e-8f : level == 2 ? 3.5527137e-15f : 2.1175824e-22f);
           break;
         }
         scale_all(o, 16777216.0f);
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int x = 0; x < NS; ++x) p[j][x] = rest[j][x];
       }
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
@@ -778,7 +827,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
         ll = fmaf(sh_el[w][r][1], f, ll);
       }
       if (whole) {
-        finish4(A, D, row_at(A, seq, head, row0 + r), d, y, e, ll);
+        finish4(A, D, row_at(A, sq, head, row0 + r), d, y, e, ll);
       } else {
         // a pair that began in an earlier CTA goes to the first slot, one that goes on in the next to the second
         const size_t ps = (static_cast<size_t>(cta) * 2 + (k0 == 0 ? 1 : 0)) * R + r;
@@ -790,19 +839,12 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
       left_record = true;
       if (tid == 0) {
         // the CTA of the pair's last unit: the largest c with total * c / ctas <= last
-        const long long last = u + nu - 1;
+        const long long last = first + nv - 1;
         const int c1 = static_cast<int>(((last + 1) * ctas - 1) / total);
-        A.record[cta] = make_int4(seq, pair, c1, 0);
+        A.record[cta] = make_int4(sq, pair, c1, 0);
       }
     }
     __syncthreads();
-    const int did = k1 - k0;
-    u += did;
-    off += did;
-    if (off == static_cast<long long>(nu) * per) {
-      off = 0;
-      ++seq;
-    }
   }
   if (!left_record && tid == 0) A.record[cta] = make_int4(0, 0, -1, 0);
 }
