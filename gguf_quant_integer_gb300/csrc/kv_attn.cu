@@ -5,12 +5,24 @@
 namespace xq {
 namespace {
 
-// Query rows of a CTA: n-tiles of 8 columns, two columns a row for fp32.
-// More rows than one tile holds take two; more than two, several row chunks,
-// which read the same keys (through L2). dim 256 has registers for one.
-int pieces(const KvAttnArgs& a) { return a.type == kF32 ? 2 : 1; }
-int tiles_for(const KvAttnArgs& a, int rows) { return rows <= 8 / pieces(a) || a.c.dim == 256 ? 1 : 2; }
+// Query rows of a CTA: n-tiles of 8 columns. fp32 takes two columns a row (its
+// two fp16 numbers). So do 16-bit queries of at most 4 rows, which have the
+// columns to spare: the weights' second numbers make them as exact as the
+// result's type, and a lane has half the scores. More rows than one tile holds
+// take two, more than two several row chunks, which read the same keys
+// (through L2). dim 256 has registers for one tile.
+struct Rows {
+  bool exact;
+  int np, nt;
+};
+Rows rows_for(const KvAttnArgs& a, int rows) {
+  const bool exact = a.type == kF32;
+  if (exact || rows <= 4) return {exact, 2, rows <= 4 || a.c.dim == 256 ? 1 : 2};
+  return {exact, 1, rows <= 8 || a.c.dim == 256 ? 1 : 2};
+}
 
+// The most CTAs and rows of partial results: four resident CTAs an SM of 4 or
+// 8 rows, three of up to 16.
 constexpr int kMaxCtas = 4 * kNumSMs;
 constexpr int kMaxRows = 16;
 
@@ -33,13 +45,17 @@ Layout layout(const KvAttnArgs& a) {
 }
 
 cudaError_t run(SplitArgs& p, const KvAttnArgs& a, int bits, cudaStream_t s) {
-  const int np = pieces(a), nt = tiles_for(a, p.rows), r = nt * 8 / np;
+  const Rows f = rows_for(a, p.rows);
+  const int r = f.nt * 8 / f.np;
   p.chunks = (p.rows + r - 1) / r;
+  const long long keys = p.flat ? p.prefix_len : static_cast<long long>(p.max_pages) << p.c.page_shift;
+  const long long units = (keys + kAttnUnit - 1) / kAttnUnit;
+  p.units = p.seqs * ((units > 1 ? units : 1) + kAttnHead) * p.c.heads * p.chunks;
   switch (a.c.dim) {
-    case 64: return KvAttnDim<64>::launch(p, bits, np, nt, s);
-    case 96: return KvAttnDim<96>::launch(p, bits, np, nt, s);
-    case 128: return KvAttnDim<128>::launch(p, bits, np, nt, s);
-    default: return KvAttnDim<256>::launch(p, bits, np, nt, s);
+    case 64: return KvAttnDim<64>::launch(p, bits, f.exact, f.np, f.nt, s);
+    case 96: return KvAttnDim<96>::launch(p, bits, f.exact, f.np, f.nt, s);
+    case 128: return KvAttnDim<128>::launch(p, bits, f.exact, f.np, f.nt, s);
+    default: return KvAttnDim<256>::launch(p, bits, f.exact, f.np, f.nt, s);
   }
 }
 

@@ -50,8 +50,7 @@ constexpr int kAttnUnit = 16 * kAttnWarps;  // keys a unit
 // Units of time that a CTA spends on a pair besides its keys (queries, page
 // ids, filling the pipeline, merging): the cut counts them, or CTAs with many
 // short sequences would finish last.
-constexpr int kAttnHead = 2;
-
+constexpr int kAttnHead = 5;
 // Kernel arguments. A pair's rows are `tokens` query tokens x group heads;
 // token and head select q's and out's row. Own pages: sequence b has the
 // tokens b * n_q .. + n_q - 1. Prefix (flat): one sequence of prefix_len keys
@@ -70,7 +69,8 @@ struct SplitArgs {
   int prefix_len;
   float scale;
   int window;
-  int ctas;         // of the launch
+  long long units;  // upper bound of the launch's units
+  int ctas;         // of the launch: as many as run at a time, or one a unit
   float* part_o;    // [2 * ctas][R][dim]
   float* part_el;   // [2 * ctas][R][2]
   int4* record;     // [ctas]: sequence, head * chunks + chunk, last CTA (or -1)
@@ -82,7 +82,7 @@ struct SplitArgs {
   bool merge;       // own pages: merge pre_o, pre_el
 };
 
-template <int BITS, int D, int NP, int NT>
+template <int BITS, int D, bool EX, int NP, int NT>
 struct SplitShape {
   static constexpr int NB = D / 32;
   static constexpr int kRow = D * BITS / 8;
@@ -110,7 +110,7 @@ struct SplitShape {
 // One dim's kernels, in a translation unit of their own.
 template <int D>
 struct KvAttnDim {
-  static cudaError_t launch(SplitArgs& a, int bits, int np, int nt, cudaStream_t s);
+  static cudaError_t launch(SplitArgs& a, int bits, bool exact, int np, int nt, cudaStream_t s);
   static cudaError_t take_error(unsigned int* code);
   static cudaError_t take_check(unsigned int* code);
 };
@@ -191,6 +191,17 @@ __device__ __forceinline__ uint32_t nib_low(uint32_t v) { return ptx::hsub2(and_
 __device__ __forceinline__ uint32_t nib_high(uint32_t v) {
   return hfma2_of(and_or(v, 0x00F000F0u, 0x64006400u), 0x2C002C00u, 0xD480D480u);  // x / 16 - 72
 }
+
+// The same codes as stored, u = q + 128 or q + 8: a zero-extended byte or nibble is the subnormal fp16 u * 2^-24, exact in
+// the tensor cores, one instruction for two values. 16-bit queries (EX = false) take K this way, and the offset out of a
+// block's score through the block's sum of q: the sums then pass through values larger than their result by the offset over
+// a typical code, which costs a few of fp32's bits. fp32 queries, which have to keep them, subtract from each code, and V
+// always does (its sum runs over keys, and a small output beside a large weight on a zero code would be lost).
+// A high nibble in place is 16 u * 2^-24: its query elements are stored 16 times smaller.
+__device__ __forceinline__ uint32_t raw02(uint32_t v) { return prmt(v, 0u, 0x4240u); }
+__device__ __forceinline__ uint32_t raw13(uint32_t v) { return prmt(v, 0u, 0x4341u); }
+__device__ __forceinline__ uint32_t raw_low(uint32_t v) { return v & 0x000F000Fu; }
+__device__ __forceinline__ uint32_t raw_high(uint32_t v) { return v & 0x00F000F0u; }
 
 // Byte offset of 16-byte chunk c of row r in a staged tile. The xor spreads a
 // chunk's 8 rows over all banks, for ldmatrix.
@@ -343,11 +354,11 @@ __device__ __forceinline__ void scale_all(float (&o)[NT][M][4], float f) {
     }
 }
 
-template <int BITS, int D, int NP, int NT>
-__global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::kCtas)
+template <int BITS, int D, bool EX, int NP, int NT>
+__global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, NT>::kCtas)
     kv_split_kernel(const __grid_constant__ SplitArgs A) {
-  using S = SplitShape<BITS, D, NP, NT>;
-  constexpr int NB = S::NB, R = S::R, kStages = S::kStages, NS = NP == 2 ? 2 : 4;
+  using S = SplitShape<BITS, D, EX, NP, NT>;
+  constexpr int NB = S::NB, R = S::R, kStages = S::kStages, NS = NP == 2 ? 2 : 4, NQ = NP == 2 ? 1 : 2;
   extern __shared__ __align__(256) uint8_t smem[];  // stage and matrix addresses are put together by xor
   __shared__ long long sh_sum[kAttnWarps];
   __shared__ int sh_seq, sh_scan[kAttnWarps];
@@ -415,7 +426,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
   const bool v_scale = lane >= S::kScales / 16;
   const int scale_lane = (v_scale ? lane - S::kScales / 16 : lane) * 16;
   const uint32_t scale_to = S::kCodes + scale_lane + (v_scale ? S::kCodes + S::kScales : 0);
-  const long long scale_from = A.c.scale_off + scale_lane + (v_scale ? v_off : 0);
+  const long long scale_from = A.c.scale_off + scale_lane - lane * 16 + (v_scale ? v_off : 0);  // from this lane's code chunk
   bool left_record = false;
   for (long long u = u0; u < u1;) {
     const int n = seq_len(A, seq), nu = unit_count(A, n), nv = nu + kAttnHead, f0 = first_unit(A, n);
@@ -438,8 +449,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
 
     // ---- queries as B operands. Column g of n-tile j: NP = 2: row 4 j + g/2, piece g & 1; NP = 1: row 8 j + g.
     uint32_t qf[NT][D / 16][2];
-    float cs[NT][NP == 2 ? 1 : 2];
-    int lim0[NT][NP == 2 ? 1 : 2], lim1[NT][NP == 2 ? 1 : 2];
+    float cs[NT][NQ], qs[NT][NB][NQ];  // score factor, and -(128 or 8) sum(q) of each block, of this lane's columns
+    int lim0[NT][NQ], lim1[NT][NQ];
     int all0 = 0, all1 = INT_MAX;  // keys that every row of the chunk sees
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -460,7 +471,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
       const float up = __uint_as_float(static_cast<unsigned>(127 + 12 - ex) << 23);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const float x = v[k].x * up, y = v[k].y * up, z = v[k].z * up, w = v[k].w * up;
+        // the elements of high nibbles 16 times smaller
+        const float f = !EX && BITS == 4 && (k & 1) ? up * 0.0625f : up;
+        const float x = v[k].x * f, y = v[k].y * f, z = v[k].z * f, w = v[k].w * f;
         uint32_t b0 = half2_of(x, z), b1 = half2_of(y, w);
         if (NP == 2 && (g & 1)) {  // lo = q - hi, exact in fp32
           const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&b0));
@@ -471,9 +484,33 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
         qf[j][k][0] = b0;
         qf[j][k][1] = b1;
       }
-      const float down = A.scale * 1.4426950408889634f * __uint_as_float(static_cast<unsigned>(127 - 12 + ex) << 23);
+      float block_sum[NB];
 #pragma unroll
-      for (int i = 0; i < (NP == 2 ? 1 : 2); ++i) {
+      for (int b = 0; b < NB; ++b) {
+        float sum2[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float2 u0 = __half22float2(*reinterpret_cast<const __half2*>(&qf[j][2 * b + x][0]));
+          const float2 u1 = __half22float2(*reinterpret_cast<const __half2*>(&qf[j][2 * b + x][1]));
+          sum2[x] = (u0.x + u0.y) + (u1.x + u1.y);
+        }
+        float sum = BITS == 4 ? fmaf(sum2[1], 16.0f, sum2[0]) : sum2[0] + sum2[1];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        block_sum[b] = sum * (BITS == 4 ? -8.0f * 5.9604645e-8f : -128.0f * 5.9604645e-8f);
+      }
+      const float down = A.scale * 1.4426950408889634f * __uint_as_float(static_cast<unsigned>(127 - 12 + (EX ? 0 : 24) + ex) << 23);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        if (NP == 2) {  // both pieces
+          qs[j][b][0] = __shfl_sync(0xffffffffu, block_sum[b], 8 * t) + __shfl_sync(0xffffffffu, block_sum[b], 8 * t + 4);
+        } else {
+          qs[j][b][0] = __shfl_sync(0xffffffffu, block_sum[b], 8 * t);
+          qs[j][b][NQ - 1] = __shfl_sync(0xffffffffu, block_sum[b], 8 * t + 4);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
         // the lane that holds this accumulator column's row as column g
         cs[j][i] = __shfl_sync(0xffffffffu, down, 8 * t + 4 * i);
         const int rr = NP == 2 ? 4 * j + t : 8 * j + 2 * t + i;
@@ -502,51 +539,65 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
     }
     const int32_t* const table = A.flat ? A.pages : A.pages + static_cast<size_t>(sq) * A.page_stride;
     const int shift = A.c.page_shift - 4;  // tiles a page
-    // page ids of the next 32 tiles, one a lane
-    int ids = lane < tiles ? table[(tile0 + lane * kAttnWarps) >> shift] : 0, ids_next = 0;
+    // Where the next 32 tiles lie, one a lane: the address of its K codes (0 if its page id is invalid), and from there to
+    // its K scales. The page ids after them are on their way.
+    auto page_of = [&](int i) { return i < tiles ? table[(tile0 + i * kAttnWarps) >> shift] : 0; };
+    long long code_at = 0;
+    int scales_at = 0;
+    auto locate = [&](int i, int page) {
+      const int line = (head << A.c.page_shift) + (((tile0 + i * kAttnWarps) & ((1 << shift) - 1)) << 4);
+      const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(A.c.n_pages);
+      code_at = ok ? reinterpret_cast<long long>(A.c.k) + page * A.c.page_bytes + line * S::kRow : 0;
+      scales_at = line * (NB * 2 - S::kRow);
+    };
+    locate(lane, page_of(lane));
+    int next_page = page_of(32 + lane);
     unsigned bad = 0;  // stages whose page id was invalid
+    // tiles clean .. clean + clean_n - 1 hold only keys that every row sees
+    int clean = ((all0 + 15) / 16 - tile0 + kAttnWarps - 1) / kAttnWarps;
+    clean = clean > 0 ? clean : 0;
+    unsigned clean_n = all1 / 16 > tile0 ? static_cast<unsigned>((all1 / 16 - tile0 + kAttnWarps - 1) / kAttnWarps) : 0u;
+    clean_n = clean_n > static_cast<unsigned>(clean) ? clean_n - clean : 0u;
     auto issue = [&](int i, int stage) {
       if (i < tiles) {
-        if ((i & 31) == 0) {
-          if (i) ids = ids_next;
-          const int ahead = i + 32 + lane;
-          ids_next = ahead < tiles ? table[(tile0 + ahead * kAttnWarps) >> shift] : 0;
+        if ((i & 31) == 0 && i > 0) {
+          locate(i + lane, next_page);
+          next_page = page_of(i + 32 + lane);
         }
-        const int tile = tile0 + i * kAttnWarps;
-        const int page = __shfl_sync(0xffffffffu, ids, i & 31);
-        const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(A.c.n_pages);
-        bad = ok ? bad & ~(1u << stage) : bad | (1u << stage);
-        if (ok) {
-          const uint8_t* const base = A.c.k + page * A.c.page_bytes;
-          const int line = (head << A.c.page_shift) + ((tile & ((1 << shift) - 1)) << 4);
-          const uint8_t* const kc = base + (line * S::kRow + lane * 16);
+        const unsigned lo = __shfl_sync(0xffffffffu, static_cast<unsigned>(code_at), i & 31);
+        const unsigned hi = __shfl_sync(0xffffffffu, static_cast<unsigned>(code_at >> 32), i & 31);
+        const int so = __shfl_sync(0xffffffffu, scales_at, i & 31);
+        if (hi != 0) {
+          const uint8_t* const kc = reinterpret_cast<const uint8_t*>((static_cast<long long>(hi) << 32) + lo + lane * 16);
           const uint8_t* const vc = kc + v_off;
-          const uint32_t dst = stage0 + stage * S::kStage + code_to;
+          const uint32_t base = stage0 + stage * S::kStage, dst = base + code_to;
 #pragma unroll
           for (int x = 0; x < S::kSteps; ++x) {
             // 32 chunks a step; a step's rows differ from the first one's in the swizzle by a constant
             const uint32_t to = S::kPow2 ? (dst ^ S::turn(x)) + x * 512
-                                         : dst - code_to + chunk_at<S::kChunks>((x * 32 + lane) / S::kChunks, (x * 32 + lane) % S::kChunks);
+                                         : base + chunk_at<S::kChunks>((x * 32 + lane) / S::kChunks, (x * 32 + lane) % S::kChunks);
             if (S::kChunks % 2 == 0 || x * 32 + lane < 16 * S::kChunks) {
               cp16(to, kc + x * 512);
               cp16(to + S::kCodes + S::kScales, vc + x * 512);
             }
           }
-          if (lane < 2 * S::kScales / 16) cp16(stage0 + stage * S::kStage + scale_to, base + (line * (NB * 2)) + scale_from);
-        } else if (lane == 0) {
-          kv_record(kKvBadPage);
+          if (lane < 2 * S::kScales / 16) cp16(base + scale_to, kc + (scale_from + so));
+        } else {
+          bad |= 1u << stage;
+          clean_n = 0;
+          if (lane == 0) kv_record(kKvBadPage);
         }
       }
       cp_commit();
     };
 
-    float o[NT][D / 16][4], er[NT][NP == 2 ? 1 : 2], l[NT][NP == 2 ? 1 : 2];
+    float o[NT][D / 16][4], er[NT][NQ], l[NT][NQ];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
 #pragma unroll
       for (int m = 0; m < D / 16; ++m) o[j][m][0] = o[j][m][1] = o[j][m][2] = o[j][m][3] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < (NP == 2 ? 1 : 2); ++i) {
+      for (int i = 0; i < NQ; ++i) {
         er[j][i] = -1e30f;
         l[j][i] = 0.0f;
       }
@@ -584,32 +635,40 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
           uint32_t a0[4], a1[4];  // operands of the block's two 16-element halves
           if (BITS == 8) {
             ldm4(from(kb, 2 * b), w);
-            a0[0] = bytes02(w[0]);
-            a0[1] = bytes02(w[1]);
-            a0[2] = bytes13(w[0]);
-            a0[3] = bytes13(w[1]);
-            a1[0] = bytes02(w[2]);
-            a1[1] = bytes02(w[3]);
-            a1[2] = bytes13(w[2]);
-            a1[3] = bytes13(w[3]);
+            a0[0] = EX ? bytes02(w[0]) : raw02(w[0]);
+            a0[1] = EX ? bytes02(w[1]) : raw02(w[1]);
+            a0[2] = EX ? bytes13(w[0]) : raw13(w[0]);
+            a0[3] = EX ? bytes13(w[1]) : raw13(w[1]);
+            a1[0] = EX ? bytes02(w[2]) : raw02(w[2]);
+            a1[1] = EX ? bytes02(w[3]) : raw02(w[3]);
+            a1[2] = EX ? bytes13(w[2]) : raw13(w[2]);
+            a1[3] = EX ? bytes13(w[3]) : raw13(w[3]);
           } else {
             // one load holds two blocks (16 bytes each); an odd last one is paired with the first
             if (b % 2 == 0) ldm4(from(kb, b), w);
-            const uint32_t x = w[2 * (b & 1)], y = w[2 * (b & 1) + 1];
-            a0[0] = nib_low(x);
-            a0[1] = nib_low(y);
-            a0[2] = nib_low(x >> 8);
-            a0[3] = nib_low(y >> 8);
-            a1[0] = nib_high(x);
-            a1[1] = nib_high(y);
-            a1[2] = nib_high(x >> 8);
-            a1[3] = nib_high(y >> 8);
+            const uint32_t x = w[2 * (b & 1)], y = w[2 * (b & 1) + 1], x8 = x >> 8, y8 = y >> 8;
+            a0[0] = EX ? nib_low(x) : raw_low(x);
+            a0[1] = EX ? nib_low(y) : raw_low(y);
+            a0[2] = EX ? nib_low(x8) : raw_low(x8);
+            a0[3] = EX ? nib_low(y8) : raw_low(y8);
+            a1[0] = EX ? nib_high(x) : raw_high(x);
+            a1[1] = EX ? nib_high(y) : raw_high(y);
+            a1[2] = EX ? nib_high(x8) : raw_high(x8);
+            a1[3] = EX ? nib_high(y8) : raw_high(y8);
           }
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
             float c[4];
             mma16_first(c, a0, qf[j][2 * b][0], qf[j][2 * b][1]);
             mma16(c, a1, qf[j][2 * b + 1][0], qf[j][2 * b + 1][1]);
+            if (!EX) {  // the offset's share
+              s[j][0] = fmaf(d0[b], qs[j][b][0], s[j][0]);
+              s[j][NS / 2] = fmaf(d1[b], qs[j][b][0], s[j][NS / 2]);
+              if (NP == 1) {
+                s[j][1] = fmaf(d0[b], qs[j][b][NQ - 1], s[j][1]);
+                s[j][NS - 1] = fmaf(d1[b], qs[j][b][NQ - 1], s[j][NS - 1]);
+              }
+            }
             if (NP == 2) {
               s[j][0] = fmaf(d0[b], c[0] + c[1], s[j][0]);
               s[j][1] = fmaf(d1[b], c[2] + c[3], s[j][1]);
@@ -625,14 +684,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
       float v0[NB], v1[NB];
       float m0 = load_scales<NB>(vs + g * NB, v0), m1 = load_scales<NB>(vs + (g + 8) * NB, v1);
       // ---- scale, and mask where the tile holds keys that some row does not see
-      const int key = (tile0 + i * kAttnWarps) * 16;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int x = 0; x < NS; ++x) s[j][x] *= cs[j][NP == 2 ? 0 : (x & 1)];
-      if (key < all0 || key + 16 > all1 || ((bad >> stage) & 1)) {
+      if (static_cast<unsigned>(i - clean) >= clean_n) {
         const bool gone = (bad >> stage) & 1;
-        const int ka = key + g, kb8 = key + g + 8;
+        bad &= ~(1u << stage);
+        const int ka = (tile0 + i * kAttnWarps) * 16 + g, kb8 = ka + 8;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -664,7 +723,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
         for (int x = 0; x < NS; ++x) {
           p[j][x] = ex2(s[j][x] - er[j][NP == 2 ? 0 : (x & 1)]);
           const float w = p[j][x] * (x < NS / 2 ? m0 : m1);
-          odd |= !(w <= kWeightTop && (NP == 1 || w >= kWeightLow));
+          odd |= !(w <= kWeightTop && (!EX || w >= kWeightLow));
         }
       const bool any_odd = __any_sync(0xffffffffu, odd);
       if (any_odd) {
@@ -680,7 +739,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int c = 0; c < (NP == 2 ? 1 : 2); ++c) {
+          for (int c = 0; c < NQ; ++c) {
             float top = fmaxf(s[j][c] + lg0, s[j][NS / 2 + c] + lg1) - 11.0f;
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
@@ -708,13 +767,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
 #pragma unroll
       for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int c = 0; c < (NP == 2 ? 1 : 2); ++c) l[j][c] += p[j][c] + p[j][NS / 2 + c];
+        for (int c = 0; c < NQ; ++c) l[j][c] += p[j][c] + p[j][NS / 2 + c];
       // ---- outputs, block by block. fp32: weights below 2^-13 would lose bits in fp16 (they count only where the larger
       // ones meet zero codes); they follow 2^24 larger, on accumulators scaled alike, at most three times: 2^-85.
       for (int level = 0;; ++level) {
         float rest[NT][NS];
         bool more = false;
-        if (NP == 2 && any_odd) {
+        if (EX && any_odd) {
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -741,15 +800,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
             a1[3] = bytes13(w[3]);
           } else {
             if (b % 2 == 0) ldm4t(from(vb, b), w);
-            const uint32_t x = w[2 * (b & 1)], y = w[2 * (b & 1) + 1];
+            const uint32_t x = w[2 * (b & 1)], y = w[2 * (b & 1) + 1], x8 = x >> 8, y8 = y >> 8;
             a0[0] = nib_low(x);
-            a0[1] = nib_low(x >> 8);
+            a0[1] = nib_low(x8);
             a0[2] = nib_low(y);
-            a0[3] = nib_low(y >> 8);
+            a0[3] = nib_low(y8);
             a1[0] = nib_high(x);
-            a1[1] = nib_high(x >> 8);
+            a1[1] = nib_high(x8);
             a1[2] = nib_high(y);
-            a1[3] = nib_high(y >> 8);
+            a1[3] = nib_high(y8);
           }
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
@@ -771,7 +830,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
             mma16(o[j][2 * b + 1], a1, b0, b1);
           }
         }
-        if (NP == 1 || !any_odd) break;
+        if (!EX || !any_odd) break;
         if (!__any_sync(0xffffffffu, more)) {
           if (level > 0) scale_all(o, level == 1 ? 5.9604645e-8f : level == 2 ? 3.5527137e-15f : 2.1175824e-22f);
           break;
@@ -792,7 +851,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, NP, NT>::
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int c = 0; c < (NP == 2 ? 1 : 2); ++c) {
+      for (int c = 0; c < NQ; ++c) {
         float sum_l = l[j][c];
         sum_l += __shfl_xor_sync(0xffffffffu, sum_l, 4);
         sum_l += __shfl_xor_sync(0xffffffffu, sum_l, 8);
@@ -899,11 +958,12 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const __grid_constant__ Sp
   finish4(A, D, row_at(A, rec.x, head, chunk * R + r), d, o, e, l);
 }
 
-template <int BITS, int D, int NP, int NT>
+template <int BITS, int D, bool EX, int NP, int NT>
 cudaError_t launch_split(SplitArgs& a, cudaStream_t s) {
-  using S = SplitShape<BITS, D, NP, NT>;
-  a.ctas = S::kCtas * kNumSMs;
-  cudaError_t e = cudaFuncSetAttribute(kv_split_kernel<BITS, D, NP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  using S = SplitShape<BITS, D, EX, NP, NT>;
+  constexpr int kResident = S::kCtas * kNumSMs;
+  a.ctas = a.units < kResident ? static_cast<int>(a.units) : kResident;
+  cudaError_t e = cudaFuncSetAttribute(kv_split_kernel<BITS, D, EX, NP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
@@ -915,7 +975,7 @@ cudaError_t launch_split(SplitArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kv_split_kernel<BITS, D, NP, NT>, a);
+  e = cudaLaunchKernelEx(&cfg, kv_split_kernel<BITS, D, EX, NP, NT>, a);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(a.ctas), S::R);
   cfg.blockDim = dim3(128);
@@ -926,13 +986,14 @@ cudaError_t launch_split(SplitArgs& a, cudaStream_t s) {
 }  // namespace
 
 template <int D>
-cudaError_t KvAttnDim<D>::launch(SplitArgs& a, int bits, int np, int nt, cudaStream_t s) {
+cudaError_t KvAttnDim<D>::launch(SplitArgs& a, int bits, bool exact, int np, int nt, cudaStream_t s) {
   constexpr int N2 = D == 256 ? 1 : 2;  // two n-tiles of dim 256 would not fit the registers
-  if (bits == 8)
-    return np == 2 ? (nt == 1 ? launch_split<8, D, 2, 1>(a, s) : launch_split<8, D, 2, N2>(a, s))
-                   : (nt == 1 ? launch_split<8, D, 1, 1>(a, s) : launch_split<8, D, 1, N2>(a, s));
-  return np == 2 ? (nt == 1 ? launch_split<4, D, 2, 1>(a, s) : launch_split<4, D, 2, N2>(a, s))
-                 : (nt == 1 ? launch_split<4, D, 1, 1>(a, s) : launch_split<4, D, 1, N2>(a, s));
+  if (exact)
+    return bits == 8 ? (nt == 1 ? launch_split<8, D, true, 2, 1>(a, s) : launch_split<8, D, true, 2, N2>(a, s))
+                     : (nt == 1 ? launch_split<4, D, true, 2, 1>(a, s) : launch_split<4, D, true, 2, N2>(a, s));
+  if (np == 2) return bits == 8 ? launch_split<8, D, false, 2, 1>(a, s) : launch_split<4, D, false, 2, 1>(a, s);
+  return bits == 8 ? (nt == 1 ? launch_split<8, D, false, 1, 1>(a, s) : launch_split<8, D, false, 1, N2>(a, s))
+                   : (nt == 1 ? launch_split<4, D, false, 1, 1>(a, s) : launch_split<4, D, false, 1, N2>(a, s));
 }
 
 template <int D>
