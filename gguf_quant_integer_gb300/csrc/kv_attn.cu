@@ -50,6 +50,8 @@ cudaError_t run(SplitArgs& p, const KvAttnArgs& a, int bits, cudaStream_t s) {
   p.chunks = (p.rows + r - 1) / r;
   const long long keys = p.flat ? p.prefix_len : static_cast<long long>(p.max_pages) << p.c.page_shift;
   const long long units = (keys + kAttnUnit - 1) / kAttnUnit;
+  // Sequences too short for a second CTA to be worth a join: whole pairs.
+  p.whole = units <= kAttnWhole;
   p.units = p.seqs * ((units > 1 ? units : 1) + kAttnHead) * p.c.heads * p.chunks;
   switch (a.c.dim) {
     case 64: return KvAttnDim<64>::launch(p, bits, f.exact, f.np, f.nt, s);

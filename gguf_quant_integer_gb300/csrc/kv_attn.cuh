@@ -51,6 +51,11 @@ constexpr int kAttnUnit = 16 * kAttnWarps;  // keys a unit
 // ids, filling the pipeline, merging): the cut counts them, or CTAs with many
 // short sequences would finish last.
 constexpr int kAttnHead = 5;
+// Pairs that can have no more units than this are not cut. A CTA takes about
+// 0.5 us a unit, the join's launch 4 us (one 97-token sequence, 8 KV heads:
+// 8.5 us cut, 6.6 us whole).
+constexpr int kAttnWhole = 4;
+
 // Kernel arguments. A pair's rows are `tokens` query tokens x group heads;
 // token and head select q's and out's row. Own pages: sequence b has the
 // tokens b * n_q .. + n_q - 1. Prefix (flat): one sequence of prefix_len keys
@@ -71,6 +76,7 @@ struct SplitArgs {
   int window;
   long long units;  // upper bound of the launch's units
   int ctas;         // of the launch: as many as run at a time, or one a unit
+  bool whole;       // pairs are not cut (the line's units are pairs): no join
   float* part_o;    // [2 * ctas][R][dim]
   float* part_el;   // [2 * ctas][R][2]
   int4* record;     // [ctas]: sequence, head * chunks + chunk, last CTA (or -1)
@@ -103,6 +109,9 @@ struct SplitShape {
   static constexpr int kStages = kStage * 3 > 13312 ? 3 : 13312 / kStage > 6 ? 6 : 13312 / kStage;
   static constexpr int kWarpBytes = kStages * kStage > R * D * 4 ? kStages * kStage : R * D * 4;
   static constexpr int kSmem = kAttnWarps * kWarpBytes;
+  // A warp's results fit one stage: the next pair's first tiles can be on
+  // their way into the others while the warps are merged.
+  static constexpr bool kOverlap = R * D * 4 <= kStage;
   // Resident CTAs an SM: the accumulators take NT * D / 4 registers a thread.
   static constexpr int kCtas = D == 256 ? 2 : NT == 1 ? 4 : 3;
 };
@@ -360,62 +369,72 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
   using S = SplitShape<BITS, D, EX, NP, NT>;
   constexpr int NB = S::NB, R = S::R, kStages = S::kStages, NS = NP == 2 ? 2 : 4, NQ = NP == 2 ? 1 : 2;
   extern __shared__ __align__(256) uint8_t smem[];  // stage and matrix addresses are put together by xor
-  __shared__ long long sh_sum[kAttnWarps];
   __shared__ int sh_seq, sh_scan[kAttnWarps];
   __shared__ long long sh_before;
   __shared__ float sh_el[kAttnWarps][R][2];
+  __shared__ uint32_t sh_at[kAttnWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its place; it waits
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- this CTA's units u0 .. u1-1 of the whole line, and the sequence of u0
   const long long per = static_cast<long long>(A.c.heads) * A.chunks;
-  long long sum = 0;
-  for (int b = tid; b < A.seqs; b += 32 * kAttnWarps) sum += unit_count(A, seq_len(A, b)) + kAttnHead;
+  const int cta = blockIdx.x;
+  // Sum of `x` over the CTA's threads up to this one, and over all of them.
+  auto scan = [&](int x, int* all) {
+    int sum = x;
 #pragma unroll
-  for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-  if (lane == 0) sh_sum[warp] = sum;
-  __syncthreads();
-  sum = sh_sum[0] + sh_sum[1] + sh_sum[2] + sh_sum[3];
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    __syncthreads();  // the last call's sums have been read
+    if (lane == 31) sh_scan[warp] = sum;
+    __syncthreads();
+    *all = 0;
+    int add = 0;
+#pragma unroll
+    for (int w = 0; w < kAttnWarps; ++w) {
+      add += w < warp ? sh_scan[w] : 0;
+      *all += sh_scan[w];
+    }
+    return sum + add;
+  };
+  auto cost = [&](int b) { return b < A.seqs ? A.whole ? 1 : unit_count(A, seq_len(A, b)) + kAttnHead : 0; };
+  int mine = cost(tid), part, more;
+  int upto = scan(mine, &part);
+  long long sum = part;
+  for (int base = 32 * kAttnWarps; base < A.seqs; base += 32 * kAttnWarps) {
+    scan(cost(base + tid), &more);
+    sum += more;
+  }
   const long long total = sum * per;
-  const int ctas = total < A.ctas ? static_cast<int>(total) : A.ctas, cta = blockIdx.x;
+  const int ctas = total < A.ctas ? static_cast<int>(total) : A.ctas;
   if (cta >= ctas) {
-    if (tid == 0) A.record[cta] = make_int4(0, 0, -1, 0);
+    if (tid == 0 && !A.whole) A.record[cta] = make_int4(0, 0, -1, 0);
     return;
   }
-  const long long u0 = total * cta / ctas, u1 = total * (cta + 1) / ctas;
+  long long u = total * cta / ctas;
+  const long long u1 = total * (cta + 1) / ctas;
   {
-    const long long v0 = u0 / per;
+    const long long v = u / per;
     long long before = 0;
-    for (int base = 0; base < A.seqs; base += 32 * kAttnWarps) {
-      const int b = base + tid;
-      const int mine = b < A.seqs ? unit_count(A, seq_len(A, b)) + kAttnHead : 0;
-      int scan = mine;
-#pragma unroll
-      for (int x = 1; x < 32; x <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, scan, x);
-        if (lane >= x) scan += o;
-      }
-      if (lane == 31) sh_scan[warp] = scan;
-      __syncthreads();
-      int add = 0, all = 0;
-#pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w) {
-        add += w < warp ? sh_scan[w] : 0;
-        all += sh_scan[w];
-      }
-      const long long end = before + add + scan;
-      if (mine && end - mine <= v0 && v0 < end) {
-        sh_seq = b;
+    for (int base = 0;;) {
+      const long long end = before + upto;
+      if (mine && end - mine <= v && v < end) {
+        sh_seq = base + tid;
         sh_before = end - mine;
       }
-      before += all;
-      __syncthreads();
-      if (before > v0) break;
+      before += part;
+      base += 32 * kAttnWarps;
+      if (base >= A.seqs || before > v) break;
+      mine = cost(base + tid);
+      upto = scan(mine, &part);
     }
+    __syncthreads();
   }
   int seq = sh_seq;
-  long long off = u0 - sh_before * per;  // units into the sequence
+  long long off = u - sh_before * per;  // units into the sequence
 
   uint8_t* const stages = smem + warp * S::kWarpBytes;
   const uint32_t stage0 = ptx::smem_addr(stages);
@@ -428,25 +447,102 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
   const uint32_t scale_to = S::kCodes + scale_lane + (v_scale ? S::kCodes + S::kScales : 0);
   const long long scale_from = A.c.scale_off + scale_lane - lane * 16 + (v_scale ? v_off : 0);  // from this lane's code chunk
   bool left_record = false;
-  for (long long u = u0; u < u1;) {
-    const int n = seq_len(A, seq), nu = unit_count(A, n), nv = nu + kAttnHead, f0 = first_unit(A, n);
-    if (!A.flat && tid == 0 && A.lens[seq] > n) kv_record(kKvBadLen);
-    const int pair = static_cast<int>(off / nv), at = static_cast<int>(off - static_cast<long long>(pair) * nv);
-    const int did = nv - at < u1 - u ? nv - at : static_cast<int>(u1 - u);
-    // units k0 .. k1-1 of the pair's keys; a CTA that gets only from its head leaves the pair to the next
-    const int k0 = at > kAttnHead ? at - kAttnHead : 0, k1 = at + did - kAttnHead;
-    const long long first = u - at;  // where the pair begins
-    u += did;
-    off += did;
-    const int sq = seq;
-    if (off == nv * per) {
-      off = 0;
-      ++seq;
+  // The part of a pair that this CTA takes next: units k0 .. k1-1 of the
+  // pair's keys. A CTA that gets only from a pair's head leaves it to the next.
+  struct Part {
+    int seq, n, nu, pair, k0, k1;
+    long long first;  // where the pair begins
+  };
+  auto next_part = [&](Part& x) {
+    while (u < u1) {
+      const int n = seq_len(A, seq), nu = unit_count(A, n), nv = A.whole ? 1 : nu + kAttnHead;
+      if (!A.flat && tid == 0 && A.lens[seq] > n) kv_record(kKvBadLen);
+      const int pair = static_cast<int>(off / nv), at = static_cast<int>(off - static_cast<long long>(pair) * nv);
+      const int did = nv - at < u1 - u ? nv - at : static_cast<int>(u1 - u);
+      x = {seq, n, nu, pair, at > kAttnHead ? at - kAttnHead : 0, A.whole ? nu : at + did - kAttnHead, u - at};
+      u += did;
+      off += did;
+      if (off == nv * per) {
+        off = 0;
+        ++seq;
+      }
+      if (x.k1 > 0) return true;
     }
-    if (k1 <= 0) continue;
+    return false;
+  };
+
+  // ---- the warp's tiles of 16 keys of a part: warp, warp + 4, ... of its units
+  int tile0 = 0, tiles = 0, line0 = 0, stage = 0;
+  const int32_t* table = nullptr;
+  const int shift = A.c.page_shift - 4;  // tiles a page
+  // Where the next 32 tiles lie, one a lane: the address of its K codes (0 if its page id is invalid), and from there to its
+  // K scales. The page ids after them are on their way.
+  long long code_at = 0;
+  int scales_at = 0, next_page = 0;
+  unsigned bad = 0;      // stages whose page id was invalid
+  unsigned clean_n = 0;  // tiles from `clean` on that hold only keys which every row sees
+  auto page_of = [&](int i) { return i < tiles ? table[(tile0 + i * kAttnWarps) >> shift] : 0; };
+  auto locate = [&](int i, int page) {
+    const int line = line0 + (((tile0 + i * kAttnWarps) & ((1 << shift) - 1)) << 4);
+    const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(A.c.n_pages);
+    code_at = ok ? reinterpret_cast<long long>(A.c.k) + page * A.c.page_bytes + line * S::kRow : 0;
+    scales_at = line * (NB * 2 - S::kRow);
+  };
+  auto issue = [&](int i, int stage) {
+    if (i < tiles) {
+      if ((i & 31) == 0 && i > 0) {
+        locate(i + lane, next_page);
+        next_page = page_of(i + 32 + lane);
+      }
+      const unsigned lo = __shfl_sync(0xffffffffu, static_cast<unsigned>(code_at), i & 31);
+      const unsigned hi = __shfl_sync(0xffffffffu, static_cast<unsigned>(code_at >> 32), i & 31);
+      const int so = __shfl_sync(0xffffffffu, scales_at, i & 31);
+      if (hi != 0) {
+        const uint8_t* const kc = reinterpret_cast<const uint8_t*>((static_cast<long long>(hi) << 32) + lo + lane * 16);
+        const uint8_t* const vc = kc + v_off;
+        const uint32_t base = stage0 + stage * S::kStage, dst = base + code_to;
+#pragma unroll
+        for (int x = 0; x < S::kSteps; ++x) {
+          // 32 chunks a step; a step's rows differ from the first one's in the swizzle by a constant
+          const uint32_t to = S::kPow2 ? (dst ^ S::turn(x)) + x * 512
+                                       : base + chunk_at<S::kChunks>((x * 32 + lane) / S::kChunks, (x * 32 + lane) % S::kChunks);
+          if (S::kChunks % 2 == 0 || x * 32 + lane < 16 * S::kChunks) {
+            cp16(to, kc + x * 512);
+            cp16(to + S::kCodes + S::kScales, vc + x * 512);
+          }
+        }
+        if (lane < 2 * S::kScales / 16) cp16(base + scale_to, kc + (scale_from + so));
+      } else {
+        bad |= 1u << stage;
+        clean_n = 0;
+        if (lane == 0) kv_record(kKvBadPage);
+      }
+    }
+    cp_commit();
+  };
+
+  // Start on a part: its first tiles into the stages from `stage` on.
+  auto begin_part = [&](const Part& x) {
+    const int all = (x.n + 15) / 16;
+    tile0 = (first_unit(A, x.n) + x.k0) * kAttnWarps + warp;
+    tiles = all > tile0 ? (all - tile0 + kAttnWarps - 1) / kAttnWarps : 0;
+    tiles = tiles < x.k1 - x.k0 ? tiles : x.k1 - x.k0;
+    line0 = (x.pair / A.chunks) << A.c.page_shift;
+    table = A.flat ? A.pages : A.pages + static_cast<size_t>(x.seq) * A.page_stride;
+    const int page = page_of(lane);
+    next_page = page_of(32 + lane);
+    locate(lane, page);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i, stage + i < kStages ? stage + i : stage + i - kStages);
+  };
+
+  Part cur;
+  bool have = next_part(cur);
+  if (have) begin_part(cur);
+  while (have) {
+    const int sq = cur.seq, n = cur.n, nu = cur.nu, pair = cur.pair, k0 = cur.k0, k1 = cur.k1;
     const int head = pair / A.chunks, chunk = pair - head * A.chunks;
     const int row0 = chunk * R, rows = A.rows - row0 < R ? A.rows - row0 : R;
-
     // ---- queries as B operands. Column g of n-tile j: NP = 2: row 4 j + g/2, piece g & 1; NP = 1: row 8 j + g.
     uint32_t qf[NT][D / 16][2];
     float cs[NT][NQ], qs[NT][NB][NQ];  // score factor, and -(128 or 8) sum(q) of each block, of this lane's columns
@@ -529,67 +625,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
       all1 = min(all1, __shfl_xor_sync(0xffffffffu, all1, x));
     }
 
-    // ---- the warp's tiles of 16 keys: warp, warp + 4, ... of the units
-    const int tile0 = (f0 + k0) * kAttnWarps + warp;
-    int tiles = k1 - k0;
-    {  // only tiles with keys
-      const int all = (n + 15) / 16;
-      const int have = all > tile0 ? (all - tile0 + kAttnWarps - 1) / kAttnWarps : 0;
-      tiles = tiles < have ? tiles : have;
-    }
-    const int32_t* const table = A.flat ? A.pages : A.pages + static_cast<size_t>(sq) * A.page_stride;
-    const int shift = A.c.page_shift - 4;  // tiles a page
-    // Where the next 32 tiles lie, one a lane: the address of its K codes (0 if its page id is invalid), and from there to
-    // its K scales. The page ids after them are on their way.
-    auto page_of = [&](int i) { return i < tiles ? table[(tile0 + i * kAttnWarps) >> shift] : 0; };
-    long long code_at = 0;
-    int scales_at = 0;
-    auto locate = [&](int i, int page) {
-      const int line = (head << A.c.page_shift) + (((tile0 + i * kAttnWarps) & ((1 << shift) - 1)) << 4);
-      const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(A.c.n_pages);
-      code_at = ok ? reinterpret_cast<long long>(A.c.k) + page * A.c.page_bytes + line * S::kRow : 0;
-      scales_at = line * (NB * 2 - S::kRow);
-    };
-    locate(lane, page_of(lane));
-    int next_page = page_of(32 + lane);
-    unsigned bad = 0;  // stages whose page id was invalid
-    // tiles clean .. clean + clean_n - 1 hold only keys that every row sees
+    // tiles clean .. clean + clean_n - 1 hold only keys that every row sees (none, once a page id was invalid)
     int clean = ((all0 + 15) / 16 - tile0 + kAttnWarps - 1) / kAttnWarps;
     clean = clean > 0 ? clean : 0;
-    unsigned clean_n = all1 / 16 > tile0 ? static_cast<unsigned>((all1 / 16 - tile0 + kAttnWarps - 1) / kAttnWarps) : 0u;
-    clean_n = clean_n > static_cast<unsigned>(clean) ? clean_n - clean : 0u;
-    auto issue = [&](int i, int stage) {
-      if (i < tiles) {
-        if ((i & 31) == 0 && i > 0) {
-          locate(i + lane, next_page);
-          next_page = page_of(i + 32 + lane);
-        }
-        const unsigned lo = __shfl_sync(0xffffffffu, static_cast<unsigned>(code_at), i & 31);
-        const unsigned hi = __shfl_sync(0xffffffffu, static_cast<unsigned>(code_at >> 32), i & 31);
-        const int so = __shfl_sync(0xffffffffu, scales_at, i & 31);
-        if (hi != 0) {
-          const uint8_t* const kc = reinterpret_cast<const uint8_t*>((static_cast<long long>(hi) << 32) + lo + lane * 16);
-          const uint8_t* const vc = kc + v_off;
-          const uint32_t base = stage0 + stage * S::kStage, dst = base + code_to;
-#pragma unroll
-          for (int x = 0; x < S::kSteps; ++x) {
-            // 32 chunks a step; a step's rows differ from the first one's in the swizzle by a constant
-            const uint32_t to = S::kPow2 ? (dst ^ S::turn(x)) + x * 512
-                                         : base + chunk_at<S::kChunks>((x * 32 + lane) / S::kChunks, (x * 32 + lane) % S::kChunks);
-            if (S::kChunks % 2 == 0 || x * 32 + lane < 16 * S::kChunks) {
-              cp16(to, kc + x * 512);
-              cp16(to + S::kCodes + S::kScales, vc + x * 512);
-            }
-          }
-          if (lane < 2 * S::kScales / 16) cp16(base + scale_to, kc + (scale_from + so));
-        } else {
-          bad |= 1u << stage;
-          clean_n = 0;
-          if (lane == 0) kv_record(kKvBadPage);
-        }
-      }
-      cp_commit();
-    };
+    clean_n = all1 / 16 > tile0 ? static_cast<unsigned>((all1 / 16 - tile0 + kAttnWarps - 1) / kAttnWarps) : 0u;
+    clean_n = clean_n > static_cast<unsigned>(clean) && !bad ? clean_n - clean : 0u;
 
     float o[NT][D / 16][4], er[NT][NQ], l[NT][NQ];
 #pragma unroll
@@ -602,9 +642,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
         l[j][i] = 0.0f;
       }
     }
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i, i);
-    int stage = 0;
     // ldmatrix row addresses: matrix m of 4 covers rows 8 (m & 1) .. + 7, chunk m >> 1
     const int lrow = (lane & 7) + (lane & 8), lch = lane >> 4;
     const uint32_t code_from = chunk_at<S::kChunks>(lrow, lch);
@@ -843,11 +880,12 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
       }
       stage = stage + 1 == kStages ? 0 : stage + 1;
     }
-    cp_wait<0>();
-    __syncwarp();
-
-    // ---- merge the four warps in shared memory (each in its own stage area)
-    float* const mine = reinterpret_cast<float*>(stages);
+    // ---- merge the four warps in shared memory. Each puts its results where its last tile was; the next part's tiles go
+    // elsewhere until the barrier after the merge.
+    __syncwarp();  // every lane has read that tile
+    const uint32_t at = S::kOverlap ? (stage == 0 ? kStages - 1 : stage - 1) * S::kStage : 0;
+    float* const mine_o = reinterpret_cast<float*>(stages + at);
+    if (lane == 0) sh_at[warp] = warp * S::kWarpBytes + at;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -866,9 +904,12 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
           const float2 y = NP == 2 ? make_float2(fmaf(o[j][m][1], 1.0f / kLoUp, o[j][m][0]),
                                                  fmaf(o[j][m][3], 1.0f / kLoUp, o[j][m][2]))
                                    : make_float2(o[j][m][c], o[j][m][2 + c]);
-          *reinterpret_cast<float2*>(mine + r * D + 16 * m + 2 * g) = y;
+          *reinterpret_cast<float2*>(mine_o + r * D + 16 * m + 2 * g) = y;
         }
       }
+    Part next;
+    const bool more_parts = next_part(next);
+    if (S::kOverlap && more_parts) begin_part(next);
     __syncthreads();
     const bool whole = k0 == 0 && k1 == nu;
     for (int x = tid * 4; x < rows * D; x += 32 * kAttnWarps * 4) {
@@ -881,7 +922,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
 #pragma unroll
       for (int w = 0; w < kAttnWarps; ++w) {
         const float f = ex2(sh_el[w][r][0] - e);
-        const float4 z = *reinterpret_cast<const float4*>(smem + w * S::kWarpBytes + x * 4);
+        const float4 z = *reinterpret_cast<const float4*>(smem + sh_at[w] + x * 4);
         y = make_float4(fmaf(z.x, f, y.x), fmaf(z.y, f, y.y), fmaf(z.z, f, y.z), fmaf(z.w, f, y.w));
         ll = fmaf(sh_el[w][r][1], f, ll);
       }
@@ -898,64 +939,87 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
       left_record = true;
       if (tid == 0) {
         // the CTA of the pair's last unit: the largest c with total * c / ctas <= last
-        const long long last = first + nv - 1;
+        const long long last = cur.first + nu + kAttnHead - 1;
         const int c1 = static_cast<int>(((last + 1) * ctas - 1) / total);
         A.record[cta] = make_int4(sq, pair, c1, 0);
       }
     }
     __syncthreads();
+    if (!S::kOverlap && more_parts) begin_part(next);
+    cur = next;
+    have = more_parts;
   }
-  if (!left_record && tid == 0) A.record[cta] = make_int4(0, 0, -1, 0);
+  if (!left_record && tid == 0 && !A.whole) A.record[cta] = make_int4(0, 0, -1, 0);
 }
 
-// The parts of the pair that begins in CTA blockIdx.x, row blockIdx.y: each
-// warp takes every fourth part, then the warps are merged.
-template <int D, int R>
-__global__ void __launch_bounds__(128) kv_join_kernel(const __grid_constant__ SplitArgs A) {
-  constexpr int kLanes = D / 4;  // threads that hold a float4 of the row
-  constexpr int kTeams = 128 / kLanes;
-  __shared__ float so[kTeams][D];
-  __shared__ float sel[kTeams][2];
+// The parts of the pair that begins in CTA blockIdx.x, RB of their R rows from RB * blockIdx.y on. A thread holds one float4
+// of the rows; each team of threads takes every kTeams-th part, several loads at a time, then the teams are merged.
+constexpr int kJoinThreads = 512;
+template <int D, int R, int RB>
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ SplitArgs A) {
+  constexpr int kLanes = RB * D / 4;
+  constexpr int kTeams = kJoinThreads / kLanes;
+  constexpr int kBatch = 8;
+  static_assert(kTeams >= 1, "a part's rows are one pass of the block");
+  __shared__ float2 sel[kTeams][RB];
+  __shared__ float4 so[kTeams][kLanes];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 rec = A.record[blockIdx.x];
   if (rec.z < 0) return;
-  const int head = rec.y / A.chunks, chunk = rec.y - head * A.chunks, r = blockIdx.y;
-  if (chunk * R + r >= A.rows) return;
-  const int team = threadIdx.x / kLanes, d = (threadIdx.x % kLanes) * 4, c0 = blockIdx.x;
+  const int c0 = blockIdx.x, parts = rec.z - c0 + 1, tid = threadIdx.x;
+  const int team = tid / kLanes, at = tid - team * kLanes, r = at / (D / 4), d = (at - r * (D / 4)) * 4;
+  const int head = rec.y / A.chunks, row = RB * blockIdx.y + r, pair_row = (rec.y - head * A.chunks) * R + row;
   float e = -1e30f, l = 0.0f;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (team < kTeams) {
-#pragma unroll 4
-    for (int c = c0 + team; c <= rec.z; c += kTeams) {
-      const size_t ps = (static_cast<size_t>(c) * 2 + (c == c0 ? 1 : 0)) * R + r;
-      const float4 z = *reinterpret_cast<const float4*>(A.part_o + ps * D + d);
-      const float2 el = *reinterpret_cast<const float2*>(A.part_el + ps * 2);
-      const float top = fmaxf(e, el.x), f = ex2(e - top), h = ex2(el.x - top);
-      o = make_float4(o.x * f + z.x * h, o.y * f + z.y * h, o.z * f + z.z * h, o.w * f + z.w * h);
-      l = l * f + el.y * h;
+  if (team < kTeams && pair_row < A.rows) {
+    for (int base = team; base < parts; base += kTeams * kBatch) {
+      float2 el[kBatch];
+      float4 z[kBatch];
+      float top = e;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const int i = base + x * kTeams;
+        if (i < parts) {
+          // part i: the second slot of the CTA where the pair begins, the first of those after it
+          const size_t slot = (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * R + row;
+          el[x] = *reinterpret_cast<const float2*>(A.part_el + slot * 2);
+          z[x] = *reinterpret_cast<const float4*>(A.part_o + slot * D + d);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x)
+        if (base + x * kTeams < parts) top = fmaxf(top, el[x].x);
+      const float keep = ex2(e - top);
+      o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+      l *= keep;
       e = top;
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x)
+        if (base + x * kTeams < parts) {
+          const float f = ex2(el[x].x - top);
+          o = make_float4(fmaf(z[x].x, f, o.x), fmaf(z[x].y, f, o.y), fmaf(z[x].z, f, o.z), fmaf(z[x].w, f, o.w));
+          l = fmaf(el[x].y, f, l);
+        }
     }
-    *reinterpret_cast<float4*>(&so[team][d]) = o;
-    if (d == 0) {
-      sel[team][0] = e;
-      sel[team][1] = l;
-    }
+    if (team > 0) so[team][at] = o;
+    if (d == 0) sel[team][r] = make_float2(e, l);
   }
   __syncthreads();
-  if (team != 0) return;
-  e = sel[0][0];
-#pragma unroll
-  for (int w = 1; w < kTeams; ++w) e = fmaxf(e, sel[w][0]);
-  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  l = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kTeams; ++w) {
-    const float f = ex2(sel[w][0] - e);
-    const float4 z = *reinterpret_cast<const float4*>(&so[w][d]);
+  if (team != 0 || pair_row >= A.rows) return;
+  const int used = parts < kTeams ? parts : kTeams;
+  const float mine = e;
+  for (int w = 1; w < used; ++w) e = fmaxf(e, sel[w][r].x);
+  float f = ex2(mine - e);
+  o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+  l *= f;
+  for (int w = 1; w < used; ++w) {
+    const float2 el = sel[w][r];
+    const float4 z = so[w][at];
+    f = ex2(el.x - e);
     o = make_float4(fmaf(z.x, f, o.x), fmaf(z.y, f, o.y), fmaf(z.z, f, o.z), fmaf(z.w, f, o.w));
-    l = fmaf(sel[w][1], f, l);
+    l = fmaf(el.y, f, l);
   }
-  finish4(A, D, row_at(A, rec.x, head, chunk * R + r), d, o, e, l);
+  finish4(A, D, row_at(A, rec.x, head, pair_row), d, o, e, l);
 }
 
 template <int BITS, int D, bool EX, int NP, int NT>
@@ -963,8 +1027,9 @@ cudaError_t launch_split(SplitArgs& a, cudaStream_t s) {
   using S = SplitShape<BITS, D, EX, NP, NT>;
   constexpr int kResident = S::kCtas * kNumSMs;
   a.ctas = a.units < kResident ? static_cast<int>(a.units) : kResident;
-  cudaError_t e = cudaFuncSetAttribute(kv_split_kernel<BITS, D, EX, NP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-  if (e != cudaSuccess) return e;
+  static const cudaError_t attr_error =
+      cudaFuncSetAttribute(kv_split_kernel<BITS, D, EX, NP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (attr_error != cudaSuccess) return attr_error;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
   cfg.blockDim = dim3(32 * kAttnWarps);
@@ -975,12 +1040,11 @@ cudaError_t launch_split(SplitArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kv_split_kernel<BITS, D, EX, NP, NT>, a);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.ctas), S::R);
-  cfg.blockDim = dim3(128);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_split_kernel<BITS, D, EX, NP, NT>, a);
+  if (e != cudaSuccess || a.whole) return e;
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, S::R>, a);
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, S::R, S::R>, a);
 }
 
 }  // namespace

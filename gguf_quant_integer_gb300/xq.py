@@ -463,7 +463,9 @@ class KVCache:
         self.qtype, self.n_pages, self.page_size, self.heads, self.dim = qtype, n_pages, page_size, heads, dim
         self._desc = xq_kv_cache(qtype, n_pages, page_size, heads, dim, self.k.data_ptr(), self.v.data_ptr())
         self._ref = ctypes.byref(self._desc)
+        self._inner = (dim, 1)
         self._lib = lib()
+        self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._ws = {}   # stream -> workspace
         self._need = {}  # sizes of a call -> workspace bytes
 
@@ -472,19 +474,25 @@ class KVCache:
             if t.device != self.device:
                 raise ValueError(f"a tensor on {t.device} for a cache on {self.device}")
 
+    def _stream(self, stream):
+        # the current stream's handle: torch's accessor of the bare handle costs a fortieth of building a Stream object
+        if stream is None:
+            return self._current(self.device.index) if self._current else self._torch.cuda.current_stream(self.device).cuda_stream
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
     def write(self, k, v, slots, stream=None):
         """Quantize rows k, v [tokens, heads, dim] into slots int64 [tokens]
         (negative ones are skipped). A token's row is contiguous; rows may be
         a part of longer ones (k.stride(0))."""
         n = slots.shape[0]
-        shape, inner = (n, self.heads, self.dim), (self.dim, 1)
-        if k.shape != shape or v.shape != shape or k.dtype != v.dtype or k.stride()[1:] != inner or v.stride()[1:] != inner:
+        shape, ks, vs = (n, self.heads, self.dim), k.stride(), v.stride()
+        if k.shape != shape or v.shape != shape or k.dtype != v.dtype or ks[1:] != self._inner or vs[1:] != self._inner:
             raise ValueError(f"k and v: {shape} of one dtype, each token's row contiguous")
         if slots.dtype != self._torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
             raise ValueError("slots: contiguous int64 [tokens]")
         self._on_device(k, v, slots)
-        rc = self._lib.xq_kv_write(self._ref, _float_type(k.dtype), k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0),
-                                   slots.data_ptr(), n, _stream(stream))
+        rc = self._lib.xq_kv_write(self._ref, _float_type(k.dtype), k.data_ptr(), ks[0], v.data_ptr(), vs[0], slots.data_ptr(), n,
+                                   self._stream(stream))
         if rc:
             raise XQError("xq_kv_write", rc)
 
@@ -494,16 +502,21 @@ class KVCache:
         torch = self._torch
         if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
             raise ValueError("slots: contiguous int64 [tokens]")
-        shape = (slots.shape[0], self.heads, self.dim)
-        dtype = (k.dtype if k is not None else torch.float32) if dtype is None else dtype
-        k = torch.empty(shape, dtype=dtype, device=self.device) if k is None else k
-        v = torch.empty(shape, dtype=dtype, device=self.device) if v is None else v
-        for t in (k, v):
-            if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-                raise ValueError(f"k and v: contiguous {shape} of {dtype}")
+        n = slots.shape[0]
+        shape = (n, self.heads, self.dim)
+        if dtype is None:
+            dtype = torch.float32 if k is None else k.dtype
+        kind = _float_type(dtype)
+        if k is None:
+            k = torch.empty(shape, dtype=dtype, device=self.device)
+        elif k.shape != shape or k.dtype != dtype or not k.is_contiguous():
+            raise ValueError(f"k: contiguous {shape} of {dtype}")
+        if v is None:
+            v = torch.empty(shape, dtype=dtype, device=self.device)
+        elif v.shape != shape or v.dtype != dtype or not v.is_contiguous():
+            raise ValueError(f"v: contiguous {shape} of {dtype}")
         self._on_device(slots, k, v)
-        rc = self._lib.xq_kv_read(self._ref, slots.data_ptr(), shape[0], _float_type(dtype), k.data_ptr(), v.data_ptr(),
-                                  _stream(stream))
+        rc = self._lib.xq_kv_read(self._ref, slots.data_ptr(), n, kind, k.data_ptr(), v.data_ptr(), self._stream(stream))
         if rc:
             raise XQError("xq_kv_read", rc)
         return k, v
@@ -546,10 +559,10 @@ class KVCache:
                                          prefix_pages.shape[0] * self.page_size < prefix_len):
             raise ValueError("prefix_pages: contiguous int32 ids of the prefix's pages")
         self._on_device(q, pages, lens, out)
-        s = _stream(stream)
+        s = self._stream(stream)
         width = pages.shape[1]
         if workspace is None:
-            workspace = self._workspace((q.dtype, batch, n_q, heads, width, prefix_len), s.value or 0)
+            workspace = self._workspace((q.dtype, batch, n_q, heads, width, prefix_len), s)
         query = xq_kv_query(_float_type(q.dtype), batch, n_q, heads, q.data_ptr(), out.data_ptr(), pages.data_ptr(),
                             pages.stride(0) if batch > 1 else width, width, lens.data_ptr(),
                             dim ** -0.5 if scale is None else scale, window,
