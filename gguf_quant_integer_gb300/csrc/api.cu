@@ -779,12 +779,14 @@ xq_status xq_device_error(xq_stream stream, unsigned int* code_out) {
       *code_out = (static_cast<unsigned int>(k + 1) << 8) | (c[k] & 0xFFu);
       break;
     }
-  unsigned int kv[2] = {0u, 0u};
+  unsigned int kv[3] = {0u, 0u, 0u}, kv_wait = 0u;
   const cudaError_t k0 = xq::take_kv_cache_error(&kv[0]);
   const cudaError_t k1 = xq::take_kv_attn_error(&kv[1]);
-  if (k0 != cudaSuccess || k1 != cudaSuccess) return XQ_ERR_CUDA;
-  for (int k = 0; k < 2 && *code_out == 0; ++k)
+  const cudaError_t k2 = xq::take_kv_tile_error(&kv[2], &kv_wait);
+  if (k0 != cudaSuccess || k1 != cudaSuccess || k2 != cudaSuccess) return XQ_ERR_CUDA;
+  for (int k = 0; k < 3 && *code_out == 0; ++k)
     if (kv[k]) *code_out = (3u << 8) | (kv[k] & 0xFFu);
+  if (kv_wait && *code_out == 0) *code_out = (4u << 8) | (kv_wait & 0xFFu);
   // checked builds: the first failed bounds check of each kernel file
   unsigned int chk[6] = {0u, 0u, 0u, 0u, 0u, 0u};
   const cudaError_t c0 = xq::take_gemv_check(&chk[0]);

@@ -1,6 +1,6 @@
 // Attention over the quantized KV cache: which kernels a call runs, and their
 // workspace.
-#include "kv_attn.cuh"
+#include "kv_tile.cuh"
 
 namespace xq {
 namespace {
@@ -21,10 +21,13 @@ Rows rows_for(const KvAttnArgs& a, int rows) {
   return {exact, 1, rows <= 8 || a.c.dim == 256 ? 1 : 2};
 }
 
-// The most CTAs and rows of partial results: four resident CTAs an SM of 4 or
-// 8 rows, three of up to 16.
+// Whether a pair's rows go to the tcgen05 tiles of 128 rows.
+bool tiled(const KvAttnArgs& a, long long rows) { return a.c.dim <= 128 && rows >= kTileMinRows; }
+
+// Rows of partial results (two a CTA): four resident CTAs an SM of 4 or 8
+// rows, three of up to 16; one of 128.
+constexpr size_t kSplitRows = 2 * 4 * kNumSMs * 16, kTileRowsAll = 2 * kNumSMs * kTileRows;
 constexpr int kMaxCtas = 4 * kNumSMs;
-constexpr int kMaxRows = 16;
 
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
@@ -33,7 +36,8 @@ struct Layout {
 };
 Layout layout(const KvAttnArgs& a) {
   Layout L;
-  const size_t rows = static_cast<size_t>(2) * kMaxCtas * kMaxRows;
+  const bool tile = tiled(a, a.rows) || (a.prefix_len > 0 && tiled(a, static_cast<long long>(a.batch) * a.rows));
+  const size_t rows = tile ? kTileRowsAll : kSplitRows;
   const size_t outs = a.prefix_len > 0 ? static_cast<size_t>(a.batch) * a.n_q * a.q_heads : 0;
   L.record = 0;
   L.part_el = L.record + kMaxCtas * sizeof(int4);
@@ -45,14 +49,23 @@ Layout layout(const KvAttnArgs& a) {
 }
 
 cudaError_t run(SplitArgs& p, const KvAttnArgs& a, int bits, cudaStream_t s) {
+  const bool tile = tiled(a, p.rows);
   const Rows f = rows_for(a, p.rows);
-  const int r = f.nt * 8 / f.np;
+  const int r = tile ? kTileRows : f.nt * 8 / f.np;
   p.chunks = (p.rows + r - 1) / r;
   const long long keys = p.flat ? p.prefix_len : static_cast<long long>(p.max_pages) << p.c.page_shift;
   const long long units = (keys + kAttnUnit - 1) / kAttnUnit;
   // Sequences too short for a second CTA to be worth a join: whole pairs.
   p.whole = units <= kAttnWhole;
-  p.units = p.seqs * ((units > 1 ? units : 1) + kAttnHead) * p.c.heads * p.chunks;
+  p.head = tile ? kTileHead : kAttnHead;
+  p.units = p.seqs * ((units > 1 ? units : 1) + p.head) * p.c.heads * p.chunks;
+  if (tile) {
+    switch (a.c.dim) {
+      case 64: return KvTileDim<64>::launch(p, bits, f.exact, s);
+      case 96: return KvTileDim<96>::launch(p, bits, f.exact, s);
+      default: return KvTileDim<128>::launch(p, bits, f.exact, s);
+    }
+  }
   switch (a.c.dim) {
     case 64: return KvAttnDim<64>::launch(p, bits, f.exact, f.np, f.nt, s);
     case 96: return KvAttnDim<96>::launch(p, bits, f.exact, f.np, f.nt, s);
@@ -122,6 +135,19 @@ cudaError_t take_kv_attn_error(unsigned int* code) {
   const TakeFn fns[4] = {KvAttnDim<64>::take_error, KvAttnDim<96>::take_error, KvAttnDim<128>::take_error,
                          KvAttnDim<256>::take_error};
   return take_all(fns, code);
+}
+cudaError_t take_kv_tile_error(unsigned int* index, unsigned int* wait) {
+  typedef cudaError_t (*TakeTile)(unsigned int*, unsigned int*);
+  const TakeTile fns[3] = {KvTileDim<64>::take_error, KvTileDim<96>::take_error, KvTileDim<128>::take_error};
+  *index = *wait = 0;
+  for (TakeTile f : fns) {
+    unsigned int i = 0, w = 0;
+    const cudaError_t e = f(&i, &w);
+    if (e != cudaSuccess) return e;
+    if (*index == 0) *index = i;
+    if (*wait == 0) *wait = w;
+  }
+  return cudaSuccess;
 }
 cudaError_t take_kv_attn_check(unsigned int* code) {
   const TakeFn fns[4] = {KvAttnDim<64>::take_check, KvAttnDim<96>::take_check, KvAttnDim<128>::take_check,

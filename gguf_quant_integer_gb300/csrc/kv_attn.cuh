@@ -77,6 +77,7 @@ struct SplitArgs {
   long long units;  // upper bound of the launch's units
   int ctas;         // of the launch: as many as run at a time, or one a unit
   bool whole;       // pairs are not cut (the line's units are pairs): no join
+  int head;         // units that a pair counts besides its keys
   float* part_o;    // [2 * ctas][R][dim]
   float* part_el;   // [2 * ctas][R][2]
   int4* record;     // [ctas]: sequence, head * chunks + chunk, last CTA (or -1)
@@ -350,6 +351,115 @@ __device__ __forceinline__ void finish4(const SplitArgs& A, int D, size_t at, in
   store4(A.out, A.type, at * D + d, y);
 }
 
+// ---- the line of units and this CTA's stretch of it
+
+struct Line {
+  long long total, per;  // units of the line; pairs of a sequence
+  long long u, u1;       // the stretch left
+  long long off;         // units into sequence seq
+  int seq, ctas;
+};
+struct LineShared {
+  int seq, scan[32];
+  long long before;
+};
+// A part of a pair: units k0 .. k1-1 of its keys' nu.
+struct Part {
+  int seq, n, nu, pair, k0, k1;
+  long long first;  // where the pair begins on the line
+};
+
+// The stretch of CTA blockIdx.x, found by all threads of its WARPS warps.
+// False (with an empty record left): there are fewer units than CTAs.
+template <int WARPS>
+__device__ __forceinline__ bool line_begin(const SplitArgs& A, LineShared& sh, Line* out) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // Sum of `x` over the CTA's threads up to this one, and over all of them.
+  auto scan = [&](int x, int* all) {
+    int sum = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    __syncthreads();  // the last call's sums have been read
+    if (lane == 31) sh.scan[warp] = sum;
+    __syncthreads();
+    *all = 0;
+    int add = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      add += w < warp ? sh.scan[w] : 0;
+      *all += sh.scan[w];
+    }
+    return sum + add;
+  };
+  auto cost = [&](int b) { return b < A.seqs ? A.whole ? 1 : unit_count(A, seq_len(A, b)) + A.head : 0; };
+  Line L;
+  L.per = static_cast<long long>(A.c.heads) * A.chunks;
+  int mine = cost(tid), part, more;
+  int upto = scan(mine, &part);
+  long long sum = part;
+  for (int base = 32 * WARPS; base < A.seqs; base += 32 * WARPS) {
+    scan(cost(base + tid), &more);
+    sum += more;
+  }
+  L.total = sum * L.per;
+  L.ctas = L.total < A.ctas ? static_cast<int>(L.total) : A.ctas;
+  const int cta = blockIdx.x;
+  if (cta >= L.ctas) {
+    if (tid == 0 && !A.whole) A.record[cta] = make_int4(0, 0, -1, 0);
+    return false;
+  }
+  L.u = L.total * cta / L.ctas;
+  L.u1 = L.total * (cta + 1) / L.ctas;
+  const long long v = L.u / L.per;
+  long long before = 0;
+  for (int base = 0;;) {
+    const long long end = before + upto;
+    if (mine && end - mine <= v && v < end) {
+      sh.seq = base + tid;
+      sh.before = end - mine;
+    }
+    before += part;
+    base += 32 * WARPS;
+    if (base >= A.seqs || before > v) break;
+    mine = cost(base + tid);
+    upto = scan(mine, &part);
+  }
+  __syncthreads();
+  L.seq = sh.seq;
+  L.off = L.u - sh.before * L.per;
+  *out = L;
+  return true;
+}
+
+// The next part of the stretch. A CTA that gets only from a pair's head
+// leaves the pair to the next.
+__device__ __forceinline__ bool line_next(const SplitArgs& A, Line& L, Part& x) {
+  while (L.u < L.u1) {
+    const int n = seq_len(A, L.seq), nu = unit_count(A, n), nv = A.whole ? 1 : nu + A.head;
+    if (!A.flat && threadIdx.x == 0 && A.lens[L.seq] > n) kv_record(kKvBadLen);
+    const int pair = static_cast<int>(L.off / nv), at = static_cast<int>(L.off - static_cast<long long>(pair) * nv);
+    const int did = nv - at < L.u1 - L.u ? nv - at : static_cast<int>(L.u1 - L.u);
+    x = {L.seq, n, nu, pair, at > A.head ? at - A.head : 0, A.whole ? nu : at + did - A.head, L.u - at};
+    L.u += did;
+    L.off += did;
+    if (L.off == nv * L.per) {
+      L.off = 0;
+      ++L.seq;
+    }
+    if (x.k1 > 0) return true;
+  }
+  return false;
+}
+
+// The CTA of the last unit of x's pair: the largest c with total * c / ctas <= that unit.
+__device__ __forceinline__ int line_last(const SplitArgs& A, const Line& L, const Part& x) {
+  const long long last = x.first + x.nu + A.head - 1;
+  return static_cast<int>(((last + 1) * L.ctas - 1) / L.total);
+}
+
 template <int NT, int M>
 __device__ __forceinline__ void scale_all(float (&o)[NT][M][4], float f) {
 #pragma unroll
@@ -369,72 +479,16 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
   using S = SplitShape<BITS, D, EX, NP, NT>;
   constexpr int NB = S::NB, R = S::R, kStages = S::kStages, NS = NP == 2 ? 2 : 4, NQ = NP == 2 ? 1 : 2;
   extern __shared__ __align__(256) uint8_t smem[];  // stage and matrix addresses are put together by xor
-  __shared__ int sh_seq, sh_scan[kAttnWarps];
-  __shared__ long long sh_before;
+  __shared__ LineShared sh_line;
   __shared__ float sh_el[kAttnWarps][R][2];
   __shared__ uint32_t sh_at[kAttnWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its place; it waits
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // ---- this CTA's units u0 .. u1-1 of the whole line, and the sequence of u0
-  const long long per = static_cast<long long>(A.c.heads) * A.chunks;
   const int cta = blockIdx.x;
-  // Sum of `x` over the CTA's threads up to this one, and over all of them.
-  auto scan = [&](int x, int* all) {
-    int sum = x;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, sum, d);
-      if (lane >= d) sum += o;
-    }
-    __syncthreads();  // the last call's sums have been read
-    if (lane == 31) sh_scan[warp] = sum;
-    __syncthreads();
-    *all = 0;
-    int add = 0;
-#pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) {
-      add += w < warp ? sh_scan[w] : 0;
-      *all += sh_scan[w];
-    }
-    return sum + add;
-  };
-  auto cost = [&](int b) { return b < A.seqs ? A.whole ? 1 : unit_count(A, seq_len(A, b)) + kAttnHead : 0; };
-  int mine = cost(tid), part, more;
-  int upto = scan(mine, &part);
-  long long sum = part;
-  for (int base = 32 * kAttnWarps; base < A.seqs; base += 32 * kAttnWarps) {
-    scan(cost(base + tid), &more);
-    sum += more;
-  }
-  const long long total = sum * per;
-  const int ctas = total < A.ctas ? static_cast<int>(total) : A.ctas;
-  if (cta >= ctas) {
-    if (tid == 0 && !A.whole) A.record[cta] = make_int4(0, 0, -1, 0);
-    return;
-  }
-  long long u = total * cta / ctas;
-  const long long u1 = total * (cta + 1) / ctas;
-  {
-    const long long v = u / per;
-    long long before = 0;
-    for (int base = 0;;) {
-      const long long end = before + upto;
-      if (mine && end - mine <= v && v < end) {
-        sh_seq = base + tid;
-        sh_before = end - mine;
-      }
-      before += part;
-      base += 32 * kAttnWarps;
-      if (base >= A.seqs || before > v) break;
-      mine = cost(base + tid);
-      upto = scan(mine, &part);
-    }
-    __syncthreads();
-  }
-  int seq = sh_seq;
-  long long off = u - sh_before * per;  // units into the sequence
+  Line line;
+  if (!line_begin<kAttnWarps>(A, sh_line, &line)) return;
 
   uint8_t* const stages = smem + warp * S::kWarpBytes;
   const uint32_t stage0 = ptx::smem_addr(stages);
@@ -447,30 +501,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
   const uint32_t scale_to = S::kCodes + scale_lane + (v_scale ? S::kCodes + S::kScales : 0);
   const long long scale_from = A.c.scale_off + scale_lane - lane * 16 + (v_scale ? v_off : 0);  // from this lane's code chunk
   bool left_record = false;
-  // The part of a pair that this CTA takes next: units k0 .. k1-1 of the
-  // pair's keys. A CTA that gets only from a pair's head leaves it to the next.
-  struct Part {
-    int seq, n, nu, pair, k0, k1;
-    long long first;  // where the pair begins
-  };
-  auto next_part = [&](Part& x) {
-    while (u < u1) {
-      const int n = seq_len(A, seq), nu = unit_count(A, n), nv = A.whole ? 1 : nu + kAttnHead;
-      if (!A.flat && tid == 0 && A.lens[seq] > n) kv_record(kKvBadLen);
-      const int pair = static_cast<int>(off / nv), at = static_cast<int>(off - static_cast<long long>(pair) * nv);
-      const int did = nv - at < u1 - u ? nv - at : static_cast<int>(u1 - u);
-      x = {seq, n, nu, pair, at > kAttnHead ? at - kAttnHead : 0, A.whole ? nu : at + did - kAttnHead, u - at};
-      u += did;
-      off += did;
-      if (off == nv * per) {
-        off = 0;
-        ++seq;
-      }
-      if (x.k1 > 0) return true;
-    }
-    return false;
-  };
-
   // ---- the warp's tiles of 16 keys of a part: warp, warp + 4, ... of its units
   int tile0 = 0, tiles = 0, line0 = 0, stage = 0;
   const int32_t* table = nullptr;
@@ -537,7 +567,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
   };
 
   Part cur;
-  bool have = next_part(cur);
+  bool have = line_next(A, line, cur);
   if (have) begin_part(cur);
   while (have) {
     const int sq = cur.seq, n = cur.n, nu = cur.nu, pair = cur.pair, k0 = cur.k0, k1 = cur.k1;
@@ -908,7 +938,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
         }
       }
     Part next;
-    const bool more_parts = next_part(next);
+    const bool more_parts = line_next(A, line, next);
     if (S::kOverlap && more_parts) begin_part(next);
     __syncthreads();
     const bool whole = k0 == 0 && k1 == nu;
@@ -937,12 +967,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
     }
     if (!whole && k0 == 0) {
       left_record = true;
-      if (tid == 0) {
-        // the CTA of the pair's last unit: the largest c with total * c / ctas <= last
-        const long long last = cur.first + nu + kAttnHead - 1;
-        const int c1 = static_cast<int>(((last + 1) * ctas - 1) / total);
-        A.record[cta] = make_int4(sq, pair, c1, 0);
-      }
+      if (tid == 0) A.record[cta] = make_int4(sq, pair, line_last(A, line, cur), 0);
     }
     __syncthreads();
     if (!S::kOverlap && more_parts) begin_part(next);

@@ -62,6 +62,7 @@ size_t kv_attn_workspace(const KvAttnArgs& a, int bits);
 // builds' words of the KV kernels.
 cudaError_t take_kv_cache_error(unsigned int* code);
 cudaError_t take_kv_attn_error(unsigned int* code);
+cudaError_t take_kv_tile_error(unsigned int* index, unsigned int* wait);  // its invalid indices, its waits that ran out
 cudaError_t take_kv_cache_check(unsigned int* code);
 cudaError_t take_kv_attn_check(unsigned int* code);
 

@@ -1,0 +1,714 @@
+// Attention over the quantized KV cache for many query rows a KV head (a
+// prefix that a whole batch shares, a long run of query tokens): tiles of 128
+// rows x 64 keys on the tcgen05 tensor cores.
+//
+// Mathematics: as in kv_attn.cuh, o = sum_j 2^(s_j - e) v_j and l alike, per
+// row, with a reference e that moves only when a weight would leave its
+// range. Both products take their A operand from tensor memory (queries,
+// 128 rows = lanes; then weights, which the thread of a row writes where its
+// scores were read: no shuffles, no shared memory) and their B operand, the
+// dequantized tile, from shared memory.
+//   16-bit queries (T = 1): everything enters as one fp16 number. K and V are
+//     code * d / 2^x rounded to fp16; 2^x, from the part's largest block scale
+//     (for V of each 32 elements), keeps them in range whatever their size.
+//   fp32 queries (T = 3): queries, weights, K and V enter as three bf16
+//     numbers each (24 bits, and fp32's exponent range, so that no scaling is
+//     needed), cut off, not rounded: a product is the six pairs that matter,
+//       1.1 + 1.2 + 2.1 + 1.3 + 2.2 + 3.1, the rest is below 2^-24.
+//
+// What bounds it: instructions of the softmax and of dequantization. A tile
+// has 8192 scores at about 6 instructions each (scale, mask test, maximum,
+// exponential, sum, conversion) and 64 * 2 * dim values to unpack at 2 (T = 1) to 9
+// (T = 3), against 2 * 128 * 64 * dim multiply-adds per product pair, 512
+// clocks of the tensor core at dim 128. So the split is by role: 8 warps for
+// the softmax (a row's 64 keys in two threads), 8 warps that copy and unpack,
+// one thread that issues the products; scores of tile i+1 are computed while
+// its weights of tile i are multiplied.
+//
+// Work is cut as in kv_attn.cuh: units of 64 keys, one CTA an SM.
+#pragma once
+
+#include "kv_attn.cuh"
+
+namespace xq {
+
+constexpr int kTileRows = 128;
+constexpr int kTileKeys = 64;
+static_assert(kTileKeys == kAttnUnit, "both kernels cut the line in the same units");
+constexpr int kTileSoft = 8, kTileConv = 8;  // warps
+constexpr int kTileWarps = kTileSoft + kTileConv + 1;
+constexpr int kTileMinRows = 64;
+constexpr int kTileHead = 6;  // units of time a pair costs besides its keys
+
+template <int BITS, int D, int T>
+struct TileShape {
+  static constexpr int NB = D / 32;
+  static constexpr int kRow = D * BITS / 8, kChunks = kRow / 16, kWords = kRow / 4;
+  // Operands in 8 x 16-byte core matrices. Neighbours in N are 144 bytes
+  // apart, so that the unpacking warps' 16-byte stores spread over the banks.
+  static constexpr int kSbo = 144;
+  static constexpr int kKLbo = kTileKeys / 8 * kSbo, kVLbo = D / 8 * kSbo;
+  static constexpr int kOperand = D * kSbo;  // one piece of K or of V: 64 keys x dim
+  static constexpr int kBufs = T == 1 ? 2 : 1;
+  static constexpr int kRawCodes = kTileKeys * kRow, kRawScales = kTileKeys * NB * 2;
+  static constexpr int kRaw = 2 * (kRawCodes + kRawScales);
+  static constexpr int kRawStages = 3;
+  static constexpr int kOffV = kBufs * T * kOperand, kOffRaw = 2 * kOffV;
+  static constexpr int kSmem = kOffRaw + kRawStages * kRaw;
+  // Tensor memory columns: queries, scores, weights, outputs.
+  static constexpr int kColS = T * D / 2, kColP = kColS + kTileKeys, kColO = kColP + T * kTileKeys / 2;
+  static constexpr int kCols = kColO + D;
+  static constexpr int kAlloc = kCols <= 256 ? 256 : 512;
+  static_assert(kCols <= 512 && kSmem <= 227 * 1024, "one CTA fits the SM");
+};
+
+template <int D>
+struct KvTileDim {
+  static cudaError_t launch(SplitArgs& a, int bits, bool exact, cudaStream_t s);
+  static cudaError_t take_error(unsigned int* index, unsigned int* wait);
+};
+
+#ifdef XQ_KV_ATTN_IMPL
+
+namespace {
+
+__device__ unsigned int g_kv_tile_error;  // a wait that ran out
+constexpr long long kTileWait = 1ll << 32;
+
+enum TileBar { kBarQ, kBarS, kBarP, kBarO, kBarK, kBarKFree = kBarK + 2, kBarV = kBarKFree + 2, kBarVFree = kBarV + 2,
+               kBarDrain = kBarVFree + 2, kBars };
+
+// Barrier of `threads` threads that gives the or of their predicates.
+__device__ __forceinline__ bool group_any(int id, int threads, bool p) {
+  int r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n selp.s32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(static_cast<int>(p)), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+// 32 lanes x 8 consecutive columns (the first 8 words of v).
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Two floats' bf16 pieces by cutting off, each pair packed (a in the low half).
+__device__ __forceinline__ void cut3(float a, float b, uint32_t (&w)[3]) {
+  const uint32_t a1 = __float_as_uint(a) & 0xFFFF0000u, b1 = __float_as_uint(b) & 0xFFFF0000u;
+  const float ra = a - __uint_as_float(a1), rb = b - __uint_as_float(b1);
+  const uint32_t a2 = __float_as_uint(ra) & 0xFFFF0000u, b2 = __float_as_uint(rb) & 0xFFFF0000u;
+  const float sa = ra - __uint_as_float(a2), sb = rb - __uint_as_float(b2);
+  w[0] = prmt(a1, b1, 0x7632u);
+  w[1] = prmt(a2, b2, 0x7632u);
+  w[2] = prmt(__float_as_uint(sa), __float_as_uint(sb), 0x7632u);
+}
+
+// Four code bytes u as floats u - 128 (BITS = 8) or nibble bytes as u - 8.
+template <int BITS>
+__device__ __forceinline__ void code_floats(uint32_t w, float (&f)[4]) {
+  constexpr float off = BITS == 8 ? 8388736.0f : 8388616.0f;  // 2^23 + 128, 2^23 + 8
+  f[0] = __uint_as_float(prmt(w, 0x4B000000u, 0x7440u)) - off;
+  f[1] = __uint_as_float(prmt(w, 0x4B000000u, 0x7441u)) - off;
+  f[2] = __uint_as_float(prmt(w, 0x4B000000u, 0x7442u)) - off;
+  f[3] = __uint_as_float(prmt(w, 0x4B000000u, 0x7443u)) - off;
+}
+// Bytes (0, 1) and (2, 3) of w as fp16 pairs u - 128 or u - 8.
+template <int BITS>
+__device__ __forceinline__ void code_halves(uint32_t w, uint32_t (&h)[2]) {
+  constexpr uint32_t off = BITS == 8 ? 0x64806480u : 0x64086408u;
+  h[0] = ptx::hsub2(prmt(w, 0x64646464u, 0x4140u), off);
+  h[1] = ptx::hsub2(prmt(w, 0x64646464u, 0x4342u), off);
+}
+
+template <int BITS, int D, int T>
+__global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __grid_constant__ SplitArgs A) {
+  using S = TileShape<BITS, D, T>;
+  constexpr int NB = S::NB;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ LineShared sh_line;
+  __shared__ __align__(8) uint64_t bars[kBars];
+  __shared__ uint32_t sh_tmem;
+  __shared__ unsigned sh_bad[4];            // tile's 16-key groups without a valid page, by tile & 3
+  __shared__ unsigned sh_top[4][1 + NB];    // T = 1: largest |scale| of the part: K's, V's blocks (fp32 bits), by part & 3
+  __shared__ float sh_x[2][kTileRows];      // exchange between a row's two threads
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto bar = [&](int i) { return ptx::smem_addr(&bars[i]); };
+  if (tid == 0) {
+    ptx::mbar_init(bar(kBarQ), kTileSoft);
+    ptx::mbar_init(bar(kBarS), 1);
+    ptx::mbar_init(bar(kBarP), kTileSoft);
+    ptx::mbar_init(bar(kBarO), 1);
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(bar(kBarK + b), kTileConv);
+      ptx::mbar_init(bar(kBarKFree + b), 1);
+      ptx::mbar_init(bar(kBarV + b), kTileConv);
+      ptx::mbar_init(bar(kBarVFree + b), 1);
+    }
+    ptx::mbar_init(bar(kBarDrain), 1);
+    ptx::mbar_init_fence();
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its place; it waits
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  Line line;
+  if (!line_begin<kTileWarps>(A, sh_line, &line)) return;
+  if (warp == kTileWarps - 1) ptx::tmem_alloc(ptx::smem_addr(&sh_tmem), S::kAlloc);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sh_tmem;
+  auto wait = [&](int i, unsigned parity, unsigned code) {
+    return ptx::mbar_wait(bar(i), parity & 1, &g_kv_tile_error, code, kTileWait);
+  };
+  auto wait_sleep = [&](int i, unsigned parity, unsigned code) {
+    return ptx::mbar_wait_sleep(bar(i), parity & 1, &g_kv_tile_error, code, kTileWait);
+  };
+  const uint32_t base = ptx::smem_addr(smem);
+  Part part;
+
+  if (warp == kTileWarps - 1) {
+    // ------------------------------------------------ products (one thread)
+    if (lane == 0) {
+      constexpr uint32_t idS = ptx::idesc_f16(kTileRows, kTileKeys, T == 3), idO = ptx::idesc_f16(kTileRows, D, T == 3);
+      // pairs of pieces (A's, B's)
+      constexpr int kPairs = T == 3 ? 6 : 1;
+      constexpr int pa[6] = {0, 0, 1, 0, 1, 2}, pb[6] = {0, 1, 0, 2, 1, 0};
+      bool ok = true;
+      unsigned it = 0, parts = 0;
+      auto scores = [&](unsigned i) {
+        const unsigned b = i % S::kBufs;
+        if (!wait(kBarK + b, i / S::kBufs, 1)) return false;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p)
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            ptx::mma_f16_ts(tmem + S::kColS, tmem + pa[p] * (D / 2) + 8 * k,
+                            ptx::smem_desc(base + (b * T + pb[p]) * S::kOperand + 2 * k * S::kKLbo, S::kKLbo, S::kSbo), idS,
+                            p + k > 0);
+        ptx::tc_commit(bar(kBarKFree + b));
+        ptx::tc_commit(bar(kBarS));
+        return true;
+      };
+      while (ok && line_next(A, line, part)) {
+        const int tiles = part.k1 - part.k0;
+        ok = wait(kBarQ, parts++, 2) && scores(it);
+        for (int i = 0; i < tiles && ok; ++i, ++it) {
+          ok = wait(kBarP, it, 3);
+          if (ok && i + 1 < tiles) ok = scores(it + 1);
+          const unsigned b = it % S::kBufs;
+          ok = ok && wait(kBarV + b, it / S::kBufs, 4);
+          if (!ok) break;
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int p = 0; p < kPairs; ++p)
+#pragma unroll
+            for (int k = 0; k < kTileKeys / 16; ++k)
+              ptx::mma_f16_ts(tmem + S::kColO, tmem + S::kColP + pa[p] * (kTileKeys / 2) + 8 * k,
+                              ptx::smem_desc(base + S::kOffV + (b * T + pb[p]) * S::kOperand + 2 * k * S::kVLbo, S::kVLbo, S::kSbo),
+                              idO, i > 0 || p + k > 0);
+          ptx::tc_commit(bar(kBarVFree + b));
+          ptx::tc_commit(bar(kBarO));
+        }
+      }
+      ptx::tc_commit(bar(kBarDrain));  // nothing is in flight when tensor memory is freed
+      wait(kBarDrain, 0, 5);
+    }
+  } else if (warp < kTileSoft) {
+    // -------------------------------------- softmax: row, and which 32 keys
+    constexpr int kThreads = 32 * kTileSoft, kBarrier = 1;
+    constexpr float kTop = T == 1 ? 15.0f : 40.0f, kStart = T == 1 ? 11.0f : 0.0f;  // log2 of weights: largest, and anew
+    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    unsigned it = 0, parts = 0;
+    bool fail = false, go = true, left_record = false;
+    while (go && line_next(A, line, part)) {
+      const int head = part.pair / A.chunks, chunk = part.pair - head * A.chunks;
+      const int row0 = chunk * kTileRows;
+      const bool live = row0 + row < A.rows;
+      const size_t at = live ? row_at(A, part.seq, head, row0 + row) : 0;
+      int lim0 = 0, lim1 = 0;
+      if (live) row_range(A, part.seq, part.n, row0 + row, &lim0, &lim1);
+      // ---- this thread's half of the row's query into tensor memory
+      float cs;
+      if (T == 1) {
+        float top = 0.0f;
+        if (live) {
+#pragma unroll 4
+          for (int d = 0; d < D; d += 4) {
+            const float4 v = load4(A.q, A.type, at * D + d);
+            top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+          }
+        }
+        int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        ex = ex < -100 ? -100 : ex;
+        const float up = __uint_as_float(static_cast<unsigned>(127 + 12 - ex) << 23);
+        cs = A.scale * 1.4426950408889634f * __uint_as_float(static_cast<unsigned>(127 - 12 + ex) << 23);
+#pragma unroll
+        for (int c = 0; c < D / 4; c += 16) {
+          uint32_t w[16];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int d = half * (D / 2) + 2 * c + 4 * x;
+            const float4 v = live && 2 * c + 4 * x < D / 2 ? load4(A.q, A.type, at * D + d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            w[2 * x] = half2_of(v.x * up, v.y * up);
+            w[2 * x + 1] = half2_of(v.z * up, v.w * up);
+          }
+          if (c + 16 <= D / 4) {
+            ptx::tmem_st16(tl + half * (D / 4) + c, w);
+          } else {
+            tmem_st8(tl + half * (D / 4) + c, w);
+          }
+        }
+      } else {
+        cs = A.scale * 1.4426950408889634f;
+#pragma unroll
+        for (int c = 0; c < D / 4; c += 8) {
+          uint32_t w[3][16];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float4 v = live ? load4(A.q, A.type, at * D + half * (D / 2) + 2 * c + 4 * x) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            uint32_t u[3];
+            cut3(v.x, v.y, u);
+            w[0][2 * x] = u[0];
+            w[1][2 * x] = u[1];
+            w[2][2 * x] = u[2];
+            cut3(v.z, v.w, u);
+            w[0][2 * x + 1] = u[0];
+            w[1][2 * x + 1] = u[1];
+            w[2][2 * x + 1] = u[2];
+          }
+#pragma unroll
+          for (int p = 0; p < 3; ++p) tmem_st8(tl + p * (D / 2) + half * (D / 4) + c, w[p]);
+        }
+      }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(kBarQ));
+
+      const int tiles = part.k1 - part.k0;
+      int key = (first_unit(A, part.n) + part.k0) * kTileKeys + half * 32;
+      float e = -1e30f, l = 0.0f;
+      for (int i = 0; i < tiles; ++i, ++it, key += kTileKeys) {
+        fail |= !wait_sleep(kBarS, it, 6);
+        ptx::tc_fence_after();
+        if (T == 1 && i == 0) {  // K's power of two, known once its first tile is there
+          const unsigned top = sh_top[parts & 3][0];
+          cs *= __uint_as_float((top >> 23 < 253 ? (top >> 23) + 1 : 254u) << 23);
+        }
+        uint32_t sv[2][16];
+        ptx::tmem_ld16(tl + S::kColS + half * 32, sv[0]);
+        ptx::tmem_ld16(tl + S::kColS + half * 32 + 16, sv[1]);
+        ptx::tmem_wait_ld();
+        float s[32], top = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < 32; ++x) s[x] = __uint_as_float(sv[x >> 4][x & 15]) * cs;
+        const unsigned bad = sh_bad[it & 3] >> (2 * half) & 3u;
+        if (key < lim0 || key + 32 > lim1 || bad) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (key + x < lim0 || key + x >= lim1 || (bad >> (x >> 4) & 1)) s[x] = -INFINITY;
+        }
+#pragma unroll
+        for (int x = 0; x < 32; ++x) top = fmaxf(top, s[x]);
+        if (group_any(kBarrier, kThreads, top - e > kTop || fail)) {
+          // ---- some row's reference moves (or a wait ran out): both threads of a row agree on the new one
+          sh_x[half][row] = top;
+          if (group_any(kBarrier, kThreads, fail)) {
+            go = false;
+            break;
+          }
+          top = fmaxf(top, sh_x[half ^ 1][row]);
+          const float next = top - e > kTop ? top - kStart : e, f = ex2(e - next);
+          e = next;
+          l *= f;
+          if (i > 0) {
+            fail |= !wait(kBarO, it - 1, 7);
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < D / 2; c += 16) {
+              uint32_t w[16];
+              ptx::tmem_ld16(tl + S::kColO + half * (D / 2) + c, w);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(__uint_as_float(w[x]) * f);
+              ptx::tmem_st16(tl + S::kColO + half * (D / 2) + c, w);
+            }
+          }
+        }
+        // ---- weights, and their operand (free once the products of the tile before are done)
+        uint32_t w[T][16];
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+          const float a = ex2(s[x] - e), b = ex2(s[x + 1] - e);
+          l += a + b;
+          if (T == 1) {
+            w[0][x / 2] = half2_of(a, b);
+          } else {
+            uint32_t u[3];
+            cut3(a, b, u);
+            w[0][x / 2] = u[0];
+            w[T / 2][x / 2] = u[1];
+            w[T - 1][x / 2] = u[2];
+          }
+        }
+        if (i > 0) {
+          fail |= !wait(kBarO, it - 1, 8);
+          ptx::tc_fence_after();
+        }
+#pragma unroll
+        for (int p = 0; p < T; ++p) ptx::tmem_st16(tl + S::kColP + p * (kTileKeys / 2) + half * 16, w[p]);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(kBarP));
+      }
+      if (!go) break;
+      // ---- the part's results
+      fail |= !wait_sleep(kBarO, it - 1, 9);
+      ptx::tc_fence_after();
+      sh_x[half][row] = l;
+      if (group_any(kBarrier, kThreads, fail)) break;
+      l += sh_x[half ^ 1][row];
+      const bool whole = part.k0 == 0 && part.k1 == part.nu;
+      const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (part.k0 == 0 ? 1 : 0)) * kTileRows + row;
+#pragma unroll
+      for (int c = 0; c < D / 2; c += 16) {
+        uint32_t w[16];
+        const int d0 = half * (D / 2) + c;
+        ptx::tmem_ld16(tl + S::kColO + d0, w);
+        ptx::tmem_wait_ld();
+        float f = 1.0f;
+        if (T == 1) {
+          const unsigned top = sh_top[parts & 3][1 + d0 / 32];
+          f = __uint_as_float((top >> 23 < 253 ? (top >> 23) + 1 : 254u) << 23);
+        }
+        if (live) {
+#pragma unroll
+          for (int x = 0; x < 16; x += 4) {
+            const float4 y = make_float4(__uint_as_float(w[x]) * f, __uint_as_float(w[x + 1]) * f, __uint_as_float(w[x + 2]) * f,
+                                         __uint_as_float(w[x + 3]) * f);
+            if (whole) {
+              finish4(A, D, at, d0 + x, y, e, l);
+            } else {
+              *reinterpret_cast<float4*>(A.part_o + slot * D + d0 + x) = y;
+              if (d0 + x == 0) *reinterpret_cast<float2*>(A.part_el + slot * 2) = make_float2(e, l);
+            }
+          }
+        }
+      }
+      if (!whole && part.k0 == 0) {
+        left_record = true;
+        if (tid == 0) A.record[blockIdx.x] = make_int4(part.seq, part.pair, line_last(A, line, part), 0);
+      }
+      ptx::tc_fence_before();
+      // the other half's sums have been read when the next barrier is passed
+      group_any(kBarrier, kThreads, false);
+      ++parts;
+    }
+    if (!left_record && tid == 0 && !A.whole) A.record[blockIdx.x] = make_int4(0, 0, -1, 0);
+  } else {
+    // ------------------------------------------------ copying and unpacking
+    constexpr int kThreads = 32 * kTileConv, kBarrier = 2;
+    const int ct = tid - 32 * kTileSoft;
+    const int groups_page = 1 << (A.c.page_shift - 4);  // 16-key groups a page
+    const long long v_off = reinterpret_cast<long long>(A.c.v) - reinterpret_cast<long long>(A.c.k);
+    unsigned it = 0, parts = 0;
+    bool fail = false, go = true;
+    while (go && line_next(A, line, part)) {
+      const int tiles = part.k1 - part.k0, unit0 = first_unit(A, part.n) + part.k0;
+      const int32_t* const table = A.flat ? A.pages : A.pages + static_cast<size_t>(part.seq) * A.page_stride;
+      const int line0 = (part.pair / A.chunks) << A.c.page_shift;
+      const int groups = (part.n + 15) / 16;  // of the sequence
+      // Address of 16-key group gi's page, or 0; its first row within the head's rows.
+      auto page_at = [&](int gi) -> long long {
+        if (gi >= groups) return 0;
+        const int page = table[gi / groups_page];
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(A.c.n_pages))
+          return reinterpret_cast<long long>(A.c.k) + page * A.c.page_bytes;
+        kv_record(kKvBadPage);
+        return 0;
+      };
+      auto row_of = [&](int gi) { return line0 + ((gi & (groups_page - 1)) << 4); };
+
+      float kf = 1.0f, vf[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) vf[b] = 1.0f;
+      if (T == 1) {
+        // ---- the part's largest scales: 1 / 17 or 1 / 9 of its bytes, which its tiles then find in L2
+        unsigned* const tops = sh_top[parts & 3];
+        if (ct <= NB) tops[ct] = 0u;
+        if (group_any(kBarrier, kThreads, fail)) break;
+        unsigned top[1 + NB];
+#pragma unroll
+        for (int b = 0; b <= NB; ++b) top[b] = 0u;
+        const int pieces = tiles * 4 * 2 * NB;  // 16-byte pieces of K's scales, 2 NB a group
+        for (int x = ct; x < pieces; x += kThreads) {
+          const int gl = x / (2 * NB), piece = x - gl * 2 * NB, gi = unit0 * 4 + gl;
+          const long long page = page_at(gi);
+          if (!page) continue;
+          const uint8_t* const p = reinterpret_cast<const uint8_t*>(page) + A.c.scale_off + row_of(gi) * (2 * NB) + piece * 16;
+          const uint4 k4 = *reinterpret_cast<const uint4*>(p), v4 = *reinterpret_cast<const uint4*>(p + v_off);
+          const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w}, vw[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+          for (int h = 0; h < 8; ++h) {
+            const int flat = piece * 8 + h;
+            if (gi * 16 + flat / NB < part.n) {
+              const unsigned sh = 16 * (h & 1);
+              const unsigned a = __float_as_uint(fabsf(half_bits_to_float(kw[h / 2] >> sh)));
+              const unsigned c = __float_as_uint(fabsf(half_bits_to_float(vw[h / 2] >> sh)));
+              top[0] = max(top[0], a);
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                if (b == flat % NB) top[1 + b] = max(top[1 + b], c);
+            }
+          }
+        }
+#pragma unroll
+        for (int b = 0; b <= NB; ++b) {
+          const unsigned m = __reduce_max_sync(0xffffffffu, top[b]);
+          if (lane == 0) atomicMax(&tops[b], m);
+        }
+        if (group_any(kBarrier, kThreads, fail)) break;
+        // 2^-(exponent + 1): scales come to at most 1
+        auto down = [](unsigned t) { return __uint_as_float((t >> 23 < 253 ? 253 - (t >> 23) : 0u) << 23); };
+        kf = down(tops[0]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) vf[b] = down(tops[1 + b]);
+      }
+
+      // ---- raw tiles, two ahead: this thread's chunks of tile i
+      unsigned bads = 0;  // 4 bits a stage
+      auto issue = [&](int i) {
+        if (i < tiles) {
+          const uint32_t to = base + S::kOffRaw + (it + i) % S::kRawStages * S::kRaw;
+          const int gi0 = (unit0 + i) * 4;
+          const long long mine = page_at(gi0 + (lane & 3));
+          const unsigned miss = __ballot_sync(0xffffffffu, mine == 0) & 15u;
+          const unsigned st = (it + i) % S::kRawStages * 4;
+          bads = (bads & ~(15u << st)) | (miss << st);
+#pragma unroll
+          for (int x = 0; x < (kTileKeys * S::kChunks + kThreads - 1) / kThreads; ++x) {
+            const int c = x * kThreads + ct, key = c / S::kChunks, ch = c - key * S::kChunks;
+            const long long page = __shfl_sync(0xffffffffu, mine, (key >> 4) & 3);
+            if (page && key < kTileKeys) {
+              const uint8_t* const p =
+                  reinterpret_cast<const uint8_t*>(page) + (row_of(gi0 + (key >> 4)) + (key & 15)) * S::kRow + ch * 16;
+              const uint32_t dst = to + chunk_at<S::kChunks>(key, ch);
+              cp16(dst, p);
+              cp16(dst + S::kRawCodes, p + v_off);
+            }
+          }
+          {
+            constexpr int kPieces = 4 * 2 * NB;  // of K's scales; V's follow
+            const int c = ct < kPieces ? ct : ct - kPieces, gl = c / (2 * NB);
+            const long long page = __shfl_sync(0xffffffffu, mine, gl & 3);
+            if (ct < 2 * kPieces && page) {
+              const uint8_t* const p = reinterpret_cast<const uint8_t*>(page) + A.c.scale_off + row_of(gi0 + gl) * (2 * NB) +
+                                       (c - gl * 2 * NB) * 16 + (ct < kPieces ? 0 : v_off);
+              cp16(to + 2 * S::kRawCodes + (ct < kPieces ? 0 : S::kRawScales) + c * 16, p);
+            }
+          }
+        }
+        cp_commit();
+      };
+      issue(0);
+      issue(1);
+      for (int i = 0; i < tiles; ++i, ++it) {
+        cp_wait<1>();
+        // every thread's copies of this tile have landed, and the tile before has been unpacked
+        if (group_any(kBarrier, kThreads, fail)) {
+          go = false;
+          break;
+        }
+        {
+          // tile it + 2 (its own index is counted from `it`, which the loop advances)
+          const unsigned keep = it;
+          it -= i;
+          issue(i + 2);
+          it = keep;
+        }
+        const uint8_t* const raw = smem + S::kOffRaw + it % S::kRawStages * S::kRaw;
+        const __half* const kd = reinterpret_cast<const __half*>(raw + 2 * S::kRawCodes);
+        const __half* const vd = kd + S::kRawScales / 2;
+        const unsigned miss = bads >> (it % S::kRawStages * 4) & 15u;
+        const int left = part.n - (unit0 + i) * kTileKeys;  // keys of the sequence from the tile's first on
+        auto gone = [&](int key) { return key >= left || (miss >> (key >> 4) & 1); };
+        const unsigned b = it % S::kBufs, turn = it / S::kBufs;
+        // ---- K: operand rows are keys. A task is a key's 16-byte chunk
+        if (turn > 0) fail |= !wait_sleep(kBarKFree + b, turn - 1, 10);
+        if (ct == 0) sh_bad[it & 3] = miss;
+        uint8_t* const ko = smem + b * T * S::kOperand;
+#pragma unroll
+        for (int x = 0; x < (kTileKeys * S::kChunks + kThreads - 1) / kThreads; ++x) {
+          const int c = x * kThreads + ct, key = c & (kTileKeys - 1), ch = c / kTileKeys;
+          if (ch < S::kChunks) {
+            const uint4 u4 = *reinterpret_cast<const uint4*>(raw + chunk_at<S::kChunks>(key, ch));
+            const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w};
+            const float d = gone(key) ? 0.0f : __half2float(kd[key * NB + (BITS == 8 ? ch / 2 : ch)]) * kf;
+            uint8_t* const to = ko + (key >> 3) * S::kSbo + (key & 7) * 16;
+#pragma unroll
+            for (int z = 0; z < (BITS == 8 ? 2 : 4); ++z) {  // 8 elements each
+              const uint32_t w0 = BITS == 8 ? u[2 * z] : (u[2 * (z & 1)] >> (z & 2 ? 4 : 0)) & 0x0F0F0F0Fu;
+              const uint32_t w1 = BITS == 8 ? u[2 * z + 1] : (u[2 * (z & 1) + 1] >> (z & 2 ? 4 : 0)) & 0x0F0F0F0Fu;
+              uint8_t* const cell = to + (ch * (BITS == 8 ? 2 : 4) + z) * S::kKLbo;
+              if (T == 1) {
+                uint32_t h0[2], h1[2];
+                code_halves<BITS>(w0, h0);
+                code_halves<BITS>(w1, h1);
+                const uint32_t dd = half2_of(d, d);
+                *reinterpret_cast<uint4*>(cell) =
+                    make_uint4(ptx::hmul2(h0[0], dd), ptx::hmul2(h0[1], dd), ptx::hmul2(h1[0], dd), ptx::hmul2(h1[1], dd));
+              } else {
+                float f0[4], f1[4];
+                code_floats<BITS>(w0, f0);
+                code_floats<BITS>(w1, f1);
+                uint32_t q[4][3];
+                cut3(f0[0] * d, f0[1] * d, q[0]);
+                cut3(f0[2] * d, f0[3] * d, q[1]);
+                cut3(f1[0] * d, f1[1] * d, q[2]);
+                cut3(f1[2] * d, f1[3] * d, q[3]);
+#pragma unroll
+                for (int p = 0; p < 3; ++p)
+                  *reinterpret_cast<uint4*>(cell + p * S::kOperand) = make_uint4(q[0][p], q[1][p], q[2][p], q[3][p]);
+              }
+            }
+          }
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(kBarK + b));
+        // ---- V: operand rows are elements. A task is a word (4 code bytes) of 8 keys
+        if (turn > 0) fail |= !wait_sleep(kBarVFree + b, turn - 1, 11);
+        uint8_t* const vo = smem + S::kOffV + b * T * S::kOperand;
+#pragma unroll
+        for (int x = 0; x < (8 * S::kWords + kThreads - 1) / kThreads; ++x) {
+          const int c = x * kThreads + ct, kg = c / S::kWords, word = c - kg * S::kWords;
+          if (kg < 8) {
+            const int blk = BITS == 8 ? word / 8 : word / 4;
+            uint32_t u[8];
+            float d[8];
+            float f = vf[0];
+#pragma unroll
+            for (int q = 1; q < NB; ++q) f = blk == q ? vf[q] : f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int key = kg * 8 + k;
+              u[k] = *reinterpret_cast<const uint32_t*>(raw + S::kRawCodes + chunk_at<S::kChunks>(key, word / 4) + (word & 3) * 4);
+              d[k] = gone(key) ? 0.0f : __half2float(vd[key * NB + blk]) * f;
+            }
+            // elements 4 word + i; of a 4-bit block 32 blk + 4 (word % 4) + i, and 16 further on those of the high halves
+#pragma unroll
+            for (int z = 0; z < (BITS == 8 ? 1 : 2); ++z) {
+              const int e0 = BITS == 8 ? 4 * word : 32 * blk + 4 * (word & 3) + 16 * z;
+              uint8_t* const to = vo + kg * S::kVLbo + (e0 >> 3) * S::kSbo + (e0 & 7) * 16;
+              uint32_t v[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = BITS == 8 ? u[k] : (u[k] >> (4 * z)) & 0x0F0F0F0Fu;
+              if (T == 1) {
+                uint32_t r[4][4];  // [element][key pair]
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) {
+                  const uint32_t lo = prmt(v[k], v[k + 1], 0x5140u), hi = prmt(v[k], v[k + 1], 0x7362u);
+                  const uint32_t dd = half2_of(d[k], d[k + 1]);
+                  uint32_t h0[2], h1[2];
+                  code_halves<BITS>(lo, h0);
+                  code_halves<BITS>(hi, h1);
+                  r[0][k / 2] = ptx::hmul2(h0[0], dd);
+                  r[1][k / 2] = ptx::hmul2(h0[1], dd);
+                  r[2][k / 2] = ptx::hmul2(h1[0], dd);
+                  r[3][k / 2] = ptx::hmul2(h1[1], dd);
+                }
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  *reinterpret_cast<uint4*>(to + y * 16) = make_uint4(r[y][0], r[y][1], r[y][2], r[y][3]);
+              } else {
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  constexpr float off = BITS == 8 ? 8388736.0f : 8388616.0f;
+                  uint32_t r[4][3];
+#pragma unroll
+                  for (int k = 0; k < 8; k += 2) {
+                    const uint32_t sel = 0x7440u + y;
+                    cut3((__uint_as_float(prmt(v[k], 0x4B000000u, sel)) - off) * d[k],
+                         (__uint_as_float(prmt(v[k + 1], 0x4B000000u, sel)) - off) * d[k + 1], r[k / 2]);
+                  }
+#pragma unroll
+                  for (int p = 0; p < 3; ++p)
+                    *reinterpret_cast<uint4*>(to + y * 16 + p * S::kOperand) = make_uint4(r[0][p], r[1][p], r[2][p], r[3][p]);
+                }
+              }
+            }
+          }
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(kBarV + b));
+      }
+      cp_wait<0>();
+      ++parts;
+      // the raw stages are free for the next part once every thread is here
+      if (go) group_any(kBarrier, kThreads, false);
+    }
+    cp_wait<0>();
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kTileWarps - 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, S::kAlloc);
+  }
+}
+
+template <int BITS, int D, int T>
+cudaError_t launch_tile_attn(SplitArgs& a, cudaStream_t s) {
+  using S = TileShape<BITS, D, T>;
+  a.ctas = a.units < kNumSMs ? static_cast<int>(a.units) : kNumSMs;
+  static const cudaError_t attr_error =
+      cudaFuncSetAttribute(kv_tile_kernel<BITS, D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (attr_error != cudaSuccess) return attr_error;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
+  cfg.blockDim = dim3(32 * kTileWarps);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_tile_kernel<BITS, D, T>, a);
+  if (e != cudaSuccess || a.whole) return e;
+  constexpr int kRowsBlock = 8;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.ctas), kTileRows / kRowsBlock);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, kTileRows, kRowsBlock>, a);
+}
+
+}  // namespace
+
+template <int D>
+cudaError_t KvTileDim<D>::launch(SplitArgs& a, int bits, bool exact, cudaStream_t s) {
+  if (bits == 8) return exact ? launch_tile_attn<8, D, 3>(a, s) : launch_tile_attn<8, D, 1>(a, s);
+  return exact ? launch_tile_attn<4, D, 3>(a, s) : launch_tile_attn<4, D, 1>(a, s);
+}
+
+template <int D>
+cudaError_t KvTileDim<D>::take_error(unsigned int* index, unsigned int* wait) {
+  unsigned int z = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(index, g_kv_attn_error, sizeof(z));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_kv_attn_error, &z, sizeof(z));
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(wait, g_kv_tile_error, sizeof(z));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_kv_tile_error, &z, sizeof(z));
+  return e;
+}
+
+#endif  // XQ_KV_ATTN_IMPL
+
+}  // namespace xq

@@ -1,0 +1,7 @@
+// The cache attention's tcgen05 kernels at head size 64 (a translation unit of its own).
+#define XQ_KV_ATTN_IMPL
+#include "kv_tile.cuh"
+
+namespace xq {
+template struct KvTileDim<64>;
+}

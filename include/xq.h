@@ -335,7 +335,8 @@ XQ_API xq_status xq_layer_mixed_static(const xq_proj *proj, int n_proj,
  * feed of xq_layer_mixed_ffn). Kernel 3 = the KV cache kernels, whose record
  * is of an invalid index, not of a wait: 1 a slot past the cache, 2 a page id
  * outside it, 3 a sequence longer than its page table (see xq_kv_write and
- * xq_kv_attn). Checked builds (the library compiled with
+ * xq_kv_attn). Kernel 4 = the cache attention's 128-row tiles (waits 1-5 the
+ * products, 6-9 the softmax, 10-11 the unpacking). Checked builds (the library compiled with
  * -DXQ_CHECK) also test the index, range or 16-byte alignment of each global
  * access whose address comes from nontrivial arithmetic, skip an access that
  * fails and record the site: kernel 9, wait = site (10-16 the GEMV, 20-26
