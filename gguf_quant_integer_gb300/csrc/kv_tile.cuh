@@ -49,14 +49,18 @@ struct TileShape {
   static constexpr int kSbo = 144;
   static constexpr int kKLbo = kTileKeys / 8 * kSbo, kVLbo = D / 8 * kSbo;
   static constexpr int kOperand = D * kSbo;  // one piece of K or of V: 64 keys x dim
-  static constexpr int kBufs = T == 1 ? 2 : 1;
+  static constexpr int kBufs = T == 1 ? 2 : 1;  // of K, V, scores and weights
   static constexpr int kRawCodes = kTileKeys * kRow, kRawScales = kTileKeys * NB * 2;
   static constexpr int kRaw = 2 * (kRawCodes + kRawScales);
-  static constexpr int kRawStages = 3;
+  static constexpr int kRawStages = 4;  // two of each group of unpacking warps
   static constexpr int kOffV = kBufs * T * kOperand, kOffRaw = 2 * kOffV;
-  static constexpr int kSmem = kOffRaw + kRawStages * kRaw;
+  // The tile's scales, ready for use: K's [64][NB], V's [NB][64], fp16 or fp32.
+  static constexpr int kScaleBytes = T == 1 ? 2 : 4;
+  static constexpr int kOffScale = kOffRaw + kRawStages * kRaw;
+  static constexpr int kScales = 2 * kTileKeys * NB * kScaleBytes;  // a table for each group
+  static constexpr int kSmem = kOffScale + 2 * kScales;
   // Tensor memory columns: queries, scores, weights, outputs.
-  static constexpr int kColS = T * D / 2, kColP = kColS + kTileKeys, kColO = kColP + T * kTileKeys / 2;
+  static constexpr int kColS = T * D / 2, kColP = kColS + kBufs * kTileKeys, kColO = kColP + kBufs * T * kTileKeys / 2;
   static constexpr int kCols = kColO + D;
   static constexpr int kAlloc = kCols <= 256 ? 256 : 512;
   static_assert(kCols <= 512 && kSmem <= 227 * 1024, "one CTA fits the SM");
@@ -75,8 +79,10 @@ namespace {
 __device__ unsigned int g_kv_tile_error;  // a wait that ran out
 constexpr long long kTileWait = 1ll << 32;
 
-enum TileBar { kBarQ, kBarS, kBarP, kBarO, kBarK, kBarKFree = kBarK + 2, kBarV = kBarKFree + 2, kBarVFree = kBarV + 2,
-               kBarDrain = kBarVFree + 2, kBars };
+// Barriers; those of buffers in pairs, one a buffer: two tiles may be complete at a time, and a barrier's parity tells only
+// a phase from the next.
+enum TileBar { kBarQ, kBarDrain, kBarS, kBarP = kBarS + 2, kBarO = kBarP + 2, kBarK = kBarO + 2, kBarKFree = kBarK + 2,
+               kBarV = kBarKFree + 2, kBarVFree = kBarV + 2, kBars = kBarVFree + 2 };
 
 // Barrier of `threads` threads that gives the or of their predicates.
 __device__ __forceinline__ bool group_any(int id, int threads, bool p) {
@@ -94,6 +100,12 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[16]
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
                "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // Two floats' bf16 pieces by cutting off, each pair packed (a in the low half).
@@ -128,7 +140,7 @@ template <int BITS, int D, int T>
 __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __grid_constant__ SplitArgs A) {
   using S = TileShape<BITS, D, T>;
   constexpr int NB = S::NB;
-  extern __shared__ __align__(1024) uint8_t smem[];
+  extern __shared__ __align__(256) uint8_t smem[];
   __shared__ LineShared sh_line;
   __shared__ __align__(8) uint64_t bars[kBars];
   __shared__ uint32_t sh_tmem;
@@ -139,13 +151,13 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
   auto bar = [&](int i) { return ptx::smem_addr(&bars[i]); };
   if (tid == 0) {
     ptx::mbar_init(bar(kBarQ), kTileSoft);
-    ptx::mbar_init(bar(kBarS), 1);
-    ptx::mbar_init(bar(kBarP), kTileSoft);
-    ptx::mbar_init(bar(kBarO), 1);
     for (int b = 0; b < 2; ++b) {
-      ptx::mbar_init(bar(kBarK + b), kTileConv);
+      ptx::mbar_init(bar(kBarS + b), 1);
+      ptx::mbar_init(bar(kBarP + b), kTileSoft);
+      ptx::mbar_init(bar(kBarO + b), 1);
+      ptx::mbar_init(bar(kBarK + b), kTileConv / 2);
       ptx::mbar_init(bar(kBarKFree + b), 1);
-      ptx::mbar_init(bar(kBarV + b), kTileConv);
+      ptx::mbar_init(bar(kBarV + b), kTileConv / 2);
       ptx::mbar_init(bar(kBarVFree + b), 1);
     }
     ptx::mbar_init(bar(kBarDrain), 1);
@@ -186,32 +198,36 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         for (int p = 0; p < kPairs; ++p)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            ptx::mma_f16_ts(tmem + S::kColS, tmem + pa[p] * (D / 2) + 8 * k,
+            ptx::mma_f16_ts(tmem + S::kColS + b * kTileKeys, tmem + pa[p] * (D / 2) + 8 * k,
                             ptx::smem_desc(base + (b * T + pb[p]) * S::kOperand + 2 * k * S::kKLbo, S::kKLbo, S::kSbo), idS,
                             p + k > 0);
         ptx::tc_commit(bar(kBarKFree + b));
-        ptx::tc_commit(bar(kBarS));
+        ptx::tc_commit(bar(kBarS + b));
         return true;
       };
       while (ok && line_next(A, line, part)) {
         const int tiles = part.k1 - part.k0;
-        ok = wait(kBarQ, parts++, 2) && scores(it);
+        ok = wait(kBarQ, parts++, 2);
+        for (int i = 0; i < S::kBufs && i < tiles && ok; ++i) ok = scores(it + i);
         for (int i = 0; i < tiles && ok; ++i, ++it) {
-          ok = wait(kBarP, it, 3);
-          if (ok && i + 1 < tiles) ok = scores(it + 1);
-          const unsigned b = it % S::kBufs;
-          ok = ok && wait(kBarV + b, it / S::kBufs, 4);
+          const unsigned b = it % S::kBufs, turn = it / S::kBufs;
+          // the tile's weights are there: its scores' buffer is free. With one buffer the next scores come before these
+          // products, or the softmax would wait for both; with two they are a tile ahead anyway
+          ok = wait(kBarP + b, turn, 3);
+          if (S::kBufs == 1 && ok && i + 1 < tiles) ok = scores(it + 1);
+          ok = ok && wait(kBarV + b, turn, 4);
           if (!ok) break;
           ptx::tc_fence_after();
 #pragma unroll
           for (int p = 0; p < kPairs; ++p)
 #pragma unroll
             for (int k = 0; k < kTileKeys / 16; ++k)
-              ptx::mma_f16_ts(tmem + S::kColO, tmem + S::kColP + pa[p] * (kTileKeys / 2) + 8 * k,
+              ptx::mma_f16_ts(tmem + S::kColO, tmem + S::kColP + (b * T + pa[p]) * (kTileKeys / 2) + 8 * k,
                               ptx::smem_desc(base + S::kOffV + (b * T + pb[p]) * S::kOperand + 2 * k * S::kVLbo, S::kVLbo, S::kSbo),
                               idO, i > 0 || p + k > 0);
           ptx::tc_commit(bar(kBarVFree + b));
-          ptx::tc_commit(bar(kBarO));
+          ptx::tc_commit(bar(kBarO + b));
+          if (S::kBufs > 1 && i + S::kBufs < tiles) ok = scores(it + S::kBufs);
         }
       }
       ptx::tc_commit(bar(kBarDrain));  // nothing is in flight when tensor memory is freed
@@ -232,39 +248,48 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       const size_t at = live ? row_at(A, part.seq, head, row0 + row) : 0;
       int lim0 = 0, lim1 = 0;
       if (live) row_range(A, part.seq, part.n, row0 + row, &lim0, &lim1);
-      // ---- this thread's half of the row's query into tensor memory
-      float cs;
+      // ---- this thread's half of the row's query into tensor memory, negated for a negative scale (so that cs > 0)
+      float cs = fmaxf(fabsf(A.scale) * 1.4426950408889634f, 1.17549435e-38f);
+      const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
       if (T == 1) {
+        uint4 raw[D / 16];
+        const uint4* const from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.q) + at * D + half * (D / 2));
         float top = 0.0f;
-        if (live) {
-#pragma unroll 4
-          for (int d = 0; d < D; d += 4) {
-            const float4 v = load4(A.q, A.type, at * D + d);
-            top = fmaxf(fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
-          }
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) raw[x] = live ? from[x] : make_uint4(0u, 0u, 0u, 0u);
+        const bool f16 = A.type == kF16;
+        auto both = [&](uint32_t w) {
+          return f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w))
+                     : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+        };
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          const float2 a = both(raw[x].x), b = both(raw[x].y), c = both(raw[x].z), d = both(raw[x].w);
+          top = fmaxf(fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y))),
+                      fmaxf(fmaxf(fabsf(c.x), fabsf(c.y)), fmaxf(fabsf(d.x), fabsf(d.y))));
         }
+        sh_x[half][row] = top;
+        if (group_any(kBarrier, kThreads, fail)) break;
+        top = fmaxf(top, sh_x[half ^ 1][row]);
         int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
         ex = ex < -100 ? -100 : ex;
-        const float up = __uint_as_float(static_cast<unsigned>(127 + 12 - ex) << 23);
-        cs = A.scale * 1.4426950408889634f * __uint_as_float(static_cast<unsigned>(127 - 12 + ex) << 23);
+        const float up = sign * __uint_as_float(static_cast<unsigned>(127 + 12 - ex) << 23);
+        cs = fmaxf(cs * __uint_as_float(static_cast<unsigned>(127 - 12 + ex) << 23), 1.17549435e-38f);
 #pragma unroll
-        for (int c = 0; c < D / 4; c += 16) {
+        for (int c = 0; c < D / 4; c += 8) {
           uint32_t w[16];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const int d = half * (D / 2) + 2 * c + 4 * x;
-            const float4 v = live && 2 * c + 4 * x < D / 2 ? load4(A.q, A.type, at * D + d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            w[2 * x] = half2_of(v.x * up, v.y * up);
-            w[2 * x + 1] = half2_of(v.z * up, v.w * up);
+          for (int x = 0; x < 2; ++x) {
+            const uint4 r = raw[c / 4 + x];
+            const float2 a = both(r.x), b = both(r.y), g = both(r.z), d = both(r.w);
+            w[4 * x] = half2_of(a.x * up, a.y * up);
+            w[4 * x + 1] = half2_of(b.x * up, b.y * up);
+            w[4 * x + 2] = half2_of(g.x * up, g.y * up);
+            w[4 * x + 3] = half2_of(d.x * up, d.y * up);
           }
-          if (c + 16 <= D / 4) {
-            ptx::tmem_st16(tl + half * (D / 4) + c, w);
-          } else {
-            tmem_st8(tl + half * (D / 4) + c, w);
-          }
+          tmem_st8(tl + half * (D / 4) + c, w);
         }
       } else {
-        cs = A.scale * 1.4426950408889634f;
 #pragma unroll
         for (int c = 0; c < D / 4; c += 8) {
           uint32_t w[3][16];
@@ -272,11 +297,11 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           for (int x = 0; x < 4; ++x) {
             const float4 v = live ? load4(A.q, A.type, at * D + half * (D / 2) + 2 * c + 4 * x) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             uint32_t u[3];
-            cut3(v.x, v.y, u);
+            cut3(v.x * sign, v.y * sign, u);
             w[0][2 * x] = u[0];
             w[1][2 * x] = u[1];
             w[2][2 * x] = u[2];
-            cut3(v.z, v.w, u);
+            cut3(v.z * sign, v.w * sign, u);
             w[0][2 * x + 1] = u[0];
             w[1][2 * x + 1] = u[1];
             w[2][2 * x + 1] = u[2];
@@ -292,29 +317,36 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
 
       const int tiles = part.k1 - part.k0;
       int key = (first_unit(A, part.n) + part.k0) * kTileKeys + half * 32;
-      float e = -1e30f, l = 0.0f;
+      float e = -1e30f;
+      ptx::f2 l = ptx::pk(0.0f, 0.0f);
       for (int i = 0; i < tiles; ++i, ++it, key += kTileKeys) {
-        fail |= !wait_sleep(kBarS, it, 6);
+        const unsigned b = it % S::kBufs, turn = it / S::kBufs;
+        fail |= !wait_sleep(kBarS + b, turn, 6);
         ptx::tc_fence_after();
         if (T == 1 && i == 0) {  // K's power of two, known once its first tile is there
           const unsigned top = sh_top[parts & 3][0];
-          cs *= __uint_as_float((top >> 23 < 253 ? (top >> 23) + 1 : 254u) << 23);
+          cs = fmaxf(cs * __uint_as_float((top >> 23 < 253 ? (top >> 23) + 1 : 254u) << 23), 1.17549435e-38f);
         }
         uint32_t sv[2][16];
-        ptx::tmem_ld16(tl + S::kColS + half * 32, sv[0]);
-        ptx::tmem_ld16(tl + S::kColS + half * 32 + 16, sv[1]);
+        ptx::tmem_ld16(tl + S::kColS + b * kTileKeys + half * 32, sv[0]);
+        ptx::tmem_ld16(tl + S::kColS + b * kTileKeys + half * 32 + 16, sv[1]);
         ptx::tmem_wait_ld();
-        float s[32], top = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < 32; ++x) s[x] = __uint_as_float(sv[x >> 4][x & 15]) * cs;
         const unsigned bad = sh_bad[it & 3] >> (2 * half) & 3u;
         if (key < lim0 || key + 32 > lim1 || bad) {
 #pragma unroll
           for (int x = 0; x < 32; ++x)
-            if (key + x < lim0 || key + x >= lim1 || (bad >> (x >> 4) & 1)) s[x] = -INFINITY;
+            if (key + x < lim0 || key + x >= lim1 || (bad >> (x >> 4) & 1)) sv[x >> 4][x & 15] = 0xFF800000u;
         }
+        float tops4[4];  // four chains: the row's thread has nothing else to do meanwhile
 #pragma unroll
-        for (int x = 0; x < 32; ++x) top = fmaxf(top, s[x]);
+        for (int x = 0; x < 4; ++x) {
+          tops4[x] = __uint_as_float(sv[x >> 1][8 * (x & 1)]);
+#pragma unroll
+          for (int y = 1; y < 7; y += 2)
+            tops4[x] = max3(tops4[x], __uint_as_float(sv[x >> 1][8 * (x & 1) + y]), __uint_as_float(sv[x >> 1][8 * (x & 1) + y + 1]));
+          tops4[x] = fmaxf(tops4[x], __uint_as_float(sv[x >> 1][8 * (x & 1) + 7]));
+        }
+        float top = fmaxf(fmaxf(tops4[0], tops4[1]), fmaxf(tops4[2], tops4[3])) * cs;
         if (group_any(kBarrier, kThreads, top - e > kTop || fail)) {
           // ---- some row's reference moves (or a wait ran out): both threads of a row agree on the new one
           sh_x[half][row] = top;
@@ -325,9 +357,9 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           top = fmaxf(top, sh_x[half ^ 1][row]);
           const float next = top - e > kTop ? top - kStart : e, f = ex2(e - next);
           e = next;
-          l *= f;
+          l = ptx::mul2(l, ptx::pk(f, f));
           if (i > 0) {
-            fail |= !wait(kBarO, it - 1, 7);
+            fail |= !wait(kBarO + (it - 1) % S::kBufs, (it - 1) / S::kBufs, 7);
             ptx::tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D / 2; c += 16) {
@@ -340,40 +372,44 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             }
           }
         }
-        // ---- weights, and their operand (free once the products of the tile before are done)
+        // ---- weights
         uint32_t w[T][16];
+        const ptx::f2 c2 = ptx::pk(cs, cs), e2 = ptx::pk(-e, -e);
 #pragma unroll
         for (int x = 0; x < 32; x += 2) {
-          const float a = ex2(s[x] - e), b = ex2(s[x + 1] - e);
-          l += a + b;
+          const ptx::f2 z = ptx::fma2(ptx::pk(__uint_as_float(sv[x >> 4][x & 15]), __uint_as_float(sv[x >> 4][(x & 15) + 1])), c2, e2);
+          const float a = ex2(ptx::lo32(z)), d = ex2(ptx::hi32(z));
+          l = ptx::add2(l, ptx::pk(a, d));
           if (T == 1) {
-            w[0][x / 2] = half2_of(a, b);
+            w[0][x / 2] = half2_of(a, d);
           } else {
             uint32_t u[3];
-            cut3(a, b, u);
+            cut3(a, d, u);
             w[0][x / 2] = u[0];
             w[T / 2][x / 2] = u[1];
             w[T - 1][x / 2] = u[2];
           }
         }
-        if (i > 0) {
-          fail |= !wait(kBarO, it - 1, 8);
+        // ---- and their operand, whose buffer is free once the products that used it last are done
+        if (i >= S::kBufs) {
+          fail |= !wait(kBarO + b, turn - 1, 8);
           ptx::tc_fence_after();
         }
 #pragma unroll
-        for (int p = 0; p < T; ++p) ptx::tmem_st16(tl + S::kColP + p * (kTileKeys / 2) + half * 16, w[p]);
+        for (int p = 0; p < T; ++p) ptx::tmem_st16(tl + S::kColP + (b * T + p) * (kTileKeys / 2) + half * 16, w[p]);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(kBarP));
+        if (lane == 0) ptx::mbar_arrive(bar(kBarP + b));
       }
       if (!go) break;
       // ---- the part's results
-      fail |= !wait_sleep(kBarO, it - 1, 9);
+      fail |= !wait_sleep(kBarO + (it - 1) % S::kBufs, (it - 1) / S::kBufs, 9);
       ptx::tc_fence_after();
-      sh_x[half][row] = l;
+      float sum = ptx::lo32(l) + ptx::hi32(l);
+      sh_x[half][row] = sum;
       if (group_any(kBarrier, kThreads, fail)) break;
-      l += sh_x[half ^ 1][row];
+      sum = half ? sh_x[0][row] + sum : sum + sh_x[1][row];
       const bool whole = part.k0 == 0 && part.k1 == part.nu;
       const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (part.k0 == 0 ? 1 : 0)) * kTileRows + row;
 #pragma unroll
@@ -393,10 +429,10 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             const float4 y = make_float4(__uint_as_float(w[x]) * f, __uint_as_float(w[x + 1]) * f, __uint_as_float(w[x + 2]) * f,
                                          __uint_as_float(w[x + 3]) * f);
             if (whole) {
-              finish4(A, D, at, d0 + x, y, e, l);
+              finish4(A, D, at, d0 + x, y, e, sum);
             } else {
               *reinterpret_cast<float4*>(A.part_o + slot * D + d0 + x) = y;
-              if (d0 + x == 0) *reinterpret_cast<float2*>(A.part_el + slot * 2) = make_float2(e, l);
+              if (d0 + x == 0) *reinterpret_cast<float2*>(A.part_el + slot * 2) = make_float2(e, sum);
             }
           }
         }
@@ -413,13 +449,14 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
     if (!left_record && tid == 0 && !A.whole) A.record[blockIdx.x] = make_int4(0, 0, -1, 0);
   } else {
     // ------------------------------------------------ copying and unpacking
-    constexpr int kThreads = 32 * kTileConv, kBarrier = 2;
-    const int ct = tid - 32 * kTileSoft;
+    // Two groups of four warps, each a tile: one's copies and barriers pass while the other unpacks.
+    constexpr int kThreads = 32 * kTileConv, kGroup = kThreads / 2, kBarrier = 2;
+    const int ct = tid - 32 * kTileSoft, group = ct / kGroup, gt = ct - group * kGroup;
     const int groups_page = 1 << (A.c.page_shift - 4);  // 16-key groups a page
     const long long v_off = reinterpret_cast<long long>(A.c.v) - reinterpret_cast<long long>(A.c.k);
     unsigned it = 0, parts = 0;
-    bool fail = false, go = true;
-    while (go && line_next(A, line, part)) {
+    bool fail = false;
+    while (line_next(A, line, part)) {
       const int tiles = part.k1 - part.k0, unit0 = first_unit(A, part.n) + part.k0;
       const int32_t* const table = A.flat ? A.pages : A.pages + static_cast<size_t>(part.seq) * A.page_stride;
       const int line0 = (part.pair / A.chunks) << A.c.page_shift;
@@ -443,34 +480,65 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         unsigned* const tops = sh_top[parts & 3];
         if (ct <= NB) tops[ct] = 0u;
         if (group_any(kBarrier, kThreads, fail)) break;
-        unsigned top[1 + NB];
+        __half2 kt = __float2half2_rn(0.0f), vt[NB % 2 ? NB : NB / 2];  // running maxima; V's by block, pairs of them if even
 #pragma unroll
-        for (int b = 0; b <= NB; ++b) top[b] = 0u;
+        for (int b = 0; b < (NB % 2 ? NB : NB / 2); ++b) vt[b] = kt;
         const int pieces = tiles * 4 * 2 * NB;  // 16-byte pieces of K's scales, 2 NB a group
-        for (int x = ct; x < pieces; x += kThreads) {
-          const int gl = x / (2 * NB), piece = x - gl * 2 * NB, gi = unit0 * 4 + gl;
-          const long long page = page_at(gi);
-          if (!page) continue;
-          const uint8_t* const p = reinterpret_cast<const uint8_t*>(page) + A.c.scale_off + row_of(gi) * (2 * NB) + piece * 16;
-          const uint4 k4 = *reinterpret_cast<const uint4*>(p), v4 = *reinterpret_cast<const uint4*>(p + v_off);
-          const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w}, vw[4] = {v4.x, v4.y, v4.z, v4.w};
+        constexpr int kAhead = 4;               // pieces a thread has in flight
+        for (int x0 = ct; x0 < pieces; x0 += kThreads * kAhead) {
+          long long page[kAhead];
+          uint4 k4[kAhead], v4[kAhead];
 #pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            const int flat = piece * 8 + h;
-            if (gi * 16 + flat / NB < part.n) {
-              const unsigned sh = 16 * (h & 1);
-              const unsigned a = __float_as_uint(fabsf(half_bits_to_float(kw[h / 2] >> sh)));
-              const unsigned c = __float_as_uint(fabsf(half_bits_to_float(vw[h / 2] >> sh)));
-              top[0] = max(top[0], a);
+          for (int y = 0; y < kAhead; ++y) {
+            const int x = x0 + y * kThreads;
+            page[y] = x < pieces ? page_at(unit0 * 4 + x / (2 * NB)) : 0;
+          }
 #pragma unroll
-              for (int b = 0; b < NB; ++b)
-                if (b == flat % NB) top[1 + b] = max(top[1 + b], c);
+          for (int y = 0; y < kAhead; ++y) {
+            const int x = x0 + y * kThreads, gl = x / (2 * NB), piece = x - gl * 2 * NB, gi = unit0 * 4 + gl;
+            k4[y] = v4[y] = make_uint4(0u, 0u, 0u, 0u);
+            if (!page[y]) continue;
+            const uint8_t* const p = reinterpret_cast<const uint8_t*>(page[y]) + A.c.scale_off + row_of(gi) * (2 * NB) + piece * 16;
+            k4[y] = *reinterpret_cast<const uint4*>(p);
+            v4[y] = *reinterpret_cast<const uint4*>(p + v_off);
+          }
+#pragma unroll
+          for (int y = 0; y < kAhead; ++y) {
+            const int x = x0 + y * kThreads, gl = x / (2 * NB), piece = x - gl * 2 * NB;
+            uint32_t kw[4] = {k4[y].x, k4[y].y, k4[y].z, k4[y].w}, vw[4] = {v4[y].x, v4[y].y, v4[y].z, v4[y].w};
+            const int left = (part.n - (unit0 * 4 + gl) * 16) * NB - piece * 8;  // scales of the sequence from the piece on
+            if (left < 8) {
+#pragma unroll
+              for (int h = 0; h < 8; ++h)
+                if (h >= left) {
+                  kw[h / 2] &= h & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                  vw[h / 2] &= h & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              kt = __hmax2_nan(kt, __habs2(*reinterpret_cast<const __half2*>(&kw[h])));
+              const __half2 a = __habs2(*reinterpret_cast<const __half2*>(&vw[h]));
+              if (NB % 2 == 0) {
+                vt[h % (NB / 2 > 0 ? NB / 2 : 1)] = __hmax2_nan(vt[h % (NB / 2 > 0 ? NB / 2 : 1)], a);
+              } else {
+#pragma unroll
+                for (int q = 0; q < NB; ++q) {
+                  if ((piece * 8 + 2 * h) % NB == q) vt[q] = __hmax2_nan(vt[q], __half2half2(__low2half(a)));
+                  if ((piece * 8 + 2 * h + 1) % NB == q) vt[q] = __hmax2_nan(vt[q], __half2half2(__high2half(a)));
+                }
+              }
             }
           }
         }
 #pragma unroll
         for (int b = 0; b <= NB; ++b) {
-          const unsigned m = __reduce_max_sync(0xffffffffu, top[b]);
+          // magnitudes order like their bits (an infinity or a NaN above all)
+          const __half2 h = b == 0 ? kt : vt[NB % 2 ? b - 1 : (b - 1) / 2];
+          const float lo = __half2float(__low2half(h)), hi = __half2float(__high2half(h));
+          const unsigned bits = b == 0 || NB % 2 ? max(__float_as_uint(lo), __float_as_uint(hi))
+                                                 : __float_as_uint((b - 1) % 2 ? hi : lo);
+          const unsigned m = __reduce_max_sync(0xffffffffu, bits);
           if (lane == 0) atomicMax(&tops[b], m);
         }
         if (group_any(kBarrier, kThreads, fail)) break;
@@ -481,19 +549,25 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         for (int b = 0; b < NB; ++b) vf[b] = down(tops[1 + b]);
       }
 
-      // ---- raw tiles, two ahead: this thread's chunks of tile i
-      unsigned bads = 0;  // 4 bits a stage
-      auto issue = [&](int i) {
+      // ---- the groups take tiles in turn. Raw tiles come one of its own tiles ahead, page ids one further
+      auto id_at = [&](int i) {
+        const int gi = (unit0 + i) * 4 + (lane & 3);
+        return i < tiles && gi < groups ? table[gi / groups_page] : -1;
+      };
+      int next_id = id_at(group);
+      unsigned miss = 0, next_miss = 0;  // 16-key groups without a valid page: of this tile, of the one on its way
+      auto issue = [&](int i, int stage) {
         if (i < tiles) {
-          const uint32_t to = base + S::kOffRaw + (it + i) % S::kRawStages * S::kRaw;
+          const uint32_t to = base + S::kOffRaw + (2 * group + stage) * S::kRaw;
           const int gi0 = (unit0 + i) * 4;
-          const long long mine = page_at(gi0 + (lane & 3));
-          const unsigned miss = __ballot_sync(0xffffffffu, mine == 0) & 15u;
-          const unsigned st = (it + i) % S::kRawStages * 4;
-          bads = (bads & ~(15u << st)) | (miss << st);
+          const bool there = static_cast<unsigned>(next_id) < static_cast<unsigned>(A.c.n_pages);
+          if (!there && gi0 + (lane & 3) < groups) kv_record(kKvBadPage);
+          const long long mine = there ? reinterpret_cast<long long>(A.c.k) + next_id * A.c.page_bytes : 0;
+          next_id = id_at(i + 2);
+          next_miss = __ballot_sync(0xffffffffu, !there) & 15u;
 #pragma unroll
-          for (int x = 0; x < (kTileKeys * S::kChunks + kThreads - 1) / kThreads; ++x) {
-            const int c = x * kThreads + ct, key = c / S::kChunks, ch = c - key * S::kChunks;
+          for (int x = 0; x < (kTileKeys * S::kChunks + kGroup - 1) / kGroup; ++x) {
+            const int c = x * kGroup + gt, key = c / S::kChunks, ch = c - key * S::kChunks;
             const long long page = __shfl_sync(0xffffffffu, mine, (key >> 4) & 3);
             if (page && key < kTileKeys) {
               const uint8_t* const p =
@@ -503,53 +577,69 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
               cp16(dst + S::kRawCodes, p + v_off);
             }
           }
-          {
-            constexpr int kPieces = 4 * 2 * NB;  // of K's scales; V's follow
-            const int c = ct < kPieces ? ct : ct - kPieces, gl = c / (2 * NB);
-            const long long page = __shfl_sync(0xffffffffu, mine, gl & 3);
-            if (ct < 2 * kPieces && page) {
-              const uint8_t* const p = reinterpret_cast<const uint8_t*>(page) + A.c.scale_off + row_of(gi0 + gl) * (2 * NB) +
-                                       (c - gl * 2 * NB) * 16 + (ct < kPieces ? 0 : v_off);
-              cp16(to + 2 * S::kRawCodes + (ct < kPieces ? 0 : S::kRawScales) + c * 16, p);
-            }
+          constexpr int kPieces = 4 * 2 * NB;  // of K's scales; V's follow
+          const int c = gt < kPieces ? gt : gt - kPieces, gl = c / (2 * NB);
+          const long long page = __shfl_sync(0xffffffffu, mine, gl & 3);
+          if (gt < 2 * kPieces && page) {
+            const uint8_t* const p = reinterpret_cast<const uint8_t*>(page) + A.c.scale_off + row_of(gi0 + gl) * (2 * NB) +
+                                     (c - gl * 2 * NB) * 16 + (gt < kPieces ? 0 : v_off);
+            cp16(to + 2 * S::kRawCodes + (gt < kPieces ? 0 : S::kRawScales) + c * 16, p);
           }
         }
         cp_commit();
       };
-      issue(0);
-      issue(1);
-      for (int i = 0; i < tiles; ++i, ++it) {
-        cp_wait<1>();
-        // every thread's copies of this tile have landed, and the tile before has been unpacked
-        if (group_any(kBarrier, kThreads, fail)) {
-          go = false;
-          break;
-        }
-        {
-          // tile it + 2 (its own index is counted from `it`, which the loop advances)
-          const unsigned keep = it;
-          it -= i;
-          issue(i + 2);
-          it = keep;
-        }
-        const uint8_t* const raw = smem + S::kOffRaw + it % S::kRawStages * S::kRaw;
-        const __half* const kd = reinterpret_cast<const __half*>(raw + 2 * S::kRawCodes);
-        const __half* const vd = kd + S::kRawScales / 2;
-        const unsigned miss = bads >> (it % S::kRawStages * 4) & 15u;
+      static_assert(2 * 4 * 2 * NB <= kGroup, "a thread copies one piece of the scales");
+      uint8_t* const scales = smem + S::kOffScale + group * S::kScales;
+      const unsigned it0 = it;
+      issue(group, 0);
+      for (int i = group, stage = 0; i < tiles; i += 2, stage ^= 1) {
+        it = it0 + i;
+        cp_wait<0>();
+        // every thread's copies of this tile have landed, and the group's last tile has been unpacked
+        if (group_any(kBarrier + 1 + group, kGroup, fail)) break;
+        miss = next_miss;
+        issue(i + 2, stage ^ 1);
+        const uint8_t* const raw = smem + S::kOffRaw + (2 * group + stage) * S::kRaw;
         const int left = part.n - (unit0 + i) * kTileKeys;  // keys of the sequence from the tile's first on
-        auto gone = [&](int key) { return key >= left || (miss >> (key >> 4) & 1); };
+        // ---- scales: scaled, and 0 for keys that are not there (whose codes may be anything)
+        for (int x = gt; x < kTileKeys * NB; x += kGroup) {
+          const int key = x / NB, blk = x - key * NB;
+          const bool gone = key >= left || (miss >> (key >> 4) & 1);
+          const __half* const kd = reinterpret_cast<const __half*>(raw + 2 * S::kRawCodes);
+          float f = vf[0];
+#pragma unroll
+          for (int q = 1; q < NB; ++q) f = blk == q ? vf[q] : f;
+          const float dk = gone ? 0.0f : __half2float(kd[x]) * kf, dv = gone ? 0.0f : __half2float(kd[S::kRawScales / 2 + x]) * f;
+          if (T == 1) {
+            reinterpret_cast<__half*>(scales)[x] = __float2half_rn(dk);
+            reinterpret_cast<__half*>(scales)[kTileKeys * NB + blk * kTileKeys + key] = __float2half_rn(dv);
+          } else {
+            reinterpret_cast<float*>(scales)[x] = dk;
+            reinterpret_cast<float*>(scales)[kTileKeys * NB + blk * kTileKeys + key] = dv;
+          }
+        }
+        group_any(kBarrier + 1 + group, kGroup, false);
         const unsigned b = it % S::kBufs, turn = it / S::kBufs;
         // ---- K: operand rows are keys. A task is a key's 16-byte chunk
+        // With one buffer the groups take turns on it, and a parity tells a phase only from the next: the other group's tile
+        // has to be in before its release can be waited for.
+        if (S::kBufs == 1 && turn > 0) fail |= !wait_sleep(kBarK + b, turn - 1, 10);
         if (turn > 0) fail |= !wait_sleep(kBarKFree + b, turn - 1, 10);
-        if (ct == 0) sh_bad[it & 3] = miss;
+        if (gt == 0) sh_bad[it & 3] = miss;
         uint8_t* const ko = smem + b * T * S::kOperand;
 #pragma unroll
-        for (int x = 0; x < (kTileKeys * S::kChunks + kThreads - 1) / kThreads; ++x) {
-          const int c = x * kThreads + ct, key = c & (kTileKeys - 1), ch = c / kTileKeys;
+        for (int x = 0; x < (kTileKeys * S::kChunks + kGroup - 1) / kGroup; ++x) {
+          const int c = x * kGroup + gt, key = c & (kTileKeys - 1), ch = c / kTileKeys;
           if (ch < S::kChunks) {
             const uint4 u4 = *reinterpret_cast<const uint4*>(raw + chunk_at<S::kChunks>(key, ch));
             const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w};
-            const float d = gone(key) ? 0.0f : __half2float(kd[key * NB + (BITS == 8 ? ch / 2 : ch)]) * kf;
+            const int si = key * NB + (BITS == 8 ? ch / 2 : ch);
+            float d = 0.0f;
+            uint32_t dd = 0u;
+            if (T == 1)
+              dd = reinterpret_cast<const uint16_t*>(scales)[si] * 0x10001u;
+            else
+              d = reinterpret_cast<const float*>(scales)[si];
             uint8_t* const to = ko + (key >> 3) * S::kSbo + (key & 7) * 16;
 #pragma unroll
             for (int z = 0; z < (BITS == 8 ? 2 : 4); ++z) {  // 8 elements each
@@ -560,7 +650,6 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
                 uint32_t h0[2], h1[2];
                 code_halves<BITS>(w0, h0);
                 code_halves<BITS>(w1, h1);
-                const uint32_t dd = half2_of(d, d);
                 *reinterpret_cast<uint4*>(cell) =
                     make_uint4(ptx::hmul2(h0[0], dd), ptx::hmul2(h0[1], dd), ptx::hmul2(h1[0], dd), ptx::hmul2(h1[1], dd));
               } else {
@@ -583,24 +672,39 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(kBarK + b));
         // ---- V: operand rows are elements. A task is a word (4 code bytes) of 8 keys
+        if (S::kBufs == 1 && turn > 0) fail |= !wait_sleep(kBarV + b, turn - 1, 11);
         if (turn > 0) fail |= !wait_sleep(kBarVFree + b, turn - 1, 11);
         uint8_t* const vo = smem + S::kOffV + b * T * S::kOperand;
 #pragma unroll
-        for (int x = 0; x < (8 * S::kWords + kThreads - 1) / kThreads; ++x) {
-          const int c = x * kThreads + ct, kg = c / S::kWords, word = c - kg * S::kWords;
+        for (int x = 0; x < (8 * S::kWords + kGroup - 1) / kGroup; ++x) {
+          const int c = x * kGroup + gt, kg = c / S::kWords, word = c - kg * S::kWords;
           if (kg < 8) {
             const int blk = BITS == 8 ? word / 8 : word / 4;
             uint32_t u[8];
-            float d[8];
-            float f = vf[0];
-#pragma unroll
-            for (int q = 1; q < NB; ++q) f = blk == q ? vf[q] : f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int key = kg * 8 + k;
-              u[k] = *reinterpret_cast<const uint32_t*>(raw + S::kRawCodes + chunk_at<S::kChunks>(key, word / 4) + (word & 3) * 4);
-              d[k] = gone(key) ? 0.0f : __half2float(vd[key * NB + blk]) * f;
+            float d[8];        // T = 3: the 8 keys' scales of the block
+            uint32_t d2[4];    // T = 1: as fp16 pairs
+            if (T == 1) {
+              const uint4 r = *reinterpret_cast<const uint4*>(scales + (kTileKeys * NB + blk * kTileKeys + kg * 8) * 2);
+              d2[0] = r.x;
+              d2[1] = r.y;
+              d2[2] = r.z;
+              d2[3] = r.w;
+            } else {
+              const float4* const r =
+                  reinterpret_cast<const float4*>(scales + (kTileKeys * NB + blk * kTileKeys + kg * 8) * 4);
+              const float4 a = r[0], c4 = r[1];
+              d[0] = a.x;
+              d[1] = a.y;
+              d[2] = a.z;
+              d[3] = a.w;
+              d[4] = c4.x;
+              d[5] = c4.y;
+              d[6] = c4.z;
+              d[7] = c4.w;
             }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              u[k] = *reinterpret_cast<const uint32_t*>(raw + S::kRawCodes + chunk_at<S::kChunks>(kg * 8 + k, word / 4) + (word & 3) * 4);
             // elements 4 word + i; of a 4-bit block 32 blk + 4 (word % 4) + i, and 16 further on those of the high halves
 #pragma unroll
             for (int z = 0; z < (BITS == 8 ? 1 : 2); ++z) {
@@ -614,7 +718,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) {
                   const uint32_t lo = prmt(v[k], v[k + 1], 0x5140u), hi = prmt(v[k], v[k + 1], 0x7362u);
-                  const uint32_t dd = half2_of(d[k], d[k + 1]);
+                  const uint32_t dd = d2[k / 2];
                   uint32_t h0[2], h1[2];
                   code_halves<BITS>(lo, h0);
                   code_halves<BITS>(hi, h1);
@@ -650,9 +754,10 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         if (lane == 0) ptx::mbar_arrive(bar(kBarV + b));
       }
       cp_wait<0>();
+      it = it0 + tiles;
       ++parts;
       // the raw stages are free for the next part once every thread is here
-      if (go) group_any(kBarrier, kThreads, false);
+      if (group_any(kBarrier, kThreads, fail)) break;
     }
     cp_wait<0>();
   }
