@@ -25,8 +25,9 @@ Rows rows_for(const KvAttnArgs& a, int rows) {
 bool tiled(const KvAttnArgs& a, long long rows) { return a.c.dim <= 128 && rows >= kTileMinRows; }
 
 // Rows of partial results (two a CTA): four resident CTAs an SM of 4 or 8
-// rows, three of up to 16; one of 128.
-constexpr size_t kSplitRows = 2 * 4 * kNumSMs * 16, kTileRowsAll = 2 * kNumSMs * kTileRows;
+// rows, three of up to 16; one of 128 or 256.
+constexpr size_t kSplitRows = 2 * 4 * kNumSMs * 16;
+size_t tile_part_rows(bool exact) { return static_cast<size_t>(2) * kNumSMs * tile_rows(exact); }
 constexpr int kMaxCtas = 4 * kNumSMs;
 
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
@@ -37,7 +38,7 @@ struct Layout {
 Layout layout(const KvAttnArgs& a) {
   Layout L;
   const bool tile = tiled(a, a.rows) || (a.prefix_len > 0 && tiled(a, static_cast<long long>(a.batch) * a.rows));
-  const size_t rows = tile ? kTileRowsAll : kSplitRows;
+  const size_t rows = tile ? tile_part_rows(a.type == kF32) : kSplitRows;
   const size_t outs = a.prefix_len > 0 ? static_cast<size_t>(a.batch) * a.n_q * a.q_heads : 0;
   L.record = 0;
   L.part_el = L.record + kMaxCtas * sizeof(int4);
@@ -51,7 +52,7 @@ Layout layout(const KvAttnArgs& a) {
 cudaError_t run(SplitArgs& p, const KvAttnArgs& a, int bits, cudaStream_t s) {
   const bool tile = tiled(a, p.rows);
   const Rows f = rows_for(a, p.rows);
-  const int r = tile ? kTileRows : f.nt * 8 / f.np;
+  const int r = tile ? tile_rows(f.exact) : f.nt * 8 / f.np;
   p.chunks = (p.rows + r - 1) / r;
   const long long keys = p.flat ? p.prefix_len : static_cast<long long>(p.max_pages) << p.c.page_shift;
   const long long units = (keys + kAttnUnit - 1) / kAttnUnit;

@@ -32,7 +32,9 @@
 
 namespace xq {
 
-constexpr int kTileRows = 128;
+constexpr int kTileRows = 128;  // of one accumulator
+// Rows of a pair's chunk: two tiles for 16-bit queries, one for fp32 ones.
+constexpr int tile_rows(bool exact) { return exact ? kTileRows : 2 * kTileRows; }
 constexpr int kTileKeys = 64;
 static_assert(kTileKeys == kAttnUnit, "both kernels cut the line in the same units");
 constexpr int kTileSoft = 8, kTileConv = 8;  // warps
@@ -49,7 +51,10 @@ struct TileShape {
   static constexpr int kSbo = 144;
   static constexpr int kKLbo = kTileKeys / 8 * kSbo, kVLbo = D / 8 * kSbo;
   static constexpr int kOperand = D * kSbo;  // one piece of K or of V: 64 keys x dim
-  static constexpr int kBufs = T == 1 ? 2 : 1;  // of K, V, scores and weights
+  static constexpr int kBufs = T == 1 ? 2 : 1;   // of K and V
+  static constexpr int kTiles = T == 1 ? 2 : 1;  // row tiles
+  static constexpr int kRows = kTiles * kTileRows;
+  static constexpr int kSoftWarps = kTileSoft / kTiles;  // of a row tile
   static constexpr int kRawCodes = kTileKeys * kRow, kRawScales = kTileKeys * NB * 2;
   static constexpr int kRaw = 2 * (kRawCodes + kRawScales);
   static constexpr int kRawStages = 4;  // two of each group of unpacking warps
@@ -59,9 +64,12 @@ struct TileShape {
   static constexpr int kOffScale = kOffRaw + kRawStages * kRaw;
   static constexpr int kScales = 2 * kTileKeys * NB * kScaleBytes;  // a table for each group
   static constexpr int kSmem = kOffScale + 2 * kScales;
-  // Tensor memory columns: queries, scores, weights, outputs.
-  static constexpr int kColS = T * D / 2, kColP = kColS + kBufs * kTileKeys, kColO = kColP + kBufs * T * kTileKeys / 2;
-  static constexpr int kCols = kColO + D;
+  // Tensor memory columns: queries, scores, weights, outputs; of each row tile where there are two. Their weights take the
+  // scores' columns, which the row's thread has read by then.
+  static constexpr int kColS = T == 1 ? kTiles * D / 2 : T * D / 2;
+  static constexpr int kColP = T == 1 ? kColS : kColS + kTileKeys;
+  static constexpr int kColO = T == 1 ? kColS + kTiles * kTileKeys : kColP + T * kTileKeys / 2;
+  static constexpr int kCols = kColO + kTiles * D;
   static constexpr int kAlloc = kCols <= 256 ? 256 : 512;
   static_assert(kCols <= 512 && kSmem <= 227 * 1024, "one CTA fits the SM");
 };
@@ -79,9 +87,8 @@ namespace {
 __device__ unsigned int g_kv_tile_error;  // a wait that ran out
 constexpr long long kTileWait = 1ll << 32;
 
-// Barriers; those of buffers in pairs, one a buffer: two tiles may be complete at a time, and a barrier's parity tells only
-// a phase from the next.
-enum TileBar { kBarQ, kBarDrain, kBarS, kBarP = kBarS + 2, kBarO = kBarP + 2, kBarK = kBarO + 2, kBarKFree = kBarK + 2,
+// Barriers: of each row tile (Q, S, P, O) and of each operand buffer, as a barrier's parity tells a phase only from the next.
+enum TileBar { kBarDrain, kBarQ, kBarS = kBarQ + 2, kBarP = kBarS + 2, kBarO = kBarP + 2, kBarK = kBarO + 2, kBarKFree = kBarK + 2,
                kBarV = kBarKFree + 2, kBarVFree = kBarV + 2, kBars = kBarVFree + 2 };
 
 // Barrier of `threads` threads that gives the or of their predicates.
@@ -150,10 +157,10 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto bar = [&](int i) { return ptx::smem_addr(&bars[i]); };
   if (tid == 0) {
-    ptx::mbar_init(bar(kBarQ), kTileSoft);
     for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(bar(kBarQ + b), S::kSoftWarps);
       ptx::mbar_init(bar(kBarS + b), 1);
-      ptx::mbar_init(bar(kBarP + b), kTileSoft);
+      ptx::mbar_init(bar(kBarP + b), S::kSoftWarps);
       ptx::mbar_init(bar(kBarO + b), 1);
       ptx::mbar_init(bar(kBarK + b), kTileConv / 2);
       ptx::mbar_init(bar(kBarKFree + b), 1);
@@ -189,61 +196,232 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       constexpr int kPairs = T == 3 ? 6 : 1;
       constexpr int pa[6] = {0, 0, 1, 0, 1, 2}, pb[6] = {0, 1, 0, 2, 1, 0};
       bool ok = true;
-      unsigned it = 0, parts = 0;
-      auto scores = [&](unsigned i) {
+      unsigned it = 0, done[2] = {0u, 0u}, parts[2] = {0u, 0u};  // tiles so far; of each row tile
+      // Row tile r's scores of tile i; last: of the part's row tiles.
+      auto scores = [&](int r, unsigned i, bool last) {
         const unsigned b = i % S::kBufs;
-        if (!wait(kBarK + b, i / S::kBufs, 1)) return false;
+        if (r == 0 && !wait(kBarK + b, i / S::kBufs, 1)) return false;
         ptx::tc_fence_after();
 #pragma unroll
         for (int p = 0; p < kPairs; ++p)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            ptx::mma_f16_ts(tmem + S::kColS + b * kTileKeys, tmem + pa[p] * (D / 2) + 8 * k,
+            ptx::mma_f16_ts(tmem + S::kColS + r * kTileKeys, tmem + (r * T + pa[p]) * (D / 2) + 8 * k,
                             ptx::smem_desc(base + (b * T + pb[p]) * S::kOperand + 2 * k * S::kKLbo, S::kKLbo, S::kSbo), idS,
                             p + k > 0);
-        ptx::tc_commit(bar(kBarKFree + b));
-        ptx::tc_commit(bar(kBarS + b));
+        if (last) ptx::tc_commit(bar(kBarKFree + b));
+        ptx::tc_commit(bar(kBarS + r));
         return true;
       };
       while (ok && line_next(A, line, part)) {
         const int tiles = part.k1 - part.k0;
-        ok = wait(kBarQ, parts++, 2);
-        for (int i = 0; i < S::kBufs && i < tiles && ok; ++i) ok = scores(it + i);
+        const int chunk = part.pair % A.chunks;
+        const int last = S::kTiles == 2 && A.rows - chunk * S::kRows > kTileRows ? 1 : 0;
+        for (int r = 0; r <= last && ok; ++r) ok = wait(kBarQ + r, parts[r]++, 2) && scores(r, it, r == last);
         for (int i = 0; i < tiles && ok; ++i, ++it) {
-          const unsigned b = it % S::kBufs, turn = it / S::kBufs;
-          // the tile's weights are there: its scores' buffer is free. With one buffer the next scores come before these
-          // products, or the softmax would wait for both; with two they are a tile ahead anyway
-          ok = wait(kBarP + b, turn, 3);
-          if (S::kBufs == 1 && ok && i + 1 < tiles) ok = scores(it + 1);
-          ok = ok && wait(kBarV + b, turn, 4);
-          if (!ok) break;
-          ptx::tc_fence_after();
+          const unsigned b = it % S::kBufs;
+          for (int r = 0; r <= last && ok; ++r) {
+            ok = wait(kBarP + r, done[r]++, 3);
+            // weights with columns of their own: the next scores come first, or the softmax would wait for both
+            if (T == 3 && ok && i + 1 < tiles) ok = scores(r, it + 1, r == last);
+            if (r == 0) ok = ok && wait(kBarV + b, it / S::kBufs, 4);
+            if (!ok) break;
+            ptx::tc_fence_after();
 #pragma unroll
-          for (int p = 0; p < kPairs; ++p)
+            for (int p = 0; p < kPairs; ++p)
 #pragma unroll
-            for (int k = 0; k < kTileKeys / 16; ++k)
-              ptx::mma_f16_ts(tmem + S::kColO, tmem + S::kColP + (b * T + pa[p]) * (kTileKeys / 2) + 8 * k,
-                              ptx::smem_desc(base + S::kOffV + (b * T + pb[p]) * S::kOperand + 2 * k * S::kVLbo, S::kVLbo, S::kSbo),
-                              idO, i > 0 || p + k > 0);
-          ptx::tc_commit(bar(kBarVFree + b));
-          ptx::tc_commit(bar(kBarO + b));
-          if (S::kBufs > 1 && i + S::kBufs < tiles) ok = scores(it + S::kBufs);
+              for (int k = 0; k < kTileKeys / 16; ++k)
+                ptx::mma_f16_ts(tmem + S::kColO + r * D, tmem + S::kColP + r * kTileKeys + pa[p] * (kTileKeys / 2) + 8 * k,
+                                ptx::smem_desc(base + S::kOffV + (b * T + pb[p]) * S::kOperand + 2 * k * S::kVLbo, S::kVLbo,
+                                               S::kSbo),
+                                idO, i > 0 || p + k > 0);
+            if (r == last) ptx::tc_commit(bar(kBarVFree + b));
+            ptx::tc_commit(bar(kBarO + r));
+            if (T == 1 && i + 1 < tiles) ok = scores(r, it + 1, r == last);
+          }
         }
       }
       ptx::tc_commit(bar(kBarDrain));  // nothing is in flight when tensor memory is freed
       wait(kBarDrain, 0, 5);
     }
-  } else if (warp < kTileSoft) {
-    // -------------------------------------- softmax: row, and which 32 keys
+  } else if (T == 1 && warp < kTileSoft) {
+    // ------------------------- softmax, two row tiles: a thread is a row; no thread needs another
+    constexpr float kTop = 15.0f, kStart = 11.0f;  // log2 of weights: the largest, and where the reference starts anew
+    const int r = warp >> 2, row = r * kTileRows + (warp & 3) * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t ts = tl + S::kColS + r * kTileKeys, to = tl + S::kColO + r * D;
+    unsigned it = 0, done = 0, parts = 0;
+    bool ok = true, left_record = false;
+    for (; ok && line_next(A, line, part); ++parts) {
+      const int head = part.pair / A.chunks, chunk = part.pair - head * A.chunks;
+      const int row0 = chunk * S::kRows, tiles = part.k1 - part.k0;
+      if (row0 + r * kTileRows >= A.rows) {  // not this row tile's
+        it += tiles;
+        continue;
+      }
+      const bool live = row0 + row < A.rows;
+      const size_t at = live ? row_at(A, part.seq, head, row0 + row) : 0;
+      int lim0 = 0, lim1 = 0;
+      if (live) row_range(A, part.seq, part.n, row0 + row, &lim0, &lim1);
+      // ---- the row's query into tensor memory: fp16, its largest element at 2^12 .. 2^13; negated for a negative scale (so
+      // that cs > 0)
+      const uint4* const from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.q) + at * D);
+      const bool f16 = A.type == kF16;
+      auto both = [&](uint32_t w) {
+        return f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w))
+                   : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+      };
+      float top = 0.0f;
+#pragma unroll 8
+      for (int x = 0; x < D / 8; ++x) {
+        const uint4 q = live ? from[x] : make_uint4(0u, 0u, 0u, 0u);
+        const float2 a = both(q.x), b = both(q.y), c = both(q.z), d = both(q.w);
+        top = fmaxf(fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y))),
+                    fmaxf(fmaxf(fabsf(c.x), fabsf(c.y)), fmaxf(fabsf(d.x), fabsf(d.y))));
+      }
+      int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+      ex = ex < -100 ? -100 : ex;
+      const float up = (A.scale < 0.0f ? -1.0f : 1.0f) * __uint_as_float(static_cast<unsigned>(127 + 12 - ex) << 23);
+      float cs = fabsf(A.scale) * 1.4426950408889634f * __uint_as_float(static_cast<unsigned>(127 - 12 + ex) << 23);
+#pragma unroll
+      for (int c = 0; c < D / 2; c += 16) {
+        uint32_t w[16];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint4 q = live ? from[c / 4 + x] : make_uint4(0u, 0u, 0u, 0u);
+          const float2 a = both(q.x), b = both(q.y), g = both(q.z), d = both(q.w);
+          w[4 * x] = half2_of(a.x * up, a.y * up);
+          w[4 * x + 1] = half2_of(b.x * up, b.y * up);
+          w[4 * x + 2] = half2_of(g.x * up, g.y * up);
+          w[4 * x + 3] = half2_of(d.x * up, d.y * up);
+        }
+        ptx::tmem_st16(tl + r * (D / 2) + c, w);
+      }
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(kBarQ + r));
+
+      int key = (first_unit(A, part.n) + part.k0) * kTileKeys;
+      float e = -1e30f;
+      ptx::f2 l = ptx::pk(0.0f, 0.0f);
+      for (int i = 0; i < tiles; ++i, ++it, ++done, key += kTileKeys) {
+        ok = __all_sync(0xffffffffu, wait(kBarS + r, done, 6));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (i == 0) {  // K's power of two, known once its first tile is there
+          const unsigned t0 = sh_top[parts & 3][0];
+          cs = fmaxf(cs * __uint_as_float((t0 >> 23 < 253 ? (t0 >> 23) + 1 : 254u) << 23), 1.17549435e-38f);
+        }
+        const unsigned bad = sh_bad[it & 3];
+        const bool edge = key < lim0 || key + kTileKeys > lim1 || bad;
+        uint32_t sv[2][16];
+        // 32 scores from column c on, those that the row does not see as -infinity
+        auto load = [&](int c) {
+          ptx::tmem_ld16(ts + c, sv[0]);
+          ptx::tmem_ld16(ts + c + 16, sv[1]);
+          ptx::tmem_wait_ld();
+          if (edge) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (key + c + x < lim0 || key + c + x >= lim1 || (bad >> ((c + x) >> 4) & 1)) sv[x >> 4][x & 15] = 0xFF800000u;
+          }
+        };
+        float tops4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // four chains
+        auto largest = [&] {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 8; y += 2)
+              tops4[x] = max3(tops4[x], __uint_as_float(sv[x >> 1][8 * (x & 1) + y]), __uint_as_float(sv[x >> 1][8 * (x & 1) + y + 1]));
+        };
+        load(32);
+        largest();
+        load(0);
+        largest();
+        const float tile_top = fmaxf(fmaxf(tops4[0], tops4[1]), fmaxf(tops4[2], tops4[3])) * cs;
+        if (__any_sync(0xffffffffu, tile_top - e > kTop)) {  // the reference of some rows moves
+          const float next = tile_top - e > kTop ? tile_top - kStart : e, f = ex2(e - next);
+          e = next;
+          l = ptx::mul2(l, ptx::pk(f, f));
+          if (i > 0) {  // these scores' products came after the outputs' last ones
+#pragma unroll
+            for (int c = 0; c < D; c += 16) {
+              uint32_t w[16];
+              ptx::tmem_ld16(to + c, w);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(__uint_as_float(w[x]) * f);
+              ptx::tmem_st16(to + c, w);
+            }
+          }
+        }
+        const ptx::f2 c2 = ptx::pk(cs, cs), e2 = ptx::pk(-e, -e);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h) load(32);
+          uint32_t w[16];
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            const ptx::f2 z =
+                ptx::fma2(ptx::pk(__uint_as_float(sv[x >> 4][x & 15]), __uint_as_float(sv[x >> 4][(x & 15) + 1])), c2, e2);
+            const float a = ex2(ptx::lo32(z)), d = ex2(ptx::hi32(z));
+            l = ptx::add2(l, ptx::pk(a, d));
+            w[x / 2] = half2_of(a, d);
+          }
+          ptx::tmem_st16(ts + 16 * h, w);  // into columns already read
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(kBarP + r));
+      }
+      if (!ok) break;
+      // ---- the part's results
+      ok = __all_sync(0xffffffffu, wait_sleep(kBarO + r, done - 1, 9));
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const float sum = ptx::lo32(l) + ptx::hi32(l);
+      const bool whole = part.k0 == 0 && part.k1 == part.nu;
+      const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (part.k0 == 0 ? 1 : 0)) * S::kRows + row;
+#pragma unroll
+      for (int c = 0; c < D; c += 16) {
+        uint32_t w[16];
+        ptx::tmem_ld16(to + c, w);
+        ptx::tmem_wait_ld();
+        const unsigned t0 = sh_top[parts & 3][1 + c / 32];
+        const float f = __uint_as_float((t0 >> 23 < 253 ? (t0 >> 23) + 1 : 254u) << 23);
+        if (live) {
+#pragma unroll
+          for (int x = 0; x < 16; x += 4) {
+            const float4 y = make_float4(__uint_as_float(w[x]) * f, __uint_as_float(w[x + 1]) * f, __uint_as_float(w[x + 2]) * f,
+                                         __uint_as_float(w[x + 3]) * f);
+            if (whole)
+              finish4(A, D, at, c + x, y, e, sum);
+            else
+              *reinterpret_cast<float4*>(A.part_o + slot * D + c + x) = y;
+          }
+        }
+      }
+      if (live && !whole) *reinterpret_cast<float2*>(A.part_el + slot * 2) = make_float2(e, sum);
+      if (!whole && part.k0 == 0) {
+        left_record = true;
+        if (tid == 0) A.record[blockIdx.x] = make_int4(part.seq, part.pair, line_last(A, line, part), 0);
+      }
+      ptx::tc_fence_before();
+    }
+    if (!left_record && tid == 0 && !A.whole) A.record[blockIdx.x] = make_int4(0, 0, -1, 0);
+  } else if (T == 3 && warp < kTileSoft) {
+    // ------------------------- softmax, one row tile: a row's 64 keys in two threads
     constexpr int kThreads = 32 * kTileSoft, kBarrier = 1;
-    constexpr float kTop = T == 1 ? 15.0f : 40.0f, kStart = T == 1 ? 11.0f : 0.0f;  // log2 of weights: largest, and anew
+    constexpr float kTop = 40.0f, kStart = 0.0f;  // log2 of weights: the largest, and where the reference starts anew
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    unsigned it = 0, parts = 0;
+    unsigned it = 0;
     bool fail = false, go = true, left_record = false;
     while (go && line_next(A, line, part)) {
       const int head = part.pair / A.chunks, chunk = part.pair - head * A.chunks;
-      const int row0 = chunk * kTileRows;
+      const int row0 = chunk * S::kRows;
       const bool live = row0 + row < A.rows;
       const size_t at = live ? row_at(A, part.seq, head, row0 + row) : 0;
       int lim0 = 0, lim1 = 0;
@@ -251,45 +429,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       // ---- this thread's half of the row's query into tensor memory, negated for a negative scale (so that cs > 0)
       float cs = fmaxf(fabsf(A.scale) * 1.4426950408889634f, 1.17549435e-38f);
       const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
-      if (T == 1) {
-        uint4 raw[D / 16];
-        const uint4* const from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.q) + at * D + half * (D / 2));
-        float top = 0.0f;
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x) raw[x] = live ? from[x] : make_uint4(0u, 0u, 0u, 0u);
-        const bool f16 = A.type == kF16;
-        auto both = [&](uint32_t w) {
-          return f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w))
-                     : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-        };
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          const float2 a = both(raw[x].x), b = both(raw[x].y), c = both(raw[x].z), d = both(raw[x].w);
-          top = fmaxf(fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y))),
-                      fmaxf(fmaxf(fabsf(c.x), fabsf(c.y)), fmaxf(fabsf(d.x), fabsf(d.y))));
-        }
-        sh_x[half][row] = top;
-        if (group_any(kBarrier, kThreads, fail)) break;
-        top = fmaxf(top, sh_x[half ^ 1][row]);
-        int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-        ex = ex < -100 ? -100 : ex;
-        const float up = sign * __uint_as_float(static_cast<unsigned>(127 + 12 - ex) << 23);
-        cs = fmaxf(cs * __uint_as_float(static_cast<unsigned>(127 - 12 + ex) << 23), 1.17549435e-38f);
-#pragma unroll
-        for (int c = 0; c < D / 4; c += 8) {
-          uint32_t w[16];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint4 r = raw[c / 4 + x];
-            const float2 a = both(r.x), b = both(r.y), g = both(r.z), d = both(r.w);
-            w[4 * x] = half2_of(a.x * up, a.y * up);
-            w[4 * x + 1] = half2_of(b.x * up, b.y * up);
-            w[4 * x + 2] = half2_of(g.x * up, g.y * up);
-            w[4 * x + 3] = half2_of(d.x * up, d.y * up);
-          }
-          tmem_st8(tl + half * (D / 4) + c, w);
-        }
-      } else {
+      {
 #pragma unroll
         for (int c = 0; c < D / 4; c += 8) {
           uint32_t w[3][16];
@@ -320,16 +460,11 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       float e = -1e30f;
       ptx::f2 l = ptx::pk(0.0f, 0.0f);
       for (int i = 0; i < tiles; ++i, ++it, key += kTileKeys) {
-        const unsigned b = it % S::kBufs, turn = it / S::kBufs;
-        fail |= !wait_sleep(kBarS + b, turn, 6);
+        fail |= !wait_sleep(kBarS, it, 6);
         ptx::tc_fence_after();
-        if (T == 1 && i == 0) {  // K's power of two, known once its first tile is there
-          const unsigned top = sh_top[parts & 3][0];
-          cs = fmaxf(cs * __uint_as_float((top >> 23 < 253 ? (top >> 23) + 1 : 254u) << 23), 1.17549435e-38f);
-        }
         uint32_t sv[2][16];
-        ptx::tmem_ld16(tl + S::kColS + b * kTileKeys + half * 32, sv[0]);
-        ptx::tmem_ld16(tl + S::kColS + b * kTileKeys + half * 32 + 16, sv[1]);
+        ptx::tmem_ld16(tl + S::kColS + half * 32, sv[0]);
+        ptx::tmem_ld16(tl + S::kColS + half * 32 + 16, sv[1]);
         ptx::tmem_wait_ld();
         const unsigned bad = sh_bad[it & 3] >> (2 * half) & 3u;
         if (key < lim0 || key + 32 > lim1 || bad) {
@@ -359,7 +494,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           e = next;
           l = ptx::mul2(l, ptx::pk(f, f));
           if (i > 0) {
-            fail |= !wait(kBarO + (it - 1) % S::kBufs, (it - 1) / S::kBufs, 7);
+            fail |= !wait(kBarO, it - 1, 7);
             ptx::tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D / 2; c += 16) {
@@ -373,61 +508,52 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           }
         }
         // ---- weights
-        uint32_t w[T][16];
+        uint32_t w[3][16];
         const ptx::f2 c2 = ptx::pk(cs, cs), e2 = ptx::pk(-e, -e);
 #pragma unroll
         for (int x = 0; x < 32; x += 2) {
           const ptx::f2 z = ptx::fma2(ptx::pk(__uint_as_float(sv[x >> 4][x & 15]), __uint_as_float(sv[x >> 4][(x & 15) + 1])), c2, e2);
           const float a = ex2(ptx::lo32(z)), d = ex2(ptx::hi32(z));
           l = ptx::add2(l, ptx::pk(a, d));
-          if (T == 1) {
-            w[0][x / 2] = half2_of(a, d);
-          } else {
-            uint32_t u[3];
-            cut3(a, d, u);
-            w[0][x / 2] = u[0];
-            w[T / 2][x / 2] = u[1];
-            w[T - 1][x / 2] = u[2];
-          }
+          uint32_t u[3];
+          cut3(a, d, u);
+          w[0][x / 2] = u[0];
+          w[1][x / 2] = u[1];
+          w[2][x / 2] = u[2];
         }
         // ---- and their operand, whose buffer is free once the products that used it last are done
-        if (i >= S::kBufs) {
-          fail |= !wait(kBarO + b, turn - 1, 8);
+        if (i > 0) {
+          fail |= !wait(kBarO, it - 1, 8);
           ptx::tc_fence_after();
         }
 #pragma unroll
-        for (int p = 0; p < T; ++p) ptx::tmem_st16(tl + S::kColP + (b * T + p) * (kTileKeys / 2) + half * 16, w[p]);
+        for (int p = 0; p < 3; ++p) ptx::tmem_st16(tl + S::kColP + p * (kTileKeys / 2) + half * 16, w[p]);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(kBarP + b));
+        if (lane == 0) ptx::mbar_arrive(bar(kBarP));
       }
       if (!go) break;
       // ---- the part's results
-      fail |= !wait_sleep(kBarO + (it - 1) % S::kBufs, (it - 1) / S::kBufs, 9);
+      fail |= !wait_sleep(kBarO, it - 1, 9);
       ptx::tc_fence_after();
       float sum = ptx::lo32(l) + ptx::hi32(l);
       sh_x[half][row] = sum;
       if (group_any(kBarrier, kThreads, fail)) break;
       sum = half ? sh_x[0][row] + sum : sum + sh_x[1][row];
       const bool whole = part.k0 == 0 && part.k1 == part.nu;
-      const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (part.k0 == 0 ? 1 : 0)) * kTileRows + row;
+      const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (part.k0 == 0 ? 1 : 0)) * S::kRows + row;
 #pragma unroll
       for (int c = 0; c < D / 2; c += 16) {
         uint32_t w[16];
         const int d0 = half * (D / 2) + c;
         ptx::tmem_ld16(tl + S::kColO + d0, w);
         ptx::tmem_wait_ld();
-        float f = 1.0f;
-        if (T == 1) {
-          const unsigned top = sh_top[parts & 3][1 + d0 / 32];
-          f = __uint_as_float((top >> 23 < 253 ? (top >> 23) + 1 : 254u) << 23);
-        }
         if (live) {
 #pragma unroll
           for (int x = 0; x < 16; x += 4) {
-            const float4 y = make_float4(__uint_as_float(w[x]) * f, __uint_as_float(w[x + 1]) * f, __uint_as_float(w[x + 2]) * f,
-                                         __uint_as_float(w[x + 3]) * f);
+            const float4 y = make_float4(__uint_as_float(w[x]), __uint_as_float(w[x + 1]), __uint_as_float(w[x + 2]),
+                                         __uint_as_float(w[x + 3]));
             if (whole) {
               finish4(A, D, at, d0 + x, y, e, sum);
             } else {
@@ -444,7 +570,6 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       ptx::tc_fence_before();
       // the other half's sums have been read when the next barrier is passed
       group_any(kBarrier, kThreads, false);
-      ++parts;
     }
     if (!left_record && tid == 0 && !A.whole) A.record[blockIdx.x] = make_int4(0, 0, -1, 0);
   } else {
@@ -790,10 +915,10 @@ cudaError_t launch_tile_attn(SplitArgs& a, cudaStream_t s) {
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_tile_kernel<BITS, D, T>, a);
   if (e != cudaSuccess || a.whole) return e;
   constexpr int kRowsBlock = 8;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.ctas), kTileRows / kRowsBlock);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.ctas), S::kRows / kRowsBlock);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, kTileRows, kRowsBlock>, a);
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, S::kRows, kRowsBlock>, a);
 }
 
 }  // namespace
