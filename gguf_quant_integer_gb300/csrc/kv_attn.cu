@@ -57,7 +57,7 @@ cudaError_t run(SplitArgs& p, const KvAttnArgs& a, int bits, cudaStream_t s) {
   const long long keys = p.flat ? p.prefix_len : static_cast<long long>(p.max_pages) << p.c.page_shift;
   const long long units = (keys + kAttnUnit - 1) / kAttnUnit;
   // Sequences too short for a second CTA to be worth a join: whole pairs.
-  p.whole = units <= kAttnWhole;
+  p.whole = units <= (p.store ? kAttnWholeOwn : kAttnWhole);
   p.head = tile ? kTileHead : kAttnHead;
   p.units = p.seqs * ((units > 1 ? units : 1) + p.head) * p.c.heads * p.chunks;
   if (tile) {
@@ -100,20 +100,23 @@ cudaError_t launch_kv_attn(const KvAttnArgs& a, int bits, void* workspace, cudaS
   p.pre_el = reinterpret_cast<float*>(ws + L.pre_el);
   p.pre_o = reinterpret_cast<float*>(ws + L.pre_o);
   p.out = a.out;
-  if (a.prefix_len > 0) {  // every row of the call against the prefix, read once
-    p.flat = true;
-    p.seqs = 1;
-    p.rows = a.batch * a.rows;
-    p.pages = a.prefix_pages;
-    const cudaError_t e = run(p, a, bits, s);
-    if (e != cudaSuccess) return e;
-    p.flat = false;
-    p.merge = true;
-  }
   p.seqs = a.batch;
   p.rows = a.rows;
   p.pages = a.pages;
   p.page_stride = a.page_stride;
+  p.store = a.prefix_len > 0;
+  cudaError_t e = run(p, a, bits, s);
+  if (e != cudaSuccess || a.prefix_len == 0) return e;
+  // Then every row of the call against the prefix, which is read once. The
+  // pass may start beside the first one where that leaves no parts (they would
+  // share the workspace).
+  p.store = false;
+  p.merge = true;
+  p.late = p.whole;
+  p.flat = true;
+  p.seqs = 1;
+  p.rows = a.batch * a.rows;
+  p.pages = a.prefix_pages;
   return run(p, a, bits, s);
 }
 

@@ -55,6 +55,9 @@ constexpr int kAttnHead = 5;
 // 0.5 us a unit, the join's launch 4 us (one 97-token sequence, 8 KV heads:
 // 8.5 us cut, 6.6 us whole).
 constexpr int kAttnWhole = 4;
+// The same for the own pages of a call with a prefix, whose pass runs beside
+// the prefix's and then needs no join of its own.
+constexpr int kAttnWholeOwn = 16;
 
 // Kernel arguments. A pair's rows are `tokens` query tokens x group heads;
 // token and head select q's and out's row. Own pages: sequence b has the
@@ -81,12 +84,14 @@ struct SplitArgs {
   float* part_o;    // [2 * ctas][R][dim]
   float* part_el;   // [2 * ctas][R][2]
   int4* record;     // [ctas]: sequence, head * chunks + chunk, last CTA (or -1)
-  // Results: out rows (o / l in the call's type), or, when flat, o and (e, l)
-  // per (token, query head) for the own pages' pass to merge.
+  // Results: out rows (o / l in the call's type). A call with a prefix runs
+  // the own pages first, whose pass stores o and (e, l) of each (token, query
+  // head), and then the prefix, whose pass merges them.
   void* out;
   float* pre_o;
   float* pre_el;
-  bool merge;       // own pages: merge pre_o, pre_el
+  bool store, merge;
+  bool late;  // starts beside the call's first pass: waits for it only where it merges, and at its end
 };
 
 template <int BITS, int D, bool EX, int NP, int NT>
@@ -333,7 +338,7 @@ __device__ __forceinline__ void row_range(const SplitArgs& A, int seq, int n, in
 
 // Row (token, head) `at` of the result: sums o and l relative to 2^e.
 __device__ __forceinline__ void finish4(const SplitArgs& A, int D, size_t at, int d, float4 o, float e, float l) {
-  if (A.flat) {
+  if (A.store) {
     *reinterpret_cast<float4*>(A.pre_o + at * D + d) = o;
     if (d == 0) *reinterpret_cast<float2*>(A.pre_el + at * 2) = make_float2(e, l);
     return;
@@ -349,6 +354,17 @@ __device__ __forceinline__ void finish4(const SplitArgs& A, int D, size_t at, in
   const float4 y = l != 0.0f ? make_float4(__fdiv_rn(o.x, l), __fdiv_rn(o.y, l), __fdiv_rn(o.z, l), __fdiv_rn(o.w, l))
                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   store4(A.out, A.type, at * D + d, y);
+}
+
+// The kernel before: waited for at the start, or (late) where its results are
+// needed and before the last thread ends, as the kernel after this one waits
+// for this one alone. The kernel after may take its place from here on: the
+// join, which waits, or a late pass, which needs nothing of this one yet but
+// that what came before it is done.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_begin(bool late) {
+  if (!late) grid_wait();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // ---- the line of units and this CTA's stretch of it
@@ -483,12 +499,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
   __shared__ float sh_el[kAttnWarps][R][2];
   __shared__ uint32_t sh_at[kAttnWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its place; it waits
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_begin(A.late);
 
   const int cta = blockIdx.x;
   Line line;
-  if (!line_begin<kAttnWarps>(A, sh_line, &line)) return;
+  if (!line_begin<kAttnWarps>(A, sh_line, &line)) {
+    if (A.late) grid_wait();
+    return;
+  }
 
   uint8_t* const stages = smem + warp * S::kWarpBytes;
   const uint32_t stage0 = ptx::smem_addr(stages);
@@ -942,6 +960,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
     if (S::kOverlap && more_parts) begin_part(next);
     __syncthreads();
     const bool whole = k0 == 0 && k1 == nu;
+    if (A.late && whole) grid_wait();
     for (int x = tid * 4; x < rows * D; x += 32 * kAttnWarps * 4) {
       const int r = x / D, d = x - r * D;
       float e = sh_el[0][r][0];
@@ -975,10 +994,12 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
     have = more_parts;
   }
   if (!left_record && tid == 0 && !A.whole) A.record[cta] = make_int4(0, 0, -1, 0);
+  if (A.late) grid_wait();
 }
 
-// The parts of the pair that begins in CTA blockIdx.x, RB of their R rows from RB * blockIdx.y on. A thread holds one float4
-// of the rows; each team of threads takes every kTeams-th part, several loads at a time, then the teams are merged.
+// The parts of the pairs that begin in CTAs blockIdx.x, + gridDim.x, ..., RB of their R rows from RB * blockIdx.y on. A
+// thread holds one float4 of the rows; each team of threads takes every kTeams-th part, several loads at a time, then the
+// teams are merged.
 constexpr int kJoinThreads = 512;
 template <int D, int R, int RB>
 __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ SplitArgs A) {
@@ -988,63 +1009,81 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_cons
   static_assert(kTeams >= 1, "a part's rows are one pass of the block");
   __shared__ float2 sel[kTeams][RB];
   __shared__ float4 so[kTeams][kLanes];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 rec = A.record[blockIdx.x];
-  if (rec.z < 0) return;
-  const int c0 = blockIdx.x, parts = rec.z - c0 + 1, tid = threadIdx.x;
+  grid_wait();
+  const int tid = threadIdx.x, lane = tid & 31;
   const int team = tid / kLanes, at = tid - team * kLanes, r = at / (D / 4), d = (at - r * (D / 4)) * 4;
-  const int head = rec.y / A.chunks, row = RB * blockIdx.y + r, pair_row = (rec.y - head * A.chunks) * R + row;
-  float e = -1e30f, l = 0.0f;
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (team < kTeams && pair_row < A.rows) {
-    for (int base = team; base < parts; base += kTeams * kBatch) {
-      float2 el[kBatch];
-      float4 z[kBatch];
-      float top = e;
+  const int row = RB * blockIdx.y + r;
+  int4 mine = make_int4(0, 0, -1, 0);  // the records, one a lane
+  const int c = blockIdx.x + lane * gridDim.x;
+  if (c < A.ctas) mine = A.record[c];
+  for (unsigned left = __ballot_sync(0xffffffffu, mine.z >= 0); left; left &= left - 1) {
+    const int from = __ffs(left) - 1, c0 = blockIdx.x + from * gridDim.x;
+    const int seq = __shfl_sync(0xffffffffu, mine.x, from), pair = __shfl_sync(0xffffffffu, mine.y, from);
+    const int parts = __shfl_sync(0xffffffffu, mine.z, from) - c0 + 1;
+    const int head = pair / A.chunks, pair_row = (pair - head * A.chunks) * R + row;
+    float e = -1e30f, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const bool live = team < kTeams && pair_row < A.rows;
+    if (live) {
+      for (int base = team; base < parts; base += kTeams * kBatch) {
+        float2 el[kBatch];
+        float4 z[kBatch];
+        float top = e;
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) {
-        const int i = base + x * kTeams;
-        if (i < parts) {
-          // part i: the second slot of the CTA where the pair begins, the first of those after it
-          const size_t slot = (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * R + row;
-          el[x] = *reinterpret_cast<const float2*>(A.part_el + slot * 2);
-          z[x] = *reinterpret_cast<const float4*>(A.part_o + slot * D + d);
+        for (int x = 0; x < kBatch; ++x) {
+          const int i = base + x * kTeams;
+          if (i < parts) {
+            // part i: the second slot of the CTA where the pair begins, the first of those after it
+            const size_t slot = (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * R + row;
+            el[x] = *reinterpret_cast<const float2*>(A.part_el + slot * 2);
+            z[x] = *reinterpret_cast<const float4*>(A.part_o + slot * D + d);
+          }
         }
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x)
+          if (base + x * kTeams < parts) top = fmaxf(top, el[x].x);
+        const float keep = ex2(e - top);
+        o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+        l *= keep;
+        e = top;
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x)
+          if (base + x * kTeams < parts) {
+            const float f = ex2(el[x].x - top);
+            o = make_float4(fmaf(z[x].x, f, o.x), fmaf(z[x].y, f, o.y), fmaf(z[x].z, f, o.z), fmaf(z[x].w, f, o.w));
+            l = fmaf(el[x].y, f, l);
+          }
       }
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x)
-        if (base + x * kTeams < parts) top = fmaxf(top, el[x].x);
-      const float keep = ex2(e - top);
-      o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
-      l *= keep;
-      e = top;
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x)
-        if (base + x * kTeams < parts) {
-          const float f = ex2(el[x].x - top);
-          o = make_float4(fmaf(z[x].x, f, o.x), fmaf(z[x].y, f, o.y), fmaf(z[x].z, f, o.z), fmaf(z[x].w, f, o.w));
-          l = fmaf(el[x].y, f, l);
-        }
+      if (team > 0) so[team][at] = o;
+      if (d == 0) sel[team][r] = make_float2(e, l);
     }
-    if (team > 0) so[team][at] = o;
-    if (d == 0) sel[team][r] = make_float2(e, l);
+    __syncthreads();
+    if (live && team == 0) {
+      const int used = parts < kTeams ? parts : kTeams;
+      const float own = e;
+      for (int w = 1; w < used; ++w) e = fmaxf(e, sel[w][r].x);
+      float f = ex2(own - e);
+      o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+      l *= f;
+      for (int w = 1; w < used; ++w) {
+        const float2 el = sel[w][r];
+        const float4 z = so[w][at];
+        f = ex2(el.x - e);
+        o = make_float4(fmaf(z.x, f, o.x), fmaf(z.y, f, o.y), fmaf(z.z, f, o.z), fmaf(z.w, f, o.w));
+        l = fmaf(el.y, f, l);
+      }
+      finish4(A, D, row_at(A, seq, head, pair_row), d, o, e, l);
+    }
+    __syncthreads();  // the sums have been read
   }
-  __syncthreads();
-  if (team != 0 || pair_row >= A.rows) return;
-  const int used = parts < kTeams ? parts : kTeams;
-  const float mine = e;
-  for (int w = 1; w < used; ++w) e = fmaxf(e, sel[w][r].x);
-  float f = ex2(mine - e);
-  o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-  l *= f;
-  for (int w = 1; w < used; ++w) {
-    const float2 el = sel[w][r];
-    const float4 z = so[w][at];
-    f = ex2(el.x - e);
-    o = make_float4(fmaf(z.x, f, o.x), fmaf(z.y, f, o.y), fmaf(z.z, f, o.z), fmaf(z.w, f, o.w));
-    l = fmaf(el.y, f, l);
-  }
-  finish4(A, D, row_at(A, rec.x, head, pair_row), d, o, e, l);
+}
+
+// Its grid: about as many blocks as run at a time, at most 32 records each.
+template <int R, int RB>
+dim3 join_grid(int ctas) {
+  const int rows = R / RB, want = 4 * kNumSMs / rows, least = (ctas + 31) / 32;
+  const int x = want < least ? least : want < ctas ? want : ctas;
+  return dim3(static_cast<unsigned>(x), static_cast<unsigned>(rows));
 }
 
 template <int BITS, int D, bool EX, int NP, int NT>
@@ -1067,6 +1106,7 @@ cudaError_t launch_split(SplitArgs& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_split_kernel<BITS, D, EX, NP, NT>, a);
   if (e != cudaSuccess || a.whole) return e;
+  cfg.gridDim = join_grid<S::R, S::R>(a.ctas);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, S::R, S::R>, a);

@@ -170,10 +170,12 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
     ptx::mbar_init(bar(kBarDrain), 1);
     ptx::mbar_init_fence();
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join may take its place; it waits
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_begin(A.late);
   Line line;
-  if (!line_begin<kTileWarps>(A, sh_line, &line)) return;
+  if (!line_begin<kTileWarps>(A, sh_line, &line)) {
+    if (A.late) grid_wait();
+    return;
+  }
   if (warp == kTileWarps - 1) ptx::tmem_alloc(ptx::smem_addr(&sh_tmem), S::kAlloc);
   ptx::tc_fence_before();
   __syncthreads();
@@ -383,6 +385,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       ptx::tc_fence_after();
       const float sum = ptx::lo32(l) + ptx::hi32(l);
       const bool whole = part.k0 == 0 && part.k1 == part.nu;
+      if (A.late && whole) grid_wait();
       const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (part.k0 == 0 ? 1 : 0)) * S::kRows + row;
 #pragma unroll
       for (int c = 0; c < D; c += 16) {
@@ -542,6 +545,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       if (group_any(kBarrier, kThreads, fail)) break;
       sum = half ? sh_x[0][row] + sum : sum + sh_x[1][row];
       const bool whole = part.k0 == 0 && part.k1 == part.nu;
+      if (A.late && whole) grid_wait();
       const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (part.k0 == 0 ? 1 : 0)) * S::kRows + row;
 #pragma unroll
       for (int c = 0; c < D / 2; c += 16) {
@@ -893,6 +897,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, S::kAlloc);
   }
+  if (A.late) grid_wait();
 }
 
 template <int BITS, int D, int T>
@@ -914,8 +919,8 @@ cudaError_t launch_tile_attn(SplitArgs& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_tile_kernel<BITS, D, T>, a);
   if (e != cudaSuccess || a.whole) return e;
-  constexpr int kRowsBlock = 8;
-  cfg.gridDim = dim3(static_cast<unsigned>(a.ctas), S::kRows / kRowsBlock);
+  constexpr int kRowsBlock = 4;
+  cfg.gridDim = join_grid<S::kRows, kRowsBlock>(a.ctas);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, S::kRows, kRowsBlock>, a);
