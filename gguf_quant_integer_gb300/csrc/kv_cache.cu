@@ -11,7 +11,7 @@
 #include <climits>
 
 #include "kv_common.cuh"
-#include "xq_ptx.cuh"
+#include "xq_common.cuh"
 
 namespace xq {
 namespace {
@@ -93,6 +93,67 @@ __device__ __forceinline__ int quant(float x, float d, float low, float top) {
   return static_cast<int>(fminf(fmaxf(y, low), top));
 }
 
+// The larger magnitude (a NaN if there is one).
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(fabsf(b)));
+  return m;
+}
+
+// The codes of N values, a byte each (q + 128, or q + 8 for BITS = 4), by
+// x * (1 / d), within 2^-16 of x / d: adding 1.5 * 2^23 + offset leaves the
+// nearest whole number in the low bits. What is left is which side of a half
+// the quotient is on.
+//   16-bit inputs, whose quotients by an 11-bit d often are exact halves and
+//     otherwise differ from one by 2^-12 at least: the remainder x - n d is
+//     exact, and is compared with d / 2.
+//   fp32 inputs, whose quotient's own rounding counts: a piece with a product
+//     within 1e-4 of a half (and one with a NaN) is divided out, about one warp
+//     in forty.
+// 8 to 13 instructions a value where a division takes 25.
+template <int BITS, int N>
+__device__ __forceinline__ void codes_of(const float (&f)[N], float d, uint32_t (&code)[N / 4]) {
+  constexpr float low = BITS == 8 ? -127.0f : -8.0f, top = BITS == 8 ? 127.0f : 7.0f;
+  constexpr float shift = 12582912.0f + (BITS == 8 ? 128.0f : 8.0f);
+  constexpr uint32_t zeros = BITS == 8 ? 0x80808080u : 0x08080808u;
+  if (!(fabsf(d) <= 65504.0f) || d == 0.0f) {  // finite / infinite, and what is not a number: 0
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) code[i] = zeros;
+    return;
+  }
+  const float inv = __frcp_rn(d), half = 0.5f * fabsf(d);
+  float off = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    uint32_t b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float x = f[4 * i + k], y = fminf(fmaxf(x * inv, low), top);
+      float z = __fadd_rn(y, shift);
+      const float n = __fadd_rn(z, -shift);
+      if (N == 8) {
+        const float r = fmaf(-n, d, x);
+        // r on x's side: n is too near zero at a half or more; on the other: too far beyond a half
+        const bool near = (__float_as_int(r) ^ __float_as_int(x)) >= 0;
+        const float step = copysignf(1.0f, y);
+        z = near ? (fabsf(r) >= half ? z + step : z) : (fabsf(r) > half ? z - step : z);
+        z = fminf(fmaxf(z, low + shift), top + shift);
+      } else {
+        off = max_abs(off, __fadd_rn(y, -n));
+      }
+      b[k] = __float_as_uint(z);
+    }
+    code[i] = prmt(prmt(b[0], b[1], 0x0040u), prmt(b[2], b[3], 0x0040u), 0x5410u);
+  }
+  if (N == 4 && !(off < 0.4999f)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const unsigned q = quant(f[i], d, low, top) + (BITS == 8 ? 128 : 8);
+      code[i / 4] = (i & 3) ? (code[i / 4] | (q << (8 * (i & 3)))) : q;
+    }
+  }
+}
+
 // The block of N values in each of 32 / N neighbouring lanes: scale, and this
 // lane's codes as stored. Q4_0: lanes of the block's first half return the
 // bytes of elements (own, own + 16), the others nothing of use.
@@ -101,12 +162,12 @@ __device__ __forceinline__ float quantize_piece(const float (&f)[N], int lane, u
   constexpr int G = 32 / N;
   __half dh;
   if (BITS == 8) {
-    unsigned top = 0;  // |x| >= 0, so its bit pattern orders like the value (a NaN above all)
+    float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(fabsf(f[i])));
+    for (int i = 0; i < N; ++i) top = max_abs(top, f[i]);
 #pragma unroll
-    for (int o = 1; o < G; o *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    dh = __float2half_rn(__fdiv_rn(__uint_as_float(top), 127.0f));
+    for (int o = 1; o < G; o *= 2) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, o));
+    dh = __float2half_rn(__fdiv_rn(top, 127.0f));
   } else {
     float m = f[0];
 #pragma unroll
@@ -122,18 +183,8 @@ __device__ __forceinline__ float quantize_piece(const float (&f)[N], int lane, u
     dh = __float2half_rn(m * -0.125f);
   }
   const float d = __half2float(dh);
-  if (BITS == 8) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const unsigned q = d != 0.0f ? quant(f[i], d, -127.0f, 127.0f) + 128 : 128;
-      code[i / 4] = (i & 3) ? (code[i / 4] | (q << (8 * (i & 3)))) : q;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const unsigned q = d != 0.0f ? quant(f[i], d, -8.0f, 7.0f) + 8 : 8;
-      code[i / 4] = (i & 3) ? (code[i / 4] | (q << (8 * (i & 3)))) : q;
-    }
+  codes_of<BITS, N>(f, d, code);
+  if (BITS == 4) {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) code[i] |= __shfl_xor_sync(0xffffffffu, code[i], G / 2) << 4;
   }
@@ -150,20 +201,13 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constan
   const bool live = u < A.units;
   const unsigned t = live ? u / A.row_blocks : 0, hb = live ? u - t * A.row_blocks : 0;
   const long long slot = A.slots[t];
+  float f[2][N];  // loaded beside the slot, whatever it turns out to be
+#pragma unroll
+  for (int z = 0; z < 2; ++z)
+    load_piece<X, N>(static_cast<const X*>(A.x[z]) + static_cast<long long>(t) * A.stride[z] + hb * 32 + piece * N, A.wide, f[z]);
   long long page;
   int row;
-  const bool ok = live && slot_row(A.c, slot, &page, &row);
-  float f[2][N];
-#pragma unroll
-  for (int z = 0; z < 2; ++z) {
-    if (ok) {
-      load_piece<X, N>(static_cast<const X*>(A.x[z]) + static_cast<long long>(t) * A.stride[z] + hb * 32 + piece * N, A.wide,
-                       f[z]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) f[z][i] = 0.0f;
-    }
-  }
+  const bool ok = slot_row(A.c, slot, &page, &row) && live;
   const int nb = A.c.dim / 32;
   const unsigned h = hb / nb, b = hb - h * nb;
 #pragma unroll
@@ -244,21 +288,17 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
 #pragma unroll
   for (int z = 0; z < 2; ++z) {
     Y* to = static_cast<Y*>(A.y[z]) + static_cast<size_t>(u) * 32 + piece * N;
-    float f[N];
-    if (BITS == 8) {
+    constexpr float off = BITS == 8 ? 8388736.0f : 8388616.0f;  // 2^23 + 128, 2^23 + 8
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        f[i] = ok ? __fmul_rn(d[z], static_cast<float>(static_cast<int>((code[z][i / 4] >> (8 * (i & 3))) & 255u) - 128)) : 0.0f;
-      store_piece<Y, N>(to, f);
-    } else {
+    for (int half = 0; half < (BITS == 8 ? 1 : 2); ++half) {
+      float f[N];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          f[i] = ok ? __fmul_rn(d[z], static_cast<float>(static_cast<int>((code[z][i / 4] >> (8 * (i & 3) + 4 * half)) & 15u) - 8))
-                    : 0.0f;
-        store_piece<Y, N>(to + 16 * half, f);
+      for (int i = 0; i < N; ++i) {
+        // a byte u as the float 2^23 + u; int-to-float conversions would keep the slow pipe busy
+        const uint32_t w = BITS == 8 ? code[z][i / 4] : (code[z][i / 4] >> (4 * half)) & 0x0F0F0F0Fu;
+        f[i] = ok ? __fmul_rn(d[z], __fadd_rn(__uint_as_float(prmt(w, 0x4B000000u, 0x7440u + (i & 3))), -off)) : 0.0f;
       }
+      store_piece<Y, N>(to + 16 * half, f);
     }
   }
 }
