@@ -20,22 +20,39 @@ __device__ unsigned int g_kv_cache_error;
 
 constexpr int kThreads = 256;
 
-struct WriteArgs {
+// A token's row of K (and of V) is row_blocks blocks of 32 in heads order; a
+// warp takes `span` pieces of it, each as many blocks as it has lane groups.
+struct RowArgs {
   KvView c;
+  const int64_t* slots;
+  unsigned warps;         // in this launch
+  unsigned warps_row;     // a token's
+  unsigned span;          // pieces of a row a warp
+  unsigned row_blocks;    // heads * dim / 32
+};
+struct WriteArgs {
+  RowArgs r;
   const void* x[2];       // K and V rows
   long long stride[2];    // elements between tokens
-  const int64_t* slots;
-  unsigned units;         // blocks of K (and of V) in this launch
-  unsigned row_blocks;    // heads * dim / 32
   bool wide;              // every 16-byte piece of x is 16-byte aligned
 };
-
 struct ReadArgs {
-  KvView c;
+  RowArgs r;
   void* y[2];
-  const int64_t* slots;
-  unsigned units;
-  unsigned row_blocks;
+};
+
+// This thread's blocks: the first, and the step to the next (blocks a piece).
+struct BlockAt {
+  unsigned hb, h, b;      // of the row; head and block of the head
+  __device__ __forceinline__ BlockAt(unsigned first, unsigned nb) : hb(first), h(first / nb), b(first - first / nb * nb) {}
+  __device__ __forceinline__ void step(unsigned by, unsigned nb) {
+    hb += by;
+    b += by;
+    while (b >= nb) {
+      b -= nb;
+      ++h;
+    }
+  }
 };
 
 template <typename X>
@@ -193,40 +210,52 @@ __device__ __forceinline__ float quantize_piece(const float (&f)[N], int lane, u
 
 template <int BITS, typename X>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const __grid_constant__ WriteArgs A) {
-  constexpr int N = 16 / sizeof(X), G = 32 / N;
+  constexpr int N = 16 / sizeof(X), G = 32 / N, kBlocks = 32 / G;  // blocks of a warp's piece
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const unsigned at = blockIdx.x * kThreads + threadIdx.x;
-  const unsigned u = at / G;  // block of 32; the lanes of a warp stay together for the shuffles
-  const int piece = static_cast<int>(at % G), lane = static_cast<int>(threadIdx.x & 31);
-  const bool live = u < A.units;
-  const unsigned t = live ? u / A.row_blocks : 0, hb = live ? u - t * A.row_blocks : 0;
-  const long long slot = A.slots[t];
-  float f[2][N];  // loaded beside the slot, whatever it turns out to be
+  const unsigned w = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  const int lane = static_cast<int>(threadIdx.x & 31), piece = lane % G;
+  if (w >= A.r.warps) return;
+  const unsigned t = w / A.r.warps_row, first = (w - t * A.r.warps_row) * A.r.span * kBlocks;
+  const unsigned nb = A.r.c.dim / 32, end = min(first + A.r.span * kBlocks, A.r.row_blocks);
+  BlockAt at(first + lane / G, nb);
+  const X* x[2];
+  float f[2][N];
+  auto load = [&](unsigned hb) {
 #pragma unroll
-  for (int z = 0; z < 2; ++z)
-    load_piece<X, N>(static_cast<const X*>(A.x[z]) + static_cast<long long>(t) * A.stride[z] + hb * 32 + piece * N, A.wide, f[z]);
+    for (int z = 0; z < 2; ++z) load_piece<X, N>(x[z] + hb * 32, A.wide, f[z]);
+  };
+#pragma unroll
+  for (int z = 0; z < 2; ++z) x[z] = static_cast<const X*>(A.x[z]) + static_cast<long long>(t) * A.stride[z] + piece * N;
+  load(at.hb < end ? at.hb : first);  // beside the slot, whatever it turns out to be
   long long page;
   int row;
-  const bool ok = slot_row(A.c, slot, &page, &row) && live;
-  const int nb = A.c.dim / 32;
-  const unsigned h = hb / nb, b = hb - h * nb;
+  if (!slot_row(A.r.c, A.r.slots[t], &page, &row)) return;
+  uint8_t* const base = A.r.c.k + page * A.r.c.page_bytes;
+  const long long v_off = A.r.c.v - A.r.c.k;
+  for (unsigned from = first; from < end; from += kBlocks) {
+    const bool live = at.hb < end;
+    const long long line = (static_cast<long long>(at.h) << A.r.c.page_shift) + row;
+    const unsigned b = at.b;
+    uint32_t code[2][N / 4];
+    float d[2];
 #pragma unroll
-  for (int z = 0; z < 2; ++z) {
-    uint32_t code[N / 4];
-    const float d = quantize_piece<BITS, N>(f[z], lane, code);
-    if (!ok) continue;
-    uint8_t* base = (z ? A.c.v : A.c.k) + page * A.c.page_bytes;
-    const long long line = (static_cast<long long>(h) << A.c.page_shift) + row;
-    if (!XQ_IN(line, static_cast<long long>(A.c.heads) << A.c.page_shift, kChkKvRow)) continue;
-    // Q8_0: every lane N bytes; Q4_0: the lanes of the first half N bytes (two elements each)
-    if (BITS == 8 || piece < G / 2) {
-      uint8_t* to = base + line * A.c.row_bytes + b * (4 * BITS) + piece * N;
-      if (N == 8)
-        *reinterpret_cast<uint2*>(to) = make_uint2(code[0], code[N / 4 - 1]);
-      else
-        *reinterpret_cast<uint32_t*>(to) = code[0];
+    for (int z = 0; z < 2; ++z) d[z] = quantize_piece<BITS, N>(f[z], lane, code[z]);
+    at.step(kBlocks, nb);
+    if (from + kBlocks < end) load(at.hb < end ? at.hb : first);
+    if (!live || !XQ_IN(line, static_cast<long long>(A.r.c.heads) << A.r.c.page_shift, kChkKvRow)) continue;
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      uint8_t* const pool = z ? base + v_off : base;
+      // Q8_0: every lane N bytes; Q4_0: the lanes of the first half N bytes (two elements each)
+      if (BITS == 8 || piece < G / 2) {
+        uint8_t* to = pool + line * A.r.c.row_bytes + b * (4 * BITS) + piece * N;
+        if (N == 8)
+          *reinterpret_cast<uint2*>(to) = make_uint2(code[z][0], code[z][N / 4 - 1]);
+        else
+          *reinterpret_cast<uint32_t*>(to) = code[z][0];
+      }
+      if (piece == 0) *reinterpret_cast<__half*>(pool + A.r.c.scale_off + (line * nb + b) * 2) = __float2half_rn(d[z]);
     }
-    if (piece == 0) *reinterpret_cast<__half*>(base + A.c.scale_off + (line * nb + b) * 2) = __float2half_rn(d);
   }
 }
 
@@ -253,60 +282,85 @@ __device__ __forceinline__ void store_piece(Y* p, const float (&f)[N]) {
 // N low and N high halves (elements j and j + 16) of a Q4_0 block.
 template <int BITS, typename Y>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ ReadArgs A) {
-  constexpr int N = 16 / sizeof(Y), G = 4 * BITS / N;
+  constexpr int N = 16 / sizeof(Y), G = 4 * BITS / N, kBlocks = 32 / G;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const unsigned at = blockIdx.x * kThreads + threadIdx.x;
-  const unsigned u = at / G;
-  const int piece = static_cast<int>(at % G);
-  if (u >= A.units) return;
-  const unsigned t = u / A.row_blocks, hb = u - t * A.row_blocks;
-  const int nb = A.c.dim / 32;
-  const unsigned h = hb / nb, b = hb - h * nb;
+  const unsigned w = blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  const int lane = static_cast<int>(threadIdx.x & 31), piece = lane % G;
+  if (w >= A.r.warps) return;
+  const unsigned t = w / A.r.warps_row, first = (w - t * A.r.warps_row) * A.r.span * kBlocks;
+  const unsigned nb = A.r.c.dim / 32, end = min(first + A.r.span * kBlocks, A.r.row_blocks);
+  BlockAt at(first + lane / G, nb);
   long long page;
   int row;
-  const bool ok = slot_row(A.c, A.slots[t], &page, &row);
-  uint32_t code[2][N / 4];
-  float d[2];
+  const bool ok = slot_row(A.r.c, A.r.slots[t], &page, &row);
+  const uint8_t* const base = A.r.c.k + page * A.r.c.page_bytes;
+  const long long v_off = A.r.c.v - A.r.c.k;
+  constexpr int kAhead = 2;  // pieces a thread has in flight
+  for (unsigned from = first; from < end; from += kAhead * kBlocks) {
+    uint32_t code[kAhead][2][N / 4];
+    float d[kAhead][2];
+    unsigned hb[kAhead];
 #pragma unroll
-  for (int z = 0; z < 2; ++z) {
-    d[z] = 0.0f;
-    code[z][0] = code[z][N / 4 - 1] = 0u;
-    if (!ok) continue;
-    const uint8_t* base = (z ? A.c.v : A.c.k) + page * A.c.page_bytes;
-    const long long line = (static_cast<long long>(h) << A.c.page_shift) + row;
-    if (!XQ_IN(line, static_cast<long long>(A.c.heads) << A.c.page_shift, kChkKvRow)) continue;
-    const uint8_t* from = base + line * A.c.row_bytes + b * (4 * BITS) + piece * N;
-    if (N == 8) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(from));
-      code[z][0] = w.x;
-      code[z][N / 4 - 1] = w.y;
-    } else {
-      code[z][0] = __ldg(reinterpret_cast<const uint32_t*>(from));
-    }
-    d[z] = __half2float(__ushort_as_half(__ldg(reinterpret_cast<const unsigned short*>(base + A.c.scale_off + (line * nb + b) * 2))));
-  }
+    for (int p = 0; p < kAhead; ++p) {
+      hb[p] = at.hb;
+      const long long line = (static_cast<long long>(at.h) << A.r.c.page_shift) + row;
+      const bool there = ok && at.hb < end && XQ_IN(line, static_cast<long long>(A.r.c.heads) << A.r.c.page_shift, kChkKvRow);
 #pragma unroll
-  for (int z = 0; z < 2; ++z) {
-    Y* to = static_cast<Y*>(A.y[z]) + static_cast<size_t>(u) * 32 + piece * N;
-    constexpr float off = BITS == 8 ? 8388736.0f : 8388616.0f;  // 2^23 + 128, 2^23 + 8
-#pragma unroll
-    for (int half = 0; half < (BITS == 8 ? 1 : 2); ++half) {
-      float f[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        // a byte u as the float 2^23 + u; int-to-float conversions would keep the slow pipe busy
-        const uint32_t w = BITS == 8 ? code[z][i / 4] : (code[z][i / 4] >> (4 * half)) & 0x0F0F0F0Fu;
-        f[i] = ok ? __fmul_rn(d[z], __fadd_rn(__uint_as_float(prmt(w, 0x4B000000u, 0x7440u + (i & 3))), -off)) : 0.0f;
+      for (int z = 0; z < 2; ++z) {
+        d[p][z] = 0.0f;
+        code[p][z][0] = code[p][z][N / 4 - 1] = 0u;
+        if (!there) continue;
+        const uint8_t* const pool = z ? base + v_off : base;
+        const uint8_t* const src = pool + line * A.r.c.row_bytes + at.b * (4 * BITS) + piece * N;
+        if (N == 8) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(src));
+          code[p][z][0] = v.x;
+          code[p][z][N / 4 - 1] = v.y;
+        } else {
+          code[p][z][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+        }
+        d[p][z] = __half2float(
+            __ushort_as_half(__ldg(reinterpret_cast<const unsigned short*>(pool + A.r.c.scale_off + (line * nb + at.b) * 2))));
       }
-      store_piece<Y, N>(to + 16 * half, f);
+      at.step(kBlocks, nb);
+    }
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p) {
+      if (hb[p] >= end) continue;
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        Y* const to = static_cast<Y*>(A.y[z]) + (static_cast<size_t>(t) * A.r.row_blocks + hb[p]) * 32 + piece * N;
+        constexpr float off = BITS == 8 ? 8388736.0f : 8388616.0f;  // 2^23 + 128, 2^23 + 8
+#pragma unroll
+        for (int half = 0; half < (BITS == 8 ? 1 : 2); ++half) {
+          float f[N];
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            // a byte u as the float 2^23 + u; int-to-float conversions would keep the slow pipe busy
+            const uint32_t v = BITS == 8 ? code[p][z][i / 4] : (code[p][z][i / 4] >> (4 * half)) & 0x0F0F0F0Fu;
+            f[i] = ok ? __fmul_rn(d[p][z], __fadd_rn(__uint_as_float(prmt(v, 0x4B000000u, 0x7440u + (i & 3))), -off)) : 0.0f;
+          }
+          store_piece<Y, N>(to + 16 * half, f);
+        }
+      }
     }
   }
 }
 
 template <typename K, typename Args>
-cudaError_t launch(K kernel, const Args& A, int lanes, cudaStream_t s) {
+cudaError_t launch(K kernel, Args& A, long long tokens, int lanes, cudaStream_t s) {
+  const unsigned blocks = 32 / lanes, pieces = (A.r.row_blocks + blocks - 1) / blocks;
+  // Few tokens: a warp a piece, for the least latency. Many: a warp up to 8
+  // pieces of a row, which share the slot's and the addresses' arithmetic
+  // (fp32 write of 16383 tokens: 40 us with one piece, 29 us with 8).
+  const long long most = 64LL * kNumSMs;
+  unsigned span = tokens * pieces > 2 * most ? 8 : tokens * pieces > most ? 2 : 1;
+  span = span < pieces ? span : pieces;
+  A.r.span = span;
+  A.r.warps_row = (pieces + span - 1) / span;
+  A.r.warps = static_cast<unsigned>(tokens) * A.r.warps_row;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((A.units + kThreads / lanes - 1) / (kThreads / lanes));
+  cfg.gridDim = dim3((A.r.warps + kThreads / 32 - 1) / (kThreads / 32));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -317,7 +371,7 @@ cudaError_t launch(K kernel, const Args& A, int lanes, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, A);
 }
 
-// Tokens per launch: thread indices stay within 31 bits.
+// Tokens per launch: warp indices stay within 31 bits.
 int tokens_per_launch(const KvView& c) {
   const long long most = (1LL << 27) / (static_cast<long long>(c.heads) * (c.dim / 32));
   return most < 1 ? 1 : most > INT_MAX ? INT_MAX : static_cast<int>(most);
@@ -329,25 +383,24 @@ cudaError_t launch_kv_write(const KvView& c, int bits, int x_type, const void* k
                             long long v_stride, const int64_t* slots, int n_tokens, cudaStream_t s) {
   const int eb = kv_elt_bytes(x_type), step = tokens_per_launch(c);
   WriteArgs A;
-  A.c = c;
+  A.r.c = c;
   A.stride[0] = k_stride;
   A.stride[1] = v_stride;
-  A.row_blocks = static_cast<unsigned>(c.heads) * (c.dim / 32);
+  A.r.row_blocks = static_cast<unsigned>(c.heads) * (c.dim / 32);
   A.wide = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v) | static_cast<uintptr_t>(k_stride * eb) |
              static_cast<uintptr_t>(v_stride * eb)) & 15u) == 0;
   for (long long t0 = 0; t0 < n_tokens; t0 += step) {
     const long long n = n_tokens - t0 < step ? n_tokens - t0 : step;
     A.x[0] = static_cast<const char*>(k) + t0 * k_stride * eb;
     A.x[1] = static_cast<const char*>(v) + t0 * v_stride * eb;
-    A.slots = slots + t0;
-    A.units = static_cast<unsigned>(n) * A.row_blocks;
+    A.r.slots = slots + t0;
     cudaError_t e;
     if (x_type == kF32)
-      e = bits == 8 ? launch(kv_write_kernel<8, float>, A, 8, s) : launch(kv_write_kernel<4, float>, A, 8, s);
+      e = bits == 8 ? launch(kv_write_kernel<8, float>, A, n, 8, s) : launch(kv_write_kernel<4, float>, A, n, 8, s);
     else if (x_type == kF16)
-      e = bits == 8 ? launch(kv_write_kernel<8, __half>, A, 4, s) : launch(kv_write_kernel<4, __half>, A, 4, s);
+      e = bits == 8 ? launch(kv_write_kernel<8, __half>, A, n, 4, s) : launch(kv_write_kernel<4, __half>, A, n, 4, s);
     else
-      e = bits == 8 ? launch(kv_write_kernel<8, __nv_bfloat16>, A, 4, s) : launch(kv_write_kernel<4, __nv_bfloat16>, A, 4, s);
+      e = bits == 8 ? launch(kv_write_kernel<8, __nv_bfloat16>, A, n, 4, s) : launch(kv_write_kernel<4, __nv_bfloat16>, A, n, 4, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -358,21 +411,20 @@ cudaError_t launch_kv_read(const KvView& c, int bits, const int64_t* slots, int 
   const int eb = kv_elt_bytes(y_type), step = tokens_per_launch(c);
   const long long row = static_cast<long long>(c.heads) * c.dim * eb;
   ReadArgs A;
-  A.c = c;
-  A.row_blocks = static_cast<unsigned>(c.heads) * (c.dim / 32);
+  A.r.c = c;
+  A.r.row_blocks = static_cast<unsigned>(c.heads) * (c.dim / 32);
   for (long long t0 = 0; t0 < n_tokens; t0 += step) {
     const long long n = n_tokens - t0 < step ? n_tokens - t0 : step;
     A.y[0] = static_cast<char*>(k) + t0 * row;
     A.y[1] = static_cast<char*>(v) + t0 * row;
-    A.slots = slots + t0;
-    A.units = static_cast<unsigned>(n) * A.row_blocks;
+    A.r.slots = slots + t0;
     cudaError_t e;  // code bytes a thread: 4 for fp32, 8 for 16-bit values
     if (y_type == kF32)
-      e = bits == 8 ? launch(kv_read_kernel<8, float>, A, 8, s) : launch(kv_read_kernel<4, float>, A, 4, s);
+      e = bits == 8 ? launch(kv_read_kernel<8, float>, A, n, 8, s) : launch(kv_read_kernel<4, float>, A, n, 4, s);
     else if (y_type == kF16)
-      e = bits == 8 ? launch(kv_read_kernel<8, __half>, A, 4, s) : launch(kv_read_kernel<4, __half>, A, 2, s);
+      e = bits == 8 ? launch(kv_read_kernel<8, __half>, A, n, 4, s) : launch(kv_read_kernel<4, __half>, A, n, 2, s);
     else
-      e = bits == 8 ? launch(kv_read_kernel<8, __nv_bfloat16>, A, 4, s) : launch(kv_read_kernel<4, __nv_bfloat16>, A, 2, s);
+      e = bits == 8 ? launch(kv_read_kernel<8, __nv_bfloat16>, A, n, 4, s) : launch(kv_read_kernel<4, __nv_bfloat16>, A, n, 2, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
