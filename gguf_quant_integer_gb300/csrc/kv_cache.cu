@@ -121,12 +121,11 @@ __device__ __forceinline__ float max_abs(float a, float b) {
 // x * (1 / d), within 2^-16 of x / d: adding 1.5 * 2^23 + offset leaves the
 // nearest whole number in the low bits. What is left is which side of a half
 // the quotient is on.
-//   16-bit inputs, whose quotients by an 11-bit d often are exact halves and
-//     otherwise differ from one by 2^-12 at least: the remainder x - n d is
+//   16-bit inputs to Q4_0, where d = x' / 8 makes many quotients exact halves
+//     (others differ from one by 2^-12 at least): the remainder x - n d is
 //     exact, and is compared with d / 2.
-//   fp32 inputs, whose quotient's own rounding counts: a piece with a product
-//     within 1e-4 of a half (and one with a NaN) is divided out, about one warp
-//     in forty.
+//   Else a piece with a product within 1e-4 of a half is divided out, about one
+//     warp in forty.
 // 8 to 13 instructions a value where a division takes 25.
 template <int BITS, int N>
 __device__ __forceinline__ void codes_of(const float (&f)[N], float d, uint32_t (&code)[N / 4]) {
@@ -148,7 +147,7 @@ __device__ __forceinline__ void codes_of(const float (&f)[N], float d, uint32_t 
       const float x = f[4 * i + k], y = fminf(fmaxf(x * inv, low), top);
       float z = __fadd_rn(y, shift);
       const float n = __fadd_rn(z, -shift);
-      if (N == 8) {
+      if (N == 8 && BITS == 4) {
         const float r = fmaf(-n, d, x);
         // r on x's side: n is too near zero at a half or more; on the other: too far beyond a half
         const bool near = (__float_as_int(r) ^ __float_as_int(x)) >= 0;
@@ -162,7 +161,7 @@ __device__ __forceinline__ void codes_of(const float (&f)[N], float d, uint32_t 
     }
     code[i] = prmt(prmt(b[0], b[1], 0x0040u), prmt(b[2], b[3], 0x0040u), 0x5410u);
   }
-  if (N == 4 && !(off < 0.4999f)) {
+  if (!(off < 0.4999f)) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const unsigned q = quant(f[i], d, low, top) + (BITS == 8 ? 128 : 8);

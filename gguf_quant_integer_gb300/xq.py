@@ -464,15 +464,12 @@ class KVCache:
         self._desc = xq_kv_cache(qtype, n_pages, page_size, heads, dim, self.k.data_ptr(), self.v.data_ptr())
         self._ref = ctypes.byref(self._desc)
         self._inner = (dim, 1)
-        self._lib = lib()
+        L = self._lib = lib()
+        self._write, self._read = L.xq_kv_write, L.xq_kv_read
+        self._empty, self._empty_like, self._int32, self._int64 = torch.empty, torch.empty_like, torch.int32, torch.int64
         self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        self._ws = {}   # stream -> workspace
+        self._ws = {}   # stream -> (workspace, bytes, address)
         self._need = {}  # sizes of a call -> workspace bytes
-
-    def _on_device(self, *tensors):
-        for t in tensors:
-            if t.device != self.device:
-                raise ValueError(f"a tensor on {t.device} for a cache on {self.device}")
 
     def _stream(self, stream):
         # the current stream's handle: torch's accessor of the bare handle costs a fortieth of building a Stream object
@@ -484,39 +481,40 @@ class KVCache:
         """Quantize rows k, v [tokens, heads, dim] into slots int64 [tokens]
         (negative ones are skipped). A token's row is contiguous; rows may be
         a part of longer ones (k.stride(0))."""
-        n = slots.shape[0]
+        n, dev = slots.shape[0], self.device
         shape, ks, vs = (n, self.heads, self.dim), k.stride(), v.stride()
         if k.shape != shape or v.shape != shape or k.dtype != v.dtype or ks[1:] != self._inner or vs[1:] != self._inner:
             raise ValueError(f"k and v: {shape} of one dtype, each token's row contiguous")
-        if slots.dtype != self._torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
+        if slots.dtype != self._int64 or slots.dim() != 1 or not slots.is_contiguous():
             raise ValueError("slots: contiguous int64 [tokens]")
-        self._on_device(k, v, slots)
-        rc = self._lib.xq_kv_write(self._ref, _float_type(k.dtype), k.data_ptr(), ks[0], v.data_ptr(), vs[0], slots.data_ptr(), n,
-                                   self._stream(stream))
+        if k.device != dev or v.device != dev or slots.device != dev:
+            raise ValueError(f"k, v and slots have to be on {dev}")
+        rc = self._write(self._ref, _float_type(k.dtype), k.data_ptr(), ks[0], v.data_ptr(), vs[0], slots.data_ptr(), n,
+                         self._stream(stream))
         if rc:
             raise XQError("xq_kv_write", rc)
 
     def read(self, slots, dtype=None, k=None, v=None, stream=None):
         """The rows of slots int64 [tokens] as floats: (k, v), each
         [tokens, heads, dim] of dtype (float32)."""
-        torch = self._torch
-        if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous():
+        if slots.dtype != self._int64 or slots.dim() != 1 or not slots.is_contiguous():
             raise ValueError("slots: contiguous int64 [tokens]")
-        n = slots.shape[0]
+        n, dev = slots.shape[0], self.device
+        if slots.device != dev:
+            raise ValueError(f"slots have to be on {dev}")
         shape = (n, self.heads, self.dim)
         if dtype is None:
-            dtype = torch.float32 if k is None else k.dtype
+            dtype = self._torch.float32 if k is None else k.dtype
         kind = _float_type(dtype)
         if k is None:
-            k = torch.empty(shape, dtype=dtype, device=self.device)
-        elif k.shape != shape or k.dtype != dtype or not k.is_contiguous():
-            raise ValueError(f"k: contiguous {shape} of {dtype}")
+            k = self._empty(shape, dtype=dtype, device=dev)
+        elif k.shape != shape or k.dtype != dtype or not k.is_contiguous() or k.device != dev:
+            raise ValueError(f"k: contiguous {shape} of {dtype} on {dev}")
         if v is None:
-            v = torch.empty(shape, dtype=dtype, device=self.device)
-        elif v.shape != shape or v.dtype != dtype or not v.is_contiguous():
-            raise ValueError(f"v: contiguous {shape} of {dtype}")
-        self._on_device(slots, k, v)
-        rc = self._lib.xq_kv_read(self._ref, slots.data_ptr(), n, kind, k.data_ptr(), v.data_ptr(), self._stream(stream))
+            v = self._empty(shape, dtype=dtype, device=dev)
+        elif v.shape != shape or v.dtype != dtype or not v.is_contiguous() or v.device != dev:
+            raise ValueError(f"v: contiguous {shape} of {dtype} on {dev}")
+        rc = self._read(self._ref, slots.data_ptr(), n, kind, k.data_ptr(), v.data_ptr(), self._stream(stream))
         if rc:
             raise XQError("xq_kv_read", rc)
         return k, v
@@ -530,44 +528,52 @@ class KVCache:
         return nb
 
     def _workspace(self, key, stream):
+        """The stream's workspace, of at least what calls of these sizes (the
+        arguments of attn_workspace_bytes) need."""
         need = self._need.get(key)
         if need is None:
             need = self._need[key] = self.attn_workspace_bytes(*key)
         ws = self._ws.get(stream)
-        if ws is None or ws.numel() < need:
+        if ws is None or ws[1] < need:
             torch = self._torch
             with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device)):
-                ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            self._ws[stream] = ws
+                t = torch.empty(need, dtype=torch.uint8, device=self.device)
+            ws = self._ws[stream] = (t, need, t.data_ptr())
         return ws
 
     def _attn(self, fn, q, pages, lens, scale, window, prefix_pages, prefix_len, out, workspace, stream):
-        torch = self._torch
-        if q.dim() != 4 or q.shape[3] != self.dim or not q.is_contiguous():
+        dev, int32, shape = self.device, self._int32, q.shape
+        if len(shape) != 4 or shape[3] != self.dim or not q.is_contiguous():
             raise ValueError(f"q: contiguous [batch, n_q, heads, {self.dim}]")
-        batch, n_q, heads, dim = q.shape
-        if pages.dtype != torch.int32 or pages.dim() != 2 or pages.shape[0] != batch or (pages.shape[1] > 1 and pages.stride(1) != 1):
+        batch, n_q, heads, dim = shape
+        ps, pshape = pages.stride(), pages.shape
+        if pages.dtype != int32 or len(pshape) != 2 or pshape[0] != batch or (ps[1] != 1 and pshape[1] > 1):
             raise ValueError("pages: int32 [batch, pages], each row contiguous")
-        if lens.dtype != torch.int32 or lens.shape != (batch,) or not lens.is_contiguous():
+        if lens.dtype != int32 or lens.shape != (batch,) or not lens.is_contiguous():
             raise ValueError("lens: contiguous int32 [batch]")
+        if q.device != dev or pages.device != dev or lens.device != dev:
+            raise ValueError(f"q, pages and lens have to be on {dev}")
         if out is None:
-            out = torch.empty_like(q)
-        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+            out = self._empty_like(q)
+        elif out.shape != shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != dev:
             raise ValueError("out: a contiguous tensor like q")
-        if prefix_pages is not None and (prefix_pages.dtype != torch.int32 or prefix_pages.dim() != 1 or
-                                         not prefix_pages.is_contiguous() or
-                                         prefix_pages.shape[0] * self.page_size < prefix_len):
-            raise ValueError("prefix_pages: contiguous int32 ids of the prefix's pages")
-        self._on_device(q, pages, lens, out)
-        s = self._stream(stream)
-        width = pages.shape[1]
+        prefix = None
+        if prefix_pages is not None:
+            if (prefix_pages.dtype != int32 or prefix_pages.dim() != 1 or not prefix_pages.is_contiguous()
+                    or prefix_pages.shape[0] * self.page_size < prefix_len or prefix_pages.device != dev):
+                raise ValueError(f"prefix_pages: contiguous int32 ids of the prefix's pages, on {dev}")
+            prefix = prefix_pages.data_ptr()
+        s, width, dtype = self._stream(stream), pshape[1], q.dtype
         if workspace is None:
-            workspace = self._workspace((q.dtype, batch, n_q, heads, width, prefix_len), s)
-        query = xq_kv_query(_float_type(q.dtype), batch, n_q, heads, q.data_ptr(), out.data_ptr(), pages.data_ptr(),
-                            pages.stride(0) if batch > 1 else width, width, lens.data_ptr(),
-                            dim ** -0.5 if scale is None else scale, window,
-                            prefix_pages.data_ptr() if prefix_pages is not None else None, prefix_len)
-        rc = fn(self._ref, ctypes.byref(query), workspace.data_ptr(), workspace.numel(), s)
+            _, ws_bytes, ws = self._workspace((dtype, batch, n_q, heads, width, prefix_len), s)
+        else:
+            ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+            if workspace.device != dev or not workspace.is_contiguous():
+                raise ValueError(f"workspace: contiguous, on {dev}")
+        query = xq_kv_query(_float_type(dtype), batch, n_q, heads, q.data_ptr(), out.data_ptr(), pages.data_ptr(),
+                            ps[0] if batch > 1 else width, width, lens.data_ptr(), dim ** -0.5 if scale is None else scale, window,
+                            prefix, prefix_len)
+        rc = fn(self._ref, query, ws, ws_bytes, s)
         if rc:
             raise XQError(fn.__name__, rc)
         return out
@@ -582,6 +588,5 @@ class KVCache:
     def attn_shared(self, q, prefix_pages, prefix_len: int, pages, lens, scale=None, out=None, workspace=None, stream=None):
         """attn for sequences that all begin with the prefix_len tokens in
         prefix_pages int32 [pages]; pages and lens are of the tokens after it."""
-        self._on_device(prefix_pages)
         return self._attn(self._lib.xq_kv_attn_shared, q, pages, lens, scale, 0, prefix_pages, prefix_len, out, workspace,
                           stream)
