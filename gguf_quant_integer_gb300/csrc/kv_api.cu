@@ -14,15 +14,18 @@ int bits_of(int type) { return type == XQ_TYPE_Q8_0 ? 8 : type == XQ_TYPE_Q4_0 ?
 
 bool float_type(int type) { return type == XQ_TYPE_F32 || type == XQ_TYPE_F16 || type == XQ_TYPE_BF16; }
 
-bool cache_shape(int n_pages, int page_size, int heads, int dim) {
+bool cache_shape(int type, int n_pages, int page_size, int heads, int dim) {
   // heads: a page's bytes and a pool's 32-blocks per token stay within an int
-  return n_pages >= 0 && page_size >= 16 && page_size <= 4096 && (page_size & (page_size - 1)) == 0 && heads > 0 &&
-         heads <= 1024 && (dim == 64 || dim == 96 || dim == 128 || dim == 256);
+  if (n_pages < 0 || page_size < 16 || page_size > 4096 || (page_size & (page_size - 1)) != 0 || heads <= 0 || heads > 1024 ||
+      (dim != 64 && dim != 96 && dim != 128 && dim != 256))
+    return false;
+  // a pool has fewer than 2^32 32-byte pieces
+  return static_cast<unsigned long long>(n_pages) * heads * page_size * (dim * bits_of(type) / 8 + dim / 16) < (1ull << 37) - 32;
 }
 
 xq_status check_cache(const xq_kv_cache* c) {
   if (!c || !bits_of(c->type)) return XQ_ERR_ARG;
-  if (!cache_shape(c->n_pages, c->page_size, c->heads, c->dim)) return XQ_ERR_SHAPE;
+  if (!cache_shape(c->type, c->n_pages, c->page_size, c->heads, c->dim)) return XQ_ERR_SHAPE;
   if (c->n_pages > 0 && (!c->k || !c->v)) return XQ_ERR_ARG;
   if (!aligned(c->k, 16) || !aligned(c->v, 16)) return XQ_ERR_ALIGN;
   return XQ_OK;
@@ -47,7 +50,7 @@ xq::KvView view_of(const xq_kv_cache* c) {
 // The parts of an attention call's arguments that its workspace depends on.
 xq_status check_sizes(const xq_kv_cache* c, const xq_kv_query* q, bool shared) {
   if (!c || !q || !bits_of(c->type) || !float_type(q->type)) return XQ_ERR_ARG;
-  if (!cache_shape(c->n_pages, c->page_size, c->heads, c->dim)) return XQ_ERR_SHAPE;
+  if (!cache_shape(c->type, c->n_pages, c->page_size, c->heads, c->dim)) return XQ_ERR_SHAPE;
   if (q->batch < 0 || q->n_q < 0 || q->heads <= 0 || q->heads % c->heads || q->max_pages < 0) return XQ_ERR_SHAPE;
   // positions (own and prefix tokens) and the rows of the call stay within an int
   const long long longest = static_cast<long long>(q->max_pages) * c->page_size + (shared ? q->prefix_len : 0);
@@ -104,7 +107,7 @@ extern "C" {
 
 size_t xq_kv_bytes(int type, int n_pages, int page_size, int heads, int dim) {
   const int bits = bits_of(type);
-  if (!bits || !cache_shape(n_pages, page_size, heads, dim)) return 0;
+  if (!bits || !cache_shape(type, n_pages, page_size, heads, dim)) return 0;
   return static_cast<size_t>(n_pages) * heads * page_size * (dim * bits / 8 + dim / 16);
 }
 

@@ -513,28 +513,32 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
   // Where this lane's copies of a tile go and come from. Scales: the first
   // lanes take K's, the next ones V's.
   const uint32_t code_to = chunk_at<S::kChunks>(lane / S::kChunks, lane % S::kChunks);
-  const long long v_off = reinterpret_cast<long long>(A.c.v) - reinterpret_cast<long long>(A.c.k);
   const bool v_scale = lane >= S::kScales / 16;
   const int scale_lane = (v_scale ? lane - S::kScales / 16 : lane) * 16;
   const uint32_t scale_to = S::kCodes + scale_lane + (v_scale ? S::kCodes + S::kScales : 0);
-  const long long scale_from = A.c.scale_off + scale_lane - lane * 16 + (v_scale ? v_off : 0);  // from this lane's code chunk
+  // A tile's place in a pool, in 32-byte steps (16 rows of codes or scales are
+  // a multiple; a pool has fewer than 2^32), is added to these.
+  const uint8_t* const k_from = A.c.k + lane * 16;
+  const uint8_t* const v_from = A.c.v + lane * 16;
+  const uint8_t* const scale_from = (v_scale ? A.c.v : A.c.k) + scale_lane;
   bool left_record = false;
   // ---- the warp's tiles of 16 keys of a part: warp, warp + 4, ... of its units
   int tile0 = 0, tiles = 0, line0 = 0, stage = 0;
   const int32_t* table = nullptr;
   const int shift = A.c.page_shift - 4;  // tiles a page
-  // Where the next 32 tiles lie, one a lane: the address of its K codes (0 if its page id is invalid), and from there to its
-  // K scales. The page ids after them are on their way.
-  long long code_at = 0;
-  int scales_at = 0, next_page = 0;
+  // Where the codes and the scales of the next 32 tiles lie, one tile a lane (all ones if its page id is invalid). The page
+  // ids after them are on their way.
+  uint32_t code_at = 0, scales_at = 0;
+  int next_page = 0;
   unsigned bad = 0;      // stages whose page id was invalid
   unsigned clean_n = 0;  // tiles from `clean` on that hold only keys which every row sees
   auto page_of = [&](int i) { return i < tiles ? table[(tile0 + i * kAttnWarps) >> shift] : 0; };
   auto locate = [&](int i, int page) {
     const int line = line0 + (((tile0 + i * kAttnWarps) & ((1 << shift) - 1)) << 4);
     const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(A.c.n_pages);
-    code_at = ok ? reinterpret_cast<long long>(A.c.k) + page * A.c.page_bytes + line * S::kRow : 0;
-    scales_at = line * (NB * 2 - S::kRow);
+    const uint32_t at = static_cast<uint32_t>(page) * static_cast<uint32_t>(A.c.page_bytes >> 5);
+    code_at = ok ? at + static_cast<uint32_t>(line / 16) * (S::kRow / 2) : ~0u;
+    scales_at = at + static_cast<uint32_t>(A.c.scale_off + line * (NB * 2)) / 32;
   };
   auto issue = [&](int i, int stage) {
     if (i < tiles) {
@@ -542,12 +546,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
         locate(i + lane, next_page);
         next_page = page_of(i + 32 + lane);
       }
-      const unsigned lo = __shfl_sync(0xffffffffu, static_cast<unsigned>(code_at), i & 31);
-      const unsigned hi = __shfl_sync(0xffffffffu, static_cast<unsigned>(code_at >> 32), i & 31);
-      const int so = __shfl_sync(0xffffffffu, scales_at, i & 31);
-      if (hi != 0) {
-        const uint8_t* const kc = reinterpret_cast<const uint8_t*>((static_cast<long long>(hi) << 32) + lo + lane * 16);
-        const uint8_t* const vc = kc + v_off;
+      const uint32_t at = __shfl_sync(0xffffffffu, code_at, i & 31), so = __shfl_sync(0xffffffffu, scales_at, i & 31);
+      if (at != ~0u) {
+        const uint8_t* const kc = k_from + static_cast<size_t>(at) * 32;
+        const uint8_t* const vc = v_from + static_cast<size_t>(at) * 32;
         const uint32_t base = stage0 + stage * S::kStage, dst = base + code_to;
 #pragma unroll
         for (int x = 0; x < S::kSteps; ++x) {
@@ -559,7 +561,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
             cp16(to + S::kCodes + S::kScales, vc + x * 512);
           }
         }
-        if (lane < 2 * S::kScales / 16) cp16(base + scale_to, kc + (scale_from + so));
+        if (lane < 2 * S::kScales / 16) cp16(base + scale_to, scale_from + static_cast<size_t>(so) * 32);
       } else {
         bad |= 1u << stage;
         clean_n = 0;

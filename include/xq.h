@@ -441,7 +441,8 @@ XQ_API xq_status xq_debug_layer_matmuls(const xq_proj *proj, int n_proj, int n_i
  * then their scales, fp16 [heads][page_size][dim / 32]. Token slot s is row
  * s % page_size of page s / page_size.
  *
- * dim is 64, 96, 128 or 256; page_size is a power of two from 16 to 4096.
+ * dim is 64, 96, 128 or 256; page_size is a power of two from 16 to 4096;
+ * heads is at most 1024; a pool is smaller than 128 GiB.
  * Every pointer is 16-byte aligned except the rows that xq_kv_write takes
  * (aligned to their element; rows at multiples of 16 bytes are read in
  * 16-byte pieces), slots (8 bytes) and pages, lens (4 bytes).
