@@ -21,14 +21,34 @@ Rows rows_for(const KvAttnArgs& a, int rows) {
   return {exact, 1, rows <= 8 || a.c.dim == 256 ? 1 : 2};
 }
 
-// Whether a pair's rows go to the tcgen05 tiles of 128 rows.
-bool tiled(const KvAttnArgs& a, long long rows) { return a.c.dim <= 128 && rows >= kTileMinRows; }
+// One pass of a call: every sequence's own pages, or the prefix for all rows.
+struct Pass {
+  int seqs, rows;   // rows of a pair
+  long long keys;   // of a sequence, at most
+};
+Pass own_pass(const KvAttnArgs& a) { return {a.batch, a.rows, static_cast<long long>(a.max_pages) << a.c.page_shift}; }
+Pass prefix_pass(const KvAttnArgs& a) { return {1, a.batch * a.rows, a.prefix_len}; }
 
-// Rows of partial results (two a CTA): four resident CTAs an SM of 4 or 8
-// rows, three of up to 16; one of 128 or 256.
-constexpr size_t kSplitRows = 2 * 4 * kNumSMs * 16;
+// Whether a pass goes to the tcgen05 tiles. They take some 20 us whatever the
+// work, and from 64 rows of 16-bit queries (128 of fp32 ones, whose products
+// are six) a fraction of the split kernel's time for it; both measured at
+// rows x keys x KV heads from 0.07 to 67 million (8 heads, dim 128, Q8_0):
+//   bf16  128 rows x 2048 keys 35 and 36 us, x 8192 42 and 61, x 32768 73 and 183
+//         64 rows x 8192 43 and 44 us;  32 rows x 32768 79 and 68
+//   fp32  128 rows x 8192 69 and 73 us, x 32768 145 and 217
+//         64 rows x 32768 152 and 120;  256 rows x 2048 55 and 52
+bool tiled(const KvAttnArgs& a, const Pass& p) {
+  const bool exact = a.type == kF32;
+  if (a.c.dim > 128 || p.rows < (exact ? 128 : 64)) return false;
+  const long long seen = a.window > 0 && p.keys > a.window + a.n_q ? a.window + a.n_q : p.keys;
+  return static_cast<double>(p.seqs) * p.rows * seen * a.c.heads >= (exact ? 8e6 : 3e6);
+}
+
+// CTAs and rows of partial results (two a CTA): three resident CTAs an SM of
+// 4 or 8 rows, two of up to 16; one of 128 or 256.
+constexpr int kMaxCtas = 3 * kNumSMs;
+constexpr size_t kSplitRows = 2 * kMaxCtas * 16;
 size_t tile_part_rows(bool exact) { return static_cast<size_t>(2) * kNumSMs * tile_rows(exact); }
-constexpr int kMaxCtas = 4 * kNumSMs;
 
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
@@ -37,7 +57,7 @@ struct Layout {
 };
 Layout layout(const KvAttnArgs& a) {
   Layout L;
-  const bool tile = tiled(a, a.rows) || (a.prefix_len > 0 && tiled(a, static_cast<long long>(a.batch) * a.rows));
+  const bool tile = tiled(a, own_pass(a)) || (a.prefix_len > 0 && tiled(a, prefix_pass(a)));
   const size_t rows = tile ? tile_part_rows(a.type == kF32) : kSplitRows;
   const size_t outs = a.prefix_len > 0 ? static_cast<size_t>(a.batch) * a.n_q * a.q_heads : 0;
   L.record = 0;
@@ -49,13 +69,14 @@ Layout layout(const KvAttnArgs& a) {
   return L;
 }
 
-cudaError_t run(SplitArgs& p, const KvAttnArgs& a, int bits, cudaStream_t s) {
-  const bool tile = tiled(a, p.rows);
+cudaError_t run(SplitArgs& p, const Pass& pass, const KvAttnArgs& a, int bits, cudaStream_t s) {
+  p.seqs = pass.seqs;
+  p.rows = pass.rows;
+  const bool tile = tiled(a, pass);
   const Rows f = rows_for(a, p.rows);
   const int r = tile ? tile_rows(f.exact) : f.nt * 8 / f.np;
   p.chunks = (p.rows + r - 1) / r;
-  const long long keys = p.flat ? p.prefix_len : static_cast<long long>(p.max_pages) << p.c.page_shift;
-  const long long units = (keys + kAttnUnit - 1) / kAttnUnit;
+  const long long units = (pass.keys + kAttnUnit - 1) / kAttnUnit;
   // Sequences too short for a second CTA to be worth a join: whole pairs.
   p.whole = units <= (p.store ? kAttnWholeOwn : kAttnWhole);
   p.head = tile ? kTileHead : kAttnHead;
@@ -100,12 +121,10 @@ cudaError_t launch_kv_attn(const KvAttnArgs& a, int bits, void* workspace, cudaS
   p.pre_el = reinterpret_cast<float*>(ws + L.pre_el);
   p.pre_o = reinterpret_cast<float*>(ws + L.pre_o);
   p.out = a.out;
-  p.seqs = a.batch;
-  p.rows = a.rows;
   p.pages = a.pages;
   p.page_stride = a.page_stride;
   p.store = a.prefix_len > 0;
-  cudaError_t e = run(p, a, bits, s);
+  const cudaError_t e = run(p, own_pass(a), a, bits, s);
   if (e != cudaSuccess || a.prefix_len == 0) return e;
   // Then every row of the call against the prefix, which is read once. The
   // pass may start beside the first one where that leaves no parts (they would
@@ -114,10 +133,8 @@ cudaError_t launch_kv_attn(const KvAttnArgs& a, int bits, void* workspace, cudaS
   p.merge = true;
   p.late = p.whole;
   p.flat = true;
-  p.seqs = 1;
-  p.rows = a.batch * a.rows;
   p.pages = a.prefix_pages;
-  return run(p, a, bits, s);
+  return run(p, prefix_pass(a), a, bits, s);
 }
 
 namespace {

@@ -111,15 +111,20 @@ struct SplitShape {
   static constexpr int kScales = 16 * NB * 2;
   static constexpr int kStage = 2 * (kCodes + kScales);
   // Stages of 16 keys a warp: about 13 KB (three 4.25 KB stages of Q8_0 at dim
-  // 128), so that 16 warps an SM keep over 100 KB in flight.
+  // 128), so that 12 warps an SM keep 100 KB in flight. (18 KB: 4 us more on
+  // the batch above.)
   static constexpr int kStages = kStage * 3 > 13312 ? 3 : 13312 / kStage > 6 ? 6 : 13312 / kStage;
   static constexpr int kWarpBytes = kStages * kStage > R * D * 4 ? kStages * kStage : R * D * 4;
   static constexpr int kSmem = kAttnWarps * kWarpBytes;
   // A warp's results fit one stage: the next pair's first tiles can be on
   // their way into the others while the warps are merged.
   static constexpr bool kOverlap = R * D * 4 <= kStage;
-  // Resident CTAs an SM: the accumulators take NT * D / 4 registers a thread.
-  static constexpr int kCtas = D == 256 ? 2 : NT == 1 ? 4 : 3;
+  // Resident CTAs an SM, by registers (168 a thread, 255 with two n-tiles): a
+  // fourth (128 registers, some spilled) costs more than its latency hiding
+  // gives (64-sequence Q8_0 fp32 batch 92 against 86 us, 131071-token Q4_0
+  // bf16 sequence 46 against 42 us; two n-tiles, 16 sequences of 5 tokens: 28
+  // against 26 us).
+  static constexpr int kCtas = D == 256 || NT == 2 ? 2 : 3;
 };
 
 // One dim's kernels, in a translation unit of their own.

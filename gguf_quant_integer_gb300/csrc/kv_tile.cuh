@@ -39,7 +39,6 @@ constexpr int kTileKeys = 64;
 static_assert(kTileKeys == kAttnUnit, "both kernels cut the line in the same units");
 constexpr int kTileSoft = 8, kTileConv = 8;  // warps
 constexpr int kTileWarps = kTileSoft + kTileConv + 1;
-constexpr int kTileMinRows = 64;
 constexpr int kTileHead = 6;  // units of time a pair costs besides its keys
 
 template <int BITS, int D, int T>

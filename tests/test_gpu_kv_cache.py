@@ -331,3 +331,55 @@ def test_repeated_calls_agree_bit_for_bit(xq):
         for _ in range(5):
             assert torch.equal(cache.attn(q, table, lens), a)
             assert torch.equal(cache.attn_shared(q, pre, 789, table, lens), s)
+
+
+# Enough rows x keys for the tcgen05 tiles: 3 million a call for 16-bit queries (64 rows or more), 8 million for fp32 ones (128).
+
+@pytest.mark.parametrize("kind,dtype,heads,group,dim,page,n_q,prefix,lens", [
+    ("q8", "bf16", 2, 4, 128, 64, 1, 3001, [1 + i % 9 for i in range(128)]),
+    ("q4", "fp16", 2, 5, 64, 32, 1, 3111, [i % 4 for i in range(100)]),           # 500 rows: a half-empty second tile
+    ("q8", "fp16", 1, 13, 96, 16, 3, 6000, [5, 0, 40, 3, 2, 1] * 3),              # 702 rows; rows that end inside the prefix
+    ("q4", "bf16", 2, 3, 128, 128, 1, 8200, [7] * 64),                            # 192 rows: one and a half row tiles
+    ("q8", "fp32", 2, 8, 128, 64, 2, 4111, [2 + i % 7 for i in range(64)]),
+    ("q4", "fp32", 2, 8, 64, 32, 1, 4000, [i % 3 for i in range(130)]),
+    ("q8", "fp32", 1, 5, 96, 64, 1, 16100, [3] * 110)])
+def test_shared_prefix_on_row_tiles(xq, kind, dtype, heads, group, dim, page, n_q, prefix, lens):
+    attention_case(xq, kind, dtype, heads, group, dim, page, n_q, lens, prefix=prefix, seed=prefix)
+
+
+@pytest.mark.parametrize("kind,dtype,heads,group,dim,page,n_q,lens,window", [
+    ("q8", "bf16", 2, 4, 128, 64, 300, [1400, 299, 1, 0, 777], 0),
+    ("q4", "fp16", 1, 7, 64, 16, 129, [2100, 129, 600], 0),
+    ("q4", "bf16", 2, 2, 96, 32, 400, [1003, 2050], 700),
+    ("q8", "fp32", 2, 4, 128, 64, 333, [1800, 332, 40, 1111], 0),
+    ("q4", "fp32", 1, 6, 64, 32, 257, [2600, 300, 2599], 1500)])
+def test_long_query_runs_on_row_tiles(xq, kind, dtype, heads, group, dim, page, n_q, lens, window):
+    attention_case(xq, kind, dtype, heads, group, dim, page, n_q, lens, window=window, seed=n_q)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16"])
+def test_row_tiles_with_bad_pages_and_odd_scales(xq, dtype):
+    """Masked groups of a page without an id, V blocks from 1e-3 to 1e3, a negative scale of the scores."""
+    heads, group, dim, page, n, rows_n = 2, 8, 64, 16, 2000, 128
+    rng = np.random.default_rng(12)
+    cache = xq.KVCache(ko.Q8_0, 126, page, heads, dim)
+    k = rows(rng, (n, heads, dim), "fp32")
+    v = rows(rng, (n, heads, dim), "fp32") * torch.logspace(-3, 3, n)[:, None, None] * torch.logspace(-2, 2, dim)
+    cache.write(k.cuda(), v.cuda(), torch.arange(n, device="cuda"))
+    kf, vf = (t.cpu().numpy().astype(np.float64) for t in cache.read(torch.arange(n, device="cuda")))
+    pre = torch.arange(125, dtype=torch.int32)
+    pre[3], pre[77], pre[124] = -1, 126, 1 << 30
+    keep = np.ones(n, bool)
+    for p in (3, 77, 124):
+        keep[p * page:(p + 1) * page] = False
+    n_q = 2 if dtype == "fp32" else 1
+    q = rows(rng, (rows_n * 2, n_q, heads * group, dim), "fp32").to(DTYPES[dtype])
+    table, lens = torch.zeros(rows_n * 2, 1, dtype=torch.int32, device="cuda"), torch.full((rows_n * 2,), n_q, dtype=torch.int32, device="cuda")
+    xq.device_error()
+    out = cache.attn_shared(q.cuda(), pre.cuda(), n, table, lens, scale=-0.05).float().cpu().numpy()
+    assert xq.device_error() == (3 << 8) | 2
+    for b in (0, 1, 100, 255):
+        kk, vv = np.concatenate((kf[keep], kf[:n_q])), np.concatenate((vf[keep], vf[:n_q]))
+        ref = ko.attention(q[b].float().numpy(), kk, vv, -0.05, [len(kk) - n_q + i for i in range(n_q)])
+        err, tol = np.abs(out[b] - ref[0]), ko.tolerance(*ref, dtype)
+        assert np.all(err <= tol), (b, float((err / tol).max()))
