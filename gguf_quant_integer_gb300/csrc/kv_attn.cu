@@ -79,7 +79,7 @@ cudaError_t run(SplitArgs& p, const Pass& pass, const KvAttnArgs& a, int bits, c
   const long long units = (pass.keys + kAttnUnit - 1) / kAttnUnit;
   // Sequences too short for a second CTA to be worth a join: whole pairs.
   p.whole = units <= (p.store ? kAttnWholeOwn : kAttnWhole);
-  p.head = tile ? kTileHead : kAttnHead;
+  p.head = tile ? kTileHead : f.nt == 2 ? kAttnHead2 : kAttnHead;
   p.units = p.seqs * ((units > 1 ? units : 1) + p.head) * p.c.heads * p.chunks;
   if (tile) {
     switch (a.c.dim) {

@@ -49,8 +49,11 @@ constexpr float kWeightTop = 32768.0f, kWeightLow = 1.220703125e-4f;  // 2^15, 2
 constexpr int kAttnUnit = 16 * kAttnWarps;  // keys a unit
 // Units of time that a CTA spends on a pair besides its keys (queries, page
 // ids, filling the pipeline, merging): the cut counts them, or CTAs with many
-// short sequences would finish last.
-constexpr int kAttnHead = 5;
+// short sequences would finish last. With two n-tiles more, as each row's
+// query is split. (64 sequences of 211 to 8192 tokens: 88.3, 86.3, 85.6, 86.2,
+// 87.8 us with 3, 4, 5, 6, 8; two n-tiles, 16 sequences of 300 to 4099: 27.8,
+// 26.0, 23.9 us with 3, 5, 8.)
+constexpr int kAttnHead = 5, kAttnHead2 = 8;
 // Pairs that can have no more units than this are not cut. A CTA takes about
 // 0.5 us a unit, the join's launch 4 us (one 97-token sequence, 8 KV heads:
 // 8.5 us cut, 6.6 us whole).

@@ -11,10 +11,12 @@
 //   16-bit queries (T = 1): everything enters as one fp16 number. K and V are
 //     code * d / 2^x rounded to fp16; 2^x, from the part's largest block scale
 //     (for V of each 32 elements), keeps them in range whatever their size.
-//   fp32 queries (T = 3): queries, weights, K and V enter as three bf16
-//     numbers each (24 bits, and fp32's exponent range, so that no scaling is
-//     needed), cut off, not rounded: a product is the six pairs that matter,
-//       1.1 + 1.2 + 2.1 + 1.3 + 2.2 + 3.1, the rest is below 2^-24.
+//   fp32 queries (T = 3): queries and K enter as two fp16 numbers each (22 bits
+//     and 19, all that a code times its scale has), scaled alike; their product
+//     is hi.hi + hi.lo + lo.hi. Weights and V enter as three bf16 numbers each
+//     (24 bits, and fp32's exponent range, which the smallest weights need),
+//     cut off, not rounded: the six pairs 1.1 + 1.2 + 2.1 + 1.3 + 2.2 + 3.1;
+//     the rest is below 2^-24.
 //
 // What bounds it: instructions of the softmax and of dequantization. A tile
 // has 8192 scores at about 6 instructions each (scale, mask test, maximum,
@@ -50,24 +52,24 @@ struct TileShape {
   static constexpr int kSbo = 144;
   static constexpr int kKLbo = kTileKeys / 8 * kSbo, kVLbo = D / 8 * kSbo;
   static constexpr int kOperand = D * kSbo;  // one piece of K or of V: 64 keys x dim
-  static constexpr int kBufs = T == 1 ? 2 : 1;   // of K and V
+  static constexpr int kKPieces = T == 1 ? 1 : 2, kVPieces = T;  // fp16 ones of q and K, those of the weights and V
+  static constexpr int kKBufs = 2, kVBufs = T == 1 ? 2 : 1;
   static constexpr int kTiles = T == 1 ? 2 : 1;  // row tiles
   static constexpr int kRows = kTiles * kTileRows;
   static constexpr int kSoftWarps = kTileSoft / kTiles;  // of a row tile
   static constexpr int kRawCodes = kTileKeys * kRow, kRawScales = kTileKeys * NB * 2;
   static constexpr int kRaw = 2 * (kRawCodes + kRawScales);
   static constexpr int kRawStages = 4;  // two of each group of unpacking warps
-  static constexpr int kOffV = kBufs * T * kOperand, kOffRaw = 2 * kOffV;
-  // The tile's scales, ready for use: K's [64][NB], V's [NB][64], fp16 or fp32.
-  static constexpr int kScaleBytes = T == 1 ? 2 : 4;
+  static constexpr int kOffV = kKBufs * kKPieces * kOperand, kOffRaw = kOffV + kVBufs * kVPieces * kOperand;
+  // The tile's scales, ready for use: K's [64][NB] fp16, V's [NB][64] fp16 or (T = 3) fp32.
+  static constexpr int kScaleK = kTileKeys * NB * 2;
   static constexpr int kOffScale = kOffRaw + kRawStages * kRaw;
-  static constexpr int kScales = 2 * kTileKeys * NB * kScaleBytes;  // a table for each group
+  static constexpr int kScales = kScaleK + kTileKeys * NB * (T == 1 ? 2 : 4);  // a table for each group
   static constexpr int kSmem = kOffScale + 2 * kScales;
-  // Tensor memory columns: queries, scores, weights, outputs; of each row tile where there are two. Their weights take the
-  // scores' columns, which the row's thread has read by then.
-  static constexpr int kColS = T == 1 ? kTiles * D / 2 : T * D / 2;
-  static constexpr int kColP = T == 1 ? kColS : kColS + kTileKeys;
-  static constexpr int kColO = T == 1 ? kColS + kTiles * kTileKeys : kColP + T * kTileKeys / 2;
+  // Tensor memory columns: queries (of two row tiles, or two pieces), scores (of two row tiles, or two buffers), weights,
+  // outputs. With two row tiles the weights take the scores' columns, which the row's thread has read by then.
+  static constexpr int kColS = D, kColP = T == 1 ? kColS : kColS + 2 * kTileKeys;
+  static constexpr int kColO = T == 1 ? kColS + 2 * kTileKeys : kColP + T * kTileKeys / 2;
   static constexpr int kCols = kColO + kTiles * D;
   static constexpr int kAlloc = kCols <= 256 ? 256 : 512;
   static_assert(kCols <= 512 && kSmem <= 227 * 1024, "one CTA fits the SM");
@@ -192,26 +194,30 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
   if (warp == kTileWarps - 1) {
     // ------------------------------------------------ products (one thread)
     if (lane == 0) {
-      constexpr uint32_t idS = ptx::idesc_f16(kTileRows, kTileKeys, T == 3), idO = ptx::idesc_f16(kTileRows, D, T == 3);
+      constexpr uint32_t idS = ptx::idesc_f16(kTileRows, kTileKeys, false), idO = ptx::idesc_f16(kTileRows, D, T == 3);
       // pairs of pieces (A's, B's)
-      constexpr int kPairs = T == 3 ? 6 : 1;
-      constexpr int pa[6] = {0, 0, 1, 0, 1, 2}, pb[6] = {0, 1, 0, 2, 1, 0};
+      constexpr int kSPairs = T == 3 ? 3 : 1, kOPairs = T == 3 ? 6 : 1;
+      constexpr int sa[3] = {0, 0, 1}, sb[3] = {0, 1, 0};
+      constexpr int oa[6] = {0, 0, 1, 0, 1, 2}, ob[6] = {0, 1, 0, 2, 1, 0};
+      // Scores are computed this many tiles ahead of the outputs.
+      constexpr int kAhead = T == 1 ? 1 : 2;
       bool ok = true;
       unsigned it = 0, done[2] = {0u, 0u}, parts[2] = {0u, 0u};  // tiles so far; of each row tile
       // Row tile r's scores of tile i; last: of the part's row tiles.
       auto scores = [&](int r, unsigned i, bool last) {
-        const unsigned b = i % S::kBufs;
-        if (r == 0 && !wait(kBarK + b, i / S::kBufs, 1)) return false;
+        const unsigned b = i % S::kKBufs;
+        if (r == 0 && !wait(kBarK + b, i / S::kKBufs, 1)) return false;
         ptx::tc_fence_after();
+        const int to = T == 1 ? r : static_cast<int>(i & 1);  // row tile, or buffer
 #pragma unroll
-        for (int p = 0; p < kPairs; ++p)
+        for (int p = 0; p < kSPairs; ++p)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            ptx::mma_f16_ts(tmem + S::kColS + r * kTileKeys, tmem + (r * T + pa[p]) * (D / 2) + 8 * k,
-                            ptx::smem_desc(base + (b * T + pb[p]) * S::kOperand + 2 * k * S::kKLbo, S::kKLbo, S::kSbo), idS,
-                            p + k > 0);
+            ptx::mma_f16_ts(tmem + S::kColS + to * kTileKeys, tmem + (r + sa[p]) * (D / 2) + 8 * k,
+                            ptx::smem_desc(base + (b * S::kKPieces + sb[p]) * S::kOperand + 2 * k * S::kKLbo, S::kKLbo, S::kSbo),
+                            idS, p + k > 0);
         if (last) ptx::tc_commit(bar(kBarKFree + b));
-        ptx::tc_commit(bar(kBarS + r));
+        ptx::tc_commit(bar(kBarS + to));
         return true;
       };
       while (ok && line_next(A, line, part)) {
@@ -219,26 +225,25 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         const int chunk = part.pair % A.chunks;
         const int last = S::kTiles == 2 && A.rows - chunk * S::kRows > kTileRows ? 1 : 0;
         for (int r = 0; r <= last && ok; ++r) ok = wait(kBarQ + r, parts[r]++, 2) && scores(r, it, r == last);
+        if (kAhead == 2 && ok && tiles > 1) ok = scores(0, it + 1, true);
         for (int i = 0; i < tiles && ok; ++i, ++it) {
-          const unsigned b = it % S::kBufs;
+          const unsigned b = it % S::kVBufs;
           for (int r = 0; r <= last && ok; ++r) {
             ok = wait(kBarP + r, done[r]++, 3);
-            // weights with columns of their own: the next scores come first, or the softmax would wait for both
-            if (T == 3 && ok && i + 1 < tiles) ok = scores(r, it + 1, r == last);
-            if (r == 0) ok = ok && wait(kBarV + b, it / S::kBufs, 4);
+            if (r == 0) ok = ok && wait(kBarV + b, it / S::kVBufs, 4);
             if (!ok) break;
             ptx::tc_fence_after();
 #pragma unroll
-            for (int p = 0; p < kPairs; ++p)
+            for (int p = 0; p < kOPairs; ++p)
 #pragma unroll
               for (int k = 0; k < kTileKeys / 16; ++k)
-                ptx::mma_f16_ts(tmem + S::kColO + r * D, tmem + S::kColP + r * kTileKeys + pa[p] * (kTileKeys / 2) + 8 * k,
-                                ptx::smem_desc(base + S::kOffV + (b * T + pb[p]) * S::kOperand + 2 * k * S::kVLbo, S::kVLbo,
-                                               S::kSbo),
+                ptx::mma_f16_ts(tmem + S::kColO + r * D, tmem + S::kColP + r * kTileKeys + oa[p] * (kTileKeys / 2) + 8 * k,
+                                ptx::smem_desc(base + S::kOffV + (b * S::kVPieces + ob[p]) * S::kOperand + 2 * k * S::kVLbo,
+                                               S::kVLbo, S::kSbo),
                                 idO, i > 0 || p + k > 0);
             if (r == last) ptx::tc_commit(bar(kBarVFree + b));
             ptx::tc_commit(bar(kBarO + r));
-            if (T == 1 && i + 1 < tiles) ok = scores(r, it + 1, r == last);
+            if (i + kAhead < tiles) ok = scores(r, it + kAhead, r == last);
           }
         }
       }
@@ -419,7 +424,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
     constexpr float kTop = 40.0f, kStart = 0.0f;  // log2 of weights: the largest, and where the reference starts anew
     const int half = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    unsigned it = 0;
+    unsigned it = 0, parts = 0;
     bool fail = false, go = true, left_record = false;
     while (go && line_next(A, line, part)) {
       const int head = part.pair / A.chunks, chunk = part.pair - head * A.chunks;
@@ -428,29 +433,39 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       const size_t at = live ? row_at(A, part.seq, head, row0 + row) : 0;
       int lim0 = 0, lim1 = 0;
       if (live) row_range(A, part.seq, part.n, row0 + row, &lim0, &lim1);
-      // ---- this thread's half of the row's query into tensor memory, negated for a negative scale (so that cs > 0)
-      float cs = fmaxf(fabsf(A.scale) * 1.4426950408889634f, 1.17549435e-38f);
-      const float sign = A.scale < 0.0f ? -1.0f : 1.0f;
-      {
+      // ---- this thread's half of the row's query into tensor memory: two fp16 numbers, the row's largest element at
+      // 2^12 .. 2^13; negated for a negative scale (so that cs > 0)
+      const float4* const from = reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + at * D + half * (D / 2));
+      float largest = 0.0f;
+#pragma unroll 8
+      for (int x = 0; x < D / 8; ++x) {
+        const float4 v = live ? from[x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        largest = fmaxf(fmaxf(largest, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+      }
+      sh_x[half][row] = largest;
+      if (group_any(kBarrier, kThreads, fail)) break;
+      largest = fmaxf(largest, sh_x[half ^ 1][row]);
+      int ex = static_cast<int>(__float_as_uint(largest) >> 23) - 127;
+      ex = ex < -100 ? -100 : ex;
+      const float up = (A.scale < 0.0f ? -1.0f : 1.0f) * __uint_as_float(static_cast<unsigned>(127 + 12 - ex) << 23);
+      float cs = fabsf(A.scale) * 1.4426950408889634f * __uint_as_float(static_cast<unsigned>(127 - 12 + ex) << 23);
 #pragma unroll
-        for (int c = 0; c < D / 4; c += 8) {
-          uint32_t w[3][16];
+      for (int c = 0; c < D / 4; c += 8) {
+        uint32_t w[2][16];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float4 v = live ? load4(A.q, A.type, at * D + half * (D / 2) + 2 * c + 4 * x) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            uint32_t u[3];
-            cut3(v.x * sign, v.y * sign, u);
-            w[0][2 * x] = u[0];
-            w[1][2 * x] = u[1];
-            w[2][2 * x] = u[2];
-            cut3(v.z * sign, v.w * sign, u);
-            w[0][2 * x + 1] = u[0];
-            w[1][2 * x + 1] = u[1];
-            w[2][2 * x + 1] = u[2];
-          }
-#pragma unroll
-          for (int p = 0; p < 3; ++p) tmem_st8(tl + p * (D / 2) + half * (D / 4) + c, w[p]);
+        for (int x = 0; x < 4; ++x) {
+          float4 v = live ? from[c / 2 + x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          v = make_float4(v.x * up, v.y * up, v.z * up, v.w * up);
+          const uint32_t h0 = half2_of(v.x, v.y), h1 = half2_of(v.z, v.w);
+          const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+          const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+          w[0][2 * x] = h0;
+          w[0][2 * x + 1] = h1;
+          w[1][2 * x] = half2_of(v.x - f0.x, v.y - f0.y);
+          w[1][2 * x + 1] = half2_of(v.z - f1.x, v.w - f1.y);
         }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) tmem_st8(tl + p * (D / 2) + half * (D / 4) + c, w[p]);
       }
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
@@ -462,11 +477,15 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       float e = -1e30f;
       ptx::f2 l = ptx::pk(0.0f, 0.0f);
       for (int i = 0; i < tiles; ++i, ++it, key += kTileKeys) {
-        fail |= !wait_sleep(kBarS, it, 6);
+        fail |= !wait_sleep(kBarS + (it & 1), it >> 1, 6);
         ptx::tc_fence_after();
+        if (i == 0) {  // K's power of two, known once its first tile is there
+          const unsigned t0 = sh_top[parts & 3][0];
+          cs = fmaxf(cs * __uint_as_float((t0 >> 23 < 253 ? (t0 >> 23) + 1 : 254u) << 23), 1.17549435e-38f);
+        }
         uint32_t sv[2][16];
-        ptx::tmem_ld16(tl + S::kColS + half * 32, sv[0]);
-        ptx::tmem_ld16(tl + S::kColS + half * 32 + 16, sv[1]);
+        ptx::tmem_ld16(tl + S::kColS + (it & 1) * kTileKeys + half * 32, sv[0]);
+        ptx::tmem_ld16(tl + S::kColS + (it & 1) * kTileKeys + half * 32 + 16, sv[1]);
         ptx::tmem_wait_ld();
         const unsigned bad = sh_bad[it & 3] >> (2 * half) & 3u;
         if (key < lim0 || key + 32 > lim1 || bad) {
@@ -573,6 +592,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       ptx::tc_fence_before();
       // the other half's sums have been read when the next barrier is passed
       group_any(kBarrier, kThreads, false);
+      ++parts;
     }
     if (!left_record && tid == 0 && !A.whole) A.record[blockIdx.x] = make_int4(0, 0, -1, 0);
   } else {
@@ -603,8 +623,8 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       float kf = 1.0f, vf[NB];
 #pragma unroll
       for (int b = 0; b < NB; ++b) vf[b] = 1.0f;
-      if (T == 1) {
-        // ---- the part's largest scales: 1 / 17 or 1 / 9 of its bytes, which its tiles then find in L2
+      {
+        // ---- the part's largest scales (K's; T = 1: V's too): 1 / 17 or 1 / 9 of its bytes, which its tiles then find in L2
         unsigned* const tops = sh_top[parts & 3];
         if (ct <= NB) tops[ct] = 0u;
         if (group_any(kBarrier, kThreads, fail)) break;
@@ -628,7 +648,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             if (!page[y]) continue;
             const uint8_t* const p = reinterpret_cast<const uint8_t*>(page[y]) + A.c.scale_off + row_of(gi) * (2 * NB) + piece * 16;
             k4[y] = *reinterpret_cast<const uint4*>(p);
-            v4[y] = *reinterpret_cast<const uint4*>(p + v_off);
+            if (T == 1) v4[y] = *reinterpret_cast<const uint4*>(p + v_off);
           }
 #pragma unroll
           for (int y = 0; y < kAhead; ++y) {
@@ -646,6 +666,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               kt = __hmax2_nan(kt, __habs2(*reinterpret_cast<const __half2*>(&kw[h])));
+              if (T == 3) continue;
               const __half2 a = __habs2(*reinterpret_cast<const __half2*>(&vw[h]));
               if (NB % 2 == 0) {
                 vt[h % (NB / 2 > 0 ? NB / 2 : 1)] = __hmax2_nan(vt[h % (NB / 2 > 0 ? NB / 2 : 1)], a);
@@ -674,7 +695,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         auto down = [](unsigned t) { return __uint_as_float((t >> 23 < 253 ? 253 - (t >> 23) : 0u) << 23); };
         kf = down(tops[0]);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) vf[b] = down(tops[1 + b]);
+        for (int b = 0; b < NB && T == 1; ++b) vf[b] = down(tops[1 + b]);
       }
 
       // ---- the groups take tiles in turn. Raw tiles come one of its own tiles ahead, page ids one further
@@ -738,23 +759,18 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
 #pragma unroll
           for (int q = 1; q < NB; ++q) f = blk == q ? vf[q] : f;
           const float dk = gone ? 0.0f : __half2float(kd[x]) * kf, dv = gone ? 0.0f : __half2float(kd[S::kRawScales / 2 + x]) * f;
-          if (T == 1) {
-            reinterpret_cast<__half*>(scales)[x] = __float2half_rn(dk);
-            reinterpret_cast<__half*>(scales)[kTileKeys * NB + blk * kTileKeys + key] = __float2half_rn(dv);
-          } else {
-            reinterpret_cast<float*>(scales)[x] = dk;
-            reinterpret_cast<float*>(scales)[kTileKeys * NB + blk * kTileKeys + key] = dv;
-          }
+          reinterpret_cast<__half*>(scales)[x] = __float2half_rn(dk);
+          if (T == 1)
+            reinterpret_cast<__half*>(scales + S::kScaleK)[blk * kTileKeys + key] = __float2half_rn(dv);
+          else
+            reinterpret_cast<float*>(scales + S::kScaleK)[blk * kTileKeys + key] = dv;
         }
         group_any(kBarrier + 1 + group, kGroup, false);
-        const unsigned b = it % S::kBufs, turn = it / S::kBufs;
         // ---- K: operand rows are keys. A task is a key's 16-byte chunk
-        // With one buffer the groups take turns on it, and a parity tells a phase only from the next: the other group's tile
-        // has to be in before its release can be waited for.
-        if (S::kBufs == 1 && turn > 0) fail |= !wait_sleep(kBarK + b, turn - 1, 10);
-        if (turn > 0) fail |= !wait_sleep(kBarKFree + b, turn - 1, 10);
+        const unsigned kb = it % S::kKBufs, kturn = it / S::kKBufs;
+        if (kturn > 0) fail |= !wait_sleep(kBarKFree + kb, kturn - 1, 10);
         if (gt == 0) sh_bad[it & 3] = miss;
-        uint8_t* const ko = smem + b * T * S::kOperand;
+        uint8_t* const ko = smem + kb * S::kKPieces * S::kOperand;
 #pragma unroll
         for (int x = 0; x < (kTileKeys * S::kChunks + kGroup - 1) / kGroup; ++x) {
           const int c = x * kGroup + gt, key = c & (kTileKeys - 1), ch = c / kTileKeys;
@@ -762,47 +778,37 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             const uint4 u4 = *reinterpret_cast<const uint4*>(raw + chunk_at<S::kChunks>(key, ch));
             const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w};
             const int si = key * NB + (BITS == 8 ? ch / 2 : ch);
-            float d = 0.0f;
-            uint32_t dd = 0u;
-            if (T == 1)
-              dd = reinterpret_cast<const uint16_t*>(scales)[si] * 0x10001u;
-            else
-              d = reinterpret_cast<const float*>(scales)[si];
+            const uint32_t dd = reinterpret_cast<const uint16_t*>(scales)[si] * 0x10001u;
             uint8_t* const to = ko + (key >> 3) * S::kSbo + (key & 7) * 16;
 #pragma unroll
             for (int z = 0; z < (BITS == 8 ? 2 : 4); ++z) {  // 8 elements each
               const uint32_t w0 = BITS == 8 ? u[2 * z] : (u[2 * (z & 1)] >> (z & 2 ? 4 : 0)) & 0x0F0F0F0Fu;
               const uint32_t w1 = BITS == 8 ? u[2 * z + 1] : (u[2 * (z & 1) + 1] >> (z & 2 ? 4 : 0)) & 0x0F0F0F0Fu;
               uint8_t* const cell = to + (ch * (BITS == 8 ? 2 : 4) + z) * S::kKLbo;
-              if (T == 1) {
-                uint32_t h0[2], h1[2];
-                code_halves<BITS>(w0, h0);
-                code_halves<BITS>(w1, h1);
-                *reinterpret_cast<uint4*>(cell) =
-                    make_uint4(ptx::hmul2(h0[0], dd), ptx::hmul2(h0[1], dd), ptx::hmul2(h1[0], dd), ptx::hmul2(h1[1], dd));
-              } else {
-                float f0[4], f1[4];
-                code_floats<BITS>(w0, f0);
-                code_floats<BITS>(w1, f1);
-                uint32_t q[4][3];
-                cut3(f0[0] * d, f0[1] * d, q[0]);
-                cut3(f0[2] * d, f0[3] * d, q[1]);
-                cut3(f1[0] * d, f1[1] * d, q[2]);
-                cut3(f1[2] * d, f1[3] * d, q[3]);
+              uint32_t h[4], v[4];
+              code_halves<BITS>(w0, *reinterpret_cast<uint32_t(*)[2]>(&h[0]));
+              code_halves<BITS>(w1, *reinterpret_cast<uint32_t(*)[2]>(&h[2]));
 #pragma unroll
-                for (int p = 0; p < 3; ++p)
-                  *reinterpret_cast<uint4*>(cell + p * S::kOperand) = make_uint4(q[0][p], q[1][p], q[2][p], q[3][p]);
+              for (int q = 0; q < 4; ++q) v[q] = ptx::hmul2(h[q], dd);
+              *reinterpret_cast<uint4*>(cell) = make_uint4(v[0], v[1], v[2], v[3]);
+              if (T == 3) {  // what the rounding left, exact
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = hfma2_of(h[q], dd, v[q] ^ 0x80008000u);
+                *reinterpret_cast<uint4*>(cell + S::kOperand) = make_uint4(v[0], v[1], v[2], v[3]);
               }
             }
           }
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(kBarK + b));
+        if (lane == 0) ptx::mbar_arrive(bar(kBarK + kb));
         // ---- V: operand rows are elements. A task is a word (4 code bytes) of 8 keys
-        if (S::kBufs == 1 && turn > 0) fail |= !wait_sleep(kBarV + b, turn - 1, 11);
+        // With one buffer the groups take turns on it, and a parity tells a phase only from the next: the other group's tile
+        // has to be in before its release can be waited for.
+        const unsigned b = it % S::kVBufs, turn = it / S::kVBufs;
+        if (S::kVBufs == 1 && turn > 0) fail |= !wait_sleep(kBarV + b, turn - 1, 11);
         if (turn > 0) fail |= !wait_sleep(kBarVFree + b, turn - 1, 11);
-        uint8_t* const vo = smem + S::kOffV + b * T * S::kOperand;
+        uint8_t* const vo = smem + S::kOffV + b * S::kVPieces * S::kOperand;
 #pragma unroll
         for (int x = 0; x < (8 * S::kWords + kGroup - 1) / kGroup; ++x) {
           const int c = x * kGroup + gt, kg = c / S::kWords, word = c - kg * S::kWords;
@@ -812,14 +818,14 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             float d[8];        // T = 3: the 8 keys' scales of the block
             uint32_t d2[4];    // T = 1: as fp16 pairs
             if (T == 1) {
-              const uint4 r = *reinterpret_cast<const uint4*>(scales + (kTileKeys * NB + blk * kTileKeys + kg * 8) * 2);
+              const uint4 r = *reinterpret_cast<const uint4*>(scales + S::kScaleK + (blk * kTileKeys + kg * 8) * 2);
               d2[0] = r.x;
               d2[1] = r.y;
               d2[2] = r.z;
               d2[3] = r.w;
             } else {
               const float4* const r =
-                  reinterpret_cast<const float4*>(scales + (kTileKeys * NB + blk * kTileKeys + kg * 8) * 4);
+                  reinterpret_cast<const float4*>(scales + S::kScaleK + (blk * kTileKeys + kg * 8) * 4);
               const float4 a = r[0], c4 = r[1];
               d[0] = a.x;
               d[1] = a.y;
