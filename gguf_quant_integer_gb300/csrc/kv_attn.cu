@@ -30,16 +30,16 @@ Pass own_pass(const KvAttnArgs& a) { return {a.batch, a.rows, static_cast<long l
 Pass prefix_pass(const KvAttnArgs& a) { return {1, a.batch * a.rows, a.prefix_len}; }
 
 // Whether a pass goes to the tcgen05 tiles. They take some 20 us whatever the
-// work, and from 64 rows of 16-bit queries (128 of fp32 ones, whose products
-// are six) a fraction of the split kernel's time for it; both measured at
-// rows x keys x KV heads from 0.07 to 67 million (8 heads, dim 128, Q8_0):
-//   bf16  128 rows x 2048 keys 35 and 36 us, x 8192 42 and 61, x 32768 73 and 183
-//         64 rows x 8192 43 and 44 us;  32 rows x 32768 79 and 68
-//   fp32  128 rows x 8192 69 and 73 us, x 32768 145 and 217
-//         64 rows x 32768 152 and 120;  256 rows x 2048 55 and 52
+// work, and then, from 64 rows on, a fraction of the split kernel's time for
+// it. Both measured (tiles, split; 8 KV heads, dim 128, Q8_0, whole calls):
+//   bf16  256 rows x 2048 keys 47 and 48 us; 128 rows x 2048 34 and 36,
+//         x 8192 41 and 61, x 32768 71 and 183; 64 rows x 8192 42 and 44;
+//         32 rows x 32768 77 and 68
+//   fp32  256 rows x 2048 58 and 52, x 8192 86 and 123; 128 rows x 2048 48 and
+//         37, x 8192 64 and 73, x 32768 120 and 217; 64 rows x 32768 117 and 120
 bool tiled(const KvAttnArgs& a, const Pass& p) {
   const bool exact = a.type == kF32;
-  if (a.c.dim > 128 || p.rows < (exact ? 128 : 64)) return false;
+  if (a.c.dim > 128 || p.rows < 64) return false;
   const long long seen = a.window > 0 && p.keys > a.window + a.n_q ? a.window + a.n_q : p.keys;
   return static_cast<double>(p.seqs) * p.rows * seen * a.c.heads >= (exact ? 8e6 : 3e6);
 }

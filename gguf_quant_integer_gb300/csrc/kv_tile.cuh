@@ -53,18 +53,19 @@ struct TileShape {
   static constexpr int kKLbo = kTileKeys / 8 * kSbo, kVLbo = D / 8 * kSbo;
   static constexpr int kOperand = D * kSbo;  // one piece of K or of V: 64 keys x dim
   static constexpr int kKPieces = T == 1 ? 1 : 2, kVPieces = T;  // fp16 ones of q and K, those of the weights and V
-  static constexpr int kKBufs = 2, kVBufs = T == 1 ? 2 : 1;
+  static constexpr int kBufs = 2;  // of K and of V
   static constexpr int kTiles = T == 1 ? 2 : 1;  // row tiles
   static constexpr int kRows = kTiles * kTileRows;
   static constexpr int kSoftWarps = kTileSoft / kTiles;  // of a row tile
   static constexpr int kRawCodes = kTileKeys * kRow, kRawScales = kTileKeys * NB * 2;
   static constexpr int kRaw = 2 * (kRawCodes + kRawScales);
-  static constexpr int kRawStages = 4;  // two of each group of unpacking warps
-  static constexpr int kOffV = kKBufs * kKPieces * kOperand, kOffRaw = kOffV + kVBufs * kVPieces * kOperand;
+  static constexpr int kOffV = kBufs * kKPieces * kOperand, kOffRaw = kOffV + kBufs * kVPieces * kOperand;
   // The tile's scales, ready for use: K's [64][NB] fp16, V's [NB][64] fp16 or (T = 3) fp32.
   static constexpr int kScaleK = kTileKeys * NB * 2;
-  static constexpr int kOffScale = kOffRaw + kRawStages * kRaw;
   static constexpr int kScales = kScaleK + kTileKeys * NB * (T == 1 ? 2 : 4);  // a table for each group
+  // Raw stages of a group of unpacking warps: two, or the one that the pieces of Q8_0 at dim 128 leave room for.
+  static constexpr int kRawStages = kOffRaw + 4 * kRaw + 2 * kScales <= 227 * 1024 - 1536 ? 2 : 1;
+  static constexpr int kOffScale = kOffRaw + 2 * kRawStages * kRaw;
   static constexpr int kSmem = kOffScale + 2 * kScales;
   // Tensor memory columns: queries (of two row tiles, or two pieces), scores (of two row tiles, or two buffers), weights,
   // outputs. With two row tiles the weights take the scores' columns, which the row's thread has read by then.
@@ -72,7 +73,7 @@ struct TileShape {
   static constexpr int kColO = T == 1 ? kColS + 2 * kTileKeys : kColP + T * kTileKeys / 2;
   static constexpr int kCols = kColO + kTiles * D;
   static constexpr int kAlloc = kCols <= 256 ? 256 : 512;
-  static_assert(kCols <= 512 && kSmem <= 227 * 1024, "one CTA fits the SM");
+  static_assert(kCols <= 512 && kSmem <= 227 * 1024 - 1536, "one CTA fits the SM");  // and its static shared memory
 };
 
 template <int D>
@@ -117,25 +118,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // Two floats' bf16 pieces by cutting off, each pair packed (a in the low half).
-__device__ __forceinline__ void cut3(float a, float b, uint32_t (&w)[3]) {
-  const uint32_t a1 = __float_as_uint(a) & 0xFFFF0000u, b1 = __float_as_uint(b) & 0xFFFF0000u;
-  const float ra = a - __uint_as_float(a1), rb = b - __uint_as_float(b1);
-  const uint32_t a2 = __float_as_uint(ra) & 0xFFFF0000u, b2 = __float_as_uint(rb) & 0xFFFF0000u;
-  const float sa = ra - __uint_as_float(a2), sb = rb - __uint_as_float(b2);
-  w[0] = prmt(a1, b1, 0x7632u);
-  w[1] = prmt(a2, b2, 0x7632u);
-  w[2] = prmt(__float_as_uint(sa), __float_as_uint(sb), 0x7632u);
+__device__ __forceinline__ void cut3(ptx::f2 v, uint32_t (&w)[3]) {
+  const ptx::f2 minus = ptx::pk(-1.0f, -1.0f);
+  const uint32_t a = __float_as_uint(ptx::lo32(v)), b = __float_as_uint(ptx::hi32(v));
+  const ptx::f2 r = ptx::fma2(ptx::pk(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u)), minus, v);
+  const uint32_t c = __float_as_uint(ptx::lo32(r)), d = __float_as_uint(ptx::hi32(r));
+  const ptx::f2 s = ptx::fma2(ptx::pk(__uint_as_float(c & 0xFFFF0000u), __uint_as_float(d & 0xFFFF0000u)), minus, r);
+  w[0] = prmt(a, b, 0x7632u);
+  w[1] = prmt(c, d, 0x7632u);
+  w[2] = prmt(__float_as_uint(ptx::lo32(s)), __float_as_uint(ptx::hi32(s)), 0x7632u);
 }
 
-// Four code bytes u as floats u - 128 (BITS = 8) or nibble bytes as u - 8.
-template <int BITS>
-__device__ __forceinline__ void code_floats(uint32_t w, float (&f)[4]) {
-  constexpr float off = BITS == 8 ? 8388736.0f : 8388616.0f;  // 2^23 + 128, 2^23 + 8
-  f[0] = __uint_as_float(prmt(w, 0x4B000000u, 0x7440u)) - off;
-  f[1] = __uint_as_float(prmt(w, 0x4B000000u, 0x7441u)) - off;
-  f[2] = __uint_as_float(prmt(w, 0x4B000000u, 0x7442u)) - off;
-  f[3] = __uint_as_float(prmt(w, 0x4B000000u, 0x7443u)) - off;
-}
 // Bytes (0, 1) and (2, 3) of w as fp16 pairs u - 128 or u - 8.
 template <int BITS>
 __device__ __forceinline__ void code_halves(uint32_t w, uint32_t (&h)[2]) {
@@ -205,8 +198,8 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       unsigned it = 0, done[2] = {0u, 0u}, parts[2] = {0u, 0u};  // tiles so far; of each row tile
       // Row tile r's scores of tile i; last: of the part's row tiles.
       auto scores = [&](int r, unsigned i, bool last) {
-        const unsigned b = i % S::kKBufs;
-        if (r == 0 && !wait(kBarK + b, i / S::kKBufs, 1)) return false;
+        const unsigned b = i % S::kBufs;
+        if (r == 0 && !wait(kBarK + b, i / S::kBufs, 1)) return false;
         ptx::tc_fence_after();
         const int to = T == 1 ? r : static_cast<int>(i & 1);  // row tile, or buffer
 #pragma unroll
@@ -227,10 +220,10 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         for (int r = 0; r <= last && ok; ++r) ok = wait(kBarQ + r, parts[r]++, 2) && scores(r, it, r == last);
         if (kAhead == 2 && ok && tiles > 1) ok = scores(0, it + 1, true);
         for (int i = 0; i < tiles && ok; ++i, ++it) {
-          const unsigned b = it % S::kVBufs;
+          const unsigned b = it % S::kBufs;
           for (int r = 0; r <= last && ok; ++r) {
             ok = wait(kBarP + r, done[r]++, 3);
-            if (r == 0) ok = ok && wait(kBarV + b, it / S::kVBufs, 4);
+            if (r == 0) ok = ok && wait(kBarV + b, it / S::kBufs, 4);
             if (!ok) break;
             ptx::tc_fence_after();
 #pragma unroll
@@ -537,7 +530,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           const float a = ex2(ptx::lo32(z)), d = ex2(ptx::hi32(z));
           l = ptx::add2(l, ptx::pk(a, d));
           uint32_t u[3];
-          cut3(a, d, u);
+          cut3(ptx::pk(a, d), u);
           w[0][x / 2] = u[0];
           w[1][x / 2] = u[1];
           w[2][x / 2] = u[2];
@@ -707,7 +700,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       unsigned miss = 0, next_miss = 0;  // 16-key groups without a valid page: of this tile, of the one on its way
       auto issue = [&](int i, int stage) {
         if (i < tiles) {
-          const uint32_t to = base + S::kOffRaw + (2 * group + stage) * S::kRaw;
+          const uint32_t to = base + S::kOffRaw + (S::kRawStages * group + stage) * S::kRaw;
           const int gi0 = (unit0 + i) * 4;
           const bool there = static_cast<unsigned>(next_id) < static_cast<unsigned>(A.c.n_pages);
           if (!there && gi0 + (lane & 3) < groups) kv_record(kKvBadPage);
@@ -741,14 +734,14 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       uint8_t* const scales = smem + S::kOffScale + group * S::kScales;
       const unsigned it0 = it;
       issue(group, 0);
-      for (int i = group, stage = 0; i < tiles; i += 2, stage ^= 1) {
+      for (int i = group, stage = 0; i < tiles; i += 2, stage ^= S::kRawStages - 1) {
         it = it0 + i;
         cp_wait<0>();
         // every thread's copies of this tile have landed, and the group's last tile has been unpacked
         if (group_any(kBarrier + 1 + group, kGroup, fail)) break;
         miss = next_miss;
-        issue(i + 2, stage ^ 1);
-        const uint8_t* const raw = smem + S::kOffRaw + (2 * group + stage) * S::kRaw;
+        if (S::kRawStages == 2) issue(i + 2, stage ^ 1);
+        const uint8_t* const raw = smem + S::kOffRaw + (S::kRawStages * group + stage) * S::kRaw;
         const int left = part.n - (unit0 + i) * kTileKeys;  // keys of the sequence from the tile's first on
         // ---- scales: scaled, and 0 for keys that are not there (whose codes may be anything)
         for (int x = gt; x < kTileKeys * NB; x += kGroup) {
@@ -767,10 +760,10 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         }
         group_any(kBarrier + 1 + group, kGroup, false);
         // ---- K: operand rows are keys. A task is a key's 16-byte chunk
-        const unsigned kb = it % S::kKBufs, kturn = it / S::kKBufs;
-        if (kturn > 0) fail |= !wait_sleep(kBarKFree + kb, kturn - 1, 10);
+        const unsigned b = it % S::kBufs, turn = it / S::kBufs;  // tiles take the buffers, and the groups the tiles, in turn
+        if (turn > 0) fail |= !wait_sleep(kBarKFree + b, turn - 1, 10);
         if (gt == 0) sh_bad[it & 3] = miss;
-        uint8_t* const ko = smem + kb * S::kKPieces * S::kOperand;
+        uint8_t* const ko = smem + b * S::kKPieces * S::kOperand;
 #pragma unroll
         for (int x = 0; x < (kTileKeys * S::kChunks + kGroup - 1) / kGroup; ++x) {
           const int c = x * kGroup + gt, key = c & (kTileKeys - 1), ch = c / kTileKeys;
@@ -801,12 +794,8 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(kBarK + kb));
+        if (lane == 0) ptx::mbar_arrive(bar(kBarK + b));
         // ---- V: operand rows are elements. A task is a word (4 code bytes) of 8 keys
-        // With one buffer the groups take turns on it, and a parity tells a phase only from the next: the other group's tile
-        // has to be in before its release can be waited for.
-        const unsigned b = it % S::kVBufs, turn = it / S::kVBufs;
-        if (S::kVBufs == 1 && turn > 0) fail |= !wait_sleep(kBarV + b, turn - 1, 11);
         if (turn > 0) fail |= !wait_sleep(kBarVFree + b, turn - 1, 11);
         uint8_t* const vo = smem + S::kOffV + b * S::kVPieces * S::kOperand;
 #pragma unroll
@@ -872,8 +861,10 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
 #pragma unroll
                   for (int k = 0; k < 8; k += 2) {
                     const uint32_t sel = 0x7440u + y;
-                    cut3((__uint_as_float(prmt(v[k], 0x4B000000u, sel)) - off) * d[k],
-                         (__uint_as_float(prmt(v[k + 1], 0x4B000000u, sel)) - off) * d[k + 1], r[k / 2]);
+                    const ptx::f2 u2 = ptx::add2(ptx::pk(__uint_as_float(prmt(v[k], 0x4B000000u, sel)),
+                                                         __uint_as_float(prmt(v[k + 1], 0x4B000000u, sel))),
+                                                 ptx::pk(-off, -off));
+                    cut3(ptx::mul2(u2, ptx::pk(d[k], d[k + 1])), r[k / 2]);
                   }
 #pragma unroll
                   for (int p = 0; p < 3; ++p)
@@ -886,6 +877,10 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(kBarV + b));
+        if (S::kRawStages == 1) {  // every thread has read the tile
+          group_any(kBarrier + 1 + group, kGroup, false);
+          issue(i + 2, 0);
+        }
       }
       cp_wait<0>();
       it = it0 + tiles;

@@ -333,7 +333,7 @@ def test_repeated_calls_agree_bit_for_bit(xq):
             assert torch.equal(cache.attn_shared(q, pre, 789, table, lens), s)
 
 
-# Enough rows x keys for the tcgen05 tiles: 3 million a call for 16-bit queries (64 rows or more), 8 million for fp32 ones (128).
+# Enough rows x keys x KV heads for the tcgen05 tiles: 3 million a call for 16-bit queries, 8 million for fp32 ones (64 rows or more).
 
 @pytest.mark.parametrize("kind,dtype,heads,group,dim,page,n_q,prefix,lens", [
     ("q8", "bf16", 2, 4, 128, 64, 1, 3001, [1 + i % 9 for i in range(128)]),
