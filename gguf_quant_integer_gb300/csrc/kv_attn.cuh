@@ -1009,19 +1009,21 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
 
 // The parts of the pairs that begin in CTAs blockIdx.x, + gridDim.x, ..., RB of their R rows from RB * blockIdx.y on. A
 // thread holds one float4 of the rows; each team of threads takes every kTeams-th part, several loads at a time, then the
-// teams are merged.
-constexpr int kJoinThreads = 512;
-template <int D, int R, int RB>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ SplitArgs A) {
+// teams are merged. COLS: the parts' outputs are stored [dim / 4][R], not [R][dim / 4].
+// Two blocks an SM, with 6 loads in flight a thread (one block with 8: 64 sequences of 211 to 8192 tokens 85.8 us instead
+// of 83.9, a prefix of 32768 tokens for 64 sequences 96.6 instead of 91.6; three with 2 to 4 help or cost as much).
+constexpr int kJoinThreads = 512, kJoinBlocks = 2, kJoinBatch = 6;
+template <int D, int R, int RB, bool COLS>
+__global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) kv_join_kernel(const __grid_constant__ SplitArgs A) {
   constexpr int kLanes = RB * D / 4;
   constexpr int kTeams = kJoinThreads / kLanes;
-  constexpr int kBatch = 8;
   static_assert(kTeams >= 1, "a part's rows are one pass of the block");
   __shared__ float2 sel[kTeams][RB];
   __shared__ float4 so[kTeams][kLanes];
   grid_wait();
   const int tid = threadIdx.x, lane = tid & 31;
-  const int team = tid / kLanes, at = tid - team * kLanes, r = at / (D / 4), d = (at - r * (D / 4)) * 4;
+  const int team = tid / kLanes, at = tid - team * kLanes;
+  const int r = COLS ? at % RB : at / (D / 4), d = (COLS ? at / RB : at % (D / 4)) * 4;
   const int row = RB * blockIdx.y + r;
   int4 mine = make_int4(0, 0, -1, 0);  // the records, one a lane
   const int c = blockIdx.x + lane * gridDim.x;
@@ -1035,29 +1037,29 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_cons
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const bool live = team < kTeams && pair_row < A.rows;
     if (live) {
-      for (int base = team; base < parts; base += kTeams * kBatch) {
-        float2 el[kBatch];
-        float4 z[kBatch];
+      for (int base = team; base < parts; base += kTeams * kJoinBatch) {
+        float2 el[kJoinBatch];
+        float4 z[kJoinBatch];
         float top = e;
 #pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
+        for (int x = 0; x < kJoinBatch; ++x) {
           const int i = base + x * kTeams;
           if (i < parts) {
             // part i: the second slot of the CTA where the pair begins, the first of those after it
             const size_t slot = (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * R + row;
             el[x] = *reinterpret_cast<const float2*>(A.part_el + slot * 2);
-            z[x] = *reinterpret_cast<const float4*>(A.part_o + slot * D + d);
+            z[x] = *reinterpret_cast<const float4*>(A.part_o + (COLS ? (slot - row) * D + d * R + row * 4 : slot * D + d));
           }
         }
 #pragma unroll
-        for (int x = 0; x < kBatch; ++x)
+        for (int x = 0; x < kJoinBatch; ++x)
           if (base + x * kTeams < parts) top = fmaxf(top, el[x].x);
         const float keep = ex2(e - top);
         o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
         l *= keep;
         e = top;
 #pragma unroll
-        for (int x = 0; x < kBatch; ++x)
+        for (int x = 0; x < kJoinBatch; ++x)
           if (base + x * kTeams < parts) {
             const float f = ex2(el[x].x - top);
             o = make_float4(fmaf(z[x].x, f, o.x), fmaf(z[x].y, f, o.y), fmaf(z[x].z, f, o.z), fmaf(z[x].w, f, o.w));
@@ -1119,7 +1121,7 @@ cudaError_t launch_split(SplitArgs& a, cudaStream_t s) {
   cfg.gridDim = join_grid<S::R, S::R>(a.ctas);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, S::R, S::R>, a);
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, S::R, S::R, false>, a);
 }
 
 }  // namespace

@@ -89,7 +89,8 @@ namespace {
 __device__ unsigned int g_kv_tile_error;  // a wait that ran out
 constexpr long long kTileWait = 1ll << 32;
 
-// Barriers: of each row tile (Q, S, P, O) and of each operand buffer, as a barrier's parity tells a phase only from the next.
+// Barriers: of each row tile (Q), of each scores buffer (S; T = 1: P and O, its weights and their products) and of each
+// operand buffer, as a barrier's parity tells a phase only from the next.
 enum TileBar { kBarDrain, kBarQ, kBarS = kBarQ + 2, kBarP = kBarS + 2, kBarO = kBarP + 2, kBarK = kBarO + 2, kBarKFree = kBarK + 2,
                kBarV = kBarKFree + 2, kBarVFree = kBarV + 2, kBars = kBarVFree + 2 };
 
@@ -104,6 +105,7 @@ __device__ __forceinline__ bool group_any(int id, int threads, bool p) {
   return r != 0;
 }
 
+// Loads and stores of tensor memory are a whole warp's: __syncwarp() where its threads may have parted.
 // 32 lanes x 8 consecutive columns (the first 8 words of v).
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
@@ -182,73 +184,92 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
     return ptx::mbar_wait_sleep(bar(i), parity & 1, &g_kv_tile_error, code, kTileWait);
   };
   const uint32_t base = ptx::smem_addr(smem);
+  // Two buffers of scores: of the two row tiles, or taken in turn by the only one. The buffer of row tile r's n-th tile, and
+  // how often it was used before.
+  const bool two = S::kTiles == 2 && A.rows > kTileRows;
+  auto buffer = [&](int r, unsigned n) { return two ? r : static_cast<int>(n & 1); };
+  auto turn = [&](unsigned n) { return two ? n : n >> 1; };
   Part part;
 
   if (warp == kTileWarps - 1) {
-    // ------------------------------------------------ products (one thread)
-    if (lane == 0) {
-      constexpr uint32_t idS = ptx::idesc_f16(kTileRows, kTileKeys, false), idO = ptx::idesc_f16(kTileRows, D, T == 3);
-      // pairs of pieces (A's, B's)
-      constexpr int kSPairs = T == 3 ? 3 : 1, kOPairs = T == 3 ? 6 : 1;
-      constexpr int sa[3] = {0, 0, 1}, sb[3] = {0, 1, 0};
-      constexpr int oa[6] = {0, 0, 1, 0, 1, 2}, ob[6] = {0, 1, 0, 2, 1, 0};
-      // Scores are computed this many tiles ahead of the outputs.
-      constexpr int kAhead = T == 1 ? 1 : 2;
-      bool ok = true;
-      unsigned it = 0, done[2] = {0u, 0u}, parts[2] = {0u, 0u};  // tiles so far; of each row tile
-      // Row tile r's scores of tile i; last: of the part's row tiles.
-      auto scores = [&](int r, unsigned i, bool last) {
-        const unsigned b = i % S::kBufs;
-        if (r == 0 && !wait(kBarK + b, i / S::kBufs, 1)) return false;
-        ptx::tc_fence_after();
-        const int to = T == 1 ? r : static_cast<int>(i & 1);  // row tile, or buffer
+    // ------------------------------------------------ products (issued by one thread). The whole warp walks through the tiles,
+    // so that the operands' addresses are its uniform values when the thread comes to the products: one a product, added to
+    // a tile's descriptor, not built anew (77 clocks a product otherwise, more than the 32 to 64 it takes).
+    constexpr uint32_t idS = ptx::idesc_f16(kTileRows, kTileKeys, false), idO = ptx::idesc_f16(kTileRows, D, T == 3);
+    // pairs of pieces (A's, B's)
+    constexpr int kSPairs = T == 3 ? 3 : 1, kOPairs = T == 3 ? 6 : 1;
+    constexpr int sa[3] = {0, 0, 1}, sb[3] = {0, 1, 0};
+    constexpr int oa[6] = {0, 0, 1, 0, 1, 2}, ob[6] = {0, 1, 0, 2, 1, 0};
+    // Scores are computed this many tiles ahead of the outputs.
+    const unsigned ahead = two ? 1 : 2;
+    const bool lead = ptx::elect_one();
+    const uint64_t k_desc = ptx::smem_desc(base, S::kKLbo, S::kSbo), v_desc = ptx::smem_desc(base + S::kOffV, S::kVLbo, S::kSbo);
+    const uint32_t at = __shfl_sync(0xffffffffu, tmem, 0);
+    auto wait_all = [&](int i, unsigned parity, unsigned code) { return __all_sync(0xffffffffu, wait(i, parity, code)) != 0; };
+    bool ok = true;
+    unsigned it = 0, scored[2] = {0u, 0u}, done[2] = {0u, 0u}, parts[2] = {0u, 0u};  // tiles so far; of each row tile
+    // Row tile r's scores of tile i; last: of the part's row tiles.
+    auto scores = [&](int r, unsigned i, bool last) {
+      const unsigned b = i % S::kBufs;
+      if (r == 0 && !wait_all(kBarK + b, i / S::kBufs, 1)) return false;
+      ptx::tc_fence_after();
+      const int to = buffer(r, scored[r]++);
+      const uint32_t d = __shfl_sync(0xffffffffu, at + S::kColS + to * kTileKeys, 0);
+      const uint32_t a = __shfl_sync(0xffffffffu, at + r * (D / 2), 0);
+      const uint64_t kd = k_desc + __shfl_sync(0xffffffffu, b * (S::kKPieces * S::kOperand / 16), 0);
+      if (lead) {
 #pragma unroll
         for (int p = 0; p < kSPairs; ++p)
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            ptx::mma_f16_ts(tmem + S::kColS + to * kTileKeys, tmem + (r + sa[p]) * (D / 2) + 8 * k,
-                            ptx::smem_desc(base + (b * S::kKPieces + sb[p]) * S::kOperand + 2 * k * S::kKLbo, S::kKLbo, S::kSbo),
-                            idS, p + k > 0);
+            ptx::mma_f16_ts(d, a + sa[p] * (D / 2) + 8 * k, kd + (sb[p] * S::kOperand + 2 * k * S::kKLbo) / 16, idS, p + k > 0);
         if (last) ptx::tc_commit(bar(kBarKFree + b));
         ptx::tc_commit(bar(kBarS + to));
-        return true;
-      };
-      while (ok && line_next(A, line, part)) {
-        const int tiles = part.k1 - part.k0;
-        const int chunk = part.pair % A.chunks;
-        const int last = S::kTiles == 2 && A.rows - chunk * S::kRows > kTileRows ? 1 : 0;
-        for (int r = 0; r <= last && ok; ++r) ok = wait(kBarQ + r, parts[r]++, 2) && scores(r, it, r == last);
-        if (kAhead == 2 && ok && tiles > 1) ok = scores(0, it + 1, true);
-        for (int i = 0; i < tiles && ok; ++i, ++it) {
-          const unsigned b = it % S::kBufs;
-          for (int r = 0; r <= last && ok; ++r) {
-            ok = wait(kBarP + r, done[r]++, 3);
-            if (r == 0) ok = ok && wait(kBarV + b, it / S::kBufs, 4);
-            if (!ok) break;
-            ptx::tc_fence_after();
+      }
+      __syncwarp();
+      return true;
+    };
+    while (ok && line_next(A, line, part)) {
+      const int tiles = part.k1 - part.k0;
+      const int chunk = part.pair % A.chunks;
+      const int last = S::kTiles == 2 && A.rows - chunk * S::kRows > kTileRows ? 1 : 0;
+      for (int r = 0; r <= last && ok; ++r) ok = wait_all(kBarQ + r, parts[r]++, 2) && scores(r, it, r == last);
+      if (ahead == 2 && ok && tiles > 1) ok = scores(0, it + 1, true);
+      for (int i = 0; i < tiles && ok; ++i, ++it) {
+        const unsigned b = it % S::kBufs;
+        for (int r = 0; r <= last && ok; ++r) {
+          const int from = T == 1 ? buffer(r, done[r]) : 0;  // the weights'
+          ok = wait_all(kBarP + from, T == 1 ? turn(done[r]) : done[r], 3);
+          ++done[r];
+          if (r == 0) ok = ok && wait_all(kBarV + b, it / S::kBufs, 4);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t d = __shfl_sync(0xffffffffu, at + S::kColO + r * D, 0);
+          const uint32_t a = __shfl_sync(0xffffffffu, at + S::kColP + from * kTileKeys, 0);
+          const uint64_t vd = v_desc + __shfl_sync(0xffffffffu, b * (S::kVPieces * S::kOperand / 16), 0);
+          if (lead) {
 #pragma unroll
             for (int p = 0; p < kOPairs; ++p)
 #pragma unroll
               for (int k = 0; k < kTileKeys / 16; ++k)
-                ptx::mma_f16_ts(tmem + S::kColO + r * D, tmem + S::kColP + r * kTileKeys + oa[p] * (kTileKeys / 2) + 8 * k,
-                                ptx::smem_desc(base + S::kOffV + (b * S::kVPieces + ob[p]) * S::kOperand + 2 * k * S::kVLbo,
-                                               S::kVLbo, S::kSbo),
-                                idO, i > 0 || p + k > 0);
+                ptx::mma_f16_ts(d, a + oa[p] * (kTileKeys / 2) + 8 * k, vd + (ob[p] * S::kOperand + 2 * k * S::kVLbo) / 16, idO,
+                                i > 0 || p + k > 0);
             if (r == last) ptx::tc_commit(bar(kBarVFree + b));
-            ptx::tc_commit(bar(kBarO + r));
-            if (i + kAhead < tiles) ok = scores(r, it + kAhead, r == last);
+            ptx::tc_commit(bar(kBarO + from));
           }
+          __syncwarp();
+          if (i + static_cast<int>(ahead) < tiles) ok = scores(r, it + ahead, r == last);
         }
       }
-      ptx::tc_commit(bar(kBarDrain));  // nothing is in flight when tensor memory is freed
-      wait(kBarDrain, 0, 5);
     }
+    if (lead) ptx::tc_commit(bar(kBarDrain));  // nothing is in flight when tensor memory is freed
+    wait(kBarDrain, 0, 5);
   } else if (T == 1 && warp < kTileSoft) {
     // ------------------------- softmax, two row tiles: a thread is a row; no thread needs another
     constexpr float kTop = 15.0f, kStart = 11.0f;  // log2 of weights: the largest, and where the reference starts anew
     const int r = warp >> 2, row = r * kTileRows + (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t ts = tl + S::kColS + r * kTileKeys, to = tl + S::kColO + r * D;
+    const uint32_t to = tl + S::kColO + r * D;
     unsigned it = 0, done = 0, parts = 0;
     bool ok = true, left_record = false;
     for (; ok && line_next(A, line, part); ++parts) {
@@ -294,6 +315,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           w[4 * x + 2] = half2_of(g.x * up, g.y * up);
           w[4 * x + 3] = half2_of(d.x * up, d.y * up);
         }
+        __syncwarp();
         ptx::tmem_st16(tl + r * (D / 2) + c, w);
       }
       ptx::tmem_wait_st();
@@ -304,19 +326,27 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       int key = (first_unit(A, part.n) + part.k0) * kTileKeys;
       float e = -1e30f;
       ptx::f2 l = ptx::pk(0.0f, 0.0f);
+      unsigned vx = 0;  // exponents of V's powers of two, 8 bits a block
       for (int i = 0; i < tiles; ++i, ++it, ++done, key += kTileKeys) {
-        ok = __all_sync(0xffffffffu, wait(kBarS + r, done, 6));
+        ok = __all_sync(0xffffffffu, wait(kBarS + buffer(r, done), turn(done), 6));
         if (!ok) break;
         ptx::tc_fence_after();
-        if (i == 0) {  // K's power of two, known once its first tile is there
-          const unsigned t0 = sh_top[parts & 3][0];
-          cs = fmaxf(cs * __uint_as_float((t0 >> 23 < 253 ? (t0 >> 23) + 1 : 254u) << 23), 1.17549435e-38f);
+        const uint32_t ts = tl + S::kColS + buffer(r, done) * kTileKeys;
+        if (i == 0) {  // the part's powers of two, known once its first tile is there (and until its weights are)
+          auto power = [&](int x) {
+            const unsigned t0 = sh_top[parts & 3][x] >> 23;
+            return t0 < 253 ? t0 + 1 : 254u;
+          };
+          cs = fmaxf(cs * __uint_as_float(power(0) << 23), 1.17549435e-38f);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) vx |= power(1 + b) << (8 * b);
         }
         const unsigned bad = sh_bad[it & 3];
         const bool edge = key < lim0 || key + kTileKeys > lim1 || bad;
         uint32_t sv[2][16];
         // 32 scores from column c on, those that the row does not see as -infinity
         auto load = [&](int c) {
+          __syncwarp();
           ptx::tmem_ld16(ts + c, sv[0]);
           ptx::tmem_ld16(ts + c + 16, sv[1]);
           ptx::tmem_wait_ld();
@@ -343,7 +373,10 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           const float next = tile_top - e > kTop ? tile_top - kStart : e, f = ex2(e - next);
           e = next;
           l = ptx::mul2(l, ptx::pk(f, f));
-          if (i > 0) {  // these scores' products came after the outputs' last ones
+          if (i > 0) {
+            ok = __all_sync(0xffffffffu, wait(kBarO + buffer(r, done - 1), turn(done - 1), 7));
+            if (!ok) break;
+            ptx::tc_fence_after();
 #pragma unroll
             for (int c = 0; c < D; c += 16) {
               uint32_t w[16];
@@ -368,16 +401,17 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             l = ptx::add2(l, ptx::pk(a, d));
             w[x / 2] = half2_of(a, d);
           }
+          __syncwarp();
           ptx::tmem_st16(ts + 16 * h, w);  // into columns already read
         }
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(kBarP + r));
+        if (lane == 0) ptx::mbar_arrive(bar(kBarP + buffer(r, done)));
       }
       if (!ok) break;
       // ---- the part's results
-      ok = __all_sync(0xffffffffu, wait_sleep(kBarO + r, done - 1, 9));
+      ok = __all_sync(0xffffffffu, wait_sleep(kBarO + buffer(r, done - 1), turn(done - 1), 9));
       if (!ok) break;
       ptx::tc_fence_after();
       const float sum = ptx::lo32(l) + ptx::hi32(l);
@@ -387,10 +421,10 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
 #pragma unroll
       for (int c = 0; c < D; c += 16) {
         uint32_t w[16];
+        __syncwarp();
         ptx::tmem_ld16(to + c, w);
         ptx::tmem_wait_ld();
-        const unsigned t0 = sh_top[parts & 3][1 + c / 32];
-        const float f = __uint_as_float((t0 >> 23 < 253 ? (t0 >> 23) + 1 : 254u) << 23);
+        const float f = __uint_as_float((vx >> (8 * (c / 32)) & 0xFFu) << 23);
         if (live) {
 #pragma unroll
           for (int x = 0; x < 16; x += 4) {
@@ -399,7 +433,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             if (whole)
               finish4(A, D, at, c + x, y, e, sum);
             else
-              *reinterpret_cast<float4*>(A.part_o + slot * D + c + x) = y;
+              *reinterpret_cast<float4*>(A.part_o + (slot - row) * D + (c + x) * S::kRows + row * 4) = y;
           }
         }
       }
@@ -457,6 +491,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           w[1][2 * x] = half2_of(v.x - f0.x, v.y - f0.y);
           w[1][2 * x + 1] = half2_of(v.z - f1.x, v.w - f1.y);
         }
+        __syncwarp();
 #pragma unroll
         for (int p = 0; p < 2; ++p) tmem_st8(tl + p * (D / 2) + half * (D / 4) + c, w[p]);
       }
@@ -477,6 +512,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           cs = fmaxf(cs * __uint_as_float((t0 >> 23 < 253 ? (t0 >> 23) + 1 : 254u) << 23), 1.17549435e-38f);
         }
         uint32_t sv[2][16];
+        __syncwarp();
         ptx::tmem_ld16(tl + S::kColS + (it & 1) * kTileKeys + half * 32, sv[0]);
         ptx::tmem_ld16(tl + S::kColS + (it & 1) * kTileKeys + half * 32 + 16, sv[1]);
         ptx::tmem_wait_ld();
@@ -513,6 +549,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
 #pragma unroll
             for (int c = 0; c < D / 2; c += 16) {
               uint32_t w[16];
+              __syncwarp();
               ptx::tmem_ld16(tl + S::kColO + half * (D / 2) + c, w);
               ptx::tmem_wait_ld();
 #pragma unroll
@@ -540,6 +577,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           fail |= !wait(kBarO, it - 1, 8);
           ptx::tc_fence_after();
         }
+        __syncwarp();
 #pragma unroll
         for (int p = 0; p < 3; ++p) ptx::tmem_st16(tl + S::kColP + p * (kTileKeys / 2) + half * 16, w[p]);
         ptx::tmem_wait_st();
@@ -562,6 +600,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       for (int c = 0; c < D / 2; c += 16) {
         uint32_t w[16];
         const int d0 = half * (D / 2) + c;
+        __syncwarp();
         ptx::tmem_ld16(tl + S::kColO + d0, w);
         ptx::tmem_wait_ld();
         if (live) {
@@ -572,7 +611,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             if (whole) {
               finish4(A, D, at, d0 + x, y, e, sum);
             } else {
-              *reinterpret_cast<float4*>(A.part_o + slot * D + d0 + x) = y;
+              *reinterpret_cast<float4*>(A.part_o + (slot - row) * D + (d0 + x) * S::kRows + row * 4) = y;
               if (d0 + x == 0) *reinterpret_cast<float2*>(A.part_el + slot * 2) = make_float2(e, sum);
             }
           }
@@ -923,7 +962,7 @@ cudaError_t launch_tile_attn(SplitArgs& a, cudaStream_t s) {
   cfg.gridDim = join_grid<S::kRows, kRowsBlock>(a.ctas);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, S::kRows, kRowsBlock>, a);
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, S::kRows, kRowsBlock, true>, a);
 }
 
 }  // namespace

@@ -110,6 +110,12 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
   return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
          (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46);
 }
+// True in one thread of a whole warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  unsigned ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(ok));
+  return ok != 0;
+}
 // Instruction descriptor of kind::f16: fp32 accumulator, A and B both fp16
 // (bf16 = false) or both bf16, both K-major, shape M x N.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool bf16) {
