@@ -47,11 +47,12 @@ template <int BITS, int D, int T>
 struct TileShape {
   static constexpr int NB = D / 32;
   static constexpr int kRow = D * BITS / 8, kChunks = kRow / 16, kWords = kRow / 4;
-  // Operands in 8 x 16-byte core matrices. Neighbours in N are 144 bytes
-  // apart, so that the unpacking warps' 16-byte stores spread over the banks.
+  // Operands in 8 x 16-byte core matrices. Neighbours in N are 144 bytes apart, K's in K 16 more than 8 of those, so that
+  // the unpacking warps' 16-byte stores spread over the banks.
   static constexpr int kSbo = 144;
-  static constexpr int kKLbo = kTileKeys / 8 * kSbo, kVLbo = D / 8 * kSbo;
-  static constexpr int kOperand = D * kSbo;  // one piece of K or of V: 64 keys x dim
+  static constexpr int kKLbo = kTileKeys / 8 * kSbo + 16, kVLbo = D / 8 * kSbo;
+  static constexpr int kOperand = D / 8 * kKLbo;  // one piece of K or of V: 64 keys x dim
+  static_assert(kOperand >= kTileKeys / 8 * kVLbo && kOperand % 16 == 0, "V's is the smaller");
   static constexpr int kKPieces = T == 1 ? 1 : 2, kVPieces = T;  // fp16 ones of q and K, those of the weights and V
   static constexpr int kBufs = 2;  // of K and of V
   static constexpr int kTiles = T == 1 ? 2 : 1;  // row tiles
@@ -90,9 +91,9 @@ __device__ unsigned int g_kv_tile_error;  // a wait that ran out
 constexpr long long kTileWait = 1ll << 32;
 
 // Barriers: of each row tile (Q), of each scores buffer (S; T = 1: P and O, its weights and their products) and of each
-// operand buffer, as a barrier's parity tells a phase only from the next.
+// operand buffer and raw stage, as a barrier's parity tells a phase only from the next.
 enum TileBar { kBarDrain, kBarQ, kBarS = kBarQ + 2, kBarP = kBarS + 2, kBarO = kBarP + 2, kBarK = kBarO + 2, kBarKFree = kBarK + 2,
-               kBarV = kBarKFree + 2, kBarVFree = kBarV + 2, kBars = kBarVFree + 2 };
+               kBarV = kBarKFree + 2, kBarVFree = kBarV + 2, kBarRaw = kBarVFree + 2, kBars = kBarRaw + 4 };
 
 // Barrier of `threads` threads that gives the or of their predicates.
 __device__ __forceinline__ bool group_any(int id, int threads, bool p) {
@@ -162,6 +163,8 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       ptx::mbar_init(bar(kBarKFree + b), 1);
       ptx::mbar_init(bar(kBarV + b), kTileConv / 2);
       ptx::mbar_init(bar(kBarVFree + b), 1);
+      ptx::mbar_init(bar(kBarRaw + b), 1);
+      ptx::mbar_init(bar(kBarRaw + 2 + b), 1);
     }
     ptx::mbar_init(bar(kBarDrain), 1);
     ptx::mbar_init_fence();
@@ -632,7 +635,9 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
     // Two groups of four warps, each a tile: one's copies and barriers pass while the other unpacks.
     constexpr int kThreads = 32 * kTileConv, kGroup = kThreads / 2, kBarrier = 2;
     const int ct = tid - 32 * kTileSoft, group = ct / kGroup, gt = ct - group * kGroup;
-    const int groups_page = 1 << (A.c.page_shift - 4);  // 16-key groups a page
+    const int group_shift = A.c.page_shift - 4, groups_page = 1 << group_shift;  // 16-key groups a page
+    const int run = groups_page < 4 ? groups_page : 4;                          // those of a tile that lie in one page
+    unsigned filled = 0, coming = 0;  // of the raw stages: phases' parities, copies on their way
     const long long v_off = reinterpret_cast<long long>(A.c.v) - reinterpret_cast<long long>(A.c.k);
     unsigned it = 0, parts = 0;
     bool fail = false;
@@ -644,13 +649,50 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       // Address of 16-key group gi's page, or 0; its first row within the head's rows.
       auto page_at = [&](int gi) -> long long {
         if (gi >= groups) return 0;
-        const int page = table[gi / groups_page];
+        const int page = table[gi >> group_shift];
         if (static_cast<unsigned>(page) < static_cast<unsigned>(A.c.n_pages))
           return reinterpret_cast<long long>(A.c.k) + page * A.c.page_bytes;
         kv_record(kKvBadPage);
         return 0;
       };
       auto row_of = [&](int gi) { return line0 + ((gi & (groups_page - 1)) << 4); };
+
+      // ---- the groups take tiles in turn. Raw tiles come one of its own tiles ahead, page ids one further. A page's rows of a
+      // head follow each other: a copy is what a tile has of a page, and each of the group's warps makes those of one kind
+      // (K's codes, V's, K's scales, V's; all from one warp, 16 keys each, took some 1900 clocks a tile)
+      auto id_at = [&](int i) {
+        const int gi = (unit0 + i) * 4 + (lane & 3);
+        return i < tiles && gi < groups ? table[gi >> group_shift] : -1;
+      };
+      int next_id = id_at(group);
+      unsigned miss = 0, next_miss = 0;  // 16-key groups without a valid page: of this tile, of the one on its way
+      auto issue = [&](int i, int stage) {
+        if (i < tiles) {
+          const int gi0 = (unit0 + i) * 4;
+          const bool there = static_cast<unsigned>(next_id) < static_cast<unsigned>(A.c.n_pages);
+          if (!there && gi0 + (lane & 3) < groups) kv_record(kKvBadPage);
+          const long long page = there ? reinterpret_cast<long long>(A.c.k) + next_id * A.c.page_bytes : 0;
+          next_id = id_at(i + 2);
+          next_miss = __ballot_sync(0xffffffffu, !there) & 15u;
+          coming |= 1u << stage;
+          constexpr unsigned kCodes = 16 * S::kRow, kScale = 16 * NB * 2;  // of 16 keys
+          const uint32_t full = bar(kBarRaw + 2 * group + stage);
+          if (gt == 0) ptx::mbar_expect_tx(full, (4 - __popc(next_miss)) * 2 * (kCodes + kScale));
+          // a run's 16-key groups before the sequence's end: those after it are in next_miss
+          const int have = groups - gi0 < 4 ? groups - gi0 : 4, n = have - lane < run ? have - lane : run;
+          if (lane < have && (lane & (run - 1)) == 0 && there) {
+            const int kind = gt >> 5, v = kind & 1, row = row_of(gi0 + lane);
+            const uint32_t to = base + S::kOffRaw + (S::kRawStages * group + stage) * S::kRaw;
+            const uint8_t* const from = reinterpret_cast<const uint8_t*>(page + (v ? v_off : 0));
+            if (kind < 2)
+              ptx::bulk_load(to + v * S::kRawCodes + lane * kCodes, from + row * S::kRow, n * kCodes, full);
+            else
+              ptx::bulk_load(to + 2 * S::kRawCodes + v * S::kRawScales + lane * kScale, from + A.c.scale_off + row * (2 * NB),
+                             n * kScale, full);
+          }
+        }
+      };
+      issue(group, 0);
 
       float kf = 1.0f, vf[NB];
 #pragma unroll
@@ -730,53 +772,14 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         for (int b = 0; b < NB && T == 1; ++b) vf[b] = down(tops[1 + b]);
       }
 
-      // ---- the groups take tiles in turn. Raw tiles come one of its own tiles ahead, page ids one further
-      auto id_at = [&](int i) {
-        const int gi = (unit0 + i) * 4 + (lane & 3);
-        return i < tiles && gi < groups ? table[gi / groups_page] : -1;
-      };
-      int next_id = id_at(group);
-      unsigned miss = 0, next_miss = 0;  // 16-key groups without a valid page: of this tile, of the one on its way
-      auto issue = [&](int i, int stage) {
-        if (i < tiles) {
-          const uint32_t to = base + S::kOffRaw + (S::kRawStages * group + stage) * S::kRaw;
-          const int gi0 = (unit0 + i) * 4;
-          const bool there = static_cast<unsigned>(next_id) < static_cast<unsigned>(A.c.n_pages);
-          if (!there && gi0 + (lane & 3) < groups) kv_record(kKvBadPage);
-          const long long mine = there ? reinterpret_cast<long long>(A.c.k) + next_id * A.c.page_bytes : 0;
-          next_id = id_at(i + 2);
-          next_miss = __ballot_sync(0xffffffffu, !there) & 15u;
-#pragma unroll
-          for (int x = 0; x < (kTileKeys * S::kChunks + kGroup - 1) / kGroup; ++x) {
-            const int c = x * kGroup + gt, key = c / S::kChunks, ch = c - key * S::kChunks;
-            const long long page = __shfl_sync(0xffffffffu, mine, (key >> 4) & 3);
-            if (page && key < kTileKeys) {
-              const uint8_t* const p =
-                  reinterpret_cast<const uint8_t*>(page) + (row_of(gi0 + (key >> 4)) + (key & 15)) * S::kRow + ch * 16;
-              const uint32_t dst = to + chunk_at<S::kChunks>(key, ch);
-              cp16(dst, p);
-              cp16(dst + S::kRawCodes, p + v_off);
-            }
-          }
-          constexpr int kPieces = 4 * 2 * NB;  // of K's scales; V's follow
-          const int c = gt < kPieces ? gt : gt - kPieces, gl = c / (2 * NB);
-          const long long page = __shfl_sync(0xffffffffu, mine, gl & 3);
-          if (gt < 2 * kPieces && page) {
-            const uint8_t* const p = reinterpret_cast<const uint8_t*>(page) + A.c.scale_off + row_of(gi0 + gl) * (2 * NB) +
-                                     (c - gl * 2 * NB) * 16 + (gt < kPieces ? 0 : v_off);
-            cp16(to + 2 * S::kRawCodes + (gt < kPieces ? 0 : S::kRawScales) + c * 16, p);
-          }
-        }
-        cp_commit();
-      };
-      static_assert(2 * 4 * 2 * NB <= kGroup, "a thread copies one piece of the scales");
       uint8_t* const scales = smem + S::kOffScale + group * S::kScales;
       const unsigned it0 = it;
-      issue(group, 0);
       for (int i = group, stage = 0; i < tiles; i += 2, stage ^= S::kRawStages - 1) {
         it = it0 + i;
-        cp_wait<0>();
-        // every thread's copies of this tile have landed, and the group's last tile has been unpacked
+        fail |= !wait_sleep(kBarRaw + 2 * group + stage, filled >> stage, 12);
+        filled ^= 1u << stage;
+        coming &= ~(1u << stage);
+        // the group's last tile has been unpacked
         if (group_any(kBarrier + 1 + group, kGroup, fail)) break;
         miss = next_miss;
         if (S::kRawStages == 2) issue(i + 2, stage ^ 1);
@@ -805,9 +808,9 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         uint8_t* const ko = smem + b * S::kKPieces * S::kOperand;
 #pragma unroll
         for (int x = 0; x < (kTileKeys * S::kChunks + kGroup - 1) / kGroup; ++x) {
-          const int c = x * kGroup + gt, key = c & (kTileKeys - 1), ch = c / kTileKeys;
-          if (ch < S::kChunks) {
-            const uint4 u4 = *reinterpret_cast<const uint4*>(raw + chunk_at<S::kChunks>(key, ch));
+          const int c = x * kGroup + gt, key = c / S::kChunks, ch = c - key * S::kChunks;
+          if (key < kTileKeys) {
+            const uint4 u4 = *reinterpret_cast<const uint4*>(raw + c * 16);
             const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w};
             const int si = key * NB + (BITS == 8 ? ch / 2 : ch);
             const uint32_t dd = reinterpret_cast<const uint16_t*>(scales)[si] * 0x10001u;
@@ -866,7 +869,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              u[k] = *reinterpret_cast<const uint32_t*>(raw + S::kRawCodes + chunk_at<S::kChunks>(kg * 8 + k, word / 4) + (word & 3) * 4);
+              u[k] = *reinterpret_cast<const uint32_t*>(raw + S::kRawCodes + (kg * 8 + k) * S::kRow + word * 4);
             // elements 4 word + i; of a 4-bit block 32 blk + 4 (word % 4) + i, and 16 further on those of the high halves
 #pragma unroll
             for (int z = 0; z < (BITS == 8 ? 1 : 2); ++z) {
@@ -921,13 +924,13 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           issue(i + 2, 0);
         }
       }
-      cp_wait<0>();
       it = it0 + tiles;
       ++parts;
       // the raw stages are free for the next part once every thread is here
       if (group_any(kBarrier, kThreads, fail)) break;
     }
-    cp_wait<0>();
+    for (int s = 0; s < 2; ++s)  // no copy is in flight when the CTA ends, even after a wait that ran out
+      if (coming >> s & 1) wait_sleep(kBarRaw + 2 * group + s, filled >> s, 12);
   }
   __syncwarp();
   ptx::tc_fence_before();
