@@ -294,19 +294,21 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         return f16 ? __half22float2(*reinterpret_cast<const __half2*>(&w))
                    : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
       };
-      float top = 0.0f;
-#pragma unroll 8
-      for (int x = 0; x < D / 8; ++x) {
-        const uint4 q = live ? from[x] : make_uint4(0u, 0u, 0u, 0u);
-        const float2 a = both(q.x), b = both(q.y), c = both(q.z), d = both(q.w);
-        top = fmaxf(fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y))),
-                    fmaxf(fmaxf(fabsf(c.x), fabsf(c.y)), fmaxf(fabsf(d.x), fabsf(d.y))));
-      }
+      uint4 qv[D / 8];  // all of it at once: one round trip to memory
+      unsigned mag = 0;  // magnitudes compare as integers
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x) qv[x] = live ? from[x] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x)
+        mag = __vmaxu2(__vmaxu2(__vmaxu2(mag, qv[x].x & 0x7FFF7FFFu), __vmaxu2(qv[x].y & 0x7FFF7FFFu, qv[x].z & 0x7FFF7FFFu)),
+                       qv[x].w & 0x7FFF7FFFu);
+      const float2 tops2 = both(mag);
+      float top = fmaxf(tops2.x, tops2.y);
       int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
       ex = ex < -100 ? -100 : ex;
       const float up = (A.scale < 0.0f ? -1.0f : 1.0f) * __uint_as_float(static_cast<unsigned>(127 + 12 - ex) << 23);
       float cs = fabsf(A.scale) * 1.4426950408889634f * __uint_as_float(static_cast<unsigned>(127 - 12 + ex) << 23);
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 2; c += 16) {
         uint32_t w[16];
 #pragma unroll
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             ok = __all_sync(0xffffffffu, wait(kBarO + buffer(r, done - 1), turn(done - 1), 7));
             if (!ok) break;
             ptx::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               uint32_t w[16];
               ptx::tmem_ld16(to + c, w);
@@ -421,7 +423,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       const bool whole = part.k0 == 0 && part.k1 == part.nu;
       if (A.late && whole) grid_wait();
       const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (part.k0 == 0 ? 1 : 0)) * S::kRows + row;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         uint32_t w[16];
         __syncwarp();
@@ -467,11 +469,12 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       // 2^12 .. 2^13; negated for a negative scale (so that cs > 0)
       const float4* const from = reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + at * D + half * (D / 2));
       float largest = 0.0f;
-#pragma unroll 8
-      for (int x = 0; x < D / 8; ++x) {
-        const float4 v = live ? from[x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        largest = fmaxf(fmaxf(largest, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
-      }
+      float4 qv[D / 8];  // all of it at once: one round trip to memory
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x) qv[x] = live ? from[x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int x = 0; x < D / 8; ++x)
+        largest = fmaxf(fmaxf(largest, fmaxf(fabsf(qv[x].x), fabsf(qv[x].y))), fmaxf(fabsf(qv[x].z), fabsf(qv[x].w)));
       sh_x[half][row] = largest;
       if (group_any(kBarrier, kThreads, fail)) break;
       largest = fmaxf(largest, sh_x[half ^ 1][row]);
@@ -479,13 +482,12 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       ex = ex < -100 ? -100 : ex;
       const float up = (A.scale < 0.0f ? -1.0f : 1.0f) * __uint_as_float(static_cast<unsigned>(127 + 12 - ex) << 23);
       float cs = fabsf(A.scale) * 1.4426950408889634f * __uint_as_float(static_cast<unsigned>(127 - 12 + ex) << 23);
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 4; c += 8) {
         uint32_t w[2][16];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          float4 v = live ? from[c / 2 + x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          v = make_float4(v.x * up, v.y * up, v.z * up, v.w * up);
+          const float4 u = live ? from[c / 2 + x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = make_float4(u.x * up, u.y * up, u.z * up, u.w * up);
           const uint32_t h0 = half2_of(v.x, v.y), h1 = half2_of(v.z, v.w);
           const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
           const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           if (i > 0) {
             fail |= !wait(kBarO, it - 1, 7);
             ptx::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 2; c += 16) {
               uint32_t w[16];
               __syncwarp();
@@ -599,7 +601,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       const bool whole = part.k0 == 0 && part.k1 == part.nu;
       if (A.late && whole) grid_wait();
       const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (part.k0 == 0 ? 1 : 0)) * S::kRows + row;
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D / 2; c += 16) {
         uint32_t w[16];
         const int d0 = half * (D / 2) + c;
@@ -839,8 +841,9 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         if (lane == 0) ptx::mbar_arrive(bar(kBarK + b));
         // ---- V: operand rows are elements. A task is a word (4 code bytes) of 8 keys
         if (turn > 0) fail |= !wait_sleep(kBarVFree + b, turn - 1, 11);
+        constexpr int kVUnroll = T == 1 ? 1 : 2;  // short code where it does not cost time
         uint8_t* const vo = smem + S::kOffV + b * S::kVPieces * S::kOperand;
-#pragma unroll
+#pragma unroll kVUnroll
         for (int x = 0; x < (8 * S::kWords + kGroup - 1) / kGroup; ++x) {
           const int c = x * kGroup + gt, kg = c / S::kWords, word = c - kg * S::kWords;
           if (kg < 8) {
