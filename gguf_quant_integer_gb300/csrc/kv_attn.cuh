@@ -271,17 +271,6 @@ __device__ __forceinline__ float load_scales(const __half* p, float (&f)[N]) {
   }
 }
 
-__device__ __forceinline__ float4 load4(const void* p, int type, size_t i) {
-  if (type == kF32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-  const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-  if (type == kF16) {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-    return make_float4(a.x, a.y, b.x, b.y);
-  }
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xFFFF0000u));
-}
 
 __device__ __forceinline__ void store4(void* p, int type, size_t i, float4 v) {
   if (type == kF32) {
@@ -497,6 +486,34 @@ __device__ __forceinline__ void scale_all(float (&o)[NT][M][4], float f) {
     }
 }
 
+// Elements 16 k + 0 .. 3 from `at` on of the queries, which are fp32 (EX) or 16-bit ones.
+template <bool EX, int D>
+__device__ __forceinline__ void load_query(const SplitArgs& A, size_t at, float4 (&v)[D / 16]) {
+  if (EX) {
+    const float4* const p = reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + at);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) v[k] = p[4 * k];
+  } else {
+    const uint2* const p = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(A.q) + at);
+    uint2 w[D / 16];
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) w[k] = p[4 * k];
+    if (A.type == kF16) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[k].x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w[k].y));
+        v[k] = make_float4(a.x, a.y, b.x, b.y);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k)
+        v[k] = make_float4(__uint_as_float(w[k].x << 16), __uint_as_float(w[k].x & 0xFFFF0000u), __uint_as_float(w[k].y << 16),
+                           __uint_as_float(w[k].y & 0xFFFF0000u));
+    }
+  }
+}
+
 template <int BITS, int D, bool EX, int NP, int NT>
 __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, NT>::kCtas)
     kv_split_kernel(const __grid_constant__ SplitArgs A) {
@@ -609,12 +626,17 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int r = NP == 2 ? 4 * j + (g >> 1) : 8 * j + g;
+      // every load before the first use: one round trip to memory (one by one: 10000 clocks, as the type is looked at for each)
       float4 v[D / 16];
+      if (r < rows) {
+        load_query<EX, D>(A, row_at(A, sq, head, row0 + r) * D + 4 * t, v);
+      } else {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
       float top = 0.0f;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        v[k] = r < rows ? load4(A.q, A.type, row_at(A, sq, head, row0 + r) * D + 16 * k + 4 * t)
-                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         top = fmaxf(fmaxf(top, fmaxf(fabsf(v[k].x), fabsf(v[k].y))), fmaxf(fabsf(v[k].z), fabsf(v[k].w)));
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
