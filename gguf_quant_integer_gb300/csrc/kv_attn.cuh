@@ -33,6 +33,7 @@
 #pragma once
 
 #include <climits>
+#include <type_traits>
 
 #include "kv_common.cuh"
 #include "xq_common.cuh"
@@ -271,7 +272,6 @@ __device__ __forceinline__ float load_scales(const __half* p, float (&f)[N]) {
   }
 }
 
-
 __device__ __forceinline__ void store4(void* p, int type, size_t i, float4 v) {
   if (type == kF32) {
     *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = v;
@@ -486,33 +486,31 @@ __device__ __forceinline__ void scale_all(float (&o)[NT][M][4], float f) {
     }
 }
 
-// Elements 16 k + 0 .. 3 from `at` on of the queries, which are fp32 (EX) or 16-bit ones.
+// A lane's share of a query row as it lies in memory, elements 16 k + 0 .. 3: fp32 (EX) or 16-bit ones.
 template <bool EX, int D>
-__device__ __forceinline__ void load_query(const SplitArgs& A, size_t at, float4 (&v)[D / 16]) {
-  if (EX) {
-    const float4* const p = reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + at);
+struct RawQuery {
+  using Piece = std::conditional_t<EX, float4, uint2>;
+  Piece x[D / 16];
+  __device__ __forceinline__ void load(const SplitArgs& A, size_t at, bool live) {
+    const Piece* const p = reinterpret_cast<const Piece*>(static_cast<const uint8_t*>(A.q) + at * (EX ? 4 : 2));
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) v[k] = p[4 * k];
-  } else {
-    const uint2* const p = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(A.q) + at);
-    uint2 w[D / 16];
+    for (int k = 0; k < D / 16; ++k) x[k] = live ? p[4 * k] : Piece{};
+  }
+  __device__ __forceinline__ void floats(bool f16, float4 (&v)[D / 16]) const {
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) w[k] = p[4 * k];
-    if (A.type == kF16) {
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[k].x));
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w[k].y));
-        v[k] = make_float4(a.x, a.y, b.x, b.y);
+    for (int k = 0; k < D / 16; ++k) {
+      if constexpr (EX) {
+        v[k] = x[k];
+      } else {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&x[k].x));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&x[k].y));
+        v[k] = f16 ? make_float4(a.x, a.y, b.x, b.y)
+                   : make_float4(__uint_as_float(x[k].x << 16), __uint_as_float(x[k].x & 0xFFFF0000u),
+                                 __uint_as_float(x[k].y << 16), __uint_as_float(x[k].y & 0xFFFF0000u));
       }
-    } else {
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        v[k] = make_float4(__uint_as_float(w[k].x << 16), __uint_as_float(w[k].x & 0xFFFF0000u), __uint_as_float(w[k].y << 16),
-                           __uint_as_float(w[k].y & 0xFFFF0000u));
     }
   }
-}
+};
 
 template <int BITS, int D, bool EX, int NP, int NT>
 __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, NT>::kCtas)
@@ -607,17 +605,24 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
     const int page = page_of(lane);
     next_page = page_of(32 + lane);
     locate(lane, page);
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < kStages - 1; ++i) issue(i, stage + i < kStages ? stage + i : stage + i - kStages);
   };
 
   Part cur;
-  bool have = line_next(A, line, cur);
-  if (have) begin_part(cur);
+  bool have = line_next(A, line, cur), begun = false;
   while (have) {
     const int sq = cur.seq, n = cur.n, nu = cur.nu, pair = cur.pair, k0 = cur.k0, k1 = cur.k1;
     const int head = pair / A.chunks, chunk = pair - head * A.chunks;
     const int row0 = chunk * R, rows = A.rows - row0 < R ? A.rows - row0 : R;
+    // ---- the queries' loads, all before the first use, and ahead of the first tiles'
+    RawQuery<EX, D> raw[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int r = NP == 2 ? 4 * j + (g >> 1) : 8 * j + g;
+      raw[j].load(A, r < rows ? row_at(A, sq, head, row0 + r) * D + 4 * t : 0, r < rows);
+    }
+    if (!begun) begin_part(cur);
     // ---- queries as B operands. Column g of n-tile j: NP = 2: row 4 j + g/2, piece g & 1; NP = 1: row 8 j + g.
     uint32_t qf[NT][D / 16][2];
     float cs[NT][NQ], qs[NT][NB][NQ];  // score factor, and -(128 or 8) sum(q) of each block, of this lane's columns
@@ -625,15 +630,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
     int all0 = 0, all1 = INT_MAX;  // keys that every row of the chunk sees
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int r = NP == 2 ? 4 * j + (g >> 1) : 8 * j + g;
-      // every load before the first use: one round trip to memory (one by one: 10000 clocks, as the type is looked at for each)
       float4 v[D / 16];
-      if (r < rows) {
-        load_query<EX, D>(A, row_at(A, sq, head, row0 + r) * D + 4 * t, v);
-      } else {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      }
+      raw[j].floats(A.type == kF16, v);
       float top = 0.0f;
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
@@ -989,7 +987,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
       }
     Part next;
     const bool more_parts = line_next(A, line, next);
-    if (S::kOverlap && more_parts) begin_part(next);
+    begun = S::kOverlap && more_parts;
+    if (begun) begin_part(next);
     __syncthreads();
     const bool whole = k0 == 0 && k1 == nu;
     if (A.late && whole) grid_wait();
@@ -1021,7 +1020,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
       if (tid == 0) A.record[cta] = make_int4(sq, pair, line_last(A, line, cur), 0);
     }
     __syncthreads();
-    if (!S::kOverlap && more_parts) begin_part(next);
     cur = next;
     have = more_parts;
   }
