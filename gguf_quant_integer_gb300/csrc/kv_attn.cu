@@ -31,17 +31,17 @@ Pass prefix_pass(const KvAttnArgs& a) { return {1, a.batch * a.rows, a.prefix_le
 
 // Whether a pass goes to the tcgen05 tiles. They take some 20 us whatever the
 // work, and then, from 64 rows on, a fraction of the split kernel's time for
-// it. Both measured (tiles, split; 8 KV heads, dim 128, Q8_0, whole calls):
-//   bf16  256 rows x 2048 keys 47 and 48 us; 128 rows x 2048 34 and 36,
-//         x 8192 41 and 61, x 32768 71 and 183; 64 rows x 8192 42 and 44;
-//         32 rows x 32768 77 and 68
-//   fp32  256 rows x 2048 58 and 52, x 8192 86 and 123; 128 rows x 2048 48 and
-//         37, x 8192 64 and 73, x 32768 120 and 217; 64 rows x 32768 117 and 120
+// it. Both measured (tiles, split; 8 KV heads, dim 128, Q8_0, whole calls, us):
+//   bf16  256 rows x 2048 keys 32.1 and 32.5, x 32768 66 and 194; 128 rows
+//         x 2048 23.0 and 23.4, x 8192 27 and 40, x 32768 46 and 105; 64 rows
+//         x 2048 22.5 and 20.6, x 8192 29.5 and 29.1; 32 rows x 32768 54, 40
+//   fp32  256 rows x 2048 37 and 46, x 32768 119 and 385; 128 rows x 2048 29.6
+//         and 30.2, x 8192 38 and 64; 64 rows x 2048 25.2 and 23.4, x 8192 34
+//         and 41; 32 rows x 32768 66 and 63
 bool tiled(const KvAttnArgs& a, const Pass& p) {
-  const bool exact = a.type == kF32;
   if (a.c.dim > 128 || p.rows < 64) return false;
   const long long seen = a.window > 0 && p.keys > a.window + a.n_q ? a.window + a.n_q : p.keys;
-  return static_cast<double>(p.seqs) * p.rows * seen * a.c.heads >= (exact ? 8e6 : 3e6);
+  return static_cast<double>(p.seqs) * p.rows * seen * a.c.heads >= 3e6;
 }
 
 // CTAs and rows of partial results (two a CTA): three resident CTAs an SM of

@@ -1027,9 +1027,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
   if (A.late) grid_wait();
 }
 
-// The parts of the pairs that begin in CTAs blockIdx.x, + gridDim.x, ..., RB of their R rows from RB * blockIdx.y on. A
-// thread holds one float4 of the rows; each team of threads takes every kTeams-th part, several loads at a time, then the
-// teams are merged. COLS: the parts' outputs are stored [dim / 4][R], not [R][dim / 4].
+// The parts of the pairs that begin in a block's stretch of CTAs (of neighbours: pairs often begin at equal distances, which
+// a step of gridDim.x may divide), RB of their R rows from RB * blockIdx.y on. A thread holds one float4 of the rows; each
+// team of threads takes every kTeams-th part, several loads at a time, then the teams are merged. COLS: the parts' outputs
+// are stored [dim / 4][R], not [R][dim / 4].
 // Two blocks an SM, with 6 loads in flight a thread (one block with 8: 64 sequences of 211 to 8192 tokens 85.8 us instead
 // of 83.9, a prefix of 32768 tokens for 64 sequences 96.6 instead of 91.6; three with 2 to 4 help or cost as much).
 constexpr int kJoinThreads = 512, kJoinBlocks = 2, kJoinBatch = 6;
@@ -1046,10 +1047,10 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) kv_join_kernel(cons
   const int r = COLS ? at % RB : at / (D / 4), d = (COLS ? at / RB : at % (D / 4)) * 4;
   const int row = RB * blockIdx.y + r;
   int4 mine = make_int4(0, 0, -1, 0);  // the records, one a lane
-  const int c = blockIdx.x + lane * gridDim.x;
-  if (c < A.ctas) mine = A.record[c];
+  const int per = (A.ctas + gridDim.x - 1) / gridDim.x, c = blockIdx.x * per + lane;
+  if (lane < per && c < A.ctas) mine = A.record[c];
   for (unsigned left = __ballot_sync(0xffffffffu, mine.z >= 0); left; left &= left - 1) {
-    const int from = __ffs(left) - 1, c0 = blockIdx.x + from * gridDim.x;
+    const int from = __ffs(left) - 1, c0 = blockIdx.x * per + from;
     const int seq = __shfl_sync(0xffffffffu, mine.x, from), pair = __shfl_sync(0xffffffffu, mine.y, from);
     const int parts = __shfl_sync(0xffffffffu, mine.z, from) - c0 + 1;
     const int head = pair / A.chunks, pair_row = (pair - head * A.chunks) * R + row;
