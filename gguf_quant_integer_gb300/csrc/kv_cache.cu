@@ -117,56 +117,66 @@ __device__ __forceinline__ float max_abs(float a, float b) {
   return m;
 }
 
+// fp16(top / 127). The product with 1 / 127 is within 3 steps of the quotient,
+// so fp16 rounds both alike unless the product lies that near the middle of two
+// fp16 numbers (one block in a thousand) or below fp16's normal ones.
+__device__ __forceinline__ __half scale_q8(float top) {
+  float q = top * (1.0f / 127.0f);
+  if (!(q >= 6.1035156e-5f) || ((__float_as_uint(q) - 0x0FFCu) & 0x1FFFu) <= 8u) q = __fdiv_rn(top, 127.0f);
+  return __float2half_rn(q);
+}
+
 // The codes of N values, a byte each (q + 128, or q + 8 for BITS = 4), by
-// x * (1 / d), within 2^-16 of x / d: adding 1.5 * 2^23 + offset leaves the
+// x * (1 / d), within 2^-15 of x / d: adding 1.5 * 2^23 + offset leaves the
 // nearest whole number in the low bits. What is left is which side of a half
 // the quotient is on.
-//   16-bit inputs to Q4_0, where d = x' / 8 makes many quotients exact halves
-//     (others differ from one by 2^-12 at least): the remainder x - n d is
-//     exact, and is compared with d / 2.
-//   Else a piece with a product within 1e-4 of a half is divided out, about one
-//     warp in forty.
-// 8 to 13 instructions a value where a division takes 25.
-template <int BITS, int N>
-__device__ __forceinline__ void codes_of(const float (&f)[N], float d, uint32_t (&code)[N / 4]) {
+//   16-bit inputs: with x and d of 11 bits, a quotient is a half or 2^-12 from
+//     one at least (2 x - (2 n + 1) d is a multiple of the smaller of 2 ulp(x)
+//     and ulp(d), 2^-11 d or more), so a step of 2^-13 away from zero takes
+//     the halves outwards and no other quotient past one.
+//   fp32: a piece with a product within 1e-4 of a half is divided out, about
+//     one warp in forty.
+// CLAMP: Q8_0's quotients pass 127.5 only where d is below fp16's normal numbers.
+// 4 to 8 instructions a value where a division takes 25.
+template <int BITS, int N, bool CLAMP>
+__device__ __forceinline__ void codes_by_product(const float (&f)[N], float d, uint32_t (&code)[N / 4]) {
   constexpr float low = BITS == 8 ? -127.0f : -8.0f, top = BITS == 8 ? 127.0f : 7.0f;
   constexpr float shift = 12582912.0f + (BITS == 8 ? 128.0f : 8.0f);
-  constexpr uint32_t zeros = BITS == 8 ? 0x80808080u : 0x08080808u;
-  if (!(fabsf(d) <= 65504.0f) || d == 0.0f) {  // finite / infinite, and what is not a number: 0
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) code[i] = zeros;
-    return;
-  }
-  const float inv = __frcp_rn(d), half = 0.5f * fabsf(d);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(d));
   float off = 0.0f;
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
     uint32_t b[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float x = f[4 * i + k], y = fminf(fmaxf(x * inv, low), top);
-      float z = __fadd_rn(y, shift);
-      const float n = __fadd_rn(z, -shift);
-      if (N == 8 && BITS == 4) {
-        const float r = fmaf(-n, d, x);
-        // r on x's side: n is too near zero at a half or more; on the other: too far beyond a half
-        const bool near = (__float_as_int(r) ^ __float_as_int(x)) >= 0;
-        const float step = copysignf(1.0f, y);
-        z = near ? (fabsf(r) >= half ? z + step : z) : (fabsf(r) > half ? z - step : z);
-        z = fminf(fmaxf(z, low + shift), top + shift);
-      } else {
-        off = max_abs(off, __fadd_rn(y, -n));
-      }
+      float y = f[4 * i + k] * inv;
+      if (N == 8) y = __fadd_rn(y, copysignf(1.220703125e-4f, y));
+      if (CLAMP) y = fminf(fmaxf(y, low), top);
+      const float z = __fadd_rn(y, shift);
+      if (N == 4) off = max_abs(off, __fadd_rn(y, -__fadd_rn(z, -shift)));
       b[k] = __float_as_uint(z);
     }
     code[i] = prmt(prmt(b[0], b[1], 0x0040u), prmt(b[2], b[3], 0x0040u), 0x5410u);
   }
-  if (!(off < 0.4999f)) {
+  if (N == 4 && !(off < 0.4999f)) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const unsigned q = quant(f[i], d, low, top) + (BITS == 8 ? 128 : 8);
       code[i / 4] = (i & 3) ? (code[i / 4] | (q << (8 * (i & 3)))) : q;
     }
+  }
+}
+template <int BITS, int N>
+__device__ __forceinline__ void codes_of(const float (&f)[N], float d, uint32_t (&code)[N / 4]) {
+  constexpr uint32_t zeros = BITS == 8 ? 0x80808080u : 0x08080808u;
+  if (BITS == 8 && d >= 6.1035156e-5f && d <= 65504.0f) {
+    codes_by_product<BITS, N, false>(f, d, code);
+  } else if (!(fabsf(d) <= 65504.0f) || d == 0.0f) {  // finite / infinite, and what is not a number: 0
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) code[i] = zeros;
+  } else {
+    codes_by_product<BITS, N, true>(f, d, code);
   }
 }
 
@@ -183,7 +193,7 @@ __device__ __forceinline__ float quantize_piece(const float (&f)[N], int lane, u
     for (int i = 0; i < N; ++i) top = max_abs(top, f[i]);
 #pragma unroll
     for (int o = 1; o < G; o *= 2) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, o));
-    dh = __float2half_rn(__fdiv_rn(top, 127.0f));
+    dh = scale_q8(top);
   } else {
     float m = f[0];
 #pragma unroll
