@@ -19,11 +19,15 @@
 // Score columns become weight columns by movmatrix, whose 8x8 transpose takes
 // an accumulator's (key, query pair) registers to the B operand.
 //
-// What bounds it: HBM, at a few query rows. One key of dim 128 is 272 bytes of
-// Q8_0 and 544 multiply-adds a query; an SM has about 24 bytes a clock to
-// itself, against 4 instructions. Unpacking costs about one instruction per
-// value, hence no per-row work on codes, and codes loaded by ldmatrix (plain
-// for K, transposed for V) straight into operand order.
+// What bounds it. One key of dim 128 is 272 bytes of Q8_0 (144 of Q4_0) and
+// 512 multiply-adds a query; an SM has about 24 bytes a clock to itself,
+// against 4 instructions. A warp's 16 keys cost some 420 instructions, so long
+// Q8_0 caches are bound by HBM and Q4_0's nearly as much by instructions: 64
+// sequences, 230000 tokens in all, 8 KV heads, fp32: 84 us, 5.9 TB/s with the
+// join; one sequence of 131071 Q4_0 tokens, bf16: 38 us, 4.0 TB/s, of which 5
+// are the join and 5 pass before the first tile's products. Short calls are
+// bound by latency: one sequence of 97 tokens 5.5 us (10000 clocks: 3000 to
+// find the work, 3000 for queries and the first tile, 1000 to 1500 a tile).
 //
 // Work split. Sequences differ in length, so the keys of all (sequence, KV
 // head, row chunk) pairs are one line of 64-key units that is cut evenly over
@@ -51,10 +55,11 @@ constexpr int kAttnUnit = 16 * kAttnWarps;  // keys a unit
 // Units of time that a CTA spends on a pair besides its keys (queries, page
 // ids, filling the pipeline, merging): the cut counts them, or CTAs with many
 // short sequences would finish last. With two n-tiles more, as each row's
-// query is split. (64 sequences of 211 to 8192 tokens: 88.3, 86.3, 85.6, 86.2,
-// 87.8 us with 3, 4, 5, 6, 8; two n-tiles, 16 sequences of 300 to 4099: 27.8,
-// 26.0, 23.9 us with 3, 5, 8.)
-constexpr int kAttnHead = 5, kAttnHead2 = 8;
+// query is split. (64 sequences of 211 to 8192 tokens: 87.9, 84.0, 84.0, 84.3,
+// 84.6 us with 2, 3, 4, 5, 6; two n-tiles, 16 sequences of 300 to 4099: 18.7,
+// 18.5, 18.6, 18.6 us with 4, 5, 6, 8, and 8 KV heads' 1000-token prefix for 8
+// sequences 16.7, 16.7, 16.5, 16.5.)
+constexpr int kAttnHead = 4, kAttnHead2 = 6;
 // Pairs that can have no more units than this are not cut. A CTA takes about
 // 0.5 us a unit, the join's launch 4 us (one 97-token sequence, 8 KV heads:
 // 8.5 us cut, 6.6 us whole).

@@ -1,14 +1,19 @@
 // Writing the quantized KV cache and reading it back (block formulas and the
 // page layout in the public header).
 //
-// Both kernels move each byte once and compute about 20 operations a value,
-// so HBM bounds them from a few hundred tokens on, and launch latency below.
+// Both kernels move each byte once. What bounds them: launch latency up to a
+// few hundred tokens (one token 3 us for a write and a read); then, for reads,
+// HBM (16383 tokens of 8 heads of 128, Q8_0 to fp32: 28 us, 6.1 TB/s; 65536
+// Q4_0 tokens to bf16: 52 us, 6.6 TB/s); for writes the instructions, some 25
+// a value in all, as fp32's 16-byte pieces hold four values only (fp32 to Q8_0
+// 32 us, 5.3 TB/s, 68 % of the issue slots; bf16 to Q4_0 29 us, 2.9 TB/s).
 // A 32-value block belongs to a group of neighbouring lanes of one warp, each
 // with 16 bytes of float values (8 lanes for fp32, 4 for 16-bit types): the
 // loads and stores of a warp are then whole 128-byte lines, and the block's
 // maximum takes two or three shuffles and no shared memory. A thread handles
 // the same block of K and of V, which doubles the loads in flight.
 #include <climits>
+#include <type_traits>
 
 #include "kv_common.cuh"
 #include "xq_common.cuh"
@@ -359,11 +364,13 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant
 template <typename K, typename Args>
 cudaError_t launch(K kernel, Args& A, long long tokens, int lanes, cudaStream_t s) {
   const unsigned blocks = 32 / lanes, pieces = (A.r.row_blocks + blocks - 1) / blocks;
-  // Few tokens: a warp a piece, for the least latency. Many: a warp up to 8
+  // Few tokens: a warp a piece, for the least latency. Many: a warp several
   // pieces of a row, which share the slot's and the addresses' arithmetic
-  // (fp32 write of 16383 tokens: 40 us with one piece, 29 us with 8).
+  // (16383 fp32 tokens of 8 heads of 128, Q8_0: writes 43.3, 32.6, 31.8 and
+  // 31.9 us with 1, 4, 8 and 16 pieces, reads 42.7, 27.9, 29.3 and 29.4).
+  constexpr unsigned kMost = std::is_same<Args, WriteArgs>::value ? 8 : 4;
   const long long most = 64LL * kNumSMs;
-  unsigned span = tokens * pieces > 2 * most ? 8 : tokens * pieces > most ? 2 : 1;
+  unsigned span = tokens * pieces > 2 * most ? kMost : tokens * pieces > most ? 2 : 1;
   span = span < pieces ? span : pieces;
   A.r.span = span;
   A.r.warps_row = (pieces + span - 1) / span;

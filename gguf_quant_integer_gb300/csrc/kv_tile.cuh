@@ -5,27 +5,40 @@
 // Mathematics: as in kv_attn.cuh, o = sum_j 2^(s_j - e) v_j and l alike, per
 // row, with a reference e that moves only when a weight would leave its
 // range. Both products take their A operand from tensor memory (queries,
-// 128 rows = lanes; then weights, which the thread of a row writes where its
-// scores were read: no shuffles, no shared memory) and their B operand, the
+// 128 rows = lanes; then weights, which a row's thread writes where it read
+// the scores: no shuffles, no shared memory) and their B operand, the
 // dequantized tile, from shared memory.
 //   16-bit queries (T = 1): everything enters as one fp16 number. K and V are
 //     code * d / 2^x rounded to fp16; 2^x, from the part's largest block scale
 //     (for V of each 32 elements), keeps them in range whatever their size.
+//     Rounding to 11 bits is 8 times finer than bf16 output and as fine as
+//     fp16's. Two row tiles share the unpacked keys.
 //   fp32 queries (T = 3): queries and K enter as two fp16 numbers each (22 bits
 //     and 19, all that a code times its scale has), scaled alike; their product
 //     is hi.hi + hi.lo + lo.hi. Weights and V enter as three bf16 numbers each
 //     (24 bits, and fp32's exponent range, which the smallest weights need),
 //     cut off, not rounded: the six pairs 1.1 + 1.2 + 2.1 + 1.3 + 2.2 + 3.1;
-//     the rest is below 2^-24.
+//     the rest is below 2^-24. One row tile, as the pieces fill the memories.
 //
-// What bounds it: instructions of the softmax and of dequantization. A tile
-// has 8192 scores at about 6 instructions each (scale, mask test, maximum,
-// exponential, sum, conversion) and 64 * 2 * dim values to unpack at 2 (T = 1) to 9
-// (T = 3), against 2 * 128 * 64 * dim multiply-adds per product pair, 512
-// clocks of the tensor core at dim 128. So the split is by role: 8 warps for
-// the softmax (a row's 64 keys in two threads), 8 warps that copy and unpack,
-// one thread that issues the products; scores of tile i+1 are computed while
-// its weights of tile i are multiplied.
+// Roles: 8 warps for the softmax (T = 1: a thread a row; T = 3: two, half of
+// the keys each), 8 that unpack, in two groups with a tile each in turn, and
+// one that issues the products. Scores are computed two tiles ahead of the
+// weights, where tensor memory has the columns (one row tile), else one.
+// Raw tiles come by bulk copies, two of a group's ahead.
+//
+// What bounds it, in clocks at dim 128, Q8_0 (the tensor cores need 1024 a
+// tile of 64 keys with two row tiles, 2300 in fp32):
+//   T = 1, 256 rows: 2600 a tile, most of it a softmax thread's 64 scores
+//     (tensor memory there and back, maximum, exponentials). Twice as many
+//     softmax warps have 72 registers a thread: 2900.
+//   T = 1, 128 rows: 1700, the unpacking warps' (5400 a group's tile before
+//     bulk copies, 2800 with).
+//   T = 3: 3500, unpacking V into three pieces and the products.
+// Before a part's first scores come some 20000 (page ids, the part's scales,
+// the first tile, and instructions seen for the first time: hence the rolled
+// loops outside the tiles'), after its last weights 6000 for the results.
+// Whole calls, 8 KV heads over 32768 keys: 256 bf16 rows 64 us (34 GFLOP, 530
+// TFLOP/s), 128 bf16 rows 45 us, 128 fp32 rows 71 us.
 //
 // Work is cut as in kv_attn.cuh: units of 64 keys, one CTA an SM.
 #pragma once

@@ -336,8 +336,8 @@ XQ_API xq_status xq_layer_mixed_static(const xq_proj *proj, int n_proj,
  * is of an invalid index, not of a wait: 1 a slot past the cache, 2 a page id
  * outside it, 3 a sequence longer than its page table (see xq_kv_write and
  * xq_kv_attn). Kernel 4 = the cache attention's 128-row tiles (waits 1-5 the
- * products, 6-9 the softmax, 10-11 the unpacking). Checked builds (the library compiled with
- * -DXQ_CHECK) also test the index, range or 16-byte alignment of each global
+ * products, 6-9 the softmax, 10-12 the unpacking). Checked builds (the
+ * library compiled with -DXQ_CHECK) also test the index, range or 16-byte alignment of each global
  * access whose address comes from nontrivial arithmetic, skip an access that
  * fails and record the site: kernel 9, wait = site (10-16 the GEMV, 20-26
  * the tile kernel, 30-32 the quantizer, 40-43 the dp4a Q6_K GEMV,
@@ -513,12 +513,15 @@ XQ_API size_t xq_kv_attn_workspace_bytes(const xq_kv_cache *cache, const xq_kv_q
  * over the keys j <= pos and, with a window, j > pos - window, where query
  * token i of a sequence of n tokens is at pos = n - n_q + i. A query that
  * sees no key (pos < 0; an idle entry with lens 0) gives 0. Scores, softmax
- * statistics and sums are fp32. fp32 queries and weights enter the tensor
- * cores as two fp16 numbers each (22 bits), 16-bit ones and their softmax
+ * statistics and sums are fp32. fp32 queries and their weights enter the
+ * tensor cores as two fp16 numbers each (22 bits), 16-bit ones and their
  * weights as one; the stored codes are exact there, and block scales are
- * applied in fp32. Results do not depend on what the slots past a sequence's
- * length hold. They depend on the other sequences of the call only through
- * where a long sequence is cut into parts (in rounding).
+ * applied in fp32. Where many rows (64 or more) read a head's many keys, K and
+ * V enter with their scales: as one fp16 number for 16-bit queries, without
+ * loss for fp32 ones, whose weights and V are then three bf16 numbers each.
+ * Results do not depend on what the slots past a sequence's length hold. They
+ * depend on the other sequences of the call only through where a long
+ * sequence is cut into parts (in rounding).
  * lens beyond max_pages * page_size are cut to that, and a page id outside
  * 0 .. n_pages-1 within a sequence's length is taken as masked keys; both
  * are recorded (xq_device_error: kernel 3, waits 3 and 2). prefix_pages and
