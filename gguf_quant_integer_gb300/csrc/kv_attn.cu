@@ -29,17 +29,18 @@ struct Pass {
 Pass own_pass(const KvAttnArgs& a) { return {a.batch, a.rows, static_cast<long long>(a.max_pages) << a.c.page_shift}; }
 Pass prefix_pass(const KvAttnArgs& a) { return {1, a.batch * a.rows, a.prefix_len}; }
 
-// Whether a pass goes to the tcgen05 tiles. They take some 20 us whatever the
-// work, and then, from 64 rows on, a fraction of the split kernel's time for
-// it. Both measured (tiles, split; 8 KV heads, dim 128, Q8_0, whole calls, us):
-//   bf16  256 rows x 2048 keys 32.1 and 32.5, x 32768 66 and 194; 128 rows
-//         x 2048 23.0 and 23.4, x 8192 27 and 40, x 32768 46 and 105; 64 rows
-//         x 2048 22.5 and 20.6, x 8192 29.5 and 29.1; 32 rows x 32768 54, 40
-//   fp32  256 rows x 2048 37 and 46, x 32768 119 and 385; 128 rows x 2048 29.6
-//         and 30.2, x 8192 38 and 64; 64 rows x 2048 25.2 and 23.4, x 8192 34
-//         and 41; 32 rows x 32768 66 and 63
+// Whether a pass goes to the tcgen05 tiles, which are for 16-bit queries. They
+// take some 20 us whatever the work, and then, from 64 rows on, a fraction of
+// the split kernel's time for it. Both measured (tiles, split; 8 KV heads, dim
+// 128, Q8_0, whole calls, us):
+//   bf16  256 rows x 2048 keys 32.1 and 31.8, x 32768 66 and 194; 128 rows
+//         x 2048 22.9 and 22.8, x 8192 27 and 40, x 32768 46 and 105; 64 rows
+//         x 2048 22.7 and 20.1, x 8192 29.7 and 29.2; 32 rows x 32768 55, 41
+//   fp16  256 rows x 2048 34.4 and 31.9, x 32768 78 and 194; 128 rows x 2048
+//         24.0 and 22.9, x 8192 29 and 40, x 32768 54 and 105; 64 rows x 32768
+//         60 and 62
 bool tiled(const KvAttnArgs& a, const Pass& p) {
-  if (a.c.dim > 128 || p.rows < 64) return false;
+  if (a.type == kF32 || a.c.dim > 128 || p.rows < 64) return false;
   const long long seen = a.window > 0 && p.keys > a.window + a.n_q ? a.window + a.n_q : p.keys;
   return static_cast<double>(p.seqs) * p.rows * seen * a.c.heads >= 3e6;
 }
@@ -48,7 +49,7 @@ bool tiled(const KvAttnArgs& a, const Pass& p) {
 // 4 or 8 rows, two of up to 16; one of 128 or 256.
 constexpr int kMaxCtas = 3 * kNumSMs;
 constexpr size_t kSplitRows = 2 * kMaxCtas * 16;
-size_t tile_part_rows(bool exact) { return static_cast<size_t>(2) * kNumSMs * tile_rows(exact); }
+constexpr size_t kTilePartRows = static_cast<size_t>(2) * kNumSMs * kTileChunk;
 
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
@@ -58,7 +59,7 @@ struct Layout {
 Layout layout(const KvAttnArgs& a) {
   Layout L;
   const bool tile = tiled(a, own_pass(a)) || (a.prefix_len > 0 && tiled(a, prefix_pass(a)));
-  const size_t rows = tile ? tile_part_rows(a.type == kF32) : kSplitRows;
+  const size_t rows = tile ? kTilePartRows : kSplitRows;
   const size_t outs = a.prefix_len > 0 ? static_cast<size_t>(a.batch) * a.n_q * a.q_heads : 0;
   L.record = 0;
   L.part_el = L.record + kMaxCtas * sizeof(int4);
@@ -74,7 +75,7 @@ cudaError_t run(SplitArgs& p, const Pass& pass, const KvAttnArgs& a, int bits, c
   p.rows = pass.rows;
   const bool tile = tiled(a, pass);
   const Rows f = rows_for(a, p.rows);
-  const int r = tile ? tile_rows(f.exact) : f.nt * 8 / f.np;
+  const int r = tile ? kTileChunk : f.nt * 8 / f.np;
   p.chunks = (p.rows + r - 1) / r;
   const long long units = (pass.keys + kAttnUnit - 1) / kAttnUnit;
   // Sequences too short for a second CTA to be worth a join: whole pairs.
@@ -83,9 +84,9 @@ cudaError_t run(SplitArgs& p, const Pass& pass, const KvAttnArgs& a, int bits, c
   p.units = p.seqs * ((units > 1 ? units : 1) + p.head) * p.c.heads * p.chunks;
   if (tile) {
     switch (a.c.dim) {
-      case 64: return KvTileDim<64>::launch(p, bits, f.exact, s);
-      case 96: return KvTileDim<96>::launch(p, bits, f.exact, s);
-      default: return KvTileDim<128>::launch(p, bits, f.exact, s);
+      case 64: return KvTileDim<64>::launch(p, bits, a.type == kF16, s);
+      case 96: return KvTileDim<96>::launch(p, bits, a.type == kF16, s);
+      default: return KvTileDim<128>::launch(p, bits, a.type == kF16, s);
     }
   }
   switch (a.c.dim) {

@@ -1,45 +1,41 @@
-// Attention over the quantized KV cache for many query rows a KV head (a
-// prefix that a whole batch shares, a long run of query tokens): tiles of 128
-// rows x 64 keys on the tcgen05 tensor cores.
+// Attention over the quantized KV cache for many 16-bit query rows a KV head
+// (a prefix that a whole batch shares, a long run of query tokens): tiles of
+// 128 rows x 64 keys on the tcgen05 tensor cores.
 //
 // Mathematics: as in kv_attn.cuh, o = sum_j 2^(s_j - e) v_j and l alike, per
 // row, with a reference e that moves only when a weight would leave its
 // range. Both products take their A operand from tensor memory (queries,
 // 128 rows = lanes; then weights, which a row's thread writes where it read
 // the scores: no shuffles, no shared memory) and their B operand, the
-// dequantized tile, from shared memory.
-//   16-bit queries (T = 1): everything enters as one fp16 number. K and V are
-//     code * d / 2^x rounded to fp16; 2^x, from the part's largest block scale
-//     (for V of each 32 elements), keeps them in range whatever their size.
-//     Rounding to 11 bits is 8 times finer than bf16 output and as fine as
-//     fp16's. Two row tiles share the unpacked keys.
-//   fp32 queries (T = 3): queries and K enter as two fp16 numbers each (22 bits
-//     and 19, all that a code times its scale has), scaled alike; their product
-//     is hi.hi + hi.lo + lo.hi. Weights and V enter as three bf16 numbers each
-//     (24 bits, and fp32's exponent range, which the smallest weights need),
-//     cut off, not rounded: the six pairs 1.1 + 1.2 + 2.1 + 1.3 + 2.2 + 3.1;
-//     the rest is below 2^-24. One row tile, as the pieces fill the memories.
+// dequantized tile, from shared memory. Everything enters as fp16; K and V are
+// code * d / 2^x, where 2^x, from the part's largest block scale (for V of each
+// 32 elements), keeps them in range whatever their size. For bf16 queries they
+// are rounded to one number (11 bits, 8 finer than the output's). For fp16 ones
+// they are two, P = 2, which hold all 19 bits of a code times its scale: one
+// would nearly double the output's error (4.1e-4 against 2.8e-4 relative, of
+// which rounding the output is 2.1e-4). fp32 queries never come here: a tensor
+// core's accumulator loses a little at each product added to it, and the 24
+// products of a tile in three bf16 pieces brought errors to 2.5e-6 .. 4e-6,
+// growing with the length, where the split kernel's are 4e-7.
 //
-// Roles: 8 warps for the softmax (T = 1: a thread a row; T = 3: two, half of
-// the keys each), 8 that unpack, in two groups with a tile each in turn, and
-// one that issues the products. Scores are computed two tiles ahead of the
-// weights, where tensor memory has the columns (one row tile), else one.
-// Raw tiles come by bulk copies, two of a group's ahead.
+// Roles: 8 warps for the softmax (a thread a row), 8 that unpack, in two groups
+// with a tile each in turn, and one that issues the products. Scores are
+// computed two tiles ahead of the outputs where tensor memory has the columns
+// (128 rows), else one. Raw tiles come by bulk copies, two of a group's ahead.
 //
-// What bounds it, in clocks at dim 128, Q8_0 (the tensor cores need 1024 a
-// tile of 64 keys with two row tiles, 2300 in fp32):
-//   T = 1, 256 rows: 2600 a tile, most of it a softmax thread's 64 scores
-//     (tensor memory there and back, maximum, exponentials). Twice as many
-//     softmax warps have 72 registers a thread: 2900.
-//   T = 1, 128 rows: 1700, the unpacking warps' (5400 a group's tile before
-//     bulk copies, 2800 with).
-//   T = 3: 3500, unpacking V into three pieces and the products.
+// What bounds it, in clocks a tile at dim 128, Q8_0 (the tensor cores need 1024
+// with two row tiles and one piece):
+//   256 rows: 2600, most of it a softmax thread's 64 scores (tensor memory
+//     there and back, maximum, exponentials); 3500 with two pieces. Twice the
+//     softmax warps would have 72 registers a thread: slower (104 us for 74 of
+//     a 64-sequence batch over 32768 shared keys).
+//   128 rows: 1600, the unpacking warps', of which a group spends 2800 on its
+//     tile (5400 with 16-byte copies by every thread).
 // Before a part's first scores come some 20000 (page ids, the part's scales,
 // the first tile, and instructions seen for the first time: hence the rolled
 // loops outside the tiles'), after its last weights 6000 for the results.
 // Whole calls, 8 KV heads over 32768 keys: 256 bf16 rows 64 us (34 GFLOP, 530
-// TFLOP/s), 128 bf16 rows 45 us, 128 fp32 rows 71 us.
-//
+// TFLOP/s), 128 bf16 rows 46 us, 256 fp16 rows 78 us.
 // Work is cut as in kv_attn.cuh: units of 64 keys, one CTA an SM.
 #pragma once
 
@@ -48,15 +44,15 @@
 namespace xq {
 
 constexpr int kTileRows = 128;  // of one accumulator
-// Rows of a pair's chunk: two tiles for 16-bit queries, one for fp32 ones.
-constexpr int tile_rows(bool exact) { return exact ? kTileRows : 2 * kTileRows; }
+constexpr int kTileChunk = 2 * kTileRows;  // rows of a pair's chunk, two tiles
 constexpr int kTileKeys = 64;
 static_assert(kTileKeys == kAttnUnit, "both kernels cut the line in the same units");
-constexpr int kTileSoft = 8, kTileConv = 8;  // warps
-constexpr int kTileWarps = kTileSoft + kTileConv + 1;
+constexpr int kTileSoft = 4, kTileConv = 8;  // warps: of a row tile's softmax; that unpack
+constexpr int kTileWarps = 2 * kTileSoft + kTileConv + 1;
 constexpr int kTileHead = 6;  // units of time a pair costs besides its keys
 
-template <int BITS, int D, int T>
+// P: fp16 pieces of K and of V, 2 where outputs are fp16.
+template <int BITS, int D, int P>
 struct TileShape {
   static constexpr int NB = D / 32;
   static constexpr int kRow = D * BITS / 8, kChunks = kRow / 16, kWords = kRow / 4;
@@ -66,33 +62,25 @@ struct TileShape {
   static constexpr int kKLbo = kTileKeys / 8 * kSbo + 16, kVLbo = D / 8 * kSbo;
   static constexpr int kOperand = D / 8 * kKLbo;  // one piece of K or of V: 64 keys x dim
   static_assert(kOperand >= kTileKeys / 8 * kVLbo && kOperand % 16 == 0, "V's is the smaller");
-  static constexpr int kKPieces = T == 1 ? 1 : 2, kVPieces = T;  // fp16 ones of q and K, those of the weights and V
   static constexpr int kBufs = 2;  // of K and of V
-  static constexpr int kTiles = T == 1 ? 2 : 1;  // row tiles
-  static constexpr int kRows = kTiles * kTileRows;
-  static constexpr int kSoftWarps = kTileSoft / kTiles;  // of a row tile
   static constexpr int kRawCodes = kTileKeys * kRow, kRawScales = kTileKeys * NB * 2;
   static constexpr int kRaw = 2 * (kRawCodes + kRawScales);
-  static constexpr int kOffV = kBufs * kKPieces * kOperand, kOffRaw = kOffV + kBufs * kVPieces * kOperand;
-  // The tile's scales, ready for use: K's [64][NB] fp16, V's [NB][64] fp16 or (T = 3) fp32.
-  static constexpr int kScaleK = kTileKeys * NB * 2;
-  static constexpr int kScales = kScaleK + kTileKeys * NB * (T == 1 ? 2 : 4);  // a table for each group
-  // Raw stages of a group of unpacking warps: two, or the one that the pieces of Q8_0 at dim 128 leave room for.
-  static constexpr int kRawStages = kOffRaw + 4 * kRaw + 2 * kScales <= 227 * 1024 - 1536 ? 2 : 1;
+  static constexpr int kOffV = kBufs * P * kOperand, kOffRaw = kOffV + kBufs * P * kOperand;
+  // The tile's scales, ready for use: K's [64][NB], V's [NB][64], fp16.
+  static constexpr int kScaleK = kTileKeys * NB * 2, kScales = 2 * kScaleK;  // a table for each group
+  static constexpr int kRawStages = 2;  // of a group of unpacking warps
   static constexpr int kOffScale = kOffRaw + 2 * kRawStages * kRaw;
   static constexpr int kSmem = kOffScale + 2 * kScales;
-  // Tensor memory columns: queries (of two row tiles, or two pieces), scores (of two row tiles, or two buffers), weights,
-  // outputs. With two row tiles the weights take the scores' columns, which the row's thread has read by then.
-  static constexpr int kColS = D, kColP = T == 1 ? kColS : kColS + 2 * kTileKeys;
-  static constexpr int kColO = T == 1 ? kColS + 2 * kTileKeys : kColP + T * kTileKeys / 2;
-  static constexpr int kCols = kColO + kTiles * D;
+  // Tensor memory columns: queries and scores of the two row tiles (or two buffers of scores of one), outputs. The weights
+  // take the scores' columns, which the row's thread has read by then.
+  static constexpr int kColS = D, kColO = kColS + 2 * kTileKeys, kCols = kColO + 2 * D;
   static constexpr int kAlloc = kCols <= 256 ? 256 : 512;
   static_assert(kCols <= 512 && kSmem <= 227 * 1024 - 1536, "one CTA fits the SM");  // and its static shared memory
 };
 
 template <int D>
 struct KvTileDim {
-  static cudaError_t launch(SplitArgs& a, int bits, bool exact, cudaStream_t s);
+  static cudaError_t launch(SplitArgs& a, int bits, bool two_pieces, cudaStream_t s);
   static cudaError_t take_error(unsigned int* index, unsigned int* wait);
 };
 
@@ -103,7 +91,7 @@ namespace {
 __device__ unsigned int g_kv_tile_error;  // a wait that ran out
 constexpr long long kTileWait = 1ll << 32;
 
-// Barriers: of each row tile (Q), of each scores buffer (S; T = 1: P and O, its weights and their products) and of each
+// Barriers: of each row tile (Q), of each scores buffer (S; P and O, its weights and their products) and of each
 // operand buffer and raw stage, as a barrier's parity tells a phase only from the next.
 enum TileBar { kBarDrain, kBarQ, kBarS = kBarQ + 2, kBarP = kBarS + 2, kBarO = kBarP + 2, kBarK = kBarO + 2, kBarKFree = kBarK + 2,
                kBarV = kBarKFree + 2, kBarVFree = kBarV + 2, kBarRaw = kBarVFree + 2, kBars = kBarRaw + 4 };
@@ -119,30 +107,12 @@ __device__ __forceinline__ bool group_any(int id, int threads, bool p) {
   return r != 0;
 }
 
-// Loads and stores of tensor memory are a whole warp's: __syncwarp() where its threads may have parted.
-// 32 lanes x 8 consecutive columns (the first 8 words of v).
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
+// Loads and stores of tensor memory are a whole warp's: hence __syncwarp() where its threads may have parted.
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
-}
-
-// Two floats' bf16 pieces by cutting off, each pair packed (a in the low half).
-__device__ __forceinline__ void cut3(ptx::f2 v, uint32_t (&w)[3]) {
-  const ptx::f2 minus = ptx::pk(-1.0f, -1.0f);
-  const uint32_t a = __float_as_uint(ptx::lo32(v)), b = __float_as_uint(ptx::hi32(v));
-  const ptx::f2 r = ptx::fma2(ptx::pk(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u)), minus, v);
-  const uint32_t c = __float_as_uint(ptx::lo32(r)), d = __float_as_uint(ptx::hi32(r));
-  const ptx::f2 s = ptx::fma2(ptx::pk(__uint_as_float(c & 0xFFFF0000u), __uint_as_float(d & 0xFFFF0000u)), minus, r);
-  w[0] = prmt(a, b, 0x7632u);
-  w[1] = prmt(c, d, 0x7632u);
-  w[2] = prmt(__float_as_uint(ptx::lo32(s)), __float_as_uint(ptx::hi32(s)), 0x7632u);
 }
 
 // Bytes (0, 1) and (2, 3) of w as fp16 pairs u - 128 or u - 8.
@@ -153,24 +123,23 @@ __device__ __forceinline__ void code_halves(uint32_t w, uint32_t (&h)[2]) {
   h[1] = ptx::hsub2(prmt(w, 0x64646464u, 0x4342u), off);
 }
 
-template <int BITS, int D, int T>
+template <int BITS, int D, int P>
 __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __grid_constant__ SplitArgs A) {
-  using S = TileShape<BITS, D, T>;
+  using S = TileShape<BITS, D, P>;
   constexpr int NB = S::NB;
   extern __shared__ __align__(256) uint8_t smem[];
   __shared__ LineShared sh_line;
   __shared__ __align__(8) uint64_t bars[kBars];
   __shared__ uint32_t sh_tmem;
   __shared__ unsigned sh_bad[4];            // tile's 16-key groups without a valid page, by tile & 3
-  __shared__ unsigned sh_top[4][1 + NB];    // T = 1: largest |scale| of the part: K's, V's blocks (fp32 bits), by part & 3
-  __shared__ float sh_x[2][kTileRows];      // exchange between a row's two threads
+  __shared__ unsigned sh_top[4][1 + NB];    // largest |scale| of the part: K's, V's blocks (fp32 bits), by part & 3
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto bar = [&](int i) { return ptx::smem_addr(&bars[i]); };
   if (tid == 0) {
     for (int b = 0; b < 2; ++b) {
-      ptx::mbar_init(bar(kBarQ + b), S::kSoftWarps);
+      ptx::mbar_init(bar(kBarQ + b), kTileSoft);
       ptx::mbar_init(bar(kBarS + b), 1);
-      ptx::mbar_init(bar(kBarP + b), S::kSoftWarps);
+      ptx::mbar_init(bar(kBarP + b), kTileSoft);
       ptx::mbar_init(bar(kBarO + b), 1);
       ptx::mbar_init(bar(kBarK + b), kTileConv / 2);
       ptx::mbar_init(bar(kBarKFree + b), 1);
@@ -202,7 +171,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
   const uint32_t base = ptx::smem_addr(smem);
   // Two buffers of scores: of the two row tiles, or taken in turn by the only one. The buffer of row tile r's n-th tile, and
   // how often it was used before.
-  const bool two = S::kTiles == 2 && A.rows > kTileRows;
+  const bool two = A.rows > kTileRows;
   auto buffer = [&](int r, unsigned n) { return two ? r : static_cast<int>(n & 1); };
   auto turn = [&](unsigned n) { return two ? n : n >> 1; };
   Part part;
@@ -211,11 +180,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
     // ------------------------------------------------ products (issued by one thread). The whole warp walks through the tiles,
     // so that the operands' addresses are its uniform values when the thread comes to the products: one a product, added to
     // a tile's descriptor, not built anew (77 clocks a product otherwise, more than the 32 to 64 it takes).
-    constexpr uint32_t idS = ptx::idesc_f16(kTileRows, kTileKeys, false), idO = ptx::idesc_f16(kTileRows, D, T == 3);
-    // pairs of pieces (A's, B's)
-    constexpr int kSPairs = T == 3 ? 3 : 1, kOPairs = T == 3 ? 6 : 1;
-    constexpr int sa[3] = {0, 0, 1}, sb[3] = {0, 1, 0};
-    constexpr int oa[6] = {0, 0, 1, 0, 1, 2}, ob[6] = {0, 1, 0, 2, 1, 0};
+    constexpr uint32_t idS = ptx::idesc_f16(kTileRows, kTileKeys, false), idO = ptx::idesc_f16(kTileRows, D, false);
     // Scores are computed this many tiles ahead of the outputs.
     const unsigned ahead = two ? 1 : 2;
     const bool lead = ptx::elect_one();
@@ -232,13 +197,13 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       const int to = buffer(r, scored[r]++);
       const uint32_t d = __shfl_sync(0xffffffffu, at + S::kColS + to * kTileKeys, 0);
       const uint32_t a = __shfl_sync(0xffffffffu, at + r * (D / 2), 0);
-      const uint64_t kd = k_desc + __shfl_sync(0xffffffffu, b * (S::kKPieces * S::kOperand / 16), 0);
+      const uint64_t kd = k_desc + __shfl_sync(0xffffffffu, b * (P * S::kOperand / 16), 0);
       if (lead) {
 #pragma unroll
-        for (int p = 0; p < kSPairs; ++p)
+        for (int p = P - 1; p >= 0; --p)  // the smaller piece first
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            ptx::mma_f16_ts(d, a + sa[p] * (D / 2) + 8 * k, kd + (sb[p] * S::kOperand + 2 * k * S::kKLbo) / 16, idS, p + k > 0);
+            ptx::mma_f16_ts(d, a + 8 * k, kd + (p * S::kOperand + 2 * k * S::kKLbo) / 16, idS, p < P - 1 || k > 0);
         if (last) ptx::tc_commit(bar(kBarKFree + b));
         ptx::tc_commit(bar(kBarS + to));
       }
@@ -248,28 +213,27 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
     while (ok && line_next(A, line, part)) {
       const int tiles = part.k1 - part.k0;
       const int chunk = part.pair % A.chunks;
-      const int last = S::kTiles == 2 && A.rows - chunk * S::kRows > kTileRows ? 1 : 0;
+      const int last = A.rows - chunk * kTileChunk > kTileRows ? 1 : 0;
       for (int r = 0; r <= last && ok; ++r) ok = wait_all(kBarQ + r, parts[r]++, 2) && scores(r, it, r == last);
       if (ahead == 2 && ok && tiles > 1) ok = scores(0, it + 1, true);
       for (int i = 0; i < tiles && ok; ++i, ++it) {
         const unsigned b = it % S::kBufs;
         for (int r = 0; r <= last && ok; ++r) {
-          const int from = T == 1 ? buffer(r, done[r]) : 0;  // the weights'
-          ok = wait_all(kBarP + from, T == 1 ? turn(done[r]) : done[r], 3);
+          const int from = buffer(r, done[r]);  // the weights'
+          ok = wait_all(kBarP + from, turn(done[r]), 3);
           ++done[r];
           if (r == 0) ok = ok && wait_all(kBarV + b, it / S::kBufs, 4);
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t d = __shfl_sync(0xffffffffu, at + S::kColO + r * D, 0);
-          const uint32_t a = __shfl_sync(0xffffffffu, at + S::kColP + from * kTileKeys, 0);
-          const uint64_t vd = v_desc + __shfl_sync(0xffffffffu, b * (S::kVPieces * S::kOperand / 16), 0);
+          const uint32_t a = __shfl_sync(0xffffffffu, at + S::kColS + from * kTileKeys, 0);
+          const uint64_t vd = v_desc + __shfl_sync(0xffffffffu, b * (P * S::kOperand / 16), 0);
           if (lead) {
 #pragma unroll
-            for (int p = 0; p < kOPairs; ++p)
+            for (int p = P - 1; p >= 0; --p)
 #pragma unroll
               for (int k = 0; k < kTileKeys / 16; ++k)
-                ptx::mma_f16_ts(d, a + oa[p] * (kTileKeys / 2) + 8 * k, vd + (ob[p] * S::kOperand + 2 * k * S::kVLbo) / 16, idO,
-                                i > 0 || p + k > 0);
+                ptx::mma_f16_ts(d, a + 8 * k, vd + (p * S::kOperand + 2 * k * S::kVLbo) / 16, idO, i > 0 || p < P - 1 || k > 0);
             if (r == last) ptx::tc_commit(bar(kBarVFree + b));
             ptx::tc_commit(bar(kBarO + from));
           }
@@ -280,7 +244,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
     }
     if (lead) ptx::tc_commit(bar(kBarDrain));  // nothing is in flight when tensor memory is freed
     wait(kBarDrain, 0, 5);
-  } else if (T == 1 && warp < kTileSoft) {
+  } else if (warp < 2 * kTileSoft) {
     // ------------------------- softmax, two row tiles: a thread is a row; no thread needs another
     constexpr float kTop = 15.0f, kStart = 11.0f;  // log2 of weights: the largest, and where the reference starts anew
     const int r = warp >> 2, row = r * kTileRows + (warp & 3) * 32 + lane;
@@ -290,7 +254,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
     bool ok = true, left_record = false;
     for (; ok && line_next(A, line, part); ++parts) {
       const int head = part.pair / A.chunks, chunk = part.pair - head * A.chunks;
-      const int row0 = chunk * S::kRows, tiles = part.k1 - part.k0;
+      const int row0 = chunk * kTileChunk, tiles = part.k1 - part.k0;
       if (row0 + r * kTileRows >= A.rows) {  // not this row tile's
         it += tiles;
         continue;
@@ -435,7 +399,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       const float sum = ptx::lo32(l) + ptx::hi32(l);
       const bool whole = part.k0 == 0 && part.k1 == part.nu;
       if (A.late && whole) grid_wait();
-      const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (part.k0 == 0 ? 1 : 0)) * S::kRows + row;
+      const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (part.k0 == 0 ? 1 : 0)) * kTileChunk + row;
 #pragma unroll 1
       for (int c = 0; c < D; c += 16) {
         uint32_t w[16];
@@ -451,7 +415,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             if (whole)
               finish4(A, D, at, c + x, y, e, sum);
             else
-              *reinterpret_cast<float4*>(A.part_o + (slot - row) * D + (c + x) * S::kRows + row * 4) = y;
+              *reinterpret_cast<float4*>(A.part_o + (slot - row) * D + (c + x) * kTileChunk + row * 4) = y;
           }
         }
       }
@@ -463,193 +427,11 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       ptx::tc_fence_before();
     }
     if (!left_record && tid == 0 && !A.whole) A.record[blockIdx.x] = make_int4(0, 0, -1, 0);
-  } else if (T == 3 && warp < kTileSoft) {
-    // ------------------------- softmax, one row tile: a row's 64 keys in two threads
-    constexpr int kThreads = 32 * kTileSoft, kBarrier = 1;
-    constexpr float kTop = 40.0f, kStart = 0.0f;  // log2 of weights: the largest, and where the reference starts anew
-    const int half = warp >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    unsigned it = 0, parts = 0;
-    bool fail = false, go = true, left_record = false;
-    while (go && line_next(A, line, part)) {
-      const int head = part.pair / A.chunks, chunk = part.pair - head * A.chunks;
-      const int row0 = chunk * S::kRows;
-      const bool live = row0 + row < A.rows;
-      const size_t at = live ? row_at(A, part.seq, head, row0 + row) : 0;
-      int lim0 = 0, lim1 = 0;
-      if (live) row_range(A, part.seq, part.n, row0 + row, &lim0, &lim1);
-      // ---- this thread's half of the row's query into tensor memory: two fp16 numbers, the row's largest element at
-      // 2^12 .. 2^13; negated for a negative scale (so that cs > 0)
-      const float4* const from = reinterpret_cast<const float4*>(static_cast<const float*>(A.q) + at * D + half * (D / 2));
-      float largest = 0.0f;
-      float4 qv[D / 8];  // all of it at once: one round trip to memory
-#pragma unroll
-      for (int x = 0; x < D / 8; ++x) qv[x] = live ? from[x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int x = 0; x < D / 8; ++x)
-        largest = fmaxf(fmaxf(largest, fmaxf(fabsf(qv[x].x), fabsf(qv[x].y))), fmaxf(fabsf(qv[x].z), fabsf(qv[x].w)));
-      sh_x[half][row] = largest;
-      if (group_any(kBarrier, kThreads, fail)) break;
-      largest = fmaxf(largest, sh_x[half ^ 1][row]);
-      int ex = static_cast<int>(__float_as_uint(largest) >> 23) - 127;
-      ex = ex < -100 ? -100 : ex;
-      const float up = (A.scale < 0.0f ? -1.0f : 1.0f) * __uint_as_float(static_cast<unsigned>(127 + 12 - ex) << 23);
-      float cs = fabsf(A.scale) * 1.4426950408889634f * __uint_as_float(static_cast<unsigned>(127 - 12 + ex) << 23);
-#pragma unroll 1
-      for (int c = 0; c < D / 4; c += 8) {
-        uint32_t w[2][16];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float4 u = live ? from[c / 2 + x] : make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = make_float4(u.x * up, u.y * up, u.z * up, u.w * up);
-          const uint32_t h0 = half2_of(v.x, v.y), h1 = half2_of(v.z, v.w);
-          const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-          const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-          w[0][2 * x] = h0;
-          w[0][2 * x + 1] = h1;
-          w[1][2 * x] = half2_of(v.x - f0.x, v.y - f0.y);
-          w[1][2 * x + 1] = half2_of(v.z - f1.x, v.w - f1.y);
-        }
-        __syncwarp();
-#pragma unroll
-        for (int p = 0; p < 2; ++p) tmem_st8(tl + p * (D / 2) + half * (D / 4) + c, w[p]);
-      }
-      ptx::tmem_wait_st();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(kBarQ));
-
-      const int tiles = part.k1 - part.k0;
-      int key = (first_unit(A, part.n) + part.k0) * kTileKeys + half * 32;
-      float e = -1e30f;
-      ptx::f2 l = ptx::pk(0.0f, 0.0f);
-      for (int i = 0; i < tiles; ++i, ++it, key += kTileKeys) {
-        fail |= !wait_sleep(kBarS + (it & 1), it >> 1, 6);
-        ptx::tc_fence_after();
-        if (i == 0) {  // K's power of two, known once its first tile is there
-          const unsigned t0 = sh_top[parts & 3][0];
-          cs = fmaxf(cs * __uint_as_float((t0 >> 23 < 253 ? (t0 >> 23) + 1 : 254u) << 23), 1.17549435e-38f);
-        }
-        uint32_t sv[2][16];
-        __syncwarp();
-        ptx::tmem_ld16(tl + S::kColS + (it & 1) * kTileKeys + half * 32, sv[0]);
-        ptx::tmem_ld16(tl + S::kColS + (it & 1) * kTileKeys + half * 32 + 16, sv[1]);
-        ptx::tmem_wait_ld();
-        const unsigned bad = sh_bad[it & 3] >> (2 * half) & 3u;
-        if (key < lim0 || key + 32 > lim1 || bad) {
-#pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (key + x < lim0 || key + x >= lim1 || (bad >> (x >> 4) & 1)) sv[x >> 4][x & 15] = 0xFF800000u;
-        }
-        float tops4[4];  // four chains: the row's thread has nothing else to do meanwhile
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          tops4[x] = __uint_as_float(sv[x >> 1][8 * (x & 1)]);
-#pragma unroll
-          for (int y = 1; y < 7; y += 2)
-            tops4[x] = max3(tops4[x], __uint_as_float(sv[x >> 1][8 * (x & 1) + y]), __uint_as_float(sv[x >> 1][8 * (x & 1) + y + 1]));
-          tops4[x] = fmaxf(tops4[x], __uint_as_float(sv[x >> 1][8 * (x & 1) + 7]));
-        }
-        float top = fmaxf(fmaxf(tops4[0], tops4[1]), fmaxf(tops4[2], tops4[3])) * cs;
-        if (group_any(kBarrier, kThreads, top - e > kTop || fail)) {
-          // ---- some row's reference moves (or a wait ran out): both threads of a row agree on the new one
-          sh_x[half][row] = top;
-          if (group_any(kBarrier, kThreads, fail)) {
-            go = false;
-            break;
-          }
-          top = fmaxf(top, sh_x[half ^ 1][row]);
-          const float next = top - e > kTop ? top - kStart : e, f = ex2(e - next);
-          e = next;
-          l = ptx::mul2(l, ptx::pk(f, f));
-          if (i > 0) {
-            fail |= !wait(kBarO, it - 1, 7);
-            ptx::tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D / 2; c += 16) {
-              uint32_t w[16];
-              __syncwarp();
-              ptx::tmem_ld16(tl + S::kColO + half * (D / 2) + c, w);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(__uint_as_float(w[x]) * f);
-              ptx::tmem_st16(tl + S::kColO + half * (D / 2) + c, w);
-            }
-          }
-        }
-        // ---- weights
-        uint32_t w[3][16];
-        const ptx::f2 c2 = ptx::pk(cs, cs), e2 = ptx::pk(-e, -e);
-#pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-          const ptx::f2 z = ptx::fma2(ptx::pk(__uint_as_float(sv[x >> 4][x & 15]), __uint_as_float(sv[x >> 4][(x & 15) + 1])), c2, e2);
-          const float a = ex2(ptx::lo32(z)), d = ex2(ptx::hi32(z));
-          l = ptx::add2(l, ptx::pk(a, d));
-          uint32_t u[3];
-          cut3(ptx::pk(a, d), u);
-          w[0][x / 2] = u[0];
-          w[1][x / 2] = u[1];
-          w[2][x / 2] = u[2];
-        }
-        // ---- and their operand, whose buffer is free once the products that used it last are done
-        if (i > 0) {
-          fail |= !wait(kBarO, it - 1, 8);
-          ptx::tc_fence_after();
-        }
-        __syncwarp();
-#pragma unroll
-        for (int p = 0; p < 3; ++p) ptx::tmem_st16(tl + S::kColP + p * (kTileKeys / 2) + half * 16, w[p]);
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(kBarP));
-      }
-      if (!go) break;
-      // ---- the part's results
-      fail |= !wait_sleep(kBarO, it - 1, 9);
-      ptx::tc_fence_after();
-      float sum = ptx::lo32(l) + ptx::hi32(l);
-      sh_x[half][row] = sum;
-      if (group_any(kBarrier, kThreads, fail)) break;
-      sum = half ? sh_x[0][row] + sum : sum + sh_x[1][row];
-      const bool whole = part.k0 == 0 && part.k1 == part.nu;
-      if (A.late && whole) grid_wait();
-      const size_t slot = (static_cast<size_t>(blockIdx.x) * 2 + (part.k0 == 0 ? 1 : 0)) * S::kRows + row;
-#pragma unroll 1
-      for (int c = 0; c < D / 2; c += 16) {
-        uint32_t w[16];
-        const int d0 = half * (D / 2) + c;
-        __syncwarp();
-        ptx::tmem_ld16(tl + S::kColO + d0, w);
-        ptx::tmem_wait_ld();
-        if (live) {
-#pragma unroll
-          for (int x = 0; x < 16; x += 4) {
-            const float4 y = make_float4(__uint_as_float(w[x]), __uint_as_float(w[x + 1]), __uint_as_float(w[x + 2]),
-                                         __uint_as_float(w[x + 3]));
-            if (whole) {
-              finish4(A, D, at, d0 + x, y, e, sum);
-            } else {
-              *reinterpret_cast<float4*>(A.part_o + (slot - row) * D + (d0 + x) * S::kRows + row * 4) = y;
-              if (d0 + x == 0) *reinterpret_cast<float2*>(A.part_el + slot * 2) = make_float2(e, sum);
-            }
-          }
-        }
-      }
-      if (!whole && part.k0 == 0) {
-        left_record = true;
-        if (tid == 0) A.record[blockIdx.x] = make_int4(part.seq, part.pair, line_last(A, line, part), 0);
-      }
-      ptx::tc_fence_before();
-      // the other half's sums have been read when the next barrier is passed
-      group_any(kBarrier, kThreads, false);
-      ++parts;
-    }
-    if (!left_record && tid == 0 && !A.whole) A.record[blockIdx.x] = make_int4(0, 0, -1, 0);
   } else {
     // ------------------------------------------------ copying and unpacking
     // Two groups of four warps, each a tile: one's copies and barriers pass while the other unpacks.
     constexpr int kThreads = 32 * kTileConv, kGroup = kThreads / 2, kBarrier = 2;
-    const int ct = tid - 32 * kTileSoft, group = ct / kGroup, gt = ct - group * kGroup;
+    const int ct = tid - 64 * kTileSoft, group = ct / kGroup, gt = ct - group * kGroup;
     const int group_shift = A.c.page_shift - 4, groups_page = 1 << group_shift;  // 16-key groups a page
     const int run = groups_page < 4 ? groups_page : 4;                          // those of a tile that lie in one page
     unsigned filled = 0, coming = 0;  // of the raw stages: phases' parities, copies on their way
@@ -713,7 +495,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
 #pragma unroll
       for (int b = 0; b < NB; ++b) vf[b] = 1.0f;
       {
-        // ---- the part's largest scales (K's; T = 1: V's too): 1 / 17 or 1 / 9 of its bytes, which its tiles then find in L2
+        // ---- the part's largest scales: 1 / 17 or 1 / 9 of its bytes, which its tiles then find in L2
         unsigned* const tops = sh_top[parts & 3];
         if (ct <= NB) tops[ct] = 0u;
         if (group_any(kBarrier, kThreads, fail)) break;
@@ -737,7 +519,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             if (!page[y]) continue;
             const uint8_t* const p = reinterpret_cast<const uint8_t*>(page[y]) + A.c.scale_off + row_of(gi) * (2 * NB) + piece * 16;
             k4[y] = *reinterpret_cast<const uint4*>(p);
-            if (T == 1) v4[y] = *reinterpret_cast<const uint4*>(p + v_off);
+            v4[y] = *reinterpret_cast<const uint4*>(p + v_off);
           }
 #pragma unroll
           for (int y = 0; y < kAhead; ++y) {
@@ -755,7 +537,6 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
               kt = __hmax2_nan(kt, __habs2(*reinterpret_cast<const __half2*>(&kw[h])));
-              if (T == 3) continue;
               const __half2 a = __habs2(*reinterpret_cast<const __half2*>(&vw[h]));
               if (NB % 2 == 0) {
                 vt[h % (NB / 2 > 0 ? NB / 2 : 1)] = __hmax2_nan(vt[h % (NB / 2 > 0 ? NB / 2 : 1)], a);
@@ -784,12 +565,12 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         auto down = [](unsigned t) { return __uint_as_float((t >> 23 < 253 ? 253 - (t >> 23) : 0u) << 23); };
         kf = down(tops[0]);
 #pragma unroll
-        for (int b = 0; b < NB && T == 1; ++b) vf[b] = down(tops[1 + b]);
+        for (int b = 0; b < NB; ++b) vf[b] = down(tops[1 + b]);
       }
 
       uint8_t* const scales = smem + S::kOffScale + group * S::kScales;
       const unsigned it0 = it;
-      for (int i = group, stage = 0; i < tiles; i += 2, stage ^= S::kRawStages - 1) {
+      for (int i = group, stage = 0; i < tiles; i += 2, stage ^= 1) {
         it = it0 + i;
         fail |= !wait_sleep(kBarRaw + 2 * group + stage, filled >> stage, 12);
         filled ^= 1u << stage;
@@ -797,7 +578,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         // the group's last tile has been unpacked
         if (group_any(kBarrier + 1 + group, kGroup, fail)) break;
         miss = next_miss;
-        if (S::kRawStages == 2) issue(i + 2, stage ^ 1);
+        issue(i + 2, stage ^ 1);
         const uint8_t* const raw = smem + S::kOffRaw + (S::kRawStages * group + stage) * S::kRaw;
         const int left = part.n - (unit0 + i) * kTileKeys;  // keys of the sequence from the tile's first on
         // ---- scales: scaled, and 0 for keys that are not there (whose codes may be anything)
@@ -810,17 +591,14 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           for (int q = 1; q < NB; ++q) f = blk == q ? vf[q] : f;
           const float dk = gone ? 0.0f : __half2float(kd[x]) * kf, dv = gone ? 0.0f : __half2float(kd[S::kRawScales / 2 + x]) * f;
           reinterpret_cast<__half*>(scales)[x] = __float2half_rn(dk);
-          if (T == 1)
-            reinterpret_cast<__half*>(scales + S::kScaleK)[blk * kTileKeys + key] = __float2half_rn(dv);
-          else
-            reinterpret_cast<float*>(scales + S::kScaleK)[blk * kTileKeys + key] = dv;
+          reinterpret_cast<__half*>(scales + S::kScaleK)[blk * kTileKeys + key] = __float2half_rn(dv);
         }
         group_any(kBarrier + 1 + group, kGroup, false);
         // ---- K: operand rows are keys. A task is a key's 16-byte chunk
         const unsigned b = it % S::kBufs, turn = it / S::kBufs;  // tiles take the buffers, and the groups the tiles, in turn
         if (turn > 0) fail |= !wait_sleep(kBarKFree + b, turn - 1, 10);
         if (gt == 0) sh_bad[it & 3] = miss;
-        uint8_t* const ko = smem + b * S::kKPieces * S::kOperand;
+        uint8_t* const ko = smem + b * P * S::kOperand;
 #pragma unroll
         for (int x = 0; x < (kTileKeys * S::kChunks + kGroup - 1) / kGroup; ++x) {
           const int c = x * kGroup + gt, key = c / S::kChunks, ch = c - key * S::kChunks;
@@ -841,7 +619,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
 #pragma unroll
               for (int q = 0; q < 4; ++q) v[q] = ptx::hmul2(h[q], dd);
               *reinterpret_cast<uint4*>(cell) = make_uint4(v[0], v[1], v[2], v[3]);
-              if (T == 3) {  // what the rounding left, exact
+              if (P == 2) {  // what the rounding left, exact
 #pragma unroll
                 for (int q = 0; q < 4; ++q) v[q] = hfma2_of(h[q], dd, v[q] ^ 0x80008000u);
                 *reinterpret_cast<uint4*>(cell + S::kOperand) = make_uint4(v[0], v[1], v[2], v[3]);
@@ -854,35 +632,15 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         if (lane == 0) ptx::mbar_arrive(bar(kBarK + b));
         // ---- V: operand rows are elements. A task is a word (4 code bytes) of 8 keys
         if (turn > 0) fail |= !wait_sleep(kBarVFree + b, turn - 1, 11);
-        constexpr int kVUnroll = T == 1 ? 1 : 2;  // short code where it does not cost time
-        uint8_t* const vo = smem + S::kOffV + b * S::kVPieces * S::kOperand;
-#pragma unroll kVUnroll
+        uint8_t* const vo = smem + S::kOffV + b * P * S::kOperand;
+#pragma unroll 1
         for (int x = 0; x < (8 * S::kWords + kGroup - 1) / kGroup; ++x) {
           const int c = x * kGroup + gt, kg = c / S::kWords, word = c - kg * S::kWords;
           if (kg < 8) {
             const int blk = BITS == 8 ? word / 8 : word / 4;
             uint32_t u[8];
-            float d[8];        // T = 3: the 8 keys' scales of the block
-            uint32_t d2[4];    // T = 1: as fp16 pairs
-            if (T == 1) {
-              const uint4 r = *reinterpret_cast<const uint4*>(scales + S::kScaleK + (blk * kTileKeys + kg * 8) * 2);
-              d2[0] = r.x;
-              d2[1] = r.y;
-              d2[2] = r.z;
-              d2[3] = r.w;
-            } else {
-              const float4* const r =
-                  reinterpret_cast<const float4*>(scales + S::kScaleK + (blk * kTileKeys + kg * 8) * 4);
-              const float4 a = r[0], c4 = r[1];
-              d[0] = a.x;
-              d[1] = a.y;
-              d[2] = a.z;
-              d[3] = a.w;
-              d[4] = c4.x;
-              d[5] = c4.y;
-              d[6] = c4.z;
-              d[7] = c4.w;
-            }
+            const uint4 d4 = *reinterpret_cast<const uint4*>(scales + S::kScaleK + (blk * kTileKeys + kg * 8) * 2);
+            const uint32_t d2[4] = {d4.x, d4.y, d4.z, d4.w};  // the 8 keys' scales of the block
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               u[k] = *reinterpret_cast<const uint32_t*>(raw + S::kRawCodes + (kg * 8 + k) * S::kRow + word * 4);
@@ -894,51 +652,32 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
               uint32_t v[8];
 #pragma unroll
               for (int k = 0; k < 8; ++k) v[k] = BITS == 8 ? u[k] : (u[k] >> (4 * z)) & 0x0F0F0F0Fu;
-              if (T == 1) {
-                uint32_t r[4][4];  // [element][key pair]
+              uint32_t r[P][4][4];  // [piece][element][key pair]
 #pragma unroll
-                for (int k = 0; k < 8; k += 2) {
-                  const uint32_t lo = prmt(v[k], v[k + 1], 0x5140u), hi = prmt(v[k], v[k + 1], 0x7362u);
-                  const uint32_t dd = d2[k / 2];
-                  uint32_t h0[2], h1[2];
-                  code_halves<BITS>(lo, h0);
-                  code_halves<BITS>(hi, h1);
-                  r[0][k / 2] = ptx::hmul2(h0[0], dd);
-                  r[1][k / 2] = ptx::hmul2(h0[1], dd);
-                  r[2][k / 2] = ptx::hmul2(h1[0], dd);
-                  r[3][k / 2] = ptx::hmul2(h1[1], dd);
-                }
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                  *reinterpret_cast<uint4*>(to + y * 16) = make_uint4(r[y][0], r[y][1], r[y][2], r[y][3]);
-              } else {
+              for (int k = 0; k < 8; k += 2) {
+                const uint32_t lo = prmt(v[k], v[k + 1], 0x5140u), hi = prmt(v[k], v[k + 1], 0x7362u);
+                const uint32_t dd = d2[k / 2];
+                uint32_t h[4];
+                code_halves<BITS>(lo, *reinterpret_cast<uint32_t(*)[2]>(&h[0]));
+                code_halves<BITS>(hi, *reinterpret_cast<uint32_t(*)[2]>(&h[2]));
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                  constexpr float off = BITS == 8 ? 8388736.0f : 8388616.0f;
-                  uint32_t r[4][3];
-#pragma unroll
-                  for (int k = 0; k < 8; k += 2) {
-                    const uint32_t sel = 0x7440u + y;
-                    const ptx::f2 u2 = ptx::add2(ptx::pk(__uint_as_float(prmt(v[k], 0x4B000000u, sel)),
-                                                         __uint_as_float(prmt(v[k + 1], 0x4B000000u, sel))),
-                                                 ptx::pk(-off, -off));
-                    cut3(ptx::mul2(u2, ptx::pk(d[k], d[k + 1])), r[k / 2]);
-                  }
-#pragma unroll
-                  for (int p = 0; p < 3; ++p)
-                    *reinterpret_cast<uint4*>(to + y * 16 + p * S::kOperand) = make_uint4(r[0][p], r[1][p], r[2][p], r[3][p]);
+                  r[0][y][k / 2] = ptx::hmul2(h[y], dd);
+                  if (P == 2) r[P - 1][y][k / 2] = hfma2_of(h[y], dd, r[0][y][k / 2] ^ 0x80008000u);
                 }
               }
+#pragma unroll
+              for (int q = 0; q < P; ++q)
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  *reinterpret_cast<uint4*>(to + q * S::kOperand + y * 16) =
+                      make_uint4(r[q][y][0], r[q][y][1], r[q][y][2], r[q][y][3]);
             }
           }
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(kBarV + b));
-        if (S::kRawStages == 1) {  // every thread has read the tile
-          group_any(kBarrier + 1 + group, kGroup, false);
-          issue(i + 2, 0);
-        }
       }
       it = it0 + tiles;
       ++parts;
@@ -958,12 +697,12 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
   if (A.late) grid_wait();
 }
 
-template <int BITS, int D, int T>
+template <int BITS, int D, int P>
 cudaError_t launch_tile_attn(SplitArgs& a, cudaStream_t s) {
-  using S = TileShape<BITS, D, T>;
+  using S = TileShape<BITS, D, P>;
   a.ctas = a.units < kNumSMs ? static_cast<int>(a.units) : kNumSMs;
   static const cudaError_t attr_error =
-      cudaFuncSetAttribute(kv_tile_kernel<BITS, D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+      cudaFuncSetAttribute(kv_tile_kernel<BITS, D, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (attr_error != cudaSuccess) return attr_error;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
@@ -975,21 +714,21 @@ cudaError_t launch_tile_attn(SplitArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_tile_kernel<BITS, D, T>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_tile_kernel<BITS, D, P>, a);
   if (e != cudaSuccess || a.whole) return e;
   constexpr int kRowsBlock = 4;
-  cfg.gridDim = join_grid<S::kRows, kRowsBlock>(a.ctas);
+  cfg.gridDim = join_grid<kTileChunk, kRowsBlock>(a.ctas);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, S::kRows, kRowsBlock, true>, a);
+  return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, kTileChunk, kRowsBlock, true>, a);
 }
 
 }  // namespace
 
 template <int D>
-cudaError_t KvTileDim<D>::launch(SplitArgs& a, int bits, bool exact, cudaStream_t s) {
-  if (bits == 8) return exact ? launch_tile_attn<8, D, 3>(a, s) : launch_tile_attn<8, D, 1>(a, s);
-  return exact ? launch_tile_attn<4, D, 3>(a, s) : launch_tile_attn<4, D, 1>(a, s);
+cudaError_t KvTileDim<D>::launch(SplitArgs& a, int bits, bool two_pieces, cudaStream_t s) {
+  if (bits == 8) return two_pieces ? launch_tile_attn<8, D, 2>(a, s) : launch_tile_attn<8, D, 1>(a, s);
+  return two_pieces ? launch_tile_attn<4, D, 2>(a, s) : launch_tile_attn<4, D, 1>(a, s);
 }
 
 template <int D>

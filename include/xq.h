@@ -516,9 +516,9 @@ XQ_API size_t xq_kv_attn_workspace_bytes(const xq_kv_cache *cache, const xq_kv_q
  * statistics and sums are fp32. fp32 queries and their weights enter the
  * tensor cores as two fp16 numbers each (22 bits), 16-bit ones and their
  * weights as one; the stored codes are exact there, and block scales are
- * applied in fp32. Where many rows (64 or more) read a head's many keys, K and
- * V enter with their scales: as one fp16 number for 16-bit queries, without
- * loss for fp32 ones, whose weights and V are then three bf16 numbers each.
+ * applied in fp32. Where many 16-bit rows (64 or more) read a head's many
+ * keys, K and V enter with their scales, without loss for fp16 queries and
+ * rounded to fp16 for bf16 ones.
  * Results do not depend on what the slots past a sequence's length hold. They
  * depend on the other sequences of the call only through where a long
  * sequence is cut into parts (in rounding).
