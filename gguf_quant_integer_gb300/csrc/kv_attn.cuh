@@ -24,7 +24,7 @@
 // against 4 instructions. A warp's 16 keys cost some 420 instructions, so long
 // Q8_0 caches are bound by HBM and Q4_0's nearly as much by instructions: 64
 // sequences, 230000 tokens in all, 8 KV heads, fp32: 84 us, 5.9 TB/s with the
-// join; one sequence of 131071 Q4_0 tokens, bf16: 38 us, 4.0 TB/s, of which 5
+// join; one sequence of 131071 Q4_0 tokens, bf16: 37 us, 4.1 TB/s, of which 4
 // are the join and 5 pass before the first tile's products. Short calls are
 // bound by latency: one sequence of 97 tokens 5.5 us (10000 clocks: 3000 to
 // find the work, 3000 for queries and the first tile, 1000 to 1500 a tile).
@@ -1039,6 +1039,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
 // Two blocks an SM, with 6 loads in flight a thread (one block with 8: 64 sequences of 211 to 8192 tokens 85.8 us instead
 // of 83.9, a prefix of 32768 tokens for 64 sequences 96.6 instead of 91.6; three with 2 to 4 help or cost as much).
 constexpr int kJoinThreads = 512, kJoinBlocks = 2, kJoinBatch = 6;
+// Parts a pair from which a block takes one row (57 parts: 37.2 us for 38.5 of a 131071-token sequence; 9 parts of 8 rows:
+// 17.9 for 16.8 of 8 sequences behind a 1000-token prefix).
+constexpr int kJoinMany = 24;
 template <int D, int R, int RB, bool COLS>
 __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) kv_join_kernel(const __grid_constant__ SplitArgs A) {
   constexpr int kLanes = RB * D / 4;
@@ -1144,9 +1147,14 @@ cudaError_t launch_split(SplitArgs& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_split_kernel<BITS, D, EX, NP, NT>, a);
   if (e != cudaSuccess || a.whole) return e;
-  cfg.gridDim = join_grid<S::R, S::R>(a.ctas);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
+  // A block a row where pairs have many parts, for more of them at a time.
+  if (a.ctas >= kJoinMany * static_cast<long long>(a.seqs) * a.c.heads * a.chunks) {
+    cfg.gridDim = join_grid<S::R, 1>(a.ctas);
+    return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, S::R, 1, false>, a);
+  }
+  cfg.gridDim = join_grid<S::R, S::R>(a.ctas);
   return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, S::R, S::R, false>, a);
 }
 
