@@ -80,6 +80,10 @@ cudaError_t run(SplitArgs& p, const Pass& pass, const KvAttnArgs& a, int bits, c
   const long long units = (pass.keys + kAttnUnit - 1) / kAttnUnit;
   // Sequences too short for a second CTA to be worth a join: whole pairs.
   p.whole = units <= (p.store ? kAttnWholeOwn : kAttnWhole);
+  // One a CTA where there are CTAs for all: that needs no lengths. Else stretches of equal work, not number (256 sequences
+  // of up to 256 tokens, 8 KV heads: 29.4 us, not 32.0).
+  p.counted = p.whole && static_cast<long long>(p.seqs) * p.c.heads * p.chunks <=
+                             (tile ? 1 : f.nt == 2 || a.c.dim == 256 ? 2 : 3) * kNumSMs;
   p.head = tile ? kTileHead : f.nt == 2 ? kAttnHead2 : kAttnHead;
   p.units = p.seqs * ((units > 1 ? units : 1) + p.head) * p.c.heads * p.chunks;
   if (tile) {

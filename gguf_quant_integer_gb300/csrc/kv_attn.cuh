@@ -88,7 +88,8 @@ struct SplitArgs {
   int window;
   long long units;  // upper bound of the launch's units
   int ctas;         // of the launch: as many as run at a time, or one a unit
-  bool whole;       // pairs are not cut (the line's units are pairs): no join
+  bool whole;       // pairs are not cut: no join
+  bool counted;     // whole, and each counts as one unit of the line
   int head;         // units that a pair counts besides its keys
   float* part_o;    // [2 * ctas][R][dim]
   float* part_el;   // [2 * ctas][R][2]
@@ -412,7 +413,7 @@ __device__ __forceinline__ bool line_begin(const SplitArgs& A, LineShared& sh, L
     }
     return sum + add;
   };
-  auto cost = [&](int b) { return b < A.seqs ? A.whole ? 1 : unit_count(A, seq_len(A, b)) + A.head : 0; };
+  auto cost = [&](int b) { return b < A.seqs ? A.counted ? 1 : unit_count(A, seq_len(A, b)) + A.head : 0; };
   Line L;
   L.per = static_cast<long long>(A.c.heads) * A.chunks;
   int mine = cost(tid), part, more;
@@ -456,11 +457,12 @@ __device__ __forceinline__ bool line_begin(const SplitArgs& A, LineShared& sh, L
 // leaves the pair to the next.
 __device__ __forceinline__ bool line_next(const SplitArgs& A, Line& L, Part& x) {
   while (L.u < L.u1) {
-    const int n = seq_len(A, L.seq), nu = unit_count(A, n), nv = A.whole ? 1 : nu + A.head;
+    const int n = seq_len(A, L.seq), nu = unit_count(A, n), nv = A.counted ? 1 : nu + A.head;
     if (!A.flat && threadIdx.x == 0 && A.lens[L.seq] > n) kv_record(kKvBadLen);
     const int pair = static_cast<int>(L.off / nv), at = static_cast<int>(L.off - static_cast<long long>(pair) * nv);
-    const int did = nv - at < L.u1 - L.u ? nv - at : static_cast<int>(L.u1 - L.u);
-    x = {L.seq, n, nu, pair, at > A.head ? at - A.head : 0, A.whole ? nu : at + did - A.head, L.u - at};
+    // a whole pair is the CTA's in whose stretch it begins
+    const int did = A.whole || nv - at < L.u1 - L.u ? nv - at : static_cast<int>(L.u1 - L.u);
+    x = {L.seq, n, nu, pair, at > A.head ? at - A.head : 0, A.whole ? (at ? 0 : nu) : at + did - A.head, L.u - at};
     L.u += did;
     L.off += did;
     if (L.off == nv * L.per) {
