@@ -316,16 +316,18 @@ __device__ __forceinline__ int unit_count(const SplitArgs& A, int n) {
 }
 
 // A pair's row r of chunk base: its query token and head.
+// a / b for a >= 0 (signed division takes more instructions).
+__device__ __forceinline__ int quot(int a, int b) { return static_cast<unsigned>(a) / static_cast<unsigned>(b); }
 __device__ __forceinline__ size_t row_at(const SplitArgs& A, int seq, int head, int r) {
-  const int token = r / A.group;
+  const int token = quot(r, A.group);
   return (static_cast<size_t>(seq) * A.n_q + token) * A.q_heads + head * A.group + (r - token * A.group);
 }
 
 // Last key + 1 and first key that row r of a pair sees.
 __device__ __forceinline__ void row_range(const SplitArgs& A, int seq, int n, int r, int* start, int* end) {
-  const int token = r / A.group;
+  const int token = quot(r, A.group);
   if (A.flat) {
-    const int b = token / A.n_q;
+    const int b = quot(token, A.n_q);
     int own = A.lens[b];
     const long long most = static_cast<long long>(A.max_pages) << A.c.page_shift;
     own = own < 0 ? 0 : own > most ? static_cast<int>(most) : own;
@@ -607,7 +609,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
     tile0 = (first_unit(A, x.n) + x.k0) * kAttnWarps + warp;
     tiles = all > tile0 ? (all - tile0 + kAttnWarps - 1) / kAttnWarps : 0;
     tiles = tiles < x.k1 - x.k0 ? tiles : x.k1 - x.k0;
-    line0 = (x.pair / A.chunks) << A.c.page_shift;
+    line0 = quot(x.pair, A.chunks) << A.c.page_shift;
     table = A.flat ? A.pages : A.pages + static_cast<size_t>(x.seq) * A.page_stride;
     const int page = page_of(lane);
     next_page = page_of(32 + lane);
@@ -620,7 +622,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
   bool have = line_next(A, line, cur), begun = false;
   while (have) {
     const int sq = cur.seq, n = cur.n, nu = cur.nu, pair = cur.pair, k0 = cur.k0, k1 = cur.k1;
-    const int head = pair / A.chunks, chunk = pair - head * A.chunks;
+    const int head = quot(pair, A.chunks), chunk = pair - head * A.chunks;
     const int row0 = chunk * R, rows = A.rows - row0 < R ? A.rows - row0 : R;
     // ---- the queries' loads, all before the first use, and ahead of the first tiles'
     RawQuery<EX, D> raw[NT];
