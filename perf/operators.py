@@ -250,7 +250,9 @@ def _quantize(x, bits):
     x = x.float().unflatten(-1, (-1, 32))
     size = x.abs()
     if bits == 8:
-        d = (size.amax(-1) / 127).half()
+        # by a number on the device: a CUDA tensor divided by a Python number is multiplied by its rounded reciprocal, which
+        # takes four fp32 significands to the neighbouring fp16 scale
+        d = (size.amax(-1) / torch.full((), 127.0, device=x.device)).half()
     else:
         d = (x.gather(-1, size.argmax(-1, keepdim=True)).squeeze(-1) / -8).half()
     wide = d.float()[..., None]
