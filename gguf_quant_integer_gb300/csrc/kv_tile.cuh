@@ -115,6 +115,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Magnitudes of an fp16 pair, 0 for what is not finite.
+__device__ __forceinline__ __half2 finite_abs(uint32_t w) {
+  const __half2 h = __habs2(*reinterpret_cast<const __half2*>(&w));
+  const uint32_t m = *reinterpret_cast<const uint32_t*>(&h) & __hle2_mask(h, __float2half2_rn(65504.0f));
+  return *reinterpret_cast<const __half2*>(&m);
+}
+
 // Bytes (0, 1) and (2, 3) of w as fp16 pairs u - 128 or u - 8.
 template <int BITS>
 __device__ __forceinline__ void code_halves(uint32_t w, uint32_t (&h)[2]) {
@@ -132,7 +139,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
   __shared__ __align__(8) uint64_t bars[kBars];
   __shared__ uint32_t sh_tmem;
   __shared__ unsigned sh_bad[4];            // tile's 16-key groups without a valid page, by tile & 3
-  __shared__ unsigned sh_top[4][1 + NB];    // largest |scale| of the part: K's, V's blocks (fp32 bits), by part & 3
+  __shared__ unsigned sh_top[4][1 + NB];    // largest finite |scale| of the part: K's, V's blocks (fp32 bits), by part & 3
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto bar = [&](int i) { return ptx::smem_addr(&bars[i]); };
   if (tid == 0) {
@@ -315,10 +322,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         ptx::tc_fence_after();
         const uint32_t ts = tl + S::kColS + buffer(r, done) * kTileKeys;
         if (i == 0) {  // the part's powers of two, known once its first tile is there (and until its weights are)
-          auto power = [&](int x) {
-            const unsigned t0 = sh_top[parts & 3][x] >> 23;
-            return t0 < 253 ? t0 + 1 : 254u;
-          };
+          auto power = [&](int x) { return (sh_top[parts & 3][x] >> 23) + 1; };
           cs = fmaxf(cs * __uint_as_float(power(0) << 23), 1.17549435e-38f);
 #pragma unroll
           for (int b = 0; b < NB; ++b) vx |= power(1 + b) << (8 * b);
@@ -495,7 +499,8 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
 #pragma unroll
       for (int b = 0; b < NB; ++b) vf[b] = 1.0f;
       {
-        // ---- the part's largest scales: 1 / 17 or 1 / 9 of its bytes, which its tiles then find in L2
+        // ---- the part's largest finite scales (one that is not belongs to the rows that see its key: in the others' way it
+        // would leave no power of two for the finite ones): 1 / 17 or 1 / 9 of its bytes, which its tiles then find in L2
         unsigned* const tops = sh_top[parts & 3];
         if (ct <= NB) tops[ct] = 0u;
         if (group_any(kBarrier, kThreads, fail)) break;
@@ -536,15 +541,15 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             }
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
-              kt = __hmax2_nan(kt, __habs2(*reinterpret_cast<const __half2*>(&kw[h])));
-              const __half2 a = __habs2(*reinterpret_cast<const __half2*>(&vw[h]));
+              kt = __hmax2(kt, finite_abs(kw[h]));
+              const __half2 a = finite_abs(vw[h]);
               if (NB % 2 == 0) {
-                vt[h % (NB / 2 > 0 ? NB / 2 : 1)] = __hmax2_nan(vt[h % (NB / 2 > 0 ? NB / 2 : 1)], a);
+                vt[h % (NB / 2 > 0 ? NB / 2 : 1)] = __hmax2(vt[h % (NB / 2 > 0 ? NB / 2 : 1)], a);
               } else {
 #pragma unroll
                 for (int q = 0; q < NB; ++q) {
-                  if ((piece * 8 + 2 * h) % NB == q) vt[q] = __hmax2_nan(vt[q], __half2half2(__low2half(a)));
-                  if ((piece * 8 + 2 * h + 1) % NB == q) vt[q] = __hmax2_nan(vt[q], __half2half2(__high2half(a)));
+                  if ((piece * 8 + 2 * h) % NB == q) vt[q] = __hmax2(vt[q], __half2half2(__low2half(a)));
+                  if ((piece * 8 + 2 * h + 1) % NB == q) vt[q] = __hmax2(vt[q], __half2half2(__high2half(a)));
                 }
               }
             }
@@ -552,7 +557,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         }
 #pragma unroll
         for (int b = 0; b <= NB; ++b) {
-          // magnitudes order like their bits (an infinity or a NaN above all)
+          // magnitudes order like their bits
           const __half2 h = b == 0 ? kt : vt[NB % 2 ? b - 1 : (b - 1) / 2];
           const float lo = __half2float(__low2half(h)), hi = __half2float(__high2half(h));
           const unsigned bits = b == 0 || NB % 2 ? max(__float_as_uint(lo), __float_as_uint(hi))
@@ -562,7 +567,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         }
         if (group_any(kBarrier, kThreads, fail)) break;
         // 2^-(exponent + 1): scales come to at most 1
-        auto down = [](unsigned t) { return __uint_as_float((t >> 23 < 253 ? 253 - (t >> 23) : 0u) << 23); };
+        auto down = [](unsigned t) { return __uint_as_float((253 - (t >> 23)) << 23); };
         kf = down(tops[0]);
 #pragma unroll
         for (int b = 0; b < NB; ++b) vf[b] = down(tops[1 + b]);

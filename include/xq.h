@@ -519,6 +519,8 @@ XQ_API size_t xq_kv_attn_workspace_bytes(const xq_kv_cache *cache, const xq_kv_q
  * applied in fp32. Where many 16-bit rows (64 or more) read a head's many
  * keys, K and V enter with their scales, without loss for fp16 queries and
  * rounded to fp16 for bf16 ones.
+ * A key whose K row has a block that is not finite makes the query rows that
+ * see it NaN, and no others.
  * Results do not depend on what the slots past a sequence's length hold. They
  * depend on the other sequences of the call only through where a long
  * sequence is cut into parts (in rounding).
