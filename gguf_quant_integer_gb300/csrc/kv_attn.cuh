@@ -212,6 +212,13 @@ __device__ __forceinline__ uint32_t hfma2_of(uint32_t a, uint32_t b, uint32_t c)
   return d;
 }
 
+// The larger of two, or a NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // fp16 pairs of codes. A stored byte u put under 0x64 is the fp16 number
 // 1024 + u, so one subtraction gives u - 128 (and u - 8 for a low nibble); a
 // high nibble in place is 1024 + 16 u, brought to u - 8 by one fma. All exact.
@@ -241,7 +248,7 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return static_cast<uint32_t>(r * NCH + x) * 16;
 }
 
-// N halves at p (4-byte aligned when N is even) as floats, and their largest magnitude.
+// N halves at p (4-byte aligned when N is even) as floats, and their largest magnitude (a NaN if there is one).
 template <int N>
 __device__ __forceinline__ float load_scales(const __half* p, float (&f)[N]) {
   if constexpr (N % 2 == 0) {
@@ -264,15 +271,15 @@ __device__ __forceinline__ float load_scales(const __half* p, float (&f)[N]) {
       const float2 v = __half22float2(h);
       f[2 * i] = v.x;
       f[2 * i + 1] = v.y;
-      if (i) top = __hmax2(top, __habs2(h));
+      if (i) top = __hmax2_nan(top, __habs2(h));
     }
-    return __half2float(__hmax(__low2half(top), __high2half(top)));
+    return __half2float(__hmax_nan(__low2half(top), __high2half(top)));
   } else {
     float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       f[i] = __half2float(p[i]);
-      top = fmaxf(top, fabsf(f[i]));
+      top = max_nan(top, fabsf(f[i]));
     }
     return top;
   }
@@ -836,9 +843,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
         }
       }
       // ---- weights p = 2^(s - e). w: p times the key's largest V scale (no less than the least fp16 step). e moves if some
-      // w passes 2^15; the fp32 form also looks for weights below 2^-13.
-      m0 = fminf(fmaxf(m0, 5.9604645e-8f), 65504.0f);
-      m1 = fminf(fmaxf(m1, 5.9604645e-8f), 65504.0f);
+      // w passes 2^15 or is not a number, as with a V scale that is not finite; the fp32 form also looks for weights below 2^-13.
+      constexpr float kLeast = 5.9604645e-8f;
+      m0 = max_nan(m0, kLeast);
+      m1 = max_nan(m1, kLeast);
       float p[NT][NS];
       bool odd = false;
 #pragma unroll
@@ -859,6 +867,37 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
         odd = __any_sync(0xffffffffu, move);
       }
       if (any_odd && odd) {
+        if (__any_sync(0xffffffffu, !(m0 <= 65504.0f) || !(m1 <= 65504.0f))) {
+          // V blocks that are not finite: their elements become NaN in the rows that see the key. The scale itself must not
+          // reach a product: a row that does not see it has the weight 0, and 0 times infinity is NaN.
+          m0 = m1 = kLeast;
+          unsigned spoilt = 0;  // blocks, by row
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const bool b0 = !(fabsf(v0[b]) <= 65504.0f), b1 = !(fabsf(v1[b]) <= 65504.0f);
+            v0[b] = b0 ? 0.0f : v0[b];
+            v1[b] = b1 ? 0.0f : v1[b];
+            m0 = fmaxf(m0, fabsf(v0[b]));
+            m1 = fmaxf(m1, fabsf(v1[b]));
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int c = 0; c < NQ; ++c)
+                if ((b0 && s[j][c] != -INFINITY) || (b1 && s[j][NS / 2 + c] != -INFINITY)) spoilt |= 1u << ((b * NT + j) * NQ + c);
+          }
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) spoilt |= __shfl_xor_sync(0xffffffffu, spoilt, x);
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int c = 0; c < NQ; ++c)
+                if (spoilt >> ((b * NT + j) * NQ + c) & 1) {
+                  o[j][2 * b][c] = o[j][2 * b][2 + c] = __int_as_float(0x7FC00000);
+                  o[j][2 * b + 1][c] = o[j][2 * b + 1][2 + c] = __int_as_float(0x7FC00000);
+                }
+        }
         const float lg0 = __log2f(m0), lg1 = __log2f(m1);
 #pragma unroll
         for (int j = 0; j < NT; ++j)

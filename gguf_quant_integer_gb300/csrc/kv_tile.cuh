@@ -91,6 +91,8 @@ namespace {
 __device__ unsigned int g_kv_tile_error;  // a wait that ran out
 constexpr long long kTileWait = 1ll << 32;
 
+constexpr unsigned kOddV = 16;  // the tile has V blocks that are not finite
+
 // Barriers: of each row tile (Q), of each scores buffer (S; P and O, its weights and their products) and of each
 // operand buffer and raw stage, as a barrier's parity tells a phase only from the next.
 enum TileBar { kBarDrain, kBarQ, kBarS = kBarQ + 2, kBarP = kBarS + 2, kBarO = kBarP + 2, kBarK = kBarO + 2, kBarKFree = kBarK + 2,
@@ -138,7 +140,8 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
   __shared__ LineShared sh_line;
   __shared__ __align__(8) uint64_t bars[kBars];
   __shared__ uint32_t sh_tmem;
-  __shared__ unsigned sh_bad[4];            // tile's 16-key groups without a valid page, by tile & 3
+  __shared__ unsigned sh_bad[4];            // tile's 16-key groups without a valid page, and kOddV, by tile & 3
+  __shared__ unsigned sh_odd[4][NB][2];     // keys whose V block is not finite, by tile & 3: only where kOddV says so
   __shared__ unsigned sh_top[4][1 + NB];    // largest finite |scale| of the part: K's, V's blocks (fp32 bits), by part & 3
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto bar = [&](int i) { return ptx::smem_addr(&bars[i]); };
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       int key = (first_unit(A, part.n) + part.k0) * kTileKeys;
       float e = -1e30f;
       ptx::f2 l = ptx::pk(0.0f, 0.0f);
-      unsigned vx = 0;  // exponents of V's powers of two, 8 bits a block
+      unsigned vx = 0;  // exponents of V's powers of two, 8 bits a block (all ones: the row's elements are NaN)
       for (int i = 0; i < tiles; ++i, ++it, ++done, key += kTileKeys) {
         ok = __all_sync(0xffffffffu, wait(kBarS + buffer(r, done), turn(done), 6));
         if (!ok) break;
@@ -328,6 +331,13 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           for (int b = 0; b < NB; ++b) vx |= power(1 + b) << (8 * b);
         }
         const unsigned bad = sh_bad[it & 3];
+        if (bad & kOddV) {  // V blocks that are not finite: their elements become NaN in the rows that see the key
+          const int from = lim0 > key ? lim0 - key : 0, to = lim1 - key < kTileKeys ? lim1 - key : kTileKeys;
+          const unsigned long long sees = from < to ? (~0ull >> (kTileKeys - (to - from))) << from : 0ull;
+#pragma unroll 1
+          for (int b = 0; b < NB; ++b)
+            if (sees & (sh_odd[it & 3][b][0] | static_cast<unsigned long long>(sh_odd[it & 3][b][1]) << 32)) vx |= 0xFFu << (8 * b);
+        }
         const bool edge = key < lim0 || key + kTileKeys > lim1 || bad;
         uint32_t sv[2][16];
         // 32 scores from column c on, those that the row does not see as -infinity
@@ -410,7 +420,8 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         __syncwarp();
         ptx::tmem_ld16(to + c, w);
         ptx::tmem_wait_ld();
-        const float f = __uint_as_float((vx >> (8 * (c / 32)) & 0xFFu) << 23);
+        const unsigned x2 = vx >> (8 * (c / 32)) & 0xFFu;
+        const float f = __uint_as_float(x2 == 0xFFu ? 0x7FC00000u : x2 << 23);
         if (live) {
 #pragma unroll
           for (int x = 0; x < 16; x += 4) {
@@ -586,19 +597,35 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         issue(i + 2, stage ^ 1);
         const uint8_t* const raw = smem + S::kOffRaw + (S::kRawStages * group + stage) * S::kRaw;
         const int left = part.n - (unit0 + i) * kTileKeys;  // keys of the sequence from the tile's first on
-        // ---- scales: scaled, and 0 for keys that are not there (whose codes may be anything)
+        // ---- scales: scaled, and 0 for keys that are not there (whose codes may be anything). A V scale that is not finite
+        // is 0 too, as the product takes it to all rows, and the rows that see its key are told
+        auto key_gone = [&](int key) { return key >= left || (miss >> (key >> 4) & 1); };
+        auto finite = [](__half h) { return (__half_as_ushort(h) & 0x7C00u) != 0x7C00u; };
+        const __half* const kd = reinterpret_cast<const __half*>(raw + 2 * S::kRawCodes);
+        const __half* const vd = kd + S::kRawScales / 2;
+        bool odd = false;
         for (int x = gt; x < kTileKeys * NB; x += kGroup) {
           const int key = x / NB, blk = x - key * NB;
-          const bool gone = key >= left || (miss >> (key >> 4) & 1);
-          const __half* const kd = reinterpret_cast<const __half*>(raw + 2 * S::kRawCodes);
+          const bool gone = key_gone(key), zero = gone || !finite(vd[x]);
+          odd |= zero && !gone;
           float f = vf[0];
 #pragma unroll
           for (int q = 1; q < NB; ++q) f = blk == q ? vf[q] : f;
-          const float dk = gone ? 0.0f : __half2float(kd[x]) * kf, dv = gone ? 0.0f : __half2float(kd[S::kRawScales / 2 + x]) * f;
+          const float dk = gone ? 0.0f : __half2float(kd[x]) * kf, dv = zero ? 0.0f : __half2float(vd[x]) * f;
           reinterpret_cast<__half*>(scales)[x] = __float2half_rn(dk);
           reinterpret_cast<__half*>(scales + S::kScaleK)[blk * kTileKeys + key] = __float2half_rn(dv);
         }
-        group_any(kBarrier + 1 + group, kGroup, false);
+        if (group_any(kBarrier + 1 + group, kGroup, odd)) {
+          unsigned* const keys = &sh_odd[it & 3][0][0];
+          if (gt < 2 * NB) keys[gt] = 0u;
+          group_any(kBarrier + 1 + group, kGroup, false);
+#pragma unroll 1
+          for (int x = gt; x < kTileKeys * NB; x += kGroup) {
+            const int key = x / NB, blk = x - key * NB;
+            if (!key_gone(key) && !finite(vd[x])) atomicOr(&keys[2 * blk + (key >> 5)], 1u << (key & 31));
+          }
+          miss |= kOddV;
+        }
         // ---- K: operand rows are keys. A task is a key's 16-byte chunk
         const unsigned b = it % S::kBufs, turn = it / S::kBufs;  // tiles take the buffers, and the groups the tiles, in turn
         if (turn > 0) fail |= !wait_sleep(kBarKFree + b, turn - 1, 10);

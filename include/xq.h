@@ -520,7 +520,8 @@ XQ_API size_t xq_kv_attn_workspace_bytes(const xq_kv_cache *cache, const xq_kv_q
  * keys, K and V enter with their scales, without loss for fp16 queries and
  * rounded to fp16 for bf16 ones.
  * A key whose K row has a block that is not finite makes the query rows that
- * see it NaN, and no others.
+ * see it NaN, one whose V row has, the 32 elements of that block in them. Rows
+ * that do not see the key are as without it.
  * Results do not depend on what the slots past a sequence's length hold. They
  * depend on the other sequences of the call only through where a long
  * sequence is cut into parts (in rounding).

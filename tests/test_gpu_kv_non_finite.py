@@ -52,3 +52,40 @@ def check_rows_beside_a_bad_key(xq, case, kind, what, value):  # noqa: F811
 @pytest.mark.parametrize("value", [float("inf"), float("nan")])
 def test_a_key_that_is_not_finite_is_for_the_rows_that_see_it(xq, case, kind, value):  # noqa: F811
     check_rows_beside_a_bad_key(xq, case, kind, "k", value)
+
+
+@pytest.mark.parametrize("case", kc.RUNS, ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("kind", ["q8", "q4"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_a_value_that_is_not_finite_is_for_the_rows_that_see_it(xq, case, kind, value):  # noqa: F811
+    check_rows_beside_a_bad_key(xq, case, kind, "v", value)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("prefix,batch,group", [(70, 3, 2), (3001, 24, 4)])  # (the second: bf16 on the tiles)
+@pytest.mark.parametrize("what", ["k", "v"])
+def test_behind_a_shared_prefix(xq, dtype, prefix, batch, group, what):  # noqa: F811
+    """A bad block in one sequence's own tokens spoils that sequence alone; one in the prefix all of them."""
+    heads, page, own = 8, 16, 5
+    rng = np.random.default_rng(prefix)
+    pages = -(-prefix // page)
+    slots = torch.cat([torch.arange(prefix)] + [(pages + b) * page + torch.arange(own) for b in range(batch)]).cuda()
+    q = rows(rng, (batch, 1, heads * group, DIM), "fp32").to(kc.DTYPES[dtype]).cuda()
+    k, v = (rows(rng, (len(slots), heads, DIM), "fp32").cuda() for _ in range(2))
+    for at, spoilt in ((prefix + own + 1, [1]), (prefix // 2, range(batch))):
+        x = [k.clone(), v.clone()]
+        x[what == "v"][at, 2, 32 * BLOCK] = float("inf")
+        cache = xq.KVCache(8, pages + batch, page, heads, DIM)
+        cache.write(*x, slots)
+        out = cache.attn_shared(q, torch.arange(pages, dtype=torch.int32, device="cuda"), prefix,
+                                torch.arange(pages, pages + batch, dtype=torch.int32, device="cuda")[:, None],
+                                torch.full((batch,), own, dtype=torch.int32, device="cuda"))[:, 0].float()
+        bad = torch.zeros_like(out, dtype=torch.bool)
+        bad[list(spoilt), 2 * group:3 * group, slice(32 * BLOCK, 32 * BLOCK + 32) if what == "v" else slice(None)] = True
+        assert torch.equal(torch.isnan(out), bad)
+        kf, vf = cache.read(slots)
+        for b in range(batch):
+            j = torch.cat((torch.arange(prefix), prefix + own * b + torch.arange(own))).cuda()
+            want = kc.attention64(q[b], kf[j], vf[j], DIM ** -0.5, kc.seen(1, own, prefix=prefix))[0]
+            assert kc.relative(out[b][~bad[b]], want[~bad[b]]) <= kc.LIMIT[dtype]
+        assert xq.device_error() == 0
