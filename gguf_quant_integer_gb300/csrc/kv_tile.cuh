@@ -8,12 +8,13 @@
 // 128 rows = lanes; then weights, which a row's thread writes where it read
 // the scores: no shuffles, no shared memory) and their B operand, the
 // dequantized tile, from shared memory. Everything enters as fp16; K and V are
-// code * d / 2^x, where 2^x, from the part's largest block scale (for V of each
-// 32 elements), keeps them in range whatever their size. For bf16 queries they
-// are rounded to one number (11 bits, 8 finer than the output's). For fp16 ones
-// they are two, P = 2, which hold all 19 bits of a code times its scale: one
-// would nearly double the output's error (4.1e-4 against 2.8e-4 relative, of
-// which rounding the output is 2.1e-4). fp32 queries never come here: a tensor
+// code * d / 2^x, where 2^x, from the part's largest finite block scale (for V
+// of each 32 elements), keeps them in range. Scales more than 2^21 (8-bit codes)
+// or 2^25 (4-bit) below that largest one lose a bit for each factor of 2. For
+// bf16 queries the products are rounded to one number (11 bits, 8 finer than the
+// output's). For fp16 ones they are two, P = 2, which hold all 19 bits of a code
+// times its scale: one would nearly double the output's error (4.1e-4 against
+// 2.8e-4 relative, of which rounding the output is 2.1e-4). fp32 queries never come here: a tensor
 // core's accumulator loses a little at each product added to it, and the 24
 // products of a tile in three bf16 pieces brought errors to 2.5e-6 .. 4e-6,
 // growing with the length, where the split kernel's are 4e-7.
@@ -68,6 +69,9 @@ struct TileShape {
   static constexpr int kOffV = kBufs * P * kOperand, kOffRaw = kOffV + kBufs * P * kOperand;
   // The tile's scales, ready for use: K's [64][NB], V's [NB][64], fp16.
   static constexpr int kScaleK = kTileKeys * NB * 2, kScales = 2 * kScaleK;  // a table for each group
+  // The part's largest scale comes to 2^kUp .. 2^(kUp + 1): with codes of 128 or 8 at most, products stay within 2^15, and
+  // scales down to 2^-(14 + kUp) of it are normal fp16 numbers, 11 bits as stored. (2^0: 2^-14 of it, and 3 % errors at 2^-20.)
+  static constexpr int kUp = BITS == 8 ? 7 : 11;
   static constexpr int kRawStages = 2;  // of a group of unpacking warps
   static constexpr int kOffScale = kOffRaw + 2 * kRawStages * kRaw;
   static constexpr int kSmem = kOffScale + 2 * kScales;
@@ -123,6 +127,9 @@ __device__ __forceinline__ __half2 finite_abs(uint32_t w) {
   const uint32_t m = *reinterpret_cast<const uint32_t*>(&h) & __hle2_mask(h, __float2half2_rn(65504.0f));
   return *reinterpret_cast<const __half2*>(&m);
 }
+
+// Biased exponent of a largest scale (fp32 bits), at least that of fp16's least number: 103 .. 142.
+__device__ __forceinline__ unsigned kv_top_exponent(unsigned bits) { return max(bits >> 23, 103u); }
 
 // Bytes (0, 1) and (2, 3) of w as fp16 pairs u - 128 or u - 8.
 template <int BITS>
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         ptx::tc_fence_after();
         const uint32_t ts = tl + S::kColS + buffer(r, done) * kTileKeys;
         if (i == 0) {  // the part's powers of two, known once its first tile is there (and until its weights are)
-          auto power = [&](int x) { return (sh_top[parts & 3][x] >> 23) + 1; };
+          auto power = [&](int x) { return kv_top_exponent(sh_top[parts & 3][x]) - S::kUp; };
           cs = fmaxf(cs * __uint_as_float(power(0) << 23), 1.17549435e-38f);
 #pragma unroll
           for (int b = 0; b < NB; ++b) vx |= power(1 + b) << (8 * b);
@@ -577,8 +584,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           if (lane == 0) atomicMax(&tops[b], m);
         }
         if (group_any(kBarrier, kThreads, fail)) break;
-        // 2^-(exponent + 1): scales come to at most 1
-        auto down = [](unsigned t) { return __uint_as_float((253 - (t >> 23)) << 23); };
+        auto down = [](unsigned t) { return __uint_as_float((254 + S::kUp - kv_top_exponent(t)) << 23); };
         kf = down(tops[0]);
 #pragma unroll
         for (int b = 0; b < NB; ++b) vf[b] = down(tops[1 + b]);

@@ -517,8 +517,12 @@ XQ_API size_t xq_kv_attn_workspace_bytes(const xq_kv_cache *cache, const xq_kv_q
  * tensor cores as two fp16 numbers each (22 bits), 16-bit ones and their
  * weights as one; the stored codes are exact there, and block scales are
  * applied in fp32. Where many 16-bit rows (64 or more) read a head's many
- * keys, K and V enter with their scales, without loss for fp16 queries and
- * rounded to fp16 for bf16 ones.
+ * keys and dim is at most 128, K and V enter with their scales, without loss
+ * for fp16 queries and rounded to fp16 for bf16 ones. There a K scale below
+ * 2^-21 (Q8_0) or 2^-25 (Q4_0) of the largest finite one of the keys that a
+ * CTA takes loses a bit for each further factor of 2, a V scale likewise
+ * against the largest of the same 32 elements, and keys whose weight is below
+ * 2^-36 of the row's largest may count as 0.
  * A key whose K row has a block that is not finite makes the query rows that
  * see it NaN, one whose V row has, the 32 elements of that block in them. Rows
  * that do not see the key are as without it.

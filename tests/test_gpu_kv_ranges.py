@@ -1,0 +1,37 @@
+"""Attention where the sizes of numbers are far apart or far from 1: the result depends on their ratios only."""
+import numpy as np
+import pytest
+import torch
+
+import kv_check as kc
+from test_gpu_kv_cache import rows, xq  # noqa: F401 (the fixture)
+
+pytestmark = pytest.mark.gpu
+DIM = 64
+IDS = lambda c: "-".join(map(str, c))  # noqa: E731
+
+
+def setup(case, seed=1):
+    _, dtype, heads, group, n_q, n = case
+    rng = np.random.default_rng(seed)
+    k, v = (rows(rng, (n, heads, DIM), "fp32").cuda() for _ in range(2))
+    q = rows(rng, (1, n_q, heads * group, DIM), "fp32").cuda()
+    return k, v, q.to(kc.DTYPES[dtype]), torch.tensor([n], dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("case", kc.RUNS, ids=IDS)
+@pytest.mark.parametrize("kind", ["q8", "q4"])
+def test_scales_far_below_the_largest(xq, kind, case):  # noqa: F811
+    """One key in the middle has a K block 2^20 times the others' (in elements where every query is 0) and the last one V
+    blocks 2^20 times the others': neither takes part in the earlier tokens' outputs, nor may it cost them bits."""
+    _, dtype, heads, group, n_q, n = case
+    k, v, q, lens = setup(case)
+    q[..., 32:] = 0
+    k, v, q = k / 32, v / 32, q * 32  # so that the large blocks' scales are fp16 numbers
+    k[n // 2, :, 32:] *= 2.0 ** 20
+    v[n - 1] *= 2.0 ** 20
+    cache, table, slots = kc.filled(xq, kind, k, v, 32)
+    out = cache.attn(q, table, lens)[0]
+    want = kc.attention64(q[0], *cache.read(slots), DIM ** -0.5, kc.seen(n_q, n))
+    assert kc.relative(out[:-1], want[:-1]) <= kc.LIMIT[dtype], kc.relative(out[:-1], want[:-1])
+    assert xq.device_error() == 0
