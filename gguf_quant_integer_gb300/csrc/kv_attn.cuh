@@ -689,7 +689,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         block_sum[b] = sum * (BITS == 4 ? -8.0f * 5.9604645e-8f : -128.0f * 5.9604645e-8f);
       }
-      const float down = A.scale * 1.4426950408889634f * __uint_as_float(static_cast<unsigned>(127 - 12 + (EX ? 0 : 24) + ex) << 23);
+      // in two steps: of 2^(ex + 12) alone the exponent would pass fp32's for bf16 queries of 2^116 and more
+      const float down = A.scale * 1.4426950408889634f * __uint_as_float(static_cast<unsigned>(127 + ex) << 23) *
+                         (EX ? 2.44140625e-4f : 4096.0f);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         if (NP == 2) {  // both pieces

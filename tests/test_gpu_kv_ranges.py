@@ -35,3 +35,18 @@ def test_scales_far_below_the_largest(xq, kind, case):  # noqa: F811
     want = kc.attention64(q[0], *cache.read(slots), DIM ** -0.5, kc.seen(n_q, n))
     assert kc.relative(out[:-1], want[:-1]) <= kc.LIMIT[dtype], kc.relative(out[:-1], want[:-1])
     assert xq.device_error() == 0
+
+
+@pytest.mark.parametrize("case", kc.RUNS, ids=IDS)
+@pytest.mark.parametrize("power", [-100, 90, 116, 120])
+def test_queries_of_any_size(xq, case, power):  # noqa: F811
+    """Queries times 2^x with a scale of 2^-x: the same scores."""
+    _, dtype, heads, group, n_q, n = case
+    k, v, q, lens = setup(case)
+    if dtype == "fp16":
+        power //= 12  # its range
+    cache, table, slots = kc.filled(xq, "q8", k, v, 32)
+    out = cache.attn(q * 2.0 ** power, table, lens, scale=DIM ** -0.5 * 2.0 ** -power)[0]
+    want = kc.attention64(q[0], *cache.read(slots), DIM ** -0.5, kc.seen(n_q, n))
+    assert kc.relative(out, want) <= kc.LIMIT[dtype], kc.relative(out, want)
+    assert xq.device_error() == 0
