@@ -906,6 +906,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
 #pragma unroll
           for (int c = 0; c < NQ; ++c) {
             float top = fmaxf(s[j][c] + lg0, s[j][NS / 2 + c] + lg1) - 11.0f;
+            // scores of 2^27, where fp32's step is 16, can leave a weight of 2^24 so
+            const float z = fmaxf((s[j][c] - top) + lg0, (s[j][NS / 2 + c] - top) + lg1);
+            top = z > 15.0f ? top + z : top;
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));

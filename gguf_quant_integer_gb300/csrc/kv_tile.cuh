@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       int key = (first_unit(A, part.n) + part.k0) * kTileKeys;
       float e = -1e30f;
       ptx::f2 l = ptx::pk(0.0f, 0.0f);
+      bool far = false;  // some reference of the warp's is past 2^20
       unsigned vx = 0;  // exponents of V's powers of two, 8 bits a block (all ones: the row's elements are NaN)
       for (int i = 0; i < tiles; ++i, ++it, ++done, key += kTileKeys) {
         ok = __all_sync(0xffffffffu, wait(kBarS + buffer(r, done), turn(done), 6));
@@ -373,8 +374,11 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         largest();
         const float tile_top = fmaxf(fmaxf(tops4[0], tops4[1]), fmaxf(tops4[2], tops4[3])) * cs;
         if (__any_sync(0xffffffffu, tile_top - e > kTop)) {  // the reference of some rows moves
-          const float next = tile_top - e > kTop ? tile_top - kStart : e, f = ex2(e - next);
+          float next = tile_top - e > kTop ? tile_top - kStart : e;
+          next = tile_top - next > kTop ? tile_top : next;  // at 2^27, where fp32's step is 16, 11 less is 16 less
+          const float f = ex2(e - next);
           e = next;
+          far = __any_sync(0xffffffffu, fabsf(e) > 1048576.0f && e != -1e30f);
           l = ptx::mul2(l, ptx::pk(f, f));
           if (i > 0) {
             ok = __all_sync(0xffffffffu, wait(kBarO + buffer(r, done - 1), turn(done - 1), 7));
@@ -391,7 +395,24 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             }
           }
         }
-        const ptx::f2 c2 = ptx::pk(cs, cs), e2 = ptx::pk(-e, -e);
+        // A weight's score times cs minus e is one operation, whose product is not rounded as the one that gave e was. Where that
+        // difference counts, with scores past 2^20, the products take the scores' place first.
+        float factor = cs;
+        if (far) {
+          factor = 1.0f;
+          __syncwarp();
+#pragma unroll 1
+          for (int c = 0; c < kTileKeys; c += 16) {
+            ptx::tmem_ld16(ts + c, sv[0]);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 16; ++x) sv[0][x] = __float_as_uint(__fmul_rn(__uint_as_float(sv[0][x]), cs));
+            ptx::tmem_st16(ts + c, sv[0]);
+          }
+          ptx::tmem_wait_st();
+          load(0);
+        }
+        const ptx::f2 c2 = ptx::pk(factor, factor), e2 = ptx::pk(-e, -e);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h) load(32);

@@ -50,3 +50,25 @@ def test_queries_of_any_size(xq, case, power):  # noqa: F811
     want = kc.attention64(q[0], *cache.read(slots), DIM ** -0.5, kc.seen(n_q, n))
     assert kc.relative(out, want) <= kc.LIMIT[dtype], kc.relative(out, want)
     assert xq.device_error() == 0
+
+
+@pytest.mark.parametrize("case", kc.RUNS, ids=IDS)
+@pytest.mark.parametrize("power", [14, 18, 20, 21, 22, 23, 24, 26, 30])
+def test_large_scores(xq, case, power):  # noqa: F811
+    """Scores whose steps in fp32 are larger than a weight's range (16 at 2^27): the key with the largest one takes all the
+    weight. V has scales above 1, which the split kernel's range follows too."""
+    _, dtype, heads, group, n_q, n = case
+    k, v, q, lens = setup(case)
+    v = v * 256
+    cache, table, slots = kc.filled(xq, "q8", k, v, 32)
+    out = cache.attn(q, table, lens, scale=2.0 ** power)[0]
+    kf, vf = cache.read(slots)
+    want = kc.attention64(q[0], kf, vf, 2.0 ** power, kc.seen(n_q, n))
+    # rows where the two largest scores are too close for the kernels' operands to tell apart are left out
+    z = torch.einsum("ihgd,lhd->ihgl", q[0].double().view(n_q, heads, group, DIM), kf.double()).masked_fill(
+        ~kc.seen(n_q, n)[:, None, None], -float("inf"))
+    top = z.topk(2, -1).values
+    clear = ((top[..., 0] - top[..., 1]) > 4e-3 * top[..., 0].abs()).reshape(n_q, heads * group)
+    assert clear.any() and torch.isfinite(out).all()
+    assert kc.relative(out[clear], want[clear]) <= kc.LIMIT[dtype], kc.relative(out[clear], want[clear])
+    assert xq.device_error() == 0
