@@ -51,6 +51,9 @@ constexpr int kAttnWarps = 4;
 // is a subnormal fp16, keep their bits.
 constexpr float kLoUp = 2048.0f;
 constexpr float kWeightTop = 32768.0f, kWeightLow = 1.220703125e-4f;  // 2^15, 2^-13
+// The reference of a row that has seen no key: below every finite score, and itself finite (a masked score is -infinity, and
+// the difference of two would not be a number).
+constexpr float kNoKey = -3.402823466e38f;
 constexpr int kAttnUnit = 16 * kAttnWarps;  // keys a unit
 // Units of time that a CTA spends on a pair besides its keys (queries, page
 // ids, filling the pipeline, merging): the cut counts them, or CTAs with many
@@ -734,7 +737,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
       for (int m = 0; m < D / 16; ++m) o[j][m][0] = o[j][m][1] = o[j][m][2] = o[j][m][3] = 0.0f;
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        er[j][i] = -1e30f;
+        er[j][i] = kNoKey;
         l[j][i] = 0.0f;
       }
     }
@@ -1110,7 +1113,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) kv_join_kernel(cons
     const int seq = __shfl_sync(0xffffffffu, mine.x, from), pair = __shfl_sync(0xffffffffu, mine.y, from);
     const int parts = __shfl_sync(0xffffffffu, mine.z, from) - c0 + 1;
     const int head = pair / A.chunks, pair_row = (pair - head * A.chunks) * R + row;
-    float e = -1e30f, l = 0.0f;
+    float e = kNoKey, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const bool live = team < kTeams && pair_row < A.rows;
     if (live) {

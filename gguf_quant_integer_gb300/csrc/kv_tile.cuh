@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       if (lane == 0) ptx::mbar_arrive(bar(kBarQ + r));
 
       int key = (first_unit(A, part.n) + part.k0) * kTileKeys;
-      float e = -1e30f;
+      float e = kNoKey;
       ptx::f2 l = ptx::pk(0.0f, 0.0f);
       bool far = false;  // some reference of the warp's is past 2^20
       unsigned vx = 0;  // exponents of V's powers of two, 8 bits a block (all ones: the row's elements are NaN)
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
           next = tile_top - next > kTop ? tile_top : next;  // at 2^27, where fp32's step is 16, 11 less is 16 less
           const float f = ex2(e - next);
           e = next;
-          far = __any_sync(0xffffffffu, fabsf(e) > 1048576.0f && e != -1e30f);
+          far = __any_sync(0xffffffffu, fabsf(e) > 1048576.0f && e != kNoKey);
           l = ptx::mul2(l, ptx::pk(f, f));
           if (i > 0) {
             ok = __all_sync(0xffffffffu, wait(kBarO + buffer(r, done - 1), turn(done - 1), 7));

@@ -72,3 +72,25 @@ def test_large_scores(xq, case, power):  # noqa: F811
     assert clear.any() and torch.isfinite(out).all()
     assert kc.relative(out[clear], want[clear]) <= kc.LIMIT[dtype], kc.relative(out[clear], want[clear])
     assert xq.device_error() == 0
+
+
+@pytest.mark.parametrize("case", [c for c in kc.RUNS if c[1] != "fp16"], ids=IDS)
+@pytest.mark.parametrize("size", [1e28, 1e30, 1e32])
+def test_scores_far_below_zero(xq, case, size):  # noqa: F811
+    """Every score is a large negative number: the key with the largest one still takes all the weight."""
+    _, dtype, heads, group, n_q, n = case
+    k, v, q, lens = setup(case)
+    k = k.abs() + 0.1
+    q = -(q.abs() + 0.1)
+    cache, table, slots = kc.filled(xq, "q8", k, v, 32)
+    out = cache.attn(q, table, lens, scale=size)[0]
+    want = kc.attention64(q[0], *cache.read(slots), size, kc.seen(n_q, n))
+    # rows where the two largest scores are too close for the kernels' operands to tell apart are left out
+    kf = cache.read(slots)[0].double()
+    z = torch.einsum("ihgd,lhd->ihgl", q[0].double().view(n_q, heads, group, DIM), kf).masked_fill(
+        ~kc.seen(n_q, n)[:, None, None], -float("inf"))
+    top = z.topk(2, -1).values
+    clear = ((top[..., 0] - top[..., 1]) > 4e-3 * top[..., 0].abs()).reshape(n_q, heads * group)
+    assert clear.any()
+    assert kc.relative(out[clear], want[clear]) <= kc.LIMIT[dtype], kc.relative(out[clear], want[clear])
+    assert xq.device_error() == 0
