@@ -41,7 +41,8 @@ Pass prefix_pass(const KvAttnArgs& a) { return {1, a.batch * a.rows, a.prefix_le
 //         60 and 62
 bool tiled(const KvAttnArgs& a, const Pass& p) {
   if (a.type == kF32 || a.c.dim > 128 || p.rows < 64) return false;
-  const long long seen = a.window > 0 && p.keys > a.window + a.n_q ? a.window + a.n_q : p.keys;
+  const long long reach = static_cast<long long>(a.window) + a.n_q;
+  const long long seen = a.window > 0 && p.keys > reach ? reach : p.keys;
   return static_cast<double>(p.seqs) * p.rows * seen * a.c.heads >= 3e6;
 }
 

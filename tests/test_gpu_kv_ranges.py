@@ -94,3 +94,14 @@ def test_scores_far_below_zero(xq, case, size):  # noqa: F811
     assert clear.any()
     assert kc.relative(out[clear], want[clear]) <= kc.LIMIT[dtype], kc.relative(out[clear], want[clear])
     assert xq.device_error() == 0
+
+
+@pytest.mark.parametrize("case", [c for c in kc.RUNS if c[0] == "tiles"], ids=IDS)
+def test_a_window_of_the_largest_size_is_no_window(xq, case):  # noqa: F811
+    """Bit for bit: the same kernel has to be chosen."""
+    k, v, q, lens = setup(case)
+    cache, table, _ = kc.filled(xq, "q8", k, v, 32)
+    out = cache.attn(q, table, lens)
+    for window in (case[5], 2 ** 31 - 200, 2 ** 31 - 1):
+        assert torch.equal(cache.attn(q, table, lens, window=window), out)
+    assert xq.device_error() == 0
