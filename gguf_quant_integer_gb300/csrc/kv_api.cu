@@ -55,7 +55,7 @@ xq_status check_sizes(const xq_kv_cache* c, const xq_kv_query* q, bool shared) {
   // positions (own and prefix tokens) and the rows of the call stay within an int
   const long long longest = static_cast<long long>(q->max_pages) * c->page_size + (shared ? q->prefix_len : 0);
   const long long rows = static_cast<long long>(q->batch) * q->n_q;
-  if (longest > (1LL << 30) || q->n_q > (1 << 20) || rows * q->heads > (1LL << 30)) return XQ_ERR_SHAPE;
+  if (longest > (1LL << 30) || q->n_q > (1 << 20) || rows > (1LL << 30) || rows * q->heads > (1LL << 30)) return XQ_ERR_SHAPE;
   if (shared && q->prefix_len < 0) return XQ_ERR_SHAPE;
   return XQ_OK;
 }
