@@ -1196,6 +1196,7 @@ cudaError_t launch_split(SplitArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  g_kv_launched.store(true, std::memory_order_relaxed);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_split_kernel<BITS, D, EX, NP, NT>, a);
   if (e != cudaSuccess || a.whole) return e;
   cfg.blockDim = dim3(kJoinThreads);
@@ -1224,11 +1225,7 @@ cudaError_t KvAttnDim<D>::launch(SplitArgs& a, int bits, bool exact, int np, int
 
 template <int D>
 cudaError_t KvAttnDim<D>::take_error(unsigned int* code) {
-  unsigned int v = 0, z = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_kv_attn_error, sizeof(v));
-  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_kv_attn_error, &z, sizeof(z));
-  *code = v;
-  return e;
+  return take_record(g_kv_attn_error, code);
 }
 
 template <int D>

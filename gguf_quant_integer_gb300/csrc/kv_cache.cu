@@ -384,6 +384,7 @@ cudaError_t launch(K kernel, Args& A, long long tokens, int lanes, cudaStream_t 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  g_kv_launched.store(true, std::memory_order_relaxed);
   return cudaLaunchKernelEx(&cfg, kernel, A);
 }
 
@@ -446,13 +447,7 @@ cudaError_t launch_kv_read(const KvView& c, int bits, const int64_t* slots, int 
   return cudaSuccess;
 }
 
-cudaError_t take_kv_cache_error(unsigned int* code) {
-  unsigned int v = 0, z = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_kv_cache_error, sizeof(v));
-  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_kv_cache_error, &z, sizeof(z));
-  *code = v;
-  return e;
-}
+cudaError_t take_kv_cache_error(unsigned int* code) { return take_record(g_kv_cache_error, code); }
 cudaError_t take_kv_cache_check(unsigned int* code) { return take_check_word(code); }
 
 }  // namespace xq

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "xq_check.cuh"
@@ -57,6 +58,23 @@ cudaError_t launch_kv_read(const KvView& c, int bits, const int64_t* slots, int 
                            cudaStream_t s);
 cudaError_t launch_kv_attn(const KvAttnArgs& a, int bits, void* workspace, cudaStream_t s);
 size_t kv_attn_workspace(const KvAttnArgs& a, int bits);
+
+namespace {
+// Whether a kernel of this translation unit was launched since the program began. Its records are read only then: a read
+// takes 8 us and loads the unit's kernels, which callers who use no KV cache need not pay for.
+std::atomic<bool> g_kv_launched{false};
+
+// Read a record (a word in device memory), and clear it if it is set.
+template <typename Word>
+inline cudaError_t take_record(const Word& word, unsigned int* code) {
+  *code = 0;
+  if (!g_kv_launched.load(std::memory_order_relaxed)) return cudaSuccess;
+  cudaError_t e = cudaMemcpyFromSymbol(code, word, sizeof(*code));
+  const unsigned int zero = 0;
+  if (e == cudaSuccess && *code != 0) e = cudaMemcpyToSymbol(word, &zero, sizeof(zero));
+  return e;
+}
+}  // namespace
 
 // Read and clear the records of invalid indices (0: none) and the checked
 // builds' words of the KV kernels.

@@ -773,6 +773,7 @@ cudaError_t launch_tile_attn(SplitArgs& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  g_kv_launched.store(true, std::memory_order_relaxed);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_tile_kernel<BITS, D, P>, a);
   if (e != cudaSuccess || a.whole) return e;
   constexpr int kRowsBlock = 4;
@@ -792,12 +793,8 @@ cudaError_t KvTileDim<D>::launch(SplitArgs& a, int bits, bool two_pieces, cudaSt
 
 template <int D>
 cudaError_t KvTileDim<D>::take_error(unsigned int* index, unsigned int* wait) {
-  unsigned int z = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(index, g_kv_attn_error, sizeof(z));
-  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_kv_attn_error, &z, sizeof(z));
-  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(wait, g_kv_tile_error, sizeof(z));
-  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_kv_tile_error, &z, sizeof(z));
-  return e;
+  const cudaError_t e = take_record(g_kv_attn_error, index);
+  return e == cudaSuccess ? take_record(g_kv_tile_error, wait) : e;
 }
 
 #endif  // XQ_KV_ATTN_IMPL
