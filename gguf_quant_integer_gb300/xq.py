@@ -442,8 +442,9 @@ class KVCache:
     pages belong to which sequence is the caller's: attn takes a page table.
 
     A call that needs a workspace uses one that the object keeps for each
-    stream. Pass `workspace` (uint8, at least attn_workspace_bytes) to use
-    another, as a CUDA graph that is replayed beside eager calls has to.
+    stream; one that is captured into a CUDA graph takes its own from the
+    graph's memory. Pass `workspace` (uint8, at least attn_workspace_bytes)
+    to use another.
     """
 
     def __init__(self, qtype: int, n_pages: int, page_size: int, heads: int, dim: int, device="cuda", k=None, v=None):
@@ -468,6 +469,7 @@ class KVCache:
         self._write, self._read = L.xq_kv_write, L.xq_kv_read
         self._empty, self._empty_like, self._int32, self._int64 = torch.empty, torch.empty_like, torch.int32, torch.int64
         self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._capturing = torch.cuda.is_current_stream_capturing
         self._ws = {}   # stream -> (workspace, bytes, address)
         self._need = {}  # sizes of a call -> workspace bytes
 
@@ -527,18 +529,29 @@ class KVCache:
             raise XQError("xq_kv_attn_workspace_bytes", 2)
         return nb
 
-    def _workspace(self, key, stream):
-        """The stream's workspace, of at least what calls of these sizes (the
-        arguments of attn_workspace_bytes) need."""
+    def _on(self, stream):
+        """The call's stream as the current one (a context manager)."""
+        cuda = self._torch.cuda
+        return cuda.stream(cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream)
+
+    def _workspace(self, key, handle, stream):
+        """(tensor, bytes, address) of a workspace of at least what calls of these sizes (the arguments of
+        attn_workspace_bytes) need: the stream's own, kept from call to call and replaced by a larger one, or, while the
+        stream is captured, a new one. A graph keeps the address it was captured with: its memory must be the graph's (it
+        stays the graph's when the tensor is dropped), and not the next graph's too."""
         need = self._need.get(key)
         if need is None:
             need = self._need[key] = self.attn_workspace_bytes(*key)
-        ws = self._ws.get(stream)
+        if stream is not None:
+            with self._on(stream):
+                return self._workspace(key, handle, None)
+        capturing = self._capturing()
+        ws = None if capturing else self._ws.get(handle)
         if ws is None or ws[1] < need:
-            torch = self._torch
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=self.device)):
-                t = torch.empty(need, dtype=torch.uint8, device=self.device)
-            ws = self._ws[stream] = (t, need, t.data_ptr())
+            t = self._empty(need, dtype=self._torch.uint8, device=self.device)
+            ws = (t, need, t.data_ptr())
+            if not capturing:
+                self._ws[handle] = ws
         return ws
 
     def _attn(self, fn, q, pages, lens, scale, window, prefix_pages, prefix_len, out, workspace, stream):
@@ -565,7 +578,7 @@ class KVCache:
             prefix = prefix_pages.data_ptr()
         s, width, dtype = self._stream(stream), pshape[1], q.dtype
         if workspace is None:
-            _, ws_bytes, ws = self._workspace((dtype, batch, n_q, heads, width, prefix_len), s)
+            held, ws_bytes, ws = self._workspace((dtype, batch, n_q, heads, width, prefix_len), s, stream)
         else:
             ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
             if workspace.device != dev or not workspace.is_contiguous():
