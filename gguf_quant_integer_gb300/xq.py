@@ -444,7 +444,8 @@ class KVCache:
     A call that needs a workspace uses one that the object keeps for each
     stream; one that is captured into a CUDA graph takes its own from the
     graph's memory. Pass `workspace` (uint8, at least attn_workspace_bytes)
-    to use another.
+    to use another. Results and workspaces that a call makes belong to the
+    stream that the call runs on, the current one or `stream`.
     """
 
     def __init__(self, qtype: int, n_pages: int, page_size: int, heads: int, dim: int, device="cuda", k=None, v=None):
@@ -467,7 +468,7 @@ class KVCache:
         self._inner = (dim, 1)
         L = self._lib = lib()
         self._write, self._read = L.xq_kv_write, L.xq_kv_read
-        self._empty, self._empty_like, self._int32, self._int64 = torch.empty, torch.empty_like, torch.int32, torch.int64
+        self._empty, self._int32, self._int64 = torch.empty, torch.int32, torch.int64
         self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._capturing = torch.cuda.is_current_stream_capturing
         self._ws = {}   # stream -> (workspace, bytes, address)
@@ -509,11 +510,11 @@ class KVCache:
             dtype = self._torch.float32 if k is None else k.dtype
         kind = _float_type(dtype)
         if k is None:
-            k = self._empty(shape, dtype=dtype, device=dev)
+            k = self._new(shape, dtype, stream)
         elif k.shape != shape or k.dtype != dtype or not k.is_contiguous() or k.device != dev:
             raise ValueError(f"k: contiguous {shape} of {dtype} on {dev}")
         if v is None:
-            v = self._empty(shape, dtype=dtype, device=dev)
+            v = self._new(shape, dtype, stream)
         elif v.shape != shape or v.dtype != dtype or not v.is_contiguous() or v.device != dev:
             raise ValueError(f"v: contiguous {shape} of {dtype} on {dev}")
         rc = self._read(self._ref, slots.data_ptr(), n, kind, k.data_ptr(), v.data_ptr(), self._stream(stream))
@@ -533,6 +534,14 @@ class KVCache:
         """The call's stream as the current one (a context manager)."""
         cuda = self._torch.cuda
         return cuda.stream(cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream)
+
+    def _new(self, shape, dtype, stream):
+        """Memory for a result. The allocator hands a stream's freed memory to the same stream without waiting, so it has to
+        be the stream that writes the result: another's may still be in use there."""
+        if stream is None:
+            return self._empty(shape, dtype=dtype, device=self.device)
+        with self._on(stream):
+            return self._empty(shape, dtype=dtype, device=self.device)
 
     def _workspace(self, key, handle, stream):
         """(tensor, bytes, address) of a workspace of at least what calls of these sizes (the arguments of
@@ -567,7 +576,7 @@ class KVCache:
         if q.device != dev or pages.device != dev or lens.device != dev:
             raise ValueError(f"q, pages and lens have to be on {dev}")
         if out is None:
-            out = self._empty_like(q)
+            out = self._new(shape, q.dtype, stream)
         elif out.shape != shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != dev:
             raise ValueError("out: a contiguous tensor like q")
         prefix = None
