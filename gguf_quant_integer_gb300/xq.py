@@ -440,6 +440,7 @@ class KVCache:
     kv_bytes(...) bytes each (k, v: existing ones; otherwise zeroed ones are
     made). Token slot s is row s % page_size of page s // page_size; which
     pages belong to which sequence is the caller's: attn takes a page table.
+    The pools' device has to be the current one when a call is made.
 
     A call that needs a workspace uses one that the object keeps for each
     stream; one that is captured into a CUDA graph takes its own from the
@@ -469,12 +470,16 @@ class KVCache:
         L = self._lib = lib()
         self._write, self._read = L.xq_kv_write, L.xq_kv_read
         self._empty, self._int32, self._int64 = torch.empty, torch.int32, torch.int64
+        self._device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         self._current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self._capturing = torch.cuda.is_current_stream_capturing
         self._ws = {}   # stream -> (workspace, bytes, address)
         self._need = {}  # sizes of a call -> workspace bytes
 
     def _stream(self, stream):
+        # kernels go to the current device, whatever device the pointers are of
+        if self._device() != self.device.index:
+            raise ValueError(f"the cache is on {self.device}: make that the current device (torch.cuda.device)")
         # the current stream's handle: torch's accessor of the bare handle costs a fortieth of building a Stream object
         if stream is None:
             return self._current(self.device.index) if self._current else self._torch.cuda.current_stream(self.device).cuda_stream
