@@ -1183,9 +1183,9 @@ cudaError_t launch_split(SplitArgs& a, cudaStream_t s) {
   using S = SplitShape<BITS, D, EX, NP, NT>;
   constexpr int kResident = S::kCtas * kNumSMs;
   a.ctas = a.units < kResident ? static_cast<int>(a.units) : kResident;
-  static const cudaError_t attr_error =
-      cudaFuncSetAttribute(kv_split_kernel<BITS, D, EX, NP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-  if (attr_error != cudaSuccess) return attr_error;
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_shared(kv_split_kernel<BITS, D, EX, NP, NT>, S::kSmem, allowed);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
   cfg.blockDim = dim3(32 * kAttnWarps);
@@ -1197,7 +1197,7 @@ cudaError_t launch_split(SplitArgs& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   g_kv_launched.store(true, std::memory_order_relaxed);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_split_kernel<BITS, D, EX, NP, NT>, a);
+  e = cudaLaunchKernelEx(&cfg, kv_split_kernel<BITS, D, EX, NP, NT>, a);
   if (e != cudaSuccess || a.whole) return e;
   cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;

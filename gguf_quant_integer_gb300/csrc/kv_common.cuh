@@ -64,6 +64,20 @@ namespace {
 // takes 8 us and loads the unit's kernels, which callers who use no KV cache need not pay for.
 std::atomic<bool> g_kv_launched{false};
 
+// Allow a kernel `bytes` of dynamic shared memory on the current device. `done`: the devices that have it (one bit each, the
+// first 64), of this kernel.
+template <typename K>
+inline cudaError_t allow_shared(K kernel, int bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // Read a record (a word in device memory), and clear it if it is set.
 template <typename Word>
 inline cudaError_t take_record(const Word& word, unsigned int* code) {

@@ -760,9 +760,9 @@ template <int BITS, int D, int P>
 cudaError_t launch_tile_attn(SplitArgs& a, cudaStream_t s) {
   using S = TileShape<BITS, D, P>;
   a.ctas = a.units < kNumSMs ? static_cast<int>(a.units) : kNumSMs;
-  static const cudaError_t attr_error =
-      cudaFuncSetAttribute(kv_tile_kernel<BITS, D, P>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-  if (attr_error != cudaSuccess) return attr_error;
+  static std::atomic<unsigned long long> allowed{0};
+  cudaError_t e = allow_shared(kv_tile_kernel<BITS, D, P>, S::kSmem, allowed);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.ctas));
   cfg.blockDim = dim3(32 * kTileWarps);
@@ -774,7 +774,7 @@ cudaError_t launch_tile_attn(SplitArgs& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   g_kv_launched.store(true, std::memory_order_relaxed);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_tile_kernel<BITS, D, P>, a);
+  e = cudaLaunchKernelEx(&cfg, kv_tile_kernel<BITS, D, P>, a);
   if (e != cudaSuccess || a.whole) return e;
   constexpr int kRowsBlock = 4;
   cfg.gridDim = join_grid<kTileChunk, kRowsBlock>(a.ctas);
