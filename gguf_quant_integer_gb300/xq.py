@@ -555,6 +555,8 @@ class KVCache:
         stays the graph's when the tensor is dropped), and not the next graph's too."""
         need = self._need.get(key)
         if need is None:
+            if len(self._need) >= 1024:  # a prefix that grows gives new sizes without end
+                self._need.clear()
             need = self._need[key] = self.attn_workspace_bytes(*key)
         if stream is not None:
             with self._on(stream):

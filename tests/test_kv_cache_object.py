@@ -24,3 +24,13 @@ def test_calls_on_another_device_than_the_current_one_are_refused(cache):
                  lambda: cache.attn_shared(q, table[0], 20, table, lens, workspace=ws)):
         with pytest.raises(ValueError, match="current device"):
             call()
+
+
+def test_remembered_sizes_are_bounded(cache):
+    cache._capturing = lambda: False
+    q, lens = torch.float32, 1
+    for prefix in range(1, 5000):
+        key = (q, 2, 1, 4, lens, prefix)
+        held = cache._workspace(key, 0, None)
+        assert held[1] >= cache.attn_workspace_bytes(*key)
+    assert len(cache._need) <= 1024 and len(cache._ws) == 1
