@@ -491,7 +491,8 @@ class KVCache:
         a part of longer ones (k.stride(0))."""
         n, dev = slots.shape[0], self.device
         shape, ks, vs = (n, self.heads, self.dim), k.stride(), v.stride()
-        if k.shape != shape or v.shape != shape or k.dtype != v.dtype or ks[1:] != self._inner or vs[1:] != self._inner:
+        rows = ks[1:] == self._inner == vs[1:] or (self.heads == 1 and ks[2:] == (1,) == vs[2:])  # (one head's stride says nothing)
+        if k.shape != shape or v.shape != shape or k.dtype != v.dtype or not rows:
             raise ValueError(f"k and v: {shape} of one dtype, each token's row contiguous")
         if slots.dtype != self._int64 or slots.dim() != 1 or not slots.is_contiguous():
             raise ValueError("slots: contiguous int64 [tokens]")
