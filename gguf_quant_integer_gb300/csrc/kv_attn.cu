@@ -130,6 +130,8 @@ cudaError_t launch_kv_attn(const KvAttnArgs& a, int bits, void* workspace, cudaS
   p.pages = a.pages;
   p.page_stride = a.page_stride;
   p.store = a.prefix_len > 0;
+  p.part_rows = static_cast<long long>((L.part_o - L.part_el) / 8);
+  p.records = kMaxCtas;
   const cudaError_t e = run(p, own_pass(a), a, bits, s);
   if (e != cudaSuccess || a.prefix_len == 0) return e;
   // Then every row of the call against the prefix, which is read once. The
@@ -146,7 +148,8 @@ cudaError_t launch_kv_attn(const KvAttnArgs& a, int bits, void* workspace, cudaS
 namespace {
 typedef cudaError_t (*TakeFn)(unsigned int*);
 // The first word recorded in any of the kernels' translation units; all are cleared.
-cudaError_t take_all(const TakeFn (&fns)[4], unsigned int* code) {
+template <size_t N>
+cudaError_t take_all(const TakeFn (&fns)[N], unsigned int* code) {
   *code = 0;
   for (TakeFn f : fns) {
     unsigned int c = 0;
@@ -177,8 +180,8 @@ cudaError_t take_kv_tile_error(unsigned int* index, unsigned int* wait) {
   return cudaSuccess;
 }
 cudaError_t take_kv_attn_check(unsigned int* code) {
-  const TakeFn fns[4] = {KvAttnDim<64>::take_check, KvAttnDim<96>::take_check, KvAttnDim<128>::take_check,
-                         KvAttnDim<256>::take_check};
+  const TakeFn fns[7] = {KvAttnDim<64>::take_check, KvAttnDim<96>::take_check, KvAttnDim<128>::take_check, KvAttnDim<256>::take_check,
+                         KvTileDim<64>::take_check, KvTileDim<96>::take_check, KvTileDim<128>::take_check};
   return take_all(fns, code);
 }
 

@@ -105,6 +105,9 @@ struct SplitArgs {
   float* pre_el;
   bool store, merge;
   bool late;  // starts beside the call's first pass: waits for it only where it merges, and at its end
+  // What the checked build measures against: rows of partial results and records that the workspace holds.
+  long long part_rows;
+  int records;
 };
 
 template <int BITS, int D, bool EX, int NP, int NT>
@@ -305,9 +308,20 @@ __device__ __forceinline__ void store4(void* p, int type, size_t i, float4 v) {
   }
 }
 
+// ---- extents, for the checked build
+__device__ __forceinline__ int table_len(const SplitArgs& A) {
+  return A.flat ? (A.prefix_len + (1 << A.c.page_shift) - 1) >> A.c.page_shift : A.max_pages;
+}
+__device__ __forceinline__ long long out_rows(const SplitArgs& A) { return static_cast<long long>(A.seqs) * A.rows * A.c.heads; }
+// bytes at byte `at` of a pool, both multiples of 16
+__device__ __forceinline__ bool in_pool(const SplitArgs& A, long long at, long long bytes) {
+  return at >= 0 && at + bytes <= A.c.n_pages * A.c.page_bytes && ((at | bytes) & 15) == 0;
+}
+
 // Tokens of sequence b that its table can hold.
 __device__ __forceinline__ int seq_len(const SplitArgs& A, int b) {
   if (A.flat) return A.prefix_len;
+  if (!XQ_IN(b, A.seqs, kChkKvLens)) return 0;
   const int n = A.lens[b];
   const long long most = static_cast<long long>(A.max_pages) << A.c.page_shift;
   return n < 0 ? 0 : n > most ? static_cast<int>(most) : n;
@@ -338,7 +352,7 @@ __device__ __forceinline__ void row_range(const SplitArgs& A, int seq, int n, in
   const int token = quot(r, A.group);
   if (A.flat) {
     const int b = quot(token, A.n_q);
-    int own = A.lens[b];
+    int own = XQ_IN(r, A.rows, kChkKvLens) ? A.lens[b] : 0;
     const long long most = static_cast<long long>(A.max_pages) << A.c.page_shift;
     own = own < 0 ? 0 : own > most ? static_cast<int>(most) : own;
     const int pos = kv_pos(A.prefix_len, own, A.n_q, token - b * A.n_q);
@@ -353,6 +367,7 @@ __device__ __forceinline__ void row_range(const SplitArgs& A, int seq, int n, in
 
 // Row (token, head) `at` of the result: sums o and l relative to 2^e.
 __device__ __forceinline__ void finish4(const SplitArgs& A, int D, size_t at, int d, float4 o, float e, float l) {
+  if (!XQ_IN(at, out_rows(A), kChkKvQuery)) return;
   if (A.store) {
     *reinterpret_cast<float4*>(A.pre_o + at * D + d) = o;
     if (d == 0) *reinterpret_cast<float2*>(A.pre_el + at * 2) = make_float2(e, l);
@@ -439,7 +454,7 @@ __device__ __forceinline__ bool line_begin(const SplitArgs& A, LineShared& sh, L
   L.ctas = L.total < A.ctas ? static_cast<int>(L.total) : A.ctas;
   const int cta = blockIdx.x;
   if (cta >= L.ctas) {
-    if (tid == 0 && !A.whole) A.record[cta] = make_int4(0, 0, -1, 0);
+    if (tid == 0 && !A.whole && XQ_IN(cta, A.records, kChkKvPart)) A.record[cta] = make_int4(0, 0, -1, 0);
     return false;
   }
   L.u = L.total * cta / L.ctas;
@@ -574,7 +589,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
   int next_page = 0;
   unsigned bad = 0;      // stages whose page id was invalid
   unsigned clean_n = 0;  // tiles from `clean` on that hold only keys which every row sees
-  auto page_of = [&](int i) { return i < tiles ? table[(tile0 + i * kAttnWarps) >> shift] : 0; };
+  auto page_of = [&](int i) {
+    const int at = (tile0 + i * kAttnWarps) >> shift;
+    return i < tiles && XQ_IN(at, table_len(A), kChkKvTable) ? table[at] : 0;
+  };
   auto locate = [&](int i, int page) {
     const int line = line0 + (((tile0 + i * kAttnWarps) & ((1 << shift) - 1)) << 4);
     const bool ok = static_cast<unsigned>(page) < static_cast<unsigned>(A.c.n_pages);
@@ -589,7 +607,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
         next_page = page_of(i + 32 + lane);
       }
       const uint32_t at = __shfl_sync(0xffffffffu, code_at, i & 31), so = __shfl_sync(0xffffffffu, scales_at, i & 31);
-      if (at != ~0u) {
+      if (at != ~0u && !XQ_CHECKED(in_pool(A, 32ll * at, 16 * S::kRow) && in_pool(A, 32ll * so, S::kScales), kChkKvTile)) {
+      } else if (at != ~0u) {
         const uint8_t* const kc = k_from + static_cast<size_t>(at) * 32;
         const uint8_t* const vc = v_from + static_cast<size_t>(at) * 32;
         const uint32_t base = stage0 + stage * S::kStage, dst = base + code_to;
@@ -639,7 +658,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const int r = NP == 2 ? 4 * j + (g >> 1) : 8 * j + g;
-      raw[j].load(A, r < rows ? row_at(A, sq, head, row0 + r) * D + 4 * t : 0, r < rows);
+      const size_t at = r < rows ? row_at(A, sq, head, row0 + r) : 0;
+      raw[j].load(A, at * D + 4 * t, r < rows && XQ_IN(at, out_rows(A), kChkKvQuery));
     }
     if (!begun) begin_part(cur);
     // ---- queries as B operands. Column g of n-tile j: NP = 2: row 4 j + g/2, piece g & 1; NP = 1: row 8 j + g.
@@ -1067,19 +1087,20 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
       } else {
         // a pair that began in an earlier CTA goes to the first slot, one that goes on in the next to the second
         const size_t ps = (static_cast<size_t>(cta) * 2 + (k0 == 0 ? 1 : 0)) * R + r;
+        if (!XQ_IN(ps, A.part_rows, kChkKvPart)) continue;
         *reinterpret_cast<float4*>(A.part_o + ps * D + d) = y;
         if (d == 0) *reinterpret_cast<float2*>(A.part_el + ps * 2) = make_float2(e, ll);
       }
     }
     if (!whole && k0 == 0) {
       left_record = true;
-      if (tid == 0) A.record[cta] = make_int4(sq, pair, line_last(A, line, cur), 0);
+      if (tid == 0 && XQ_IN(cta, A.records, kChkKvPart)) A.record[cta] = make_int4(sq, pair, line_last(A, line, cur), 0);
     }
     __syncthreads();
     cur = next;
     have = more_parts;
   }
-  if (!left_record && tid == 0 && !A.whole) A.record[cta] = make_int4(0, 0, -1, 0);
+  if (!left_record && tid == 0 && !A.whole && XQ_IN(cta, A.records, kChkKvPart)) A.record[cta] = make_int4(0, 0, -1, 0);
   if (A.late) grid_wait();
 }
 
@@ -1107,7 +1128,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) kv_join_kernel(cons
   const int row = RB * blockIdx.y + r;
   int4 mine = make_int4(0, 0, -1, 0);  // the records, one a lane
   const int per = (A.ctas + gridDim.x - 1) / gridDim.x, c = blockIdx.x * per + lane;
-  if (lane < per && c < A.ctas) mine = A.record[c];
+  if (lane < per && c < A.ctas && XQ_IN(c, A.records, kChkKvPart)) mine = A.record[c];
   for (unsigned left = __ballot_sync(0xffffffffu, mine.z >= 0); left; left &= left - 1) {
     const int from = __ffs(left) - 1, c0 = blockIdx.x * per + from;
     const int seq = __shfl_sync(0xffffffffu, mine.x, from), pair = __shfl_sync(0xffffffffu, mine.y, from);
@@ -1127,6 +1148,9 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) kv_join_kernel(cons
           if (i < parts) {
             // part i: the second slot of the CTA where the pair begins, the first of those after it
             const size_t slot = (static_cast<size_t>(c0 + i) * 2 + (i == 0 ? 1 : 0)) * R + row;
+            el[x] = make_float2(kNoKey, 0.0f);
+            z[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (!XQ_IN(slot, A.part_rows, kChkKvPart)) continue;
             el[x] = *reinterpret_cast<const float2*>(A.part_el + slot * 2);
             z[x] = *reinterpret_cast<const float4*>(A.part_o + (COLS ? (slot - row) * D + d * R + row * 4 : slot * D + d));
           }

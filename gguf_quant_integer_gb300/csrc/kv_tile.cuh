@@ -86,6 +86,7 @@ template <int D>
 struct KvTileDim {
   static cudaError_t launch(SplitArgs& a, int bits, bool two_pieces, cudaStream_t s);
   static cudaError_t take_error(unsigned int* index, unsigned int* wait);
+  static cudaError_t take_check(unsigned int* code);
 };
 
 #ifdef XQ_KV_ATTN_IMPL
@@ -276,8 +277,9 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
         it += tiles;
         continue;
       }
-      const bool live = row0 + row < A.rows;
-      const size_t at = live ? row_at(A, part.seq, head, row0 + row) : 0;
+      const bool mine = row0 + row < A.rows;
+      const size_t at = mine ? row_at(A, part.seq, head, row0 + row) : 0;
+      const bool live = mine && XQ_IN(at, out_rows(A), kChkKvQuery);
       int lim0 = 0, lim1 = 0;
       if (live) row_range(A, part.seq, part.n, row0 + row, &lim0, &lim1);
       // ---- the row's query into tensor memory: fp16, its largest element at 2^12 .. 2^13; negated for a negative scale (so
@@ -457,19 +459,22 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
                                          __uint_as_float(w[x + 3]) * f);
             if (whole)
               finish4(A, D, at, c + x, y, e, sum);
-            else
+            else if (XQ_IN(slot, A.part_rows, kChkKvPart))
               *reinterpret_cast<float4*>(A.part_o + (slot - row) * D + (c + x) * kTileChunk + row * 4) = y;
           }
         }
       }
-      if (live && !whole) *reinterpret_cast<float2*>(A.part_el + slot * 2) = make_float2(e, sum);
+      if (live && !whole && XQ_IN(slot, A.part_rows, kChkKvPart))
+        *reinterpret_cast<float2*>(A.part_el + slot * 2) = make_float2(e, sum);
       if (!whole && part.k0 == 0) {
         left_record = true;
-        if (tid == 0) A.record[blockIdx.x] = make_int4(part.seq, part.pair, line_last(A, line, part), 0);
+        if (tid == 0 && XQ_IN(blockIdx.x, A.records, kChkKvPart))
+          A.record[blockIdx.x] = make_int4(part.seq, part.pair, line_last(A, line, part), 0);
       }
       ptx::tc_fence_before();
     }
-    if (!left_record && tid == 0 && !A.whole) A.record[blockIdx.x] = make_int4(0, 0, -1, 0);
+    if (!left_record && tid == 0 && !A.whole && XQ_IN(blockIdx.x, A.records, kChkKvPart))
+      A.record[blockIdx.x] = make_int4(0, 0, -1, 0);
   } else {
     // ------------------------------------------------ copying and unpacking
     // Two groups of four warps, each a tile: one's copies and barriers pass while the other unpacks.
@@ -488,7 +493,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       const int groups = (part.n + 15) / 16;  // of the sequence
       // Address of 16-key group gi's page, or 0; its first row within the head's rows.
       auto page_at = [&](int gi) -> long long {
-        if (gi >= groups) return 0;
+        if (gi >= groups || !XQ_IN(gi >> group_shift, table_len(A), kChkKvTable)) return 0;
         const int page = table[gi >> group_shift];
         if (static_cast<unsigned>(page) < static_cast<unsigned>(A.c.n_pages))
           return reinterpret_cast<long long>(A.c.k) + page * A.c.page_bytes;
@@ -502,7 +507,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
       // (K's codes, V's, K's scales, V's; all from one warp, 16 keys each, took some 1900 clocks a tile)
       auto id_at = [&](int i) {
         const int gi = (unit0 + i) * 4 + (lane & 3);
-        return i < tiles && gi < groups ? table[gi >> group_shift] : -1;
+        return i < tiles && gi < groups && XQ_IN(gi >> group_shift, table_len(A), kChkKvTable) ? table[gi >> group_shift] : -1;
       };
       int next_id = id_at(group);
       unsigned miss = 0, next_miss = 0;  // 16-key groups without a valid page: of this tile, of the one on its way
@@ -524,11 +529,14 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             const int kind = gt >> 5, v = kind & 1, row = row_of(gi0 + lane);
             const uint32_t to = base + S::kOffRaw + (S::kRawStages * group + stage) * S::kRaw;
             const uint8_t* const from = reinterpret_cast<const uint8_t*>(page + (v ? v_off : 0));
-            if (kind < 2)
+            if (!XQ_CHECKED(in_pool(A, page - reinterpret_cast<long long>(A.c.k) + (kind < 2 ? row * S::kRow : A.c.scale_off + row * (2 * NB)),
+                                    n * (kind < 2 ? kCodes : kScale)), kChkKvTile)) {
+            } else if (kind < 2) {
               ptx::bulk_load(to + v * S::kRawCodes + lane * kCodes, from + row * S::kRow, n * kCodes, full);
-            else
+            } else {
               ptx::bulk_load(to + 2 * S::kRawCodes + v * S::kRawScales + lane * kScale, from + A.c.scale_off + row * (2 * NB),
                              n * kScale, full);
+            }
           }
         }
       };
@@ -562,6 +570,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 1) kv_tile_kernel(const __gri
             k4[y] = v4[y] = make_uint4(0u, 0u, 0u, 0u);
             if (!page[y]) continue;
             const uint8_t* const p = reinterpret_cast<const uint8_t*>(page[y]) + A.c.scale_off + row_of(gi) * (2 * NB) + piece * 16;
+            if (!XQ_CHECKED(in_pool(A, p - A.c.k, 16), kChkKvTile)) continue;
             k4[y] = *reinterpret_cast<const uint4*>(p);
             v4[y] = *reinterpret_cast<const uint4*>(p + v_off);
           }
@@ -795,6 +804,11 @@ template <int D>
 cudaError_t KvTileDim<D>::take_error(unsigned int* index, unsigned int* wait) {
   const cudaError_t e = take_record(g_kv_attn_error, index);
   return e == cudaSuccess ? take_record(g_kv_tile_error, wait) : e;
+}
+
+template <int D>
+cudaError_t KvTileDim<D>::take_check(unsigned int* code) {
+  return take_check_word(code);
 }
 
 #endif  // XQ_KV_ATTN_IMPL

@@ -74,8 +74,14 @@ enum CheckSite : unsigned {
   kChkQ6Act = 41,  // quant / d8 read inside the Q8 buffer
   kChkQ6Y = 42,
   kChkQ6Isum = 43,
-  // kv_cache.cu, kv_attn.cu
-  kChkKvRow = 50,   // row inside its page
+  // kv_cache.cu
+  kChkKvRow = 50,    // row inside its page
+  // kv_attn.cuh, kv_tile.cuh
+  kChkKvTable = 51,  // entry of a page table inside its row
+  kChkKvTile = 52,   // codes and scales of 16 keys (or a page's part of a tile) inside the pool, on 16-byte boundaries
+  kChkKvQuery = 53,  // row of q, of the result or of the stored first pass inside [tokens][heads]
+  kChkKvPart = 54,   // partial result or record inside the workspace
+  kChkKvLens = 55,   // sequence inside the batch
 };
 
 }  // namespace xq
