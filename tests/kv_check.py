@@ -35,10 +35,10 @@ def filled(xq, kind, k, v, page, seed=0):
     return cache, table[None], slots
 
 
-def seen(n_q, n, window=0, prefix=0):
+def seen(n_q, n, window=0, prefix=0, device="cuda"):
     """bool [n_q, prefix + n]: which keys each query token sees."""
-    pos = torch.arange(prefix + n - n_q, prefix + n, device="cuda")[:, None]
-    j = torch.arange(prefix + n, device="cuda")
+    pos = torch.arange(prefix + n - n_q, prefix + n, device=device)[:, None]
+    j = torch.arange(prefix + n, device=device)
     mask = j <= pos
     return mask & (j > pos - window) if window else mask
 
@@ -48,6 +48,8 @@ def attention64(q, k, v, scale, mask):
     What is not finite in K or V counts as 0: callers look at rows that see none of it."""
     n_q, hq, dim = q.shape
     heads = k.shape[1]
+    if k.shape[0] == 0:
+        return torch.zeros(q.shape, dtype=torch.float64, device=q.device)
     k, v = (torch.nan_to_num(x.double(), 0.0, 0.0, 0.0) for x in (k, v))
     z = torch.einsum("ihgd,lhd->hgil", q.double().view(n_q, heads, hq // heads, dim), k) * scale
     z = z.masked_fill(~mask, -float("inf"))
