@@ -600,6 +600,10 @@ class KVCache:
             ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
             if workspace.device != dev or not workspace.is_contiguous():
                 raise ValueError(f"workspace: contiguous, on {dev}")
+        # ctypes keeps the low 32 bits of an int: a larger window would become another one
+        window = window if window < 0x7FFFFFFF else 0x7FFFFFFF
+        if prefix_len > 0x7FFFFFFF or window < -0x80000000:
+            raise XQError(fn.__name__, 2)
         query = xq_kv_query(_float_type(dtype), batch, n_q, heads, q.data_ptr(), out.data_ptr(), pages.data_ptr(),
                             ps[0] if batch > 1 else width, width, lens.data_ptr(), dim ** -0.5 if scale is None else scale, window,
                             prefix, prefix_len)
