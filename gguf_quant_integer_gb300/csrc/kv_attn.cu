@@ -32,13 +32,18 @@ Pass prefix_pass(const KvAttnArgs& a) { return {1, a.batch * a.rows, a.prefix_le
 // Whether a pass goes to the tcgen05 tiles, which are for 16-bit queries. They
 // take some 20 us whatever the work, and then, from 64 rows on, a fraction of
 // the split kernel's time for it. Both measured (tiles, split; 8 KV heads, dim
-// 128, Q8_0, whole calls, us):
-//   bf16  256 rows x 2048 keys 32.1 and 31.8, x 32768 66 and 194; 128 rows
-//         x 2048 22.9 and 22.8, x 8192 27 and 40, x 32768 46 and 105; 64 rows
-//         x 2048 22.7 and 20.1, x 8192 29.7 and 29.2; 32 rows x 32768 55, 41
-//   fp16  256 rows x 2048 34.4 and 31.9, x 32768 78 and 194; 128 rows x 2048
-//         24.0 and 22.9, x 8192 29 and 40, x 32768 54 and 105; 64 rows x 32768
-//         60 and 62
+// 128, Q8_0, whole calls behind a prefix of that many keys, us):
+//   bf16  256 rows x 2048 keys 32 and 32, x 8192 40 and 65, x 32768 69 and 196;
+//         128 rows x 2048 24 and 23, x 8192 28 and 40, x 32768 48 and 106;
+//         64 rows x 2048 24 and 20, x 8192 31 and 29, x 32768 59 and 62;
+//         32 rows x 32768 57 and 41
+//   fp16  256 rows x 2048 34 and 32, x 8192 45 and 65, x 32768 81 and 196;
+//         128 rows x 2048 25 and 23, x 8192 31 and 40, x 32768 55 and 106;
+//         64 rows x 8192 34 and 29, x 32768 65 and 62
+// Where the rule is wrong: at 4.2 million (256 x 2048, 64 x 8192) the tiles are
+// as fast or 7 % slower for bf16 and 7 to 16 % slower for fp16, and 64 fp16
+// rows never gain. It counts the table's width, not the lengths, which are on
+// the device.
 bool tiled(const KvAttnArgs& a, const Pass& p) {
   if (a.type == kF32 || a.c.dim > 128 || p.rows < 64) return false;
   const long long reach = static_cast<long long>(a.window) + a.n_q;

@@ -16,6 +16,8 @@
 // e is a running reference per query instead of the exact running maximum: it
 // moves only when some weight w would pass 2^15 (it then restarts at 2^11), which also keeps w inside
 // fp16 whatever the sizes of V. One vote per 16 keys; the rescale is rare.
+// A V scale that is not finite stops there too: its block becomes NaN in the
+// rows that see the key, and the scale 0 for the products.
 // Score columns become weight columns by movmatrix, whose 8x8 transpose takes
 // an accumulator's (key, query pair) registers to the B operand.
 //
@@ -24,7 +26,7 @@
 // against 4 instructions. A warp's 16 keys cost some 420 instructions, so long
 // Q8_0 caches are bound by HBM and Q4_0's nearly as much by instructions: 64
 // sequences, 230000 tokens in all, 8 KV heads, fp32: 84 us, 5.9 TB/s with the
-// join; one sequence of 131071 Q4_0 tokens, bf16: 37 us, 4.1 TB/s, of which 4
+// join; one sequence of 131071 Q4_0 tokens, bf16: 38 us, 4.0 TB/s, of which 4
 // are the join and 5 pass before the first tile's products. Short calls are
 // bound by latency: one sequence of 97 tokens 5.5 us (10000 clocks: 3000 to
 // find the work, 3000 for queries and the first tile, 1000 to 1500 a tile).

@@ -24,8 +24,12 @@
 // computed two tiles ahead of the outputs where tensor memory has the columns
 // (128 rows), else one. Raw tiles come by bulk copies, two of a group's ahead.
 //
+// Not finite: a K scale gives its key's column NaN, which the rows that do not
+// see the key mask; a V scale is 0 in the operand, and the rows that see its key
+// are told which block to end as NaN (kOddV). Large scores: see `far`.
+//
 // What bounds it, in clocks a tile at dim 128, Q8_0 (the tensor cores need 1024
-// with two row tiles and one piece):
+// with two row tiles and one piece; taken before what the paragraph above adds, 3 %):
 //   256 rows: 2600, most of it a softmax thread's 64 scores (tensor memory
 //     there and back, maximum, exponentials); 3500 with two pieces. Twice the
 //     softmax warps would have 72 registers a thread: slower (104 us for 74 of
@@ -35,8 +39,8 @@
 // Before a part's first scores come some 20000 (page ids, the part's scales,
 // the first tile, and instructions seen for the first time: hence the rolled
 // loops outside the tiles'), after its last weights 6000 for the results.
-// Whole calls, 8 KV heads over 32768 keys: 256 bf16 rows 64 us (34 GFLOP, 530
-// TFLOP/s), 128 bf16 rows 46 us, 256 fp16 rows 78 us.
+// Whole calls, 8 KV heads over 32768 keys: 256 bf16 rows 69 us (34 GFLOP, 500
+// TFLOP/s), 128 bf16 rows 48 us, 256 fp16 rows 81 us.
 // Work is cut as in kv_attn.cuh: units of 64 keys, one CTA an SM.
 #pragma once
 
