@@ -12,7 +12,8 @@
 // elements x 16 keys) and block scales applied in fp32: dk to a block's sum,
 // dv to the weight. q and w enter as fp16: 16-bit queries as one number,
 // fp32 ones as two (hi + lo, 22 bits, one column each), so that a column pair
-// adds up to the fp32 product.
+// adds up to the fp32 product. fp32 outputs are summed in fp32 additions every
+// kAttnRun tiles.
 // e is a running reference per query instead of the exact running maximum: it
 // moves only when some weight w would pass 2^15 (it then restarts at 2^11), which also keeps w inside
 // fp16 whatever the sizes of V. One vote per 16 keys; the rescale is rare.
@@ -131,9 +132,12 @@ struct SplitShape {
   // Stages of 16 keys a warp: about 13 KB (three 4.25 KB stages of Q8_0 at dim
   // 128), so that 12 warps an SM keep 100 KB in flight. (18 KB: 4 us more on
   // the batch above.)
-  static constexpr int kStages = kStage * 3 > 13312 ? 3 : 13312 / kStage > 6 ? 6 : 13312 / kStage;
+  // Two where a third and the fp32 sums below would leave the SM one CTA.
+  static constexpr int kStages = EX && kStage > 8192 ? 2 : kStage * 3 > 13312 ? 3 : 13312 / kStage > 6 ? 6 : 13312 / kStage;
   static constexpr int kWarpBytes = kStages * kStage > R * D * 4 ? kStages * kStage : R * D * 4;
-  static constexpr int kSmem = kAttnWarps * kWarpBytes;
+  // fp32: a warp's sums (a lane's own, four floats a step) and their references.
+  static constexpr int kSums = R * D * 4, kSumBytes = EX ? kSums + NT * 32 * 4 : 0;
+  static constexpr int kSmem = kAttnWarps * (kWarpBytes + kSumBytes);
   // A warp's results fit one stage: the next pair's first tiles can be on
   // their way into the others while the warps are merged.
   static constexpr bool kOverlap = R * D * 4 <= kStage;
@@ -144,6 +148,13 @@ struct SplitShape {
   // against 26 us).
   static constexpr int kCtas = D == 256 || NT == 2 ? 2 : 3;
 };
+
+// Tiles of a warp after which fp32 outputs leave the tensor cores' accumulators for sums in shared memory. An accumulator
+// cuts off what an fp32 addition would round, and always towards 0: some 1.2e-8 of the output a tile, 6e-6 over the 512 tiles a
+// warp of 64 sequences behind 32768 keys, where the same in fp32 operations has 5e-7. With 32 tiles the error is 3.5e-7 to
+// 5.8e-7 at any length. 64 sequences of 8000 keys, fp32: 173 us with and without; two n-tiles 399 and 399, head size 256 with
+// 4-bit codes 38.6 for 36.6. (Inside the tiles' loop instead of around it: two n-tiles 428.)
+constexpr int kAttnRun = 32;
 
 // One dim's kernels, in a translation unit of their own.
 template <int D>
@@ -568,6 +579,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
   }
 
   uint8_t* const stages = smem + warp * S::kWarpBytes;
+  uint8_t* const sums = smem + kAttnWarps * S::kWarpBytes + warp * S::kSumBytes;  // fp32: this warp's
   const uint32_t stage0 = ptx::smem_addr(stages);
   // Where this lane's copies of a tile go and come from. Scales: the first
   // lanes take K's, the next ones V's.
@@ -770,271 +782,301 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
     auto from = [&](uint32_t base, int c) {
       return S::kPow2 ? (base + code_from) ^ (c * 16) : base + chunk_at<S::kChunks>(lrow, (c + lch) % S::kChunks);
     };
-    for (int i = 0; i < tiles; ++i) {
-      cp_wait<kStages - 2>();
-      __syncwarp();  // this tile has landed for every lane, and the one before has been read by every lane
-      issue(i + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
-      const uint32_t kb = stage0 + stage * S::kStage, vb = kb + S::kCodes + S::kScales;
-      const __half* ks = reinterpret_cast<const __half*>(stages + stage * S::kStage + S::kCodes);
-      const __half* vs = ks + (S::kCodes + S::kScales) / 2;
-      // ---- scores of keys g and g + 8
-      float s[NT][NS];
+    // fp32: the accumulators into this lane's sums, in fp32 additions, relative to the references of now.
+    auto to_sums = [&](bool first) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j) {
+        float* const ref = reinterpret_cast<float*>(sums + S::kSums) + j * 32 + lane;
+        const float f = first ? 0.0f : ex2(*ref - er[j][0]);
+        *ref = er[j][0];
 #pragma unroll
-        for (int x = 0; x < NS; ++x) s[j][x] = 0.0f;
-      {
-        float d0[NB], d1[NB];
-        load_scales<NB>(ks + g * NB, d0);
-        load_scales<NB>(ks + (g + 8) * NB, d1);
-        uint32_t w[4];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          uint32_t a0[4], a1[4];  // operands of the block's two 16-element halves
-          if (BITS == 8) {
-            ldm4(from(kb, 2 * b), w);
-            a0[0] = EX ? bytes02(w[0]) : raw02(w[0]);
-            a0[1] = EX ? bytes02(w[1]) : raw02(w[1]);
-            a0[2] = EX ? bytes13(w[0]) : raw13(w[0]);
-            a0[3] = EX ? bytes13(w[1]) : raw13(w[1]);
-            a1[0] = EX ? bytes02(w[2]) : raw02(w[2]);
-            a1[1] = EX ? bytes02(w[3]) : raw02(w[3]);
-            a1[2] = EX ? bytes13(w[2]) : raw13(w[2]);
-            a1[3] = EX ? bytes13(w[3]) : raw13(w[3]);
-          } else {
-            // one load holds two blocks (16 bytes each); an odd last one is paired with the first
-            if (b % 2 == 0) ldm4(from(kb, b), w);
-            const uint32_t x = w[2 * (b & 1)], y = w[2 * (b & 1) + 1], x8 = x >> 8, y8 = y >> 8;
-            a0[0] = EX ? nib_low(x) : raw_low(x);
-            a0[1] = EX ? nib_low(y) : raw_low(y);
-            a0[2] = EX ? nib_low(x8) : raw_low(x8);
-            a0[3] = EX ? nib_low(y8) : raw_low(y8);
-            a1[0] = EX ? nib_high(x) : raw_high(x);
-            a1[1] = EX ? nib_high(y) : raw_high(y);
-            a1[2] = EX ? nib_high(x8) : raw_high(x8);
-            a1[3] = EX ? nib_high(y8) : raw_high(y8);
+        for (int m = 0; m < D / 16; m += 2) {
+          float4* const sum = reinterpret_cast<float4*>(sums) + (j * (D / 32) + m / 2) * 32 + lane;
+          float4 y;
+          y.x = fmaf(o[j][m][1], 1.0f / kLoUp, o[j][m][0]);
+          y.y = fmaf(o[j][m][3], 1.0f / kLoUp, o[j][m][2]);
+          y.z = fmaf(o[j][m + 1][1], 1.0f / kLoUp, o[j][m + 1][0]);
+          y.w = fmaf(o[j][m + 1][3], 1.0f / kLoUp, o[j][m + 1][2]);
+          if (!first) {
+            const float4 x = *sum;
+            y = make_float4(fmaf(x.x, f, y.x), fmaf(x.y, f, y.y), fmaf(x.z, f, y.z), fmaf(x.w, f, y.w));
           }
+          *sum = y;
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            float c[4];
-            mma16_first(c, a0, qf[j][2 * b][0], qf[j][2 * b][1]);
-            mma16(c, a1, qf[j][2 * b + 1][0], qf[j][2 * b + 1][1]);
-            if (!EX) {  // the offset's share
-              s[j][0] = fmaf(d0[b], qs[j][b][0], s[j][0]);
-              s[j][NS / 2] = fmaf(d1[b], qs[j][b][0], s[j][NS / 2]);
-              if (NP == 1) {
-                s[j][1] = fmaf(d0[b], qs[j][b][NQ - 1], s[j][1]);
-                s[j][NS - 1] = fmaf(d1[b], qs[j][b][NQ - 1], s[j][NS - 1]);
-              }
-            }
-            if (NP == 2) {
-              s[j][0] = fmaf(d0[b], c[0] + c[1], s[j][0]);
-              s[j][1] = fmaf(d1[b], c[2] + c[3], s[j][1]);
-            } else {
-              s[j][0] = fmaf(d0[b], c[0], s[j][0]);
-              s[j][1] = fmaf(d0[b], c[1], s[j][1]);
-              s[j][NS - 2] = fmaf(d1[b], c[2], s[j][NS - 2]);
-              s[j][NS - 1] = fmaf(d1[b], c[3], s[j][NS - 1]);
-            }
-          }
+          for (int x = 0; x < 4; ++x) o[j][m][x] = o[j][m + 1][x] = 0.0f;
         }
       }
-      float v0[NB], v1[NB];
-      float m0 = load_scales<NB>(vs + g * NB, v0), m1 = load_scales<NB>(vs + (g + 8) * NB, v1);
-      // ---- scale, and mask where the tile holds keys that some row does not see
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int x = 0; x < NS; ++x) s[j][x] *= cs[j][NP == 2 ? 0 : (x & 1)];
-      if (static_cast<unsigned>(i - clean) >= clean_n) {
-        const bool gone = (bad >> stage) & 1;
-        bad &= ~(1u << stage);
-        const int ka = (tile0 + i * kAttnWarps) * 16 + g, kb8 = ka + 8;
+    };
+    const bool summed = EX && tiles > kAttnRun;
+    for (int i = 0, run = 0; run < tiles; run += kAttnRun) {
+      for (const int end = EX && tiles - run > kAttnRun ? run + kAttnRun : tiles; i < end; ++i) {
+        cp_wait<kStages - 2>();
+        __syncwarp();  // this tile has landed for every lane, and the one before has been read by every lane
+        issue(i + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+        const uint32_t kb = stage0 + stage * S::kStage, vb = kb + S::kCodes + S::kScales;
+        const __half* ks = reinterpret_cast<const __half*>(stages + stage * S::kStage + S::kCodes);
+        const __half* vs = ks + (S::kCodes + S::kScales) / 2;
+        // ---- scores of keys g and g + 8
+        float s[NT][NS];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int x = 0; x < NS; ++x) {
-            const int col = NP == 2 ? 0 : (x & 1), kk = x < NS / 2 ? ka : kb8;
-            if (gone || kk < lim0[j][col] || kk >= lim1[j][col]) s[j][x] = -INFINITY;
-          }
-        // what lies past the sequence may be anything: its scales must not reach a product
-        if (gone || ka >= n) {
-#pragma unroll
-          for (int b = 0; b < NB; ++b) v0[b] = 0.0f;
-          m0 = 0.0f;
-        }
-        if (gone || kb8 >= n) {
-#pragma unroll
-          for (int b = 0; b < NB; ++b) v1[b] = 0.0f;
-          m1 = 0.0f;
-        }
-      }
-      // ---- weights p = 2^(s - e). w: p times the key's largest V scale (no less than the least fp16 step). e moves if some
-      // w passes 2^15 or is not a number, as with a V scale that is not finite; the fp32 form also looks for weights below 2^-13.
-      constexpr float kLeast = 5.9604645e-8f;
-      m0 = max_nan(m0, kLeast);
-      m1 = max_nan(m1, kLeast);
-      float p[NT][NS];
-      bool odd = false;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int x = 0; x < NS; ++x) {
-          p[j][x] = ex2(s[j][x] - er[j][NP == 2 ? 0 : (x & 1)]);
-          const float w = p[j][x] * (x < NS / 2 ? m0 : m1);
-          odd |= !(w <= kWeightTop && (!EX || w >= kWeightLow));
-        }
-      const bool any_odd = __any_sync(0xffffffffu, odd);
-      if (any_odd) {
-        bool move = false;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-          for (int x = 0; x < NS; ++x) move |= !(p[j][x] * (x < NS / 2 ? m0 : m1) <= kWeightTop);
-        odd = __any_sync(0xffffffffu, move);
-      }
-      if (any_odd && odd) {
-        if (__any_sync(0xffffffffu, !(m0 <= 65504.0f) || !(m1 <= 65504.0f))) {
-          // V blocks that are not finite: their elements become NaN in the rows that see the key. The scale itself must not
-          // reach a product: a row that does not see it has the weight 0, and 0 times infinity is NaN.
-          m0 = m1 = kLeast;
-          unsigned spoilt = 0;  // blocks, by row
+          for (int x = 0; x < NS; ++x) s[j][x] = 0.0f;
+        {
+          float d0[NB], d1[NB];
+          load_scales<NB>(ks + g * NB, d0);
+          load_scales<NB>(ks + (g + 8) * NB, d1);
+          uint32_t w[4];
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            const bool b0 = !(fabsf(v0[b]) <= 65504.0f), b1 = !(fabsf(v1[b]) <= 65504.0f);
-            v0[b] = b0 ? 0.0f : v0[b];
-            v1[b] = b1 ? 0.0f : v1[b];
-            m0 = fmaxf(m0, fabsf(v0[b]));
-            m1 = fmaxf(m1, fabsf(v1[b]));
+            uint32_t a0[4], a1[4];  // operands of the block's two 16-element halves
+            if (BITS == 8) {
+              ldm4(from(kb, 2 * b), w);
+              a0[0] = EX ? bytes02(w[0]) : raw02(w[0]);
+              a0[1] = EX ? bytes02(w[1]) : raw02(w[1]);
+              a0[2] = EX ? bytes13(w[0]) : raw13(w[0]);
+              a0[3] = EX ? bytes13(w[1]) : raw13(w[1]);
+              a1[0] = EX ? bytes02(w[2]) : raw02(w[2]);
+              a1[1] = EX ? bytes02(w[3]) : raw02(w[3]);
+              a1[2] = EX ? bytes13(w[2]) : raw13(w[2]);
+              a1[3] = EX ? bytes13(w[3]) : raw13(w[3]);
+            } else {
+              // one load holds two blocks (16 bytes each); an odd last one is paired with the first
+              if (b % 2 == 0) ldm4(from(kb, b), w);
+              const uint32_t x = w[2 * (b & 1)], y = w[2 * (b & 1) + 1], x8 = x >> 8, y8 = y >> 8;
+              a0[0] = EX ? nib_low(x) : raw_low(x);
+              a0[1] = EX ? nib_low(y) : raw_low(y);
+              a0[2] = EX ? nib_low(x8) : raw_low(x8);
+              a0[3] = EX ? nib_low(y8) : raw_low(y8);
+              a1[0] = EX ? nib_high(x) : raw_high(x);
+              a1[1] = EX ? nib_high(y) : raw_high(y);
+              a1[2] = EX ? nib_high(x8) : raw_high(x8);
+              a1[3] = EX ? nib_high(y8) : raw_high(y8);
+            }
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-              for (int c = 0; c < NQ; ++c)
-                if ((b0 && s[j][c] != -INFINITY) || (b1 && s[j][NS / 2 + c] != -INFINITY)) spoilt |= 1u << ((b * NT + j) * NQ + c);
-          }
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) spoilt |= __shfl_xor_sync(0xffffffffu, spoilt, x);
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-              for (int c = 0; c < NQ; ++c)
-                if (spoilt >> ((b * NT + j) * NQ + c) & 1) {
-                  o[j][2 * b][c] = o[j][2 * b][2 + c] = __int_as_float(0x7FC00000);
-                  o[j][2 * b + 1][c] = o[j][2 * b + 1][2 + c] = __int_as_float(0x7FC00000);
+            for (int j = 0; j < NT; ++j) {
+              float c[4];
+              mma16_first(c, a0, qf[j][2 * b][0], qf[j][2 * b][1]);
+              mma16(c, a1, qf[j][2 * b + 1][0], qf[j][2 * b + 1][1]);
+              if (!EX) {  // the offset's share
+                s[j][0] = fmaf(d0[b], qs[j][b][0], s[j][0]);
+                s[j][NS / 2] = fmaf(d1[b], qs[j][b][0], s[j][NS / 2]);
+                if (NP == 1) {
+                  s[j][1] = fmaf(d0[b], qs[j][b][NQ - 1], s[j][1]);
+                  s[j][NS - 1] = fmaf(d1[b], qs[j][b][NQ - 1], s[j][NS - 1]);
                 }
+              }
+              if (NP == 2) {
+                s[j][0] = fmaf(d0[b], c[0] + c[1], s[j][0]);
+                s[j][1] = fmaf(d1[b], c[2] + c[3], s[j][1]);
+              } else {
+                s[j][0] = fmaf(d0[b], c[0], s[j][0]);
+                s[j][1] = fmaf(d0[b], c[1], s[j][1]);
+                s[j][NS - 2] = fmaf(d1[b], c[2], s[j][NS - 2]);
+                s[j][NS - 1] = fmaf(d1[b], c[3], s[j][NS - 1]);
+              }
+            }
+          }
         }
-        const float lg0 = __log2f(m0), lg1 = __log2f(m1);
+        float v0[NB], v1[NB];
+        float m0 = load_scales<NB>(vs + g * NB, v0), m1 = load_scales<NB>(vs + (g + 8) * NB, v1);
+        // ---- scale, and mask where the tile holds keys that some row does not see
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int c = 0; c < NQ; ++c) {
-            float top = fmaxf(s[j][c] + lg0, s[j][NS / 2 + c] + lg1) - 11.0f;
-            // scores of 2^27, where fp32's step is 16, can leave a weight of 2^24 so
-            const float z = fmaxf((s[j][c] - top) + lg0, (s[j][NS / 2 + c] - top) + lg1);
-            top = z > 15.0f ? top + z : top;
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            top = fmaxf(top, er[j][c]);
-            const float f = ex2(er[j][c] - top);
-            er[j][c] = top;
-            l[j][c] *= f;
-#pragma unroll
-            for (int m = 0; m < D / 16; ++m) {
-              if (NP == 2) {
-                o[j][m][0] *= f;
-                o[j][m][1] *= f;
-                o[j][m][2] *= f;
-                o[j][m][3] *= f;
-              } else {
-                o[j][m][c] *= f;
-                o[j][m][2 + c] *= f;
-              }
-            }
-            p[j][c] = ex2(s[j][c] - top);
-            p[j][NS / 2 + c] = ex2(s[j][NS / 2 + c] - top);
-          }
-      }
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int c = 0; c < NQ; ++c) l[j][c] += p[j][c] + p[j][NS / 2 + c];
-      // ---- outputs, block by block. fp32: weights below 2^-13 would lose bits in fp16 (they count only where the larger
-      // ones meet zero codes); they follow 2^24 larger, on accumulators scaled alike, at most three times: 2^-85.
-      for (int level = 0;; ++level) {
-        float rest[NT][NS];
-        bool more = false;
-        if (EX && any_odd) {
+          for (int x = 0; x < NS; ++x) s[j][x] *= cs[j][NP == 2 ? 0 : (x & 1)];
+        if (static_cast<unsigned>(i - clean) >= clean_n) {
+          const bool gone = (bad >> stage) & 1;
+          bad &= ~(1u << stage);
+          const int ka = (tile0 + i * kAttnWarps) * 16 + g, kb8 = ka + 8;
 #pragma unroll
           for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int x = 0; x < NS; ++x) {
-              const bool later = level < 3 && p[j][x] * (x < NS / 2 ? m0 : m1) < kWeightLow;
-              rest[j][x] = later ? p[j][x] * 16777216.0f : 0.0f;
-              p[j][x] = later ? 0.0f : p[j][x];
-              more |= rest[j][x] > 0.0f;
+              const int col = NP == 2 ? 0 : (x & 1), kk = x < NS / 2 ? ka : kb8;
+              if (gone || kk < lim0[j][col] || kk >= lim1[j][col]) s[j][x] = -INFINITY;
             }
-        }
-        uint32_t w[4];
+          // what lies past the sequence may be anything: its scales must not reach a product
+          if (gone || ka >= n) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          uint32_t a0[4], a1[4];
-          if (BITS == 8) {
-            ldm4t(from(vb, 2 * b), w);
-            a0[0] = bytes02(w[0]);
-            a0[1] = bytes13(w[0]);
-            a0[2] = bytes02(w[1]);
-            a0[3] = bytes13(w[1]);
-            a1[0] = bytes02(w[2]);
-            a1[1] = bytes13(w[2]);
-            a1[2] = bytes02(w[3]);
-            a1[3] = bytes13(w[3]);
-          } else {
-            if (b % 2 == 0) ldm4t(from(vb, b), w);
-            const uint32_t x = w[2 * (b & 1)], y = w[2 * (b & 1) + 1], x8 = x >> 8, y8 = y >> 8;
-            a0[0] = nib_low(x);
-            a0[1] = nib_low(x8);
-            a0[2] = nib_low(y);
-            a0[3] = nib_low(y8);
-            a1[0] = nib_high(x);
-            a1[1] = nib_high(x8);
-            a1[2] = nib_high(y);
-            a1[3] = nib_high(y8);
+            for (int b = 0; b < NB; ++b) v0[b] = 0.0f;
+            m0 = 0.0f;
           }
+          if (gone || kb8 >= n) {
 #pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            uint32_t b0, b1;
-            if (NP == 2) {
-              const ptx::f2 up = ptx::pk(kLoUp, kLoUp), down = ptx::pk(-kLoUp, -kLoUp);
-              const ptx::f2 x = ptx::mul2(ptx::pk(p[j][0], p[j][1]), ptx::pk(v0[b], v1[b]));
-              const uint32_t hi = half2_of(ptx::lo32(x), ptx::hi32(x));
-              const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-              const ptx::f2 r = ptx::fma2(ptx::pk(h.x, h.y), down, ptx::mul2(x, up));  // (w - hi) * 2^11, exact
-              const uint32_t lo = half2_of(ptx::lo32(r), ptx::hi32(r));
-              b0 = transpose8(prmt(hi, lo, 0x5410u));
-              b1 = transpose8(prmt(hi, lo, 0x7632u));
-            } else {
-              b0 = transpose8(half2_of(p[j][0] * v0[b], p[j][1] * v0[b]));
-              b1 = transpose8(half2_of(p[j][NS - 2] * v1[b], p[j][NS - 1] * v1[b]));
-            }
-            mma16(o[j][2 * b], a0, b0, b1);
-            mma16(o[j][2 * b + 1], a1, b0, b1);
+            for (int b = 0; b < NB; ++b) v1[b] = 0.0f;
+            m1 = 0.0f;
           }
         }
-        if (!EX || !any_odd) break;
-        if (!__any_sync(0xffffffffu, more)) {
-          if (level > 0) scale_all(o, level == 1 ? 5.9604645e-8f : level == 2 ? 3.5527137e-15f : 2.1175824e-22f);
-          break;
-        }
-        scale_all(o, 16777216.0f);
+        // ---- weights p = 2^(s - e). w: p times the key's largest V scale (no less than the least fp16 step). e moves if some
+        // w passes 2^15 or is not a number, as with a V scale that is not finite; the fp32 form also looks for weights below 2^-13.
+        constexpr float kLeast = 5.9604645e-8f;
+        m0 = max_nan(m0, kLeast);
+        m1 = max_nan(m1, kLeast);
+        float p[NT][NS];
+        bool odd = false;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int x = 0; x < NS; ++x) p[j][x] = rest[j][x];
+          for (int x = 0; x < NS; ++x) {
+            p[j][x] = ex2(s[j][x] - er[j][NP == 2 ? 0 : (x & 1)]);
+            const float w = p[j][x] * (x < NS / 2 ? m0 : m1);
+            odd |= !(w <= kWeightTop && (!EX || w >= kWeightLow));
+          }
+        const bool any_odd = __any_sync(0xffffffffu, odd);
+        if (any_odd) {
+          bool move = false;
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int x = 0; x < NS; ++x) move |= !(p[j][x] * (x < NS / 2 ? m0 : m1) <= kWeightTop);
+          odd = __any_sync(0xffffffffu, move);
+        }
+        if (any_odd && odd) {
+          if (__any_sync(0xffffffffu, !(m0 <= 65504.0f) || !(m1 <= 65504.0f))) {
+            // V blocks that are not finite: their elements become NaN in the rows that see the key. The scale itself must not
+            // reach a product: a row that does not see it has the weight 0, and 0 times infinity is NaN.
+            m0 = m1 = kLeast;
+            unsigned spoilt = 0;  // blocks, by row
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              const bool b0 = !(fabsf(v0[b]) <= 65504.0f), b1 = !(fabsf(v1[b]) <= 65504.0f);
+              v0[b] = b0 ? 0.0f : v0[b];
+              v1[b] = b1 ? 0.0f : v1[b];
+              m0 = fmaxf(m0, fabsf(v0[b]));
+              m1 = fmaxf(m1, fabsf(v1[b]));
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int c = 0; c < NQ; ++c)
+                  if ((b0 && s[j][c] != -INFINITY) || (b1 && s[j][NS / 2 + c] != -INFINITY)) spoilt |= 1u << ((b * NT + j) * NQ + c);
+            }
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) spoilt |= __shfl_xor_sync(0xffffffffu, spoilt, x);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int c = 0; c < NQ; ++c)
+                  if (spoilt >> ((b * NT + j) * NQ + c) & 1) {
+                    o[j][2 * b][c] = o[j][2 * b][2 + c] = __int_as_float(0x7FC00000);
+                    o[j][2 * b + 1][c] = o[j][2 * b + 1][2 + c] = __int_as_float(0x7FC00000);
+                  }
+          }
+          const float lg0 = __log2f(m0), lg1 = __log2f(m1);
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int c = 0; c < NQ; ++c) {
+              float top = fmaxf(s[j][c] + lg0, s[j][NS / 2 + c] + lg1) - 11.0f;
+              // scores of 2^27, where fp32's step is 16, can leave a weight of 2^24 so
+              const float z = fmaxf((s[j][c] - top) + lg0, (s[j][NS / 2 + c] - top) + lg1);
+              top = z > 15.0f ? top + z : top;
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+              top = fmaxf(top, er[j][c]);
+              const float f = ex2(er[j][c] - top);
+              er[j][c] = top;
+              l[j][c] *= f;
+#pragma unroll
+              for (int m = 0; m < D / 16; ++m) {
+                if (NP == 2) {
+                  o[j][m][0] *= f;
+                  o[j][m][1] *= f;
+                  o[j][m][2] *= f;
+                  o[j][m][3] *= f;
+                } else {
+                  o[j][m][c] *= f;
+                  o[j][m][2 + c] *= f;
+                }
+              }
+              p[j][c] = ex2(s[j][c] - top);
+              p[j][NS / 2 + c] = ex2(s[j][NS / 2 + c] - top);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int c = 0; c < NQ; ++c) l[j][c] += p[j][c] + p[j][NS / 2 + c];
+        // ---- outputs, block by block. fp32: weights below 2^-13 would lose bits in fp16 (they count only where the larger
+        // ones meet zero codes); they follow 2^24 larger, on accumulators scaled alike, at most three times: 2^-85.
+        for (int level = 0;; ++level) {
+          float rest[NT][NS];
+          bool more = false;
+          if (EX && any_odd) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int x = 0; x < NS; ++x) {
+                const bool later = level < 3 && p[j][x] * (x < NS / 2 ? m0 : m1) < kWeightLow;
+                rest[j][x] = later ? p[j][x] * 16777216.0f : 0.0f;
+                p[j][x] = later ? 0.0f : p[j][x];
+                more |= rest[j][x] > 0.0f;
+              }
+          }
+          uint32_t w[4];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            uint32_t a0[4], a1[4];
+            if (BITS == 8) {
+              ldm4t(from(vb, 2 * b), w);
+              a0[0] = bytes02(w[0]);
+              a0[1] = bytes13(w[0]);
+              a0[2] = bytes02(w[1]);
+              a0[3] = bytes13(w[1]);
+              a1[0] = bytes02(w[2]);
+              a1[1] = bytes13(w[2]);
+              a1[2] = bytes02(w[3]);
+              a1[3] = bytes13(w[3]);
+            } else {
+              if (b % 2 == 0) ldm4t(from(vb, b), w);
+              const uint32_t x = w[2 * (b & 1)], y = w[2 * (b & 1) + 1], x8 = x >> 8, y8 = y >> 8;
+              a0[0] = nib_low(x);
+              a0[1] = nib_low(x8);
+              a0[2] = nib_low(y);
+              a0[3] = nib_low(y8);
+              a1[0] = nib_high(x);
+              a1[1] = nib_high(x8);
+              a1[2] = nib_high(y);
+              a1[3] = nib_high(y8);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              uint32_t b0, b1;
+              if (NP == 2) {
+                const ptx::f2 up = ptx::pk(kLoUp, kLoUp), down = ptx::pk(-kLoUp, -kLoUp);
+                const ptx::f2 x = ptx::mul2(ptx::pk(p[j][0], p[j][1]), ptx::pk(v0[b], v1[b]));
+                const uint32_t hi = half2_of(ptx::lo32(x), ptx::hi32(x));
+                const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                const ptx::f2 r = ptx::fma2(ptx::pk(h.x, h.y), down, ptx::mul2(x, up));  // (w - hi) * 2^11, exact
+                const uint32_t lo = half2_of(ptx::lo32(r), ptx::hi32(r));
+                b0 = transpose8(prmt(hi, lo, 0x5410u));
+                b1 = transpose8(prmt(hi, lo, 0x7632u));
+              } else {
+                b0 = transpose8(half2_of(p[j][0] * v0[b], p[j][1] * v0[b]));
+                b1 = transpose8(half2_of(p[j][NS - 2] * v1[b], p[j][NS - 1] * v1[b]));
+              }
+              mma16(o[j][2 * b], a0, b0, b1);
+              mma16(o[j][2 * b + 1], a1, b0, b1);
+            }
+          }
+          if (!EX || !any_odd) break;
+          if (!__any_sync(0xffffffffu, more)) {
+            if (level > 0) scale_all(o, level == 1 ? 5.9604645e-8f : level == 2 ? 3.5527137e-15f : 2.1175824e-22f);
+            break;
+          }
+          scale_all(o, 16777216.0f);
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int x = 0; x < NS; ++x) p[j][x] = rest[j][x];
+        }
+        stage = stage + 1 == kStages ? 0 : stage + 1;
       }
-      stage = stage + 1 == kStages ? 0 : stage + 1;
+      if (!EX) break;
+      if (summed) to_sums(run == 0);
     }
     // ---- merge the four warps in shared memory. Each puts its results where its last tile was; the next part's tiles go
     // elsewhere until the barrier after the merge.
@@ -1057,9 +1099,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps, SplitShape<BITS, D, EX, NP, N
         }
 #pragma unroll
         for (int m = 0; m < D / 16; ++m) {
-          const float2 y = NP == 2 ? make_float2(fmaf(o[j][m][1], 1.0f / kLoUp, o[j][m][0]),
+          float2 y = NP == 2 ? make_float2(fmaf(o[j][m][1], 1.0f / kLoUp, o[j][m][0]),
                                                  fmaf(o[j][m][3], 1.0f / kLoUp, o[j][m][2]))
                                    : make_float2(o[j][m][c], o[j][m][2 + c]);
+          if (summed) y = reinterpret_cast<const float2*>(sums)[((j * (D / 32) + m / 2) * 32 + lane) * 2 + m % 2];
           *reinterpret_cast<float2*>(mine_o + r * D + 16 * m + 2 * g) = y;
         }
       }
