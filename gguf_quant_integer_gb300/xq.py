@@ -506,6 +506,11 @@ class KVCache:
     def read(self, slots, dtype=None, k=None, v=None, stream=None):
         """The rows of slots int64 [tokens] as floats: (k, v), each
         [tokens, heads, dim] of dtype (float32)."""
+        if stream is not None and (k is None or v is None):
+            on = self._on(stream)
+            if on:
+                with on:
+                    return self.read(slots, dtype, k, v)
         if slots.dtype != self._int64 or slots.dim() != 1 or not slots.is_contiguous():
             raise ValueError("slots: contiguous int64 [tokens]")
         n, dev = slots.shape[0], self.device
@@ -516,11 +521,11 @@ class KVCache:
             dtype = self._torch.float32 if k is None else k.dtype
         kind = _float_type(dtype)
         if k is None:
-            k = self._new(shape, dtype, stream)
+            k = self._empty(shape, dtype=dtype, device=dev)
         elif k.shape != shape or k.dtype != dtype or not k.is_contiguous() or k.device != dev:
             raise ValueError(f"k: contiguous {shape} of {dtype} on {dev}")
         if v is None:
-            v = self._new(shape, dtype, stream)
+            v = self._empty(shape, dtype=dtype, device=dev)
         elif v.shape != shape or v.dtype != dtype or not v.is_contiguous() or v.device != dev:
             raise ValueError(f"v: contiguous {shape} of {dtype} on {dev}")
         rc = self._read(self._ref, slots.data_ptr(), n, kind, k.data_ptr(), v.data_ptr(), self._stream(stream))
@@ -537,31 +542,24 @@ class KVCache:
         return nb
 
     def _on(self, stream):
-        """The call's stream as the current one (a context manager)."""
+        """Context that makes `stream` the current one, for a call that makes memory: the allocator hands a stream's freed
+        memory to the same stream without waiting, so it has to be the stream that writes it. None if it is the current one."""
+        handle = self._stream(stream)
+        if handle == self._stream(None):
+            return None
         cuda = self._torch.cuda
-        return cuda.stream(cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream)
+        return cuda.stream(cuda.ExternalStream(handle, device=self.device) if isinstance(stream, int) else stream)
 
-    def _new(self, shape, dtype, stream):
-        """Memory for a result. The allocator hands a stream's freed memory to the same stream without waiting, so it has to
-        be the stream that writes the result: another's may still be in use there."""
-        if stream is None:
-            return self._empty(shape, dtype=dtype, device=self.device)
-        with self._on(stream):
-            return self._empty(shape, dtype=dtype, device=self.device)
-
-    def _workspace(self, key, handle, stream):
+    def _workspace(self, key, handle):
         """(tensor, bytes, address) of a workspace of at least what calls of these sizes (the arguments of
-        attn_workspace_bytes) need: the stream's own, kept from call to call and replaced by a larger one, or, while the
-        stream is captured, a new one. A graph keeps the address it was captured with: its memory must be the graph's (it
+        attn_workspace_bytes) need on the current stream: its own, kept from call to call and replaced by a larger one, or,
+        while the stream is captured, a new one. A graph keeps the address it was captured with: its memory must be the graph's (it
         stays the graph's when the tensor is dropped), and not the next graph's too."""
         need = self._need.get(key)
         if need is None:
             if len(self._need) >= 1024:  # a prefix that grows gives new sizes without end
                 self._need.clear()
             need = self._need[key] = self.attn_workspace_bytes(*key)
-        if stream is not None:
-            with self._on(stream):
-                return self._workspace(key, handle, None)
         capturing = self._capturing()
         ws = None if capturing else self._ws.get(handle)
         if ws is None or ws[1] < need:
@@ -572,6 +570,11 @@ class KVCache:
         return ws
 
     def _attn(self, fn, q, pages, lens, scale, window, prefix_pages, prefix_len, out, workspace, stream):
+        if stream is not None and (out is None or workspace is None):
+            on = self._on(stream)
+            if on:
+                with on:
+                    return self._attn(fn, q, pages, lens, scale, window, prefix_pages, prefix_len, out, workspace, None)
         dev, int32, shape = self.device, self._int32, q.shape
         if len(shape) != 4 or shape[3] != self.dim or not q.is_contiguous():
             raise ValueError(f"q: contiguous [batch, n_q, heads, {self.dim}]")
@@ -584,7 +587,7 @@ class KVCache:
         if q.device != dev or pages.device != dev or lens.device != dev:
             raise ValueError(f"q, pages and lens have to be on {dev}")
         if out is None:
-            out = self._new(shape, q.dtype, stream)
+            out = self._empty(shape, dtype=q.dtype, device=dev)
         elif out.shape != shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != dev:
             raise ValueError("out: a contiguous tensor like q")
         prefix = None
@@ -595,7 +598,7 @@ class KVCache:
             prefix = prefix_pages.data_ptr()
         s, width, dtype = self._stream(stream), pshape[1], q.dtype
         if workspace is None:
-            held, ws_bytes, ws = self._workspace((dtype, batch, n_q, heads, width, prefix_len), s, stream)
+            held, ws_bytes, ws = self._workspace((dtype, batch, n_q, heads, width, prefix_len), s)
         else:
             ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
             if workspace.device != dev or not workspace.is_contiguous():

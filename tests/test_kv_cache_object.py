@@ -31,7 +31,7 @@ def test_remembered_sizes_are_bounded(cache):
     q, lens = torch.float32, 1
     for prefix in range(1, 5000):
         key = (q, 2, 1, 4, lens, prefix)
-        held = cache._workspace(key, 0, None)
+        held = cache._workspace(key, 0)
         assert held[1] >= cache.attn_workspace_bytes(*key)
     assert len(cache._need) <= 1024 and len(cache._ws) == 1
 
