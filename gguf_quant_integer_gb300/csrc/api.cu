@@ -3,6 +3,7 @@
 #include <cstdint>
 
 #include "kv_common.cuh"
+#include "ops_common.cuh"
 #include "xq.h"
 #include "xq_common.cuh"
 
@@ -787,18 +788,28 @@ xq_status xq_device_error(xq_stream stream, unsigned int* code_out) {
   for (int k = 0; k < 3 && *code_out == 0; ++k)
     if (kv[k]) *code_out = (3u << 8) | (kv[k] & 0xFFu);
   if (kv_wait && *code_out == 0) *code_out = (4u << 8) | (kv_wait & 0xFFu);
+  unsigned int ops[2] = {0u, 0u}, prompt_wait = 0u;
+  const cudaError_t o0 = xq::take_lora_error(&ops[0]);
+  const cudaError_t o1 = xq::take_prompt_error(&ops[1], &prompt_wait);
+  if (o0 != cudaSuccess || o1 != cudaSuccess) return XQ_ERR_CUDA;
+  for (int k = 0; k < 2 && *code_out == 0; ++k)
+    if (ops[k]) *code_out = (5u << 8) | (ops[k] & 0xFFu);
+  if (prompt_wait && *code_out == 0) *code_out = (6u << 8) | (prompt_wait & 0xFFu);
   // checked builds: the first failed bounds check of each kernel file
-  unsigned int chk[6] = {0u, 0u, 0u, 0u, 0u, 0u};
+  unsigned int chk[9] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
   const cudaError_t c0 = xq::take_gemv_check(&chk[0]);
   const cudaError_t c1 = xq::take_tile_check(&chk[1]);
   const cudaError_t c2 = xq::take_quant_check(&chk[2]);
   const cudaError_t c3 = xq::take_q6k_check(&chk[3]);
   const cudaError_t c4 = xq::take_kv_cache_check(&chk[4]);
   const cudaError_t c5 = xq::take_kv_attn_check(&chk[5]);
+  const cudaError_t c6 = xq::take_lora_check(&chk[6]);
+  const cudaError_t c7 = xq::take_rope_check(&chk[7]);
+  const cudaError_t c8 = xq::take_prompt_check(&chk[8]);
   if (c0 != cudaSuccess || c1 != cudaSuccess || c2 != cudaSuccess || c3 != cudaSuccess || c4 != cudaSuccess ||
-      c5 != cudaSuccess)
+      c5 != cudaSuccess || c6 != cudaSuccess || c7 != cudaSuccess || c8 != cudaSuccess)
     return XQ_ERR_CUDA;
-  for (int k = 0; k < 6 && *code_out == 0; ++k)
+  for (int k = 0; k < 9 && *code_out == 0; ++k)
     if (chk[k]) *code_out = (9u << 8) | (chk[k] & 0xFFu);
   return XQ_OK;
 }

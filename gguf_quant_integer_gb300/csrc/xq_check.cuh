@@ -82,6 +82,8 @@ enum CheckSite : unsigned {
   kChkKvQuery = 53,  // row of q, of the result or of the stored first pass inside [tokens][heads]
   kChkKvPart = 54,   // partial result or record inside the workspace
   kChkKvLens = 55,   // sequence inside the batch
+  // qk_rope.cu
+  kChkRope = 60,     // 8 elements inside a row of a token of the call
 };
 
 }  // namespace xq

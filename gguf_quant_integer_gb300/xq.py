@@ -37,7 +37,7 @@ SYMBOLS = ("xq_status_str", "xq_q8_bytes", "xq_weight_bytes", "xq_quantize_q8",
            "xq_debug_isums_iq4xs", "xq_device_error", "xq_debug_stalled_matmul_q4k", "xq_debug_tile_sums",
            "xq_debug_layer_matmuls", "xq_debug_check_probe", "xq_debug_stalled_ffn_layer",
            "xq_kv_bytes", "xq_kv_write", "xq_kv_read", "xq_kv_attn_workspace_bytes", "xq_kv_attn",
-           "xq_kv_attn_shared")
+           "xq_kv_attn_shared", "xq_lora_add", "xq_qk_norm_rope", "xq_prompt_attn_workspace_bytes", "xq_prompt_attn")
 
 
 class XQError(RuntimeError):
@@ -63,6 +63,30 @@ class xq_kv_query(ctypes.Structure):
                 ("page_stride", ctypes.c_int), ("max_pages", ctypes.c_int), ("lens", ctypes.c_void_p),
                 ("scale", ctypes.c_float), ("window", ctypes.c_int), ("prefix_pages", ctypes.c_void_p),
                 ("prefix_len", ctypes.c_int)]
+
+
+class xq_adapters(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("n", ctypes.c_int), ("rank", ctypes.c_int), ("K", ctypes.c_int), ("N", ctypes.c_int),
+                ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("input", ctypes.c_int)]
+
+
+class xq_qk_rows(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("y_type", ctypes.c_int), ("tokens", ctypes.c_int), ("heads", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("dim", ctypes.c_int), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong), ("q_out", ctypes.c_void_p),
+                ("k_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_longlong), ("k_out_stride", ctypes.c_longlong),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("positions", ctypes.c_void_p), ("turns", ctypes.c_void_p), ("rot", ctypes.c_int), ("pairs", ctypes.c_int),
+                ("magnitude", ctypes.c_float)]
+
+
+class xq_prompts(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int), ("tokens", ctypes.c_int), ("batch", ctypes.c_int), ("heads", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("dim", ctypes.c_int), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong),
+                ("v_stride", ctypes.c_longlong), ("out", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("scale", ctypes.c_float),
+                ("window", ctypes.c_int)]
 
 
 _lib = None
@@ -131,6 +155,13 @@ def lib(path: str | None = None):
     for fn in ("xq_kv_attn", "xq_kv_attn_shared"):
         getattr(L, fn).argtypes = [C, Q, P, S, P]
     for fn in ("xq_kv_write", "xq_kv_read", "xq_kv_attn", "xq_kv_attn_shared"):
+        getattr(L, fn).restype = I
+    L.xq_lora_add.argtypes = [ctypes.POINTER(xq_adapters), I, ctypes.POINTER(P), I, I, P, P]
+    L.xq_qk_norm_rope.argtypes = [ctypes.POINTER(xq_qk_rows), P]
+    L.xq_prompt_attn_workspace_bytes.argtypes = [ctypes.POINTER(xq_prompts)]
+    L.xq_prompt_attn_workspace_bytes.restype = S
+    L.xq_prompt_attn.argtypes = [ctypes.POINTER(xq_prompts), P, S, P]
+    for fn in ("xq_lora_add", "xq_qk_norm_rope", "xq_prompt_attn"):
         getattr(L, fn).restype = I
     for fn in ("xq_quantize_q8", "xq_matmul_q4k_q8", "xq_matmul_q6k_q8", "xq_debug_isums_q4k",
                "xq_debug_isums_q6k", "xq_layer_mixed", "xq_layer_mixed_static", "xq_matmul_q8_0_q8",
@@ -393,9 +424,11 @@ class Layer:
 
     Weights are uploaded once (the raw GGUF bytes stay resident; nothing is
     dequantized) and `forward` runs xq_layer_mixed on the current stream.
+    adapters: {index of a projection: (a, b, scales)} of its low-rank adapters
+    (see Adapters); forward's ids then name each row's.
     """
 
-    def __init__(self, projs, weights, M: int, device="cuda", codebooks=None):
+    def __init__(self, projs, weights, M: int, device="cuda", codebooks=None, adapters=None):
         import torch
         self.projs = projs
         self.M = M
@@ -407,9 +440,22 @@ class Layer:
         self.desc = [(p.qtype, p.N, p.K, self.W[i], self.y[i], p.input, cbs[i]) for i, p in enumerate(projs)]
         nb = layer_workspace_bytes(self.desc, n_in, M)
         self.workspace = torch.empty(max(nb, 256), dtype=torch.uint8, device=device)
+        self.adapters = None
+        if adapters:
+            at = sorted(adapters)
+            for i in at:
+                if adapters[i][0].shape[2:] != (projs[i].K,) or adapters[i][1].shape[1:2] != (projs[i].N,):
+                    raise ValueError(f"adapters of projection {i}: K = {projs[i].K} and N = {projs[i].N} expected")
+            self.adapters = Adapters([(*adapters[i], projs[i].input) for i in at])
+            self.adapted = [self.y[i] for i in at]
 
-    def forward(self, inputs, stream=None):
+    def forward(self, inputs, stream=None, ids=None):
+        """The projections' outputs; with ids int32 [M], each row's adapter (negative: none) added to them."""
+        if ids is not None and self.adapters is None:
+            raise ValueError("the layer has no adapters")
         layer_mixed(self.desc, inputs, self.M, self.workspace, stream)
+        if ids is not None:
+            self.adapters.add(inputs, self.adapted, ids, stream)
         return self.y
 
     def weight_bytes(self) -> int:
@@ -627,3 +673,213 @@ class KVCache:
         prefix_pages int32 [pages]; pages and lens are of the tokens after it."""
         return self._attn(self._lib.xq_kv_attn_shared, q, pages, lens, scale, 0, prefix_pages, prefix_len, out, workspace,
                           stream)
+
+
+_torch_calls = None
+
+
+def _calls():
+    """(device, stream handle, capturing) accessors of torch: the bare handle's costs a fortieth of building a Stream object."""
+    global _torch_calls
+    if _torch_calls is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _torch_calls = (torch, getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                        raw or (lambda d: torch.cuda.current_stream(d).cuda_stream))
+    return _torch_calls
+
+
+def _handle(device, stream):
+    """The stream's handle. Kernels go to the current device, whatever device the pointers are of."""
+    _, current, raw = _calls()
+    if device.type != "cuda" or current() != device.index:
+        raise ValueError(f"the tensors are on {device}: CUDA tensors on the current device expected (torch.cuda.device)")
+    if stream is None:
+        return raw(device.index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _other_stream(device, stream):
+    """Context that makes `stream` the current one, for a call that makes memory: the allocator hands a stream's freed memory
+    to the same stream without waiting, so it has to be the stream that writes it. None if it is the current one."""
+    if stream is None:
+        return None
+    handle = _handle(device, stream)
+    if handle == _handle(device, None):
+        return None
+    cuda = _calls()[0].cuda
+    return cuda.stream(cuda.ExternalStream(handle, device=device) if isinstance(stream, int) else stream)
+
+
+class Adapters:
+    """Low-rank adapters of projections that run together.
+
+    projs: (a, b, scales, input) of each projection: a [n, rank, K] and b
+    [n, N, rank] of one dtype (float32, float16 or bfloat16), scales fp32 [n]
+    or None, and which of `add`'s inputs it takes. The tensors are kept.
+    """
+
+    def __init__(self, projs):
+        torch = _calls()[0]
+        if not 1 <= len(projs) <= 16:
+            raise ValueError("1 to 16 projections a call")
+        self.device = projs[0][0].device
+        self._keep, self._shapes = [], []
+        arr = (xq_adapters * len(projs))()
+        for e, (a, b, scales, inp) in zip(arr, projs):
+            if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2] or a.dtype != b.dtype:
+                raise ValueError("a: [n, rank, K], b: [n, N, rank], of one dtype")
+            if not a.is_contiguous() or not b.is_contiguous() or a.device != self.device or b.device != self.device:
+                raise ValueError(f"a and b have to be contiguous, on {self.device}")
+            n, rank, K = a.shape
+            if scales is not None and (scales.dtype != torch.float32 or scales.shape != (n,) or not scales.is_contiguous()
+                                       or scales.device != self.device):
+                raise ValueError(f"scales: contiguous float32 [{n}], on {self.device}")
+            if rank % 8 or not 8 <= rank <= 256 or K % 32 or K == 0:
+                raise ValueError(f"rank a multiple of 8 up to 256 and K a multiple of 32 expected, got {rank} and {K}")
+            if inp < 0:
+                raise ValueError("an input's index is not negative")
+            e.type, e.n, e.rank, e.K, e.N, e.input = _float_type(a.dtype), n, rank, K, b.shape[1], inp
+            e.a, e.b, e.scales = a.data_ptr(), b.data_ptr(), None if scales is None else scales.data_ptr()
+            self._keep.append((a, b, scales))
+            self._shapes.append((K, b.shape[1], inp))
+        self._type, self._fixed = type(arr), bytes(arr)
+        self._add = lib().xq_lora_add
+        self._float32, self._int32 = torch.float32, torch.int32
+
+    def add(self, inputs, ys, ids, stream=None):
+        """Add to each row of the projections' outputs ys (fp32 [M, N] each) what the adapter that ids int32 [M] names gives
+        for the row of its input (fp32 [M, K]); rows of a negative id are left as they are. Returns ys."""
+        dev, M = self.device, ids.shape[0]
+        if ids.dtype != self._int32 or ids.dim() != 1 or not ids.is_contiguous() or ids.device != dev:
+            raise ValueError(f"ids: contiguous int32 [M], on {dev}")
+        if len(ys) != len(self._shapes):
+            raise ValueError(f"{len(self._shapes)} outputs expected, got {len(ys)}")
+        arr = self._type.from_buffer_copy(self._fixed)  # a call's own: calls may run side by side
+        ins = (ctypes.c_void_p * max(1, len(inputs)))()
+        for e, y, (K, N, inp) in zip(arr, ys, self._shapes):
+            if inp >= len(inputs):
+                raise ValueError(f"input {inp} is missing")
+            x = inputs[inp]
+            if x.shape != (M, K) or x.dtype != self._float32 or not x.is_contiguous() or x.device != dev:
+                raise ValueError(f"input {inp}: contiguous float32 [{M}, {K}], on {dev}")
+            if y.shape != (M, N) or y.dtype != self._float32 or not y.is_contiguous() or y.device != dev:
+                raise ValueError(f"an output: contiguous float32 [{M}, {N}], on {dev}")
+            e.y, ins[inp] = y.data_ptr(), x.data_ptr()
+        rc = self._add(arr, len(ys), ins, len(inputs), M, ids.data_ptr(), _handle(dev, stream))
+        if rc:
+            raise XQError("xq_lora_add", rc)
+        return ys
+
+
+class Rope:
+    """Position rotation: the first `rot` elements of a head turn in rot / 2 pairs, pair i by base^(-2i / rot) radians a
+    position, divided by factors[i] if given. pairs: neighbouring elements (2i, 2i + 1) make a pair, otherwise (i, i + rot / 2).
+    magnitude: factor of the rotated elements."""
+
+    def __init__(self, rot: int, base: float = 10000.0, factors=None, pairs: bool = False, magnitude: float = 1.0, device="cuda"):
+        import numpy as np
+        torch = _calls()[0]
+        if rot < 0 or rot % 16:
+            raise ValueError("rot: a multiple of 16")
+        freq = float(base) ** (np.arange(0, rot, 2, dtype=np.float64) / -max(rot, 1))
+        if factors is not None:
+            factors = np.asarray(factors.cpu() if hasattr(factors, "cpu") else factors, dtype=np.float64)
+            if factors.shape != freq.shape:
+                raise ValueError(f"{rot // 2} factors expected")
+            freq = freq / factors
+        turns = freq / (2 * np.pi)
+        if not np.isfinite(turns).all():
+            raise ValueError("base and factors have to give finite frequencies")
+        turns = np.rint((turns - np.floor(turns)) * 2.0 ** 64)  # whole turns a position change nothing
+        self.rot, self.pairs, self.magnitude = rot, bool(pairs), float(magnitude)
+        self.turns = torch.tensor([(int(t) + (1 << 63)) % (1 << 64) - (1 << 63) for t in turns], dtype=torch.int64, device=device)
+        self._ptr = self.turns.data_ptr()
+
+
+def qk_norm_rope(q, k, positions, rope, q_weight=None, k_weight=None, eps: float = 1e-6, dtype=None, q_out=None, k_out=None,
+                 stream=None):
+    """Each head's row of q [tokens, heads, dim] and k [tokens, kv_heads, dim] normalized (x * weight / sqrt(mean(x^2) + eps);
+    not without a weight) and rotated to its position (int64 [tokens]). A token's rows are contiguous; tokens may be parts of
+    longer rows. Returns (q_out, k_out) of `dtype` (the inputs'); an output may be its input."""
+    if stream is not None and (q_out is None or k_out is None):
+        on = _other_stream(q.device, stream)
+        if on:
+            with on:
+                return qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, dtype, q_out, k_out)
+    torch, dev = _calls()[0], q.device
+    (T, H, D), ks = q.shape, k.shape
+    if len(ks) != 3 or ks[0] != T or ks[2] != D or k.dtype != q.dtype or k.device != dev:
+        raise ValueError("q: [tokens, heads, dim], k: [tokens, kv_heads, dim], of one dtype and device")
+    if positions.dtype != torch.int64 or positions.shape != (T,) or not positions.is_contiguous() or positions.device != dev:
+        raise ValueError(f"positions: contiguous int64 [{T}], on {dev}")
+    if dtype is None:
+        dtype = q.dtype if q_out is None else q_out.dtype
+    if q_out is None:
+        q_out = torch.empty((T, H, D), dtype=dtype, device=dev)
+    if k_out is None:
+        k_out = torch.empty(ks, dtype=dtype, device=dev)
+    row = (D, 1)
+    for x, shape, kind in ((q, q.shape, q.dtype), (k, ks, q.dtype), (q_out, q.shape, dtype), (k_out, ks, dtype)):
+        st = x.stride()
+        if x.shape != shape or x.dtype != kind or x.device != dev or (st[1:] != row and (shape[1] > 1 or st[2] != 1)):
+            raise ValueError(f"{tuple(shape)} of {kind} on {dev} expected, each token's rows contiguous")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != torch.float32 or w.shape != (D,) or not w.is_contiguous() or w.device != dev):
+            raise ValueError(f"weights: contiguous float32 [{D}], on {dev}")
+    if rope.turns.device != dev:
+        raise ValueError(f"the rotation's table has to be on {dev}")
+    rows = xq_qk_rows(_float_type(q.dtype), _float_type(dtype), T, H, ks[1], D, q.data_ptr(), k.data_ptr(), q.stride(0), k.stride(0),
+                      q_out.data_ptr(), k_out.data_ptr(), q_out.stride(0), k_out.stride(0),
+                      None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps,
+                      positions.data_ptr(), rope._ptr, rope.rot, rope.pairs, rope.magnitude)
+    rc = lib().xq_qk_norm_rope(rows, _handle(dev, stream))
+    if rc:
+        raise XQError("xq_qk_norm_rope", rc)
+    return q_out, k_out
+
+
+def prompt_attn(q, k, v, starts, scale=None, window: int = 0, out=None, workspace=None, stream=None):
+    """Causal attention of packed prompts: q [tokens, heads, dim], k and v [tokens, kv_heads, dim]; sequence b is rows
+    starts[b] .. starts[b + 1] - 1 (starts int32 [batch + 1]). A token's rows are contiguous; tokens may be parts of longer
+    rows. scale: 1 / sqrt(dim). window: how many keys a query sees at most, 0 for all. Returns out [tokens, heads, dim]; its
+    rows that belong to no sequence are not written."""
+    if stream is not None and (out is None or workspace is None):
+        on = _other_stream(q.device, stream)
+        if on:
+            with on:
+                return prompt_attn(q, k, v, starts, scale, window, out, workspace)
+    torch, dev, dtype = _calls()[0], q.device, q.dtype
+    (T, H, D), ks = q.shape, k.shape
+    if len(ks) != 3 or ks[0] != T or ks[2] != D or v.shape != ks:
+        raise ValueError("q: [tokens, heads, dim], k and v: [tokens, kv_heads, dim]")
+    row = (D, 1)
+    for x in (q, k, v):
+        st = x.stride()
+        if x.dtype != dtype or x.device != dev or (st[1:] != row and (x.shape[1] > 1 or st[2] != 1)):
+            raise ValueError(f"q, k and v: of {dtype} on {dev}, each token's rows contiguous")
+    if starts.dtype != torch.int32 or starts.dim() != 1 or starts.shape[0] < 1 or not starts.is_contiguous() or starts.device != dev:
+        raise ValueError(f"starts: contiguous int32 [batch + 1], on {dev}")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=dtype, device=dev)
+    elif out.shape != q.shape or out.dtype != dtype or not out.is_contiguous() or out.device != dev:
+        raise ValueError(f"out: contiguous {tuple(q.shape)} of {dtype} on {dev}")
+    if window < 0:
+        raise XQError("xq_prompt_attn", 2)
+    # ctypes keeps the low 32 bits of an int: a larger window would become another one
+    p = xq_prompts(_float_type(dtype), T, starts.shape[0] - 1, H, ks[1], D, q.data_ptr(), k.data_ptr(), v.data_ptr(), q.stride(0),
+                   k.stride(0), v.stride(0), out.data_ptr(), starts.data_ptr(), D ** -0.5 if scale is None else scale,
+                   min(window, 0x7FFFFFFF))
+    L = lib()
+    if workspace is None:
+        need = L.xq_prompt_attn_workspace_bytes(p)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 16 else None
+        at, size = (ws.data_ptr(), need) if need > 16 else (None, 0)
+    else:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace: contiguous, on {dev}")
+        at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    rc = L.xq_prompt_attn(p, at, size, _handle(dev, stream))
+    if rc:
+        raise XQError("xq_prompt_attn", rc)
+    return out

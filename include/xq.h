@@ -336,12 +336,14 @@ XQ_API xq_status xq_layer_mixed_static(const xq_proj *proj, int n_proj,
  * is of an invalid index, not of a wait: 1 a slot past the cache, 2 a page id
  * outside it, 3 a sequence longer than its page table (see xq_kv_write and
  * xq_kv_attn). Kernel 4 = the cache attention's 128-row tiles (waits 1-5 the
- * products, 6-9 the softmax, 10-12 the unpacking). Checked builds (the
+ * products, 6-9 the softmax, 10-12 the unpacking). Kernel 5 = adapters and
+ * prompt attention, an invalid index: 1 an adapter id, 2 a sequence's bounds
+ * (see xq_lora_add and xq_prompt_attn). Kernel 6 = a wait of prompt attention. Checked builds (the
  * library compiled with -DXQ_CHECK) also test the index, range or 16-byte alignment of each global
  * access whose address comes from nontrivial arithmetic, skip an access that
  * fails and record the site: kernel 9, wait = site (10-16 the GEMV, 20-26
  * the tile kernel, 30-32 the quantizer, 40-43 the dp4a Q6_K GEMV,
- * 50-55 the KV cache kernels), reported
+ * 50-55 the KV cache kernels, 60 norms with rotation), reported
  * after any wait code. If several kernels recorded one,
  * the lowest kernel number is reported and all are cleared. The reads and
  * writes are synchronous. XQ_ERR_ARG for a null code_out, XQ_ERR_CUDA if the
@@ -542,6 +544,109 @@ XQ_API xq_status xq_kv_attn(const xq_kv_cache *cache, const xq_kv_query *query, 
  * The prefix is read once for the whole batch. window must be 0. */
 XQ_API xq_status xq_kv_attn_shared(const xq_kv_cache *cache, const xq_kv_query *query, void *workspace,
                                    size_t ws_bytes, xq_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Between a layer's projections and its cache: low-rank adapters beside the
+ * projections, norms of queries and keys with the position rotation, and
+ * attention over whole prompts.
+ * ---------------------------------------------------------------------- */
+
+/* The low-rank adapters of one projection: n adapters of one rank (pad
+ * smaller ones with zeros). */
+typedef struct {
+    int type;            /* XQ_TYPE_F32, XQ_TYPE_F16 or XQ_TYPE_BF16, of a and b */
+    int n;               /* adapters */
+    int rank;            /* a multiple of 8, 8 .. 256 */
+    int K, N;            /* the projection's: K a positive multiple of 32 */
+    const void *a;       /* [n][rank][K] */
+    const void *b;       /* [n][N][rank] */
+    const float *scales; /* [n], or NULL for 1 */
+    float *y;            /* [M][N] fp32, added to */
+    int input;           /* index into the call's inputs */
+} xq_adapters;
+
+/* Add to each row of each projection's y what the row's adapter gives:
+ *   y[m] += scales[i] * (x[m] a[i]^T) b[i]^T,   i = ids[m],
+ * for the 1 .. 16 projections of proj in one launch, x = inputs[proj.input]
+ * fp32 [M][K]. Call it behind the projections (xq_layer_mixed or a matmul)
+ * whose y it adds to.
+ *   ids    : int32 [M], device, shared by the projections. Rows of a negative
+ *            id are left as they are. One that is not below a projection's n is
+ *            too, and is recorded (xq_device_error: kernel 5, wait 1).
+ *   inputs : host array of n_inputs (at most 64) device pointers.
+ * The y of different projections must not overlap, nor y and x. x, a and b
+ * are 16-byte aligned, y, scales and ids 4-byte. Products are of fp32's
+ * precision (x and x a^T enter the tensor cores as two tf32 numbers each, 22
+ * bits, fp32 adapters too, 16-bit ones exactly), sums are fp32. A row's result
+ * does not depend on the other rows' values. M == 0 enqueues nothing. */
+XQ_API xq_status xq_lora_add(const xq_adapters *proj, int n_proj, const float *const *inputs, int n_inputs, int M,
+                             const int32_t *ids, xq_stream stream);
+
+/* Queries and keys of a norm-and-rotation call. */
+typedef struct {
+    int type, y_type;    /* XQ_TYPE_F32, XQ_TYPE_F16 or XQ_TYPE_BF16: of q and k, of the results */
+    int tokens;
+    int heads, kv_heads; /* rows of q and of k in a token */
+    int dim;             /* head size: 64, 96, 128 or 256 */
+    const void *q, *k;   /* element (t, h, i) at q[t * q_stride + h * dim + i] */
+    long long q_stride, k_stride;          /* elements, at least heads * dim and kv_heads * dim */
+    void *q_out, *k_out;                   /* the same with their own strides */
+    long long q_out_stride, k_out_stride;
+    const float *q_weight, *k_weight;      /* fp32 [dim] of the norms; NULL: not normalized */
+    float eps;                             /* of the norms, at least 0 */
+    const int64_t *positions;              /* [tokens] */
+    const uint64_t *turns;  /* [rot / 2]: how far a position turns pair i, in 2^-64 of a full turn */
+    int rot;             /* elements of a head that are rotated, its first: a multiple of 16, 0 .. dim */
+    int pairs;           /* 0: pair i is (i, i + rot / 2); 1: (2i, 2i + 1) */
+    float magnitude;     /* of the rotated elements, usually 1 */
+} xq_qk_rows;
+
+/* For each head's row x of q and of k:
+ *   r = x * weight / sqrt(mean(x^2) + eps)   (r = x without a weight)
+ *   (r_a, r_b) of pair i becomes magnitude * (r_a cos - r_b sin, r_b cos + r_a sin),
+ *   angle = 2 pi * frac(position * turns[i] / 2^64),
+ * in fp32, rounded once to y_type. The product of a position and turns is
+ * taken modulo 2^64, so angles are as exact at far positions (negative ones
+ * too) as at near ones. An output may be its input (same pointer, type and
+ * stride); otherwise it must not overlap an input. q, k and the results are
+ * aligned to their elements (rows at multiples of 16 bytes are moved in
+ * 16-byte pieces), positions and turns to 8 bytes, weights to 4.
+ * tokens == 0 enqueues nothing. */
+XQ_API xq_status xq_qk_norm_rope(const xq_qk_rows *rows, xq_stream stream);
+
+/* Prompts packed one behind the other. */
+typedef struct {
+    int type;            /* XQ_TYPE_F32, XQ_TYPE_F16 or XQ_TYPE_BF16, of q, k, v and out */
+    int tokens;          /* rows of q, k, v and out */
+    int batch;           /* sequences */
+    int heads, kv_heads; /* heads a multiple of kv_heads: heads h*g .. h*g+g-1 read KV head h */
+    int dim;             /* head size: 64, 96, 128 or 256 */
+    const void *q, *k, *v;                  /* element (t, h, i) at q[t * q_stride + h * dim + i] */
+    long long q_stride, k_stride, v_stride; /* elements; rows may be a part of a longer q/k/v row */
+    void *out;           /* [tokens][heads][dim], contiguous */
+    const int32_t *starts; /* [batch + 1], device: sequence b is rows starts[b] .. starts[b+1]-1 */
+    float scale;         /* of the scores, usually 1 / sqrt(dim) */
+    int window;          /* 0, or how many keys a query sees at most, its own among them */
+} xq_prompts;
+
+/* Workspace bytes of xq_prompt_attn for these prompts (type, tokens, batch,
+ * heads, kv_heads and dim are looked at). 0 on bad arguments; at least 16
+ * otherwise. */
+XQ_API size_t xq_prompt_attn_workspace_bytes(const xq_prompts *prompts);
+
+/* Causal attention of every token over its own sequence:
+ *   s_j = scale * sum_d q_d * k_jd,   o = sum_j softmax(s)_j * v_j
+ * over the keys j of its sequence up to itself and, with a window, the last
+ * `window` of those. Scores, softmax statistics and sums are fp32; the softmax
+ * weights of 16-bit calls are rounded to that type for the product with V.
+ * Rows of out that belong to no sequence (before starts[0], behind
+ * starts[batch]) are left as they were. What a row does not see does not
+ * reach it, infinities and NaN included. A sequence whose bounds do not
+ * satisfy 0 <= starts[b] <= starts[b+1] <= tokens is left out and recorded
+ * (xq_device_error: kernel 5, wait 2). q, k, v and out are 16-byte aligned,
+ * strides multiples of 16 bytes, starts 4-byte aligned; out must not overlap
+ * an input. */
+XQ_API xq_status xq_prompt_attn(const xq_prompts *prompts, void *workspace, size_t ws_bytes, xq_stream stream);
 
 #ifdef __cplusplus
 }
