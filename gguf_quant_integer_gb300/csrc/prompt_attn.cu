@@ -2,7 +2,7 @@
 //
 // o_i = sum_j w_ij v_j / sum_j w_ij, w_ij = 2^(s_ij - m_i), s_ij = log2(e) scale q_i.k_j, over the keys j of the
 // row's sequence up to its own place (the last `window` of them).
-#include "ops_common.cuh"
+#include "prompt_tile.cuh"
 
 namespace xq {
 namespace {
@@ -88,13 +88,47 @@ size_t prompt_attn_workspace(const PromptArgs&) { return 0; }
 
 cudaError_t launch_prompt_attn(const PromptArgs& a, void*, cudaStream_t s) {
   g_kv_launched.store(true, std::memory_order_relaxed);
-  return a.type == kF32 ? launch<kF32>(a, s) : a.type == kF16 ? launch<kF16>(a, s) : launch<kBF16>(a, s);
+  if (a.type == kF32) return launch<kF32>(a, s);
+  PromptTileArgs p;
+  p.a = a;
+  const int group = a.heads / a.kv_heads;
+  // a group's heads share a tile's rows where that leaves at most a quarter of them empty
+  p.pack = group <= kPromptRows && kPromptRows / group * group >= 96 ? group : 1;
+  p.tokens_tile = kPromptRows / p.pack;
+  p.units = a.heads / p.pack;
+  switch (a.dim) {
+    case 64: return PromptTileDim<64>::launch(p, s);
+    case 96: return PromptTileDim<96>::launch(p, s);
+    case 128: return PromptTileDim<128>::launch(p, s);
+    default: return PromptTileDim<256>::launch(p, s);
+  }
 }
 
 cudaError_t take_prompt_error(unsigned int* index, unsigned int* wait) {
+  typedef cudaError_t (*TakeTile)(unsigned int*, unsigned int*);
+  const TakeTile fns[4] = {PromptTileDim<64>::take_error, PromptTileDim<96>::take_error, PromptTileDim<128>::take_error,
+                           PromptTileDim<256>::take_error};
   *wait = 0;
-  return take_record(g_prompt_error, index);
+  cudaError_t e = take_record(g_prompt_error, index);
+  for (TakeTile f : fns) {
+    unsigned int i = 0, w = 0;
+    if (e == cudaSuccess) e = f(&i, &w);
+    if (*index == 0) *index = i;
+    if (*wait == 0) *wait = w;
+  }
+  return e;
 }
-cudaError_t take_prompt_check(unsigned int* code) { return take_check_word(code); }
+cudaError_t take_prompt_check(unsigned int* code) {
+  typedef cudaError_t (*TakeFn)(unsigned int*);
+  const TakeFn fns[4] = {PromptTileDim<64>::take_check, PromptTileDim<96>::take_check, PromptTileDim<128>::take_check,
+                         PromptTileDim<256>::take_check};
+  cudaError_t e = take_check_word(code);
+  for (TakeFn f : fns) {
+    unsigned int c = 0;
+    if (e == cudaSuccess) e = f(&c);
+    if (*code == 0) *code = c;
+  }
+  return e;
+}
 
 }  // namespace xq

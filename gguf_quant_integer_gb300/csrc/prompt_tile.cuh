@@ -1,0 +1,671 @@
+// Prompt attention of 16-bit rows on the tcgen05 tensor cores.
+//
+// o_i = sum_j w_ij v_j / sum_j w_ij with w_ij = 2^(s_ij - e_i), s_ij = log2(e) scale q_i.k_j. The reference e_i of a row
+// moves only when a weight would leave its range, so outputs are rescaled rarely; w enters the second product as a 16-bit
+// number, its sum is fp32.
+//
+// A tile is 128 rows x 128 keys. Rows are the query heads of a KV head that lie side by side, times tokens: row r is token
+// r / pack, head r % pack, so that K and V are read once for all of them. A CTA has two row tiles (one with head size 256,
+// whose outputs fill tensor memory), so that one's softmax passes under the other's products. Q, K and V come by TMA with
+// the swizzle that the products read; V is the K-outer operand as it lies in memory. Scores go to tensor memory, a softmax
+// thread takes a row of them and leaves the weights in the same columns, the second product's A operand.
+//
+// Roles: warps 0-3 and 4-7 softmax and results of a row tile, then one that issues products, one that copies, two that
+// look through V (below). CTAs are
+// persistent and take items (row tiles of a sequence and heads) longest first, in rounds of alternating direction; the
+// copying warp finds them from the sequences' bounds (see next_item) an item ahead, so Q, K and V of the next item are on
+// their way while one ends.
+//
+// What is not finite: scores of keys that a row does not see are replaced, but such a key's V would meet a weight of 0 in
+// the product, where an infinity or NaN spoils the row. So two warps look through the V tiles of which some row does not see
+// all keys, before the product, and put 0 in the place of such elements. Rows that do see one of them, and rows whose result
+// or sum is not finite (a score, a V that all rows see), are computed again by themselves (one_row).
+#pragma once
+
+#include "ops_common.cuh"
+#include "xq_common.cuh"
+#include "xq_ptx.cuh"
+
+namespace xq {
+
+constexpr int kPromptRows = 128;  // of a row tile
+
+struct PromptTileArgs {
+  PromptArgs a;
+  int pack;      // query heads of a KV head in a tile's rows
+  int tokens_tile;  // of a row tile: 128 / pack
+  int units;     // head units: kv_heads * group / pack
+  CUtensorMap q, k, v;
+};
+
+template <int D>
+struct PromptTileDim {
+  static cudaError_t launch(PromptTileArgs& a, cudaStream_t s);
+  static cudaError_t take_error(unsigned int* index, unsigned int* wait);
+  static cudaError_t take_check(unsigned int* code);
+};
+
+#ifdef XQ_PROMPT_TILE_IMPL
+
+namespace {
+
+__device__ unsigned int g_prompt_error;  // invalid indices
+__device__ unsigned int g_prompt_wait;   // a wait that ran out
+constexpr long long kPromptWait = 1ll << 32;
+constexpr int kRows = kPromptRows, kKeys = 128;
+
+template <int D>
+struct PromptShape {
+  static constexpr int kTiles = D == 256 ? 1 : 2;               // row tiles
+  static constexpr int kBox = D % 64 == 0 ? 64 : 32;            // elements of a swizzled row
+  static constexpr int kLine = kBox * 2, kBoxes = D / kBox;
+  static constexpr int kQ = kRows * D * 2, kStage = kKeys * D * 2;  // bytes: Q of a row tile; K or V of a tile
+  static constexpr int kStages = D == 256 ? 2 : D == 128 ? 5 : D == 96 ? 7 : 10;
+  static constexpr int kSmem = kTiles * kQ + kStages * kStage + 1024;
+  static constexpr int kColS = 0, kColO = 2 * kKeys, kAlloc = 512;
+  static constexpr int kWarps = 4 * kTiles + 4;
+  static_assert(kColO + kTiles * D <= kAlloc && kSmem <= 227 * 1024 - 1024, "one CTA fits the SM");
+  // Operand descriptors. Q and K: rows of kLine bytes are the K extent, 8 of them 8 * kLine apart. V: rows are keys, the
+  // N extent runs along them, blocks of kBox elements kKeys * kLine apart.
+  static constexpr uint64_t kSwizzle = kLine == 128 ? 2ull : 4ull;
+  static constexpr uint64_t kCommon = (1ull << 46) | (kSwizzle << 61) | (static_cast<uint64_t>(8 * kLine / 16) << 32);
+  static constexpr uint64_t kDescK = kCommon | (1ull << 16);
+  static constexpr uint64_t kDescV = kCommon | (static_cast<uint64_t>(kKeys * kLine / 16) << 16);
+};
+
+struct Item {
+  int first, n;     // the sequence's first row and its rows
+  int place;        // of row tile 0's first token
+  int head;         // first query head
+  int begin[2], end[2];  // key tiles of the row tiles
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+template <int TYPE>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  uint32_t d;
+  if constexpr (TYPE == kF16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+  return d;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(mbar)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
+        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
+        "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
+        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// One row by one warp, lanes over the head's elements.
+template <int TYPE, int D>
+__device__ __noinline__ void one_row(const PromptArgs& A, int first, int place, int head) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31, kv = head / (A.heads / A.kv_heads);
+  const size_t token = static_cast<size_t>(first) + place;
+  float q[E], o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    q[e] = load_elt<TYPE>(A.q, token * A.q_stride + static_cast<size_t>(head) * D + lane + 32 * e);
+    o[e] = 0.0f;
+  }
+  const float cs = A.scale * 1.4426950408889634f;
+  float m = -INFINITY, l = 0.0f;
+  for (int j = A.window && place >= A.window ? place - A.window + 1 : 0; j <= place; ++j) {
+    const size_t key = static_cast<size_t>(first) + j;
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      s = fmaf(q[e], load_elt<TYPE>(A.k, key * A.k_stride + static_cast<size_t>(kv) * D + lane + 32 * e), s);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+    s = __fmul_rn(s, cs);
+    const float next = fmaxf(m, s);
+    const float f = m == next ? 1.0f : exp2f(m - next), w = s == -INFINITY && next == s ? 0.0f : exp2f(s - next);
+    m = next;
+    l = fmaf(l, f, w);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      o[e] = fmaf(o[e], f, w * load_elt<TYPE>(A.v, key * A.v_stride + static_cast<size_t>(kv) * D + lane + 32 * e));
+  }
+  const size_t row = token * A.heads + head;
+  if (XQ_IN(row, static_cast<size_t>(A.tokens) * A.heads, kChkPromptRow))
+#pragma unroll
+    for (int e = 0; e < E; ++e) store_elt<TYPE>(A.out, row * D + lane + 32 * e, o[e] / l);
+}
+
+// Sequence b's rows and their number; 0, and recorded, if its bounds are no range of the call's rows.
+__device__ __forceinline__ int sequence(const PromptArgs& A, int b, int* first) {
+  if (b >= A.batch) return 0;
+  const int s0 = A.starts[b], s1 = A.starts[b + 1];
+  *first = s0;
+  if (s0 < 0 || s1 < s0 || s1 > A.tokens) {
+    atomicCAS(&g_prompt_error, 0u, kOpsBadStart);
+    return 0;
+  }
+  return s1 - s0;
+}
+
+// Items in descending order of their work. An item is a head unit of a group of `step` tokens of a sequence; group L of any
+// sequence has the keys up to it, so all groups L of all sequences (a level) are alike. A warp walks down the levels,
+// counting the sequences that reach each.
+struct Walk {
+  int level;        // of the current one
+  long long before; // groups in the levels before it
+  int count;        // sequences that reach it
+};
+__device__ __forceinline__ int walk_count(const PromptArgs& A, int level, int step) {
+  int c = 0;
+  for (int b = threadIdx.x & 31; b < A.batch; b += 32) {
+    int first;
+    c += sequence(A, b, &first) > level * static_cast<long long>(step);
+  }
+  return __reduce_add_sync(0xffffffffu, c);
+}
+__device__ __forceinline__ void walk_begin(const PromptArgs& A, int step, Walk& w) {
+  int most = 0;
+  for (int b = threadIdx.x & 31; b < A.batch; b += 32) {
+    int first;
+    most = max(most, sequence(A, b, &first));
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  w.level = (most + step - 1) / step - 1;
+  w.before = 0;
+  w.count = w.level >= 0 ? walk_count(A, w.level, step) : 0;
+}
+// The item of this rank; false behind the last. Ranks come in ascending order.
+__device__ __forceinline__ bool next_item(const PromptTileArgs& P, int tiles, long long rank, Walk& w, Item& it) {
+  const PromptArgs& A = P.a;
+  const int step = tiles * P.tokens_tile, lane = threadIdx.x & 31;
+  const long long group = rank / P.units;
+  const int unit = static_cast<int>(rank - group * P.units);
+  while (w.level >= 0 && group >= w.before + w.count) {
+    w.before += w.count;
+    --w.level;
+    if (w.level >= 0) w.count = walk_count(A, w.level, step);
+  }
+  if (w.level < 0) return false;
+  int left = static_cast<int>(group - w.before);  // sequences to pass over, of those that reach the level
+  for (int b0 = 0; b0 < A.batch; b0 += 32) {
+    int first = 0;
+    const int n = sequence(A, b0 + lane, &first);
+    const unsigned reach = __ballot_sync(0xffffffffu, n > w.level * static_cast<long long>(step));
+    const int c = __popc(reach);
+    if (left >= c) {
+      left -= c;
+      continue;
+    }
+    const int at = __fns(reach, 0, left + 1);
+    it.first = __shfl_sync(0xffffffffu, first, at);
+    it.n = __shfl_sync(0xffffffffu, n, at);
+    break;
+  }
+  it.place = w.level * step;
+  it.head = unit * P.pack;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int p0 = it.place + r * P.tokens_tile, p1 = min(p0 + P.tokens_tile, it.n) - 1;  // first and last row's
+    const int k0 = A.window ? max(0, p0 - A.window + 1) : 0;
+    it.begin[r] = r < tiles && p1 >= p0 ? k0 / kKeys : 0;
+    it.end[r] = r < tiles && p1 >= p0 ? p1 / kKeys + 1 : 0;
+  }
+  return true;
+}
+
+enum PromptBar { kPbDrain, kPbItem, kPbItemFree = kPbItem + 2, kPbQ = kPbItemFree + 2, kPbQFree = kPbQ + 2, kPbS = kPbQFree + 2,
+                 kPbP = kPbS + 2, kPbO = kPbP + 2, kPbFull = kPbO + 2 };
+
+// Whether some row of row tile r does not see some key of a tile from `key` on.
+__device__ __forceinline__ bool masked(const PromptTileArgs& P, int place, int key) {
+  return key + kKeys > place + 1 || (P.a.window && key < place + P.tokens_tile - P.a.window);
+}
+
+// Bit 15 of each half: it is an infinity or NaN.
+template <int TYPE>
+__device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
+  constexpr uint32_t field = TYPE == kF16 ? 0x7C007C00u : 0x7F807F80u, one = TYPE == kF16 ? 0x04000400u : 0x00800080u;
+  return ((w & field) + one) & 0x80008000u;
+}
+
+template <int TYPE, int D>
+__global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_kernel(const __grid_constant__ PromptTileArgs P) {
+  using S = PromptShape<D>;
+  constexpr int kTiles = S::kTiles, kStages = S::kStages, kPbFree = kPbFull + kStages, kPbChecked = kPbFree + kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[kPbFull + 3 * kStages];
+  __shared__ uint32_t sh_tmem;
+  __shared__ Item sh_item[2];
+  __shared__ unsigned sh_odd[2];  // elements of V that are not finite were put to 0, by item & 1
+  const PromptArgs& A = P.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kMma = 4 * kTiles, kLoad = kMma + 1, kCheck = kMma + 2;
+  auto bar = [&](int i) { return ptx::smem_addr(&bars[i]); };
+  const uint32_t base = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u;
+  if (tid == 0) {
+    ptx::mbar_init(bar(kPbDrain), 1);
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(bar(kPbItem + b), 1);
+      ptx::mbar_init(bar(kPbItemFree + b), 4 * kTiles + 3);
+      ptx::mbar_init(bar(kPbQ + b), 1);
+      ptx::mbar_init(bar(kPbQFree + b), 1);
+      ptx::mbar_init(bar(kPbS + b), 1);
+      ptx::mbar_init(bar(kPbP + b), 4);
+      ptx::mbar_init(bar(kPbO + b), 1);
+    }
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(bar(kPbFull + i), 1);
+      ptx::mbar_init(bar(kPbFree + i), 1);
+      ptx::mbar_init(bar(kPbChecked + i), 2);
+    }
+    ptx::mbar_init_fence();
+  }
+  if (warp == kMma) ptx::tmem_alloc(ptx::smem_addr(&sh_tmem), S::kAlloc);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sh_tmem;
+  auto wait = [&](int i, unsigned parity, unsigned code) {
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar(i), parity & 1, &g_prompt_wait, code, kPromptWait)) != 0;
+  };
+  // buffer of scores of row tile r's n-th tile, and how often it was used before
+  auto buffer = [](int r, unsigned n) { return kTiles == 2 ? r : static_cast<int>(n & 1); };
+  auto turn = [](unsigned n) { return kTiles == 2 ? n : n >> 1; };
+  unsigned items = 0;  // taken so far
+  auto take = [&](Item& it) {  // false: the last one is done (or a wait ran out)
+    if (!wait(kPbItem + (items & 1), items >> 1, 1)) return false;
+    it = sh_item[items & 1];
+    return it.n >= 0;
+  };
+  auto leave = [&] {  // its last use of the item's place
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(bar(kPbItemFree + (items & 1)));
+    ++items;
+  };
+
+  if (warp == kLoad) {
+    // ------------------------------------------------ copies
+    Walk w;
+    walk_begin(A, kTiles * P.tokens_tile, w);
+    const bool lead = ptx::elect_one();
+    unsigned loaded = 0, q_done[2] = {0u, 0u};
+    bool ok = true;
+    for (unsigned round = 0; ok; ++round) {
+      Item it;
+      const long long rank = static_cast<long long>(round) * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      const bool there = next_item(P, kTiles, rank, w, it);
+      if (!there) it.n = -1;
+      if (round >= 2 && !wait(kPbItemFree + (round & 1), (round >> 1) + 1, 2)) break;
+      if (lead) {
+        sh_item[round & 1] = it;
+        sh_odd[round & 1] = 0u;
+        ptx::mbar_arrive(bar(kPbItem + (round & 1)));
+      }
+      __syncwarp();
+      if (!there) break;
+      const int kv = it.head / (A.heads / A.kv_heads);
+      const bool second = kTiles == 2 && it.end[1] > 0;
+      for (int r = 0; r < (second ? 2 : 1) && ok; ++r) {
+        if (q_done[r] > 0) ok = wait(kPbQFree + r, q_done[r] - 1, 3);
+        ++q_done[r];
+        if (ok && lead) {
+          ptx::mbar_expect_tx(bar(kPbQ + r), P.pack * P.tokens_tile * D * 2);
+#pragma unroll
+          for (int x = 0; x < S::kBoxes; ++x)
+            tma_load_3d(base + r * S::kQ + x * (kRows * S::kLine), &P.q, x * S::kBox, it.head, it.first + it.place + r * P.tokens_tile,
+                        bar(kPbQ + r));
+        }
+      }
+      const int last = second ? it.end[1] : it.end[0];
+      for (int j = it.begin[0]; j < last && ok; ++j) {
+#pragma unroll 1
+        for (int v = 0; v < 2 && ok; ++v, ++loaded) {
+          const unsigned st = loaded % kStages;
+          if (loaded >= kStages) ok = wait(kPbFree + st, loaded / kStages - 1, 4);
+          if (ok && lead) {
+            ptx::mbar_expect_tx(bar(kPbFull + st), S::kStage);
+#pragma unroll
+            for (int x = 0; x < S::kBoxes; ++x)
+              tma_load_3d(base + kTiles * S::kQ + st * S::kStage + x * (kKeys * S::kLine), v ? &P.v : &P.k, x * S::kBox, kv,
+                          it.first + j * kKeys, bar(kPbFull + st));
+          }
+        }
+      }
+      __syncwarp();
+    }
+    // copies in flight land before the CTA ends
+    for (unsigned i = loaded > kStages ? loaded - kStages : 0; i < loaded; ++i)
+      if (!wait(kPbFull + i % kStages, i / kStages, 5)) break;
+  } else if (warp == kMma) {
+    // ------------------------------------------------ products, issued by one thread
+    constexpr uint32_t idS = ptx::idesc_f16(kRows, kKeys, TYPE == kBF16), idO = ptx::idesc_f16(kRows, D, TYPE == kBF16) | (1u << 16);
+    const bool lead = ptx::elect_one();
+    const uint32_t at = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t stage0 = static_cast<uint64_t>((base + kTiles * S::kQ) >> 4), q0 = static_cast<uint64_t>(base >> 4);
+    unsigned used = 0;  // loads of the items before
+    unsigned scored[2] = {0u, 0u}, done[2] = {0u, 0u}, parts[2] = {0u, 0u};
+    bool ok = true;
+    Item it;
+    while (ok && take(it)) {
+      leave();
+      const bool second = kTiles == 2 && it.end[1] > 0;
+      const int first = it.begin[0], last = second ? it.end[1] : it.end[0];
+      auto k_load = [&](int j) { return used + 2 * (j - first); };  // V's is the next
+      auto scores = [&](int r, int j) {
+        if (j == it.begin[r]) {
+          ok = wait(kPbQ + r, parts[r]++, 6);
+          if (!ok) return;
+        }
+        const unsigned ld = k_load(j), st = ld % kStages;
+        ok = wait(kPbFull + st, ld / kStages, 7);
+        if (!ok) return;
+        ptx::tc_fence_after();
+        const int to = buffer(r, scored[r]++);
+        const uint32_t d = __shfl_sync(0xffffffffu, at + S::kColS + to * kKeys, 0);
+        const uint64_t kd = S::kDescK | (stage0 + __shfl_sync(0xffffffffu, st * (S::kStage / 16), 0));
+        const uint64_t qd = S::kDescK | (q0 + r * (S::kQ / 16));
+        if (lead) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            constexpr int kSteps = S::kBox / 16;
+            const int off = (k / kSteps) * (kRows * S::kLine / 16) + (k % kSteps) * 2;
+            ptx::mma_f16_ss(d, qd + off, kd + off, idS, k > 0);
+          }
+          ptx::tc_commit(bar(kPbS + to));
+          if (j + 1 == it.end[r]) ptx::tc_commit(bar(kPbQFree + r));
+        }
+        __syncwarp();
+      };
+      auto outputs = [&](int r, int j) {
+        const int from = buffer(r, done[r]);
+        ok = wait(kPbP + from, turn(done[r]), 8);
+        ++done[r];
+        if (!ok) return;
+        const unsigned ld = k_load(j) + 1, st = ld % kStages;
+        ok = wait(kPbFull + st, ld / kStages, 9) && wait(kPbChecked + ld / 2 % kStages, ld / 2 / kStages, 14);
+        if (!ok) return;
+        ptx::tc_fence_after();
+        const uint32_t d = __shfl_sync(0xffffffffu, at + S::kColO + r * D, 0);
+        const uint32_t a = __shfl_sync(0xffffffffu, at + S::kColS + from * kKeys, 0);
+        const uint64_t vd = S::kDescV | (stage0 + __shfl_sync(0xffffffffu, st * (S::kStage / 16), 0));
+        if (lead) {
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            ptx::mma_f16_ts(d, a + 8 * k, vd + k * (2 * 8 * S::kLine / 16), idO, j > it.begin[r] || k > 0);
+          ptx::tc_commit(bar(kPbO + from));
+        }
+        __syncwarp();
+      };
+      auto release = [&](unsigned ld) {
+        if (lead) ptx::tc_commit(bar(kPbFree + ld % kStages));
+        __syncwarp();
+      };
+      for (int j = first - 1; j < last && ok; ++j) {
+        if (kTiles == 2) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            if (ok && j >= it.begin[r] && j < it.end[r]) outputs(r, j);
+            if (ok && j + 1 >= it.begin[r] && j + 1 < it.end[r]) scores(r, j + 1);
+          }
+        } else {
+          if (j + 1 < last) scores(0, j + 1);
+          if (ok && j >= first) outputs(0, j);
+        }
+        if (!ok) break;
+        if (j + 1 < last) release(k_load(j + 1));
+        if (j >= first) release(k_load(j) + 1);
+      }
+      used += 2 * (last - first);
+    }
+    if (lead) ptx::tc_commit(bar(kPbDrain));  // nothing is in flight when tensor memory is freed
+    wait(kPbDrain, 0, 10);
+  } else if (warp >= kCheck) {
+    // ------------------------------------------------ V's elements that are not finite
+    unsigned tiles = 0;  // V tiles so far
+    bool ok = true;
+    Item it;
+    while (ok && take(it)) {
+      const bool second = kTiles == 2 && it.end[1] > 0;
+      const int last = second ? it.end[1] : it.end[0];
+      for (int j = it.begin[0]; j < last; ++j, ++tiles) {
+        const unsigned ld = 2 * tiles + 1, st = ld % kStages;
+        ok = wait(kPbFull + st, ld / kStages, 15);
+        if (!ok) break;
+        if (masked(P, it.place, j * kKeys) || (second && masked(P, it.place + P.tokens_tile, j * kKeys))) {
+          const uint32_t from = base + kTiles * S::kQ + st * S::kStage + ((warp - kCheck) * 32 + lane) * 16;
+          bool found = false;
+#pragma unroll 8
+          for (int x = 0; x < S::kStage; x += 64 * 16) {
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from + x));
+            if (odd_halves<TYPE>(w[0]) | odd_halves<TYPE>(w[1]) | odd_halves<TYPE>(w[2]) | odd_halves<TYPE>(w[3])) {
+              found = true;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) w[i] &= ~((odd_halves<TYPE>(w[i]) >> 15) * 0xFFFFu);
+              asm volatile("st.shared.v4.b32 [%4], {%0, %1, %2, %3};" ::"r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(from + x) : "memory");
+            }
+          }
+          if (found) {
+            sh_odd[items & 1] = 1u;
+            ptx::fence_proxy_async_smem();
+          }
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(kPbChecked + tiles % kStages));
+      }
+      leave();
+    }
+  } else {
+    // ------------------------------------------------ softmax and results: a thread is a row
+    // log2 of weights: the largest, and where the reference starts anew. fp16 keeps 2^-24 at least, so its weights begin above 1.
+    constexpr float kTop = TYPE == kF16 ? 15.0f : 20.0f, kStart = TYPE == kF16 ? 8.0f : 0.0f;
+    constexpr float kLowest = -3.402823466e38f;
+    const int r = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16), to = tl + S::kColO + r * D;
+    // a scale that is not positive goes to the scores first, so that cs > 0 and what is masked stays -infinity
+    const bool turned = !(A.scale > 0.0f);
+    const float sign = A.scale < 0.0f ? -1.0f : 0.0f, cs = A.scale == 0.0f ? 1.0f : fabsf(A.scale) * 1.4426950408889634f;
+    const int token = row / P.pack, part = row - token * P.pack;
+    unsigned done = 0;
+    bool ok = true;
+    Item it;
+    while (ok && take(it)) {
+      const int tiles = it.end[r] - it.begin[r];
+      if (tiles <= 0) {
+        leave();
+        continue;
+      }
+      const int place = it.place + r * P.tokens_tile + token;
+      const bool live = token < P.tokens_tile && place < it.n;
+      const int lim1 = place + 1, lim0 = A.window ? max(0, lim1 - A.window) : 0;
+      const int p0 = it.place + r * P.tokens_tile;
+      float e = kLowest;
+      ptx::f2 l = ptx::pk(0.0f, 0.0f);
+      for (int i = 0; i < tiles; ++i, ++done) {
+        const int key = (it.begin[r] + i) * kKeys;
+        ok = wait(kPbS + buffer(r, done), turn(done), 11);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t ts = tl + S::kColS + buffer(r, done) * kKeys;
+        uint32_t sv[kKeys];
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 32) tmem_ld32(ts + c, sv + c);
+        ptx::tmem_wait_ld();
+        if (turned) {
+#pragma unroll
+          for (int x = 0; x < kKeys; ++x) sv[x] = __float_as_uint(__uint_as_float(sv[x]) * sign);
+        }
+        if (masked(P, p0, key)) {
+#pragma unroll
+          for (int x = 0; x < kKeys; ++x)
+            if (key + x < lim0 || key + x >= lim1) sv[x] = 0xFF800000u;
+        }
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int x = 0; x < kKeys; x += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            tops[y] = max3(tops[y], __uint_as_float(sv[x + 2 * y]), __uint_as_float(sv[x + 2 * y + 1]));
+        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * cs;
+        if (__any_sync(0xffffffffu, top - e > kTop)) {  // the reference of some rows moves
+          const float next = top - e > kTop ? top - kStart : e;
+          const float f = ex2(e - next);
+          e = next;
+          l = ptx::mul2(l, ptx::pk(f, f));
+          if (i > 0) {
+            ok = wait(kPbO + buffer(r, done - 1), turn(done - 1), 12);
+            if (!ok) break;
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t w[16];
+              ptx::tmem_ld16(to + c, w);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(__uint_as_float(w[x]) * f);
+              ptx::tmem_st16(to + c, w);
+            }
+          }
+        }
+        const ptx::f2 c2 = ptx::pk(cs, cs), e2 = ptx::pk(-e, -e);
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            const ptx::f2 z = ptx::fma2(ptx::pk(__uint_as_float(sv[c + x]), __uint_as_float(sv[c + x + 1])), c2, e2);
+            const float a = ex2(ptx::lo32(z)), b = ex2(ptx::hi32(z));
+            l = ptx::add2(l, ptx::pk(a, b));
+            w[x / 2] = pack2<TYPE>(a, b);
+          }
+          ptx::tmem_st16(ts + c / 2, w);
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(kPbP + buffer(r, done)));
+      }
+      if (!ok) break;
+      // ---- the rows' results
+      ok = wait(kPbO + buffer(r, done - 1), turn(done - 1), 13);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const float sum = ptx::lo32(l) + ptx::hi32(l), inv = 1.0f / sum;
+      const size_t at = (static_cast<size_t>(it.first) + place) * A.heads + it.head + part;
+      const bool store = live && XQ_IN(at, static_cast<size_t>(A.tokens) * A.heads, kChkPromptRow);
+      uint4* const out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + at * D);
+      float odd[4] = {sum * 0.0f, 0.0f, 0.0f, 0.0f};  // NaN if anything is not finite
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        uint32_t w[32];
+        tmem_ld32(to + c, w);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 32; ++x) odd[x & 3] = fmaf(__uint_as_float(w[x]), 0.0f, odd[x & 3]);
+        if (store) {
+#pragma unroll
+          for (int x = 0; x < 32; x += 8) {
+            uint4 y;
+            y.x = pack2<TYPE>(__uint_as_float(w[x]) * inv, __uint_as_float(w[x + 1]) * inv);
+            y.y = pack2<TYPE>(__uint_as_float(w[x + 2]) * inv, __uint_as_float(w[x + 3]) * inv);
+            y.z = pack2<TYPE>(__uint_as_float(w[x + 4]) * inv, __uint_as_float(w[x + 5]) * inv);
+            y.w = pack2<TYPE>(__uint_as_float(w[x + 6]) * inv, __uint_as_float(w[x + 7]) * inv);
+            out[(c + x) / 8] = y;
+          }
+        }
+      }
+      ptx::tc_fence_before();
+      bool meets = false;  // an element that was put to 0
+      if (sh_odd[items & 1]) {
+        const int kv = it.head / (A.heads / A.kv_heads);
+#pragma unroll 1
+        for (int j = it.begin[r]; j < it.end[r]; ++j)
+          if (masked(P, it.place, j * kKeys) || (it.end[1] > 0 && masked(P, it.place + P.tokens_tile, j * kKeys)))
+#pragma unroll 1
+            for (int key = j * kKeys; key < min((j + 1) * kKeys, it.n); ++key) {
+              bool odd_v = false;
+              for (int x = lane; x < D; x += 32)
+                odd_v |= !isfinite(load_elt<TYPE>(A.v, (static_cast<size_t>(it.first) + key) * A.v_stride + static_cast<size_t>(kv) * D + x));
+              if (__any_sync(0xffffffffu, odd_v)) meets |= key >= lim0 && key < lim1;
+            }
+      }
+      unsigned again = __ballot_sync(0xffffffffu, live && (meets || !(odd[0] + odd[1] + odd[2] + odd[3] == 0.0f && sum > 0.0f)));
+      while (again) {
+        const int src = __ffs(again) - 1;
+        again &= again - 1;
+        one_row<TYPE, D>(A, it.first, __shfl_sync(0xffffffffu, place, src), it.head + __shfl_sync(0xffffffffu, part, src));
+      }
+      leave();
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == kMma) ptx::tmem_dealloc(tmem, S::kAlloc);
+}
+
+template <int TYPE, int D>
+cudaError_t launch_tile(const PromptTileArgs& p, cudaStream_t s) {
+  using S = PromptShape<D>;
+  static std::atomic<unsigned long long> allowed{0};
+  const cudaError_t e = allow_shared(prompt_tile_kernel<TYPE, D>, S::kSmem, allowed);
+  if (e != cudaSuccess) return e;
+  // no more items than this: whole groups of tokens, and a part of one for each sequence
+  const long long items = (p.a.tokens / (S::kTiles * p.tokens_tile) + static_cast<long long>(p.a.batch)) * p.units;
+  const int grid = static_cast<int>(items < 152 ? (items < 1 ? 1 : items) : 152);
+  prompt_tile_kernel<TYPE, D><<<grid, 32 * S::kWarps, S::kSmem, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+template <int D>
+cudaError_t PromptTileDim<D>::launch(PromptTileArgs& p, cudaStream_t s) {
+  using S = PromptShape<D>;
+  g_kv_launched.store(true, std::memory_order_relaxed);
+  const PromptArgs& a = p.a;
+  const bool bf16 = a.type == kBF16;
+  const bool one = a.tokens == 1;
+  if (!encode_tma_heads(&p.q, bf16, a.q, D, a.heads, a.tokens, one ? static_cast<long long>(a.heads) * D : a.q_stride, S::kBox, p.pack,
+                        p.tokens_tile) ||
+      !encode_tma_heads(&p.k, bf16, a.k, D, a.kv_heads, a.tokens, one ? static_cast<long long>(a.kv_heads) * D : a.k_stride, S::kBox, 1,
+                        kKeys) ||
+      !encode_tma_heads(&p.v, bf16, a.v, D, a.kv_heads, a.tokens, one ? static_cast<long long>(a.kv_heads) * D : a.v_stride, S::kBox, 1,
+                        kKeys))
+    return cudaErrorInvalidValue;
+  return bf16 ? launch_tile<kBF16, D>(p, s) : launch_tile<kF16, D>(p, s);
+}
+
+template <int D>
+cudaError_t PromptTileDim<D>::take_error(unsigned int* index, unsigned int* wait) {
+  const cudaError_t e = take_record(g_prompt_error, index);
+  return e != cudaSuccess ? e : take_record(g_prompt_wait, wait);
+}
+template <int D>
+cudaError_t PromptTileDim<D>::take_check(unsigned int* code) {
+  return take_check_word(code);
+}
+
+#endif  // XQ_PROMPT_TILE_IMPL
+
+}  // namespace xq

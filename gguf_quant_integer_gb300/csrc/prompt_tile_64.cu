@@ -1,0 +1,7 @@
+// Prompt attention of 16-bit rows, head size 64.
+#define XQ_PROMPT_TILE_IMPL
+#include "prompt_tile.cuh"
+
+namespace xq {
+template struct PromptTileDim<64>;
+}  // namespace xq

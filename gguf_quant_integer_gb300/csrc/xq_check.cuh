@@ -84,6 +84,8 @@ enum CheckSite : unsigned {
   kChkKvLens = 55,   // sequence inside the batch
   // qk_rope.cu
   kChkRope = 60,     // 8 elements inside a row of a token of the call
+  // prompt_tile.cuh
+  kChkPromptRow = 61,  // row of the result inside [tokens][heads]
 };
 
 }  // namespace xq

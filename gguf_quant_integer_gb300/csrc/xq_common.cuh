@@ -279,6 +279,10 @@ cudaError_t take_q6k_check(unsigned int* code);
 // if the driver entry point is missing or rejects the arguments.
 bool encode_tma_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, unsigned long long dim0,
                    unsigned long long dim1, unsigned long long stride1, unsigned box0, unsigned box1);
+// 3D tensor map of heads' rows of a 16-bit type, [rows][heads][dim], rows `stride` elements apart (zero fill): boxes of
+// box_rows x box_heads x box_dim elements, box_dim 64 (128-byte swizzle) or 32 (64-byte).
+bool encode_tma_heads(CUtensorMap* map, bool bf16, const void* base, int dim, int heads, int rows, long long stride, int box_dim,
+                      int box_heads, int box_rows);
 
 // y = x W^T for M > 64 tokens on the tensor-memory tile kernel; type is 12
 // (Q4_K), 14 (Q6_K), 8 (Q8_0) or 23 (IQ4_XS, with its codebook as 4
