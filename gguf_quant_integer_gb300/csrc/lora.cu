@@ -1,5 +1,21 @@
-// Low-rank adapters of many requests beside shared projections:
-// y[m] += scale[i] * (x[m] A[i]^T) B[i]^T with the row's adapter i.
+// Low-rank adapters of many requests beside shared projections.
+//
+// y[m] += scale[i] (x[m] A[i]^T) B[i]^T with the row's adapter i. A job is up to T rows of one adapter and projection, one
+// cluster of 8 CTAs: each CTA multiplies its eighth of K (x against A, warps sharing that out once more), the CTAs add up
+// their parts of t = x A^T [T][rank] through distributed shared memory in a fixed order, and each then adds t B^T to its
+// eighth of y's columns. So one launch does both products, A and B of a job are read once, and t never leaves the SMs.
+//
+// Which rows make up a job is found in the kernel (count rows by adapter, number the jobs, collect the rows), as only the
+// device knows the ids; all CTAs of a cluster find the same.
+//
+// Precision: both products run on the warp-level tensor cores in tf32, x and t as two numbers each (11 + 11 bits; hi is cut
+// off, so that nothing overflows) and fp32 adapters too (without lo x lo); 16-bit adapters are exact. A tensor core's
+// accumulator cuts off, towards 0, what an fp32 addition rounds, so sums over K leave it every 32 elements (kept in it for
+// K / 16, 4096 elements had 1.3e-6 of error) and y is added in fp32 behind them.
+#include <algorithm>
+#include <type_traits>
+#include <utility>
+
 #include "ops_common.cuh"
 
 namespace xq {
@@ -7,50 +23,416 @@ namespace {
 
 __device__ unsigned int g_lora_error;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kCluster = 8;
+constexpr int kRankBlock = 64;        // ranks of a pass over x
+constexpr int kPartFloats = 8192;     // partial sums of the warps: [8 / MT][16 * MT][64]
+constexpr int kJobsGrid = 512;        // jobs of a projection with clusters of their own
+constexpr int kMaxAdapters = 8192;
 
-template <int TYPE>
-__device__ __forceinline__ void row(const AdapterProj& p, int m, int id, float* t) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < p.rank; r += kThreads / 32) {
-    float s = 0.0f;
-    for (int k = lane; k < p.K; k += 32)
-      s = fmaf(p.x[static_cast<size_t>(m) * p.K + k], load_elt<TYPE>(p.a, (static_cast<size_t>(id) * p.rank + r) * p.K + k), s);
+struct LoraGrid {
+  int jobs;       // at most, of a projection
+  int first;      // index of the launch's projections
+  int rank_most;  // of the launch's projections
+  int rows;       // T
+};
+
+// Row stride of t's pairs in bytes: 64 bytes beside whole 128-byte lines, so that two rows' quads share a load's banks.
+__host__ __device__ constexpr int pair_stride(int rank) { return rank * 8 + (rank * 8 % 128 == 64 ? 0 : 64); }
+__host__ __device__ constexpr int align16(int x) { return (x + 15) & ~15; }
+// Shared memory: t's part [T][rank] fp32, then what follows one behind the other: row counts by adapter, the warps' partial
+// sums, t as pairs.
+__host__ __device__ constexpr int part_bytes(int rows, int rank) { return rows * rank * 4; }
+inline int shared_bytes(int rows, int rank, int n) {
+  return part_bytes(rows, rank) + std::max({kPartFloats * 4, rows * pair_stride(rank), align16(n * 4)});
+}
+
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x = hi + lo to 22 bits: hi the upper 11 cut off (an infinity stays one, with lo = 0), lo rounded.
+__device__ __forceinline__ void split(float x, uint32_t* hi, uint32_t* lo) {
+  *hi = __float_as_uint(x) & 0xFFFFE000u;
+  const float h = __uint_as_float(*hi), rest = h == x ? 0.0f : x - h;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(*lo) : "f"(rest));
+}
+
+// W consecutive weights (8, 4 or 2) as tf32 numbers: hi, and lo for fp32 ones.
+template <int TYPE, int W>
+struct Weights {
+  uint32_t raw[TYPE == kF32 ? W : W / 2];
+  __device__ __forceinline__ void load(const void* p, size_t at, bool there) {
+    constexpr int kWords = TYPE == kF32 ? W : W / 2;
+    const uint32_t* const f = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p) + at * (TYPE == kF32 ? 4 : 2));
+    if (!there) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) t[r] = s * (p.scales ? p.scales[id] : 1.0f);
+      for (int i = 0; i < kWords; ++i) raw[i] = 0u;
+    } else if constexpr (kWords >= 4) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(f + i));
+        raw[i] = v.x, raw[i + 1] = v.y, raw[i + 2] = v.z, raw[i + 3] = v.w;
+      }
+    } else if constexpr (kWords == 2) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(f));
+      raw[0] = v.x, raw[1] = v.y;
+    } else {
+      raw[0] = __ldg(f);
+    }
+  }
+  // the i-th, i even, and the one after it
+  __device__ __forceinline__ void get(int i, uint32_t (&hi)[2], uint32_t (&lo)[2]) const {
+    if constexpr (TYPE == kF32) {
+      split(__uint_as_float(raw[i]), &hi[0], &lo[0]);
+      split(__uint_as_float(raw[i + 1]), &hi[1], &lo[1]);
+    } else if constexpr (TYPE == kF16) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&raw[i / 2]));
+      hi[0] = __float_as_uint(f.x), hi[1] = __float_as_uint(f.y);
+    } else {
+      hi[0] = raw[i / 2] << 16, hi[1] = raw[i / 2] & 0xFFFF0000u;
+    }
+  }
+};
+// d += (ahi + alo) x (bhi + blo), small products first
+template <int TYPE>
+__device__ __forceinline__ void product(float (&d)[4], const uint32_t (&ahi)[4], const uint32_t (&alo)[4], const uint32_t (&bhi)[2],
+                                        const uint32_t (&blo)[2]) {
+  if constexpr (TYPE == kF32) mma_tf32(d, ahi, blo[0], blo[1]);
+  mma_tf32(d, alo, bhi[0], bhi[1]);
+  mma_tf32(d, ahi, bhi[0], bhi[1]);
+}
+
+__device__ __forceinline__ uint32_t smem_at(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer(uint32_t at, unsigned cta) {
+  uint32_t d;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(at), "r"(cta));
+  return d;
+}
+__device__ __forceinline__ float4 peer_load4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void peer_store4(uint32_t at, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
+struct JobShared {
+  int rows[64];
+  int adapter, chunk;
+  int sums[kWarps];
+};
+
+// The j-th job of a projection with n adapters: its adapter, and its rows in sh.rows; returns how many, 0 if there is none.
+__device__ int find_job(const int32_t* ids, int M, int n, int T, int j, int* counts, JobShared& sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < n; i += kThreads) counts[i] = 0;
+  if (tid == 0) sh.adapter = -1;
+  __syncthreads();
+  for (int m0 = warp * 32; m0 < M; m0 += kThreads) {
+    const int id = m0 + lane < M ? ids[m0 + lane] : -1;
+    if (id >= n) atomicCAS(&g_lora_error, 0u, kOpsBadAdapter);
+    const unsigned same = __match_any_sync(0xffffffffu, id);
+    if (id >= 0 && id < n && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&counts[id], __popc(same));
   }
   __syncthreads();
-  for (int n = threadIdx.x; n < p.N; n += kThreads) {
-    float s = 0.0f;
-    for (int r = 0; r < p.rank; ++r) s = fmaf(t[r], load_elt<TYPE>(p.b, (static_cast<size_t>(id) * p.N + n) * p.rank + r), s);
-    p.y[static_cast<size_t>(m) * p.N + n] += s;
+  // jobs are numbered by adapter: a thread's adapters are neighbours
+  const int each = (n + kThreads - 1) / kThreads, i0 = tid * each, i1 = min(n, i0 + each);
+  int jobs = 0;
+  for (int i = i0; i < i1; ++i) jobs += (counts[i] + T - 1) / T;
+  int before = jobs;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  if (lane == 31) sh.sums[warp] = before;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) before += sh.sums[w];
+  before -= jobs;
+  if (j >= before && j < before + jobs) {
+    int i = i0;
+    for (; j >= before + (counts[i] + T - 1) / T; ++i) before += (counts[i] + T - 1) / T;
+    sh.adapter = i;
+    sh.chunk = j - before;
+  }
+  __syncthreads();
+  const int adapter = sh.adapter;
+  if (adapter < 0) return 0;
+  const int lo = sh.chunk * T, have = min(T, counts[adapter] - lo);
+  // each warp's rows, a run of them: how many before it, then their places
+  const int run = ((M + kThreads - 1) / kThreads) * 32, m1 = min(M, (warp + 1) * run);
+  int mine = 0;
+  for (int m = warp * run; m < m1; m += 32) mine += __popc(__ballot_sync(0xffffffffu, m + lane < M && ids[m + lane] == adapter));
+  if (lane == 0) sh.sums[warp] = mine;
+  __syncthreads();
+  int at = 0;
+  for (int w = 0; w < warp; ++w) at += sh.sums[w];
+  for (int m = warp * run; m < m1 && at < lo + have; m += 32) {
+    const bool is = m + lane < M && ids[m + lane] == adapter;
+    const unsigned all = __ballot_sync(0xffffffffu, is);
+    const int place = at + __popc(all & ((1u << lane) - 1u)) - lo;
+    if (is && place >= 0 && place < have) sh.rows[place] = m + lane;
+    at += __popc(all);
+  }
+  __syncthreads();
+  return have;
+}
+
+// Place of rank r among the pairs: a thread's ranks are 8, 4 or 2 neighbours (what it loads of B at once), of which step s of
+// a chunk takes two; the places of a step's four threads are neighbours.
+__device__ __forceinline__ int pair_place(int r, int rank) {
+  const int whole = rank & ~31, half = whole + (rank & 16);
+  const int c0 = r < whole ? r & ~31 : r < half ? whole : half;
+  const int per = r < whole ? 8 : r < half ? 4 : 2, i = r - c0, t = i / per, q = i - t * per;
+  return c0 + (q >> 1) * 8 + t * 2 + (q & 1);
+}
+
+// The products of W * 4 ranks from r0 on: t (pairs) x B of 32 columns.
+template <int TYPE, int MT, int W>
+__device__ __forceinline__ void expand(float (&acc)[MT][4][4], const AdapterProj& p, size_t b_row, const int (&col)[4], int r0,
+                                       const uint8_t* pairs, int stride, int tiles) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  Weights<TYPE, W> w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j].load(p.b, (b_row + col[j]) * p.rank + r0 + t * W, col[j] < p.N);
+#pragma unroll
+  for (int s = 0; s < W / 2; ++s) {
+    uint32_t bhi[4][2], blo[4][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j].get(2 * s, bhi[j], blo[j]);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      if (mt < tiles) {
+        const uint8_t* const from = pairs + (mt * 16 + g) * stride + (r0 + 8 * s + 2 * t) * 8;
+        const uint4 a = *reinterpret_cast<const uint4*>(from), b = *reinterpret_cast<const uint4*>(from + 8 * stride);
+        const uint32_t hi[4] = {a.x, b.x, a.z, b.z}, lo[4] = {a.y, b.y, a.w, b.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) product<TYPE>(acc[mt][j], hi, lo, bhi[j], blo[j]);
+      }
+    }
   }
 }
 
-__global__ void __launch_bounds__(kThreads) lora_kernel(const __grid_constant__ LoraArgs A) {
-  __shared__ float t[256];
-  const AdapterProj& p = A.p[blockIdx.y];
-  const int m = blockIdx.x, id = A.ids[m];
-  if (id < 0) return;
-  if (id >= p.n) {
-    if (threadIdx.x == 0) atomicCAS(&g_lora_error, 0u, kOpsBadAdapter);
-    return;
+template <int TYPE, int MT>
+__global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant__ LoraArgs A, const LoraGrid G) {
+  constexpr int T = 16 * MT, kSplit = kWarps / MT;  // warps that share out a CTA's part of K
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ JobShared sh;
+  const AdapterProj& p = A.p[G.first + blockIdx.y];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int cta = blockIdx.x % kCluster;
+  float* const part = reinterpret_cast<float*>(smem);
+  uint8_t* const rest = smem + part_bytes(T, G.rank_most);
+  const int rank = p.rank, K = p.K, N = p.N;
+  for (int job = blockIdx.x / kCluster; job < G.jobs; job += gridDim.x / kCluster) {
+    const int have = find_job(A.ids, A.M, p.n, T, job, reinterpret_cast<int*>(rest), sh);
+    if (have == 0) return;  // nor are there later ones; so for all of the cluster
+    const int id = sh.adapter, tiles = (have + 15) / 16;
+    // ---- t's part from this CTA's K: warp (mt, ks) has 16 rows and a share of the 32-element chunks
+    const int chunks = K / 32, mt = warp % MT, ks = warp / MT;
+    const int c0 = chunks * cta / kCluster, c1 = chunks * (cta + 1) / kCluster;
+    const int k0 = c0 + (c1 - c0) * ks / kSplit, k1 = c0 + (c1 - c0) * (ks + 1) / kSplit;
+    const bool row0 = mt * 16 + g < have, row1 = mt * 16 + g + 8 < have;
+    const float* const x0 = p.x + static_cast<size_t>(row0 ? sh.rows[mt * 16 + g] : 0) * K + t * 8;
+    const float* const x1 = p.x + static_cast<size_t>(row1 ? sh.rows[mt * 16 + g + 8] : 0) * K + t * 8;
+    float* const sums = reinterpret_cast<float*>(rest);  // [kSplit][T][kRankBlock]
+    for (int rb = 0; rb < rank; rb += kRankBlock) {
+      const int nt = min(kRankBlock, rank - rb) / 8;
+      float acc[kRankBlock / 8][4];
+#pragma unroll
+      for (int n = 0; n < kRankBlock / 8; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+      if (mt < tiles) {
+        const size_t a0 = (static_cast<size_t>(id) * rank + rb + g) * K + t * 8;
+        for (int c = k0; c < k1; ++c) {
+          float xs[2][8];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float4* const f = reinterpret_cast<const float4*>((i ? x1 : x0) + c * 32);
+            const bool there = i ? row1 : row0;
+            const float4 u = there ? f[0] : make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = there ? f[1] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            xs[i][0] = u.x, xs[i][1] = u.y, xs[i][2] = u.z, xs[i][3] = u.w, xs[i][4] = v.x, xs[i][5] = v.y, xs[i][6] = v.z, xs[i][7] = v.w;
+          }
+          uint32_t hi[4][4], lo[4][4];
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            split(xs[0][2 * s], &hi[s][0], &lo[s][0]);
+            split(xs[1][2 * s], &hi[s][1], &lo[s][1]);
+            split(xs[0][2 * s + 1], &hi[s][2], &lo[s][2]);
+            split(xs[1][2 * s + 1], &hi[s][3], &lo[s][3]);
+          }
+#pragma unroll
+          for (int n = 0; n < kRankBlock / 8; ++n) {
+            if (n < nt) {
+              Weights<TYPE, 8> w;
+              w.load(p.a, a0 + static_cast<size_t>(n * 8) * K + c * 32, true);
+              float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+              for (int s = 0; s < 4; ++s) {
+                uint32_t bhi[2], blo[2];
+                w.get(2 * s, bhi, blo);
+                product<TYPE>(d, hi[s], lo[s], bhi, blo);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[n][i] += d[i];
+            }
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < kRankBlock / 8; ++n) {
+          if (n < nt) {
+            float* const to = sums + (ks * T + mt * 16 + g) * kRankBlock + n * 8 + 2 * t;
+            *reinterpret_cast<float2*>(to) = make_float2(acc[n][0], acc[n][1]);
+            *reinterpret_cast<float2*>(to + 8 * kRankBlock) = make_float2(acc[n][2], acc[n][3]);
+          }
+        }
+      }
+      __syncthreads();
+      // the warps' shares together: [tiles * 16][nt * 8], four at a time
+      for (int i = tid; i < tiles * 16 * nt * 2; i += kThreads) {
+        const int row = i / (nt * 2), r = (i - row * nt * 2) * 4;
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kSplit; ++w) {
+          const float4 v = *reinterpret_cast<const float4*>(sums + (w * T + row) * kRankBlock + r);
+          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        *reinterpret_cast<float4*>(part + row * rank + rb + r) = s;
+      }
+      __syncthreads();
+    }
+    cluster_sync();
+    // ---- t: the parts of all CTAs in order, each CTA an eighth of it, which it hands to all
+    const float scale = p.scales ? p.scales[id] : 1.0f;
+    const int quads = tiles * 4 * rank, stride = pair_stride(rank);  // groups of four ranks
+    for (int i = cta * kThreads + tid; i < quads; i += kCluster * kThreads) {
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int c = 0; c < kCluster; ++c) {
+        const float4 v = peer_load4(peer(smem_at(part + i * 4), c));
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      }
+      s.x *= scale, s.y *= scale, s.z *= scale, s.w *= scale;
+      const int row = i / (rank / 4), r = (i - row * (rank / 4)) * 4;
+      uint32_t h[4], l[4];
+      split(s.x, &h[0], &l[0]);
+      split(s.y, &h[1], &l[1]);
+      split(s.z, &h[2], &l[2]);
+      split(s.w, &h[3], &l[3]);
+      // ranks 2k and 2k + 1 keep neighbouring places
+      const uint32_t to0 = smem_at(rest + row * stride + pair_place(r, rank) * 8), to1 = smem_at(rest + row * stride + pair_place(r + 2, rank) * 8);
+#pragma unroll
+      for (int c = 0; c < kCluster; ++c) {
+        peer_store4(peer(to0, c), make_float4(__uint_as_float(h[0]), __uint_as_float(l[0]), __uint_as_float(h[1]), __uint_as_float(l[1])));
+        peer_store4(peer(to1, c), make_float4(__uint_as_float(h[2]), __uint_as_float(l[2]), __uint_as_float(h[3]), __uint_as_float(l[3])));
+      }
+    }
+    cluster_sync();
+    // ---- y: a warp has 32 columns; a lane's are 8 neighbours (two of each of four products)
+    const size_t b_row = static_cast<size_t>(id) * N;
+    const bool wide = N % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
+    for (int n0 = (cta * kWarps + warp) * 32; n0 < N; n0 += kCluster * kWarps * 32) {
+      int col[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) col[j] = n0 + (g >> 1) * 8 + 2 * j + (g & 1);
+      float acc[MT][4][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.0f;
+      int r0 = 0;
+      for (; r0 + 32 <= rank; r0 += 32) expand<TYPE, MT, 8>(acc, p, b_row, col, r0, rest, stride, tiles);
+      if (rank & 16) expand<TYPE, MT, 4>(acc, p, b_row, col, r0, rest, stride, tiles), r0 += 16;
+      if (rank & 8) expand<TYPE, MT, 2>(acc, p, b_row, col, r0, rest, stride, tiles);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int place = m * 16 + h * 8 + g, n = n0 + t * 8;
+          if (place >= have) continue;
+          const int row = sh.rows[place];
+          if (!XQ_IN(row, A.M, kChkLoraRow)) continue;
+          float* const y = p.y + static_cast<size_t>(row) * N + n;
+          if (wide && n + 8 <= N) {
+            float4 u = reinterpret_cast<float4*>(y)[0], v = reinterpret_cast<float4*>(y)[1];
+            u.x += acc[m][0][2 * h], u.y += acc[m][0][2 * h + 1], u.z += acc[m][1][2 * h], u.w += acc[m][1][2 * h + 1];
+            v.x += acc[m][2][2 * h], v.y += acc[m][2][2 * h + 1], v.z += acc[m][3][2 * h], v.w += acc[m][3][2 * h + 1];
+            reinterpret_cast<float4*>(y)[0] = u;
+            reinterpret_cast<float4*>(y)[1] = v;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (n + 2 * j + i < N) y[2 * j + i] += acc[m][j][2 * h + i];
+          }
+        }
+      }
+    }
+    __syncthreads();  // of t and the rows, before the next job's
   }
-  if (p.type == kF32)
-    row<kF32>(p, m, id, t);
-  else if (p.type == kF16)
-    row<kF16>(p, m, id, t);
-  else
-    row<kBF16>(p, m, id, t);
+}
+
+template <int TYPE, int MT>
+cudaError_t launch(const LoraArgs& a, const LoraGrid& g, int n_proj, int n_most, cudaStream_t s) {
+  const int bytes = shared_bytes(16 * MT, g.rank_most, n_most);
+  static std::atomic<unsigned long long> allowed{0};
+  const cudaError_t e = allow_shared(lora_kernel<TYPE, MT>, 200 * 1024, allowed);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCluster * std::min(g.jobs, kJobsGrid), n_proj);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = kCluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, lora_kernel<TYPE, MT>, a, g);
 }
 
 }  // namespace
 
-cudaError_t launch_lora(const LoraArgs& a, cudaStream_t s) {
+cudaError_t launch_lora(const LoraArgs& args, cudaStream_t s) {
   g_kv_launched.store(true, std::memory_order_relaxed);
-  lora_kernel<<<dim3(a.M, a.n_proj), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  // projections of one type together
+  LoraArgs a = args;
+  for (int i = 1; i < a.n_proj; ++i)
+    for (int k = i; k > 0 && a.p[k].type < a.p[k - 1].type; --k) std::swap(a.p[k], a.p[k - 1]);
+  for (int i = 0; i < a.n_proj;) {
+    LoraGrid g = {};
+    int e = i, n_most = 0;
+    g.first = i;
+    for (; e < a.n_proj && a.p[e].type == a.p[i].type; ++e) {
+      g.rank_most = std::max(g.rank_most, a.p[e].rank);
+      n_most = std::max(n_most, a.p[e].n);
+    }
+    const int MT = static_cast<long long>(a.M) * (e - i) <= 16 * 38 ? 1 : g.rank_most > 128 ? 2 : 4;
+    g.rows = 16 * MT;
+    g.jobs = std::max(1, std::min(a.M, n_most) + a.M / g.rows);
+    cudaError_t r;
+    auto by_rows = [&](auto type) {
+      constexpr int TYPE = decltype(type)::value;
+      return MT == 1 ? launch<TYPE, 1>(a, g, e - i, n_most, s) : MT == 2 ? launch<TYPE, 2>(a, g, e - i, n_most, s) : launch<TYPE, 4>(a, g, e - i, n_most, s);
+    };
+    if (a.p[i].type == kF32)
+      r = by_rows(std::integral_constant<int, kF32>());
+    else if (a.p[i].type == kF16)
+      r = by_rows(std::integral_constant<int, kF16>());
+    else
+      r = by_rows(std::integral_constant<int, kBF16>());
+    if (r != cudaSuccess) return r;
+    i = e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t take_lora_error(unsigned int* code) { return take_record(g_lora_error, code); }

@@ -85,6 +85,7 @@ enum CheckSite : unsigned {
   // qk_rope.cu
   kChkRope = 60,     // 8 elements inside a row of a token of the call
   // prompt_tile.cuh
+  kChkLoraRow = 62,    // row of y inside [M]
   kChkPromptRow = 61,  // row of the result inside [tokens][heads]
 };
 

@@ -737,8 +737,8 @@ class Adapters:
                 raise ValueError(f"scales: contiguous float32 [{n}], on {self.device}")
             if rank % 8 or not 8 <= rank <= 256 or K % 32 or K == 0:
                 raise ValueError(f"rank a multiple of 8 up to 256 and K a multiple of 32 expected, got {rank} and {K}")
-            if inp < 0:
-                raise ValueError("an input's index is not negative")
+            if inp < 0 or n > 8192:
+                raise ValueError("an input's index is not negative, and there are at most 8192 adapters")
             e.type, e.n, e.rank, e.K, e.N, e.input = _float_type(a.dtype), n, rank, K, b.shape[1], inp
             e.a, e.b, e.scales = a.data_ptr(), b.data_ptr(), None if scales is None else scales.data_ptr()
             self._keep.append((a, b, scales))

@@ -28,7 +28,7 @@ def lora(xq, n_proj=1, n_inputs=1, M=1, ids=FAKE, x=FAKE, **kw):
     (dict(type=8), 1), (dict(type=2), 1), (dict(input=1), 1), (dict(input=-1), 1), (dict(n_proj=17), 1), (dict(n_proj=-1), 1),
     (dict(n_inputs=65), 1), (dict(n_inputs=-1), 1), (dict(n_inputs=0), 1), (dict(x=None), 1), (dict(a=None), 1), (dict(b=None), 1), (dict(y=None), 1),
     (dict(ids=None), 1), (dict(rank=0), 2), (dict(rank=12), 2), (dict(rank=264), 2), (dict(K=0), 2), (dict(K=40), 2), (dict(K=-32), 2),
-    (dict(N=-1), 2), (dict(n=-1), 2), (dict(M=-1), 2), (dict(a=FAKE + 8), 3), (dict(b=FAKE + 2), 3), (dict(x=FAKE + 4), 3), (dict(y=FAKE + 2), 3),
+    (dict(N=-1), 2), (dict(n=-1), 2), (dict(n=8193), 2), (dict(M=-1), 2), (dict(a=FAKE + 8), 3), (dict(b=FAKE + 2), 3), (dict(x=FAKE + 4), 3), (dict(y=FAKE + 2), 3),
     (dict(scales=FAKE + 1), 3), (dict(ids=FAKE + 2), 3), (dict(M=0, ids=None), 0), (dict(N=0, y=None), 0), (dict(n_proj=0), 0)])
 def test_adapters(xq, kw, code):
     assert lora(xq, **kw) == code
