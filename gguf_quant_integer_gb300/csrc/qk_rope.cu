@@ -6,7 +6,7 @@
 // 2^-64 of a full turn: an integer product whose overflow drops whole turns, so
 // it is exact at any position (position * frequency in fp32 is off by 0.004
 // at 131071). What is left after the nearest quarter turn is at most an eighth
-// of a turn and enters sincospi with 2^-33.
+// of a turn, known to 2^-34 of one.
 //
 // A lane has 8 elements of a row, so a row of 64, 128 or 256 takes 8, 16 or 32
 // lanes (96: 12 of 16) and its sum 3 to 5 shuffles; a warp takes several heads
@@ -18,7 +18,7 @@
 namespace xq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kRowsAhead = 4;  // rows a lane group loads before it works on them
 
 // 8 elements from p + at; wide: a 16-byte boundary.
@@ -77,99 +77,146 @@ __device__ __forceinline__ void store8(void* p, size_t at, bool wide, const floa
   for (int i = 0; i < 8; ++i) store_elt<TYPE>(p, at + i, x[i]);
 }
 
+// Cosine and sine of a phase, 2^-64 of a full turn: the nearest quarter turn, and an angle of at most pi / 4 beside it by the
+// power series (the first terms left out are 2e-9 and 2e-9 of 1).
 __device__ __forceinline__ void cos_sin(uint64_t phase, float* c, float* s) {
   const uint64_t quarter = (phase + (1ull << 61)) >> 62;
-  const int rest = static_cast<int>(static_cast<int64_t>(phase - (quarter << 62)) >> 30);  // -2^31 .. 2^31 - 1: an eighth
-  float sn, cn;
-  sincospif(static_cast<float>(rest) * 1.16415321826934814453125e-10f, &sn, &cn);  // 2^-33 half turns
-  *c = quarter == 0 ? cn : quarter == 1 ? -sn : quarter == 2 ? -cn : sn;
-  *s = quarter == 0 ? sn : quarter == 1 ? cn : quarter == 2 ? -sn : -cn;
+  const int rest = static_cast<int>(static_cast<int64_t>(phase - (quarter << 62)) >> 30);  // in 2^-34 of a turn
+  const float x = static_cast<float>(rest) * 3.657295198e-10f, x2 = x * x;                   // 2 pi 2^-34
+  float sn = fmaf(x2, 2.7557319e-6f, -1.9841270e-4f);  // 1/9!, 1/7!
+  sn = fmaf(sn, x2, 8.3333333e-3f);
+  sn = fmaf(sn, x2, -0.16666667f);
+  sn = fmaf(sn * x2, x, x);
+  float cn = fmaf(x2, -2.7557319e-7f, 2.4801587e-5f);  // 1/10!, 1/8!
+  cn = fmaf(cn, x2, -1.3888889e-3f);
+  cn = fmaf(cn, x2, 4.1666667e-2f);
+  cn = fmaf(cn, x2, -0.5f);
+  cn = fmaf(cn, x2, 1.0f);
+  const float a = quarter & 1 ? sn : cn, b = quarter & 1 ? cn : sn;
+  *c = (quarter + 1) & 2 ? -a : a;
+  *s = quarter & 2 ? -b : b;
 }
 
 struct RopeGrid {
   int span;         // row groups a warp takes
-  int warps_token;
+  int warps_token;  // 1, 2, 4 or a multiple of the warps of a block
+  int tokens_block;
   bool wide_x, wide_y;
 };
 
 // W: lanes a row.
 template <int XT, int YT, int W>
-__global__ void __launch_bounds__(kThreads) qk_rope_kernel(const __grid_constant__ RopeArgs A, const RopeGrid G) {
+__global__ void __launch_bounds__(kThreads, 3) qk_rope_kernel(const __grid_constant__ RopeArgs A, const RopeGrid G) {
   constexpr int kGroups = 32 / W;
+  __shared__ __align__(16) float sh_cos[kWarps][128], sh_sin[kWarps][128];  // of the block's tokens
   const int lane = threadIdx.x & 31, li = lane & (W - 1), group = lane / W;
-  const long long warp = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const long long token = warp / G.warps_token;
-  if (token >= A.tokens) return;
-  const int heads = A.side[0].heads, rows = heads + A.side[1].heads;
-  const int first = static_cast<int>(warp - token * G.warps_token) * G.span;  // row group
+  const long long warp = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const long long token = warp / G.warps_token, token0 = static_cast<long long>(blockIdx.x) * kWarps / G.warps_token;
+  // row groups: q's, then k's
+  const int groups_q = (A.side[0].heads + kGroups - 1) / kGroups, groups = groups_q + (A.side[1].heads + kGroups - 1) / kGroups;
+  int next = static_cast<int>(warp - token * G.warps_token) * G.span;
+  const int end = min(next + G.span, groups);
   const int e0 = 8 * li, half = A.rot / 2;
-  const bool in = e0 < A.dim, turns = e0 < A.rot;
-  // the 8 elements' cosines and sines, these negated for a pair's first element; the lane that has their partners
-  float cs[8], sn[8];
-  int from = lane;
-  if (turns) {
-    const uint64_t position = static_cast<uint64_t>(A.positions[token]);
-    if (A.pairs) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float c, s;
-        cos_sin(position * A.turns[e0 / 2 + i], &c, &s);
-        cs[2 * i] = cs[2 * i + 1] = c * A.magnitude;
-        sn[2 * i + 1] = s * A.magnitude;
-        sn[2 * i] = -sn[2 * i + 1];
-      }
-    } else {
-      const bool high = e0 >= half;
-      from = high ? lane - half / 8 : lane + half / 8;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float c, s;
-        cos_sin(position * A.turns[(high ? e0 - half : e0) + i], &c, &s);
-        cs[i] = c * A.magnitude;
-        sn[i] = (high ? s : -s) * A.magnitude;
-      }
-    }
-  }
-  for (int b = 0; b < G.span; b += kRowsAhead) {
-    float x[kRowsAhead][8];
+  const bool in = e0 < A.dim && token < A.tokens, turns = e0 < A.rot;
+  float x[kRowsAhead][8];
+  // rows of one side from row group `first` on; `n` of them at most
+  auto load = [&](const RopeSide& side, int first, int n) {
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
-      const int row = (first + b + u) * kGroups + group;
-      const bool there = in && b + u < G.span && row < rows;
-      const RopeSide& side = A.side[row < heads ? 0 : 1];
-      const size_t at = static_cast<size_t>(token) * side.x_stride + static_cast<size_t>(row < heads ? row : row - heads) * A.dim + e0;
-      if (there && XQ_CHECKED(token < A.tokens && e0 + 8 <= A.dim, kChkRope))
-        load8<XT>(side.x, at, G.wide_x, x[u]);
+      const int row = (first + u) * kGroups + group;
+      if (in && u < n && row < side.heads && XQ_CHECKED(token < A.tokens && e0 + 8 <= A.dim, kChkRope))
+        load8<XT>(side.x, static_cast<size_t>(token) * side.x_stride + static_cast<size_t>(row) * A.dim + e0, G.wide_x, x[u]);
       else
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[u][i] = 0.0f;
     }
-#pragma unroll
-    for (int u = 0; u < kRowsAhead; ++u) {
-      if (b + u >= G.span) break;
-      const int row = (first + b + u) * kGroups + group;
-      const RopeSide& side = A.side[row < heads ? 0 : 1];
-      float ss = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(x[u][i], x[u][i], ss);
-#pragma unroll
-      for (int o = W / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (side.weight && in) {
-        const float inv = 1.0f / sqrtf(ss / static_cast<float>(A.dim) + A.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[u][i] = x[u][i] * inv * side.weight[e0 + i];
-      }
-      float y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float near = x[u][i ^ 1];
-        const float other = __shfl_sync(0xffffffffu, x[u][i], from);
-        y[i] = turns ? fmaf(x[u][i], cs[i], (A.pairs ? near : other) * sn[i]) : x[u][i];
-      }
-      if (in && row < rows)
-        store8<YT>(side.y, static_cast<size_t>(token) * side.y_stride + static_cast<size_t>(row < heads ? row : row - heads) * A.dim + e0,
-                   G.wide_y, y);
+  };
+  // the first rows are on their way while the angles are worked out
+  if (next < groups_q)
+    load(A.side[0], next, min(end, groups_q) - next);
+  else
+    load(A.side[1], next - groups_q, end - next);
+  for (int i = threadIdx.x; i < G.tokens_block * half; i += kThreads) {
+    const int t = i / half, pair = i - t * half;
+    if (token0 + t < A.tokens) {
+      float c, s;
+      cos_sin(static_cast<uint64_t>(A.positions[token0 + t]) * A.turns[pair], &c, &s);
+      sh_cos[t][pair] = c * A.magnitude;
+      sh_sin[t][pair] = s * A.magnitude;
     }
+  }
+  __syncthreads();
+  if (token >= A.tokens) return;
+  bool loaded = true;
+#pragma unroll 1
+  for (int z = 0; z < 2; ++z) {
+    const RopeSide& side = A.side[z];
+    const int before = z ? groups_q : 0, stop = z ? end : min(end, groups_q);
+    if (next >= stop) continue;
+    // y = inv * (x * near + (its partner's x) * other), weights in the factors: w cos, and the partner's w times sin, negated
+    // for a pair's first element; the lane that has the partners
+    float near[8], other[8];
+    int from = lane;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) near[i] = side.weight && in ? side.weight[e0 + i] : 1.0f;
+    if (turns && in) {
+      const float *const c = sh_cos[token - token0], *const s = sh_sin[token - token0];
+      if (A.pairs) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const float cn = c[(e0 + i) / 2], sn = s[(e0 + i) / 2], w0 = near[i], w1 = near[i + 1];
+          other[i] = -(w1 * sn), other[i + 1] = w0 * sn;
+          near[i] = w0 * cn, near[i + 1] = w1 * cn;
+        }
+      } else {
+        const bool high = e0 >= half;
+        from = high ? lane - half / 8 : lane + half / 8;
+        const int at = high ? e0 - half : e0, partner = high ? at : e0 + half;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float sn = side.weight ? side.weight[partner + i] * s[at + i] : s[at + i];
+          other[i] = high ? sn : -sn;
+          near[i] *= c[at + i];
+        }
+      }
+    }
+    const float over_dim = 1.0f / static_cast<float>(A.dim);
+    for (; next < stop; next += kRowsAhead) {
+      if (!loaded) load(side, next - before, stop - next);
+      loaded = false;
+#pragma unroll
+      for (int u = 0; u < kRowsAhead; ++u) {
+        if (next + u >= stop) break;
+        const int row = (next - before + u) * kGroups + group;
+        float inv = 1.0f;
+        if (side.weight) {
+          float ss = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ss = fmaf(x[u][i], x[u][i], ss);
+#pragma unroll
+          for (int o = W / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          inv = rsqrtf(fmaf(ss, over_dim, A.eps));
+        }
+        float y[8];
+        if (A.pairs) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = turns ? fmaf(x[u][i], near[i], x[u][i ^ 1] * other[i]) : x[u][i] * near[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float partner = __shfl_sync(0xffffffffu, x[u][i], from);
+            y[i] = turns ? fmaf(x[u][i], near[i], partner * other[i]) : x[u][i] * near[i];
+          }
+        }
+        if (side.weight) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] *= inv;
+        }
+        if (in && row < side.heads)
+          store8<YT>(side.y, static_cast<size_t>(token) * side.y_stride + static_cast<size_t>(row) * A.dim + e0, G.wide_y, y);
+      }
+    }
+    next = stop;
   }
 }
 
@@ -180,15 +227,22 @@ bool on16(const void* p, long long stride, int bytes, bool one) {
 template <int XT, int YT>
 cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
   const int lanes = a.dim <= 64 ? 8 : a.dim <= 128 ? 16 : 32, groups = 32 / lanes;
-  const int row_groups = (a.side[0].heads + a.side[1].heads + groups - 1) / groups;
+  const int row_groups = (a.side[0].heads + groups - 1) / groups + (a.side[1].heads + groups - 1) / groups;
   RopeGrid g;
-  g.span = 1;
-  g.warps_token = (row_groups + g.span - 1) / g.span;
+  // warps a token: one takes all its rows where that fills the device (three blocks an SM); few tokens are shared out. Measured
+  // with 1, 2, 4, 8, 16, 24: 16383 tokens of 32 + 8 heads 90, 94, 114, 165, 208, 278 us, 257 tokens of 12 + 2 heads 5.3,
+  // 3.8, 2.9, 2.9, 4.2, 4.8, one token of 32 + 8 heads 9.4, 6.0, 4.5, 4.1, 3.2, 3.0.
+  const long long enough = 152 * 3 * kWarps;
+  g.warps_token = 1;
+  while (g.warps_token < row_groups && static_cast<long long>(g.warps_token) * a.tokens < enough)
+    g.warps_token = g.warps_token < kWarps ? 2 * g.warps_token : g.warps_token + kWarps;
+  g.span = (row_groups + g.warps_token - 1) / g.warps_token;
+  g.tokens_block = g.warps_token < kWarps ? kWarps / g.warps_token : 1;
   const int xb = kv_elt_bytes(a.type), yb = kv_elt_bytes(a.y_type);
   g.wide_x = on16(a.side[0].x, a.side[0].x_stride, xb, a.tokens == 1) && on16(a.side[1].x, a.side[1].x_stride, xb, a.tokens == 1);
   g.wide_y = on16(a.side[0].y, a.side[0].y_stride, yb, a.tokens == 1) && on16(a.side[1].y, a.side[1].y_stride, yb, a.tokens == 1);
   const long long warps = static_cast<long long>(a.tokens) * g.warps_token;
-  const unsigned blocks = static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32));
+  const unsigned blocks = static_cast<unsigned>((warps + kWarps - 1) / kWarps);
   if (lanes == 8)
     qk_rope_kernel<XT, YT, 8><<<blocks, kThreads, 0, s>>>(a, g);
   else if (lanes == 16)
