@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 from . import synth
 
@@ -156,11 +157,12 @@ def lib(path: str | None = None):
         getattr(L, fn).argtypes = [C, Q, P, S, P]
     for fn in ("xq_kv_write", "xq_kv_read", "xq_kv_attn", "xq_kv_attn_shared"):
         getattr(L, fn).restype = I
-    L.xq_lora_add.argtypes = [ctypes.POINTER(xq_adapters), I, ctypes.POINTER(P), I, I, P, P]
-    L.xq_qk_norm_rope.argtypes = [ctypes.POINTER(xq_qk_rows), P]
-    L.xq_prompt_attn_workspace_bytes.argtypes = [ctypes.POINTER(xq_prompts)]
+    # structures as bytes, or by reference
+    L.xq_lora_add.argtypes = [P, I, P, I, I, P, P]
+    L.xq_qk_norm_rope.argtypes = [P, P]
+    L.xq_prompt_attn_workspace_bytes.argtypes = [P]
     L.xq_prompt_attn_workspace_bytes.restype = S
-    L.xq_prompt_attn.argtypes = [ctypes.POINTER(xq_prompts), P, S, P]
+    L.xq_prompt_attn.argtypes = [P, P, S, P]
     for fn in ("xq_lora_add", "xq_qk_norm_rope", "xq_prompt_attn"):
         getattr(L, fn).restype = I
     for fn in ("xq_quantize_q8", "xq_matmul_q4k_q8", "xq_matmul_q6k_q8", "xq_debug_isums_q4k",
@@ -679,7 +681,7 @@ _torch_calls = None
 
 
 def _calls():
-    """(device, stream handle, capturing) accessors of torch: the bare handle's costs a fortieth of building a Stream object."""
+    """(torch, current device, raw stream of a device) accessors: the bare handle's costs a fortieth of building a Stream object."""
     global _torch_calls
     if _torch_calls is None:
         import torch
@@ -690,25 +692,30 @@ def _calls():
 
 
 def _handle(device, stream):
-    """The stream's handle. Kernels go to the current device, whatever device the pointers are of."""
-    _, current, raw = _calls()
-    if device.type != "cuda" or current() != device.index:
-        raise ValueError(f"the tensors are on {device}: CUDA tensors on the current device expected (torch.cuda.device)")
+    """The stream's handle, for tensors on CUDA device number `device` (get_device; -1: none). Kernels go to the current device,
+    whatever device the pointers are of."""
+    _, current, raw = _torch_calls or _calls()
+    if device < 0 or current() != device:
+        raise ValueError("CUDA tensors on the current device expected (torch.cuda.device)")
     if stream is None:
-        return raw(device.index)
+        return raw(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _other_stream(device, stream):
     """Context that makes `stream` the current one, for a call that makes memory: the allocator hands a stream's freed memory
     to the same stream without waiting, so it has to be the stream that writes it. None if it is the current one."""
-    if stream is None:
-        return None
     handle = _handle(device, stream)
     if handle == _handle(device, None):
         return None
     cuda = _calls()[0].cuda
     return cuda.stream(cuda.ExternalStream(handle, device=device) if isinstance(stream, int) else stream)
+
+
+# Structures of the C ABI as bytes: packing them costs a third of filling ctypes fields.
+_ADAPTERS = "iiiii4xPPPPi4x"
+_pack_rows = struct.Struct("@iiiiiiPPqqPPqqPPf4xPPiif4x").pack
+_pack_prompts = struct.Struct("@iiiiiiPPPqqqPPfi").pack
 
 
 class Adapters:
@@ -723,50 +730,50 @@ class Adapters:
         torch = _calls()[0]
         if not 1 <= len(projs) <= 16:
             raise ValueError("1 to 16 projections a call")
-        self.device = projs[0][0].device
-        self._keep, self._shapes = [], []
-        arr = (xq_adapters * len(projs))()
-        for e, (a, b, scales, inp) in zip(arr, projs):
+        self._device = dev = projs[0][0].get_device()
+        self._keep, self._shapes, self._args = [], [], []
+        for a, b, scales, inp in projs:
             if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2] or a.dtype != b.dtype:
                 raise ValueError("a: [n, rank, K], b: [n, N, rank], of one dtype")
-            if not a.is_contiguous() or not b.is_contiguous() or a.device != self.device or b.device != self.device:
-                raise ValueError(f"a and b have to be contiguous, on {self.device}")
+            if not a.is_contiguous() or not b.is_contiguous() or dev < 0 or a.get_device() != dev or b.get_device() != dev:
+                raise ValueError("a and b have to be contiguous, on one CUDA device")
             n, rank, K = a.shape
             if scales is not None and (scales.dtype != torch.float32 or scales.shape != (n,) or not scales.is_contiguous()
-                                       or scales.device != self.device):
-                raise ValueError(f"scales: contiguous float32 [{n}], on {self.device}")
+                                       or scales.get_device() != dev):
+                raise ValueError(f"scales: contiguous float32 [{n}], on the adapters' device")
             if rank % 8 or not 8 <= rank <= 256 or K % 32 or K == 0:
                 raise ValueError(f"rank a multiple of 8 up to 256 and K a multiple of 32 expected, got {rank} and {K}")
-            if inp < 0 or n > 8192:
-                raise ValueError("an input's index is not negative, and there are at most 8192 adapters")
-            e.type, e.n, e.rank, e.K, e.N, e.input = _float_type(a.dtype), n, rank, K, b.shape[1], inp
-            e.a, e.b, e.scales = a.data_ptr(), b.data_ptr(), None if scales is None else scales.data_ptr()
+            if not 0 <= inp < 64 or n > 8192:
+                raise ValueError("an input's index is 0 to 63, and there are at most 8192 adapters")
+            self._args += [_float_type(a.dtype), n, rank, K, b.shape[1], a.data_ptr(), b.data_ptr(),
+                           0 if scales is None else scales.data_ptr(), 0, inp]
             self._keep.append((a, b, scales))
-            self._shapes.append((K, b.shape[1], inp))
-        self._type, self._fixed = type(arr), bytes(arr)
+            self._shapes.append(((b.shape[1],), (K,), inp))
+        self._pack = struct.Struct("@" + _ADAPTERS * len(projs)).pack
+        self._n_inputs = 1 + max(p[3] for p in projs)
+        self._pack_inputs = struct.Struct(f"@{self._n_inputs}P").pack
         self._add = lib().xq_lora_add
         self._float32, self._int32 = torch.float32, torch.int32
 
     def add(self, inputs, ys, ids, stream=None):
         """Add to each row of the projections' outputs ys (fp32 [M, N] each) what the adapter that ids int32 [M] names gives
         for the row of its input (fp32 [M, K]); rows of a negative id are left as they are. Returns ys."""
-        dev, M = self.device, ids.shape[0]
-        if ids.dtype != self._int32 or ids.dim() != 1 or not ids.is_contiguous() or ids.device != dev:
-            raise ValueError(f"ids: contiguous int32 [M], on {dev}")
-        if len(ys) != len(self._shapes):
-            raise ValueError(f"{len(self._shapes)} outputs expected, got {len(ys)}")
-        arr = self._type.from_buffer_copy(self._fixed)  # a call's own: calls may run side by side
-        ins = (ctypes.c_void_p * max(1, len(inputs)))()
-        for e, y, (K, N, inp) in zip(arr, ys, self._shapes):
-            if inp >= len(inputs):
-                raise ValueError(f"input {inp} is missing")
+        dev, f32, rows = self._device, self._float32, tuple(ids.shape)
+        if len(rows) != 1 or ids.dtype != self._int32 or not ids.is_contiguous() or ids.get_device() != dev:
+            raise ValueError("ids: contiguous int32 [M], on the adapters' device")
+        if len(ys) != len(self._shapes) or len(inputs) < self._n_inputs:
+            raise ValueError(f"{len(self._shapes)} outputs and {self._n_inputs} inputs expected, got {len(ys)} and {len(inputs)}")
+        args, ins, at = self._args.copy(), [0] * self._n_inputs, 8  # a call's own: calls may run side by side
+        for y, (N, K, inp) in zip(ys, self._shapes):
             x = inputs[inp]
-            if x.shape != (M, K) or x.dtype != self._float32 or not x.is_contiguous() or x.device != dev:
-                raise ValueError(f"input {inp}: contiguous float32 [{M}, {K}], on {dev}")
-            if y.shape != (M, N) or y.dtype != self._float32 or not y.is_contiguous() or y.device != dev:
-                raise ValueError(f"an output: contiguous float32 [{M}, {N}], on {dev}")
-            e.y, ins[inp] = y.data_ptr(), x.data_ptr()
-        rc = self._add(arr, len(ys), ins, len(inputs), M, ids.data_ptr(), _handle(dev, stream))
+            if x.shape != rows + K or x.dtype != f32 or not x.is_contiguous() or x.get_device() != dev:
+                raise ValueError(f"input {inp}: contiguous float32 {[*rows, *K]}, on the adapters' device")
+            if y.shape != rows + N or y.dtype != f32 or not y.is_contiguous() or y.get_device() != dev:
+                raise ValueError(f"an output: contiguous float32 {[*rows, *N]}, on the adapters' device")
+            args[at], ins[inp] = y.data_ptr(), x.data_ptr()
+            at += 10
+        rc = self._add(self._pack(*args), len(ys), self._pack_inputs(*ins), self._n_inputs, rows[0], ids.data_ptr(),
+                       _handle(dev, stream))
         if rc:
             raise XQError("xq_lora_add", rc)
         return ys
@@ -787,14 +794,23 @@ class Rope:
             factors = np.asarray(factors.cpu() if hasattr(factors, "cpu") else factors, dtype=np.float64)
             if factors.shape != freq.shape:
                 raise ValueError(f"{rot // 2} factors expected")
-            freq = freq / factors
+            with np.errstate(divide="ignore", invalid="ignore"):
+                freq = freq / factors
         turns = freq / (2 * np.pi)
         if not np.isfinite(turns).all():
             raise ValueError("base and factors have to give finite frequencies")
         turns = np.rint((turns - np.floor(turns)) * 2.0 ** 64)  # whole turns a position change nothing
         self.rot, self.pairs, self.magnitude = rot, bool(pairs), float(magnitude)
         self.turns = torch.tensor([(int(t) + (1 << 63)) % (1 << 64) - (1 << 63) for t in turns], dtype=torch.int64, device=device)
-        self._ptr = self.turns.data_ptr()
+        self._device, self._at = self.turns.get_device(), self.turns.data_ptr()
+
+
+def _rows_of(x, shape, dtype, device):
+    """The stride between tokens of x [tokens, heads, dim], each token's rows contiguous."""
+    st = x.stride()
+    if x.shape != shape or x.dtype != dtype or x.get_device() != device or st[2] != 1 or (st[1] != shape[2] and shape[1] > 1):
+        raise ValueError(f"{tuple(shape)} of {dtype} expected on the call's device, each token's rows contiguous")
+    return st[0]
 
 
 def qk_norm_rope(q, k, positions, rope, q_weight=None, k_weight=None, eps: float = 1e-6, dtype=None, q_out=None, k_out=None,
@@ -802,41 +818,47 @@ def qk_norm_rope(q, k, positions, rope, q_weight=None, k_weight=None, eps: float
     """Each head's row of q [tokens, heads, dim] and k [tokens, kv_heads, dim] normalized (x * weight / sqrt(mean(x^2) + eps);
     not without a weight) and rotated to its position (int64 [tokens]). A token's rows are contiguous; tokens may be parts of
     longer rows. Returns (q_out, k_out) of `dtype` (the inputs'); an output may be its input."""
+    dev = q.get_device()
     if stream is not None and (q_out is None or k_out is None):
-        on = _other_stream(q.device, stream)
+        on = _other_stream(dev, stream)
         if on:
             with on:
                 return qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, dtype, q_out, k_out)
-    torch, dev = _calls()[0], q.device
-    (T, H, D), ks = q.shape, k.shape
-    if len(ks) != 3 or ks[0] != T or ks[2] != D or k.dtype != q.dtype or k.device != dev:
-        raise ValueError("q: [tokens, heads, dim], k: [tokens, kv_heads, dim], of one dtype and device")
-    if positions.dtype != torch.int64 or positions.shape != (T,) or not positions.is_contiguous() or positions.device != dev:
-        raise ValueError(f"positions: contiguous int64 [{T}], on {dev}")
-    if dtype is None:
-        dtype = q.dtype if q_out is None else q_out.dtype
-    if q_out is None:
-        q_out = torch.empty((T, H, D), dtype=dtype, device=dev)
-    if k_out is None:
-        k_out = torch.empty(ks, dtype=dtype, device=dev)
-    row = (D, 1)
-    for x, shape, kind in ((q, q.shape, q.dtype), (k, ks, q.dtype), (q_out, q.shape, dtype), (k_out, ks, dtype)):
-        st = x.stride()
-        if x.shape != shape or x.dtype != kind or x.device != dev or (st[1:] != row and (shape[1] > 1 or st[2] != 1)):
-            raise ValueError(f"{tuple(shape)} of {kind} on {dev} expected, each token's rows contiguous")
+    torch, kind, qs, ks = _calls()[0], q.dtype, q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3 or ks[0] != qs[0] or ks[2] != qs[2]:
+        raise ValueError("q: [tokens, heads, dim], k: [tokens, kv_heads, dim]")
+    T, H, D = qs
+    q_stride, k_stride = _rows_of(q, qs, kind, dev), _rows_of(k, ks, kind, dev)
+    if positions.dtype != torch.int64 or positions.shape != (T,) or not positions.is_contiguous() or positions.get_device() != dev:
+        raise ValueError(f"positions: contiguous int64 [{T}], on the call's device")
     for w in (q_weight, k_weight):
-        if w is not None and (w.dtype != torch.float32 or w.shape != (D,) or not w.is_contiguous() or w.device != dev):
-            raise ValueError(f"weights: contiguous float32 [{D}], on {dev}")
-    if rope.turns.device != dev:
-        raise ValueError(f"the rotation's table has to be on {dev}")
-    rows = xq_qk_rows(_float_type(q.dtype), _float_type(dtype), T, H, ks[1], D, q.data_ptr(), k.data_ptr(), q.stride(0), k.stride(0),
-                      q_out.data_ptr(), k_out.data_ptr(), q_out.stride(0), k_out.stride(0),
-                      None if q_weight is None else q_weight.data_ptr(), None if k_weight is None else k_weight.data_ptr(), eps,
-                      positions.data_ptr(), rope._ptr, rope.rot, rope.pairs, rope.magnitude)
-    rc = lib().xq_qk_norm_rope(rows, _handle(dev, stream))
+        if w is not None and (w.dtype != torch.float32 or w.shape != (D,) or not w.is_contiguous() or w.get_device() != dev):
+            raise ValueError(f"weights: contiguous float32 [{D}], on the call's device")
+    if rope._device != dev:
+        raise ValueError("the rotation's table has to be on the call's device")
+    handle = _handle(dev, stream)
+    if dtype is None:
+        dtype = kind if q_out is None else q_out.dtype
+    y_type = _float_type(dtype)
+    if q_out is None:
+        q_out, q_out_stride = torch.empty(qs, dtype=dtype, device=q.device), H * D
+    else:
+        q_out_stride = _rows_of(q_out, qs, dtype, dev)
+    if k_out is None:
+        k_out, k_out_stride = torch.empty(ks, dtype=dtype, device=q.device), ks[1] * D
+    else:
+        k_out_stride = _rows_of(k_out, ks, dtype, dev)
+    rc = lib().xq_qk_norm_rope(
+        _pack_rows(_float_type(kind), y_type, T, H, ks[1], D, q.data_ptr(), k.data_ptr(), q_stride, k_stride, q_out.data_ptr(),
+                   k_out.data_ptr(), q_out_stride, k_out_stride, 0 if q_weight is None else q_weight.data_ptr(),
+                   0 if k_weight is None else k_weight.data_ptr(), eps, positions.data_ptr(), rope._at, rope.rot, rope.pairs,
+                   rope.magnitude), handle)
     if rc:
         raise XQError("xq_qk_norm_rope", rc)
     return q_out, k_out
+
+
+_prompt_need = {}  # sizes of a call -> workspace bytes
 
 
 def prompt_attn(q, k, v, starts, scale=None, window: int = 0, out=None, workspace=None, stream=None):
@@ -844,42 +866,44 @@ def prompt_attn(q, k, v, starts, scale=None, window: int = 0, out=None, workspac
     starts[b] .. starts[b + 1] - 1 (starts int32 [batch + 1]). A token's rows are contiguous; tokens may be parts of longer
     rows. scale: 1 / sqrt(dim). window: how many keys a query sees at most, 0 for all. Returns out [tokens, heads, dim]; its
     rows that belong to no sequence are not written."""
+    dev, kind = q.get_device(), q.dtype
     if stream is not None and (out is None or workspace is None):
-        on = _other_stream(q.device, stream)
+        on = _other_stream(dev, stream)
         if on:
             with on:
                 return prompt_attn(q, k, v, starts, scale, window, out, workspace)
-    torch, dev, dtype = _calls()[0], q.device, q.dtype
-    (T, H, D), ks = q.shape, k.shape
-    if len(ks) != 3 or ks[0] != T or ks[2] != D or v.shape != ks:
+    torch, qs, ks = _calls()[0], q.shape, k.shape
+    if len(qs) != 3 or len(ks) != 3 or ks[0] != qs[0] or ks[2] != qs[2]:
         raise ValueError("q: [tokens, heads, dim], k and v: [tokens, kv_heads, dim]")
-    row = (D, 1)
-    for x in (q, k, v):
-        st = x.stride()
-        if x.dtype != dtype or x.device != dev or (st[1:] != row and (x.shape[1] > 1 or st[2] != 1)):
-            raise ValueError(f"q, k and v: of {dtype} on {dev}, each token's rows contiguous")
-    if starts.dtype != torch.int32 or starts.dim() != 1 or starts.shape[0] < 1 or not starts.is_contiguous() or starts.device != dev:
-        raise ValueError(f"starts: contiguous int32 [batch + 1], on {dev}")
+    T, H, D = qs
+    q_stride, k_stride, v_stride = _rows_of(q, qs, kind, dev), _rows_of(k, ks, kind, dev), _rows_of(v, ks, kind, dev)
+    if starts.dtype != torch.int32 or starts.dim() != 1 or starts.shape[0] < 1 or not starts.is_contiguous() or starts.get_device() != dev:
+        raise ValueError("starts: contiguous int32 [batch + 1], on the call's device")
+    handle, x_type, batch = _handle(dev, stream), _float_type(kind), starts.shape[0] - 1
     if out is None:
-        out = torch.empty((T, H, D), dtype=dtype, device=dev)
-    elif out.shape != q.shape or out.dtype != dtype or not out.is_contiguous() or out.device != dev:
-        raise ValueError(f"out: contiguous {tuple(q.shape)} of {dtype} on {dev}")
-    if window < 0:
+        out = torch.empty(qs, dtype=kind, device=q.device)
+    elif out.shape != qs or out.dtype != kind or not out.is_contiguous() or out.get_device() != dev:
+        raise ValueError(f"out: contiguous {tuple(qs)} of {kind}, on the call's device")
+    # a larger window than an int holds is no window
+    if not 0 <= window:
         raise XQError("xq_prompt_attn", 2)
-    # ctypes keeps the low 32 bits of an int: a larger window would become another one
-    p = xq_prompts(_float_type(dtype), T, starts.shape[0] - 1, H, ks[1], D, q.data_ptr(), k.data_ptr(), v.data_ptr(), q.stride(0),
-                   k.stride(0), v.stride(0), out.data_ptr(), starts.data_ptr(), D ** -0.5 if scale is None else scale,
-                   min(window, 0x7FFFFFFF))
+    p = _pack_prompts(x_type, T, batch, H, ks[1], D, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_stride, k_stride, v_stride,
+                      out.data_ptr(), starts.data_ptr(), D ** -0.5 if scale is None else scale, min(window, 0x7FFFFFFF))
     L = lib()
     if workspace is None:
-        need = L.xq_prompt_attn_workspace_bytes(p)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need > 16 else None
+        sizes = (x_type, T, batch, H, ks[1], D)
+        need = _prompt_need.get(sizes)
+        if need is None:
+            if len(_prompt_need) >= 1024:
+                _prompt_need.clear()
+            need = _prompt_need[sizes] = L.xq_prompt_attn_workspace_bytes(p)
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need > 16 else None
         at, size = (ws.data_ptr(), need) if need > 16 else (None, 0)
     else:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace: contiguous, on {dev}")
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace: contiguous, on the call's device")
         at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    rc = L.xq_prompt_attn(p, at, size, _handle(dev, stream))
+    rc = L.xq_prompt_attn(p, at, size, handle)
     if rc:
         raise XQError("xq_prompt_attn", rc)
     return out

@@ -91,3 +91,19 @@ def test_prompt_attention_workspace(xq):
     assert size(type=8) == 0 and size(heads=3) == 0 and size(dim=100) == 0 and L.xq_prompt_attn_workspace_bytes(None) == 0
     assert L.xq_prompt_attn(None, FAKE, 1 << 40, None) == 1
     assert L.xq_prompt_attn(ctypes.byref(prompts(xq)), FAKE + 4, 1 << 40, None) == 3
+
+
+def test_packed_structures_have_the_structures_layout(xq):
+    """The binding packs arguments as bytes: fields at the same places as the C structures'."""
+    import struct
+    for form, kind in (("@" + xq._ADAPTERS, xq.xq_adapters), ("@" + 3 * xq._ADAPTERS, xq.xq_adapters * 3)):
+        assert struct.calcsize(form) == ctypes.sizeof(kind)
+    values = list(range(1, 11))
+    a = xq.xq_adapters.from_buffer_copy(struct.pack("@" + xq._ADAPTERS, *values))
+    assert [getattr(a, f[0]) for f in a._fields_] == values
+    values = [*range(1, 17), 0.5, 18, 19, 20, 1, 2.5]
+    r = xq.xq_qk_rows.from_buffer_copy(xq._pack_rows(*values))
+    assert [getattr(r, f[0]) for f in r._fields_] == values and len(xq._pack_rows(*values)) == ctypes.sizeof(r)
+    values = [*range(1, 15), 0.25, 16]
+    p = xq.xq_prompts.from_buffer_copy(xq._pack_prompts(*values))
+    assert [getattr(p, f[0]) for f in p._fields_] == values and len(xq._pack_prompts(*values)) == ctypes.sizeof(p)
