@@ -24,7 +24,7 @@ xq_status check_prompt_sizes(const xq_prompts* p) {
     return XQ_ERR_SHAPE;
   // positions, rows of all heads and sequences stay within an int
   if (p->tokens > (1 << 30) || p->batch > (1 << 24) || static_cast<long long>(p->tokens) * p->heads > (1LL << 30) ||
-      p->heads > (1 << 16))
+      p->heads > (1 << 16) || (p->type == XQ_TYPE_F32 && p->tokens >= (1 << 30)))
     return XQ_ERR_SHAPE;
   return XQ_OK;
 }

@@ -1,0 +1,7 @@
+// Prompt attention of fp32 rows, head size 256.
+#define XQ_PROMPT_TILE_IMPL
+#include "prompt_pieces.cuh"
+
+namespace xq {
+template struct PromptPiecesDim<256>;
+}  // namespace xq

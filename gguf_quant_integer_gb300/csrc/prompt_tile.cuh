@@ -22,21 +22,9 @@
 // or sum is not finite (a score, a V that all rows see), are computed again by themselves (one_row).
 #pragma once
 
-#include "ops_common.cuh"
-#include "xq_common.cuh"
-#include "xq_ptx.cuh"
+#include "prompt_items.cuh"
 
 namespace xq {
-
-constexpr int kPromptRows = 128;  // of a row tile
-
-struct PromptTileArgs {
-  PromptArgs a;
-  int pack;      // query heads of a KV head in a tile's rows
-  int tokens_tile;  // of a row tile: 128 / pack
-  int units;     // head units: kv_heads * group / pack
-  CUtensorMap q, k, v;
-};
 
 template <int D>
 struct PromptTileDim {
@@ -49,10 +37,7 @@ struct PromptTileDim {
 
 namespace {
 
-__device__ unsigned int g_prompt_error;  // invalid indices
-__device__ unsigned int g_prompt_wait;   // a wait that ran out
-constexpr long long kPromptWait = 1ll << 32;
-constexpr int kRows = kPromptRows, kKeys = 128;
+constexpr int kKeys = 128;
 
 template <int D>
 struct PromptShape {
@@ -72,181 +57,10 @@ struct PromptShape {
   static constexpr uint64_t kDescK = kCommon | (1ull << 16);
   static constexpr uint64_t kDescV = kCommon | (static_cast<uint64_t>(kKeys * kLine / 16) << 16);
 };
-
-struct Item {
-  int first, n;     // the sequence's first row and its rows
-  int place;        // of row tile 0's first token
-  int head;         // first query head
-  int begin[2], end[2];  // key tiles of the row tiles
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-template <int TYPE>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  uint32_t d;
-  if constexpr (TYPE == kF16)
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
-  else
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
-  return d;
-}
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(mbar)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]), "=r"(v[9]),
-        "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]),
-        "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
-        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-      : "r"(taddr)
-      : "memory");
-}
-
-// One row by one warp, lanes over the head's elements.
-template <int TYPE, int D>
-__device__ __noinline__ void one_row(const PromptArgs& A, int first, int place, int head) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, kv = head / (A.heads / A.kv_heads);
-  const size_t token = static_cast<size_t>(first) + place;
-  float q[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = load_elt<TYPE>(A.q, token * A.q_stride + static_cast<size_t>(head) * D + lane + 32 * e);
-    o[e] = 0.0f;
-  }
-  const float cs = A.scale * 1.4426950408889634f;
-  float m = -INFINITY, l = 0.0f;
-  for (int j = A.window && place >= A.window ? place - A.window + 1 : 0; j <= place; ++j) {
-    const size_t key = static_cast<size_t>(first) + j;
-    float s = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      s = fmaf(q[e], load_elt<TYPE>(A.k, key * A.k_stride + static_cast<size_t>(kv) * D + lane + 32 * e), s);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s = __fmul_rn(s, cs);
-    const float next = fmaxf(m, s);
-    const float f = m == next ? 1.0f : exp2f(m - next), w = s == -INFINITY && next == s ? 0.0f : exp2f(s - next);
-    m = next;
-    l = fmaf(l, f, w);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = fmaf(o[e], f, w * load_elt<TYPE>(A.v, key * A.v_stride + static_cast<size_t>(kv) * D + lane + 32 * e));
-  }
-  const size_t row = token * A.heads + head;
-  if (XQ_IN(row, static_cast<size_t>(A.tokens) * A.heads, kChkPromptRow))
-#pragma unroll
-    for (int e = 0; e < E; ++e) store_elt<TYPE>(A.out, row * D + lane + 32 * e, o[e] / l);
-}
-
-// Sequence b's rows and their number; 0, and recorded, if its bounds are no range of the call's rows.
-__device__ __forceinline__ int sequence(const PromptArgs& A, int b, int* first) {
-  if (b >= A.batch) return 0;
-  const int s0 = A.starts[b], s1 = A.starts[b + 1];
-  *first = s0;
-  if (s0 < 0 || s1 < s0 || s1 > A.tokens) {
-    atomicCAS(&g_prompt_error, 0u, kOpsBadStart);
-    return 0;
-  }
-  return s1 - s0;
-}
-
-// Items in descending order of their work. An item is a head unit of a group of `step` tokens of a sequence; group L of any
-// sequence has the keys up to it, so all groups L of all sequences (a level) are alike. A warp walks down the levels,
-// counting the sequences that reach each.
-struct Walk {
-  int level;        // of the current one
-  long long before; // groups in the levels before it
-  int count;        // sequences that reach it
-};
-__device__ __forceinline__ int walk_count(const PromptArgs& A, int level, int step) {
-  int c = 0;
-  for (int b = threadIdx.x & 31; b < A.batch; b += 32) {
-    int first;
-    c += sequence(A, b, &first) > level * static_cast<long long>(step);
-  }
-  return __reduce_add_sync(0xffffffffu, c);
-}
-__device__ __forceinline__ void walk_begin(const PromptArgs& A, int step, Walk& w) {
-  int most = 0;
-  for (int b = threadIdx.x & 31; b < A.batch; b += 32) {
-    int first;
-    most = max(most, sequence(A, b, &first));
-  }
-  most = __reduce_max_sync(0xffffffffu, most);
-  w.level = (most + step - 1) / step - 1;
-  w.before = 0;
-  w.count = w.level >= 0 ? walk_count(A, w.level, step) : 0;
-}
-// The item of this rank; false behind the last. Ranks come in ascending order.
-__device__ __forceinline__ bool next_item(const PromptTileArgs& P, int tiles, long long rank, Walk& w, Item& it) {
-  const PromptArgs& A = P.a;
-  const int step = tiles * P.tokens_tile, lane = threadIdx.x & 31;
-  const long long group = rank / P.units;
-  const int unit = static_cast<int>(rank - group * P.units);
-  while (w.level >= 0 && group >= w.before + w.count) {
-    w.before += w.count;
-    --w.level;
-    if (w.level >= 0) w.count = walk_count(A, w.level, step);
-  }
-  if (w.level < 0) return false;
-  int left = static_cast<int>(group - w.before);  // sequences to pass over, of those that reach the level
-  for (int b0 = 0; b0 < A.batch; b0 += 32) {
-    int first = 0;
-    const int n = sequence(A, b0 + lane, &first);
-    const unsigned reach = __ballot_sync(0xffffffffu, n > w.level * static_cast<long long>(step));
-    const int c = __popc(reach);
-    if (left >= c) {
-      left -= c;
-      continue;
-    }
-    const int at = __fns(reach, 0, left + 1);
-    it.first = __shfl_sync(0xffffffffu, first, at);
-    it.n = __shfl_sync(0xffffffffu, n, at);
-    break;
-  }
-  it.place = w.level * step;
-  it.head = unit * P.pack;
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int p0 = it.place + r * P.tokens_tile, p1 = min(p0 + P.tokens_tile, it.n) - 1;  // first and last row's
-    const int k0 = A.window ? max(0, p0 - A.window + 1) : 0;
-    it.begin[r] = r < tiles && p1 >= p0 ? k0 / kKeys : 0;
-    it.end[r] = r < tiles && p1 >= p0 ? p1 / kKeys + 1 : 0;
-  }
-  return true;
-}
-
 enum PromptBar { kPbDrain, kPbItem, kPbItemFree = kPbItem + 2, kPbQ = kPbItemFree + 2, kPbQFree = kPbQ + 2, kPbS = kPbQFree + 2,
                  kPbP = kPbS + 2, kPbO = kPbP + 2, kPbFull = kPbO + 2 };
 
-// Whether some row of row tile r does not see some key of a tile from `key` on.
-__device__ __forceinline__ bool masked(const PromptTileArgs& P, int place, int key) {
-  return key + kKeys > place + 1 || (P.a.window && key < place + P.tokens_tile - P.a.window);
-}
 
-// Bit 15 of each half: it is an infinity or NaN.
-template <int TYPE>
-__device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
-  constexpr uint32_t field = TYPE == kF16 ? 0x7C007C00u : 0x7F807F80u, one = TYPE == kF16 ? 0x04000400u : 0x00800080u;
-  return ((w & field) + one) & 0x80008000u;
-}
 
 template <int TYPE, int D>
 __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_kernel(const __grid_constant__ PromptTileArgs P) {
@@ -313,7 +127,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
     for (unsigned round = 0; ok; ++round) {
       Item it;
       const long long rank = static_cast<long long>(round) * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      const bool there = next_item(P, kTiles, rank, w, it);
+      const bool there = next_item<kKeys, 1>(P, kTiles, rank, w, it);
       if (!there) it.n = -1;
       if (round >= 2 && !wait(kPbItemFree + (round & 1), (round >> 1) + 1, 2)) break;
       if (lead) {
@@ -451,7 +265,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
         const unsigned ld = 2 * tiles + 1, st = ld % kStages;
         ok = wait(kPbFull + st, ld / kStages, 15);
         if (!ok) break;
-        if (masked(P, it.place, j * kKeys) || (second && masked(P, it.place + P.tokens_tile, j * kKeys))) {
+        if (masked<kKeys>(P, it.place, j * kKeys) || (second && masked<kKeys>(P, it.place + P.tokens_tile, j * kKeys))) {
           const uint32_t from = base + kTiles * S::kQ + st * S::kStage + ((warp - kCheck) * 32 + lane) * 16;
           bool found = false;
 #pragma unroll 8
@@ -515,7 +329,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
 #pragma unroll
           for (int x = 0; x < kKeys; ++x) sv[x] = __float_as_uint(__uint_as_float(sv[x]) * sign);
         }
-        if (masked(P, p0, key)) {
+        if (masked<kKeys>(P, p0, key)) {
 #pragma unroll
           for (int x = 0; x < kKeys; ++x)
             if (key + x < lim0 || key + x >= lim1) sv[x] = 0xFF800000u;
@@ -600,7 +414,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
         const int kv = it.head / (A.heads / A.kv_heads);
 #pragma unroll 1
         for (int j = it.begin[r]; j < it.end[r]; ++j)
-          if (masked(P, it.place, j * kKeys) || (it.end[1] > 0 && masked(P, it.place + P.tokens_tile, j * kKeys)))
+          if (masked<kKeys>(P, it.place, j * kKeys) || (it.end[1] > 0 && masked<kKeys>(P, it.place + P.tokens_tile, j * kKeys)))
 #pragma unroll 1
             for (int key = j * kKeys; key < min((j + 1) * kKeys, it.n); ++key) {
               bool odd_v = false;

@@ -84,6 +84,7 @@ enum CheckSite : unsigned {
   kChkKvLens = 55,   // sequence inside the batch
   // qk_rope.cu
   kChkRope = 60,     // 8 elements inside a row of a token of the call
+  kChkPromptSlot = 63, // a tile's powers of two inside the workspace
   // prompt_tile.cuh
   kChkLoraRow = 62,    // row of y inside [M]
   kChkPromptRow = 61,  // row of the result inside [tokens][heads]

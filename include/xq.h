@@ -343,8 +343,8 @@ XQ_API xq_status xq_layer_mixed_static(const xq_proj *proj, int n_proj,
  * access whose address comes from nontrivial arithmetic, skip an access that
  * fails and record the site: kernel 9, wait = site (10-16 the GEMV, 20-26
  * the tile kernel, 30-32 the quantizer, 40-43 the dp4a Q6_K GEMV,
- * 50-55 the KV cache kernels, 60 norms with rotation, 61 prompt attention, 62
- * adapters), reported
+ * 50-55 the KV cache kernels, 60 norms with rotation, 61 and 63 prompt
+ * attention, 62 adapters), reported
  * after any wait code. If several kernels recorded one,
  * the lowest kernel number is reported and all are cleared. The reads and
  * writes are synchronous. XQ_ERR_ARG for a null code_out, XQ_ERR_CUDA if the
