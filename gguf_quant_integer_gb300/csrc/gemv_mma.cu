@@ -1469,17 +1469,27 @@ bool encode_tma_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, u
          CUDA_SUCCESS;
 }
 
-bool encode_tma_heads(CUtensorMap* map, bool bf16, const void* base, int dim, int heads, int rows, long long stride, int box_dim,
-                      int box_heads, int box_rows) {
+static bool encode_heads(CUtensorMap* map, CUtensorMapDataType dt, int bytes, const void* base, int dim, int heads, int rows,
+                         long long stride, int box_dim, int box_heads, int box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(dim) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(dim) * bytes, static_cast<cuuint64_t>(stride) * bytes};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_dim), static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides,
-            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, box_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return fn(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box_dim * bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_tma_heads(CUtensorMap* map, bool bf16, const void* base, int dim, int heads, int rows, long long stride, int box_dim,
+                      int box_heads, int box_rows) {
+  return encode_heads(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dim, heads, rows, stride,
+                      box_dim, box_heads, box_rows);
+}
+
+bool encode_tma_heads_f32(CUtensorMap* map, const void* base, int dim, int heads, int rows, long long stride, int box_heads, int box_rows) {
+  return encode_heads(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, dim, heads, rows, stride, 32, box_heads, box_rows);
 }
 
 int q6k_row_shift(int K) {

@@ -16,15 +16,15 @@ PromptPieces pieces(const PromptArgs& a, uint8_t* base) {
     at += (bytes + 255) & ~static_cast<size_t>(255);
     return p;
   };
-  const size_t q = static_cast<size_t>(a.tokens) * a.heads, k = static_cast<size_t>(a.tokens) * a.kv_heads, d = a.dim;
+  const size_t k = static_cast<size_t>(a.tokens) * a.kv_heads, d = a.dim;
   w.slots = a.tokens / prompt_piece_keys(a.dim) + a.batch;
-  w.q = reinterpret_cast<__half*>(take(q * d * 4));
+  const size_t tiles = static_cast<size_t>(w.slots) * a.kv_heads;
   w.k = reinterpret_cast<__half*>(take(k * d * 4));
   w.v = reinterpret_cast<__half*>(take(k * d * 4));
-  w.q_power = reinterpret_cast<float*>(take(q * 4));
-  w.k_power = reinterpret_cast<float*>(take(k * 4));
-  w.v_power = reinterpret_cast<float*>(take(static_cast<size_t>(w.slots) * a.kv_heads * d * 4));
-  w.owner = reinterpret_cast<int*>(take(static_cast<size_t>(w.slots) * a.kv_heads * prompt_piece_halves(a.dim) * 4));
+  w.k_power = reinterpret_cast<float*>(take(tiles * 4));
+  w.v_power = reinterpret_cast<float*>(take(tiles * d * 4));
+  w.k_owner = reinterpret_cast<int*>(take(tiles * 4));
+  w.v_owner = reinterpret_cast<int*>(take(tiles * 4));
   w.bytes = at;
   return w;
 }

@@ -25,6 +25,7 @@ __device__ unsigned int g_prompt_error;  // invalid indices
 __device__ unsigned int g_prompt_wait;   // a wait that ran out
 constexpr long long kPromptWait = 1ll << 32;
 constexpr int kRows = kPromptRows;
+constexpr int kWalkKept = 2;  // sequences a lane keeps in registers
 
 struct Item {
   int first, n;     // the sequence's first row and its rows
@@ -60,6 +61,11 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(mbar)
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
   asm volatile(
@@ -129,54 +135,73 @@ struct Walk {
   int level;        // of the current one
   long long before; // groups in the levels before it
   int count;        // sequences that reach it
+  int n[kWalkKept], first[kWalkKept];  // of sequences lane, lane + 32, ...: a level costs no memory round trip
 };
-__device__ __forceinline__ int walk_count(const PromptArgs& A, int level, int step) {
+// Rows (and the first) of the lane's i-th sequence.
+__device__ __forceinline__ int walk_sequence(const PromptArgs& A, const Walk& w, int i, int* first) {
+  int n = 0;
+  if (i >= kWalkKept) return sequence(A, i * 32 + (threadIdx.x & 31), first);
+#pragma unroll
+  for (int k = 0; k < kWalkKept; ++k)
+    if (k == i) n = w.n[k], *first = w.first[k];
+  return n;
+}
+__device__ __forceinline__ int walk_count(const PromptArgs& A, const Walk& w, int level, int step) {
+  const int beyond = level * step;
   int c = 0;
-  for (int b = threadIdx.x & 31; b < A.batch; b += 32) {
+#pragma unroll
+  for (int k = 0; k < kWalkKept; ++k) c += w.n[k] > beyond;
+  for (int i = kWalkKept; i * 32 < A.batch; ++i) {
     int first;
-    c += sequence(A, b, &first) > level * static_cast<long long>(step);
+    c += sequence(A, i * 32 + (threadIdx.x & 31), &first) > beyond;
   }
   return __reduce_add_sync(0xffffffffu, c);
 }
 __device__ __forceinline__ void walk_begin(const PromptArgs& A, int step, Walk& w) {
   int most = 0;
-  for (int b = threadIdx.x & 31; b < A.batch; b += 32) {
+#pragma unroll
+  for (int k = 0; k < kWalkKept; ++k) {
+    w.first[k] = 0;
+    w.n[k] = sequence(A, k * 32 + (threadIdx.x & 31), &w.first[k]);
+    most = max(most, w.n[k]);
+  }
+  for (int i = kWalkKept; i * 32 < A.batch; ++i) {
     int first;
-    most = max(most, sequence(A, b, &first));
+    most = max(most, sequence(A, i * 32 + (threadIdx.x & 31), &first));
   }
   most = __reduce_max_sync(0xffffffffu, most);
   w.level = (most + step - 1) / step - 1;
   w.before = 0;
-  w.count = w.level >= 0 ? walk_count(A, w.level, step) : 0;
+  w.count = w.level >= 0 ? walk_count(A, w, w.level, step) : 0;
 }
 // The item of this rank; false behind the last. Ranks come in ascending order. KEYS: of a tile.
 template <int KEYS, int HALVES>
 __device__ __forceinline__ bool next_item(const PromptTileArgs& P, int tiles, long long rank, Walk& w, Item& it) {
   const PromptArgs& A = P.a;
-  const int step = tiles * P.tokens_tile, lane = threadIdx.x & 31;
-  const int units = P.units * HALVES;
-  const long long group = rank / units;
+  const int step = tiles * P.tokens_tile, units = P.units * HALVES;
+  const long long group = rank >> 32 ? rank / units : static_cast<unsigned>(rank) / static_cast<unsigned>(units);
   const int unit = static_cast<int>(rank - group * units);
   while (w.level >= 0 && group >= w.before + w.count) {
     w.before += w.count;
     --w.level;
-    if (w.level >= 0) w.count = walk_count(A, w.level, step);
+    if (w.level >= 0) w.count = walk_count(A, w, w.level, step);
   }
   if (w.level < 0) return false;
   int left = static_cast<int>(group - w.before);  // sequences to pass over, of those that reach the level
-  for (int b0 = 0; b0 < A.batch; b0 += 32) {
+  for (int i = 0; i * 32 < A.batch; ++i) {
     int first = 0;
-    const int n = sequence(A, b0 + lane, &first);
-    const unsigned reach = __ballot_sync(0xffffffffu, n > w.level * static_cast<long long>(step));
+    const int n = walk_sequence(A, w, i, &first);
+    unsigned reach = __ballot_sync(0xffffffffu, n > w.level * step);
     const int c = __popc(reach);
     if (left >= c) {
       left -= c;
       continue;
     }
-    const int at = __fns(reach, 0, left + 1);
+    for (; left > 0; --left) reach &= reach - 1;
+    const int at = __ffs(reach) - 1;
     it.first = __shfl_sync(0xffffffffu, first, at);
     it.n = __shfl_sync(0xffffffffu, n, at);
-    it.sequence = b0 + at;
+    it.sequence = i * 32 + at;
     break;
   }
   it.place = w.level * step;

@@ -1,21 +1,25 @@
 // Prompt attention of fp32 rows on the tcgen05 tensor cores: every operand as two fp16 numbers.
 //
 // x = 2^-s (hi + lo) with hi and lo of 11 bits each, so a product takes three: hi hi, hi lo, lo hi (what is left out is
-// 2^-21 of it at most, in the mean 2^-24). A first kernel (prompt_split) makes the pieces of Q, K and V in the workspace.
-// Powers of two keep them in fp16's range: one for each row of Q and of K, which the softmax applies to the scores, and for
-// V one for each column of a tile of keys, which is applied to the tile's output.
+// 2^-21 of it at most, in the mean 2^-24). A first kernel (prompt_split) makes the pieces of K and V in the workspace, a
+// row's thread those of its query in tensor memory. Powers of two keep them in fp16's range: one for a row of Q and for a
+// tile of K, which the softmax applies to the scores, and for V one for each column of a tile, which is applied to the
+// tile's output.
 //
 // Sums: a tensor core's accumulator cuts off, towards 0, what an fp32 addition rounds, so it only ever holds one tile's sum,
 // small products first; outputs are added up in registers. Scores of large and small weights: a weight is 2^(z - e), its
 // reference e as in prompt_tile.cuh, hi cut off and lo the rest.
 //
-// V rows of a tile that differ by more than 2^12 in size would cost the small ones bits where no large one has a weight;
-// rows of such tiles (as those that see something not finite) are computed by themselves (one_row).
+// K or V rows of a tile that differ by more than 2^12 in size would cost the small ones bits where no large one has a
+// weight; query rows that meet such tiles (as those that see something not finite) are computed by themselves (one_row).
 //
-// A CTA has 128 rows; scores and a tile's output are double-buffered in tensor memory, so that the products of tile j + 1
-// pass beside the softmax of tile j and the addition of tile j - 1. With head size 256 it has half of V's columns, and
-// tiles of 64 keys. Roles: warps 0-3 softmax (a thread a row), 4-7 outputs (a thread a row), then products, copies, and two
-// warps that bring the tiles' powers of two and look through V. Items as in prompt_tile.cuh.
+// A CTA has 128 rows. Q and the weights are the products' first operands in tensor memory (Q in shared memory was read at
+// 107 clocks a product, of which the tensor cores need 64), scores are double-buffered there, so that the products of a
+// tile pass beside the softmax of the two before it. With head size 256 a CTA has half of V's columns, and tiles of 64
+// keys. Roles: two groups of 4 warps take the tiles' softmax in turn (a thread a row; each has a reference and a sum of
+// its own), and an item's last one the next item's queries; 4 warps add up outputs (a thread a row), then one that issues
+// the products of Q and K, one those of weights and V, one that copies, and one that brings the tiles' powers of two and
+// looks through V. Items as in prompt_tile.cuh.
 #pragma once
 
 #include "prompt_items.cuh"
@@ -24,10 +28,9 @@ namespace xq {
 
 // The workspace.
 struct PromptPieces {
-  __half *q, *k, *v;       // [2][tokens][heads][dim], hi and lo
-  float *q_power, *k_power;  // [tokens][heads], [kv_heads][tokens]: what a row's pieces are to be multiplied by
-  float* v_power;          // [slots][kv_heads][dim]
-  int* owner;              // [slots][kv_heads][halves]: the slot's sequence; -1: none, -2: rows too far apart
+  __half *k, *v;           // [2][tokens][kv_heads][dim], hi and lo
+  float *k_power, *v_power;  // [slots][kv_heads], [slots][kv_heads][dim]: what the pieces are to be multiplied by
+  int *k_owner, *v_owner;  // [slots][kv_heads]: the slot's sequence; -1: none, -2: rows too far apart
   int slots;               // tiles of keys of all sequences: tile j of sequence b has slot starts[b] / keys + b + j
   size_t bytes;
 };
@@ -51,26 +54,30 @@ template <int D>
 struct PieceShape {
   static constexpr int kKeys = prompt_piece_keys(D), kHalves = prompt_piece_halves(D), kV = D / kHalves;
   static constexpr int kBox = D % 64 == 0 ? 64 : 32, kLine = kBox * 2, kBoxes = kV / kBox;  // of a part: kV elements of a row
-  static constexpr int kQPart = kRows * kV * 2, kQ = kHalves * kQPart;                      // of a piece
   static constexpr int kStage = kKeys * kV * 2;  // a part of a piece of a tile
-  static constexpr int kStages = D == 128 ? 4 : D == 64 ? 11 : D == 96 ? 6 : 5;
-  static constexpr int kLoads = 2 * kHalves + 2;  // of a tile: K's lo parts, K's hi parts, V lo, V hi
-  // A tile's scores are computed before the outputs of the one before it. Its K parts then come while V's two are there: with
-  // head size 256 the stages for that do not fit.
-  static constexpr bool kAhead = kStages >= 2 * kHalves + 2;
-  static constexpr int kSmem = 2 * kQ + kStages * kStage + 1024;
-  static constexpr int kColO = 2 * kKeys, kAlloc = 512;
-  static constexpr int kWarps = 12;
-  static_assert(kColO + 2 * kV <= kAlloc && kSmem <= 227 * 1024 - 6 * 1024, "one CTA fits the SM");
+  // Stages of K parts and of V parts. A tile's are K's lo parts, then K's hi parts (all of these are needed at a time);
+  // V lo, V hi.
+  static constexpr int kKParts = 2 * kHalves, kKStages = D == 128 ? 4 : D == 96 ? 5 : 8, kVStages = D == 128 || D == 96 ? 2 : 4;
+  // An item's queries come through K's stages before its first tile: boxes of 128 rows x 32 fp32 columns.
+  static constexpr int kQBoxes = kStage / (kRows * 128), kQParts = D / 32 / kQBoxes;
+  static constexpr int kStages = kKStages + kVStages;
+  static constexpr int kRowsOut = 4 * 4096;  // results on their way out: 32 rows x 128 bytes of each output warp
+  static constexpr int kSmem = kStages * kStage + kRowsOut + 1024;
+  static constexpr int kColO = 2 * kKeys, kColQ = kColO + kV, kAlloc = 512;  // scores twice, outputs, Q's hi and lo
+  static constexpr int kWarps = 16;
+  // registers a thread: of the softmax, the outputs, the others; four warps each, launched with 128
+  static constexpr int kRegsSoft = 112, kRegsOut = 208, kRegsRest = 80;
+  static_assert(2 * kRegsSoft + kRegsOut + kRegsRest <= 4 * 128, "an increase beyond what was launched with waits forever");
+  static_assert(D / 32 % kQBoxes == 0 && kKStages >= kQParts && kKStages > kHalves && kVStages >= 2 && kColQ + D <= kAlloc && kSmem <= 227 * 1024 - 8 * 1024, "one CTA fits the SM");
   static constexpr uint64_t kSwizzle = kLine == 128 ? 2ull : 4ull;
   static constexpr uint64_t kCommon = (1ull << 46) | (kSwizzle << 61) | (static_cast<uint64_t>(8 * kLine / 16) << 32);
   static constexpr uint64_t kDescK = kCommon | (1ull << 16);
   static constexpr uint64_t kDescV = kCommon | (static_cast<uint64_t>(kKeys * kLine / 16) << 16);
 };
 
-enum PieceBar { kQbDrain, kQbQ, kQbQFree, kQbItem, kQbItemFree = kQbItem + 2, kQbS = kQbItemFree + 2, kQbP = kQbS + 2, kQbO = kQbP + 2,
-                kQbOFree = kQbO + 2, kQbPower = kQbOFree + 2, kQbPowerFree = kQbPower + 2, kQbChecked = kQbPowerFree + 2,
-                kQbSum = kQbChecked + 2, kQbFull = kQbSum + 2 };
+enum PieceBar { kQbDrain, kQbQ, kQbItem, kQbItemFree = kQbItem + 2, kQbS = kQbItemFree + 2, kQbP = kQbS + 2,
+                kQbO = kQbP + 2, kQbOFree = kQbO + 2, kQbPower = kQbOFree + 2, kQbPowerFree = kQbPower + 2, kQbChecked = kQbPowerFree + 2,
+                kQbSum = kQbChecked + 2, kQbFull = kQbSum + 2 };  // then a stage's full and free: K's, V's
 
 // Two fp32 numbers as fp16 pairs: hi (each cut off to 11 bits; exact above 2^-14) and what is left.
 __device__ __forceinline__ void halves_of(float a, float b, uint32_t* hi, uint32_t* lo) {
@@ -84,35 +91,35 @@ template <int D>
 __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
     prompt_pieces_kernel(const __grid_constant__ PromptTileArgs P, const __grid_constant__ PromptPieces W) {
   using S = PieceShape<D>;
-  constexpr int kKeys = S::kKeys, kStages = S::kStages, kQbFree = kQbFull + kStages, kMma = 8, kLoad = 9, kAux = 10;
+  constexpr int kKeys = S::kKeys, kStages = S::kStages, kQbFree = kQbFull + kStages, kOut = 8, kScores = 12, kOutputs = 13, kLoad = 14, kAux = 15;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kQbFull + 2 * kStages];
   __shared__ uint32_t sh_tmem;
   __shared__ Item sh_item[2];
   __shared__ unsigned sh_odd[2];                        // rows of the item have to be looked at (1) or computed by themselves (2)
-  __shared__ __align__(16) float sh_k[2][kKeys];        // the tile's powers of two, by tile & 1
+  __shared__ float sh_k[2];                             // the tile's powers of two, by tile & 1
   __shared__ __align__(16) float sh_v[2][S::kV];
-  __shared__ float sh_move[2][kRows];                   // factor of what a row summed up before the tile, by tile & 1
-  __shared__ float sh_sum[2][kRows];                    // sums of weights, by item & 1
+  __shared__ float sh_ref[2][kRows];                    // the rows' references, by tile & 1
+  __shared__ float sh_q[2][kRows];                      // the queries' powers of two, by item & 1
+  __shared__ float2 sh_sum[2][2][kRows];                // sums of weights and their references, by item & 1 and group
   const PromptArgs& A = P.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto bar = [&](int i) { return ptx::smem_addr(&bars[i]); };
-  const uint32_t base = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u, stages = base + 2 * S::kQ;
+  const uint32_t base = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u, stages = base, rows_out = base + kStages * S::kStage;
   if (tid == 0) {
-    ptx::mbar_init(bar(kQbDrain), 1);
-    ptx::mbar_init(bar(kQbQ), 1);
-    ptx::mbar_init(bar(kQbQFree), 1);
+    ptx::mbar_init(bar(kQbDrain), 2);
+    ptx::mbar_init(bar(kQbQ), 4);
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(bar(kQbItem + b), 1);
-      ptx::mbar_init(bar(kQbItemFree + b), 11);
+      ptx::mbar_init(bar(kQbItemFree + b), 15);
       ptx::mbar_init(bar(kQbS + b), 1);
       ptx::mbar_init(bar(kQbP + b), 4);
       ptx::mbar_init(bar(kQbO + b), 1);
       ptx::mbar_init(bar(kQbOFree + b), 4);
-      ptx::mbar_init(bar(kQbPower + b), 2);
+      ptx::mbar_init(bar(kQbPower + b), 1);
       ptx::mbar_init(bar(kQbPowerFree + b), 8);
-      ptx::mbar_init(bar(kQbChecked + b), 2);
-      ptx::mbar_init(bar(kQbSum + b), 4);
+      ptx::mbar_init(bar(kQbChecked + b), 1);
+      ptx::mbar_init(bar(kQbSum + b), 8);
     }
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(bar(kQbFull + i), 1);
@@ -120,7 +127,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
     }
     ptx::mbar_init_fence();
   }
-  if (warp == kMma) ptx::tmem_alloc(ptx::smem_addr(&sh_tmem), S::kAlloc);
+  if (warp == kScores) ptx::tmem_alloc(ptx::smem_addr(&sh_tmem), S::kAlloc);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -147,26 +154,38 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
   bool ok = true;
   Item it;
 
+  if (warp >= kScores) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsRest));
   if (warp == kLoad) {
     // ------------------------------------------------ copies
     Walk w;
     walk_begin(A, P.tokens_tile, w);
     const bool lead = ptx::elect_one();
-    unsigned loaded = 0;
-    auto load = [&](const CUtensorMap* map, int x, int y, int z) {  // a part of a piece: kV elements of kKeys rows
-      const unsigned st = loaded % kStages;
-      if (loaded >= kStages) ok = ok && wait(kQbFree + st, loaded / kStages - 1, 4);
-      ++loaded;
-      if (!ok || !lead) return;
+    unsigned loaded[2] = {0u, 0u};  // parts of K, of V
+    // the next stage of a ring, its last contents done with; -1 if a wait ran out
+    auto stage = [&](int v) {
+      const unsigned ring = v ? S::kVStages : S::kKStages, turn = loaded[v] / ring, st = (v ? S::kKStages : 0) + loaded[v] % ring;
+      if (turn > 0) ok = ok && wait(kQbFree + st, turn - 1, 4);
+      ++loaded[v];
+      return ok ? static_cast<int>(st) : -1;
+    };
+    // a part of a piece: kV elements of kKeys rows
+    auto load = [&](int v, const CUtensorMap* map, int x, int y, int z) {
+      const int st = stage(v);
+      if (st < 0 || !lead) return;
       ptx::mbar_expect_tx(bar(kQbFull + st), S::kStage);
 #pragma unroll
       for (int b = 0; b < S::kBoxes; ++b)
         tma_load_3d(stages + st * S::kStage + b * (kKeys * S::kLine), map, x + b * S::kBox, y, z, bar(kQbFull + st));
     };
-    for (unsigned round = 0; ok; ++round) {
+    Item next;
+    auto find = [&](unsigned round) {
       const long long rank = static_cast<long long>(round) * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      const bool there = next_item<kKeys, S::kHalves>(P, 1, rank, w, it);
-      if (!there) it.n = -1;
+      if (!next_item<kKeys, S::kHalves>(P, 1, rank, w, next)) next.n = -1;
+    };
+    find(0);
+    for (unsigned round = 0; ok; ++round) {
+      it = next;
+      const bool there = it.n >= 0;
       if (round >= 2 && !wait(kQbItemFree + (round & 1), (round >> 1) + 1, 2)) break;
       if (lead) {
         sh_item[round & 1] = it;
@@ -175,163 +194,163 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
       }
       __syncwarp();
       if (!there) break;
-      if (round > 0 && !wait(kQbQFree, round - 1, 3)) break;
-      if (lead) {
-        ptx::mbar_expect_tx(bar(kQbQ), 2 * P.pack * P.tokens_tile * D * 2);
+      for (int i = 0; i < S::kQParts && ok; ++i) {
+        const int st = stage(0);
+        if (st < 0 || !lead) continue;
+        ptx::mbar_expect_tx(bar(kQbFull + st), S::kQBoxes * P.pack * P.tokens_tile * 128);
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-          for (int b = 0; b < D / S::kBox; ++b)
-            tma_load_3d(base + p * S::kQ + b * (kRows * S::kLine), &P.q, b * S::kBox, it.head, p * A.tokens + it.first + it.place, bar(kQbQ));
+        for (int b = 0; b < S::kQBoxes; ++b)
+          tma_load_3d(stages + st * S::kStage + b * (kRows * 128), &P.q, (i * S::kQBoxes + b) * 32, it.head, it.first + it.place, bar(kQbFull + st));
       }
+      __syncwarp();
+      // in the order of the products: K a tile before V
       const int kv = it.head / group;
-      for (int j = it.begin[0]; j < it.end[0] && ok; ++j) {
+      for (int j = it.begin[0]; j <= it.end[0] && ok; ++j) {
         const int row = it.first + j * kKeys;
-        for (int c = 0; c < S::kHalves; ++c) load(&P.k, c * S::kV, kv, row + A.tokens);
-        for (int c = 0; c < S::kHalves; ++c) load(&P.k, c * S::kV, kv, row);
-        load(&P.v, it.half * S::kV, kv, row + A.tokens);
-        load(&P.v, it.half * S::kV, kv, row);
+        for (int c = 0; c < S::kKParts && j < it.end[0]; ++c)
+          load(0, &P.k, c % S::kHalves * S::kV, kv, c < S::kHalves ? row + A.tokens : row);
+        if (j == it.begin[0]) find(round + 1);  // while the first copies are on their way
+        for (int p = 1; p >= 0 && j > it.begin[0]; --p) load(1, &P.v, it.half * S::kV, kv, row - kKeys + p * A.tokens);
       }
       __syncwarp();
     }
     // copies in flight land before the CTA ends
-    for (unsigned i = loaded > kStages ? loaded - kStages : 0; i < loaded; ++i)
-      if (!wait(kQbFull + i % kStages, i / kStages, 5)) break;
-  } else if (warp == kMma) {
-    // ------------------------------------------------ products, issued by one thread
-    constexpr uint32_t idS = ptx::idesc_f16(kRows, kKeys, false), idO = ptx::idesc_f16(kRows, S::kV, false) | (1u << 16);
+    for (int v = 0; v < 2; ++v) {
+      const unsigned ring = v ? S::kVStages : S::kKStages;
+      for (unsigned i = loaded[v] > ring ? loaded[v] - ring : 0; i < loaded[v]; ++i)
+        if (!wait(kQbFull + (v ? S::kKStages : 0) + i % ring, i / ring, 5)) break;
+    }
+  } else if (warp == kScores) {
+    // ------------------------------------------------ products of Q and K, issued by one thread
+    constexpr uint32_t idS = ptx::idesc_f16(kRows, kKeys, false);
     constexpr int kSteps = S::kBox / 16;
     const bool lead = ptx::elect_one();
     const uint32_t at = __shfl_sync(0xffffffffu, tmem, 0);
-    const uint64_t stage0 = stages >> 4, q0 = base >> 4;
-    auto full = [&](unsigned ld, unsigned code) { return wait(kQbFull + ld % kStages, ld / kStages, code); };
-    auto release = [&](unsigned ld) {
-      if (lead) ptx::tc_commit(bar(kQbFree + ld % kStages));
-      __syncwarp();
-    };
-    // Q piece p, part c x the K part of load ld
-    auto qk = [&](uint32_t d, int p, int c, unsigned ld, bool first) {
-      const uint64_t kd = S::kDescK | (stage0 + __shfl_sync(0xffffffffu, (ld % kStages) * (S::kStage / 16), 0));
-      const uint64_t qd = S::kDescK | (q0 + (p * S::kQ + c * S::kQPart) / 16);
+    const uint64_t stage0 = stages >> 4;
+    auto full = [&](unsigned i) { return wait(kQbFull + i % S::kKStages, i / S::kKStages, 7); };
+    // Q piece p, part c x the K part number i
+    auto qk = [&](uint32_t d, int p, int c, unsigned i, bool first, bool last) {
+      const uint64_t kd = S::kDescK | (stage0 + __shfl_sync(0xffffffffu, i % S::kKStages * (S::kStage / 16), 0));
+      const uint32_t q = __shfl_sync(0xffffffffu, at + S::kColQ + p * (D / 2) + c * (S::kV / 2), 0);
       if (lead) {
 #pragma unroll
-        for (int k = 0; k < S::kV / 16; ++k) {
-          const int step = k % kSteps * 2, box = k / kSteps;
-          ptx::mma_f16_ss(d, qd + box * (kRows * S::kLine / 16) + step, kd + box * (kKeys * S::kLine / 16) + step, idS, !first || k > 0);
-        }
+        for (int k = 0; k < S::kV / 16; ++k)
+          ptx::mma_f16_ts(d, q + 8 * k, kd + k / kSteps * (kKeys * S::kLine / 16) + k % kSteps * 2, idS, !first || k > 0);
+        if (last) ptx::tc_commit(bar(kQbFree + i % S::kKStages));
       }
       __syncwarp();
     };
-    auto scores = [&](unsigned t, bool last) {
-      const unsigned ld = t * S::kLoads;
-      const uint32_t d = __shfl_sync(0xffffffffu, at + (t & 1) * kKeys, 0);
-      for (int c = 0; c < S::kHalves && ok; ++c) {
-        ok = full(ld + c, 7);
-        if (!ok) return;
-        ptx::tc_fence_after();
-        qk(d, 0, c, ld + c, c == 0);
-        release(ld + c);
-      }
-      for (int c = 0; c < S::kHalves && ok; ++c) {
-        ok = full(ld + S::kHalves + c, 7);
-        if (!ok) return;
-        ptx::tc_fence_after();
-        qk(d, 1, c, ld + S::kHalves + c, false);
-      }
-      for (int c = 0; c < S::kHalves; ++c) {
-        qk(d, 0, c, ld + S::kHalves + c, false);
-        release(ld + S::kHalves + c);
-      }
-      if (lead) {
-        ptx::tc_commit(bar(kQbS + (t & 1)));
-        if (last) ptx::tc_commit(bar(kQbQFree));
-      }
-      __syncwarp();
-    };
-    auto outputs = [&](unsigned t) {
-      const unsigned ld = t * S::kLoads + 2 * S::kHalves;
-      ok = wait(kQbP + (t & 1), t >> 1, 8) && wait(kQbChecked + (t & 1), t >> 1, 14) && full(ld, 9) && full(ld + 1, 9) &&
-           (t < 2 || wait(kQbOFree + (t & 1), (t >> 1) - 1, 16));
-      if (!ok) return;
-      ptx::tc_fence_after();
-      const uint32_t d = __shfl_sync(0xffffffffu, at + S::kColO + (t & 1) * S::kV, 0);
-      const uint32_t a = __shfl_sync(0xffffffffu, at + (t & 1) * kKeys, 0);
-      const uint64_t lo = S::kDescV | (stage0 + __shfl_sync(0xffffffffu, ld % kStages * (S::kStage / 16), 0));
-      const uint64_t hi = S::kDescV | (stage0 + __shfl_sync(0xffffffffu, (ld + 1) % kStages * (S::kStage / 16), 0));
-      if (lead) {
-        // weights of 32 keys: 16 columns of hi, 16 of lo
-        auto pv = [&](int p, uint64_t vd, bool first) {
-#pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            ptx::mma_f16_ts(d, a + k / 2 * 32 + p * 16 + k % 2 * 8, vd + k * (2 * 8 * S::kLine / 16), idO, !first || k > 0);
-        };
-        pv(0, lo, true);
-        ptx::tc_commit(bar(kQbFree + ld % kStages));
-        pv(1, hi, false);
-        pv(0, hi, false);
-        ptx::tc_commit(bar(kQbFree + (ld + 1) % kStages));
-        ptx::tc_commit(bar(kQbO + (t & 1)));
-      }
-      __syncwarp();
-    };
-    for (; ok && take(it);) {
+    while (ok && take(it)) {
       ok = wait(kQbQ, items, 6);
+      for (int i = 0; i < S::kQParts && lead; ++i) ptx::mbar_arrive(bar(kQbFree + (items * S::kQParts + n * S::kKParts + i) % S::kKStages));
+      __syncwarp();
       leave();
-      const int tiles = it.end[0] - it.begin[0];
-      if (S::kAhead && ok) scores(n, tiles == 1);
-      for (int i = 0; i < tiles && ok; ++i, ++n) {
-        if (!S::kAhead) scores(n, i + 1 == tiles);
-        if (S::kAhead && i + 1 < tiles) scores(n + 1, i + 2 == tiles);
-        if (ok) outputs(n);
+      for (int j = it.begin[0]; j < it.end[0] && ok; ++j, ++n) {
+        const unsigned lo = items * S::kQParts + n * S::kKParts, hi = lo + S::kHalves;
+        const uint32_t d = __shfl_sync(0xffffffffu, at + (n & 1) * kKeys, 0);
+        // the weights that lay there are done with
+        ok = n < 2 || wait(kQbO + (n & 1), (n >> 1) - 1, 8);
+#pragma unroll
+        for (int c = 0; c < S::kHalves; ++c) {
+          ok = ok && full(lo + c);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          qk(d, 0, c, lo + c, c == 0, true);
+        }
+#pragma unroll
+        for (int c = 0; c < S::kHalves; ++c) {
+          ok = ok && full(hi + c);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          qk(d, 1, c, hi + c, false, false);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < S::kHalves; ++c) qk(d, 0, c, hi + c, false, true);
+        if (lead) ptx::tc_commit(bar(kQbS + (n & 1)));
+        __syncwarp();
       }
     }
     if (lead) ptx::tc_commit(bar(kQbDrain));  // nothing is in flight when tensor memory is freed
     wait(kQbDrain, 0, 10);
+  } else if (warp == kOutputs) {
+    // ------------------------------------------------ products of weights and V: a warp of its own, so that its waits and the
+    // other's pass beside each other's products
+    constexpr uint32_t idO = ptx::idesc_f16(kRows, S::kV, false) | (1u << 16);
+    const bool lead = ptx::elect_one();
+    const uint32_t at = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t stage0 = stages >> 4;
+    auto full = [&](unsigned i) { return wait(kQbFull + S::kKStages + i % S::kVStages, i / S::kVStages, 9); };
+    while (ok && take(it)) {
+      leave();
+      for (int j = it.begin[0]; j < it.end[0] && ok; ++j, ++n) {
+        const unsigned b = n & 1, lo = 2 * n, hi = lo + 1, st_lo = S::kKStages + lo % S::kVStages, st_hi = S::kKStages + hi % S::kVStages;
+        ok = wait(kQbChecked + b, n >> 1, 14) && full(lo) && full(hi) && (n == 0 || wait(kQbOFree + ((n - 1) & 1), (n - 1) >> 1, 16)) &&
+             wait(kQbP + b, n >> 1, 8);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t d = __shfl_sync(0xffffffffu, at + S::kColO, 0), a = __shfl_sync(0xffffffffu, at + b * kKeys, 0);
+        const uint64_t lo_d = S::kDescV | (stage0 + __shfl_sync(0xffffffffu, st_lo * (S::kStage / 16), 0));
+        const uint64_t hi_d = S::kDescV | (stage0 + __shfl_sync(0xffffffffu, st_hi * (S::kStage / 16), 0));
+        if (lead) {
+          // weights of 32 keys: 16 columns of hi, 16 of lo
+          auto pv = [&](int p, uint64_t vd, bool first) {
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+              ptx::mma_f16_ts(d, a + k / 2 * 32 + p * 16 + k % 2 * 8, vd + k * (2 * 8 * S::kLine / 16), idO, !first || k > 0);
+          };
+          pv(0, lo_d, true);
+          ptx::tc_commit(bar(kQbFree + st_lo));
+          pv(1, hi_d, false);
+          pv(0, hi_d, false);
+          ptx::tc_commit(bar(kQbFree + st_hi));
+          ptx::tc_commit(bar(kQbO + b));
+        }
+        __syncwarp();
+      }
+    }
+    if (lead) ptx::tc_commit(bar(kQbDrain));
+    wait(kQbDrain, 0, 10);
   } else if (warp >= kAux) {
     // ------------------------------------------------ powers of two, and V's elements that are not finite
-    const int at = (warp - kAux) * 32 + lane;
     for (; ok && take(it); leave()) {
       const int kv = it.head / group;
       for (int j = it.begin[0]; j < it.end[0]; ++j, ++n) {
         const unsigned b = n & 1;
-        const int key = it.first + j * kKeys, slot = it.first / kKeys + it.sequence + j;
+        const int slot = it.first / kKeys + it.sequence + j;
         const bool known = XQ_IN(slot, W.slots, kChkPromptSlot);
-        float kp[kKeys / 64], vp[(S::kV + 63) / 64];
+        const size_t place = (known ? static_cast<size_t>(slot) * A.kv_heads : 0) + kv;
+        float vp[S::kV / 32];
 #pragma unroll
-        for (int x = 0; x < kKeys / 64; ++x)
-          kp[x] = key + x * 64 + at < A.tokens ? W.k_power[static_cast<size_t>(kv) * A.tokens + key + x * 64 + at] : 0.0f;
-#pragma unroll
-        for (int x = 0; x < (S::kV + 63) / 64; ++x)
-          vp[x] = x * 64 + at < S::kV && known
-                      ? W.v_power[(static_cast<size_t>(slot) * A.kv_heads + kv) * D + it.half * S::kV + x * 64 + at]
-                      : 0.0f;
-        const int owner = known ? W.owner[(static_cast<size_t>(slot) * A.kv_heads + kv) * S::kHalves + it.half] : -1;
+        for (int x = 0; x < S::kV / 32; ++x) vp[x] = W.v_power[place * D + it.half * S::kV + x * 32 + lane];
+        const float kp = W.k_power[place];
+        const bool whole = known && W.k_owner[place] == it.sequence && W.v_owner[place] == it.sequence;
         ok = n < 2 || wait(kQbPowerFree + b, (n >> 1) - 1, 17);
         if (!ok) break;
 #pragma unroll
-        for (int x = 0; x < kKeys / 64; ++x) sh_k[b][x * 64 + at] = kp[x];
-#pragma unroll
-        for (int x = 0; x < (S::kV + 63) / 64; ++x)
-          if (x * 64 + at < S::kV) sh_v[b][x * 64 + at] = vp[x];
-        if (owner != it.sequence && at == 0) atomicOr(&sh_odd[items & 1], 2u);
+        for (int x = 0; x < S::kV / 32; ++x) sh_v[b][x * 32 + lane] = vp[x];
+        if (lane == 0) {
+          sh_k[b] = kp;
+          if (!whole) atomicOr(&sh_odd[items & 1], 2u);
+        }
         arrive(kQbPower + b);
-        const unsigned ld = n * S::kLoads + 2 * S::kHalves;  // V lo's, hi's is the next
-        ok = wait(kQbFull + ld % kStages, ld / kStages, 15) && wait(kQbFull + (ld + 1) % kStages, (ld + 1) / kStages, 15);
+        const unsigned st[2] = {S::kKStages + 2 * n % S::kVStages, S::kKStages + (2 * n + 1) % S::kVStages};  // V's lo and hi
+        ok = wait(kQbFull + st[0], 2 * n / S::kVStages, 15) && wait(kQbFull + st[1], (2 * n + 1) / S::kVStages, 15);
         if (!ok) break;
         if (masked<kKeys>(P, it.place, j * kKeys)) {
           constexpr int kBlock = kKeys * S::kLine;  // bytes of a column block
           const int end = min(it.n - j * kKeys, kKeys) * S::kLine;  // of the sequence's rows in each; the pieces behind are anyone's
-          const uint32_t from = stages + (ld + 1) % kStages * S::kStage + at * 16;
+          const uint32_t from = stages + st[1] * S::kStage + lane * 16;
           bool found = false;
-          for (int x = end + at * 16; x < kBlock; x += 64 * 16) {
+          for (int x = end + lane * 16; x < kBlock; x += 32 * 16) {
 #pragma unroll
             for (int i = 0; i < 2 * S::kBoxes; ++i)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(stages + (ld + i % 2) % kStages * S::kStage + i / 2 * kBlock + x),
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(stages + st[i % 2] * S::kStage + i / 2 * kBlock + x),
                            "r"(0u) : "memory");
           }
 #pragma unroll 8
-          for (int x = 0; x < S::kStage; x += 64 * 16) {
-            if ((x + at * 16) % kBlock >= end) continue;
+          for (int x = 0; x < S::kStage; x += 32 * 16) {
+            if ((x + lane * 16) % kBlock >= end) continue;
             uint32_t w[4];
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from + x));
             if (odd_halves<kF16>(w[0]) | odd_halves<kF16>(w[1]) | odd_halves<kF16>(w[2]) | odd_halves<kF16>(w[3])) {
@@ -351,24 +370,73 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
   } else {
     const int row = (warp & 3) * 32 + lane, token = row / P.pack, part = row - token * P.pack;
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    if (warp < 4) {
-      // ---------------------------------------------- softmax: a thread is a row
+    if (warp < kOut) {
+      // ---------------------------------------------- softmax: a thread is a row, a group of warps has every second tile
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsSoft));
+      const unsigned b = warp >> 2;
       constexpr float kTop = 15.0f, kStart = 11.0f;  // log2 of weights: the largest, and where the reference starts anew
       const bool turned = !(A.scale > 0.0f);  // as in prompt_tile.cuh
       const float sign = A.scale < 0.0f ? -1.0f : 0.0f, cs = A.scale == 0.0f ? 1.0f : fabsf(A.scale) * 1.4426950408889634f;
+      // An item's queries into tensor memory, by the group that had the last tile of the item before (its scores were the last
+      // product of the queries there): hi and lo, the row's largest at 2^14 .. 2^15. In rolled loops: instructions that are
+      // seen once an item are waited for (unrolled, 20000 clocks).
+      auto query = [&](const Item& q) {
+        const bool there = token < P.tokens_tile && q.place + token < q.n;
+        const unsigned first = items * S::kQParts + n * S::kKParts;  // of the ring's parts
+        for (int i = 0; i < S::kQParts && ok; ++i) ok = wait(kQbFull + (first + i) % S::kKStages, (first + i) / S::kKStages, 22);
+        if (!ok) return;
+        // columns 4 c .. 4 c + 3
+        auto chunk = [&](int c) {
+          const unsigned box = c / 8, st = (first + box / S::kQBoxes) % S::kKStages;
+          float4 x;
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                       : "r"(stages + st * S::kStage + box % S::kQBoxes * (kRows * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)));
+          return x;
+        };
+        unsigned top = 0u;
+#pragma unroll 4
+        for (int c = 0; c < D / 4; ++c) {
+          const float4 x = chunk(c);
+          top = max(top, max(max(__float_as_uint(x.x) & 0x7FFFFFFFu, __float_as_uint(x.y) & 0x7FFFFFFFu),
+                             max(__float_as_uint(x.z) & 0x7FFFFFFFu, __float_as_uint(x.w) & 0x7FFFFFFFu)));
+        }
+        // a row that is not finite is computed by itself: its pieces need not hold it
+        const unsigned biased = !there || top == 0u ? 127u : min(254u, max(1u, 268u - min(267u, top >> 23)));
+        const float up = there ? __uint_as_float(biased << 23) : 0.0f;
+        sh_q[items & 1][row] = biased == 254u ? __uint_as_float(1u << 22) : __uint_as_float((254u - biased) << 23);
+#pragma unroll 1
+        for (int c = 0; c < D / 4; c += 4) {
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float4 x = chunk(c + i);
+            x = there ? make_float4(x.x * up, x.y * up, x.z * up, x.w * up) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            halves_of(x.x, x.y, &hi[2 * i], &lo[2 * i]);
+            halves_of(x.z, x.w, &hi[2 * i + 1], &lo[2 * i + 1]);
+          }
+          __syncwarp();
+          tmem_st8(tl + S::kColQ + 2 * c, hi);
+          tmem_st8(tl + S::kColQ + D / 2 + 2 * c, lo);
+        }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        arrive(kQbQ);
+      };
       for (; ok && take(it); leave()) {
+        if ((n & 1) != b) query(it);
+        if (!ok) break;
         const int place = it.place + token;
-        const bool live = token < P.tokens_tile && place < it.n;
         const int lim1 = place + 1, lim0 = A.window ? max(0, lim1 - A.window) : 0;
-        const float cq = live ? cs * W.q_power[(static_cast<size_t>(it.first) + place) * A.heads + it.head + part] : 0.0f;
         float e = -3.402823466e38f, l = 0.0f;
         for (int j = it.begin[0]; j < it.end[0]; ++j, ++n) {
-          const unsigned b = n & 1;
+          if ((n & 1) != b) continue;
           const int key = j * kKeys;
           ok = wait(kQbPower + b, n >> 1, 18) && wait(kQbS + b, n >> 1, 11);
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t ts = tl + b * kKeys;
+          const float cq = cs * sh_q[items & 1][row] * sh_k[b];
           const bool edge = masked<kKeys>(P, it.place, key);
           // 32 scores from column c on, those that the row does not see as -infinity
           ptx::f2 s[16];
@@ -378,11 +446,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
             tmem_ld32(ts + c, v);
             ptx::tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-              const float4 k = *reinterpret_cast<const float4*>(&sh_k[b][c + x]);
-              s[x / 2] = ptx::mul2(ptx::pk(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), ptx::pk(k.x, k.y));
-              s[x / 2 + 1] = ptx::mul2(ptx::pk(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), ptx::pk(k.z, k.w));
-            }
+            for (int x = 0; x < 32; x += 2) s[x / 2] = ptx::pk(__uint_as_float(v[x]), __uint_as_float(v[x + 1]));
             if (turned) {
 #pragma unroll
               for (int x = 0; x < 16; ++x) s[x] = ptx::mul2(s[x], ptx::pk(sign, sign));
@@ -403,18 +467,16 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
             for (int x = 0; x < 16; ++x) tops[x & 3] = max3(tops[x & 3], ptx::lo32(s[x]), ptx::hi32(s[x]));
           }
           const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * cq;
-          float f = 1.0f;
-          if (top - e > kTop) {  // the row's reference moves
-            const float next = top - kStart;
-            f = ex2(e - next);
+          if (top - e > kTop) {  // the row's reference moves, by steps of 4 so that the groups' are mostly the same
+            const float next = ceilf((top - kStart) * 0.25f) * 4.0f;
+            l *= ex2(e - next);
             e = next;
-            l *= f;
           }
           ok = n < 2 || wait(kQbOFree + b, (n >> 1) - 1, 19);
           if (!ok) break;
-          sh_move[b][row] = f;
+          sh_ref[b][row] = e;
           const ptx::f2 c2 = ptx::pk(cq, cq), e2 = ptx::pk(-e, -e);
-          ptx::f2 sum = ptx::pk(0.0f, 0.0f);
+          ptx::f2 sum[2] = {ptx::pk(0.0f, 0.0f), ptx::pk(0.0f, 0.0f)};
 #pragma unroll
           for (int c = 0; c < kKeys; c += 32) {
             load(c);
@@ -423,49 +485,61 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
             for (int x = 0; x < 16; ++x) {
               const ptx::f2 z = ptx::fma2(s[x], c2, e2);
               const float u = ex2(ptx::lo32(z)), v = ex2(ptx::hi32(z));
-              sum = ptx::add2(sum, ptx::pk(u, v));
+              sum[x & 1] = ptx::add2(sum[x & 1], ptx::pk(u, v));
               halves_of(u, v, &hi[x], &lo[x]);
             }
             __syncwarp();
             ptx::tmem_st16(ts + c, hi);  // into columns already read
             ptx::tmem_st16(ts + c + 16, lo);
           }
-          l += ptx::lo32(sum) + ptx::hi32(sum);
+          sum[0] = ptx::add2(sum[0], sum[1]);
+          l += ptx::lo32(sum[0]) + ptx::hi32(sum[0]);
           ptx::tmem_wait_st();
           ptx::tc_fence_before();
           arrive(kQbP + b);
           if (lane == 0) ptx::mbar_arrive(bar(kQbPowerFree + b));
         }
         if (!ok) break;
-        sh_sum[items & 1][row] = l;
+        sh_sum[items & 1][b][row] = make_float2(l, e);
         arrive(kQbSum + (items & 1));
       }
     } else {
       // ---------------------------------------------- outputs: a thread is a row
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsOut));
       for (; ok && take(it); leave()) {
         const int place = it.place + token, kv = it.head / group;
         const bool live = token < P.tokens_tile && place < it.n;
         ptx::f2 o[S::kV / 2];
 #pragma unroll
         for (int x = 0; x < S::kV / 2; ++x) o[x] = ptx::pk(0.0f, 0.0f);
+        float e = -3.402823466e38f;  // the outputs' reference: the largest of the tiles'
         for (int j = it.begin[0]; j < it.end[0]; ++j, ++n) {
           const unsigned b = n & 1;
           ok = wait(kQbP + b, n >> 1, 20) && wait(kQbO + b, n >> 1, 12) && wait(kQbPower + b, n >> 1, 21);
           if (!ok) break;
           ptx::tc_fence_after();
-          const float f = sh_move[b][row];
-          if (__any_sync(0xffffffffu, f != 1.0f)) {
+          const float ref = sh_ref[b][row];
+          float f = 1.0f;  // of this tile's
+          if (__any_sync(0xffffffffu, ref != e)) {
+            const float next = fmaxf(e, ref), g = ex2(e - next);
+            f = ex2(ref - next);
+            e = next;
 #pragma unroll
-            for (int x = 0; x < S::kV / 2; ++x) o[x] = ptx::mul2(o[x], ptx::pk(f, f));
+            for (int x = 0; x < S::kV / 2; ++x) o[x] = ptx::mul2(o[x], ptx::pk(g, g));
           }
-          const uint32_t from = tl + S::kColO + b * S::kV;
+          const bool scaled = __any_sync(0xffffffffu, f != 1.0f);
+          const uint32_t from = tl + S::kColO;
 #pragma unroll
-          for (int c = 0; c < S::kV; c += 16) {
-            uint32_t v[16];
-            ptx::tmem_ld16(from + c, v);
+          for (int c = 0; c < S::kV; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(from + c, v);
             ptx::tmem_wait_ld();
+            if (scaled) {
 #pragma unroll
-            for (int x = 0; x < 16; x += 4) {
+              for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
+            }
+#pragma unroll
+            for (int x = 0; x < 32; x += 4) {
               const float4 p = *reinterpret_cast<const float4*>(&sh_v[b][c + x]);
               o[(c + x) / 2] = ptx::fma2(ptx::pk(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), ptx::pk(p.x, p.y), o[(c + x) / 2]);
               o[(c + x) / 2 + 1] =
@@ -480,17 +554,39 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
         // ---- the rows' results
         ok = wait(kQbSum + (items & 1), items >> 1, 13);
         if (!ok) break;
-        const float sum = sh_sum[items & 1][row], inv = 1.0f / sum;
-        const size_t at = (static_cast<size_t>(it.first) + place) * A.heads + it.head + part;
-        const bool store = live && XQ_IN(at, static_cast<size_t>(A.tokens) * A.heads, kChkPromptRow);
-        float4* const out = reinterpret_cast<float4*>(static_cast<float*>(A.out) + at * D + it.half * S::kV);
+        const float2 s0 = sh_sum[items & 1][0][row], s1 = sh_sum[items & 1][1][row];
+        const float sum = s0.x * ex2(s0.y - e) + s1.x * ex2(s1.y - e), inv = 1.0f / sum;
+        const int at = (it.first + place) * A.heads + it.head + part;
+        const int to = live && XQ_IN(at, static_cast<size_t>(A.tokens) * A.heads, kChkPromptRow) ? at : -1;
         ptx::f2 odd = ptx::pk(sum * 0.0f, 0.0f);  // NaN if anything is not finite
 #pragma unroll
-        for (int x = 0; x < S::kV / 2; x += 2) {
-          odd = ptx::fma2(o[x], ptx::pk(0.0f, 0.0f), odd);
-          odd = ptx::fma2(o[x + 1], ptx::pk(0.0f, 0.0f), odd);
-          if (store)
-            out[x / 2] = make_float4(ptx::lo32(o[x]) * inv, ptx::hi32(o[x]) * inv, ptx::lo32(o[x + 1]) * inv, ptx::hi32(o[x + 1]) * inv);
+        for (int x = 0; x < S::kV / 2; ++x) odd = ptx::fma2(o[x], ptx::pk(0.0f, 0.0f), odd);
+        // 32 columns at a time through shared memory, so that a store has 4 rows' lines, not 32
+        const uint32_t mine = rows_out + (warp & 3) * 4096 + lane * 128, other = rows_out + (warp & 3) * 4096 + (lane >> 3) * 128;
+        int row_to[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) row_to[i] = __shfl_sync(0xffffffffu, to, 4 * i + (lane >> 3));
+#pragma unroll
+        for (int c = 0; c < S::kV; c += 32) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const ptx::f2 u = o[c / 2 + 2 * i], v = o[c / 2 + 2 * i + 1];
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mine + ((i ^ (lane & 7)) << 4)), "f"(ptx::lo32(u) * inv), "f"(ptx::hi32(u) * inv),
+                         "f"(ptx::lo32(v) * inv), "f"(ptx::hi32(v) * inv)
+                         : "memory");
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float4 y;
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
+                         : "r"(other + i * 512 + (((lane & 7) ^ ((4 * i + (lane >> 3)) & 7)) << 4))
+                         : "memory");
+            if (row_to[i] >= 0)
+              *reinterpret_cast<float4*>(static_cast<float*>(A.out) + static_cast<size_t>(row_to[i]) * D + it.half * S::kV + c + (lane & 7) * 4) = y;
+          }
+          __syncwarp();
         }
         const unsigned look = sh_odd[items & 1];
         bool meets = (look & 2u) != 0;  // pieces that do not hold the values, or an element that was put to 0
@@ -519,7 +615,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == kMma) ptx::tmem_dealloc(tmem, S::kAlloc);
+  if (warp == kScores) ptx::tmem_dealloc(tmem, S::kAlloc);
 }
 
 }  // namespace
@@ -529,14 +625,22 @@ cudaError_t PromptPiecesDim<D>::launch(PromptTileArgs& p, const PromptPieces& w,
   using S = PieceShape<D>;
   g_kv_launched.store(true, std::memory_order_relaxed);
   const PromptArgs& a = p.a;
-  const long long qs = static_cast<long long>(a.heads) * D, ks = static_cast<long long>(a.kv_heads) * D;
-  if (!encode_tma_heads(&p.q, false, w.q, D, a.heads, 2 * a.tokens, qs, S::kBox, p.pack, p.tokens_tile) ||
+  const long long ks = static_cast<long long>(a.kv_heads) * D;
+  if (!encode_tma_heads_f32(&p.q, a.q, D, a.heads, a.tokens, a.tokens == 1 ? static_cast<long long>(a.heads) * D : a.q_stride, p.pack, p.tokens_tile) ||
       !encode_tma_heads(&p.k, false, w.k, D, a.kv_heads, 2 * a.tokens, ks, S::kBox, 1, S::kKeys) ||
       !encode_tma_heads(&p.v, false, w.v, D, a.kv_heads, 2 * a.tokens, ks, S::kBox, 1, S::kKeys))
     return cudaErrorInvalidValue;
   static std::atomic<unsigned long long> allowed{0};
-  const cudaError_t e = allow_shared(prompt_pieces_kernel<D>, S::kSmem, allowed);
+  static std::atomic<int> registers{0};
+  cudaError_t e = allow_shared(prompt_pieces_kernel<D>, S::kSmem, allowed);
+  if (e == cudaSuccess && registers.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes f;
+    e = cudaFuncGetAttributes(&f, prompt_pieces_kernel<D>);
+    if (e == cudaSuccess) registers.store(f.numRegs, std::memory_order_relaxed);
+  }
   if (e != cudaSuccess) return e;
+  // the split of registers goes by 128 a thread at launch: with fewer its increase would wait forever
+  if (registers.load(std::memory_order_relaxed) != 128) return cudaErrorInvalidConfiguration;
   const long long items = (a.tokens / p.tokens_tile + static_cast<long long>(a.batch)) * p.units * S::kHalves;
   prompt_pieces_kernel<D><<<static_cast<int>(items < 152 ? items : 152), 32 * S::kWarps, S::kSmem, s>>>(p, w);
   return cudaGetLastError();

@@ -124,11 +124,15 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
     const bool lead = ptx::elect_one();
     unsigned loaded = 0, q_done[2] = {0u, 0u};
     bool ok = true;
-    for (unsigned round = 0; ok; ++round) {
-      Item it;
+    Item next;
+    auto find = [&](unsigned round) {
       const long long rank = static_cast<long long>(round) * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-      const bool there = next_item<kKeys, 1>(P, kTiles, rank, w, it);
-      if (!there) it.n = -1;
+      if (!next_item<kKeys, 1>(P, kTiles, rank, w, next)) next.n = -1;
+    };
+    find(0);
+    for (unsigned round = 0; ok; ++round) {
+      const Item it = next;
+      const bool there = it.n >= 0;
       if (round >= 2 && !wait(kPbItemFree + (round & 1), (round >> 1) + 1, 2)) break;
       if (lead) {
         sh_item[round & 1] = it;
@@ -164,6 +168,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
                           it.first + j * kKeys, bar(kPbFull + st));
           }
         }
+        if (j == it.begin[0]) find(round + 1);  // while the first copies are on their way
       }
       __syncwarp();
     }

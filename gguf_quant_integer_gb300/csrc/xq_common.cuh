@@ -283,6 +283,8 @@ bool encode_tma_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, u
 // box_rows x box_heads x box_dim elements, box_dim 64 (128-byte swizzle) or 32 (64-byte).
 bool encode_tma_heads(CUtensorMap* map, bool bf16, const void* base, int dim, int heads, int rows, long long stride, int box_dim,
                       int box_heads, int box_rows);
+// The same of fp32 rows, boxes 32 elements wide (128-byte swizzle).
+bool encode_tma_heads_f32(CUtensorMap* map, const void* base, int dim, int heads, int rows, long long stride, int box_heads, int box_rows);
 
 // y = x W^T for M > 64 tokens on the tensor-memory tile kernel; type is 12
 // (Q4_K), 14 (Q6_K), 8 (Q8_0) or 23 (IQ4_XS, with its codebook as 4
