@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
             }
           };
           float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < kKeys; c += 32) {
             load(c);
 #pragma unroll
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
           sh_ref[b][row] = e;
           const ptx::f2 c2 = ptx::pk(cq, cq), e2 = ptx::pk(-e, -e);
           ptx::f2 sum[2] = {ptx::pk(0.0f, 0.0f), ptx::pk(0.0f, 0.0f)};
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < kKeys; c += 32) {
             load(c);
             uint32_t hi[16], lo[16];
