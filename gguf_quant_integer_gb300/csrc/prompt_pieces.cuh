@@ -16,10 +16,12 @@
 // A CTA has 128 rows. Q and the weights are the products' first operands in tensor memory (Q in shared memory was read at
 // 107 clocks a product, of which the tensor cores need 64), scores are double-buffered there, so that the products of a
 // tile pass beside the softmax of the two before it. With head size 256 a CTA has half of V's columns, and tiles of 64
-// keys. Roles: two groups of 4 warps take the tiles' softmax in turn (a thread a row; each has a reference and a sum of
-// its own), and an item's last one the next item's queries; 4 warps add up outputs (a thread a row), then one that issues
-// the products of Q and K, one those of weights and V, one that copies, and one that brings the tiles' powers of two and
-// looks through V. Items as in prompt_tile.cuh.
+// keys. Roles: two groups of 4 warps share a tile's softmax (a thread has half a row's keys; the halves' maxima are
+// exchanged), 4 warps add up outputs (a thread a row), then one that issues the products of Q and K, one those of weights
+// and V, one that copies, and one that brings the tiles' powers of two and looks through V. Items as in prompt_tile.cuh.
+//
+// Loops are rolled wherever registers allow: many roles' code at once does not fit the instruction caches (unrolled, the
+// softmax's two passes alone made 5 sequences of 33 to 1500 take 195 us instead of 156).
 #pragma once
 
 #include "prompt_items.cuh"
@@ -75,7 +77,7 @@ struct PieceShape {
   static constexpr uint64_t kDescV = kCommon | (static_cast<uint64_t>(kKeys * kLine / 16) << 16);
 };
 
-enum PieceBar { kQbDrain, kQbQ, kQbItem, kQbItemFree = kQbItem + 2, kQbS = kQbItemFree + 2, kQbP = kQbS + 2,
+enum PieceBar { kQbDrain, kQbQ, kQbTop, kQbItem, kQbItemFree = kQbItem + 2, kQbS = kQbItemFree + 2, kQbP = kQbS + 2,
                 kQbO = kQbP + 2, kQbOFree = kQbO + 2, kQbPower = kQbOFree + 2, kQbPowerFree = kQbPower + 2, kQbChecked = kQbPowerFree + 2,
                 kQbSum = kQbChecked + 2, kQbFull = kQbSum + 2 };  // then a stage's full and free: K's, V's
 
@@ -100,24 +102,25 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
   __shared__ float sh_k[2];                             // the tile's powers of two, by tile & 1
   __shared__ __align__(16) float sh_v[2][S::kV];
   __shared__ float sh_ref[2][kRows];                    // the rows' references, by tile & 1
-  __shared__ float sh_q[2][kRows];                      // the queries' powers of two, by item & 1
-  __shared__ float2 sh_sum[2][2][kRows];                // sums of weights and their references, by item & 1 and group
+  __shared__ float sh_top[2][2][kRows];                 // largest scores of the halves, by tile & 1 and half
+  __shared__ float sh_sum[2][2][kRows];                 // sums of weights, by item & 1 and half
   const PromptArgs& A = P.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   auto bar = [&](int i) { return ptx::smem_addr(&bars[i]); };
   const uint32_t base = (ptx::smem_addr(smem_raw) + 1023u) & ~1023u, stages = base, rows_out = base + kStages * S::kStage;
   if (tid == 0) {
     ptx::mbar_init(bar(kQbDrain), 2);
-    ptx::mbar_init(bar(kQbQ), 4);
+    ptx::mbar_init(bar(kQbQ), 8);
+    ptx::mbar_init(bar(kQbTop), 8);
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(bar(kQbItem + b), 1);
       ptx::mbar_init(bar(kQbItemFree + b), 15);
       ptx::mbar_init(bar(kQbS + b), 1);
-      ptx::mbar_init(bar(kQbP + b), 4);
+      ptx::mbar_init(bar(kQbP + b), 8);
       ptx::mbar_init(bar(kQbO + b), 1);
       ptx::mbar_init(bar(kQbOFree + b), 4);
       ptx::mbar_init(bar(kQbPower + b), 1);
-      ptx::mbar_init(bar(kQbPowerFree + b), 8);
+      ptx::mbar_init(bar(kQbPowerFree + b), 12);
       ptx::mbar_init(bar(kQbChecked + b), 1);
       ptx::mbar_init(bar(kQbSum + b), 8);
     }
@@ -373,13 +376,14 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
     if (warp < kOut) {
       // ---------------------------------------------- softmax: a thread is a row, a group of warps has every second tile
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsSoft));
-      const unsigned b = warp >> 2;
+      const int half = warp >> 2;
+      float cq = 0.0f;  // the row's: of the scale and its query's power of two
       constexpr float kTop = 15.0f, kStart = 11.0f;  // log2 of weights: the largest, and where the reference starts anew
       const bool turned = !(A.scale > 0.0f);  // as in prompt_tile.cuh
       const float sign = A.scale < 0.0f ? -1.0f : 0.0f, cs = A.scale == 0.0f ? 1.0f : fabsf(A.scale) * 1.4426950408889634f;
-      // An item's queries into tensor memory, by the group that had the last tile of the item before (its scores were the last
-      // product of the queries there): hi and lo, the row's largest at 2^14 .. 2^15. In rolled loops: instructions that are
-      // seen once an item are waited for (unrolled, 20000 clocks).
+      // An item's queries into tensor memory (the scores of the last tile before, which the group has had, were the last
+      // product of those there): hi and lo, the row's largest at 2^14 .. 2^15, half of the columns by each group. (In unrolled
+      // loops, whose instructions are waited for at every item: 20000 clocks instead of 4000.)
       auto query = [&](const Item& q) {
         const bool there = token < P.tokens_tile && q.place + token < q.n;
         const unsigned first = items * S::kQParts + n * S::kKParts;  // of the ring's parts
@@ -404,9 +408,9 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
         // a row that is not finite is computed by itself: its pieces need not hold it
         const unsigned biased = !there || top == 0u ? 127u : min(254u, max(1u, 268u - min(267u, top >> 23)));
         const float up = there ? __uint_as_float(biased << 23) : 0.0f;
-        sh_q[items & 1][row] = biased == 254u ? __uint_as_float(1u << 22) : __uint_as_float((254u - biased) << 23);
+        cq = cs * (biased == 254u ? __uint_as_float(1u << 22) : __uint_as_float((254u - biased) << 23));
 #pragma unroll 1
-        for (int c = 0; c < D / 4; c += 4) {
+        for (int c = half * (D / 8); c < (half + 1) * (D / 8); c += 4) {
           uint32_t hi[8], lo[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -424,20 +428,20 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
         arrive(kQbQ);
       };
       for (; ok && take(it); leave()) {
-        if ((n & 1) != b) query(it);
+        query(it);
         if (!ok) break;
         const int place = it.place + token;
         const int lim1 = place + 1, lim0 = A.window ? max(0, lim1 - A.window) : 0;
         float e = -3.402823466e38f, l = 0.0f;
         for (int j = it.begin[0]; j < it.end[0]; ++j, ++n) {
-          if ((n & 1) != b) continue;
-          const int key = j * kKeys;
+          const unsigned b = n & 1;
+          const int key = j * kKeys + half * (kKeys / 2);
           ok = wait(kQbPower + b, n >> 1, 18) && wait(kQbS + b, n >> 1, 11);
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t ts = tl + b * kKeys;
-          const float cq = cs * sh_q[items & 1][row] * sh_k[b];
-          const bool edge = masked<kKeys>(P, it.place, key);
+          const uint32_t ts = tl + b * kKeys + half * (kKeys / 2);
+          const float c_tile = cq * sh_k[b];
+          const bool edge = masked<kKeys>(P, it.place, j * kKeys);
           // 32 scores from column c on, those that the row does not see as -infinity
           ptx::f2 s[16];
           auto load = [&](int c) {
@@ -461,24 +465,31 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
           };
           float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-          for (int c = 0; c < kKeys; c += 32) {
+          for (int c = 0; c < kKeys / 2; c += 32) {
             load(c);
 #pragma unroll
             for (int x = 0; x < 16; ++x) tops[x & 3] = max3(tops[x & 3], ptx::lo32(s[x]), ptx::hi32(s[x]));
           }
-          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * cq;
-          if (top - e > kTop) {  // the row's reference moves, by steps of 4 so that the groups' are mostly the same
-            const float next = ceilf((top - kStart) * 0.25f) * 4.0f;
+          float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * c_tile;
+          sh_top[b][half][row] = top;
+          arrive(kQbTop);
+          ok = wait(kQbTop, n, 23);
+          if (!ok) break;
+          top = fmaxf(top, sh_top[b][half ^ 1][row]);
+          if (top - e > kTop) {  // the row's reference moves
+            const float next = top - kStart;
             l *= ex2(e - next);
             e = next;
           }
-          ok = n < 2 || wait(kQbOFree + b, (n >> 1) - 1, 19);
-          if (!ok) break;
-          sh_ref[b][row] = e;
-          const ptx::f2 c2 = ptx::pk(cq, cq), e2 = ptx::pk(-e, -e);
+          if (half == 0) {
+            ok = n < 2 || wait(kQbOFree + b, (n >> 1) - 1, 19);
+            if (!ok) break;
+            sh_ref[b][row] = e;
+          }
+          const ptx::f2 c2 = ptx::pk(c_tile, c_tile), e2 = ptx::pk(-e, -e);
           ptx::f2 sum[2] = {ptx::pk(0.0f, 0.0f), ptx::pk(0.0f, 0.0f)};
 #pragma unroll 1
-          for (int c = 0; c < kKeys; c += 32) {
+          for (int c = 0; c < kKeys / 2; c += 32) {
             load(c);
             uint32_t hi[16], lo[16];
 #pragma unroll
@@ -500,7 +511,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
           if (lane == 0) ptx::mbar_arrive(bar(kQbPowerFree + b));
         }
         if (!ok) break;
-        sh_sum[items & 1][b][row] = make_float2(l, e);
+        sh_sum[items & 1][half][row] = l;
         arrive(kQbSum + (items & 1));
       }
     } else {
@@ -512,32 +523,25 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
         ptx::f2 o[S::kV / 2];
 #pragma unroll
         for (int x = 0; x < S::kV / 2; ++x) o[x] = ptx::pk(0.0f, 0.0f);
-        float e = -3.402823466e38f;  // the outputs' reference: the largest of the tiles'
+        float e = -3.402823466e38f;  // the outputs' reference
         for (int j = it.begin[0]; j < it.end[0]; ++j, ++n) {
           const unsigned b = n & 1;
           ok = wait(kQbP + b, n >> 1, 20) && wait(kQbO + b, n >> 1, 12) && wait(kQbPower + b, n >> 1, 21);
           if (!ok) break;
           ptx::tc_fence_after();
           const float ref = sh_ref[b][row];
-          float f = 1.0f;  // of this tile's
           if (__any_sync(0xffffffffu, ref != e)) {
-            const float next = fmaxf(e, ref), g = ex2(e - next);
-            f = ex2(ref - next);
-            e = next;
+            const float g = ex2(e - ref);
+            e = ref;
 #pragma unroll
             for (int x = 0; x < S::kV / 2; ++x) o[x] = ptx::mul2(o[x], ptx::pk(g, g));
           }
-          const bool scaled = __any_sync(0xffffffffu, f != 1.0f);
           const uint32_t from = tl + S::kColO;
 #pragma unroll
           for (int c = 0; c < S::kV; c += 32) {
             uint32_t v[32];
             tmem_ld32(from + c, v);
             ptx::tmem_wait_ld();
-            if (scaled) {
-#pragma unroll
-              for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
-            }
 #pragma unroll
             for (int x = 0; x < 32; x += 4) {
               const float4 p = *reinterpret_cast<const float4*>(&sh_v[b][c + x]);
@@ -554,8 +558,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
         // ---- the rows' results
         ok = wait(kQbSum + (items & 1), items >> 1, 13);
         if (!ok) break;
-        const float2 s0 = sh_sum[items & 1][0][row], s1 = sh_sum[items & 1][1][row];
-        const float sum = s0.x * ex2(s0.y - e) + s1.x * ex2(s1.y - e), inv = 1.0f / sum;
+        const float sum = sh_sum[items & 1][0][row] + sh_sum[items & 1][1][row], inv = 1.0f / sum;
         const int at = (it.first + place) * A.heads + it.head + part;
         const int to = live && XQ_IN(at, static_cast<size_t>(A.tokens) * A.heads, kChkPromptRow) ? at : -1;
         ptx::f2 odd = ptx::pk(sum * 0.0f, 0.0f);  // NaN if anything is not finite
