@@ -551,8 +551,8 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
             }
           }
           ptx::tc_fence_before();
-          arrive(kQbOFree + b);
-          if (lane == 0) ptx::mbar_arrive(bar(kQbPowerFree + b));
+          if (j + 1 < it.end[0]) arrive(kQbOFree + b);  // behind the last tile the results go through it
+          arrive(kQbPowerFree + b);
         }
         if (!ok) break;
         // ---- the rows' results
@@ -564,20 +564,30 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
         ptx::f2 odd = ptx::pk(sum * 0.0f, 0.0f);  // NaN if anything is not finite
 #pragma unroll
         for (int x = 0; x < S::kV / 2; ++x) odd = ptx::fma2(o[x], ptx::pk(0.0f, 0.0f), odd);
-        // 32 columns at a time through shared memory, so that a store has 4 rows' lines, not 32
-        const uint32_t mine = rows_out + (warp & 3) * 4096 + lane * 128, other = rows_out + (warp & 3) * 4096 + (lane >> 3) * 128;
-        int row_to[8];
+        // Back into tensor memory, and from there 32 columns at a time in a rolled loop (see above), through shared memory, so
+        // that a store has 4 rows' lines, not 32.
 #pragma unroll
-        for (int i = 0; i < 8; ++i) row_to[i] = __shfl_sync(0xffffffffu, to, 4 * i + (lane >> 3));
+        for (int c = 0; c < S::kV; c += 16) {
+          uint32_t w[16];
 #pragma unroll
-        for (int c = 0; c < S::kV; c += 32) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const ptx::f2 u = o[c / 2 + 2 * i], v = o[c / 2 + 2 * i + 1];
-            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mine + ((i ^ (lane & 7)) << 4)), "f"(ptx::lo32(u) * inv), "f"(ptx::hi32(u) * inv),
-                         "f"(ptx::lo32(v) * inv), "f"(ptx::hi32(v) * inv)
-                         : "memory");
+          for (int x = 0; x < 16; x += 2) {
+            const ptx::f2 u = ptx::mul2(o[(c + x) / 2], ptx::pk(inv, inv));
+            w[x] = __float_as_uint(ptx::lo32(u)), w[x + 1] = __float_as_uint(ptx::hi32(u));
           }
+          ptx::tmem_st16(tl + S::kColO + c, w);
+        }
+        ptx::tmem_wait_st();
+        const uint32_t mine = rows_out + (warp & 3) * 4096 + lane * 128, other = rows_out + (warp & 3) * 4096 + (lane >> 3) * 128;
+#pragma unroll 1
+        for (int c = 0; c < S::kV; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(tl + S::kColO + c, v);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + ((i ^ (lane & 7)) << 4)), "r"(v[4 * i]), "r"(v[4 * i + 1]),
+                         "r"(v[4 * i + 2]), "r"(v[4 * i + 3])
+                         : "memory");
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -586,11 +596,14 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
                          : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
                          : "r"(other + i * 512 + (((lane & 7) ^ ((4 * i + (lane >> 3)) & 7)) << 4))
                          : "memory");
-            if (row_to[i] >= 0)
-              *reinterpret_cast<float4*>(static_cast<float*>(A.out) + static_cast<size_t>(row_to[i]) * D + it.half * S::kV + c + (lane & 7) * 4) = y;
+            const int row_to = __shfl_sync(0xffffffffu, to, 4 * i + (lane >> 3));
+            if (row_to >= 0)
+              *reinterpret_cast<float4*>(static_cast<float*>(A.out) + static_cast<size_t>(row_to) * D + it.half * S::kV + c + (lane & 7) * 4) = y;
           }
           __syncwarp();
         }
+        ptx::tc_fence_before();
+        arrive(kQbOFree + ((n - 1) & 1));
         const unsigned look = sh_odd[items & 1];
         bool meets = (look & 2u) != 0;  // pieces that do not hold the values, or an element that was put to 0
         if (look & 1u) {
