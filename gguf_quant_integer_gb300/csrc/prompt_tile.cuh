@@ -45,8 +45,9 @@ struct PromptShape {
   static constexpr int kBox = D % 64 == 0 ? 64 : 32;            // elements of a swizzled row
   static constexpr int kLine = kBox * 2, kBoxes = D / kBox;
   static constexpr int kQ = kRows * D * 2, kStage = kKeys * D * 2;  // bytes: Q of a row tile; K or V of a tile
-  static constexpr int kStages = D == 256 ? 2 : D == 128 ? 5 : D == 96 ? 7 : 10;
-  static constexpr int kSmem = kTiles * kQ + kStages * kStage + 1024;
+  static constexpr int kStages = D == 256 ? 2 : D == 128 ? 4 : D == 96 ? 6 : 9;
+  static constexpr int kRowsOut = 4 * kTiles * 2048;  // results on their way out: 32 rows x 64 bytes of each softmax warp
+  static constexpr int kSmem = kTiles * kQ + kStages * kStage + kRowsOut + 1024;
   static constexpr int kColS = 0, kColO = 2 * kKeys, kAlloc = 512;
   static constexpr int kWarps = 4 * kTiles + 4;
   static_assert(kColO + kTiles * D <= kAlloc && kSmem <= 227 * 1024 - 1024, "one CTA fits the SM");
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
         if (masked<kKeys>(P, it.place, j * kKeys) || (second && masked<kKeys>(P, it.place + P.tokens_tile, j * kKeys))) {
           const uint32_t from = base + kTiles * S::kQ + st * S::kStage + ((warp - kCheck) * 32 + lane) * 16;
           bool found = false;
-#pragma unroll 8
+#pragma unroll 2
           for (int x = 0; x < S::kStage; x += 64 * 16) {
             uint32_t w[4];
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from + x));
@@ -392,26 +393,36 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
       const float sum = ptx::lo32(l) + ptx::hi32(l), inv = 1.0f / sum;
       const size_t at = (static_cast<size_t>(it.first) + place) * A.heads + it.head + part;
       const bool store = live && XQ_IN(at, static_cast<size_t>(A.tokens) * A.heads, kChkPromptRow);
-      uint4* const out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + at * D);
+      const int to_row = store ? static_cast<int>(at) : -1;
+      const uint32_t rows_out = base + kTiles * S::kQ + kStages * S::kStage, mine = rows_out + warp * 2048 + lane * 64;
       float odd[4] = {sum * 0.0f, 0.0f, 0.0f, 0.0f};  // NaN if anything is not finite
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         uint32_t w[32];
+        __syncwarp();
         tmem_ld32(to + c, w);
         ptx::tmem_wait_ld();
 #pragma unroll
         for (int x = 0; x < 32; ++x) odd[x & 3] = fmaf(__uint_as_float(w[x]), 0.0f, odd[x & 3]);
-        if (store) {
 #pragma unroll
-          for (int x = 0; x < 32; x += 8) {
-            uint4 y;
-            y.x = pack2<TYPE>(__uint_as_float(w[x]) * inv, __uint_as_float(w[x + 1]) * inv);
-            y.y = pack2<TYPE>(__uint_as_float(w[x + 2]) * inv, __uint_as_float(w[x + 3]) * inv);
-            y.z = pack2<TYPE>(__uint_as_float(w[x + 4]) * inv, __uint_as_float(w[x + 5]) * inv);
-            y.w = pack2<TYPE>(__uint_as_float(w[x + 6]) * inv, __uint_as_float(w[x + 7]) * inv);
-            out[(c + x) / 8] = y;
-          }
+        for (int x = 0; x < 4; ++x) {
+          uint32_t y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = pack2<TYPE>(__uint_as_float(w[8 * x + 2 * i]) * inv, __uint_as_float(w[8 * x + 2 * i + 1]) * inv);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(mine + ((x ^ (lane >> 1 & 3)) << 4)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r8 = 8 * i + (lane >> 2), row_to = __shfl_sync(0xffffffffu, to_row, r8);
+          uint4 y;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                       : "r"(rows_out + warp * 2048 + r8 * 64 + (((lane & 3) ^ (r8 >> 1 & 3)) << 4))
+                       : "memory");
+          if (row_to >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(A.out) + static_cast<size_t>(row_to) * D + c + (lane & 3) * 8) = y;
+        }
+        __syncwarp();
       }
       ptx::tc_fence_before();
       bool meets = false;  // an element that was put to 0
