@@ -25,8 +25,9 @@ __device__ unsigned int g_lora_error;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kCluster = 8;
-constexpr int kRankBlock = 64;        // ranks of a pass over x
-constexpr int kPartFloats = 8192;     // partial sums of the warps: [8 / MT][16 * MT][64]
+// Ranks of a pass over x. Few: what matters with few rows is how many instructions are seen for the first time.
+__host__ __device__ constexpr int rank_block(int mt) { return mt == 1 ? 16 : 32; }
+__host__ __device__ constexpr int sum_bytes(int mt) { return 8 / mt * 16 * mt * rank_block(mt) * 4; }  // the warps' parts of it
 constexpr int kJobsGrid = 512;        // jobs of a projection with clusters of their own
 constexpr int kMaxAdapters = 8192;
 
@@ -44,7 +45,7 @@ __host__ __device__ constexpr int align16(int x) { return (x + 15) & ~15; }
 // sums, t as pairs.
 __host__ __device__ constexpr int part_bytes(int rows, int rank) { return rows * rank * 4; }
 inline int shared_bytes(int rows, int rank, int n) {
-  return part_bytes(rows, rank) + std::max({kPartFloats * 4, rows * pair_stride(rank), align16(n * 4)});
+  return part_bytes(rows, rank) + std::max({sum_bytes(rows / 16), rows * pair_stride(rank), align16(n * 4)});
 }
 
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -60,6 +61,17 @@ __device__ __forceinline__ void split(float x, uint32_t* hi, uint32_t* lo) {
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(*lo) : "f"(rest));
 }
 
+// Loads that are issued where they stand: a warp's loads go out together, before the products that wait for the first.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float4 load_floats(const float* p) {
+  const uint4 v = load16(p);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+}
+
 // W consecutive weights (8, 4 or 2) as tf32 numbers: hi, and lo for fp32 ones.
 template <int TYPE, int W>
 struct Weights {
@@ -67,20 +79,19 @@ struct Weights {
   __device__ __forceinline__ void load(const void* p, size_t at, bool there) {
     constexpr int kWords = TYPE == kF32 ? W : W / 2;
     const uint32_t* const f = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p) + at * (TYPE == kF32 ? 4 : 2));
-    if (!there) {
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) raw[i] = 0u;
-    } else if constexpr (kWords >= 4) {
+    for (int i = 0; i < kWords; ++i) raw[i] = 0u;
+    if (!there) return;
+    if constexpr (kWords >= 4) {
 #pragma unroll
       for (int i = 0; i < kWords; i += 4) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(f + i));
+        const uint4 v = load16(f + i);
         raw[i] = v.x, raw[i + 1] = v.y, raw[i + 2] = v.z, raw[i + 3] = v.w;
       }
     } else if constexpr (kWords == 2) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(f));
-      raw[0] = v.x, raw[1] = v.y;
+      asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(raw[0]), "=r"(raw[1]) : "l"(f));
     } else {
-      raw[0] = __ldg(f);
+      asm volatile("ld.global.b32 %0, [%1];" : "=r"(raw[0]) : "l"(f));
     }
   }
   // the i-th, i even, and the one after it
@@ -129,17 +140,35 @@ struct JobShared {
   int sums[kWarps];
 };
 
+// The ids of up to 8 x 32 rows from row m on (those before row `end`), a lane's in steps of 32.
+struct Ids {
+  int id[8];
+  __device__ __forceinline__ void load(const int32_t* ids, int m, int end) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) id[i] = m + 32 * i + static_cast<int>(threadIdx.x & 31) < end ? ids[m + 32 * i + (threadIdx.x & 31)] : -1;
+  }
+};
+
 // The j-th job of a projection with n adapters: its adapter, and its rows in sh.rows; returns how many, 0 if there is none.
-__device__ int find_job(const int32_t* ids, int M, int n, int T, int j, int* counts, JobShared& sh) {
+// A warp has a run of the rows; up to 256 of them it reads once.
+__device__ __noinline__ int find_job(const int32_t* ids, int M, int n, int T, int j, int* counts, JobShared& sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int run = ((M + kThreads - 1) / kThreads) * 32, m0 = warp * run, m1 = min(M, m0 + run);
+  Ids x;
+  x.load(ids, m0, m1);
   for (int i = tid; i < n; i += kThreads) counts[i] = 0;
   if (tid == 0) sh.adapter = -1;
   __syncthreads();
-  for (int m0 = warp * 32; m0 < M; m0 += kThreads) {
-    const int id = m0 + lane < M ? ids[m0 + lane] : -1;
-    if (id >= n) atomicCAS(&g_lora_error, 0u, kOpsBadAdapter);
-    const unsigned same = __match_any_sync(0xffffffffu, id);
-    if (id >= 0 && id < n && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&counts[id], __popc(same));
+  for (int m = m0; m < m1; m += 256) {
+    if (m > m0) x.load(ids, m, m1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (m + 32 * i >= m1) break;
+      const int id = x.id[i];
+      if (id >= n) atomicCAS(&g_lora_error, 0u, kOpsBadAdapter);
+      const unsigned same = __match_any_sync(0xffffffffu, id);
+      if (id >= 0 && id < n && (same & ((1u << lane) - 1u)) == 0) atomicAdd(&counts[id], __popc(same));
+    }
   }
   __syncthreads();
   // jobs are numbered by adapter: a thread's adapters are neighbours
@@ -166,20 +195,26 @@ __device__ int find_job(const int32_t* ids, int M, int n, int T, int j, int* cou
   const int adapter = sh.adapter;
   if (adapter < 0) return 0;
   const int lo = sh.chunk * T, have = min(T, counts[adapter] - lo);
-  // each warp's rows, a run of them: how many before it, then their places
-  const int run = ((M + kThreads - 1) / kThreads) * 32, m1 = min(M, (warp + 1) * run);
+  // the warps' numbers of its rows, then their places
   int mine = 0;
-  for (int m = warp * run; m < m1; m += 32) mine += __popc(__ballot_sync(0xffffffffu, m + lane < M && ids[m + lane] == adapter));
+  for (int m = m0; m < m1; m += 256) {
+    if (run > 256) x.load(ids, m, m1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mine += __popc(__ballot_sync(0xffffffffu, x.id[i] == adapter));
+  }
   if (lane == 0) sh.sums[warp] = mine;
   __syncthreads();
   int at = 0;
   for (int w = 0; w < warp; ++w) at += sh.sums[w];
-  for (int m = warp * run; m < m1 && at < lo + have; m += 32) {
-    const bool is = m + lane < M && ids[m + lane] == adapter;
-    const unsigned all = __ballot_sync(0xffffffffu, is);
-    const int place = at + __popc(all & ((1u << lane) - 1u)) - lo;
-    if (is && place >= 0 && place < have) sh.rows[place] = m + lane;
-    at += __popc(all);
+  for (int m = m0; m < m1 && at < lo + have; m += 256) {
+    if (run > 256) x.load(ids, m, m1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const unsigned all = __ballot_sync(0xffffffffu, x.id[i] == adapter);
+      const int place = at + __popc(all & ((1u << lane) - 1u)) - lo;
+      if (x.id[i] == adapter && place >= 0 && place < have) sh.rows[place] = m + 32 * i + lane;
+      at += __popc(all);
+    }
   }
   __syncthreads();
   return have;
@@ -194,35 +229,58 @@ __device__ __forceinline__ int pair_place(int r, int rank) {
   return c0 + (q >> 1) * 8 + t * 2 + (q & 1);
 }
 
-// The products of W * 4 ranks from r0 on: t (pairs) x B of 32 columns.
-template <int TYPE, int MT, int W>
-__device__ __forceinline__ void expand(float (&acc)[MT][4][4], const AdapterProj& p, size_t b_row, const int (&col)[4], int r0,
-                                       const uint8_t* pairs, int stride, int tiles) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  Weights<TYPE, W> w[4];
+// B's W * 4 ranks from r0 on, of a lane's column in each of four products: columns are dealt out so that the results' lane t
+// has columns 4 t .. 4 t + 3 and 16 more than those.
+template <int TYPE, int W>
+__device__ __forceinline__ void load_columns(Weights<TYPE, W> (&w)[4], const AdapterProj& p, size_t b_row, int n0, int r0) {
+  const int g = (threadIdx.x & 31) >> 2;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w[j].load(p.b, (b_row + col[j]) * p.rank + r0 + t * W, col[j] < p.N);
+  for (int j = 0; j < 4; ++j) {
+    const int col = n0 + (j >> 1) * 16 + (g >> 1) * 4 + (j & 1) * 2 + (g & 1);
+    w[j].load(p.b, (b_row + col) * p.rank + r0 + (threadIdx.x & 3) * W, col < p.N);
+  }
+}
+// t (pairs) x those.
+template <int TYPE, int MH, int W>
+__device__ __forceinline__ void expand(float (&acc)[MH][4][4], const Weights<TYPE, W> (&w)[4], int r0, const uint8_t* pairs, int stride, int tiles) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int s = 0; s < W / 2; ++s) {
     uint32_t bhi[4][2], blo[4][2];
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j].get(2 * s, bhi[j], blo[j]);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (mt < tiles) {
-        const uint8_t* const from = pairs + (mt * 16 + g) * stride + (r0 + 8 * s + 2 * t) * 8;
-        const uint4 a = *reinterpret_cast<const uint4*>(from), b = *reinterpret_cast<const uint4*>(from + 8 * stride);
-        const uint32_t hi[4] = {a.x, b.x, a.z, b.z}, lo[4] = {a.y, b.y, a.w, b.w};
+    for (int m = 0; m < MH; ++m) {
+      if (m >= tiles) break;
+      const uint8_t* const from = pairs + (m * 16 + g) * stride + (r0 + 8 * s + 2 * t) * 8;
+      const uint4 a = *reinterpret_cast<const uint4*>(from), b = *reinterpret_cast<const uint4*>(from + 8 * stride);
+      const uint32_t hi[4] = {a.x, b.x, a.z, b.z}, lo[4] = {a.y, b.y, a.w, b.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) product<TYPE>(acc[mt][j], hi, lo, bhi[j], blo[j]);
-      }
+      for (int j = 0; j < 4; ++j) product<TYPE>(acc[m][j], hi, lo, bhi[j], blo[j]);
     }
   }
 }
 
+// The same of up to 32 rows, by each warp for itself: jobs are numbered by their first rows.
+__device__ __forceinline__ int find_job_32(const int32_t* ids, int M, int n, int T, int j, JobShared& sh) {
+  const int lane = threadIdx.x & 31, id = lane < M ? ids[lane] : -1;
+  if (id >= n) atomicCAS(&g_lora_error, 0u, kOpsBadAdapter);
+  const unsigned same = __match_any_sync(0xffffffffu, id);
+  const int place = __popc(same & ((1u << lane) - 1u));  // among the adapter's rows
+  unsigned first = __ballot_sync(0xffffffffu, id >= 0 && id < n && place % T == 0);
+  for (int i = 0; i < j; ++i) first &= first - 1;
+  if (first == 0) return 0;
+  const int lead = __ffs(first) - 1, lo = __shfl_sync(0xffffffffu, place, lead);
+  const unsigned all = __shfl_sync(0xffffffffu, same, lead);
+  if ((all >> lane & 1) && place >= lo && place < lo + T) sh.rows[place - lo] = lane;  // all warps write the same
+  if (lane == lead) sh.adapter = id;
+  __syncwarp();
+  return min(T, __popc(all) - lo);
+}
+
 template <int TYPE, int MT>
 __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant__ LoraArgs A, const LoraGrid G) {
-  constexpr int T = 16 * MT, kSplit = kWarps / MT;  // warps that share out a CTA's part of K
+  constexpr int T = 16 * MT, kSplit = kWarps / MT, kRankBlock = rank_block(MT);  // kSplit warps share out a CTA's part of K
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ JobShared sh;
   const AdapterProj& p = A.p[G.first + blockIdx.y];
@@ -232,9 +290,15 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
   uint8_t* const rest = smem + part_bytes(T, G.rank_most);
   const int rank = p.rank, K = p.K, N = p.N;
   for (int job = blockIdx.x / kCluster; job < G.jobs; job += gridDim.x / kCluster) {
-    const int have = find_job(A.ids, A.M, p.n, T, job, reinterpret_cast<int*>(rest), sh);
+    const int have = A.M <= 32 ? find_job_32(A.ids, A.M, p.n, T, job, sh) : find_job(A.ids, A.M, p.n, T, job, reinterpret_cast<int*>(rest), sh);
     if (have == 0) return;  // nor are there later ones; so for all of the cluster
     const int id = sh.adapter, tiles = (have + 15) / 16;
+    const size_t b_row = static_cast<size_t>(id) * N;
+    constexpr int kStep = kCluster * kWarps * 32;
+    constexpr bool kAhead = TYPE != kF32;  // the next 32 ranks' weights are loaded beside a block's products
+    Weights<TYPE, 8> w[4];
+    int n0 = (cta * kWarps + warp) * 32;
+    if (MT == 1 && kAhead && rank >= 32 && n0 < N) load_columns(w, p, b_row, n0, 0);
     // ---- t's part from this CTA's K: warp (mt, ks) has 16 rows and a share of the 32-element chunks
     const int chunks = K / 32, mt = warp % MT, ks = warp / MT;
     const int c0 = chunks * cta / kCluster, c1 = chunks * (cta + 1) / kCluster;
@@ -250,39 +314,53 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
       for (int n = 0; n < kRankBlock / 8; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
       if (mt < tiles) {
         const size_t a0 = (static_cast<size_t>(id) * rank + rb + g) * K + t * 8;
-        for (int c = k0; c < k1; ++c) {
-          float xs[2][8];
+        float4 x[4];  // of the next chunk: two rows, 8 elements each
+        auto load_x = [&](int c) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float4* const f = reinterpret_cast<const float4*>((i ? x1 : x0) + c * 32);
-            const bool there = i ? row1 : row0;
-            const float4 u = there ? f[0] : make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = there ? f[1] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            xs[i][0] = u.x, xs[i][1] = u.y, xs[i][2] = u.z, xs[i][3] = u.w, xs[i][4] = v.x, xs[i][5] = v.y, xs[i][6] = v.z, xs[i][7] = v.w;
-          }
-          uint32_t hi[4][4], lo[4][4];
+          for (int i = 0; i < 4; ++i) x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (row0 && c < k1) x[0] = load_floats(x0 + c * 32), x[1] = load_floats(x0 + c * 32 + 4);
+          if (row1 && c < k1) x[2] = load_floats(x1 + c * 32), x[3] = load_floats(x1 + c * 32 + 4);
+        };
+        constexpr int kN = kRankBlock / 8;
+        Weights<TYPE, 8> a_next[kN];
+        auto load_a = [&](int c) {
+#pragma unroll
+          for (int n = 0; n < kN; ++n) a_next[n].load(p.a, a0 + static_cast<size_t>(n * 8) * K + c * 32, n < nt && c < k1);
+        };
+        load_x(k0);
+        load_a(k0);
+#pragma unroll 1
+        for (int c = k0; c < k1; ++c) {
+          const float xs[2][8] = {{x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w},
+                                  {x[2].x, x[2].y, x[2].z, x[2].w, x[3].x, x[3].y, x[3].z, x[3].w}};
+          Weights<TYPE, 8> aw[kN];
+#pragma unroll
+          for (int n = 0; n < kN; ++n) aw[n] = a_next[n];
+          load_x(c + 1);
+          load_a(c + 1);
+          float d[kN][4];
+#pragma unroll
+          for (int n = 0; n < kN; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.0f;
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            split(xs[0][2 * s], &hi[s][0], &lo[s][0]);
-            split(xs[1][2 * s], &hi[s][1], &lo[s][1]);
-            split(xs[0][2 * s + 1], &hi[s][2], &lo[s][2]);
-            split(xs[1][2 * s + 1], &hi[s][3], &lo[s][3]);
-          }
+            uint32_t hi[4], lo[4];
+            split(xs[0][2 * s], &hi[0], &lo[0]);
+            split(xs[1][2 * s], &hi[1], &lo[1]);
+            split(xs[0][2 * s + 1], &hi[2], &lo[2]);
+            split(xs[1][2 * s + 1], &hi[3], &lo[3]);
 #pragma unroll
-          for (int n = 0; n < kRankBlock / 8; ++n) {
-            if (n < nt) {
-              Weights<TYPE, 8> w;
-              w.load(p.a, a0 + static_cast<size_t>(n * 8) * K + c * 32, true);
-              float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-              for (int s = 0; s < 4; ++s) {
+            for (int n = 0; n < kN; ++n) {
+              if (n < nt) {
                 uint32_t bhi[2], blo[2];
-                w.get(2 * s, bhi, blo);
-                product<TYPE>(d, hi[s], lo[s], bhi, blo);
+                aw[n].get(2 * s, bhi, blo);
+                product<TYPE>(d[n], hi, lo, bhi, blo);
               }
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[n][i] += d[i];
             }
           }
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][i] += d[n][i];
         }
 #pragma unroll
         for (int n = 0; n < kRankBlock / 8; ++n) {
@@ -308,73 +386,102 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
       __syncthreads();
     }
     cluster_sync();
-    // ---- t: the parts of all CTAs in order, each CTA an eighth of it, which it hands to all
+    // ---- t: the parts of all CTAs in order. Few rows: each CTA adds them all up; more: an eighth of them, which it hands to all
     const float scale = p.scales ? p.scales[id] : 1.0f;
     const int quads = tiles * 4 * rank, stride = pair_stride(rank);  // groups of four ranks
-    for (int i = cta * kThreads + tid; i < quads; i += kCluster * kThreads) {
+    for (int i = MT == 1 ? tid : cta * kThreads + tid; i < quads; i += (MT == 1 ? 1 : kCluster) * kThreads) {
+      float4 v[kCluster];
+#pragma unroll
+      for (int c = 0; c < kCluster; ++c) v[c] = peer_load4(peer(smem_at(part + i * 4), c));
       float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int c = 0; c < kCluster; ++c) {
-        const float4 v = peer_load4(peer(smem_at(part + i * 4), c));
-        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-      }
-      s.x *= scale, s.y *= scale, s.z *= scale, s.w *= scale;
+      for (int c = 0; c < kCluster; ++c) s.x += v[c].x, s.y += v[c].y, s.z += v[c].z, s.w += v[c].w;
       const int row = i / (rank / 4), r = (i - row * (rank / 4)) * 4;
       uint32_t h[4], l[4];
-      split(s.x, &h[0], &l[0]);
-      split(s.y, &h[1], &l[1]);
-      split(s.z, &h[2], &l[2]);
-      split(s.w, &h[3], &l[3]);
+      split(s.x * scale, &h[0], &l[0]);
+      split(s.y * scale, &h[1], &l[1]);
+      split(s.z * scale, &h[2], &l[2]);
+      split(s.w * scale, &h[3], &l[3]);
       // ranks 2k and 2k + 1 keep neighbouring places
-      const uint32_t to0 = smem_at(rest + row * stride + pair_place(r, rank) * 8), to1 = smem_at(rest + row * stride + pair_place(r + 2, rank) * 8);
-#pragma unroll
-      for (int c = 0; c < kCluster; ++c) {
-        peer_store4(peer(to0, c), make_float4(__uint_as_float(h[0]), __uint_as_float(l[0]), __uint_as_float(h[1]), __uint_as_float(l[1])));
-        peer_store4(peer(to1, c), make_float4(__uint_as_float(h[2]), __uint_as_float(l[2]), __uint_as_float(h[3]), __uint_as_float(l[3])));
+      uint8_t *const to0 = rest + row * stride + pair_place(r, rank) * 8, *const to1 = rest + row * stride + pair_place(r + 2, rank) * 8;
+      if (MT == 1) {
+        *reinterpret_cast<uint4*>(to0) = make_uint4(h[0], l[0], h[1], l[1]);
+        *reinterpret_cast<uint4*>(to1) = make_uint4(h[2], l[2], h[3], l[3]);
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < kCluster; ++c) {
+          peer_store4(peer(smem_at(to0), c), make_float4(__uint_as_float(h[0]), __uint_as_float(l[0]), __uint_as_float(h[1]), __uint_as_float(l[1])));
+          peer_store4(peer(smem_at(to1), c), make_float4(__uint_as_float(h[2]), __uint_as_float(l[2]), __uint_as_float(h[3]), __uint_as_float(l[3])));
+        }
       }
     }
-    cluster_sync();
-    // ---- y: a warp has 32 columns; a lane's are 8 neighbours (two of each of four products)
-    const size_t b_row = static_cast<size_t>(id) * N;
+    if (MT == 1) {
+      asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // this CTA has read the others' parts
+      __syncthreads();
+    } else {
+      cluster_sync();
+    }
+    // ---- y: a warp has 32 columns, a lane 4 and 4 of them (two of each of four products). A value is added to y in L2, by the
+    // only addition that it gets in the call: no loads to wait for.
     const bool wide = N % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
-    for (int n0 = (cta * kWarps + warp) * 32; n0 < N; n0 += kCluster * kWarps * 32) {
-      int col[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) col[j] = n0 + (g >> 1) * 8 + 2 * j + (g & 1);
+    Weights<TYPE, 8> next[4];
+    if (MT > 1 && kAhead && rank >= 32 && n0 < N) load_columns(w, p, b_row, n0, 0);
+    for (; n0 < N; n0 += kStep) {
       float acc[MT][4][4];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[m][j][0] = acc[m][j][1] = acc[m][j][2] = acc[m][j][3] = 0.0f;
       int r0 = 0;
-      for (; r0 + 32 <= rank; r0 += 32) expand<TYPE, MT, 8>(acc, p, b_row, col, r0, rest, stride, tiles);
-      if (rank & 16) expand<TYPE, MT, 4>(acc, p, b_row, col, r0, rest, stride, tiles), r0 += 16;
-      if (rank & 8) expand<TYPE, MT, 2>(acc, p, b_row, col, r0, rest, stride, tiles);
+#pragma unroll 1
+      for (; r0 + 32 <= rank; r0 += 32) {
+        if (kAhead) {
+          const bool more = r0 + 64 <= rank;
+          if (more || n0 + kStep < N) load_columns(next, p, b_row, more ? n0 : n0 + kStep, more ? r0 + 32 : 0);
+        } else {
+          load_columns(w, p, b_row, n0, r0);
+        }
+        expand<TYPE, MT, 8>(acc, w, r0, rest, stride, tiles);
+        if (kAhead) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = next[j];
+        }
+      }
+      if (rank & 16) {
+        Weights<TYPE, 4> part_w[4];
+        load_columns(part_w, p, b_row, n0, r0);
+        expand<TYPE, MT, 4>(acc, part_w, r0, rest, stride, tiles);
+        r0 += 16;
+      }
+      if (rank & 8) {
+        Weights<TYPE, 2> part_w[4];
+        load_columns(part_w, p, b_row, n0, r0);
+        expand<TYPE, MT, 2>(acc, part_w, r0, rest, stride, tiles);
+      }
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
+        if (m >= tiles) break;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int place = m * 16 + h * 8 + g, n = n0 + t * 8;
-          if (place >= have) continue;
-          const int row = sh.rows[place];
-          if (!XQ_IN(row, A.M, kChkLoraRow)) continue;
-          float* const y = p.y + static_cast<size_t>(row) * N + n;
-          if (wide && n + 8 <= N) {
-            float4 u = reinterpret_cast<float4*>(y)[0], v = reinterpret_cast<float4*>(y)[1];
-            u.x += acc[m][0][2 * h], u.y += acc[m][0][2 * h + 1], u.z += acc[m][1][2 * h], u.w += acc[m][1][2 * h + 1];
-            v.x += acc[m][2][2 * h], v.y += acc[m][2][2 * h + 1], v.z += acc[m][3][2 * h], v.w += acc[m][3][2 * h + 1];
-            reinterpret_cast<float4*>(y)[0] = u;
-            reinterpret_cast<float4*>(y)[1] = v;
-          } else {
+          const int place = m * 16 + h * 8 + g, row = place < have ? sh.rows[place] : -1;
+          if (row < 0 || !XQ_IN(row, A.M, kChkLoraRow)) continue;
+          float* const to = p.y + static_cast<size_t>(row) * N;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+          for (int q = 0; q < 2; ++q) {
+            const int n = n0 + 16 * q + 4 * t;
+            const float v[4] = {acc[m][2 * q][2 * h], acc[m][2 * q][2 * h + 1], acc[m][2 * q + 1][2 * h], acc[m][2 * q + 1][2 * h + 1]};
+            if (wide && n + 4 <= N) {
+              asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to + n), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
+            } else {
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                if (n + 2 * j + i < N) y[2 * j + i] += acc[m][j][2 * h + i];
+              for (int i = 0; i < 4; ++i)
+                if (n + i < N) to[n + i] += v[i];
+            }
           }
         }
       }
     }
+    if (MT == 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // its own are no longer read
     __syncthreads();  // of t and the rows, before the next job's
   }
 }
