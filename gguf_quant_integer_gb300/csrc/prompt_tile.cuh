@@ -144,30 +144,36 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
       if (!there) break;
       const int kv = it.head / (A.heads / A.kv_heads);
       const bool second = kTiles == 2 && it.end[1] > 0;
-      for (int r = 0; r < (second ? 2 : 1) && ok; ++r) {
-        if (q_done[r] > 0) ok = wait(kPbQFree + r, q_done[r] - 1, 3);
-        ++q_done[r];
-        if (ok && lead) {
-          ptx::mbar_expect_tx(bar(kPbQ + r), P.pack * P.tokens_tile * D * 2);
+      // the first K before the queries, whose place is free later
+      auto queries = [&] {
+        for (int r = 0; r < (second ? 2 : 1) && ok; ++r) {
+          if (q_done[r] > 0) ok = wait(kPbQFree + r, q_done[r] - 1, 3);
+          ++q_done[r];
+          if (ok && lead) {
+            ptx::mbar_expect_tx(bar(kPbQ + r), P.pack * P.tokens_tile * D * 2);
 #pragma unroll
-          for (int x = 0; x < S::kBoxes; ++x)
-            tma_load_3d(base + r * S::kQ + x * (kRows * S::kLine), &P.q, x * S::kBox, it.head, it.first + it.place + r * P.tokens_tile,
-                        bar(kPbQ + r));
+            for (int x = 0; x < S::kBoxes; ++x)
+              tma_load_3d(base + r * S::kQ + x * (kRows * S::kLine), &P.q, x * S::kBox, it.head, it.first + it.place + r * P.tokens_tile,
+                          bar(kPbQ + r));
+          }
         }
-      }
+      };
       const int last = second ? it.end[1] : it.end[0];
       for (int j = it.begin[0]; j < last && ok; ++j) {
 #pragma unroll 1
-        for (int v = 0; v < 2 && ok; ++v, ++loaded) {
+        for (int v = 0; v < 2 && ok; ++v) {
           const unsigned st = loaded % kStages;
           if (loaded >= kStages) ok = wait(kPbFree + st, loaded / kStages - 1, 4);
-          if (ok && lead) {
+          if (!ok) break;
+          ++loaded;
+          if (lead) {
             ptx::mbar_expect_tx(bar(kPbFull + st), S::kStage);
 #pragma unroll
             for (int x = 0; x < S::kBoxes; ++x)
               tma_load_3d(base + kTiles * S::kQ + st * S::kStage + x * (kKeys * S::kLine), v ? &P.v : &P.k, x * S::kBox, kv,
                           it.first + j * kKeys, bar(kPbFull + st));
           }
+          if (v == 0 && j == it.begin[0]) queries();
         }
         if (j == it.begin[0]) find(round + 1);  // while the first copies are on their way
       }
@@ -185,18 +191,19 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
     unsigned used = 0;  // loads of the items before
     unsigned scored[2] = {0u, 0u}, done[2] = {0u, 0u}, parts[2] = {0u, 0u};
     bool ok = true;
-    Item it;
-    while (ok && take(it)) {
-      leave();
+    Item it, next;
+    bool more = take(it), begun = false;  // begun: the item's first scores of row tile 0 were issued before the last outputs of the one before
+    if (more) leave();
+    while (ok && more) {
       const bool second = kTiles == 2 && it.end[1] > 0;
       const int first = it.begin[0], last = second ? it.end[1] : it.end[0];
       auto k_load = [&](int j) { return used + 2 * (j - first); };  // V's is the next
-      auto scores = [&](int r, int j) {
+      auto scores_of = [&](const Item& it, int r, int j, unsigned ld) {
         if (j == it.begin[r]) {
           ok = wait(kPbQ + r, parts[r]++, 6);
           if (!ok) return;
         }
-        const unsigned ld = k_load(j), st = ld % kStages;
+        const unsigned st = ld % kStages;
         ok = wait(kPbFull + st, ld / kStages, 7);
         if (!ok) return;
         ptx::tc_fence_after();
@@ -216,6 +223,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
         }
         __syncwarp();
       };
+      auto scores = [&](int r, int j) { scores_of(it, r, j, k_load(j)); };
       auto outputs = [&](int r, int j) {
         const int from = buffer(r, done[r]);
         ok = wait(kPbP + from, turn(done[r]), 8);
@@ -241,14 +249,25 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
         __syncwarp();
       };
       for (int j = first - 1; j < last && ok; ++j) {
+        // behind the last scores of row tile 0 come the next item's first
+        auto begin_next = [&] {
+          more = take(next);
+          if (!more) return;
+          leave();
+          scores_of(next, 0, next.begin[0], used + 2 * (last - first));
+        };
         if (kTiles == 2) {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
+            if (r == 1 && ok && j + 1 == last) begin_next();
             if (ok && j >= it.begin[r] && j < it.end[r]) outputs(r, j);
-            if (ok && j + 1 >= it.begin[r] && j + 1 < it.end[r]) scores(r, j + 1);
+            if (ok && j + 1 >= it.begin[r] && j + 1 < it.end[r] && !(r == 0 && begun && j + 1 == first)) scores(r, j + 1);
           }
         } else {
-          if (j + 1 < last) scores(0, j + 1);
+          if (j + 1 == last)
+            begin_next();
+          else if (!(begun && j + 1 == first))
+            scores(0, j + 1);
           if (ok && j >= first) outputs(0, j);
         }
         if (!ok) break;
@@ -256,6 +275,8 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
         if (j >= first) release(k_load(j) + 1);
       }
       used += 2 * (last - first);
+      it = next;
+      begun = true;
     }
     if (lead) ptx::tc_commit(bar(kPbDrain));  // nothing is in flight when tensor memory is freed
     wait(kPbDrain, 0, 10);
