@@ -2,13 +2,13 @@
 """One decode step of a layer's attention half, from quantized weights to quantized weights.
 
 A batch of sequences continues one shared prompt. The step runs what an engine
-would: q, k and v projections from GGUF weights (xq_layer_mixed), the new K and
+would: q, k and v projections from GGUF weights (xq_layer_mixed), norms of q and
+k for each head with the position rotation (xq_qk_norm_rope), the new K and
 V rows into the paged cache (xq_kv_write), attention over the shared prompt and
 each sequence's own tokens (xq_kv_attn_shared), and the output projection. The
 cached rows of the prompt and of the first new tokens are written the same way
 beforehand, and read back at the end (xq_kv_read) to check the attention in 64
-bits. (A model's position embedding would go between the projections and the
-cache; it is left out.)
+bits.
 
     python examples/decode_step.py [--batch 8] [--prompt 1000] [--steps 4] [--cache q8_0|q4_0]
 """
@@ -45,21 +45,33 @@ class AttentionHalf:
         self.cache = xq.KVCache(cache_type, head + batch * own, PAGE, KV_HEADS, DIM)
         self.prompt_pages, self.pages = order[:head].contiguous(), order[head:].view(batch, own).contiguous()
         self.lens = torch.zeros(batch, dtype=torch.int32, device="cuda")
+        gen = torch.Generator("cuda").manual_seed(seed)
+        self.q_norm, self.k_norm = (1 + 0.1 * torch.randn(DIM, device="cuda", generator=gen) for _ in range(2))
+        self.rope = xq.Rope(DIM, base=1e6)
+
+    def turned(self, q, k, positions):
+        """q and k rows normalized for each head and rotated to their positions, in place."""
+        q, k = q.view(-1, HEADS, DIM), k.view(-1, KV_HEADS, DIM)
+        return xq.qk_norm_rope(q, k, positions, self.rope, self.q_norm, self.k_norm, q_out=q, k_out=k)
 
     def prefill(self, x):
-        """K and V of the prompt's inputs x [prompt, HIDDEN] into its pages."""
+        """K and V of the prompt's inputs x [prompt, HIDDEN] into its pages; the prompt's own attention."""
         torch = self.torch
         a = xq.quantize_q8(x)
-        k, v = (xq.matmul(p.qtype, self.layer.W[i], a, self.prompt, p.N, p.K) for i, p in ((1, self.qkv[1]), (2, self.qkv[2])))
+        q, k, v = (xq.matmul(p.qtype, self.layer.W[i], a, self.prompt, p.N, p.K) for i, p in enumerate(self.qkv))
         t = torch.arange(self.prompt, device="cuda")
+        q, k = self.turned(q, k, t)
         self.prompt_slots = self.prompt_pages[t // PAGE].long() * PAGE + t % PAGE
         self.cache.write(k.view(-1, KV_HEADS, DIM), v.view(-1, KV_HEADS, DIM), self.prompt_slots)
+        starts = torch.tensor([0, self.prompt], dtype=torch.int32, device="cuda")
+        return xq.prompt_attn(q, k, v.view(-1, KV_HEADS, DIM), starts)
 
     def step(self, x):
         """One token of each sequence: x [batch, HIDDEN] -> the half's output [batch, HIDDEN]."""
         torch = self.torch
         q, k, v = self.layer.forward([x])
         at = self.lens.long()
+        q, k = self.turned(q, k, self.prompt + at)
         slots = self.pages.gather(1, (at // PAGE)[:, None])[:, 0].long() * PAGE + at % PAGE
         self.cache.write(k.view(-1, KV_HEADS, DIM), v.view(-1, KV_HEADS, DIM), slots)
         self.lens += 1
