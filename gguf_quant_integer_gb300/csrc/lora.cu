@@ -34,6 +34,7 @@ constexpr int kMaxAdapters = 8192;
 struct LoraGrid {
   int jobs;       // at most, of a projection
   int first;      // index of the launch's projections
+  int projections;
   int rank_most;  // of the launch's projections
   int rows;       // T
 };
@@ -261,21 +262,38 @@ __device__ __forceinline__ void expand(float (&acc)[MH][4][4], const Weights<TYP
   }
 }
 
-// The same of up to 32 rows, by each warp for itself: jobs are numbered by their first rows.
-__device__ __forceinline__ int find_job_32(const int32_t* ids, int M, int n, int T, int j, JobShared& sh) {
-  const int lane = threadIdx.x & 31, id = lane < M ? ids[lane] : -1;
-  if (id >= n) atomicCAS(&g_lora_error, 0u, kOpsBadAdapter);
-  const unsigned same = __match_any_sync(0xffffffffu, id);
-  const int place = __popc(same & ((1u << lane) - 1u));  // among the adapter's rows
-  unsigned first = __ballot_sync(0xffffffffu, id >= 0 && id < n && place % T == 0);
-  for (int i = 0; i < j; ++i) first &= first - 1;
-  if (first == 0) return 0;
-  const int lead = __ffs(first) - 1, lo = __shfl_sync(0xffffffffu, place, lead);
-  const unsigned all = __shfl_sync(0xffffffffu, same, lead);
-  if ((all >> lane & 1) && place >= lo && place < lo + T) sh.rows[place - lo] = lane;  // all warps write the same
-  if (lane == lead) sh.adapter = id;
+// The same of up to 64 rows, by each warp for itself and without a barrier: jobs are numbered by their first rows.
+__device__ __forceinline__ int find_job_64(const int32_t* ids, int M, int n, int T, int j, JobShared& sh) {
+  const int lane = threadIdx.x & 31;
+  const unsigned below = (1u << lane) - 1u;
+  const int id0 = lane < M ? ids[lane] : -1, id1 = lane + 32 < M ? ids[lane + 32] : -1;
+  if (max(id0, id1) >= n) atomicCAS(&g_lora_error, 0u, kOpsBadAdapter);
+  // a row's place among its adapter's
+  const int place0 = __popc(__match_any_sync(0xffffffffu, id0) & below);
+  int place1 = 0;
+  if (M > 32) {
+    place1 = __popc(__match_any_sync(0xffffffffu, id1) & below);
+#pragma unroll 4
+    for (int i = 0; i < 32; ++i) place1 += __shfl_sync(0xffffffffu, id0, i) == id1;
+  }
+  unsigned first0 = __ballot_sync(0xffffffffu, id0 >= 0 && id0 < n && place0 % T == 0);
+  unsigned first1 = __ballot_sync(0xffffffffu, id1 >= 0 && id1 < n && place1 % T == 0);
+  for (int i = 0; i < j; ++i) {
+    if (first0 != 0u)
+      first0 &= first0 - 1;
+    else
+      first1 &= first1 - 1;
+  }
+  if ((first0 | first1) == 0u) return 0;
+  const int lead = __ffs(first0 != 0u ? first0 : first1) - 1;
+  const int lo = __shfl_sync(0xffffffffu, first0 != 0u ? place0 : place1, lead), id = __shfl_sync(0xffffffffu, first0 != 0u ? id0 : id1, lead);
+  // all warps write the same
+  if (id0 == id && place0 >= lo && place0 < lo + T) sh.rows[place0 - lo] = lane;
+  if (id1 == id && place1 >= lo && place1 < lo + T) sh.rows[place1 - lo] = lane + 32;
+  if (lane == 0) sh.adapter = id;
+  const int all = __popc(__ballot_sync(0xffffffffu, id0 == id)) + __popc(__ballot_sync(0xffffffffu, id1 == id));
   __syncwarp();
-  return min(T, __popc(all) - lo);
+  return min(T, all - lo);
 }
 
 template <int TYPE, int MT>
@@ -283,14 +301,16 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
   constexpr int T = 16 * MT, kSplit = kWarps / MT, kRankBlock = rank_block(MT);  // kSplit warps share out a CTA's part of K
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ JobShared sh;
-  const AdapterProj& p = A.p[G.first + blockIdx.y];
+  // the projections' jobs in turn: those that there are come before those that there may be
+  const int cluster = blockIdx.x / kCluster, clusters = gridDim.x / kCluster / G.projections;
+  const AdapterProj& p = A.p[G.first + cluster % G.projections];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int cta = blockIdx.x % kCluster;
   float* const part = reinterpret_cast<float*>(smem);
   uint8_t* const rest = smem + part_bytes(T, G.rank_most);
   const int rank = p.rank, K = p.K, N = p.N;
-  for (int job = blockIdx.x / kCluster; job < G.jobs; job += gridDim.x / kCluster) {
-    const int have = A.M <= 32 ? find_job_32(A.ids, A.M, p.n, T, job, sh) : find_job(A.ids, A.M, p.n, T, job, reinterpret_cast<int*>(rest), sh);
+  for (int job = cluster / G.projections; job < G.jobs; job += clusters) {
+    const int have = A.M <= 64 ? find_job_64(A.ids, A.M, p.n, T, job, sh) : find_job(A.ids, A.M, p.n, T, job, reinterpret_cast<int*>(rest), sh);
     if (have == 0) return;  // nor are there later ones; so for all of the cluster
     const int id = sh.adapter, tiles = (have + 15) / 16;
     const size_t b_row = static_cast<size_t>(id) * N;
@@ -487,13 +507,13 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
 }
 
 template <int TYPE, int MT>
-cudaError_t launch(const LoraArgs& a, const LoraGrid& g, int n_proj, int n_most, cudaStream_t s) {
+cudaError_t launch(const LoraArgs& a, const LoraGrid& g, int n_most, cudaStream_t s) {
   const int bytes = shared_bytes(16 * MT, g.rank_most, n_most);
   static std::atomic<unsigned long long> allowed{0};
   const cudaError_t e = allow_shared(lora_kernel<TYPE, MT>, 200 * 1024, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCluster * std::min(g.jobs, kJobsGrid), n_proj);
+  cfg.gridDim = dim3(kCluster * std::min(g.jobs, kJobsGrid) * g.projections);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
@@ -523,12 +543,13 @@ cudaError_t launch_lora(const LoraArgs& args, cudaStream_t s) {
       n_most = std::max(n_most, a.p[e].n);
     }
     const int MT = static_cast<long long>(a.M) * (e - i) <= 16 * 38 ? 1 : g.rank_most > 128 ? 2 : 4;
+    g.projections = e - i;
     g.rows = 16 * MT;
     g.jobs = std::max(1, std::min(a.M, n_most) + a.M / g.rows);
     cudaError_t r;
     auto by_rows = [&](auto type) {
       constexpr int TYPE = decltype(type)::value;
-      return MT == 1 ? launch<TYPE, 1>(a, g, e - i, n_most, s) : MT == 2 ? launch<TYPE, 2>(a, g, e - i, n_most, s) : launch<TYPE, 4>(a, g, e - i, n_most, s);
+      return MT == 1 ? launch<TYPE, 1>(a, g, n_most, s) : MT == 2 ? launch<TYPE, 2>(a, g, n_most, s) : launch<TYPE, 4>(a, g, n_most, s);
     };
     if (a.p[i].type == kF32)
       r = by_rows(std::integral_constant<int, kF32>());
