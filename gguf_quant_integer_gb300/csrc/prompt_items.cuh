@@ -79,36 +79,69 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
       : "memory");
 }
 
-// One row by one warp, lanes over the head's elements.
+// 4 elements from p + at.
+template <int TYPE>
+__device__ __forceinline__ float4 load4(const void* p, size_t at) {
+  if constexpr (TYPE == kF32) {
+    return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+    if constexpr (TYPE == kF16) {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+      return make_float4(a.x, a.y, b.x, b.y);
+    } else {
+      return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                         __uint_as_float(v.y & 0xFFFF0000u));
+    }
+  }
+}
+
+// One row by one warp, in fp32: 32 keys' scores at a time, a lane each, then their values, lanes over the head's elements.
 template <int TYPE, int D>
 __device__ __noinline__ void one_row(const PromptArgs& A, int first, int place, int head) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, kv = head / (A.heads / A.kv_heads);
-  const size_t token = static_cast<size_t>(first) + place;
-  float q[E], o[E];
+  const size_t token = static_cast<size_t>(first) + place, q0 = token * A.q_stride + static_cast<size_t>(head) * D;
+  float o[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = load_elt<TYPE>(A.q, token * A.q_stride + static_cast<size_t>(head) * D + lane + 32 * e);
-    o[e] = 0.0f;
-  }
+  for (int e = 0; e < E; ++e) o[e] = 0.0f;
   const float cs = A.scale * 1.4426950408889634f;
   float m = -INFINITY, l = 0.0f;
-  for (int j = A.window && place >= A.window ? place - A.window + 1 : 0; j <= place; ++j) {
-    const size_t key = static_cast<size_t>(first) + j;
-    float s = 0.0f;
+  for (int j0 = A.window && place >= A.window ? place - A.window + 1 : 0; j0 <= place; j0 += 32) {
+    const int n = min(32, place - j0 + 1);
+    float s = -INFINITY;
+    if (lane < n) {
+      const size_t k0 = (static_cast<size_t>(first) + j0 + lane) * A.k_stride + static_cast<size_t>(kv) * D;
+      s = 0.0f;
+#pragma unroll 4
+      for (int c = 0; c < D; c += 4) {
+        const float4 q = load4<TYPE>(A.q, q0 + c), k = load4<TYPE>(A.k, k0 + c);
+        s = fmaf(q.w, k.w, fmaf(q.z, k.z, fmaf(q.y, k.y, fmaf(q.x, k.x, s))));
+      }
+      s = __fmul_rn(s, cs);
+    }
+    float top = s;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      s = fmaf(q[e], load_elt<TYPE>(A.k, key * A.k_stride + static_cast<size_t>(kv) * D + lane + 32 * e), s);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s = __fmul_rn(s, cs);
-    const float next = fmaxf(m, s);
-    const float f = m == next ? 1.0f : exp2f(m - next), w = s == -INFINITY && next == s ? 0.0f : exp2f(s - next);
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float next = fmaxf(m, top);
+    // an infinite score above all others leaves NaN, as infinity minus infinity does; none above minus infinity, no weight
+    const float f = m == next ? 1.0f : exp2f(m - next);
+    const float w = lane >= n || (s == -INFINITY && next == s) ? 0.0f : exp2f(s - next);
     m = next;
-    l = fmaf(l, f, w);
+    float sum = w;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = fmaf(o[e], f, w * load_elt<TYPE>(A.v, key * A.v_stride + static_cast<size_t>(kv) * D + lane + 32 * e));
+    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    l = fmaf(l, f, sum);
+    if (l != l) break;  // a NaN among the scores is the whole row's
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= f;
+    const size_t v0 = (static_cast<size_t>(first) + j0) * A.v_stride + static_cast<size_t>(kv) * D + lane;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(wj, load_elt<TYPE>(A.v, v0 + j * A.v_stride + 32 * e), o[e]);
+    }
   }
   const size_t row = token * A.heads + head;
   if (XQ_IN(row, static_cast<size_t>(A.tokens) * A.heads, kChkPromptRow))

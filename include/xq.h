@@ -578,8 +578,9 @@ typedef struct {
  * The y of different projections must not overlap, nor y and x. x, a and b
  * are 16-byte aligned, y, scales and ids 4-byte. Products are of fp32's
  * precision (x and x a^T enter the tensor cores as two tf32 numbers each, 22
- * bits, fp32 adapters too, 16-bit ones exactly), sums are fp32. A row's result
- * does not depend on the other rows' values. M == 0 enqueues nothing. */
+ * bits, fp32 adapters too, 16-bit ones exactly), sums are fp32; a value of y
+ * that lies below fp32's normal range may count as 0. A row's result does not
+ * depend on the other rows' values. M == 0 enqueues nothing. */
 XQ_API xq_status xq_lora_add(const xq_adapters *proj, int n_proj, const float *const *inputs, int n_inputs, int M,
                              const int32_t *ids, xq_stream stream);
 
@@ -642,7 +643,10 @@ XQ_API size_t xq_prompt_attn_workspace_bytes(const xq_prompts *prompts);
  * weights of 16-bit calls are rounded to that type for the product with V.
  * Rows of out that belong to no sequence (before starts[0], behind
  * starts[batch]) are left as they were. What a row does not see does not
- * reach it, infinities and NaN included. A sequence whose bounds do not
+ * reach it, infinities and NaN included. fp32 rows enter the tensor cores as two
+ * fp16 numbers each (22 bits). Rows that see something not finite, and fp32 rows
+ * that meet 128 keys whose K or V rows differ by more than 2^12 in size, are
+ * computed one by one (hundreds of times slower). A sequence whose bounds do not
  * satisfy 0 <= starts[b] <= starts[b+1] <= tokens is left out and recorded
  * (xq_device_error: kernel 5, wait 2). q, k, v and out are 16-byte aligned,
  * strides multiples of 16 bytes, starts 4-byte aligned; out must not overlap

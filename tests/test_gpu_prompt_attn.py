@@ -257,3 +257,71 @@ def test_refusals_and_empty_calls(xq):
     assert bool((out == 7.0).all())
     assert xq.prompt_attn(q[:0], k[:0], v[:0], s).shape == (0, 4, 128)
     assert xq.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+def test_rows_computed_one_by_one(xq, dtype):
+    """One bad element that all rows see: every row is computed by itself, its other elements as exactly as ever (fp32's sums; the
+    weights are not rounded), over more keys than a step has and with a window."""
+    T, D = 3000, 128
+    q, k, v = inputs(T, 2, 1, D, dtype, 21)
+    starts = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    for window in (0, 77):
+        v2 = v.clone()
+        v2[::60, 0, 9] = float("nan")  # a window of 77 has at least one
+        got = xq.prompt_attn(q, k, v2, starts, window=window)
+        want, bound = ops_check.attention(q, k, v, [0, T], D ** -0.5, window)
+        assert bool(torch.isnan(got[60:, :, 9]).all())
+        want[:, :, 9] = math.nan
+        ops_check.within(got, want, bound)
+    assert xq.device_error() == 0
+
+
+def test_rows_of_very_different_size(xq):
+    """fp32 keys and values from 2^-40 to 2^60 beside each other, in the same 128 keys: each row as exact as its own sums allow."""
+    T, D = 400, 128
+    q, k, v = inputs(T, 2, 1, D, "fp32", 22)
+    starts = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    size = 2.0 ** torch.linspace(-40, 60, T, device="cuda")[torch.randperm(T, device="cuda", generator=torch.Generator("cuda").manual_seed(1))]
+    for kk, vv in ((k, v * size[:, None, None]), (k * (size[:, None, None] ** 0.05), v), (k * 1e-20, v * 1e-30), (k * 2.0 ** 100, v * 2.0 ** 100)):
+        scale = D ** -0.5 / float(kk.abs().amax()) * 4
+        got = xq.prompt_attn(q, kk.contiguous(), vv.contiguous(), starts, scale=scale)
+        want, bound = ops_check.attention(q, kk, vv, [0, T], scale)
+        ops_check.within(got, want, bound)
+    # a channel far larger than the others
+    v2 = v.clone()
+    v2[:, :, 17] *= 1e9
+    got = xq.prompt_attn(q, k, v2, starts)
+    want, bound = ops_check.attention(q, k, v2, [0, T], D ** -0.5)
+    assert ops_check.rms(got[..., :17], want[..., :17]) <= 1e-6 and ops_check.rms(got[..., 17], want[..., 17]) <= 1e-6
+    assert xq.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_offsets_past_32_bits(xq, dtype):
+    """More than 2^31 elements of q and of the result: the last sequence's rows, under a window."""
+    H, D, lens = 32, 128, [524288 + 11, 700]
+    T = sum(lens)
+    g = torch.Generator("cuda").manual_seed(2)
+    q = torch.empty(T, H, D, dtype=DTYPES[dtype], device="cuda").normal_(generator=g)
+    k, v = (torch.empty(T, 1, D, dtype=DTYPES[dtype], device="cuda").normal_(generator=g) for _ in range(2))
+    s = torch.tensor([0, lens[0], T], dtype=torch.int32, device="cuda")
+    got = xq.prompt_attn(q, k, v, s, window=300)
+    for a, e in ((lens[0] - 600, lens[0]), (lens[0], T)):
+        want, bound = ops_check.attention(q[a:e], k[a:e], v[a:e], [0, e - a], D ** -0.5, 300)
+        skip = 300 if a < lens[0] else 0  # rows whose window begins before the part that is compared
+        ops_check.within(got[a + skip:e], want[skip:], bound[skip:])
+    assert xq.device_error() == 0
+
+
+def test_a_long_sequence(xq):
+    """131071 keys: the last rows' sums over all of them."""
+    T, D = 131071, 128
+    for dtype, limit in (("bf16", 3e-3), ("fp32", 1.5e-6)):
+        q, k, v = inputs(T, 1, 1, D, dtype, 31)
+        s = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+        got = xq.prompt_attn(q, k, v, s)[-40:, 0]
+        z = (q[-40:, 0].double() @ k[:, 0].double().T) * D ** -0.5
+        at = torch.arange(T, device="cuda")
+        z = z.masked_fill(at > at[-40:, None], -math.inf)
+        assert ops_check.rms(got, torch.softmax(z, -1) @ v[:, 0].double()) <= limit
