@@ -97,8 +97,9 @@ __device__ __forceinline__ float4 load4(const void* p, size_t at) {
 }
 
 // One row by one warp, in fp32: 32 keys' scores at a time, a lane each, then their values, lanes over the head's elements.
+// Writes columns c0 .. c1 - 1, multiples of 32 or, with lanes left out, of 16.
 template <int TYPE, int D>
-__device__ __noinline__ void one_row(const PromptArgs& A, int first, int place, int head) {
+__device__ __noinline__ void one_row(const PromptArgs& A, int first, int place, int head, int c0, int c1) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, kv = head / (A.heads / A.kv_heads);
   const size_t token = static_cast<size_t>(first) + place, q0 = token * A.q_stride + static_cast<size_t>(head) * D;
@@ -146,7 +147,8 @@ __device__ __noinline__ void one_row(const PromptArgs& A, int first, int place, 
   const size_t row = token * A.heads + head;
   if (XQ_IN(row, static_cast<size_t>(A.tokens) * A.heads, kChkPromptRow))
 #pragma unroll
-    for (int e = 0; e < E; ++e) store_elt<TYPE>(A.out, row * D + lane + 32 * e, o[e] / l);
+    for (int e = 0; e < E; ++e)
+      if (lane + 32 * e >= c0 && lane + 32 * e < c1) store_elt<TYPE>(A.out, row * D + lane + 32 * e, o[e] / l);
 }
 
 // Sequence b's rows and their number; 0, and recorded, if its bounds are no range of the call's rows.

@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
         while (again) {
           const int src = __ffs(again) - 1;
           again &= again - 1;
-          one_row<kF32, D>(A, it.first, __shfl_sync(0xffffffffu, place, src), it.head + __shfl_sync(0xffffffffu, part, src));
+          one_row<kF32, D>(A, it.first, __shfl_sync(0xffffffffu, place, src), it.head + __shfl_sync(0xffffffffu, part, src), it.half * S::kV, (it.half + 1) * S::kV);
         }
       }
     }

@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
       while (again) {
         const int src = __ffs(again) - 1;
         again &= again - 1;
-        one_row<TYPE, D>(A, it.first, __shfl_sync(0xffffffffu, place, src), it.head + __shfl_sync(0xffffffffu, part, src));
+        one_row<TYPE, D>(A, it.first, __shfl_sync(0xffffffffu, place, src), it.head + __shfl_sync(0xffffffffu, part, src), 0, D);
       }
       leave();
     }
