@@ -11,7 +11,16 @@
 // Precision: both products run on the warp-level tensor cores in tf32, x and t as two numbers each (11 + 11 bits; hi is cut
 // off, so that nothing overflows) and fp32 adapters too (without lo x lo); 16-bit adapters are exact. A tensor core's
 // accumulator cuts off, towards 0, what an fp32 addition rounds, so sums over K leave it every 32 elements (kept in it for
-// K / 16, 4096 elements had 1.3e-6 of error) and y is added in fp32 behind them.
+// K / 16, 4096 elements had 1.3e-6 of error) and y is added to in L2, in fp32, by one reduction a value.
+//
+// T is 16 rows where that fills the device no more than once (up to 608 rows times projections), else 64 (32 beyond rank
+// 128): A and B are read once a job, so more rows save L2 traffic, and fewer start more clusters. What bounds it: with few
+// rows, a chain of memory round trips and instructions seen for the first time (one row 4096 -> 4096, rank 16: 5.9 us, of
+// 9500 clocks 3400 for x A^T, 2300 for the exchange, 3000 for y; 64 rows of 16 adapters at q, k and v: 11 us); with many, the
+// warp-level tensor cores, 8 clocks a product of 16 x 8 x 8 (4099 rows, rank 64, two projections 4096 -> 14336: 383 us, 126000
+// products a sub-core quarter of which 130 us would be the least; y's 0.94 GB are 139 us); 777 mixed rows to 2 x 8960, rank 8:
+// 39 us, 0.1 GB. Tried and slower: y loaded and stored (expansion 180000 clocks a job instead of 100000), its lines
+// prefetched into L2 (40 us for 39, 394 for 383), 85 registers and three CTAs an SM for 16-row jobs (one row 7.6 us).
 #include <algorithm>
 #include <type_traits>
 #include <utility>

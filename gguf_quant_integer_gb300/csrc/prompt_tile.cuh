@@ -11,15 +11,22 @@
 // thread takes a row of them and leaves the weights in the same columns, the second product's A operand.
 //
 // Roles: warps 0-3 and 4-7 softmax and results of a row tile, then one that issues products, one that copies, two that
-// look through V (below). CTAs are
-// persistent and take items (row tiles of a sequence and heads) longest first, in rounds of alternating direction; the
-// copying warp finds them from the sequences' bounds (see next_item) an item ahead, so Q, K and V of the next item are on
-// their way while one ends.
+// look through V (below). CTAs are persistent and take items (row tiles of a sequence and heads) longest first, in rounds of
+// alternating direction; the copying warp finds them from the sequences' bounds (see next_item) an item ahead, so Q, K and V
+// of the next item are on their way, and its first scores are computed, while one ends.
 //
 // What is not finite: scores of keys that a row does not see are replaced, but such a key's V would meet a weight of 0 in
 // the product, where an infinity or NaN spoils the row. So two warps look through the V tiles of which some row does not see
 // all keys, before the product, and put 0 in the place of such elements. Rows that do see one of them, and rows whose result
 // or sum is not finite (a score, a V that all rows see), are computed again by themselves (one_row).
+//
+// What bounds it, at head size 128: the tensor cores have 2048 clocks of work for the two row tiles' 128 keys, which take
+// 3450: a tile's scores, softmax (1600), weights and outputs follow each other, and two of them do not fill the pipe. 12287
+// bf16 tokens of 32/8 heads 827 us, 1.50 PFLOP/s; 16 sequences of 17 to 2048 219 us (0.98; masked halves of tiles count as
+// nothing), where an item of some 9 tiles ends and begins in about 8000 clocks.
+// Tried and slower: 32 scores at a time in rolled loops (long 974 us for 935), products issued by two warps (one is then left
+// to look through V: 241 us for 229, packed), masks as bits of a word (247 for 229), results stored from registers (258 for
+// 235: a store of 32 rows takes 32 lines' turns), the scan of V unrolled eight times instead of twice (234 for 229).
 #pragma once
 
 #include "prompt_items.cuh"

@@ -12,7 +12,12 @@
 // lanes (96: 12 of 16) and its sum 3 to 5 shuffles; a warp takes several heads
 // of one token, as the cosines are the token's. Element i and its partner
 // i + rot / 2 lie the same number of lanes apart for all (rot is a multiple of
-// 16), neighbouring pairs in one lane.
+// 16), neighbouring pairs in one lane. Weights go into the cosines and sines,
+// which the block's threads work out once a token.
+//
+// What bounds it: HBM, 82 % of the copy rate (16383 tokens of 32 + 8 heads of
+// 128, fp32 to bf16: 90 us, 5.6 TB/s; 327 us with the angles worked out by every
+// warp); with few tokens the launch and one round trip (2.9 to 3.1 us).
 #include "ops_common.cuh"
 
 namespace xq {
