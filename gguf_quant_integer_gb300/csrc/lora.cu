@@ -1,9 +1,11 @@
 // Low-rank adapters of many requests beside shared projections.
 //
 // y[m] += scale[i] (x[m] A[i]^T) B[i]^T with the row's adapter i. A job is up to T rows of one adapter and projection, one
-// cluster of 8 CTAs: each CTA multiplies its eighth of K (x against A, warps sharing that out once more), the CTAs add up
-// their parts of t = x A^T [T][rank] through distributed shared memory in a fixed order, and each then adds t B^T to its
-// eighth of y's columns. So one launch does both products, A and B of a job are read once, and t never leaves the SMs.
+// cluster of 8 or 16 CTAs: each CTA multiplies its part of K (x against A, shared out among its warps), the CTAs add up their
+// parts of t = x A^T [T][rank] through distributed shared memory in a fixed order, and each then adds t B^T to its part of y's
+// columns. So one launch does both products, and t never leaves the SMs. Of large ranks a warp has 16 (or 32) and all of the
+// CTA's K, before K is shared out too: rank 128 is one pass over x with no sums among the warps, where passes of 16 ranks, one
+// behind the other, had 3500 clocks of latency each (4 rows, 4096 -> 2 x 14336: 33 us, now 23).
 //
 // Which rows make up a job is found in the kernel (count rows by adapter, number the jobs, collect the rows), as only the
 // device knows the ids; all CTAs of a cluster find the same.
@@ -13,16 +15,19 @@
 // accumulator cuts off, towards 0, what an fp32 addition rounds, so sums over K leave it every 32 elements (kept in it for
 // K / 16, 4096 elements had 1.3e-6 of error) and y is added to in L2, in fp32, by one reduction a value.
 //
-// T is 16 rows where that fills the device no more than once (up to 608 rows times projections), else 64 (32 beyond rank
-// 128): A and B are read once a job, so more rows save L2 traffic, and fewer start more clusters. What bounds it: with few
-// rows, a chain of memory round trips and instructions seen for the first time (one row 4096 -> 4096, rank 16: 5.9 us, of
-// 9500 clocks 3400 for x A^T, 2300 for the exchange, 3000 for y; 64 rows of 16 adapters at q, k and v: 11 us); with many, the
-// warp-level tensor cores, 8 clocks a product of 16 x 8 x 8 (4099 rows, rank 64, two projections 4096 -> 14336: 383 us, 126000
-// products a sub-core quarter of which 130 us would be the least; y's 0.94 GB are 139 us); 777 mixed rows to 2 x 8960, rank 8:
-// 39 us, 0.1 GB. Tried and slower: y loaded and stored (expansion 180000 clocks a job instead of 100000), its lines
-// prefetched into L2 (40 us for 39, 394 for 383), 85 registers and three CTAs an SM for 16-row jobs (one row 7.6 us).
+// T is 16 rows up to 2432 rows times projections, else 64 (32 beyond rank 128: shared memory): A and B are read once a job,
+// so more rows save L2 traffic, and fewer start more clusters (352 rows of rank 128 to 2 x 14336: 55 us, 137 with 64 rows a
+// job; 2854 rows of 25 adapters, 8960 -> 1536, rank 24: 87 us, 114 with 16). Few jobs have clusters of 16, and as many
+// clusters for a job's columns as fill the device, which all work out x A^T (1 row to 2 x 14336, rank 16: 6.0 us, 9.8 with 8
+// CTAs a job). What bounds it: with few rows, a chain of memory round trips and instructions seen for the first time (one row
+// 4096 -> 4096, rank 16: 5.2 us, x A^T, the exchange and y in like parts; 64 rows of 16 adapters at q, k and v: 11.4 us); with
+// many, the warp-level tensor cores, 8 clocks a product of 16 x 8 x 8 on one of an SM's four sub-cores (4099 rows, rank 64, two
+// projections 4096 -> 14336: 371 us; 19.2 million products are 130 us at least, y's 0.94 GB 139 us); 777 mixed rows to 2 x
+// 8960, rank 8: 38 us, 0.1 GB. Tried and slower: y loaded and stored (expansion 180000 clocks a job instead of 100000; at widths
+// that are no multiple of 4, 1504 rows to 130 and 77 columns 38 us, 23 with single reductions), its lines prefetched into L2 (40
+// us for 39), 85 registers and three CTAs an SM for 16-row jobs (one row 7.6 us), 64 ranks a warp (spills), x and A two or
+// three chunks ahead (one row 5.6 us, 352 rows above 60 and 76).
 #include <algorithm>
-#include <type_traits>
 #include <utility>
 
 #include "ops_common.cuh"
@@ -33,10 +38,8 @@ namespace {
 __device__ unsigned int g_lora_error;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kCluster = 8;
-// Ranks of a pass over x. Few: what matters with few rows is how many instructions are seen for the first time.
-__host__ __device__ constexpr int rank_block(int mt) { return mt == 1 ? 16 : 32; }
-__host__ __device__ constexpr int sum_bytes(int mt) { return 8 / mt * 16 * mt * rank_block(mt) * 4; }  // the warps' parts of it
+// The warps' parts of a pass's sums: [8 / MT][16 * MT][RB].
+__host__ __device__ constexpr int sum_bytes(int rank_block) { return 8 * 16 * rank_block * 4; }
 constexpr int kJobsGrid = 512;        // jobs of a projection with clusters of their own
 constexpr int kMaxAdapters = 8192;
 
@@ -44,6 +47,7 @@ struct LoraGrid {
   int jobs;       // at most, of a projection
   int first;      // index of the launch's projections
   int projections;
+  int splits;  // clusters that share out a job's columns
   int rank_most;  // of the launch's projections
   int rows;       // T
 };
@@ -54,8 +58,8 @@ __host__ __device__ constexpr int align16(int x) { return (x + 15) & ~15; }
 // Shared memory: t's part [T][rank] fp32, then what follows one behind the other: row counts by adapter, the warps' partial
 // sums, t as pairs.
 __host__ __device__ constexpr int part_bytes(int rows, int rank) { return rows * rank * 4; }
-inline int shared_bytes(int rows, int rank, int n) {
-  return part_bytes(rows, rank) + std::max({sum_bytes(rows / 16), rows * pair_stride(rank), align16(n * 4)});
+inline int shared_bytes(int rows, int rank, int rank_block, int n) {
+  return part_bytes(rows, rank) + std::max({sum_bytes(rank_block), rows * pair_stride(rank), align16(n * 4)});
 }
 
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -305,13 +309,16 @@ __device__ __forceinline__ int find_job_64(const int32_t* ids, int M, int n, int
   return min(T, all - lo);
 }
 
-template <int TYPE, int MT>
+// MT: row tiles of 16. RB: a warp's ranks in a pass over x (few for few rows: what matters there is how many instructions are
+// seen for the first time). CS: CTAs of a cluster.
+template <int TYPE, int MT, int RB, int CS>
 __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant__ LoraArgs A, const LoraGrid G) {
-  constexpr int T = 16 * MT, kSplit = kWarps / MT, kRankBlock = rank_block(MT);  // kSplit warps share out a CTA's part of K
+  constexpr int T = 16 * MT, kSplit = kWarps / MT, kRankBlock = RB, kCluster = CS;  // kSplit warps share out a CTA's part of K
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ JobShared sh;
   // the projections' jobs in turn: those that there are come before those that there may be
-  const int cluster = blockIdx.x / kCluster, clusters = gridDim.x / kCluster / G.projections;
+  const int cluster = blockIdx.x / kCluster / G.splits, clusters = gridDim.x / kCluster / G.splits / G.projections;
+  const int share = blockIdx.x / kCluster % G.splits;
   const AdapterProj& p = A.p[G.first + cluster % G.projections];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int cta = blockIdx.x % kCluster;
@@ -323,25 +330,29 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
     if (have == 0) return;  // nor are there later ones; so for all of the cluster
     const int id = sh.adapter, tiles = (have + 15) / 16;
     const size_t b_row = static_cast<size_t>(id) * N;
-    constexpr int kStep = kCluster * kWarps * 32;
+    const int step = G.splits * kCluster * kWarps * 32;
     constexpr bool kAhead = TYPE != kF32;  // the next 32 ranks' weights are loaded beside a block's products
     Weights<TYPE, 8> w[4];
-    int n0 = (cta * kWarps + warp) * 32;
+    int n0 = ((share * kCluster + cta) * kWarps + warp) * 32;
     if (MT == 1 && kAhead && rank >= 32 && n0 < N) load_columns(w, p, b_row, n0, 0);
     // ---- t's part from this CTA's K: warp (mt, ks) has 16 rows and a share of the 32-element chunks
     const int chunks = K / 32, mt = warp % MT, ks = warp / MT;
     const int c0 = chunks * cta / kCluster, c1 = chunks * (cta + 1) / kCluster;
-    const int k0 = c0 + (c1 - c0) * ks / kSplit, k1 = c0 + (c1 - c0) * (ks + 1) / kSplit;
+    // large ranks: the warps share out the ranks first, then K
+    int groups = 1;
+    while (groups < kSplit && groups * kRankBlock < rank) groups *= 2;
+    const int shares = kSplit / groups, part_k = ks / groups, wide_block = groups * kRankBlock;
+    const int k0 = c0 + (c1 - c0) * part_k / shares, k1 = c0 + (c1 - c0) * (part_k + 1) / shares;
     const bool row0 = mt * 16 + g < have, row1 = mt * 16 + g + 8 < have;
     const float* const x0 = p.x + static_cast<size_t>(row0 ? sh.rows[mt * 16 + g] : 0) * K + t * 8;
     const float* const x1 = p.x + static_cast<size_t>(row1 ? sh.rows[mt * 16 + g + 8] : 0) * K + t * 8;
-    float* const sums = reinterpret_cast<float*>(rest);  // [kSplit][T][kRankBlock]
-    for (int rb = 0; rb < rank; rb += kRankBlock) {
-      const int nt = min(kRankBlock, rank - rb) / 8;
+    float* const sums = reinterpret_cast<float*>(rest);  // [shares][T][wide_block]
+    for (int block = 0; block < rank; block += wide_block) {
+      const int rb = block + ks % groups * kRankBlock, nt = min(kRankBlock, rank - rb) / 8;
       float acc[kRankBlock / 8][4];
 #pragma unroll
       for (int n = 0; n < kRankBlock / 8; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-      if (mt < tiles) {
+      if (mt < tiles && nt > 0) {
         const size_t a0 = (static_cast<size_t>(id) * rank + rb + g) * K + t * 8;
         float4 x[4];  // of the next chunk: two rows, 8 elements each
         auto load_x = [&](int c) {
@@ -391,40 +402,50 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[n][i] += d[n][i];
         }
+        const int across = shares == 1 ? rank : wide_block;  // one share: it is the sum
+        float* const row = shares == 1 ? part + (mt * 16 + g) * rank + rb : sums + (part_k * T + mt * 16 + g) * wide_block + rb - block;
 #pragma unroll
         for (int n = 0; n < kRankBlock / 8; ++n) {
           if (n < nt) {
-            float* const to = sums + (ks * T + mt * 16 + g) * kRankBlock + n * 8 + 2 * t;
+            float* const to = row + n * 8 + 2 * t;
             *reinterpret_cast<float2*>(to) = make_float2(acc[n][0], acc[n][1]);
-            *reinterpret_cast<float2*>(to + 8 * kRankBlock) = make_float2(acc[n][2], acc[n][3]);
+            *reinterpret_cast<float2*>(to + 8 * across) = make_float2(acc[n][2], acc[n][3]);
           }
         }
       }
+      if (shares == 1) continue;
       __syncthreads();
-      // the warps' shares together: [tiles * 16][nt * 8], four at a time
-      for (int i = tid; i < tiles * 16 * nt * 2; i += kThreads) {
-        const int row = i / (nt * 2), r = (i - row * nt * 2) * 4;
+      // the warps' shares together, four ranks at a time
+      const int quads = min(wide_block, rank - block) / 4;
+      for (int i = tid; i < have * quads; i += kThreads) {
+        const int row = i / quads, r = (i - row * quads) * 4;
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kSplit; ++w) {
-          const float4 v = *reinterpret_cast<const float4*>(sums + (w * T + row) * kRankBlock + r);
+          if (w >= shares) break;
+          const float4 v = *reinterpret_cast<const float4*>(sums + (w * T + row) * wide_block + r);
           s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
         }
-        *reinterpret_cast<float4*>(part + row * rank + rb + r) = s;
+        *reinterpret_cast<float4*>(part + row * rank + block + r) = s;
       }
       __syncthreads();
     }
     cluster_sync();
-    // ---- t: the parts of all CTAs in order. Few rows: each CTA adds them all up; more: an eighth of them, which it hands to all
+    // ---- t: the parts of all CTAs in order. Few values: each CTA adds them all up (one barrier less: 64 rows 11.4 us for 11.7);
+    // more: its share of them, which it hands to all (rank 128, 4 rows: 13000 clocks by all, 2500 this way)
     const float scale = p.scales ? p.scales[id] : 1.0f;
-    const int quads = tiles * 4 * rank, stride = pair_stride(rank);  // groups of four ranks
-    for (int i = MT == 1 ? tid : cta * kThreads + tid; i < quads; i += (MT == 1 ? 1 : kCluster) * kThreads) {
-      float4 v[kCluster];
-#pragma unroll
-      for (int c = 0; c < kCluster; ++c) v[c] = peer_load4(peer(smem_at(part + i * 4), c));
+    const int quads = have * (rank / 4), stride = pair_stride(rank);  // groups of four ranks
+    const bool alone = MT == 1 && quads <= 4096 / kCluster;
+    for (int i = alone ? tid : cta * kThreads + tid; i < quads; i += (alone ? 1 : kCluster) * kThreads) {
       float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int c = 0; c < kCluster; ++c) s.x += v[c].x, s.y += v[c].y, s.z += v[c].z, s.w += v[c].w;
+      for (int c0 = 0; c0 < kCluster; c0 += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[c] = peer_load4(peer(smem_at(part + i * 4), c0 + c));
+#pragma unroll
+        for (int c = 0; c < 8; ++c) s.x += v[c].x, s.y += v[c].y, s.z += v[c].z, s.w += v[c].w;
+      }
       const int row = i / (rank / 4), r = (i - row * (rank / 4)) * 4;
       uint32_t h[4], l[4];
       split(s.x * scale, &h[0], &l[0]);
@@ -433,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
       split(s.w * scale, &h[3], &l[3]);
       // ranks 2k and 2k + 1 keep neighbouring places
       uint8_t *const to0 = rest + row * stride + pair_place(r, rank) * 8, *const to1 = rest + row * stride + pair_place(r + 2, rank) * 8;
-      if (MT == 1) {
+      if (alone) {
         *reinterpret_cast<uint4*>(to0) = make_uint4(h[0], l[0], h[1], l[1]);
         *reinterpret_cast<uint4*>(to1) = make_uint4(h[2], l[2], h[3], l[3]);
       } else {
@@ -444,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
         }
       }
     }
-    if (MT == 1) {
+    if (alone) {
       asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // this CTA has read the others' parts
       __syncthreads();
     } else {
@@ -455,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
     const bool wide = N % 4 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15) == 0;
     Weights<TYPE, 8> next[4];
     if (MT > 1 && kAhead && rank >= 32 && n0 < N) load_columns(w, p, b_row, n0, 0);
-    for (; n0 < N; n0 += kStep) {
+    for (; n0 < N; n0 += step) {
       float acc[MT][4][4];
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -466,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
       for (; r0 + 32 <= rank; r0 += 32) {
         if (kAhead) {
           const bool more = r0 + 64 <= rank;
-          if (more || n0 + kStep < N) load_columns(next, p, b_row, more ? n0 : n0 + kStep, more ? r0 + 32 : 0);
+          if (more || n0 + step < N) load_columns(next, p, b_row, more ? n0 : n0 + step, more ? r0 + 32 : 0);
         } else {
           load_columns(w, p, b_row, n0, r0);
         }
@@ -504,35 +525,61 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
             } else {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                if (n + i < N) to[n + i] += v[i];
+                if (n + i < N) asm volatile("red.global.add.f32 [%0], %1;" ::"l"(to + n + i), "f"(v[i]) : "memory");
             }
           }
         }
       }
     }
-    if (MT == 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // its own are no longer read
+    if (alone) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // its own are no longer read
     __syncthreads();  // of t and the rows, before the next job's
   }
 }
 
-template <int TYPE, int MT>
+template <int TYPE, int MT, int RB, int CS>
 cudaError_t launch(const LoraArgs& a, const LoraGrid& g, int n_most, cudaStream_t s) {
-  const int bytes = shared_bytes(16 * MT, g.rank_most, n_most);
-  static std::atomic<unsigned long long> allowed{0};
-  const cudaError_t e = allow_shared(lora_kernel<TYPE, MT>, 200 * 1024, allowed);
+  static std::atomic<unsigned long long> allowed{0}, wide{0};
+  cudaError_t e = allow_shared(lora_kernel<TYPE, MT, RB, CS>, 200 * 1024, allowed);
+  if (CS > 8 && e == cudaSuccess) {  // once a device, as allow_shared
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (e == cudaSuccess && !(wide.load(std::memory_order_relaxed) & bit)) {
+      e = cudaFuncSetAttribute(lora_kernel<TYPE, MT, RB, CS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e == cudaSuccess) wide.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCluster * std::min(g.jobs, kJobsGrid) * g.projections);
+  cfg.gridDim = dim3(CS * std::min(g.jobs, kJobsGrid) * g.projections * g.splits);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bytes;
+  cfg.dynamicSmemBytes = shared_bytes(16 * MT, g.rank_most, RB, n_most);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kCluster;
+  at[0].val.clusterDim.x = CS;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, lora_kernel<TYPE, MT>, a, g);
+  return cudaLaunchKernelEx(&cfg, lora_kernel<TYPE, MT, RB, CS>, a, g);
+}
+
+template <int TYPE>
+cudaError_t launch_type(const LoraArgs& a, LoraGrid g, int n_most, int columns_most, cudaStream_t s) {
+  constexpr int kPlaces = 304;  // CTAs that are resident, two an SM
+  const long long rows = static_cast<long long>(a.M) * g.projections;
+  const int MT = rows < 2432 ? 1 : g.rank_most > 128 ? 2 : 4;
+  g.rows = 16 * MT;
+  g.jobs = std::max(1, std::min(a.M, n_most) + a.M / g.rows);
+  g.splits = 1;
+  if (MT == 4) return launch<TYPE, 4, 32, 8>(a, g, n_most, s);
+  if (MT == 2) return launch<TYPE, 2, 32, 8>(a, g, n_most, s);
+  // Few jobs: larger clusters, and several of them for a job's columns.
+  const long long clusters = static_cast<long long>(std::min(g.jobs, kJobsGrid)) * g.projections;
+  const bool wide = clusters * 16 <= kPlaces / 2;
+  const int size = wide ? 16 : 8;  // a warp has 32 columns: 256 a CTA
+  g.splits = static_cast<int>(std::max(1ll, std::min(kPlaces / (clusters * size), (columns_most + 256ll * size - 1) / (256 * size))));
+  return wide ? launch<TYPE, 1, 16, 16>(a, g, n_most, s) : launch<TYPE, 1, 16, 8>(a, g, n_most, s);
 }
 
 }  // namespace
@@ -545,27 +592,18 @@ cudaError_t launch_lora(const LoraArgs& args, cudaStream_t s) {
     for (int k = i; k > 0 && a.p[k].type < a.p[k - 1].type; --k) std::swap(a.p[k], a.p[k - 1]);
   for (int i = 0; i < a.n_proj;) {
     LoraGrid g = {};
-    int e = i, n_most = 0;
+    int e = i, n_most = 0, columns_most = 0;
     g.first = i;
     for (; e < a.n_proj && a.p[e].type == a.p[i].type; ++e) {
       g.rank_most = std::max(g.rank_most, a.p[e].rank);
       n_most = std::max(n_most, a.p[e].n);
+      columns_most = std::max(columns_most, a.p[e].N);
     }
-    const int MT = static_cast<long long>(a.M) * (e - i) <= 16 * 38 ? 1 : g.rank_most > 128 ? 2 : 4;
     g.projections = e - i;
-    g.rows = 16 * MT;
-    g.jobs = std::max(1, std::min(a.M, n_most) + a.M / g.rows);
-    cudaError_t r;
-    auto by_rows = [&](auto type) {
-      constexpr int TYPE = decltype(type)::value;
-      return MT == 1 ? launch<TYPE, 1>(a, g, n_most, s) : MT == 2 ? launch<TYPE, 2>(a, g, n_most, s) : launch<TYPE, 4>(a, g, n_most, s);
-    };
-    if (a.p[i].type == kF32)
-      r = by_rows(std::integral_constant<int, kF32>());
-    else if (a.p[i].type == kF16)
-      r = by_rows(std::integral_constant<int, kF16>());
-    else
-      r = by_rows(std::integral_constant<int, kBF16>());
+    const int type = a.p[i].type;
+    const cudaError_t r = type == kF32   ? launch_type<kF32>(a, g, n_most, columns_most, s)
+                          : type == kF16 ? launch_type<kF16>(a, g, n_most, columns_most, s)
+                                         : launch_type<kBF16>(a, g, n_most, columns_most, s);
     if (r != cudaSuccess) return r;
     i = e;
   }

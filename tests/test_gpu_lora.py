@@ -57,6 +57,15 @@ def test_rows_get_their_adapters(xq, dtype, M, n, rank, K, N, spread):
     run(xq, M, [adapters(n, rank, K, N, dtype)], some_ids(M, n, spread=spread))
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("M,n,rank,K,N", [
+    (1, 1, 256, 32, 4100), (4, 2, 128, 4096, 9001), (16, 1, 64, 544, 4096), (16, 1, 72, 512, 300), (17, 1, 136, 1056, 130), (90, 2, 40, 2048, 515),
+    (33, 5, 248, 96, 77), (2431, 30, 16, 64, 36), (2432, 30, 16, 64, 36), (2500, 9, 64, 512, 264), (2450, 3, 256, 96, 130), (2600, 40, 8, 32, 77),
+])
+def test_ranks_and_rows_shared_out_otherwise(xq, dtype, M, n, rank, K, N):
+    run(xq, M, [adapters(n, rank, K, N, dtype)], some_ids(M, n, idle=M > 16))
+
+
 @pytest.mark.parametrize("M", [1, 5, 64, 300])
 def test_projections_together(xq, M):
     """Widths, ranks, types and numbers of adapters that differ, two inputs, one projection without scales."""
