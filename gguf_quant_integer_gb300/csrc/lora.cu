@@ -12,21 +12,22 @@
 //
 // Precision: both products run on the warp-level tensor cores in tf32, x and t as two numbers each (11 + 11 bits; hi is cut
 // off, so that nothing overflows) and fp32 adapters too (without lo x lo); 16-bit adapters are exact. A tensor core's
-// accumulator cuts off, towards 0, what an fp32 addition rounds, so sums over K leave it every 32 elements (kept in it for
-// K / 16, 4096 elements had 1.3e-6 of error) and y is added to in L2, in fp32, by one reduction a value.
+// accumulator cuts off, towards 0, what an fp32 addition rounds, and all these errors have one sign: so sums leave it every 16
+// elements of K and every 16 ranks (kept in it for K / 16, 4096 elements had 1.3e-6 of error; all of 256 ranks, with fp32
+// adapters, 2.2e-6, now 0.4e-6 at any rank; every 8 would be 0.37e-6). y is added to in L2, in fp32, by one reduction a value.
 //
 // T is 16 rows up to 2432 rows times projections, else 64 (32 beyond rank 128: shared memory): A and B are read once a job,
 // so more rows save L2 traffic, and fewer start more clusters (352 rows of rank 128 to 2 x 14336: 55 us, 137 with 64 rows a
-// job; 2854 rows of 25 adapters, 8960 -> 1536, rank 24: 87 us, 114 with 16). Few jobs have clusters of 16, and as many
+// job; 2854 rows of 25 adapters, 8960 -> 1536, rank 24: 72 us, above 110 with 16). Few jobs have clusters of 16, and as many
 // clusters for a job's columns as fill the device, which all work out x A^T (1 row to 2 x 14336, rank 16: 6.0 us, 9.8 with 8
 // CTAs a job). What bounds it: with few rows, a chain of memory round trips and instructions seen for the first time (one row
 // 4096 -> 4096, rank 16: 5.2 us, x A^T, the exchange and y in like parts; 64 rows of 16 adapters at q, k and v: 11.4 us); with
 // many, the warp-level tensor cores, 8 clocks a product of 16 x 8 x 8 on one of an SM's four sub-cores (4099 rows, rank 64, two
-// projections 4096 -> 14336: 371 us; 19.2 million products are 130 us at least, y's 0.94 GB 139 us); 777 mixed rows to 2 x
-// 8960, rank 8: 38 us, 0.1 GB. Tried and slower: y loaded and stored (expansion 180000 clocks a job instead of 100000; at widths
-// that are no multiple of 4, 1504 rows to 130 and 77 columns 38 us, 23 with single reductions), its lines prefetched into L2 (40
-// us for 39), 85 registers and three CTAs an SM for 16-row jobs (one row 7.6 us), 64 ranks a warp (spills), x and A two or
-// three chunks ahead (one row 5.6 us, 352 rows above 60 and 76).
+// projections 4096 -> 14336: 398 us, 371 with sums left in the tensor cores; 19.2 million products are 130 us at least, y's
+// 0.94 GB 139 us); 777 mixed rows to 2 x 8960, rank 8: 38 us, 0.1 GB. Tried and slower: y loaded and stored (at widths that are
+// no multiple of 4, 1504 rows to 130 and 77 columns 38 us, 21 with single reductions), its lines prefetched into L2 (40 us for
+// 39), 85 registers and three CTAs an SM for 16-row jobs (one row 7.6 us), 64 ranks a warp (spills), x and A two or three
+// chunks ahead (352 rows above 60 and 76).
 #include <algorithm>
 #include <utility>
 
@@ -258,19 +259,30 @@ __device__ __forceinline__ void load_columns(Weights<TYPE, W> (&w)[4], const Ada
 template <int TYPE, int MH, int W>
 __device__ __forceinline__ void expand(float (&acc)[MH][4][4], const Weights<TYPE, W> (&w)[4], int r0, const uint8_t* pairs, int stride, int tiles) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  constexpr int kSteps = W / 2 < 2 ? W / 2 : 2;  // products of 8 ranks before a sum leaves the tensor cores
 #pragma unroll
-  for (int s = 0; s < W / 2; ++s) {
-    uint32_t bhi[4][2], blo[4][2];
+  for (int s0 = 0; s0 < W / 2; s0 += kSteps) {
+    uint32_t bhi[kSteps][4][2], blo[kSteps][4][2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j].get(2 * s, bhi[j], blo[j]);
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j].get(2 * (s0 + s), bhi[s][j], blo[s][j]);
 #pragma unroll
     for (int m = 0; m < MH; ++m) {
       if (m >= tiles) break;
-      const uint8_t* const from = pairs + (m * 16 + g) * stride + (r0 + 8 * s + 2 * t) * 8;
-      const uint4 a = *reinterpret_cast<const uint4*>(from), b = *reinterpret_cast<const uint4*>(from + 8 * stride);
-      const uint32_t hi[4] = {a.x, b.x, a.z, b.z}, lo[4] = {a.y, b.y, a.w, b.w};
+      float d[4][4] = {};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) product<TYPE>(acc[m][j], hi, lo, bhi[j], blo[j]);
+      for (int s = 0; s < kSteps; ++s) {
+        const uint8_t* const from = pairs + (m * 16 + g) * stride + (r0 + 8 * (s0 + s) + 2 * t) * 8;
+        const uint4 a = *reinterpret_cast<const uint4*>(from), b = *reinterpret_cast<const uint4*>(from + 8 * stride);
+        const uint32_t hi[4] = {a.x, b.x, a.z, b.z}, lo[4] = {a.y, b.y, a.w, b.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) product<TYPE>(d[j], hi, lo, bhi[s][j], blo[s][j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][j][i] += d[j][i];
     }
   }
 }
@@ -331,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
     const int id = sh.adapter, tiles = (have + 15) / 16;
     const size_t b_row = static_cast<size_t>(id) * N;
     const int step = G.splits * kCluster * kWarps * 32;
-    constexpr bool kAhead = TYPE != kF32;  // the next 32 ranks' weights are loaded beside a block's products
+    // the next 32 ranks' weights are loaded beside a block's products; no registers for it with 64 rows (442 us for 400)
+    constexpr bool kAhead = TYPE != kF32 && MT < 4;
     Weights<TYPE, 8> w[4];
     int n0 = ((share * kCluster + cta) * kWarps + warp) * 32;
     if (MT == 1 && kAhead && rank >= 32 && n0 < N) load_columns(w, p, b_row, n0, 0);
@@ -380,9 +393,11 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
           load_a(c + 1);
           float d[kN][4];
 #pragma unroll
-          for (int n = 0; n < kN; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.0f;
-#pragma unroll
           for (int s = 0; s < 4; ++s) {
+            if (s % 2 == 0) {
+#pragma unroll
+              for (int n = 0; n < kN; ++n) d[n][0] = d[n][1] = d[n][2] = d[n][3] = 0.0f;
+            }
             uint32_t hi[4], lo[4];
             split(xs[0][2 * s], &hi[0], &lo[0]);
             split(xs[1][2 * s], &hi[1], &lo[1]);
@@ -396,11 +411,13 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
                 product<TYPE>(d[n], hi, lo, bhi, blo);
               }
             }
+            if (s % 2 == 1) {
+#pragma unroll
+              for (int n = 0; n < kN; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[n][i] += d[n][i];
+            }
           }
-#pragma unroll
-          for (int n = 0; n < kN; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] += d[n][i];
         }
         const int across = shares == 1 ? rank : wide_block;  // one share: it is the sum
         float* const row = shares == 1 ? part + (mt * 16 + g) * rank + rb : sums + (part_k * T + mt * 16 + g) * wide_block + rb - block;

@@ -137,6 +137,20 @@ def test_root_mean_square(xq, M, spread):
     assert ops_check.rms(y, want) <= 64 * 2.0 ** -24 / 4
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("M,n,rank,K,N", [(5, 4, 128, 8960, 1536), (3, 1, 256, 512, 4096), (3000, 4, 128, 4096, 1536), (3000, 2, 256, 1024, 520)])
+def test_sums_over_ranks_do_not_drift(xq, dtype, M, n, rank, K, N):
+    """A cut-off addition loses 2^-24 of the running sum on average and 2^-23 at most, always towards 0: with up to six between
+    two sums in fp32 that is 6 x 2^-24 of a product, 12 x 2^-24 for both; the dropped products of two lower halves are another
+    2^-22 / 4 each, and fp32 roundings at random some 3 x 2^-24: 17 x 2^-24 in all."""
+    a, b, s = adapters(n, rank, K, N, dtype, scaled=False)
+    ids = some_ids(M, n, idle=False)
+    x, y = torch.randn(M, K, device="cuda", generator=torch.Generator("cuda").manual_seed(9)), torch.zeros(M, N, device="cuda")
+    want, _ = ops_check.lora(x, a, b, s, ids, y)
+    xq.Adapters([(a, b, s, 0)]).add([x], [y], ids)
+    assert ops_check.rms(y, want) <= 17 * 2.0 ** -24
+
+
 def test_repeated_captured_and_on_another_stream(xq):
     """Bit for bit the same: no result depends on timing."""
     a, b, s = adapters(5, 16, 1024, 300, "fp16")
