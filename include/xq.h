@@ -640,7 +640,8 @@ XQ_API size_t xq_prompt_attn_workspace_bytes(const xq_prompts *prompts);
  *   s_j = scale * sum_d q_d * k_jd,   o = sum_j softmax(s)_j * v_j
  * over the keys j of its sequence up to itself and, with a window, the last
  * `window` of those. Scores, softmax statistics and sums are fp32; the softmax
- * weights of 16-bit calls are rounded to that type for the product with V.
+ * weights of 16-bit calls are rounded to that type for the product with V, and
+ * divided by their sum as rounded.
  * Rows of out that belong to no sequence (before starts[0], behind
  * starts[batch]) are left as they were. What a row does not see does not
  * reach it, infinities and NaN included. fp32 rows enter the tensor cores as two
