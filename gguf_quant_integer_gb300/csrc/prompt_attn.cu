@@ -29,16 +29,8 @@ PromptPieces pieces(const PromptArgs& a, uint8_t* base) {
   return w;
 }
 
-typedef cudaError_t (*TakeTwo)(unsigned int*, unsigned int*);
-typedef cudaError_t (*TakeOne)(unsigned int*);
-
-}  // namespace
-
-size_t prompt_attn_workspace(const PromptArgs& a) {
-  return a.type == kF32 && a.tokens > 0 && a.batch > 0 ? pieces(a, nullptr).bytes : 0;
-}
-
-cudaError_t launch_prompt_attn(const PromptArgs& a, void* workspace, cudaStream_t s) {
+// How a call's heads and tokens make row tiles.
+PromptTileArgs tiles(const PromptArgs& a) {
   PromptTileArgs p;
   p.a = a;
   const int group = a.heads / a.kv_heads;
@@ -46,6 +38,26 @@ cudaError_t launch_prompt_attn(const PromptArgs& a, void* workspace, cudaStream_
   p.pack = group <= kPromptRows && kPromptRows / group * group >= 96 ? group : 1;
   p.tokens_tile = kPromptRows / p.pack;
   p.units = a.heads / p.pack;
+  p.sums = nullptr;
+  return p;
+}
+
+typedef cudaError_t (*TakeTwo)(unsigned int*, unsigned int*);
+typedef cudaError_t (*TakeOne)(unsigned int*);
+
+}  // namespace
+
+size_t prompt_attn_workspace(const PromptArgs& a) {
+  if (a.tokens <= 0 || a.batch <= 0) return 0;
+  if (a.type == kF32) return pieces(a, nullptr).bytes;
+  // no row sees more keys than there are tokens
+  if (a.tokens <= kPromptRun * kPromptTileKeys) return 0;
+  const int row_tiles = prompt_row_tiles(a.dim);
+  return static_cast<size_t>(prompt_tile_grid(tiles(a), row_tiles)) * row_tiles * prompt_run_quads(a.dim) * sizeof(float4);
+}
+
+cudaError_t launch_prompt_attn(const PromptArgs& a, void* workspace, cudaStream_t s) {
+  PromptTileArgs p = tiles(a);
   if (a.type == kF32) {
     const PromptPieces w = pieces(a, static_cast<uint8_t*>(workspace));
     const cudaError_t e = launch_prompt_split(a, w, s);
@@ -57,6 +69,7 @@ cudaError_t launch_prompt_attn(const PromptArgs& a, void* workspace, cudaStream_
       default: return PromptPiecesDim<256>::launch(p, w, s);
     }
   }
+  p.sums = static_cast<float4*>(workspace);
   switch (a.dim) {
     case 64: return PromptTileDim<64>::launch(p, s);
     case 96: return PromptTileDim<96>::launch(p, s);

@@ -21,6 +21,10 @@
 // alternating direction; the copying warp finds them from the sequences' bounds (see next_item) an item ahead, so Q, K and V
 // of the next item are on their way, and its first scores are computed, while one ends.
 //
+// Sums: a tensor core's accumulator cuts off, towards 0, what an fp32 addition rounds, so an output that stayed there over a long
+// sequence would be too small by 8e-9 a key (fp16, V of one sign, 131071 keys: 1e-3, two half steps of the result). So after
+// kPromptRun key tiles the outputs are added to the row's sum in the workspace, in fp32, and the accumulator begins anew.
+//
 // What is not finite: scores of keys that a row does not see are replaced, but such a key's V would meet a weight of 0 in
 // the product, where an infinity or NaN spoils the row. So two warps look through the V tiles of which some row does not see
 // all keys, before the product, and put 0 in the place of such elements. Rows that do see one of them, and rows whose result
@@ -39,6 +43,9 @@
 
 namespace xq {
 
+constexpr int prompt_row_tiles(int dim) { return dim == 256 ? 1 : 2; }  // of a CTA: head size 256's outputs fill tensor memory
+constexpr int prompt_run_quads(int dim) { return kPromptRows * (dim + 1) / 4; }  // a row tile's sums and references, in 16 bytes
+
 template <int D>
 struct PromptTileDim {
   static cudaError_t launch(PromptTileArgs& a, cudaStream_t s);
@@ -50,11 +57,11 @@ struct PromptTileDim {
 
 namespace {
 
-constexpr int kKeys = 128;
+constexpr int kKeys = kPromptTileKeys;
 
 template <int D>
 struct PromptShape {
-  static constexpr int kTiles = D == 256 ? 1 : 2;               // row tiles
+  static constexpr int kTiles = prompt_row_tiles(D);            // row tiles
   static constexpr int kBox = D % 64 == 0 ? 64 : 32;            // elements of a swizzled row
   static constexpr int kLine = kBox * 2, kBoxes = D / kBox;
   static constexpr int kQ = kRows * D * 2, kStage = kKeys * D * 2;  // bytes: Q of a row tile; K or V of a tile
@@ -75,6 +82,54 @@ enum PromptBar { kPbDrain, kPbItem, kPbItemFree = kPbItem + 2, kPbQ = kPbItemFre
                  kPbP = kPbS + 2, kPbO = kPbP + 2, kPbFull = kPbO + 2 };
 
 
+
+// A row's sum over runs of tiles and the reference that it goes by (a row's 4 columns lie beside the other rows', the references
+// behind all columns). Functions of their own, that find these again each time, so that the softmax loop keeps its registers: written
+// into it they cost 16 sequences of 17 to 2048, which have no use for them, 208 -> 243 us.
+template <int D>
+__device__ __forceinline__ float4* run_sum(float4* sums, float** reference) {
+  const int r = threadIdx.x >> 7, row = threadIdx.x & 127;
+  float4* const sum = sums + (static_cast<size_t>(blockIdx.x) * prompt_row_tiles(D) + r) * prompt_run_quads(D);
+  *reference = reinterpret_cast<float*>(sum + D / 4 * kRows) + row;
+  return sum + row;
+}
+// JOIN: outputs += sum 2^(reference - e), else sum = sum 2^(reference - e) + outputs; `there`: there is a sum.
+template <int D, bool JOIN>
+__device__ __noinline__ void run_add(float4* sums, uint32_t outputs, float e, bool there) {
+  float* reference;
+  float4* const sum = run_sum<D>(sums, &reference);
+  const float f = there ? ex2(*reference - e) : 0.0f;
+  if (!JOIN) *reference = e;
+  float4 o[8], next[8];
+  auto load = [&](int c) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) next[x] = there ? sum[(c / 4 + x) * kRows] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  };
+  load(0);
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) o[x] = next[x];
+    if (c + 32 < D) load(c + 32);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[16];
+      __syncwarp();
+      ptx::tmem_ld16(outputs + c + 16 * h, w);
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float4 s = o[4 * h + x];
+        const float4 y = make_float4(fmaf(s.x, f, __uint_as_float(w[4 * x])), fmaf(s.y, f, __uint_as_float(w[4 * x + 1])),
+                                     fmaf(s.z, f, __uint_as_float(w[4 * x + 2])), fmaf(s.w, f, __uint_as_float(w[4 * x + 3])));
+        if (!JOIN) sum[(c / 4 + 4 * h + x) * kRows] = y;
+        w[4 * x] = __float_as_uint(y.x), w[4 * x + 1] = __float_as_uint(y.y), w[4 * x + 2] = __float_as_uint(y.z), w[4 * x + 3] = __float_as_uint(y.w);
+      }
+      if (JOIN) ptx::tmem_st16(outputs + c + 16 * h, w);
+    }
+  }
+  if (JOIN) ptx::tmem_wait_st();
+}
 
 template <int TYPE, int D>
 __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_kernel(const __grid_constant__ PromptTileArgs P) {
@@ -252,7 +307,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
         if (lead) {
 #pragma unroll
           for (int k = 0; k < kKeys / 16; ++k)
-            ptx::mma_f16_ts(d, a + 8 * k, vd + k * (2 * 8 * S::kLine / 16), idO, j > it.begin[r] || k > 0);
+            ptx::mma_f16_ts(d, a + 8 * k, vd + k * (2 * 8 * S::kLine / 16), idO, (j - it.begin[r]) % kPromptRun > 0 || k > 0);
           ptx::tc_commit(bar(kPbO + from));
         }
         __syncwarp();
@@ -357,6 +412,13 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
       ptx::f2 l = ptx::pk(0.0f, 0.0f);
       for (int i = 0; i < tiles; ++i, ++done) {
         const int key = (it.begin[r] + i) * kKeys;
+        const bool anew = i > 0 && i % kPromptRun == 0;
+        if (anew) {
+          ok = wait(kPbO + buffer(r, done - 1), turn(done - 1), 12);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          run_add<D, false>(P.sums, to, e, i > kPromptRun);
+        }
         ok = wait(kPbS + buffer(r, done), turn(done), 11);
         if (!ok) break;
         ptx::tc_fence_after();
@@ -386,7 +448,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
           const float f = ex2(e - next);
           e = next;
           l = ptx::mul2(l, ptx::pk(f, f));
-          if (i > 0) {
+          if (i > 0 && !anew) {
             ok = wait(kPbO + buffer(r, done - 1), turn(done - 1), 12);
             if (!ok) break;
             ptx::tc_fence_after();
@@ -429,6 +491,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
       ok = wait(kPbO + buffer(r, done - 1), turn(done - 1), 13);
       if (!ok) break;
       ptx::tc_fence_after();
+      if (tiles > kPromptRun) run_add<D, true>(P.sums, to, e, true);
       const float sum = ptx::lo32(l) + ptx::hi32(l), inv = 1.0f / sum;
       const size_t at = (static_cast<size_t>(it.first) + place) * A.heads + it.head + part;
       const bool store = live && XQ_IN(at, static_cast<size_t>(A.tokens) * A.heads, kChkPromptRow);
@@ -499,10 +562,7 @@ cudaError_t launch_tile(const PromptTileArgs& p, cudaStream_t s) {
   static std::atomic<unsigned long long> allowed{0};
   const cudaError_t e = allow_shared(prompt_tile_kernel<TYPE, D>, S::kSmem, allowed);
   if (e != cudaSuccess) return e;
-  // no more items than this: whole groups of tokens, and a part of one for each sequence
-  const long long items = (p.a.tokens / (S::kTiles * p.tokens_tile) + static_cast<long long>(p.a.batch)) * p.units;
-  const int grid = static_cast<int>(items < 152 ? (items < 1 ? 1 : items) : 152);
-  prompt_tile_kernel<TYPE, D><<<grid, 32 * S::kWarps, S::kSmem, s>>>(p);
+  prompt_tile_kernel<TYPE, D><<<prompt_tile_grid(p, S::kTiles), 32 * S::kWarps, S::kSmem, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -641,7 +641,9 @@ XQ_API size_t xq_prompt_attn_workspace_bytes(const xq_prompts *prompts);
  * over the keys j of its sequence up to itself and, with a window, the last
  * `window` of those. Scores, softmax statistics and sums are fp32; the softmax
  * weights of 16-bit calls are rounded to that type for the product with V, and
- * divided by their sum as rounded.
+ * divided by their sum as rounded. A tensor core's sums are cut off instead of
+ * rounded; a 16-bit call's cover 4096 keys at most (less than 3e-5 of the
+ * result, in the mean 6e-6) and go on in fp32, in the workspace.
  * Rows of out that belong to no sequence (before starts[0], behind
  * starts[batch]) are left as they were. What a row does not see does not
  * reach it, infinities and NaN included. fp32 rows enter the tensor cores as two

@@ -26,3 +26,73 @@ def test_what_all_weights_lose_alike_cancels(xq, dtype, H, Hk, D, window):  # no
     several = torch.ones(T, dtype=torch.bool, device="cuda")
     several[torch.tensor(starts[:-1])] = False  # a first token sees itself alone: exact
     assert ops_check.rms(out[several], want[several]) <= 1.02 * ops_check.rms(want[several].to(out.dtype), want[several])
+
+
+@pytest.mark.parametrize("T,D,H,window", [(131071, 128, 8, 0), (60000, 64, 16, 50000), (40000, 256, 4, 0), (40000, 96, 10, 30000)])
+def test_long_sums_do_not_drift(xq, T, D, H, window):  # noqa: F811
+    """Values of one sign: an addition in a tensor core's accumulator cuts off less than 2^-23 of the sum, always towards 0. A sum
+    stays in it for 4096 keys, 256 additions, and grows over them from 0: 2^-23 * 256 / 2 = 1.5e-5 of the result in the mean. The
+    mean of results rounded to fp16 at random (half steps of 2^-11 of values of 1 to 2: 2.8e-4 / 1.5) is off by 1.9e-4 / sqrt(1000),
+    four times which is 2.4e-5: 3.9e-5 in all."""
+    g = torch.Generator("cuda").manual_seed(12)
+    q = torch.randn(T, H, D, device="cuda", generator=g).half()
+    k = (0.1 * torch.randn(T, H, D, device="cuda", generator=g)).half()
+    v = (1 + torch.rand(H, D, device="cuda", generator=g) + 0.05 * torch.randn(T, H, D, device="cuda", generator=g)).half()
+    got = xq.prompt_attn(q, k, v, torch.tensor([0, T], dtype=torch.int32, device="cuda"), window=window)[-1].double()
+    first = max(0, T - window) if window else 0
+    z = torch.einsum("hd,jhd->hj", q[-1].double(), k[first:].double()) * D ** -0.5
+    want = torch.stack([torch.softmax(z[h], -1) @ v[first:, h].double() for h in range(H)])
+    assert abs(float(((got - want) / want).mean())) <= 3.9e-5
+    assert ops_check.rms(got, want) <= 3e-4  # at random: the result's rounding 2.0e-4, and the weights'
+    assert xq.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("slope", [6.0, -6.0, 0.0])
+def test_sums_over_runs_of_tiles(xq, dtype, D, slope):  # noqa: F811
+    """Keys enough for several runs of tiles whose sums are added up apart; scores that rise (each run has a reference of its
+    own), fall (later runs weigh nothing) and neither."""
+    lens = [9000, 4097, 4096, 60]
+    starts = starts_of(lens)
+    T = starts[-1]
+    q, k, v = inputs(T, 2, 1, D, dtype, 15)
+    if slope:
+        at = torch.cat([torch.arange(n, device="cuda") / n for n in lens])
+        q[:] = 1.0
+        k[:] = (k * 0.02 + slope * at[:, None, None]).to(k.dtype)
+    s = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    for window in (0, 4500):
+        out = xq.prompt_attn(q, k, v, s, scale=64 / D if slope else None, window=window)
+        want, bound = ops_check.attention(q, k, v, starts, 64 / D if slope else D ** -0.5, window)
+        ops_check.within(out, want, bound)
+    assert xq.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_runs_of_tiles_captured_and_side_by_side(xq, dtype):  # noqa: F811
+    """Two graphs whose calls have workspaces of their own, replayed at the same time, and a call with a workspace that is handed in."""
+    T = 9000
+    q, k, v = inputs(T, 4, 2, 128, dtype, 16)
+    s = torch.tensor([0, 8900, T], dtype=torch.int32, device="cuda")
+    wants = [xq.prompt_attn(q, k, v, s, window=w) for w in (0, 5000)]
+    outs, graphs = [], []
+    for w in (0, 5000):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(xq.prompt_attn(q, k, v, s, window=w))
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, graph in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], wants[0]) and torch.equal(outs[1], wants[1])
+    whole = torch.full((64 << 20,), 7, dtype=torch.uint8, device="cuda")
+    xq.prompt_attn(q, k, v, s, out=outs[0], workspace=whole[:32 << 20])
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], wants[0]) and bool((whole[32 << 20:] == 7).all())
+    with pytest.raises(xq.XQError):
+        xq.prompt_attn(q, k, v, s, workspace=whole[:1 << 20])
