@@ -11,7 +11,8 @@
 // reference e as in prompt_tile.cuh, hi cut off and lo the rest.
 //
 // K or V rows of a tile that differ by more than 2^12 in size would cost the small ones bits where no large one has a
-// weight; query rows that meet such tiles (as those that see something not finite) are computed by themselves (one_row).
+// weight; query rows that meet such tiles (as those that see something not finite, or keys that belong to two sequences, which bounds
+// out of order allow) are computed by themselves (one_row).
 //
 // A CTA has 128 rows. Q and the weights are the products' first operands in tensor memory (Q in shared memory was read at
 // 107 clocks a product, of which the tensor cores need 64), scores are double-buffered there, so that the products of a
@@ -40,7 +41,7 @@ namespace xq {
 struct PromptPieces {
   __half *k, *v;           // [2][tokens][kv_heads][dim], hi and lo
   float *k_power, *v_power;  // [slots][kv_heads], [slots][kv_heads][dim]: what the pieces are to be multiplied by
-  int *k_owner, *v_owner;  // [slots][kv_heads]: the slot's sequence; -1: none, -2: rows too far apart
+  int *k_owner, *v_owner;  // [slots][kv_heads]: the slot's sequence; -1: none, -2: rows too far apart, or another sequence's too
   int slots;               // tiles of keys of all sequences: tile j of sequence b has slot starts[b] / keys + b + j
   size_t bytes;
 };

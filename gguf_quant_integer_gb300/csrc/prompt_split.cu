@@ -3,6 +3,10 @@
 // x 2^s = hi + lo: hi = fp16(x 2^s), lo = fp16(x 2^s - hi), with 2^s from the largest finite magnitude of a tile of keys (K)
 // or of a column of it (V), which comes to 2^14 .. 2^15: 22 bits for everything down to 2^-17 of that, and an error of 2^-39
 // of it below. An element that is not finite is one in hi, and 0 in lo.
+//
+// Pieces lie at their rows' places, in sizes that go by their slot. With bounds that go back, a sequence that is left out may lie
+// between two that have rows in common: slots with such rows get no pieces, and who needs them computes his rows from the
+// values themselves.
 #include <climits>
 
 #include "prompt_pieces.cuh"
@@ -42,18 +46,20 @@ template <int D, bool VALUES>
 __device__ __forceinline__ void split_tile(const PromptArgs& A, const PromptPieces& W, int slot, int kv) {
   constexpr int kKeys = prompt_piece_keys(D);
   constexpr int kLanes = D == 96 ? 32 : D / 4, kGroups = kThreads / kLanes, kEach = kKeys / kGroups, kRowLanes = kLanes < 32 ? kLanes : 32;
-  __shared__ int sh_sequence;
+  __shared__ int sh_sequence, sh_back, sh_shared;
   __shared__ __align__(16) float sh_col[kGroups][D], sh_up[D];
   __shared__ unsigned sh_most, sh_least;
   const int tid = threadIdx.x;
   if (tid == 0) {
     sh_sequence = INT_MAX;
+    sh_back = sh_shared = 0;
     sh_most = 0u;
     sh_least = 0x7F800000u;
   }
   __syncthreads();
   for (int b = tid; b < A.batch; b += kThreads) {
     const int s0 = A.starts[b], s1 = A.starts[b + 1];
+    if (s1 < s0) sh_back = 1;
     if (s0 < 0 || s1 <= s0 || s1 > A.tokens) continue;
     const int at = slot - (s0 / kKeys + b);
     if (at >= 0 && at <= (s1 - s0 - 1) / kKeys) atomicMin(&sh_sequence, b);  // one, but for sequences that overlap
@@ -67,6 +73,18 @@ __device__ __forceinline__ void split_tile(const PromptArgs& A, const PromptPiec
     return;
   }
   const int s0 = A.starts[b], n = A.starts[b + 1] - s0, j0 = (slot - (s0 / kKeys + b)) * kKeys;
+  if (sh_back) {  // bounds that never go back have no rows in common
+    const int r0 = s0 + j0, r1 = s0 + min(n, j0 + kKeys);
+    for (int o = tid; o < A.batch; o += kThreads) {
+      const int o0 = A.starts[o], o1 = A.starts[o + 1];
+      if (o != b && o0 >= 0 && o1 <= A.tokens && max(o0, r0) < min(o1, r1)) sh_shared = 1;
+    }
+    __syncthreads();
+    if (sh_shared) {
+      if (tid == 0) owner[place] = -2;
+      return;
+    }
+  }
   const int l = tid % kLanes, g = tid / kLanes;
   const bool in = 4 * l < D;
   const size_t col = static_cast<size_t>(kv) * D + 4 * l;

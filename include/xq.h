@@ -651,7 +651,8 @@ XQ_API size_t xq_prompt_attn_workspace_bytes(const xq_prompts *prompts);
  * that meet 128 keys whose K or V rows differ by more than 2^12 in size, are
  * computed one by one (hundreds of times slower). A sequence whose bounds do not
  * satisfy 0 <= starts[b] <= starts[b+1] <= tokens is left out and recorded
- * (xq_device_error: kernel 5, wait 2). q, k, v and out are 16-byte aligned,
+ * (xq_device_error: kernel 5, wait 2); where the others then have rows in
+ * common, such a row of out is any one's of them. q, k, v and out are 16-byte aligned,
  * strides multiples of 16 bytes, starts 4-byte aligned; out must not overlap
  * an input. */
 XQ_API xq_status xq_prompt_attn(const xq_prompts *prompts, void *workspace, size_t ws_bytes, xq_stream stream);
