@@ -50,6 +50,24 @@ xq::PromptArgs prompt_args(const xq_prompts* p) {
   return a;
 }
 
+xq_status prompt_attn(const xq_prompts* p, void* workspace, size_t ws_bytes, xq_stream stream, long long wait, bool withhold) {
+  const xq_status st = check_prompt_sizes(p);
+  if (st != XQ_OK) return st;
+  if (p->window < 0 || !std::isfinite(p->scale)) return XQ_ERR_SHAPE;
+  const long long wq = static_cast<long long>(p->heads) * p->dim, wk = static_cast<long long>(p->kv_heads) * p->dim;
+  if (p->tokens > 1 && (p->q_stride < wq || p->k_stride < wk || p->v_stride < wk)) return XQ_ERR_SHAPE;
+  if (p->tokens == 0 || p->batch == 0) return XQ_OK;
+  if (!p->q || !p->k || !p->v || !p->out || !p->starts) return XQ_ERR_ARG;
+  const long long piece = 16 / xq::kv_elt_bytes(p->type);
+  if (!aligned(p->q, 16) || !aligned(p->k, 16) || !aligned(p->v, 16) || !aligned(p->out, 16) || !aligned(p->starts, 4) ||
+      !aligned(workspace, 16) || (p->tokens > 1 && (p->q_stride % piece || p->k_stride % piece || p->v_stride % piece)))
+    return XQ_ERR_ALIGN;
+  const xq::PromptArgs a = prompt_args(p);
+  const size_t need = xq::prompt_attn_workspace(a);
+  if (need > ws_bytes || (need > 0 && !workspace)) return XQ_ERR_WORKSPACE;
+  return status_of(xq::launch_prompt_attn(a, workspace, reinterpret_cast<cudaStream_t>(stream), wait, withhold));
+}
+
 }  // namespace
 
 extern "C" {
@@ -119,21 +137,13 @@ size_t xq_prompt_attn_workspace_bytes(const xq_prompts* prompts) {
 }
 
 xq_status xq_prompt_attn(const xq_prompts* p, void* workspace, size_t ws_bytes, xq_stream stream) {
-  const xq_status st = check_prompt_sizes(p);
-  if (st != XQ_OK) return st;
-  if (p->window < 0 || !std::isfinite(p->scale)) return XQ_ERR_SHAPE;
-  const long long wq = static_cast<long long>(p->heads) * p->dim, wk = static_cast<long long>(p->kv_heads) * p->dim;
-  if (p->tokens > 1 && (p->q_stride < wq || p->k_stride < wk || p->v_stride < wk)) return XQ_ERR_SHAPE;
-  if (p->tokens == 0 || p->batch == 0) return XQ_OK;
-  if (!p->q || !p->k || !p->v || !p->out || !p->starts) return XQ_ERR_ARG;
-  const long long piece = 16 / xq::kv_elt_bytes(p->type);
-  if (!aligned(p->q, 16) || !aligned(p->k, 16) || !aligned(p->v, 16) || !aligned(p->out, 16) || !aligned(p->starts, 4) ||
-      !aligned(workspace, 16) || (p->tokens > 1 && (p->q_stride % piece || p->k_stride % piece || p->v_stride % piece)))
-    return XQ_ERR_ALIGN;
-  const xq::PromptArgs a = prompt_args(p);
-  const size_t need = xq::prompt_attn_workspace(a);
-  if (need > ws_bytes || (need > 0 && !workspace)) return XQ_ERR_WORKSPACE;
-  return status_of(xq::launch_prompt_attn(a, workspace, reinterpret_cast<cudaStream_t>(stream)));
+  return prompt_attn(p, workspace, ws_bytes, stream, 0, false);
+}
+
+xq_status xq_debug_stalled_prompt_attn(const xq_prompts* p, void* workspace, size_t ws_bytes, long long clocks, int withhold,
+                                       xq_stream stream) {
+  if (clocks < 1 || clocks > (1ll << 32)) return XQ_ERR_ARG;
+  return prompt_attn(p, workspace, ws_bytes, stream, clocks, withhold != 0);
 }
 
 }  // extern "C"

@@ -58,7 +58,8 @@ enum OpsRecord : unsigned { kOpsBadAdapter = 1, kOpsBadStart = 2 };
 cudaError_t launch_lora(const LoraArgs& a, cudaStream_t s);
 cudaError_t launch_qk_rope(const RopeArgs& a, cudaStream_t s);
 size_t prompt_attn_workspace(const PromptArgs& a);
-cudaError_t launch_prompt_attn(const PromptArgs& a, void* workspace, cudaStream_t s);
+// wait: clocks that a wait lasts at most beside what slow work may take, 0 for the usual; withhold: test hook, no copies are issued.
+cudaError_t launch_prompt_attn(const PromptArgs& a, void* workspace, cudaStream_t s, long long wait = 0, bool withhold = false);
 
 // Read and clear the records of invalid indices (0: none), and the checked builds' words.
 cudaError_t take_lora_error(unsigned int* code);

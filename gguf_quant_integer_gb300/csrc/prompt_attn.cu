@@ -39,6 +39,8 @@ PromptTileArgs tiles(const PromptArgs& a) {
   p.tokens_tile = kPromptRows / p.pack;
   p.units = a.heads / p.pack;
   p.sums = nullptr;
+  p.wait = prompt_wait_limit(a, kPromptWait);
+  p.withhold = false;
   return p;
 }
 
@@ -56,8 +58,10 @@ size_t prompt_attn_workspace(const PromptArgs& a) {
   return static_cast<size_t>(prompt_tile_grid(tiles(a), row_tiles)) * row_tiles * prompt_run_quads(a.dim) * sizeof(float4);
 }
 
-cudaError_t launch_prompt_attn(const PromptArgs& a, void* workspace, cudaStream_t s) {
+cudaError_t launch_prompt_attn(const PromptArgs& a, void* workspace, cudaStream_t s, long long wait, bool withhold) {
   PromptTileArgs p = tiles(a);
+  if (wait > 0) p.wait = prompt_wait_limit(a, wait);
+  p.withhold = withhold;
   if (a.type == kF32) {
     const PromptPieces w = pieces(a, static_cast<uint8_t*>(workspace));
     const cudaError_t e = launch_prompt_split(a, w, s);

@@ -8,6 +8,14 @@
 namespace xq {
 
 constexpr int kPromptRows = 128;  // of a row tile
+constexpr long long kPromptWait = 1ll << 32;
+// A wait's limit in clocks: `base`, and what slow work of the CTA that it may be a wait for can take. That is up to 32 rows by
+// themselves, one behind the other (one_row; 32 keys take up to 16000 clocks at head size 128, with all SMs at it), and a search
+// of the next item (at most 304 levels, as each has an item at least; 32 sequences are a memory round trip). Eight times as much is allowed,
+// or twice. (Limits that begin anew while some word in shared memory counts on cost 5 to 11 % in the loops that poll.)
+inline long long prompt_wait_limit(const PromptArgs& a, long long base) {
+  return base + 1024ll * a.tokens * a.dim + 2048ll * 306 * (a.batch / 32 + 1);
+}
 
 struct PromptTileArgs {
   PromptArgs a;
@@ -15,6 +23,8 @@ struct PromptTileArgs {
   int tokens_tile;  // of a row tile: 128 / pack
   int units;     // head units: heads / pack
   CUtensorMap q, k, v;
+  long long wait;  // clocks that a wait lasts at most
+  bool withhold;   // test hook: no copies
   float4* sums;  // 16-bit rows: a CTA's row tiles' sums of outputs over runs of key tiles, [dim / 4][128 rows], and references, [128]
 };
 
@@ -33,7 +43,6 @@ namespace {
 
 __device__ unsigned int g_prompt_error;  // invalid indices
 __device__ unsigned int g_prompt_wait;   // a wait that ran out
-constexpr long long kPromptWait = 1ll << 32;
 constexpr int kRows = kPromptRows;
 constexpr int kWalkKept = 2;  // sequences a lane keeps in registers
 

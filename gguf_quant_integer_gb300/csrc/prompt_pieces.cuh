@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = sh_tmem;
   auto wait = [&](int i, unsigned parity, unsigned code) {
-    return __all_sync(0xffffffffu, ptx::mbar_wait(bar(i), parity & 1, &g_prompt_wait, code, kPromptWait)) != 0;
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar(i), parity & 1, &g_prompt_wait, code, P.wait)) != 0;
   };
   auto arrive = [&](int i) {
     __syncwarp();
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
         ptx::mbar_arrive(bar(kQbItem + (round & 1)));
       }
       __syncwarp();
-      if (!there) break;
+      if (!there || P.withhold) break;
       for (int i = 0; i < S::kQParts && ok; ++i) {
         const int st = stage(0);
         if (st < 0 || !lead) continue;

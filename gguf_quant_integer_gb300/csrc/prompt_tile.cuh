@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
   ptx::tc_fence_after();
   const uint32_t tmem = sh_tmem;
   auto wait = [&](int i, unsigned parity, unsigned code) {
-    return __all_sync(0xffffffffu, ptx::mbar_wait(bar(i), parity & 1, &g_prompt_wait, code, kPromptWait)) != 0;
+    return __all_sync(0xffffffffu, ptx::mbar_wait(bar(i), parity & 1, &g_prompt_wait, code, P.wait)) != 0;
   };
   // buffer of scores of row tile r's n-th tile, and how often it was used before
   auto buffer = [](int r, unsigned n) { return kTiles == 2 ? r : static_cast<int>(n & 1); };
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
         ptx::mbar_arrive(bar(kPbItem + (round & 1)));
       }
       __syncwarp();
-      if (!there) break;
+      if (!there || P.withhold) break;
       const int kv = it.head / (A.heads / A.kv_heads);
       const bool second = kTiles == 2 && it.end[1] > 0;
       // the first K before the queries, whose place is free later

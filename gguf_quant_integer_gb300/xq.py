@@ -38,7 +38,8 @@ SYMBOLS = ("xq_status_str", "xq_q8_bytes", "xq_weight_bytes", "xq_quantize_q8",
            "xq_debug_isums_iq4xs", "xq_device_error", "xq_debug_stalled_matmul_q4k", "xq_debug_tile_sums",
            "xq_debug_layer_matmuls", "xq_debug_check_probe", "xq_debug_stalled_ffn_layer",
            "xq_kv_bytes", "xq_kv_write", "xq_kv_read", "xq_kv_attn_workspace_bytes", "xq_kv_attn",
-           "xq_kv_attn_shared", "xq_lora_add", "xq_qk_norm_rope", "xq_prompt_attn_workspace_bytes", "xq_prompt_attn")
+           "xq_kv_attn_shared", "xq_lora_add", "xq_qk_norm_rope", "xq_prompt_attn_workspace_bytes", "xq_prompt_attn",
+           "xq_debug_stalled_prompt_attn")
 
 
 class XQError(RuntimeError):
@@ -163,7 +164,8 @@ def lib(path: str | None = None):
     L.xq_prompt_attn_workspace_bytes.argtypes = [P]
     L.xq_prompt_attn_workspace_bytes.restype = S
     L.xq_prompt_attn.argtypes = [P, P, S, P]
-    for fn in ("xq_lora_add", "xq_qk_norm_rope", "xq_prompt_attn"):
+    L.xq_debug_stalled_prompt_attn.argtypes = [P, P, S, ctypes.c_longlong, I, P]
+    for fn in ("xq_lora_add", "xq_qk_norm_rope", "xq_prompt_attn", "xq_debug_stalled_prompt_attn"):
         getattr(L, fn).restype = I
     for fn in ("xq_quantize_q8", "xq_matmul_q4k_q8", "xq_matmul_q6k_q8", "xq_debug_isums_q4k",
                "xq_debug_isums_q6k", "xq_layer_mixed", "xq_layer_mixed_static", "xq_matmul_q8_0_q8",
@@ -861,7 +863,7 @@ def qk_norm_rope(q, k, positions, rope, q_weight=None, k_weight=None, eps: float
 _prompt_need = {}  # sizes of a call -> workspace bytes
 
 
-def prompt_attn(q, k, v, starts, scale=None, window: int = 0, out=None, workspace=None, stream=None):
+def prompt_attn(q, k, v, starts, scale=None, window: int = 0, out=None, workspace=None, stream=None, _hook=None):
     """Causal attention of packed prompts: q [tokens, heads, dim], k and v [tokens, kv_heads, dim]; sequence b is rows
     starts[b] .. starts[b + 1] - 1 (starts int32 [batch + 1]). A token's rows are contiguous; tokens may be parts of longer
     rows. scale: 1 / sqrt(dim). window: how many keys a query sees at most, 0 for all. Returns out [tokens, heads, dim]; its
@@ -871,7 +873,7 @@ def prompt_attn(q, k, v, starts, scale=None, window: int = 0, out=None, workspac
         on = _other_stream(dev, stream)
         if on:
             with on:
-                return prompt_attn(q, k, v, starts, scale, window, out, workspace)
+                return prompt_attn(q, k, v, starts, scale, window, out, workspace, _hook=_hook)
     torch, qs, ks = _calls()[0], q.shape, k.shape
     if len(qs) != 3 or len(ks) != 3 or ks[0] != qs[0] or ks[2] != qs[2]:
         raise ValueError("q: [tokens, heads, dim], k and v: [tokens, kv_heads, dim]")
@@ -903,7 +905,13 @@ def prompt_attn(q, k, v, starts, scale=None, window: int = 0, out=None, workspac
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace: contiguous, on the call's device")
         at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    rc = L.xq_prompt_attn(p, at, size, handle)
+    rc = L.xq_prompt_attn(p, at, size, handle) if _hook is None else L.xq_debug_stalled_prompt_attn(p, at, size, *_hook, handle)
     if rc:
         raise XQError("xq_prompt_attn", rc)
     return out
+
+
+def debug_stalled_prompt_attn(q, k, v, starts, clocks: int, withhold: bool, **kw):
+    """Test hook: prompt_attn with `clocks` for the 2^32 of its waits' limit, and with withhold without its first copies, so that the
+    waits run out (see xq_debug_stalled_prompt_attn)."""
+    return prompt_attn(q, k, v, starts, _hook=(clocks, int(withhold)), **kw)

@@ -338,7 +338,9 @@ XQ_API xq_status xq_layer_mixed_static(const xq_proj *proj, int n_proj,
  * xq_kv_attn). Kernel 4 = the cache attention's 128-row tiles (waits 1-5 the
  * products, 6-9 the softmax, 10-12 the unpacking). Kernel 5 = adapters and
  * prompt attention, an invalid index: 1 an adapter id, 2 a sequence's bounds
- * (see xq_lora_add and xq_prompt_attn). Kernel 6 = a wait of prompt attention. Checked builds (the
+ * (see xq_lora_add and xq_prompt_attn). Kernel 6 = a wait of prompt attention
+ * (2^32 clocks, and 1024 * tokens * dim for rows computed one by one, and
+ * 20000 a sequence for the search of a CTA's next rows). Checked builds (the
  * library compiled with -DXQ_CHECK) also test the index, range or 16-byte alignment of each global
  * access whose address comes from nontrivial arithmetic, skip an access that
  * fails and record the site: kernel 9, wait = site (10-16 the GEMV, 20-26
@@ -656,6 +658,14 @@ XQ_API size_t xq_prompt_attn_workspace_bytes(const xq_prompts *prompts);
  * strides multiples of 16 bytes, starts 4-byte aligned; out must not overlap
  * an input. */
 XQ_API xq_status xq_prompt_attn(const xq_prompts *prompts, void *workspace, size_t ws_bytes, xq_stream stream);
+
+/* Test hook for the failure detection of xq_prompt_attn: the same call, with
+ * `clocks` (1 .. 2^32) for the 2^32 of its waits' limit, and with
+ * withhold != 0 the first item's copies never issued, so that the waits run
+ * out: out is left unwritten and xq_device_error reports kernel 6. Arguments
+ * and errors otherwise as xq_prompt_attn. */
+XQ_API xq_status xq_debug_stalled_prompt_attn(const xq_prompts *prompts, void *workspace, size_t ws_bytes,
+                                              long long clocks, int withhold, xq_stream stream);
 
 #ifdef __cplusplus
 }

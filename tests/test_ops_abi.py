@@ -107,3 +107,9 @@ def test_packed_structures_have_the_structures_layout(xq):
     values = [*range(1, 15), 0.25, 16]
     p = xq.xq_prompts.from_buffer_copy(xq._pack_prompts(*values))
     assert [getattr(p, f[0]) for f in p._fields_] == values and len(xq._pack_prompts(*values)) == ctypes.sizeof(p)
+
+
+@pytest.mark.parametrize("clocks,code", [(0, 1), (-1, 1), ((1 << 32) + 1, 1), (1, 1), (1 << 32, 1)])
+def test_stalled_prompt_attention(xq, clocks, code):
+    assert xq.lib().xq_debug_stalled_prompt_attn(ctypes.byref(prompts(xq, q=None)), FAKE, 1 << 40, clocks, 1, None) == code
+    assert xq.lib().xq_debug_stalled_prompt_attn(ctypes.byref(prompts(xq, tokens=0, q=None)), FAKE, 1 << 40, 1000, 1, None) == 0
