@@ -16,6 +16,10 @@
 // elements of K and every 16 ranks (kept in it for K / 16, 4096 elements had 1.3e-6 of error; all of 256 ranks, with fp32
 // adapters, 2.2e-6, now 0.4e-6 at any rank; every 8 would be 0.37e-6). y is added to in L2, in fp32, by one reduction a value.
 //
+// Infinities: one number of two is 0 where the other holds the value exactly, and 0 x infinity is NaN where the sum of products is an
+// infinity. So what comes out of the tensor cores not finite is computed again in fp32, term by term (the test for it costs 1 row
+// 0.15 us, 64 rows at q, k and v 0.25, 4099 rows nothing).
+//
 // T is 16 rows up to 2432 rows times projections, else 64 (32 beyond rank 128: shared memory): A and B are read once a job,
 // so more rows save L2 traffic, and fewer start more clusters (352 rows of rank 128 to 2 x 14336: 55 us, 137 with 64 rows a
 // job; 2854 rows of 25 adapters, 8960 -> 1536, rank 24: 72 us, above 110 with 16). Few jobs have clusters of 16, and as many
@@ -69,7 +73,7 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x = hi + lo to 22 bits: hi the upper 11 cut off (an infinity stays one, with lo = 0), lo rounded.
+// x = hi + lo to 22 bits: hi the upper 11 cut off (an infinity stays one, with lo = 0; what it meets see above), lo rounded.
 __device__ __forceinline__ void split(float x, uint32_t* hi, uint32_t* lo) {
   *hi = __float_as_uint(x) & 0xFFFFE000u;
   const float h = __uint_as_float(*hi), rest = h == x ? 0.0f : x - h;
@@ -147,6 +151,35 @@ __device__ __forceinline__ float4 peer_load4(uint32_t at) {
 }
 __device__ __forceinline__ void peer_store4(uint32_t at, float4 v) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+
+// Place of rank r among the pairs: a thread's ranks are 8, 4 or 2 neighbours (what it loads of B at once), of which step s of
+// a chunk takes two; the places of a step's four threads are neighbours.
+__device__ __forceinline__ int pair_place(int r, int rank) {
+  const int whole = rank & ~31, half = whole + (rank & 16);
+  const int c0 = r < whole ? r & ~31 : r < half ? whole : half;
+  const int per = r < whole ? 8 : r < half ? 4 : 2, i = r - c0, t = i / per, q = i - t * per;
+  return c0 + (q >> 1) * 8 + t * 2 + (q & 1);
+}
+
+// A part of a row's product with a row of A, term by term.
+template <int TYPE>
+__device__ __forceinline__ float exact_part(const float* x, const void* w, size_t at, int n) {
+  float s = 0.0f;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) s = fmaf(x[i], load_elt<TYPE>(w, at + i), s);
+  return s;
+}
+// The same of t's pairs and a row of B.
+template <int TYPE>
+__device__ __forceinline__ float exact_column(const uint8_t* pairs, const void* b, size_t at, int rank) {
+  float s = 0.0f;
+#pragma unroll 1
+  for (int r = 0; r < rank; ++r) {
+    const float2 t = *reinterpret_cast<const float2*>(pairs + pair_place(r, rank) * 8);
+    s = fmaf(t.x + t.y, load_elt<TYPE>(b, at + r), s);
+  }
+  return s;
 }
 
 struct JobShared {
@@ -233,15 +266,6 @@ __device__ __noinline__ int find_job(const int32_t* ids, int M, int n, int T, in
   }
   __syncthreads();
   return have;
-}
-
-// Place of rank r among the pairs: a thread's ranks are 8, 4 or 2 neighbours (what it loads of B at once), of which step s of
-// a chunk takes two; the places of a step's four threads are neighbours.
-__device__ __forceinline__ int pair_place(int r, int rank) {
-  const int whole = rank & ~31, half = whole + (rank & 16);
-  const int c0 = r < whole ? r & ~31 : r < half ? whole : half;
-  const int per = r < whole ? 8 : r < half ? 4 : 2, i = r - c0, t = i / per, q = i - t * per;
-  return c0 + (q >> 1) * 8 + t * 2 + (q & 1);
 }
 
 // B's W * 4 ranks from r0 on, of a lane's column in each of four products: columns are dealt out so that the results' lane t
@@ -429,6 +453,18 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
             *reinterpret_cast<float2*>(to + 8 * across) = make_float2(acc[n][2], acc[n][3]);
           }
         }
+        float odd = 0.0f;  // not finite if a sum is not
+#pragma unroll
+        for (int n = 0; n < kN; ++n) odd += (acc[n][0] + acc[n][1]) + (acc[n][2] + acc[n][3]);
+        if (!(fabsf(odd) < INFINITY)) {
+#pragma unroll 1
+          for (int i = 0; i < 4 * nt; ++i) {
+            const int r = i / 4 * 8 + 2 * t + (i & 1);
+            float* const at = row + r + (i & 2) * 4 * across;
+            if ((i & 2 ? row1 : row0) && !isfinite(*at))
+              *at = exact_part<TYPE>((i & 2 ? x1 : x0) - t * 8 + k0 * 32, p.a, (static_cast<size_t>(id) * rank + rb + r) * K + k0 * 32, (k1 - k0) * 32);
+          }
+        }
       }
       if (shares == 1) continue;
       __syncthreads();
@@ -525,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
         load_columns(part_w, p, b_row, n0, r0);
         expand<TYPE, MT, 2>(acc, part_w, r0, rest, stride, tiles);
       }
+      unsigned bad = 0u;  // a bit for the eight values of a row if they are not all finite
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         if (m >= tiles) break;
@@ -533,6 +570,13 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
           const int place = m * 16 + h * 8 + g, row = place < have ? sh.rows[place] : -1;
           if (row < 0 || !XQ_IN(row, A.M, kChkLoraRow)) continue;
           float* const to = p.y + static_cast<size_t>(row) * N;
+          float sum = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sum += acc[m][j][2 * h] + acc[m][j][2 * h + 1];
+          if (!(fabsf(sum) < INFINITY)) {
+            bad |= 1u << (m * 2 + h);
+            continue;
+          }
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const int n = n0 + 16 * q + 4 * t;
@@ -546,6 +590,12 @@ __global__ void __launch_bounds__(kThreads, 2) lora_kernel(const __grid_constant
             }
           }
         }
+      }
+      for (; bad != 0u; bad &= bad - 1u) {
+        const int place = (__ffs(bad) - 1) * 8 + g, n = n0 + 4 * t;
+#pragma unroll 1
+        for (int c = n; c < min(n + 20, N); c += (c - n) == 3 ? 13 : 1)
+          atomicAdd(p.y + static_cast<size_t>(sh.rows[place]) * N + c, exact_column<TYPE>(rest + place * stride, p.b, (b_row + c) * rank, rank));
       }
     }
     if (alone) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // its own are no longer read

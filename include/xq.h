@@ -581,8 +581,9 @@ typedef struct {
  * are 16-byte aligned, y, scales and ids 4-byte. Products are of fp32's
  * precision (x and x a^T enter the tensor cores as two tf32 numbers each, 22
  * bits, fp32 adapters too, 16-bit ones exactly), sums are fp32; a value of y
- * that lies below fp32's normal range may count as 0. A row's result does not
- * depend on the other rows' values. M == 0 enqueues nothing. */
+ * that lies below fp32's normal range may count as 0. Infinities and NaN give
+ * what sums of products give. A row's result does not depend on the other
+ * rows' values. M == 0 enqueues nothing. */
 XQ_API xq_status xq_lora_add(const xq_adapters *proj, int n_proj, const float *const *inputs, int n_inputs, int M,
                              const int32_t *ids, xq_stream stream);
 
