@@ -4,8 +4,9 @@
 // Mathematics: r = x * w / sqrt(mean(x^2) + eps); pair (a, b) of r turns by
 // the angle of its position. An angle is position * turns mod 2^64 in units of
 // 2^-64 of a full turn: an integer product whose overflow drops whole turns, so
-// it is exact at any position (position * frequency in fp32 is off by 0.004
-// at 131071). What is left after the nearest quarter turn is at most an eighth
+// it is exact at any position for the turns it is given, which a table rounds
+// to 2^-65 (at position 2^40 that is 2e-7; position * frequency in fp32 is off
+// by 0.004 at 131071). What is left after the nearest quarter turn is at most an eighth
 // of a turn, known to 2^-34 of one.
 //
 // A lane has 8 elements of a row, so a row of 64, 128 or 256 takes 8, 16 or 32

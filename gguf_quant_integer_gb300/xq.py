@@ -8,6 +8,7 @@ name. A missing library is an error: there is no CPU or library fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import struct
 
@@ -781,29 +782,60 @@ class Adapters:
         return ys
 
 
+def _turns(base, rot, factors):
+    """base^(-2i / rot) / factors[i] radians as parts of a full turn in units of 2^-64, to the nearest one. With 64-bit floats they had
+    53 bits, and an angle at position 2^40 was off by 1.6e-4."""
+    import decimal
+
+    import numpy as np
+    with np.errstate(all="ignore"):
+        freq = np.float64(base) ** (np.arange(0, rot, 2, dtype=np.float64) / -max(rot, 1))
+        if factors is not None:
+            freq = freq / factors
+    if not np.isfinite(freq).all():
+        raise ValueError("base and factors have to give finite frequencies")
+    with decimal.localcontext() as ctx:
+        # 64 bits behind the point, whatever is before it
+        ctx.prec = 45 + max([0, *(math.frexp(f)[1] * 3 // 10 + 1 for f in freq.tolist())])
+        ctx.Emin, ctx.Emax = decimal.MIN_EMIN, decimal.MAX_EMAX
+        D = decimal.Decimal
+
+        def arctan(n):  # of 1 / n
+            total = term = D(1) / n
+            k = 1
+            while abs(term) > D(10) ** -ctx.prec:
+                term /= -n * n
+                k += 2
+                total += term / k
+            return total
+
+        over_turn = D(2) ** 64 / (8 * (4 * arctan(5) - arctan(239)))  # 2^64 / (2 pi), Machin's formula
+        step = -2 * D(float(base)).ln() / rot if rot and math.isfinite(base) else D(0)
+        turns = []
+        for i, f in enumerate(freq.tolist()):
+            exact = D(0) if f == 0.0 else (step * i).exp() / (D(1) if factors is None else D(float(factors[i]))) * over_turn
+            turns.append(int(exact.to_integral_value(decimal.ROUND_HALF_EVEN)) % (1 << 64))
+    return turns
+
+
 class Rope:
     """Position rotation: the first `rot` elements of a head turn in rot / 2 pairs, pair i by base^(-2i / rot) radians a
     position, divided by factors[i] if given. pairs: neighbouring elements (2i, 2i + 1) make a pair, otherwise (i, i + rot / 2).
-    magnitude: factor of the rotated elements."""
+    magnitude: factor of the rotated elements. The table's angles are rounded to 2^-64 of a turn a position, which is all that is
+    lost at far positions."""
 
     def __init__(self, rot: int, base: float = 10000.0, factors=None, pairs: bool = False, magnitude: float = 1.0, device="cuda"):
         import numpy as np
         torch = _calls()[0]
         if rot < 0 or rot % 16:
             raise ValueError("rot: a multiple of 16")
-        freq = float(base) ** (np.arange(0, rot, 2, dtype=np.float64) / -max(rot, 1))
         if factors is not None:
             factors = np.asarray(factors.cpu() if hasattr(factors, "cpu") else factors, dtype=np.float64)
-            if factors.shape != freq.shape:
+            if factors.shape != (rot // 2,):
                 raise ValueError(f"{rot // 2} factors expected")
-            with np.errstate(divide="ignore", invalid="ignore"):
-                freq = freq / factors
-        turns = freq / (2 * np.pi)
-        if not np.isfinite(turns).all():
-            raise ValueError("base and factors have to give finite frequencies")
-        turns = np.rint((turns - np.floor(turns)) * 2.0 ** 64)  # whole turns a position change nothing
         self.rot, self.pairs, self.magnitude = rot, bool(pairs), float(magnitude)
-        self.turns = torch.tensor([(int(t) + (1 << 63)) % (1 << 64) - (1 << 63) for t in turns], dtype=torch.int64, device=device)
+        turns = [(t + (1 << 63)) % (1 << 64) - (1 << 63) for t in _turns(float(base), rot, factors)]
+        self.turns = torch.tensor(turns, dtype=torch.int64, device=device)
         self._device, self._at = self.turns.get_device(), self.turns.data_ptr()
 
 

@@ -611,8 +611,8 @@ typedef struct {
  *   (r_a, r_b) of pair i becomes magnitude * (r_a cos - r_b sin, r_b cos + r_a sin),
  *   angle = 2 pi * frac(position * turns[i] / 2^64),
  * in fp32, rounded once to y_type. The product of a position and turns is
- * taken modulo 2^64, so angles are as exact at far positions (negative ones
- * too) as at near ones. An output may be its input (same pointer, type and
+ * taken modulo 2^64, so at far positions (negative ones too) an angle is off by
+ * no more than turns[i] is, times the position. An output may be its input (same pointer, type and
  * stride); otherwise it must not overlap an input. q, k and the results are
  * aligned to their elements (rows at multiples of 16 bytes are moved in
  * 16-byte pieces), positions and turns to 8 bytes, weights to 4.
