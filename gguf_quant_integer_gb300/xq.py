@@ -458,9 +458,11 @@ class Layer:
         """The projections' outputs; with ids int32 [M], each row's adapter (negative: none) added to them."""
         if ids is not None and self.adapters is None:
             raise ValueError("the layer has no adapters")
+        # refused or not, before the projections write y
+        call = None if ids is None else self.adapters._call(inputs, self.adapted, ids, stream)
         layer_mixed(self.desc, inputs, self.M, self.workspace, stream)
-        if ids is not None:
-            self.adapters.add(inputs, self.adapted, ids, stream)
+        if call is not None:
+            self.adapters._launch(call)
         return self.y
 
     def weight_bytes(self) -> int:
@@ -734,7 +736,7 @@ class Adapters:
         if not 1 <= len(projs) <= 16:
             raise ValueError("1 to 16 projections a call")
         self._device = dev = projs[0][0].get_device()
-        self._keep, self._shapes, self._args = [], [], []
+        self._keep, self._shapes, self._args, self._aligned = [], [], [], True
         for a, b, scales, inp in projs:
             if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2] or a.dtype != b.dtype:
                 raise ValueError("a: [n, rank, K], b: [n, N, rank], of one dtype")
@@ -750,6 +752,7 @@ class Adapters:
                 raise ValueError("an input's index is 0 to 63, and there are at most 8192 adapters")
             self._args += [_float_type(a.dtype), n, rank, K, b.shape[1], a.data_ptr(), b.data_ptr(),
                            0 if scales is None else scales.data_ptr(), 0, inp]
+            self._aligned &= b.shape[1] == 0 or (a.data_ptr() | b.data_ptr()) % 16 == 0
             self._keep.append((a, b, scales))
             self._shapes.append(((b.shape[1],), (K,), inp))
         self._pack = struct.Struct("@" + _ADAPTERS * len(projs)).pack
@@ -761,12 +764,17 @@ class Adapters:
     def add(self, inputs, ys, ids, stream=None):
         """Add to each row of the projections' outputs ys (fp32 [M, N] each) what the adapter that ids int32 [M] names gives
         for the row of its input (fp32 [M, K]); rows of a negative id are left as they are. Returns ys."""
+        self._launch(self._call(inputs, ys, ids, stream))
+        return ys
+
+    def _call(self, inputs, ys, ids, stream):
+        """The arguments of a call that nothing is wrong with."""
         dev, f32, rows = self._device, self._float32, tuple(ids.shape)
         if len(rows) != 1 or ids.dtype != self._int32 or not ids.is_contiguous() or ids.get_device() != dev:
             raise ValueError("ids: contiguous int32 [M], on the adapters' device")
         if len(ys) != len(self._shapes) or len(inputs) < self._n_inputs:
             raise ValueError(f"{len(self._shapes)} outputs and {self._n_inputs} inputs expected, got {len(ys)} and {len(inputs)}")
-        args, ins, at = self._args.copy(), [0] * self._n_inputs, 8  # a call's own: calls may run side by side
+        args, ins, at, odd = self._args.copy(), [0] * self._n_inputs, 8, 0  # a call's own: calls may run side by side
         for y, (N, K, inp) in zip(ys, self._shapes):
             x = inputs[inp]
             if x.shape != rows + K or x.dtype != f32 or not x.is_contiguous() or x.get_device() != dev:
@@ -775,11 +783,15 @@ class Adapters:
                 raise ValueError(f"an output: contiguous float32 {[*rows, *N]}, on the adapters' device")
             args[at], ins[inp] = y.data_ptr(), x.data_ptr()
             at += 10
-        rc = self._add(self._pack(*args), len(ys), self._pack_inputs(*ins), self._n_inputs, rows[0], ids.data_ptr(),
-                       _handle(dev, stream))
+            odd |= x.data_ptr() & 15 if N[0] else 0
+        if rows[0] and (odd or not self._aligned):
+            raise XQError("xq_lora_add", 3)  # not on a 16-byte boundary
+        return (self._pack(*args), len(ys), self._pack_inputs(*ins), self._n_inputs, rows[0], ids.data_ptr(), _handle(dev, stream))
+
+    def _launch(self, call):
+        rc = self._add(*call)
         if rc:
             raise XQError("xq_lora_add", rc)
-        return ys
 
 
 def _turns(base, rot, factors):
