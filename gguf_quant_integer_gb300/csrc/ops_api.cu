@@ -84,7 +84,9 @@ xq_status xq_lora_add(const xq_adapters* proj, int n_proj, const float* const* i
   for (int i = 0; i < n_proj; ++i) {
     const xq_adapters& p = proj[i];
     if (!float_type(p.type) || p.input < 0 || p.input >= n_inputs) return XQ_ERR_ARG;
-    if (p.n < 0 || p.n > 8192 || p.rank < 8 || p.rank > 256 || p.rank % 8 || p.K <= 0 || p.K % 32 || p.N < 0) return XQ_ERR_SHAPE;
+    if (p.n < 0 || p.n > 8192 || p.rank < 8 || p.rank > 256 || p.rank % 8 || p.K <= 0 || p.K % 32 || p.N < 0 ||
+        p.N > (1 << 30))  // a cluster's steps over the columns stay within an int
+      return XQ_ERR_SHAPE;
     if (M == 0 || p.N == 0) continue;
     const float* const x = inputs[p.input];
     if (!x || !p.y || (p.n > 0 && (!p.a || !p.b))) return XQ_ERR_ARG;

@@ -560,7 +560,7 @@ typedef struct {
     int type;            /* XQ_TYPE_F32, XQ_TYPE_F16 or XQ_TYPE_BF16, of a and b */
     int n;               /* adapters, at most 8192 */
     int rank;            /* a multiple of 8, 8 .. 256 */
-    int K, N;            /* the projection's: K a positive multiple of 32 */
+    int K, N;            /* the projection's: K a positive multiple of 32, N at most 2^30 */
     const void *a;       /* [n][rank][K] */
     const void *b;       /* [n][N][rank] */
     const float *scales; /* [n], or NULL for 1 */

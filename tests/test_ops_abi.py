@@ -113,3 +113,9 @@ def test_packed_structures_have_the_structures_layout(xq):
 def test_stalled_prompt_attention(xq, clocks, code):
     assert xq.lib().xq_debug_stalled_prompt_attn(ctypes.byref(prompts(xq, q=None)), FAKE, 1 << 40, clocks, 1, None) == code
     assert xq.lib().xq_debug_stalled_prompt_attn(ctypes.byref(prompts(xq, tokens=0, q=None)), FAKE, 1 << 40, 1000, 1, None) == 0
+
+
+@pytest.mark.parametrize("N,code", [((1 << 30) + 1, 2), ((1 << 31) - 1, 2), (1 << 30, 0)])
+def test_adapters_of_very_many_columns(xq, N, code):
+    """A step over the columns past 2^31 would be a negative column. (No rows: nothing is launched.)"""
+    assert lora(xq, N=N, M=0 if code == 0 else 1) == code
