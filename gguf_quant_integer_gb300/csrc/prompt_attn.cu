@@ -23,6 +23,7 @@ PromptPieces pieces(const PromptArgs& a, uint8_t* base) {
   w.v = reinterpret_cast<__half*>(take(k * d * 4));
   w.k_power = reinterpret_cast<float*>(take(tiles * 4));
   w.v_power = reinterpret_cast<float*>(take(tiles * d * 4));
+  w.v_most = reinterpret_cast<float*>(take(tiles * 4));
   w.k_owner = reinterpret_cast<int*>(take(tiles * 4));
   w.v_owner = reinterpret_cast<int*>(take(tiles * 4));
   w.bytes = at;

@@ -10,9 +10,9 @@ namespace xq {
 constexpr int kPromptRows = 128;  // of a row tile
 constexpr long long kPromptWait = 1ll << 32;
 // A wait's limit in clocks: `base`, and what slow work of the CTA that it may be a wait for can take. That is up to 32 rows by
-// themselves, one behind the other (one_row; 32 keys take up to 16000 clocks at head size 128, with all SMs at it), and a search
-// of the next item (at most 304 levels, as each has an item at least; 32 sequences are a memory round trip). Eight times as much is allowed,
-// or twice. (Limits that begin anew while some word in shared memory counts on cost 5 to 11 % in the loops that poll.)
+// themselves, one behind the other (one_row; 32 keys take up to 18000 clocks at head size 128, with all SMs at it; 131000 are allowed),
+// and a search of the next item (at most 304 levels, as each has an item at least; 32 sequences are a memory round trip, some 600
+// clocks; 2048 are allowed). (Limits that begin anew while some word in shared memory counts on cost 5 to 11 % in the loops that poll.)
 inline long long prompt_wait_limit(const PromptArgs& a, long long base) {
   return base + 1024ll * a.tokens * a.dim + 2048ll * 306 * (a.batch / 32 + 1);
 }

@@ -10,9 +10,10 @@
 // small products first; outputs are added up in registers. Scores of large and small weights: a weight is 2^(z - e), its
 // reference e as in prompt_tile.cuh, hi cut off and lo the rest.
 //
-// K or V rows of a tile that differ by more than 2^12 in size would cost the small ones bits where no large one has a
-// weight; query rows that meet such tiles (as those that see something not finite, or keys that belong to two sequences, which bounds
-// out of order allow) are computed by themselves (one_row).
+// Pieces below fp16's normal range are off by 2^-39 of the tile's largest (K) or the column's (V). Where a tile's rows differ by
+// more than 2^12 in size, that may show: in K, for scores that could pass 2^20, of which it is 2^-20 or more (c_tile below); in V,
+// for results below 2^-15 of the tile's largest row, which has no weight there. Such rows, as those that see something not
+// finite, or keys that belong to two sequences (which bounds out of order allow), are computed by themselves (one_row).
 //
 // A CTA has 128 rows. Q and the weights are the products' first operands in tensor memory (Q in shared memory was read at
 // 107 clocks a product, of which the tensor cores need 64), scores are double-buffered there, so that the products of a
@@ -40,8 +41,9 @@ namespace xq {
 // The workspace.
 struct PromptPieces {
   __half *k, *v;           // [2][tokens][kv_heads][dim], hi and lo
-  float *k_power, *v_power;  // [slots][kv_heads], [slots][kv_heads][dim]: what the pieces are to be multiplied by
-  int *k_owner, *v_owner;  // [slots][kv_heads]: the slot's sequence; -1: none, -2: rows too far apart, or another sequence's too
+  float *k_power, *v_power;  // [slots][kv_heads] (negative: rows far apart), [slots][kv_heads][dim]: what the pieces are to be multiplied by
+  float* v_most;           // [slots][kv_heads]: the largest value, 0 unless rows are far apart
+  int *k_owner, *v_owner;  // [slots][kv_heads]: the slot's sequence; -1: none, -2: another sequence's too
   int slots;               // tiles of keys of all sequences: tile j of sequence b has slot starts[b] / keys + b + j
   size_t bytes;
 };
@@ -108,6 +110,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
   __shared__ uint32_t sh_tmem;
   __shared__ Item sh_item[2];
   __shared__ unsigned sh_odd[2];                        // rows of the item have to be looked at (1) or computed by themselves (2)
+  __shared__ unsigned sh_most[2];                       // largest value of the item's tiles whose V rows are far apart, as bits
   __shared__ float sh_k[2];                             // the tile's powers of two, by tile & 1
   __shared__ __align__(16) float sh_v[2][S::kV];
   __shared__ float sh_ref[2][kRows];                    // the rows' references, by tile & 1
@@ -202,6 +205,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
       if (lead) {
         sh_item[round & 1] = it;
         sh_odd[round & 1] = 0u;
+        sh_most[round & 1] = 0u;
         ptx::mbar_arrive(bar(kQbItem + (round & 1)));
       }
       __syncwarp();
@@ -335,7 +339,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
         float vp[S::kV / 32];
 #pragma unroll
         for (int x = 0; x < S::kV / 32; ++x) vp[x] = W.v_power[place * D + it.half * S::kV + x * 32 + lane];
-        const float kp = W.k_power[place];
+        const float kp = W.k_power[place], most = W.v_most[place];
         const bool whole = known && W.k_owner[place] == it.sequence && W.v_owner[place] == it.sequence;
         ok = n < 2 || wait(kQbPowerFree + b, (n >> 1) - 1, 17);
         if (!ok) break;
@@ -344,6 +348,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
         if (lane == 0) {
           sh_k[b] = kp;
           if (!whole) atomicOr(&sh_odd[items & 1], 2u);
+          if (most > 0.0f) atomicMax(&sh_most[items & 1], __float_as_uint(most));
         }
         arrive(kQbPower + b);
         const unsigned st[2] = {S::kKStages + 2 * n % S::kVStages, S::kKStages + (2 * n + 1) % S::kVStages};  // V's lo and hi
@@ -449,7 +454,9 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
           if (!ok) break;
           ptx::tc_fence_after();
           const uint32_t ts = tl + b * kKeys + half * (kKeys / 2);
-          const float c_tile = cq * sh_k[b];
+          const float kp = sh_k[b], c_tile = cq * fabsf(kp);
+          // rows far apart: what K's pieces leave out comes to this much of a score (2^15 2^-25 for each product)
+          if (kp < 0.0f && !(c_tile * (D * 0x1p-10f) < 0x1p-20f)) l = NAN;
           const bool edge = masked<kKeys>(P, it.place, j * kKeys);
           // 32 scores from column c on, those that the row does not see as -infinity
           ptx::f2 s[16];
@@ -573,6 +580,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
         ptx::f2 odd = ptx::pk(sum * 0.0f, 0.0f);  // NaN if anything is not finite
 #pragma unroll
         for (int x = 0; x < S::kV / 2; ++x) odd = ptx::fma2(o[x], ptx::pk(0.0f, 0.0f), odd);
+        float top = 0.0f;  // the row's largest result
         // Back into tensor memory, and from there 32 columns at a time in a rolled loop (see above), through shared memory, so
         // that a store has 4 rows' lines, not 32.
 #pragma unroll
@@ -582,6 +590,7 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
           for (int x = 0; x < 16; x += 2) {
             const ptx::f2 u = ptx::mul2(o[(c + x) / 2], ptx::pk(inv, inv));
             w[x] = __float_as_uint(ptx::lo32(u)), w[x + 1] = __float_as_uint(ptx::hi32(u));
+            top = max3(top, fabsf(ptx::lo32(u)), fabsf(ptx::hi32(u)));
           }
           ptx::tmem_st16(tl + S::kColO + c, w);
         }
@@ -615,6 +624,8 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
         arrive(kQbOFree + ((n - 1) & 1));
         const unsigned look = sh_odd[items & 1];
         bool meets = (look & 2u) != 0;  // pieces that do not hold the values, or an element that was put to 0
+        const float most = __uint_as_float(sh_most[items & 1]);
+        meets |= most > 0.0f && !(top >= most * 0x1p-15f);
         if (look & 1u) {
           const int lim1 = place + 1, lim0 = A.window ? max(0, lim1 - A.window) : 0;
 #pragma unroll 1

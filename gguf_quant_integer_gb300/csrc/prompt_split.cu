@@ -113,6 +113,7 @@ __device__ __forceinline__ void split_tile(const PromptArgs& A, const PromptPiec
   }
   if (in) *reinterpret_cast<float4*>(&sh_col[g][4 * l]) = top;
   __syncthreads();
+  const bool apart = __uint_as_float(sh_most) > 4096.0f * __uint_as_float(sh_least);  // its rows differ much in size
   for (int c = tid; c < D; c += kThreads) {
     float t = 0.0f, down;
     if (VALUES) {
@@ -125,9 +126,12 @@ __device__ __forceinline__ void split_tile(const PromptArgs& A, const PromptPiec
     if (VALUES)
       W.v_power[place * D + c] = down;
     else if (c == 0)
-      W.k_power[place] = down;
+      W.k_power[place] = apart ? -down : down;
   }
-  if (tid == 0) owner[place] = __uint_as_float(sh_most) > 4096.0f * __uint_as_float(sh_least) ? -2 : b;
+  if (tid == 0) {
+    owner[place] = b;
+    if (VALUES) W.v_most[place] = apart ? __uint_as_float(sh_most) : 0.0f;
+  }
   __syncthreads();
   if (!in) return;
   const float4 up = *reinterpret_cast<const float4*>(&sh_up[4 * l]);

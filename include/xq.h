@@ -650,9 +650,11 @@ XQ_API size_t xq_prompt_attn_workspace_bytes(const xq_prompts *prompts);
  * Rows of out that belong to no sequence (before starts[0], behind
  * starts[batch]) are left as they were. What a row does not see does not
  * reach it, infinities and NaN included. fp32 rows enter the tensor cores as two
- * fp16 numbers each (22 bits). Rows that see something not finite, and fp32 rows
- * that meet 128 keys whose K or V rows differ by more than 2^12 in size, are
- * computed one by one (hundreds of times slower). A sequence whose bounds do not
+ * fp16 numbers each (22 bits). Rows that see something not finite are computed
+ * one by one (hundreds of times slower), and so are fp32 rows that meet 128 keys
+ * (64 at head size 256) whose K or V rows differ by more than 2^12 in size, if
+ * their scores could pass 2^20 or their results lie below 2^-15 of the largest
+ * of those V. A sequence whose bounds do not
  * satisfy 0 <= starts[b] <= starts[b+1] <= tokens is left out and recorded
  * (xq_device_error: kernel 5, wait 2); where the others then have rows in
  * common, such a row of out is any one's of them. q, k, v and out are 16-byte aligned,

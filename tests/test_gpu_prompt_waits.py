@@ -39,17 +39,13 @@ def test_rows_computed_one_by_one_are_waited_for(xq, dtype, H, D, T):  # noqa: F
     the limit has beside the short time. No row may be lost."""
     assert xq.device_error() == 0
     q, k, v = inputs(T, H, 1, D, dtype, 42)
-    if dtype == "fp32":
-        k[0] *= 2.0 ** -14  # finite, and all rows are computed one by one
-    else:
-        v[0, 0, 9] = float("nan")
+    v[0, 0, 9] = float("nan")
     s = torch.tensor([0, T], dtype=torch.int32, device="cuda")
     out = xq.debug_stalled_prompt_attn(q, k, v, s, SHORT, False, out=torch.full_like(q, 7.0))
     assert xq.device_error() == 0
     want, bound = ops_check.attention(q, k, v, [0, T], D ** -0.5)
-    if dtype != "fp32":
-        assert bool(torch.isnan(out[..., 9]).all())
-        want[..., 9] = math.nan
+    assert bool(torch.isnan(out[..., 9]).all())
+    want[..., 9] = math.nan
     ops_check.within(out, want, bound)
 
 
