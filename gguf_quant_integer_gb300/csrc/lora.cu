@@ -25,13 +25,16 @@
 // job; 2854 rows of 25 adapters, 8960 -> 1536, rank 24: 72 us, above 110 with 16). Few jobs have clusters of 16, and as many
 // clusters for a job's columns as fill the device, which all work out x A^T (1 row to 2 x 14336, rank 16: 6.0 us, 9.8 with 8
 // CTAs a job). What bounds it: with few rows, a chain of memory round trips and instructions seen for the first time (one row
-// 4096 -> 4096, rank 16: 5.2 us, x A^T, the exchange and y in like parts; 64 rows of 16 adapters at q, k and v: 11.4 us); with
+// 4096 -> 4096, rank 16: 5.3 us, x A^T, the exchange and y in like parts; 64 rows of 16 adapters at q, k and v: 11.7 us); with
 // many, the warp-level tensor cores, 8 clocks a product of 16 x 8 x 8 on one of an SM's four sub-cores (4099 rows, rank 64, two
-// projections 4096 -> 14336: 398 us, 371 with sums left in the tensor cores; 19.2 million products are 130 us at least, y's
-// 0.94 GB 139 us); 777 mixed rows to 2 x 8960, rank 8: 38 us, 0.1 GB. Tried and slower: y loaded and stored (at widths that are
-// no multiple of 4, 1504 rows to 130 and 77 columns 38 us, 21 with single reductions), its lines prefetched into L2 (40 us for
-// 39), 85 registers and three CTAs an SM for 16-row jobs (one row 7.6 us), 64 ranks a warp (spills), x and A two or three
-// chunks ahead (352 rows above 60 and 76).
+// projections 4096 -> 14336: 400 us, 371 with sums left in the tensor cores; 19.2 million products are 130 us at least, y's
+// 0.94 GB 139 us); 777 mixed rows to 2 x 8960, rank 8: 39 us, 0.1 GB. Every CTA of every job reads all ids, so the search grows
+// with rows x jobs (8 adapters, 1024 -> 1024, rank 16: 4099 rows 57 us, 131072 rows 8.5 ms). Tried and slower: y loaded and stored
+// (at widths that are no multiple of 4, 1504 rows to 130 and 77 columns 38 us, 21 with single reductions), its lines prefetched
+// into L2 (40 us for 39), 85 registers and three CTAs an SM for 16-row jobs (one row 7.6 us), 64 ranks a warp (spills), x and A
+// two or three chunks ahead (352 rows above 60 and 76). With 128 registers a thread some are spilled: 16-bit adapters 40 bytes with
+// 64 rows a job, 88 with 32, none with 16; fp32 ones 552, 216 and 24 (4099 rows, rank 64: 618 us, three products for two and no
+// weights ahead).
 #include <algorithm>
 #include <utility>
 
@@ -46,7 +49,6 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 // The warps' parts of a pass's sums: [8 / MT][16 * MT][RB].
 __host__ __device__ constexpr int sum_bytes(int rank_block) { return 8 * 16 * rank_block * 4; }
 constexpr int kJobsGrid = 512;        // jobs of a projection with clusters of their own
-constexpr int kMaxAdapters = 8192;
 
 struct LoraGrid {
   int jobs;       // at most, of a projection

@@ -27,8 +27,8 @@
 //
 // What bounds it, at head size 128: a tile's 48 products take the tensor cores some 3100 clocks; the outputs' way out of tensor
 // memory, which has no room for a second one beside them, and the scores', softmax and weights' make it some 4000. An item
-// costs some 12000 more (queries, first scores, results). 5 sequences of 33 to 1500, 32/8 heads: 133 us and 14 for the split,
-// 260 TFLOP/s of fp32 work (780 of the tensor cores'), error against 64 bits 4.9e-7 to 5.5e-7 (plain fp32 5.7e-7 to 6.9e-7).
+// costs some 12000 more (queries, first scores, results). 5 sequences of 33 to 1500, 32/8 heads: 136 us and 15 for the split,
+// 252 TFLOP/s of fp32 work (760 of the tensor cores'), error against 64 bits 4.9e-7 to 5.5e-7 (plain fp32 5.7e-7 to 6.9e-7).
 // Tried and slower: a softmax group a tile (156 us for 154), queries by threads from memory (18000 clocks an item), outputs in
 // two column groups with barriers of their own (160: products of 64 columns are not twice as fast), eight output warps (154
 // for 149), the next item's queries before the last tile's softmax (157).
@@ -388,7 +388,8 @@ __global__ void __launch_bounds__(32 * PieceShape<D>::kWarps, 1)
     const int row = (warp & 3) * 32 + lane, token = row / P.pack, part = row - token * P.pack;
     const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     if (warp < kOut) {
-      // ---------------------------------------------- softmax: a thread is a row, a group of warps has every second tile
+      // ---------------------------------------------- softmax: a thread has half a row's keys of a tile, the other group of warps the other
+      // half
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsSoft));
       const int half = warp >> 2;
       float cq = 0.0f;  // the row's: of the scale and its query's power of two

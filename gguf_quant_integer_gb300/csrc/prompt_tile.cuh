@@ -31,9 +31,9 @@
 // or sum is not finite (a score, a V that all rows see), are computed again by themselves (one_row).
 //
 // What bounds it, at head size 128: the tensor cores have 2048 clocks of work for the two row tiles' 128 keys, which take
-// 3450: a tile's scores, softmax (1600), weights and outputs follow each other, and two of them do not fill the pipe. 12287
-// bf16 tokens of 32/8 heads 827 us, 1.50 PFLOP/s; 16 sequences of 17 to 2048 219 us (0.98; masked halves of tiles count as
-// nothing), where an item of some 9 tiles ends and begins in about 8000 clocks.
+// some 3600: a tile's scores (107 clocks a product, with both operands in shared memory), softmax (1700), weights and outputs follow each
+// other, and two of them do not fill the pipe. 12287 bf16 tokens of 32/8 heads 891 us, 1.39 PFLOP/s; 16 sequences of 17 to 2048
+// 209 us (1.03; masked halves of tiles count as nothing), where an item of some 9 tiles ends and begins in about 8000 clocks.
 // Tried and slower: 32 scores at a time in rolled loops (long 974 us for 935), products issued by two warps (one is then left
 // to look through V: 241 us for 229, packed), masks as bits of a word (247 for 229), results stored from registers (258 for
 // 235: a store of 32 rows takes 32 lines' turns), the scan of V unrolled eight times instead of twice (234 for 229).

@@ -83,11 +83,13 @@ enum CheckSite : unsigned {
   kChkKvPart = 54,   // partial result or record inside the workspace
   kChkKvLens = 55,   // sequence inside the batch
   // qk_rope.cu
-  kChkRope = 60,     // 8 elements inside a row of a token of the call
-  kChkPromptSlot = 63, // a tile's powers of two inside the workspace
-  // prompt_tile.cuh
-  kChkLoraRow = 62,    // row of y inside [M]
+  kChkRope = 60,       // 8 elements inside a row of a token of the call
+  // prompt_items.cuh, prompt_tile.cuh, prompt_pieces.cuh
   kChkPromptRow = 61,  // row of the result inside [tokens][heads]
+  // lora.cu
+  kChkLoraRow = 62,    // row of y inside [M]
+  // prompt_pieces.cuh
+  kChkPromptSlot = 63, // a tile's powers of two inside the workspace
 };
 
 }  // namespace xq
