@@ -23,7 +23,9 @@
 //
 // Sums: a tensor core's accumulator cuts off, towards 0, what an fp32 addition rounds, so an output that stayed there over a long
 // sequence would be too small by 8e-9 a key (fp16, V of one sign, 131071 keys: 1e-3, two half steps of the result). So after
-// kPromptRun key tiles the outputs are added to the row's sum in the workspace, in fp32, and the accumulator begins anew.
+// kPromptRun key tiles the outputs are added to the row's sum in the workspace, in fp32, and the accumulator begins anew. The sum of
+// weights goes tile by tile, with what each addition rounds off kept beside it (one after the other, equal weights of 524287 keys
+// were all rounded the same way: 3e-3).
 //
 // What is not finite: scores of keys that a row does not see are replaced, but such a key's V would meet a weight of 0 in
 // the product, where an infinity or NaN spoils the row. So two warps look through the V tiles of which some row does not see
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
       const int lim1 = place + 1, lim0 = A.window ? max(0, lim1 - A.window) : 0;
       const int p0 = it.place + r * P.tokens_tile;
       float e = kLowest;
-      ptx::f2 l = ptx::pk(0.0f, 0.0f);
+      float l = 0.0f, l_rest = 0.0f;  // the sum of weights, and what its additions rounded off
       for (int i = 0; i < tiles; ++i, ++done) {
         const int key = (it.begin[r] + i) * kKeys;
         const bool anew = i > 0 && i % kPromptRun == 0;
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
           const float next = top - e > kTop ? top - kStart : e;
           const float f = ex2(e - next);
           e = next;
-          l = ptx::mul2(l, ptx::pk(f, f));
+          l *= f, l_rest *= f;
           if (i > 0 && !anew) {
             ok = wait(kPbO + buffer(r, done - 1), turn(done - 1), 12);
             if (!ok) break;
@@ -464,6 +466,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
           }
         }
         const ptx::f2 c2 = ptx::pk(cs, cs), e2 = ptx::pk(-e, -e);
+        ptx::f2 tile_sum = ptx::pk(0.0f, 0.0f);
 #pragma unroll
         for (int c = 0; c < kKeys; c += 32) {
           uint32_t w[16];
@@ -474,9 +477,9 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
             w[x / 2] = pack2<TYPE>(a, b);
             if constexpr (TYPE == kF16) {
               const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[x / 2]));  // the weights as rounded
-              l = ptx::add2(l, ptx::pk(f.x, f.y));
+              tile_sum = ptx::add2(tile_sum, ptx::pk(f.x, f.y));
             } else {
-              l = ptx::add2(l, ptx::pk(__uint_as_float(w[x / 2] << 16), __uint_as_float(w[x / 2] & 0xFFFF0000u)));
+              tile_sum = ptx::add2(tile_sum, ptx::pk(__uint_as_float(w[x / 2] << 16), __uint_as_float(w[x / 2] & 0xFFFF0000u)));
             }
           }
           ptx::tmem_st16(ts + c / 2, w);
@@ -485,6 +488,9 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(kPbP + buffer(r, done)));
+        const float add = ptx::lo32(tile_sum) + ptx::hi32(tile_sum), next_l = l + add, kept = next_l - l;
+        l_rest += (l - (next_l - kept)) + (add - kept);
+        l = next_l;
       }
       if (!ok) break;
       // ---- the rows' results
@@ -492,7 +498,7 @@ __global__ void __launch_bounds__(32 * PromptShape<D>::kWarps, 1) prompt_tile_ke
       if (!ok) break;
       ptx::tc_fence_after();
       if (tiles > kPromptRun) run_add<D, true>(P.sums, to, e, true);
-      const float sum = ptx::lo32(l) + ptx::hi32(l), inv = 1.0f / sum;
+      const float sum = l + l_rest, inv = 1.0f / sum;
       const size_t at = (static_cast<size_t>(it.first) + place) * A.heads + it.head + part;
       const bool store = live && XQ_IN(at, static_cast<size_t>(A.tokens) * A.heads, kChkPromptRow);
       const int to_row = store ? static_cast<int>(at) : -1;

@@ -96,3 +96,17 @@ def test_runs_of_tiles_captured_and_side_by_side(xq, dtype):  # noqa: F811
     assert torch.equal(outs[0], wants[0]) and bool((whole[32 << 20:] == 7).all())
     with pytest.raises(xq.XQError):
         xq.prompt_attn(q, k, v, s, workspace=whole[:1 << 20])
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("T", [131071, 524287])
+@pytest.mark.parametrize("ahead", [0.1, 0.35, 0.77, 1.3, 2.2, 3.1])
+def test_equal_weights_add_up(xq, dtype, T, ahead):  # noqa: F811
+    """All keys but the first score alike, so all weights are one number, no power of two, whose additions to a long sum would all be rounded
+    one way. Values of 1.5: the result is off by some 3e-5 at most (what the tensor cores cut off), and half a step of it is 3e-4: exact."""
+    q = torch.zeros(T, 1, 64, device="cuda", dtype=ops_check.DTYPES[dtype])
+    k, v = torch.zeros_like(q), torch.full_like(q, 1.5)
+    q[..., 0] = 1
+    k[0, 0, 0] = ahead
+    out = xq.prompt_attn(q, k, v, torch.tensor([0, T], dtype=torch.int32, device="cuda"), scale=1.0)
+    assert bool((out == 1.5).all())
