@@ -806,10 +806,9 @@ def _turns(base, rot, factors):
             freq = freq / factors
     if not np.isfinite(freq).all():
         raise ValueError("base and factors have to give finite frequencies")
-    with decimal.localcontext() as ctx:
-        # 64 bits behind the point, whatever is before it
-        ctx.prec = 45 + max([0, *(math.frexp(f)[1] * 3 // 10 + 1 for f in freq.tolist())])
-        ctx.Emin, ctx.Emax = decimal.MIN_EMIN, decimal.MAX_EMAX
+    # 64 bits behind the point, whatever is before it
+    digits = 45 + max([0, *(math.frexp(f)[1] * 3 // 10 + 1 for f in freq.tolist())])
+    with decimal.localcontext(decimal.Context(prec=digits, Emin=decimal.MIN_EMIN, Emax=decimal.MAX_EMAX)) as ctx:
         D = decimal.Decimal
 
         def arctan(n):  # of 1 / n
@@ -822,11 +821,13 @@ def _turns(base, rot, factors):
             return total
 
         over_turn = D(2) ** 64 / (8 * (4 * arctan(5) - arctan(239)))  # 2^64 / (2 pi), Machin's formula
-        step = -2 * D(float(base)).ln() / rot if rot and math.isfinite(base) else D(0)
-        turns = []
+        # base^(-2 / rot), and its powers one from the other: they lose three digits of 25 that are not needed
+        step = (-2 * D(float(base)).ln() / rot).exp() if rot and math.isfinite(base) else D(0)
+        turns, power = [], D(1)
         for i, f in enumerate(freq.tolist()):
-            exact = D(0) if f == 0.0 else (step * i).exp() / (D(1) if factors is None else D(float(factors[i]))) * over_turn
+            exact = D(0) if f == 0.0 else power / (D(1) if factors is None else D(float(factors[i]))) * over_turn
             turns.append(int(exact.to_integral_value(decimal.ROUND_HALF_EVEN)) % (1 << 64))
+            power *= step
     return turns
 
 
