@@ -116,17 +116,25 @@ __device__ __forceinline__ float4 load4(const void* p, size_t at) {
 }
 
 // One row by one warp, in fp32: 32 keys' scores at a time, a lane each, then their values, lanes over the head's elements.
+// Sums go 32 keys at a time, with what an addition rounds off kept beside them, as a long row's would be far off (fp32, 131071 equal
+// weights one after the other: 5e-4).
 // Writes columns c0 .. c1 - 1, multiples of 32 or, with lanes left out, of 16.
 template <int TYPE, int D>
 __device__ __noinline__ void one_row(const PromptArgs& A, int first, int place, int head, int c0, int c1) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, kv = head / (A.heads / A.kv_heads);
   const size_t token = static_cast<size_t>(first) + place, q0 = token * A.q_stride + static_cast<size_t>(head) * D;
-  float o[E];
+  float o[E], o_rest[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.0f;
+  for (int e = 0; e < E; ++e) o[e] = o_rest[e] = 0.0f;
+  // sum += x
+  auto add = [](float& sum, float& rest, float x) {
+    const float next = sum + x, kept = next - sum;
+    rest += (sum - (next - kept)) + (x - kept);
+    sum = next;
+  };
   const float cs = A.scale * 1.4426950408889634f;
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, l = 0.0f, l_rest = 0.0f;
   for (int j0 = A.window && place >= A.window ? place - A.window + 1 : 0; j0 <= place; j0 += 32) {
     const int n = min(32, place - j0 + 1);
     float s = -INFINITY;
@@ -151,23 +159,30 @@ __device__ __noinline__ void one_row(const PromptArgs& A, int first, int place, 
     float sum = w;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    l = fmaf(l, f, sum);
-    if (l != l) break;  // a NaN among the scores is the whole row's
+    if (sum != sum) {  // a NaN among the scores is the whole row's
+      l = sum;
+      break;
+    }
+    l *= f, l_rest *= f;
+    add(l, l_rest, sum);
+    float part[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= f;
+    for (int e = 0; e < E; ++e) o[e] *= f, o_rest[e] *= f, part[e] = 0.0f;
     const size_t v0 = (static_cast<size_t>(first) + j0) * A.v_stride + static_cast<size_t>(kv) * D + lane;
 #pragma unroll 4
     for (int j = 0; j < n; ++j) {
       const float wj = __shfl_sync(0xffffffffu, w, j);
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(wj, load_elt<TYPE>(A.v, v0 + j * A.v_stride + 32 * e), o[e]);
+      for (int e = 0; e < E; ++e) part[e] = fmaf(wj, load_elt<TYPE>(A.v, v0 + j * A.v_stride + 32 * e), part[e]);
     }
+#pragma unroll
+    for (int e = 0; e < E; ++e) add(o[e], o_rest[e], part[e]);
   }
   const size_t row = token * A.heads + head;
   if (XQ_IN(row, static_cast<size_t>(A.tokens) * A.heads, kChkPromptRow))
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      if (lane + 32 * e >= c0 && lane + 32 * e < c1) store_elt<TYPE>(A.out, row * D + lane + 32 * e, o[e] / l);
+      if (lane + 32 * e >= c0 && lane + 32 * e < c1) store_elt<TYPE>(A.out, row * D + lane + 32 * e, (isfinite(o[e]) ? o[e] + o_rest[e] : o[e]) / (l + l_rest));
 }
 
 // Sequence b's rows and their number; 0, and recorded, if its bounds are no range of the call's rows.

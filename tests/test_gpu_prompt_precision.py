@@ -110,3 +110,26 @@ def test_equal_weights_add_up(xq, dtype, T, ahead):  # noqa: F811
     k[0, 0, 0] = ahead
     out = xq.prompt_attn(q, k, v, torch.tensor([0, T], dtype=torch.int32, device="cuda"), scale=1.0)
     assert bool((out == 1.5).all())
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("D", [64, 256])
+def test_long_rows_by_themselves(xq, dtype, D):  # noqa: F811
+    """The last rows see a NaN in one element of V and are computed one by one: equal weights and values of 131071 keys, whose
+    additions would all be rounded one way. Sums of 32 terms (2^-24 * 32), then kept exactly: 2^-18 with the quotient, all told.
+    At head size 256 fp32 columns 128 and on are computed apart, do not see the NaN, and go the usual way: their sums of outputs and of
+    weights are 2048 tiles' each, added in fp32, off by 2^-24 of the running sum, half of the last one in the mean: 2 * 2048 * 2^-25."""
+    T = 131071
+    q = torch.zeros(T, 1, D, device="cuda", dtype=ops_check.DTYPES[dtype])
+    k, v = torch.zeros_like(q), torch.full_like(q, 1.5)
+    q[..., 0] = 1
+    k[0, 0, 0] = 0.77
+    v[T - 20, 0, 9] = float("nan")
+    out = xq.prompt_attn(q, k, v, torch.tensor([0, T], dtype=torch.int32, device="cuda"), scale=1.0)[T - 20:, 0]
+    assert bool(torch.isnan(out[:, 9]).all())
+    out[:, 9] = 1.5
+    off = (out.double() / 1.5 - 1).abs()
+    alone = 128 if dtype == "fp32" and D == 256 else D
+    assert float(off[:, :alone].max()) <= 2.0 ** -18
+    assert alone == D or float(off[:, alone:].max()) <= 2.0 ** -18 + 2 * 2048 * 2.0 ** -25
+    assert xq.device_error() == 0
